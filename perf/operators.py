@@ -225,7 +225,7 @@ def _plain_norm(s):
         b = n.view(n.shape[0], -1, 32)
         # the smallest power of two that brings the block's largest value to 448 or below
         m, e = torch.frexp(b.abs().amax(-1))
-        e = (e - 9 + (m > 0.875).int()).clamp(-127, 127)
+        e = torch.where(m == 0, -127, e - 9 + (m > 0.875).int()).clamp(-127, 127)
         q = (b * torch.exp2(-e.float()).unsqueeze(-1)).to(torch.float8_e4m3fn).view(n.shape)
         sc = (e + 127).to(torch.uint8)
     return _norm_outputs(total, n.to(torch.bfloat16) if s["y"] is not None else None, q, sc)
