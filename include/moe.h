@@ -396,6 +396,115 @@ MoeStatus moe_route_static_status(void *cuda_stream);
  * Errors: MOE_EINVAL (NULL handle, limit_us outside [1, 1000000]). */
 MoeStatus moe_debug_expire_next_wait(MoeHandle *h, int limit_us);
 
+/* ---- Operators around the layer ----
+ *
+ * What a decoder step runs beside the experts: the norm that makes the layer's
+ * x out of the residual stream (moe_add_rmsnorm), the linear layers on x or on
+ * attention's output, the router's own product among them (moe_linear_*), and
+ * group-limited routing (moe_route_grouped), whose ids and weights feed
+ * moe_forward_routed.  All are forward operators, like the layer itself.  No
+ * counterpart in the papers.
+ *
+ * Rows: a matrix of T rows of H values, row t at data + t * ld elements.
+ * MOE_ROWS_MXFP8 rows are E4M3 bytes with one E8M0 byte per 32 consecutive
+ * values of a row beside them ([T][H/32], no gaps): the value is
+ * e4m3 * 2^(byte - 127), a byte of 255 is NaN. */
+typedef enum { MOE_ROWS_BF16 = 0, MOE_ROWS_F32 = 1, MOE_ROWS_MXFP8 = 2 } MoeRowType;
+
+/* Residual addition and RMS norm of T rows of H values:
+ *   s = residual + delta              (added in FP32, rounded to residual's type)
+ *   n = s / sqrt(mean(s^2) + eps) * gain                     (over what s holds)
+ *   y = BF16 of n;   q, q_scales = MXFP8 of n
+ * The mean and n are FP32.  An MXFP8 block takes the smallest power of two that
+ * brings its largest |n| to 448 or below, so that nothing saturates; a block of
+ * zeros takes byte 0.  A non-finite n becomes the E4M3 NaN (0x7F).
+ *  residual   BF16 or F32 rows;  delta  BF16 or F32 rows, or NULL (nothing is added)
+ *  gain       [H] BF16 or F32 (gain_type), or NULL (ones)
+ *  sum        receives s in residual's type, or NULL; may be residual itself
+ *             (in place, same ld)
+ *  y          BF16 rows or NULL;  q  E4M3 rows with q_scales [T][H/32], or NULL
+ * H is a multiple of 32 in 32 .. 65536.  Every row starts on a 16-byte
+ * boundary.  An output must not overlap an input, except sum in place of
+ * residual, or of delta where their types and ld agree.  T == 0 enqueues nothing.
+ * Errors: MOE_EINVAL (T outside [0, 2^24], NULL residual, no output at all, q
+ * without q_scales, a row type that does not fit, ld < H, misaligned rows, eps
+ * negative or not finite), MOE_EDIMS (H), MOE_ECUDA. */
+MoeStatus moe_add_rmsnorm(const void *residual, MoeRowType residual_type, long long residual_ld, const void *delta,
+                          MoeRowType delta_type, long long delta_ld, const void *gain, MoeRowType gain_type,
+                          float eps, int T, int H, void *sum, long long sum_ld, void *y, long long y_ld, void *q,
+                          long long q_ld, void *q_scales, void *cuda_stream);
+
+typedef enum { MOE_SCORE_SOFTMAX = 0, MOE_SCORE_SIGMOID = 1 } MoeScore;
+typedef enum { MOE_GROUP_MAX = 0, MOE_GROUP_TOP2 = 1 } MoeGroupScore;
+
+/* Largest E, n_groups and k moe_route_grouped takes. */
+#define MOE_ROUTE_GROUPED_MAX_EXPERTS 1024
+#define MOE_ROUTE_GROUPED_MAX_GROUPS 32
+
+/* Group-limited routing.  For token t, over the experts e whose logit is not
+ * -inf (a logit of -inf switches the expert off for that token):
+ *   s_e = 1 / (1 + exp(-l_e)), or exp(l_e) / sum over all E of exp(l)
+ *   c_e = s_e + bias_e                       (the bias decides only the selection)
+ *   a group is E / n_groups consecutive experts; its score is its largest c, or
+ *   the sum of its two largest (of the one, where only one is not switched off)
+ * The k_groups groups with the largest scores stay, and of their experts the k
+ * with the largest c are kept, the largest first; equal values go to the lower
+ * index and NaN ranks below every number.  w_j = scale * s_j, over the sum of
+ * the kept s with renormalize (0 where that sum is 0).  A slot left over when
+ * the groups that stay hold fewer than k experts is an empty slot of
+ * moe_forward_routed: id -1, weight 0.
+ * The selection is that of FP64 scores; weights are FP32.
+ *  router_logits [T][E] float, bias [E] float or NULL (zeros), topk_ids and
+ *  topk_w [T][k]: device pointers, 4-byte aligned, enqueued on cuda_stream.
+ * No handle and no workspace.  T == 0 enqueues nothing.
+ * Errors: MOE_EINVAL (T outside [0, 2^24], E outside [1,
+ * MOE_ROUTE_GROUPED_MAX_EXPERTS], n_groups outside [1,
+ * MOE_ROUTE_GROUPED_MAX_GROUPS] or no divisor of E, k_groups outside [1,
+ * n_groups], k outside [1, min(32, k_groups * E / n_groups)], an unknown score,
+ * NULL or misaligned pointers), MOE_ECUDA. */
+MoeStatus moe_route_grouped(const float *router_logits, const float *bias, int T, int E, int k, int n_groups,
+                            int k_groups, MoeScore score, MoeGroupScore group_score, int renormalize, float scale,
+                            int32_t *topk_ids, float *topk_w, void *cuda_stream);
+
+/* A linear layer y = x W^T with W [N][K] in one of the library's weight
+ * formats: 4-bit for projections, BF16 for the router's own product.
+ * moe_linear_load copies the weights into the library's own layouts, as
+ * moe_load_weights does (synchronous; the caller's buffers can be freed when it
+ * returns).  N in 1 .. 1048576; K a multiple of 32 in 32 .. 65536.
+ * Errors: MOE_EINVAL (NULL pointers, unknown format, N, INT4 scales not 2-byte
+ * aligned), MOE_EDIMS (K), MOE_ESCALE, MOE_ENOMEM, MOE_ECUDA.  *out is set only
+ * on MOE_OK. */
+typedef struct MoeLinear MoeLinear;
+MoeStatus moe_linear_load(int N, int K, MoeWeightFormat fmt, const MoeMx *w, void *cuda_stream, MoeLinear **out);
+
+/* Bytes of device workspace moe_linear_forward needs for T tokens (0 for few
+ * tokens, for a NULL handle and for T <= 0). */
+size_t moe_linear_workspace_bytes(const MoeLinear *l, int T);
+
+/* y[t][n] = sum_k x[t][k] w[n][k] for T tokens.  Products accumulate in FP32;
+ * 4-bit weights decode exactly, and x keeps its value as long as it is within
+ * 2^-24 of the largest |x| of its token.
+ *  x         BF16 or MXFP8 rows of K values (x_scales [T][K/32] for MXFP8, else NULL)
+ *  y         F32 or BF16 rows of N values; F32 rows are overwritten, or added
+ *            to when accumulate != 0 (BF16 rows cannot accumulate)
+ *  workspace >= moe_linear_workspace_bytes(l, T) bytes, 256-byte aligned;
+ *            contents on entry do not matter; may be NULL when that is 0
+ * Rows of x start on 16-byte boundaries; rows of y on boundaries of their
+ * elements.  Several streams may use one handle at a time, each with a
+ * workspace of its own.  T == 0 enqueues nothing.
+ * Errors: MOE_EINVAL (NULL handle or pointers, T outside [0, 2^20], a row type
+ * that does not fit, ld too small, misaligned rows, accumulate into BF16),
+ * MOE_EWORKSPACE, MOE_EDEVICE, MOE_ECUDA. */
+MoeStatus moe_linear_forward(MoeLinear *l, const void *x, MoeRowType x_type, long long x_ld, const void *x_scales,
+                             int T, void *y, MoeRowType y_type, long long y_ld, int accumulate, void *workspace,
+                             size_t ws_bytes, void *cuda_stream);
+
+/* Wait for `cuda_stream`, then report as moe_sync_status does for a layer. */
+MoeStatus moe_linear_sync_status(MoeLinear *l, void *cuda_stream);
+
+/* Release the handle and its weight copies (waits for the device; NULL is a no-op). */
+void moe_linear_free(MoeLinear *l);
+
 /* Human-readable description of the last non-OK status returned on the
  * calling thread (thread-local, never NULL). */
 const char *moe_last_error(void);

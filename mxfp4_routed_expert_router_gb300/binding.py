@@ -19,12 +19,17 @@ MOE_OK, MOE_EINVAL, MOE_EDIMS, MOE_ESCALE, MOE_ENOMEM, MOE_ECUDA, MOE_EWORKSPACE
 STATUS_NAMES = ["MOE_OK", "MOE_EINVAL", "MOE_EDIMS", "MOE_ESCALE", "MOE_ENOMEM", "MOE_ECUDA", "MOE_EWORKSPACE",
                 "MOE_EDEVICE"]
 MOE_W_MXFP4, MOE_W_BF16, MOE_W_INT4G32 = 0, 1, 2
+MOE_ROWS_BF16, MOE_ROWS_F32, MOE_ROWS_MXFP8 = 0, 1, 2
+MOE_SCORE_SOFTMAX, MOE_SCORE_SIGMOID = 0, 1
+MOE_GROUP_MAX, MOE_GROUP_TOP2 = 0, 1
 
 # every symbol include/moe.h declares
 EXPORTED = ("moe_load_weights", "moe_workspace_bytes", "moe_forward", "moe_forward_routed", "moe_set_expert_range",
             "moe_route_sigmoid", "moe_dense_sliced_forward", "moe_sync_status", "moe_profile_enable",
             "moe_profile_read", "moe_route_static", "moe_route_static_status", "moe_graph_create",
-            "moe_graph_launch", "moe_graph_free", "moe_debug_expire_next_wait", "moe_last_error", "moe_free")
+            "moe_graph_launch", "moe_graph_free", "moe_debug_expire_next_wait", "moe_last_error", "moe_free",
+            "moe_add_rmsnorm", "moe_route_grouped", "moe_linear_load", "moe_linear_workspace_bytes",
+            "moe_linear_forward", "moe_linear_sync_status", "moe_linear_free")
 STAGES = ("routing", "grouping", "gate_up", "down", "combine", "layer")
 
 
@@ -94,6 +99,21 @@ def _load():
     L.moe_route_static_status.restype = ci
     L.moe_debug_expire_next_wait.argtypes = [vp, ci]
     L.moe_debug_expire_next_wait.restype = ci
+    ll, cf = ctypes.c_longlong, ctypes.c_float
+    L.moe_add_rmsnorm.argtypes = [vp, ci, ll, vp, ci, ll, vp, ci, cf, ci, ci, vp, ll, vp, ll, vp, ll, vp, vp]
+    L.moe_add_rmsnorm.restype = ci
+    L.moe_route_grouped.argtypes = [vp, vp, ci, ci, ci, ci, ci, ci, ci, ci, cf, vp, vp, vp]
+    L.moe_route_grouped.restype = ci
+    L.moe_linear_load.argtypes = [ci, ci, ci, ctypes.POINTER(MoeMx), vp, ctypes.POINTER(vp)]
+    L.moe_linear_load.restype = ci
+    L.moe_linear_workspace_bytes.argtypes = [vp, ci]
+    L.moe_linear_workspace_bytes.restype = sz
+    L.moe_linear_forward.argtypes = [vp, vp, ci, ll, vp, ci, vp, ci, ll, ci, vp, sz, vp]
+    L.moe_linear_forward.restype = ci
+    L.moe_linear_sync_status.argtypes = [vp, vp]
+    L.moe_linear_sync_status.restype = ci
+    L.moe_linear_free.argtypes = [vp]
+    L.moe_linear_free.restype = None
     L.moe_last_error.argtypes = []
     L.moe_last_error.restype = ctypes.c_char_p
     L.moe_free.argtypes = [vp]
@@ -235,6 +255,97 @@ def moe_debug_expire_next_wait(handle: int, limit_us: int) -> None:
 
 def moe_free(handle: int) -> None:
     lib.moe_free(handle)
+
+
+def _rows(t, name: str) -> Tuple[Optional[int], int, int]:
+    """Address, row type and row stride (elements) of a [T, H] tensor, (None, 0, 0) for None."""
+    if t is None:
+        return None, 0, 0
+    ty = _row_types().get(t.dtype)
+    if ty is None:
+        raise MoeError(MOE_EINVAL, f"{name}: rows are bfloat16, float32 or float8_e4m3fn, not {t.dtype}")
+    if t.dim() != 2 or (t.shape[1] > 1 and t.stride(1) != 1):
+        raise MoeError(MOE_EINVAL, f"{name}: a [T, H] tensor whose rows have no gaps is needed")
+    return t.data_ptr(), ty, (t.stride(0) if t.shape[0] > 1 else t.shape[1])
+
+
+_ROW_TYPES = {}
+
+
+def _row_types() -> dict:
+    if not _ROW_TYPES:
+        import torch
+        _ROW_TYPES.update({torch.bfloat16: MOE_ROWS_BF16, torch.float32: MOE_ROWS_F32,
+                           torch.float8_e4m3fn: MOE_ROWS_MXFP8})
+    return _ROW_TYPES
+
+
+def _same_rows(name: str, t, T: int, H: int) -> None:
+    if t is not None and tuple(t.shape) != (T, H):
+        raise MoeError(MOE_EINVAL, f"{name}: shape {tuple(t.shape)} where ({T}, {H}) is needed")
+
+
+def moe_add_rmsnorm(residual, delta, gain, eps: float, sum=None, y=None, q=None, q_scales=None, stream=None) -> None:
+    """s = residual + delta, the RMS norm of s times gain as BF16 rows (y) and MXFP8 rows (q, q_scales); see
+    include/moe.h.  residual, delta and sum are bfloat16 or float32 [T, H] tensors, y bfloat16, q float8_e4m3fn,
+    q_scales uint8 [T, H/32]; delta, gain and any output may be None, and sum may be residual itself."""
+    T, H = residual.shape
+    for name, t in (("delta", delta), ("sum", sum), ("y", y), ("q", q)):
+        _same_rows(name, t, T, H)
+    if gain is not None and (tuple(gain.shape) != (H,) or not gain.is_contiguous()):
+        raise MoeError(MOE_EINVAL, f"gain: a dense vector of {H} values is needed")
+    if q_scales is not None and (tuple(q_scales.shape) != (T, H // 32) or not q_scales.is_contiguous()
+                                 or q_scales.element_size() != 1):
+        raise MoeError(MOE_EINVAL, f"q_scales: a dense uint8 [{T}, {H // 32}] tensor is needed")
+    r, rt, rld = _rows(residual, "residual")
+    d, dt, dld = _rows(delta, "delta")
+    s, sty, sld = _rows(sum, "sum")
+    yp, yt, yld = _rows(y, "y")
+    qp, qt, qld = _rows(q, "q")
+    if s is not None and sty != rt:
+        raise MoeError(MOE_EINVAL, "sum: the residual's type is needed")
+    if (yp is not None and yt != MOE_ROWS_BF16) or (qp is not None and qt != MOE_ROWS_MXFP8):
+        raise MoeError(MOE_EINVAL, "y is bfloat16 and q float8_e4m3fn")
+    gt = 0 if gain is None else _row_types().get(gain.dtype, -1)
+    _check(lib.moe_add_rmsnorm(r, rt, rld, d, dt, dld, _ptr(gain), gt, eps, T, H, s, sld, yp, yld, qp, qld,
+                               _ptr(q_scales), _stream(stream)))
+
+
+def moe_route_grouped(router_logits, bias, T: int, E: int, k: int, n_groups: int, k_groups: int, score: int,
+                      group_score: int, renormalize: bool, scale: float, topk_ids, topk_w, stream=None) -> None:
+    """Group-limited routing (see include/moe.h); the outputs feed moe_forward_routed."""
+    _check(lib.moe_route_grouped(_ptr(router_logits), _ptr(bias), T, E, k, n_groups, k_groups, score, group_score,
+                                 int(bool(renormalize)), scale, _ptr(topk_ids), _ptr(topk_w), _stream(stream)))
+
+
+def moe_linear_load(N: int, K: int, fmt: int, codes, scales=None, zeros=None, stream=None) -> int:
+    """Copy a [N, K] weight (formats and layouts of moe_load_weights) into the library; returns its handle."""
+    h = ctypes.c_void_p()
+    _check(lib.moe_linear_load(N, K, fmt, ctypes.byref(MoeMx(_ptr(codes), _ptr(scales), _ptr(zeros))),
+                               _stream(stream), ctypes.byref(h)))
+    return h.value
+
+
+def moe_linear_workspace_bytes(handle: int, T: int) -> int:
+    return int(lib.moe_linear_workspace_bytes(handle, T))
+
+
+def moe_linear_forward(handle: int, x, x_scales, y, accumulate: bool = False, workspace=None, ws_bytes: int = 0,
+                       stream=None) -> None:
+    """y = x W^T (see include/moe.h): x is bfloat16 [T, K], or float8_e4m3fn [T, K] with x_scales uint8 [T, K/32];
+    y is float32 or bfloat16 [T, N]."""
+    xp, xt, xld = _rows(x, "x")
+    yp, yt, yld = _rows(y, "y")
+    _check(lib.moe_linear_forward(handle, xp, xt, xld, _ptr(x_scales), x.shape[0], yp, yt, yld,
+                                  int(bool(accumulate)), _ptr(workspace), ws_bytes, _stream(stream)))
+
+
+def moe_linear_sync_status(handle: int, stream=None) -> None:
+    _check(lib.moe_linear_sync_status(handle, _stream(stream)))
+
+
+def moe_linear_free(handle: int) -> None:
+    lib.moe_linear_free(handle)
 
 
 def routing_out(topk_ids=None, topk_w=None, expert_offsets=None, sorted_slot=None, slot_pos=None) -> MoeRoutingOut:

@@ -1,0 +1,84 @@
+"""A linear layer with 4-bit or BF16 weights held by the library.
+
+torch is used only for device memory and streams; the products run in
+libmoe_gb300.so through ``binding``.
+"""
+from __future__ import annotations
+
+from typing import Optional
+
+import torch
+
+from . import binding as B
+
+FORMATS = {"mxfp4": B.MOE_W_MXFP4, "bf16": B.MOE_W_BF16, "int4g32": B.MOE_W_INT4G32}
+
+
+class QuantLinear:
+    """y = x W^T for a weight W [N, K] in one of the library's formats.
+
+    * "mxfp4": codes uint8 [N, K/2], scales uint8 (E8M0) [N, K/32]
+    * "int4g32": codes uint8 [N, K/2], scales float16 [N, K/32], zeros uint8 [N, K/32] or None (all 8)
+    * "bf16": codes bfloat16 [N, K]
+
+    The library keeps its own copy: the tensors given here may be freed.
+    """
+
+    def __init__(self, fmt: str, codes: torch.Tensor, scales: Optional[torch.Tensor] = None,
+                 zeros: Optional[torch.Tensor] = None, stream=None):
+        self.handle = None
+        if fmt not in FORMATS:
+            raise B.MoeError(B.MOE_EINVAL, f"unknown weight format {fmt!r}")
+        if codes.dim() != 2:
+            raise B.MoeError(B.MOE_EINVAL, "codes: a [N, K] or [N, K/2] matrix is needed")
+        self.fmt = fmt
+        self.N, self.K = codes.shape[0], codes.shape[1] * (1 if fmt == "bf16" else 2)
+        want = {"mxfp4": (torch.uint8, torch.uint8), "int4g32": (torch.uint8, torch.float16),
+                "bf16": (torch.bfloat16, None)}[fmt]
+        self._dense("codes", codes, want[0], codes.shape)
+        if want[1] is not None:
+            if scales is None:
+                raise B.MoeError(B.MOE_EINVAL, f"{fmt} weights have scales")
+            self._dense("scales", scales, want[1], (self.N, self.K // 32))
+        if fmt == "int4g32" and zeros is not None:
+            self._dense("zeros", zeros, torch.uint8, (self.N, self.K // 32))
+        self.device = codes.device
+        self.handle = B.moe_linear_load(self.N, self.K, FORMATS[fmt], codes, scales, zeros, stream)
+
+    @staticmethod
+    def _dense(name, t, dtype, shape):
+        if t.dtype != dtype or tuple(t.shape) != tuple(shape) or not t.is_contiguous():
+            raise B.MoeError(B.MOE_EINVAL, f"{name}: a dense {dtype} tensor of shape {tuple(shape)} is needed, "
+                                           f"not {t.dtype} {tuple(t.shape)}")
+
+    def forward(self, x: torch.Tensor, x_scales: Optional[torch.Tensor] = None, out: Optional[torch.Tensor] = None,
+                accumulate: bool = False, stream=None) -> torch.Tensor:
+        """x: bfloat16 [T, K], or float8_e4m3fn [T, K] with x_scales uint8 [T, K/32] (MXFP8 rows).
+        out: float32 (the default) or bfloat16 [T, N]; accumulate adds to a float32 out."""
+        if x.dim() != 2 or x.shape[1] != self.K:
+            raise B.MoeError(B.MOE_EINVAL, f"x: shape {tuple(x.shape)} where [T, {self.K}] is needed")
+        T = x.shape[0]
+        if x_scales is not None and (tuple(x_scales.shape) != (T, self.K // 32) or not x_scales.is_contiguous()):
+            raise B.MoeError(B.MOE_EINVAL, f"x_scales: a dense [{T}, {self.K // 32}] tensor is needed")
+        if out is None:
+            if accumulate:
+                raise B.MoeError(B.MOE_EINVAL, "accumulate needs an out to add to")
+            out = torch.empty((T, self.N), dtype=torch.float32, device=self.device)
+        elif tuple(out.shape) != (T, self.N):
+            raise B.MoeError(B.MOE_EINVAL, f"out: shape {tuple(out.shape)} where ({T}, {self.N}) is needed")
+        B.moe_linear_forward(self.handle, x, x_scales, out, accumulate, stream=stream)
+        return out
+
+    def sync(self, stream=None):
+        B.moe_linear_sync_status(self.handle, stream)
+
+    def free(self):
+        if self.handle:
+            B.moe_linear_free(self.handle)
+            self.handle = None
+
+    def __del__(self):
+        try:
+            self.free()
+        except Exception:
+            pass

@@ -1,0 +1,108 @@
+"""Refusals of the operators around the layer that need no GPU: every argument
+is checked on the host before any CUDA call."""
+import ctypes
+
+import pytest
+
+
+@pytest.fixture(scope="module")
+def b():
+    from mxfp4_routed_expert_router_gb300 import build
+    build.build()
+    from mxfp4_routed_expert_router_gb300 import binding
+    return binding
+
+
+NORM = dict(residual=256, rt=0, rld=64, delta=256, dt=0, dld=64, gain=256, gt=1, eps=1e-6, T=2, H=64, sum=256, sld=64,
+            y=256, yld=64, q=256, qld=64, qs=256)
+
+
+def _norm(b, **kw):
+    v = {**NORM, **kw}
+    return b.lib.moe_add_rmsnorm(*[v[k] for k in NORM], None)
+
+
+@pytest.mark.parametrize("kw,status", [
+    (dict(T=-1), "MOE_EINVAL"), (dict(T=(1 << 24) + 1), "MOE_EINVAL"), (dict(H=0), "MOE_EDIMS"),
+    (dict(H=48), "MOE_EDIMS"), (dict(H=65568), "MOE_EDIMS"), (dict(rt=2), "MOE_EINVAL"), (dict(dt=2), "MOE_EINVAL"),
+    (dict(gt=-1), "MOE_EINVAL"), (dict(eps=-1.0), "MOE_EINVAL"), (dict(eps=float("nan")), "MOE_EINVAL"),
+    (dict(eps=float("inf")), "MOE_EINVAL"), (dict(residual=None), "MOE_EINVAL"),
+    (dict(sum=None, y=None, q=None), "MOE_EINVAL"), (dict(qs=None), "MOE_EINVAL"), (dict(rld=63), "MOE_EINVAL"),
+    (dict(dld=32), "MOE_EINVAL"), (dict(sld=0), "MOE_EINVAL"), (dict(yld=-64), "MOE_EINVAL"), (dict(qld=8), "MOE_EINVAL"),
+    (dict(residual=264), "MOE_EINVAL"), (dict(rld=68), "MOE_EINVAL"), (dict(delta=258), "MOE_EINVAL"),
+    (dict(y=272 + 2), "MOE_EINVAL"), (dict(q=257), "MOE_EINVAL"), (dict(qld=72), "MOE_EINVAL"),
+    (dict(gain=260), "MOE_EINVAL"), (dict(T=0), "MOE_OK"), (dict(T=0, residual=None), "MOE_OK"),
+])
+def test_norm_refusals(b, kw, status):
+    assert _norm(b, **kw) == getattr(b, status)
+
+
+ROUTE = dict(logits=256, bias=256, T=2, E=64, k=4, G=8, KG=2, score=1, gs=1, renorm=1, scale=1.0, ids=256, w=256)
+
+
+def _route(b, **kw):
+    v = {**ROUTE, **kw}
+    return b.lib.moe_route_grouped(*[v[k] for k in ROUTE], None)
+
+
+@pytest.mark.parametrize("kw,status", [
+    (dict(T=-1), "MOE_EINVAL"), (dict(T=(1 << 24) + 1), "MOE_EINVAL"), (dict(E=0), "MOE_EINVAL"),
+    (dict(E=1025), "MOE_EINVAL"), (dict(G=0), "MOE_EINVAL"), (dict(G=7), "MOE_EINVAL"), (dict(G=64), "MOE_EINVAL"),
+    (dict(KG=0), "MOE_EINVAL"), (dict(KG=9), "MOE_EINVAL"), (dict(k=0), "MOE_EINVAL"), (dict(k=17), "MOE_EINVAL"),
+    (dict(k=33, KG=8), "MOE_EINVAL"), (dict(score=2), "MOE_EINVAL"), (dict(gs=-1), "MOE_EINVAL"),
+    (dict(logits=None), "MOE_EINVAL"), (dict(ids=None), "MOE_EINVAL"), (dict(w=None), "MOE_EINVAL"),
+    (dict(logits=258), "MOE_EINVAL"), (dict(bias=257), "MOE_EINVAL"), (dict(ids=262), "MOE_EINVAL"),
+    (dict(T=0), "MOE_OK"), (dict(T=0, logits=None), "MOE_OK"),
+])
+def test_route_refusals(b, kw, status):
+    assert _route(b, **kw) == getattr(b, status)
+
+
+def test_linear_refusals(b):
+    L = b.lib
+    h = ctypes.c_void_p()
+    mx = b.MoeMx(256, 256, None)
+
+    def load(N=16, K=64, fmt=b.MOE_W_MXFP4, w=mx, out=h):
+        return L.moe_linear_load(N, K, fmt, None if w is None else ctypes.byref(w), None,
+                                 None if out is None else ctypes.byref(out))
+
+    assert load(w=None) == b.MOE_EINVAL and load(out=None) == b.MOE_EINVAL
+    assert load(fmt=5) == b.MOE_EINVAL
+    assert load(N=0) == b.MOE_EINVAL and load(N=(1 << 20) + 1) == b.MOE_EINVAL
+    for K in (0, 31, 48, 65568):
+        assert load(K=K) == b.MOE_EDIMS
+    assert load(w=b.MoeMx(None, 256, None)) == b.MOE_EINVAL
+    assert load(w=b.MoeMx(256, None, None)) == b.MOE_EINVAL
+    assert load(fmt=b.MOE_W_INT4G32, w=b.MoeMx(256, 257, None)) == b.MOE_EINVAL
+    assert b"2-byte aligned" in L.moe_last_error()
+    assert h.value is None
+    assert L.moe_linear_forward(None, 256, 0, 64, None, 1, 256, 1, 16, 0, None, 0, None) == b.MOE_EINVAL
+    assert L.moe_linear_workspace_bytes(None, 4) == 0
+    assert L.moe_linear_sync_status(None, None) == b.MOE_EINVAL
+    L.moe_linear_free(None)  # no-op
+
+
+def test_wrappers_check_shapes_and_types(b):
+    import torch
+    from mxfp4_routed_expert_router_gb300.linear import QuantLinear
+    x = torch.zeros((3, 64))
+    for call in (lambda: b.moe_add_rmsnorm(x, x[:2], None, 1e-6, x),
+                 lambda: b.moe_add_rmsnorm(x, None, torch.ones(63), 1e-6, x),
+                 lambda: b.moe_add_rmsnorm(x, None, None, 1e-6, x.bfloat16()),
+                 lambda: b.moe_add_rmsnorm(x, None, None, 1e-6, None, x),
+                 lambda: b.moe_add_rmsnorm(x.half(), None, None, 1e-6, x.half()),
+                 lambda: b.moe_add_rmsnorm(x.t(), None, None, 1e-6, None),
+                 lambda: b.moe_add_rmsnorm(x, None, None, 1e-6, None, None, x.to(torch.float8_e4m3fn),
+                                           torch.zeros((3, 3), dtype=torch.uint8)),
+                 lambda: QuantLinear("mxfp3", x),
+                 lambda: QuantLinear("mxfp4", x, x),
+                 lambda: QuantLinear("mxfp4", torch.zeros((4, 32), dtype=torch.uint8)),
+                 lambda: QuantLinear("mxfp4", torch.zeros((4, 32), dtype=torch.uint8),
+                                     torch.zeros((4, 3), dtype=torch.uint8)),
+                 lambda: QuantLinear("int4g32", torch.zeros((4, 32), dtype=torch.uint8),
+                                     torch.zeros((4, 2), dtype=torch.uint8)),
+                 lambda: QuantLinear("bf16", torch.zeros((4, 64)))):
+        with pytest.raises(b.MoeError) as e:
+            call()
+        assert e.value.status == b.MOE_EINVAL
