@@ -132,10 +132,27 @@ def _ptr(t) -> Optional[int]:
     return t.data_ptr()
 
 
+def _current_stream() -> int:
+    """torch's current stream on the current device, as a cudaStream_t (without building a torch.cuda.Stream: that
+    costs as much as a launch)."""
+    global _current_stream
+    import torch
+    try:
+        raw, device = torch._C._cuda_getCurrentRawStream, torch._C._cuda_getDevice
+        raw(device())
+    except AttributeError:
+        def current():
+            return torch.cuda.current_stream().cuda_stream
+    else:
+        def current():
+            return raw(device())
+    _current_stream = current
+    return current()
+
+
 def _stream(stream) -> Optional[int]:
     if stream is None:
-        import torch
-        return torch.cuda.current_stream().cuda_stream
+        return _current_stream()
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
@@ -257,65 +274,73 @@ def moe_free(handle: int) -> None:
     lib.moe_free(handle)
 
 
-def _rows(t, name: str) -> Tuple[Optional[int], int, int]:
-    """Address, row type and row stride (elements) of a [T, H] tensor, (None, 0, 0) for None."""
-    if t is None:
-        return None, 0, 0
-    ty = _row_types().get(t.dtype)
-    if ty is None:
-        raise MoeError(MOE_EINVAL, f"{name}: rows are bfloat16, float32 or float8_e4m3fn, not {t.dtype}")
-    if t.dim() != 2 or (t.shape[1] > 1 and t.stride(1) != 1):
-        raise MoeError(MOE_EINVAL, f"{name}: a [T, H] tensor whose rows have no gaps is needed")
-    return t.data_ptr(), ty, (t.stride(0) if t.shape[0] > 1 else t.shape[1])
-
-
 _ROW_TYPES = {}
 
 
-def _row_types() -> dict:
+def _row_type(dtype) -> int:
+    """The row type of a torch dtype, -1 for one that has none."""
     if not _ROW_TYPES:
         import torch
         _ROW_TYPES.update({torch.bfloat16: MOE_ROWS_BF16, torch.float32: MOE_ROWS_F32,
                            torch.float8_e4m3fn: MOE_ROWS_MXFP8})
-    return _ROW_TYPES
+    return _ROW_TYPES.get(dtype, -1)
 
 
-def _same_rows(name: str, t, T: int, H: int) -> None:
-    if t is not None and tuple(t.shape) != (T, H):
-        raise MoeError(MOE_EINVAL, f"{name}: shape {tuple(t.shape)} where ({T}, {H}) is needed")
+def _rows(t, name: str, shape):
+    """Address, row type and row stride (elements) of a tensor of rows of that shape, (None, 0, 0) for None."""
+    if t is None:
+        return None, 0, 0
+    if t.shape != shape:
+        raise MoeError(MOE_EINVAL, f"{name}: shape {tuple(t.shape)} where {tuple(shape)} is needed")
+    ty = _ROW_TYPES.get(t.dtype, -1)
+    if ty < 0 and (ty := _row_type(t.dtype)) < 0:
+        raise MoeError(MOE_EINVAL, f"{name}: rows are bfloat16, float32 or float8_e4m3fn, not {t.dtype}")
+    ld, step = t.stride()
+    if step != 1 and shape[1] > 1:
+        raise MoeError(MOE_EINVAL, f"{name}: the values of a row must lie side by side")
+    return t.data_ptr(), ty, (ld if shape[0] > 1 else shape[1])
 
 
 def moe_add_rmsnorm(residual, delta, gain, eps: float, sum=None, y=None, q=None, q_scales=None, stream=None) -> None:
     """s = residual + delta, the RMS norm of s times gain as BF16 rows (y) and MXFP8 rows (q, q_scales); see
     include/moe.h.  residual, delta and sum are bfloat16 or float32 [T, H] tensors, y bfloat16, q float8_e4m3fn,
     q_scales uint8 [T, H/32]; delta, gain and any output may be None, and sum may be residual itself."""
-    T, H = residual.shape
-    for name, t in (("delta", delta), ("sum", sum), ("y", y), ("q", q)):
-        _same_rows(name, t, T, H)
-    if gain is not None and (tuple(gain.shape) != (H,) or not gain.is_contiguous()):
-        raise MoeError(MOE_EINVAL, f"gain: a dense vector of {H} values is needed")
-    if q_scales is not None and (tuple(q_scales.shape) != (T, H // 32) or not q_scales.is_contiguous()
-                                 or q_scales.element_size() != 1):
-        raise MoeError(MOE_EINVAL, f"q_scales: a dense uint8 [{T}, {H // 32}] tensor is needed")
-    r, rt, rld = _rows(residual, "residual")
-    d, dt, dld = _rows(delta, "delta")
-    s, sty, sld = _rows(sum, "sum")
-    yp, yt, yld = _rows(y, "y")
-    qp, qt, qld = _rows(q, "q")
-    if s is not None and sty != rt:
+    shape = residual.shape
+    if len(shape) != 2:
+        raise MoeError(MOE_EINVAL, "residual: a [T, H] tensor is needed")
+    T, H = shape
+    r, rt, rld = _rows(residual, "residual", shape)
+    d, dt, dld = _rows(delta, "delta", shape)
+    s, sty, sld = _rows(sum, "sum", shape)
+    yp, yt, yld = _rows(y, "y", shape)
+    qp, qt, qld = _rows(q, "q", shape)
+    if sty != rt and s is not None:
         raise MoeError(MOE_EINVAL, "sum: the residual's type is needed")
-    if (yp is not None and yt != MOE_ROWS_BF16) or (qp is not None and qt != MOE_ROWS_MXFP8):
+    if yt != MOE_ROWS_BF16 or (qt != MOE_ROWS_MXFP8 and qp is not None):
         raise MoeError(MOE_EINVAL, "y is bfloat16 and q float8_e4m3fn")
-    gt = 0 if gain is None else _row_types().get(gain.dtype, -1)
-    _check(lib.moe_add_rmsnorm(r, rt, rld, d, dt, dld, _ptr(gain), gt, eps, T, H, s, sld, yp, yld, qp, qld,
-                               _ptr(q_scales), _stream(stream)))
+    g = gt = 0
+    if gain is not None:
+        if gain.shape != (H,) or not gain.is_contiguous():
+            raise MoeError(MOE_EINVAL, f"gain: a dense vector of {H} values is needed")
+        g, gt = gain.data_ptr(), _row_type(gain.dtype)
+    qs = None
+    if q_scales is not None:
+        if q_scales.shape != (T, H // 32) or not q_scales.is_contiguous() or q_scales.element_size() != 1:
+            raise MoeError(MOE_EINVAL, f"q_scales: a dense uint8 [{T}, {H // 32}] tensor is needed")
+        qs = q_scales.data_ptr()
+    status = lib.moe_add_rmsnorm(r, rt, rld, d, dt, dld, g, gt, eps, T, H, s, sld, yp, yld, qp, qld, qs,
+                                 _stream(stream))
+    if status:
+        _check(status)
 
 
 def moe_route_grouped(router_logits, bias, T: int, E: int, k: int, n_groups: int, k_groups: int, score: int,
                       group_score: int, renormalize: bool, scale: float, topk_ids, topk_w, stream=None) -> None:
     """Group-limited routing (see include/moe.h); the outputs feed moe_forward_routed."""
-    _check(lib.moe_route_grouped(_ptr(router_logits), _ptr(bias), T, E, k, n_groups, k_groups, score, group_score,
-                                 int(bool(renormalize)), scale, _ptr(topk_ids), _ptr(topk_w), _stream(stream)))
+    status = lib.moe_route_grouped(_ptr(router_logits), _ptr(bias), T, E, k, n_groups, k_groups, score, group_score,
+                                   bool(renormalize), scale, _ptr(topk_ids), _ptr(topk_w), _stream(stream))
+    if status:
+        _check(status)
 
 
 def moe_linear_load(N: int, K: int, fmt: int, codes, scales=None, zeros=None, stream=None) -> int:
@@ -334,10 +359,14 @@ def moe_linear_forward(handle: int, x, x_scales, y, accumulate: bool = False, wo
                        stream=None) -> None:
     """y = x W^T (see include/moe.h): x is bfloat16 [T, K], or float8_e4m3fn [T, K] with x_scales uint8 [T, K/32];
     y is float32 or bfloat16 [T, N]."""
-    xp, xt, xld = _rows(x, "x")
-    yp, yt, yld = _rows(y, "y")
-    _check(lib.moe_linear_forward(handle, xp, xt, xld, _ptr(x_scales), x.shape[0], yp, yt, yld,
-                                  int(bool(accumulate)), _ptr(workspace), ws_bytes, _stream(stream)))
+    if x.dim() != 2 or y.dim() != 2 or x.shape[0] != y.shape[0]:
+        raise MoeError(MOE_EINVAL, f"x {tuple(x.shape)} and y {tuple(y.shape)}: [T, K] and [T, N] are needed")
+    xp, xt, xld = _rows(x, "x", x.shape)
+    yp, yt, yld = _rows(y, "y", y.shape)
+    status = lib.moe_linear_forward(handle, xp, xt, xld, _ptr(x_scales), x.shape[0], yp, yt, yld, bool(accumulate),
+                                    _ptr(workspace), ws_bytes, _stream(stream))
+    if status:
+        _check(status)
 
 
 def moe_linear_sync_status(handle: int, stream=None) -> None:
