@@ -32,12 +32,14 @@ namespace moe {
 
 namespace {
 
-constexpr int WARPS = 8, THREADS = WARPS * 32;
+using gemm::smem_addr;
+
+constexpr int WARPS = 16, THREADS = WARPS * 32;
 constexpr int UNIT_BYTES = 16 * CHUNK_K / 2;  // 1024: codes of 16 rows of a chunk
 
 struct LinArgs {
     const uint8_t *w;
-    int N, K, kchunks, chunk_bytes;
+    int N, K, kchunks;
     const void *x;
     const uint8_t *xscales;
     long long x_ld;
@@ -46,9 +48,9 @@ struct LinArgs {
     void *y;
     long long y_ld;
     int y_f32, accumulate;
-    int kw;             // warps of a CTA that split its K range (1, 2, 4, 8)
-    int pairs;          // 256-value steps of K: ceil(kchunks / 2)
-    int xs_off, red_off;  // shared-memory offsets (bytes) of the token scales and block sums, and of the partial sums
+    int steps;          // steps of K (step_chunks)
+    int rgroups;        // groups of 16 rows per CTA
+    int xs_off, sum_off, red_off, fin_off;  // shared-memory offsets (bytes), see linear_kernel
 };
 
 __device__ __forceinline__ uint4 ldg_stream(const uint8_t *p)
@@ -119,46 +121,110 @@ __device__ __forceinline__ float2 half_pair(uint32_t w)
     return __half22float2(*reinterpret_cast<const __half2 *>(&w));
 }
 
-// 2^e as a product of two floats for any e that the callers have (|e| <= 252)
-__device__ __forceinline__ float scale_pow2(float v, int e)
+// exponent e of the power of two that FP16 x is divided by, from the bits of
+// max |x|: max |x| * 2^-e in [2^14, 2^15), or below for rows of tiny values, whose
+// e stops at -127
+__device__ __forceinline__ int x_exponent(uint32_t max_bits) { return max((int)(max_bits >> 23) - 141, -127); }
+
+// 2^e for -127 <= e <= 127
+__device__ __forceinline__ float pow2f(int e) { return __int_as_float(e < -126 ? 0x400000 : (127 + e) << 23); }
+
+// 8 values of token row t from column k (a multiple of 8; zeros from kend, a
+// multiple of 32) as they lie in memory: BF16, or E4M3 in x, y and the block's
+// E8M0 byte in z.
+__device__ __forceinline__ uint4 load_x8(const LinArgs &a, long long t, int k, int kend)
 {
-    const int h = e / 2;
-    return v * __int_as_float((127 + h) << 23) * __int_as_float((127 + e - h) << 23);
+    uint4 u = make_uint4(0, 0, 0, 0);
+    if (k < kend) {
+        if (a.x_mx) {
+            const uint2 c = __ldg(reinterpret_cast<const uint2 *>(static_cast<const uint8_t *>(a.x) + t * a.x_ld + k));
+            u = make_uint4(c.x, c.y, __ldg(a.xscales + t * (a.K / 32) + k / 32), 0);
+        } else {
+            u = __ldg(reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(a.x) + t * a.x_ld + k));
+        }
+    }
+    return u;
 }
 
-// 8 values of token row t from column k (k and K are multiples of 8 and 32; zeros past K)
-__device__ __forceinline__ void load_x8(const LinArgs &a, long long t, int k, float v[8])
+// E4M3 pairs of load_x8 as FP16 pairs (exact); NaN where the scale byte is 255
+__device__ __forceinline__ void e4m3_f16(const uint4 &u, uint32_t h[4])
 {
-    if (k >= a.K) {
+    const uint32_t w[2] = {u.x, u.y};
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
-            v[i] = 0.f;
-        return;
+    for (int i = 0; i < 4; ++i) {
+        const uint16_t c = (uint16_t)(w[i >> 1] >> (16 * (i & 1)));
+        asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h[i]) : "h"(c));
+        if (u.z == 255u)
+            h[i] = 0x7FFF7FFFu;
     }
+}
+
+// The same values as BF16 pairs (E4M3 times a power of two: exact inside BF16's range).
+__device__ __forceinline__ void x8_bf16(const LinArgs &a, const uint4 &u, uint32_t o[4])
+{
     if (a.x_mx) {
-        const uint2 u = __ldg(reinterpret_cast<const uint2 *>(static_cast<const uint8_t *>(a.x) + t * a.x_ld + k));
-        const int e = __ldg(a.xscales + t * (a.K / 32) + k / 32);
-        const float s = e == 255 ? __int_as_float(0x7FC00000) : __int_as_float(e ? e << 23 : 0x400000);
-        const uint32_t w[2] = {u.x, u.y};
+        uint32_t h[4];
+        e4m3_f16(u, h);
+        const float s = pow2f((int)u.z - 127);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            const uint16_t c = (uint16_t)(w[i >> 1] >> (16 * (i & 1)));
-            uint32_t h;
-            asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"(c));
-            const float2 f = half_pair(h);
-            v[2 * i] = f.x * s;
-            v[2 * i + 1] = f.y * s;
+            const float2 f = half_pair(h[i]);
+            const __nv_bfloat162 b = __floats2bfloat162_rn(f.x * s, f.y * s);
+            o[i] = *reinterpret_cast<const uint32_t *>(&b);
         }
     } else {
-        const uint4 u =
-            __ldg(reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(a.x) + t * a.x_ld + k));
-        const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+        o[0] = u.x, o[1] = u.y, o[2] = u.z, o[3] = u.w;
+    }
+}
+
+// The same values of a warp's 32 vectors as FP16 pairs times 2^-e, with e from
+// the largest of them; returns e.
+__device__ __forceinline__ int x8_f16(const LinArgs &a, const uint4 &u, uint32_t o[4])
+{
+    float f[8];
+    float m;
+    int es = 0;
+    if (a.x_mx) {
+        uint32_t h[4];
+        e4m3_f16(u, h);
+        es = (int)u.z - 127;
+        m = 0.f;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            v[2 * i] = __uint_as_float(w[i] << 16);
-            v[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+            const float2 p = half_pair(h[i]);
+            f[2 * i] = p.x;
+            f[2 * i + 1] = p.y;
+            m = fmaxf(m, fmaxf(fabsf(p.x), fabsf(p.y)));  // (NaN is left out and stays NaN in FP16)
         }
+        m *= pow2f(es);
+    } else {
+        const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+        uint32_t mx = 0;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            mx = __vmaxu2(mx, w[i] & 0x7FFF7FFFu);
+            f[2 * i] = __uint_as_float(w[i] << 16);
+            f[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+        }
+        m = __uint_as_float(max(mx & 0xFFFF0000u, mx << 16));
     }
+    const int e = x_exponent(__reduce_max_sync(0xffffffffu, __float_as_uint(m)));
+    const float mul = pow2f(max(-127, min(127, es - e)));
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const __half2 hh = __floats2half2_rn(f[2 * i] * mul, f[2 * i + 1] * mul);
+        o[i] = *reinterpret_cast<const uint32_t *>(&hh);
+    }
+    return e;
+}
+
+// 16 bytes of shared memory into registers where on != 0 (others keep theirs)
+__device__ __forceinline__ void lds16_if(uint32_t on, uint32_t addr, uint32_t r[4])
+{
+    asm volatile("{\n .reg .pred p;\n setp.ne.u32 p, %4, 0;\n @p ld.shared.v4.u32 {%0,%1,%2,%3}, [%5];\n}"
+                 : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3])
+                 : "r"(on), "r"(addr)
+                 : "memory");
 }
 
 __device__ __forceinline__ void cluster_sync()
@@ -166,140 +232,243 @@ __device__ __forceinline__ void cluster_sync()
     asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 
-// registers of one 256-value step of 16 rows
+// chunks of a step of K (256 values with 4-bit weights, 128 with BF16 weights)
 template <int FMT>
+constexpr int step_chunks = FMT == FMT_BF16 ? 1 : 2;
+template <int FMT>
+constexpr int chunk_bytes = FMT == FMT_MXFP4 ? CHUNK_MX_BYTES : FMT == FMT_INT4 ? CHUNK_I4_BYTES : CHUNK_BF16_BYTES;
+
+// Registers of one step of 16 rows.  Scales are those of this lane's columns:
+// with eight blocks side by side (NB = 8) just the two blocks 2q, 2q + 1 of its
+// rows g and g + 8, else every block of both chunks.
+template <int FMT, int NB>
 struct Step {
-    uint4 c[FMT == FMT_BF16 ? 16 : 4];
-    uint4 s[2];  // INT4: FP16 scales of both chunks; MXFP4: E8M0 bytes in .x, .y
-    uint2 z[2];  // INT4: zero points
+    uint4 c[FMT == FMT_BF16 ? 8 : 4];
+};
+template <int NB>
+struct Step<FMT_MXFP4, NB> {
+    uint4 c[4];
+    uint2 e[2];  // chunk: E8M0 bytes of row g, row g + 8
+};
+template <>
+struct Step<FMT_MXFP4, 8> {
+    uint4 c[4];
+    uint32_t ea, eb;  // 16 bits each
+};
+template <int NB>
+struct Step<FMT_INT4, NB> {
+    uint4 c[4];
+    uint4 s[2];  // chunk: FP16 scales of row g (x, y), row g + 8 (z, w)
+    uint2 z[2];  // chunk: zero points of row g, row g + 8
+};
+template <>
+struct Step<FMT_INT4, 8> {
+    uint4 c[4];
+    uint32_t sa, sb, za, zb;
 };
 
-// One CTA: WARPS / kw groups of 16 rows, its K range (the whole of K, or a
-// share of a cluster's) split over kw warps by steps of 256 values; up to TB * NT
-// tokens.  blockIdx.x = row tile * cluster size + rank, blockIdx.y = token tile.
+// Scales (and zero points) of the lane's columns 2q, 2q + 1 for rows g (a) and
+// g + 8 (b) of block group `grp` (NB blocks) of a step.
+struct ColScales {
+    float2 a, b, za, zb;
+};
+
+template <int FMT, int NB>
+__device__ __forceinline__ ColScales col_scales(const Step<FMT, NB> &s, int grp, int q)
+{
+    ColScales r;
+    r.za = r.zb = make_float2(0.f, 0.f);
+    if constexpr (NB == 8 && FMT == FMT_MXFP4) {
+        r.a = e8m0_pair(s.ea);
+        r.b = e8m0_pair(s.eb);
+    } else if constexpr (NB == 8) {
+        r.a = half_pair(s.sa);
+        r.b = half_pair(s.sb);
+        r.za = make_float2((float)(s.za & 255u), (float)(s.za >> 8));
+        r.zb = make_float2((float)(s.zb & 255u), (float)(s.zb >> 8));
+    } else {
+        const int h = grp * NB / 4;  // chunk
+        // which half of the chunk's four blocks: NB = 4 by lane, else by group
+        const bool second = NB == 4 ? (q & 1) != 0 : NB == 2 ? (grp & 1) != 0 : ((grp & 3) >> 1) != 0;
+        if constexpr (FMT == FMT_MXFP4) {
+            r.a = e8m0_pair(second ? s.e[h].x >> 16 : s.e[h].x);
+            r.b = e8m0_pair(second ? s.e[h].y >> 16 : s.e[h].y);
+        } else {
+            r.a = half_pair(second ? s.s[h].y : s.s[h].x);
+            r.b = half_pair(second ? s.s[h].w : s.s[h].z);
+            const uint32_t z0 = second ? s.z[h].x >> 16 : s.z[h].x, z1 = second ? s.z[h].y >> 16 : s.z[h].y;
+            r.za = make_float2((float)(z0 & 255u), (float)((z0 >> 8) & 255u));
+            r.zb = make_float2((float)(z1 & 255u), (float)((z1 >> 8) & 255u));
+        }
+        if constexpr (NB == 1) {  // both columns are the same block
+            const bool odd = grp & 1;
+            r.a.x = r.a.y = odd ? r.a.y : r.a.x;
+            r.b.x = r.b.y = odd ? r.b.y : r.b.x;
+            r.za.x = r.za.y = odd ? r.za.y : r.za.x;
+            r.zb.x = r.zb.y = odd ? r.zb.y : r.zb.x;
+        }
+    }
+    return r;
+}
+
+// Steps are cut evenly: warp w of n takes steps [w * units / n, (w + 1) * units
+// / n) of the CTA's row groups laid end to end; the warp that holds step u:
+__device__ __forceinline__ int owner_of(int u, int units, int n) { return ((u + 1) * n - 1) / units; }
+
+// One CTA: `rgroups` groups of 16 rows (fewer at the end), its K range (the
+// whole of K, or a share of a cluster's), up to TB * NT tokens.  x is staged
+// once; then every warp streams its share of the CTA's steps with DEPTH of them
+// in flight and writes a partial sum for each row group that it touches.
+// blockIdx.x = row tile * cluster size + rank, blockIdx.y = token tile.
 template <int FMT, int TB, int NT>
-__global__ void __launch_bounds__(THREADS) linear_kernel(const LinArgs a)
+__global__ void __launch_bounds__(THREADS, 1) linear_kernel(const __grid_constant__ LinArgs a)
 {
     constexpr int NB = 8 / TB;         // blocks side by side in the columns of one n-tile
     constexpr bool BF = FMT == FMT_BF16;
     constexpr int TT = TB * NT;        // tokens of a tile
+    constexpr int SC = step_chunks<FMT>, SB = SC * 4;  // chunks and 32-value blocks of a step
+    constexpr int BLK_BYTES = TT * 64;                 // B fragments of a block
+    constexpr int CB = chunk_bytes<FMT>;
     static_assert(NT == 1 || TB == 8, "several n-tiles hold 8 tokens each");
     extern __shared__ __align__(16) uint8_t smem[];
-    uint8_t *xf = smem;                                              // B fragments: [block][token][64 bytes]
-    int *xmax = reinterpret_cast<int *>(smem + a.xs_off);            // [TT] bits of max |x|
-    float *xsum = reinterpret_cast<float *>(smem + a.xs_off + 64);   // INT4: [block][token] sums of the FP16 values
-    float *red = reinterpret_cast<float *>(smem + a.red_off);        // [kw][token][rows of the CTA]
+    uint8_t *xf = smem;                                              // B fragments
+    float *xscale = reinterpret_cast<float *>(smem + a.xs_off);      // [256 values][TT] powers of two
+    float *xsum = reinterpret_cast<float *>(smem + a.sum_off);       // INT4: [block][TT] sums of the FP16 values
+    float *red = reinterpret_cast<float *>(smem + a.red_off);        // [warp + row group][token][16]
+    float *fin = reinterpret_cast<float *>(smem + a.fin_off);        // [row group][token][16] (clusters)
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, q = lane & 3;
     uint32_t crank, csize;
     asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(crank));
     asm("mov.u32 %0, %%cluster_nctarank;" : "=r"(csize));
-    const int rgroups = WARPS / a.kw;
-    const int tile = blockIdx.x / csize;
-    const int kwi = warp % a.kw, rwi = warp / a.kw;
-    const int rg = tile * rgroups + rwi;  // this warp's group of 16 rows
-    const int p0 = (int)((long long)a.pairs * crank / csize), p1 = (int)((long long)a.pairs * (crank + 1) / csize);
+    const int n16 = (a.N + 15) / 16;
+    const int rg0 = (int)(blockIdx.x / csize) * a.rgroups;
+    const int R = min(a.rgroups, n16 - rg0);
+    const int p0 = (int)((long long)a.steps * crank / csize), p1 = (int)((long long)a.steps * (crank + 1) / csize);
+    const int P = p1 - p0;
     const long long t0 = (long long)blockIdx.y * TT;
     const int tv = min(TT, (int)(a.T - t0));  // tokens of this tile
+    const int units = R * P, nw = min(WARPS, units);
+    const int u0 = nw ? min(units, warp * units / nw) : 0, u1 = nw ? min(units, (warp + 1) * units / nw) : 0;
 
-    // ---- weights of this warp's first steps are in flight while x is staged
-    const bool live = rg * 16 < a.N;
-    const uint8_t *wrow = a.w + (size_t)(rg >> 3) * a.kchunks * (size_t)a.chunk_bytes;
-    const int w8 = rg & 7;
-    auto load = [&](Step<FMT> &s, int p) {
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            const int kc = 2 * p + h;
-            const bool in = live && p < p1 && kc < a.kchunks;
-            const uint8_t *ch = wrow + (size_t)kc * a.chunk_bytes;
-            if (BF) {
-#pragma unroll
-                for (int j = 0; j < 8; ++j)
-                    s.c[(8 * h + j) % (BF ? 16 : 4)] =
-                        in ? ldg_stream(ch + ((w8 * 8 + j) * 32 + lane) * 16) : make_uint4(0, 0, 0, 0);
-            } else {
-#pragma unroll
-                for (int j = 0; j < 2; ++j)
-                    s.c[2 * h + j] = in ? ldg_stream(ch + w8 * UNIT_BYTES + j * 512 + lane * 16) : make_uint4(0, 0, 0, 0);
-                if (FMT == FMT_MXFP4) {
-                    const uint2 v = in ? ldg_stream8(ch + CHUNK_MX_CODE_BYTES + (w8 * 8 + g) * 8) : make_uint2(0, 0);
-                    s.s[h].x = v.x;
-                    s.s[h].y = v.y;
-                } else {
-                    s.s[h] = in ? ldg_stream(ch + CHUNK_MX_CODE_BYTES + (w8 * 8 + g) * 16) : make_uint4(0, 0, 0, 0);
-                    s.z[h] = in ? ldg_stream8(ch + CHUNK_MX_CODE_BYTES + CHUNK_I4_SCALE_BYTES + (w8 * 8 + g) * 8)
-                                : make_uint2(0, 0);
-                }
-            }
-        }
+    // ---- weights of this warp's first steps are in flight while x is staged.
+    // A step past the row's last chunk (an odd number of chunks) reads what
+    // follows in the store: x is zero there, and every code and scale is finite.
+    int lu = u0, lr = P ? u0 / P : 0, lp = P ? u0 % P : 0;  // load cursor: step, its row group and place in K
+    const uint8_t *wp = nullptr;  // the cursor's chunk
+    int w8 = 0;
+    auto locate = [&]() {
+        const int rg = rg0 + lr;
+        w8 = rg & 7;
+        wp = a.w + ((size_t)(rg >> 3) * a.kchunks + (size_t)(p0 + lp) * SC) * CB;
     };
-    constexpr int DEPTH = BF ? 1 : 2;
-    Step<FMT> st[DEPTH];
-    int p = p0 + kwi;
-#pragma unroll
-    for (int d = 0; d < DEPTH; ++d)
-        load(st[d], p + d * a.kw);
-
-    // ---- x: this CTA's columns of the tile's tokens, as B fragments.  FP16
-    // operands take x * 2^-e with e from the largest |x| of the token in these
-    // columns (in [2^14, 2^15) then): exact for BF16 and E4M3 values within
-    // 2^-29 of it.
-    const int nvec = (p1 - p0) * 32;  // vectors of 8 values per token
-    if (!BF) {
-        if (tid < TT)
-            xmax[tid] = 0;
-        __syncthreads();
-        for (int i = tid; i < tv * nvec; i += THREADS) {
-            const int t = i / nvec, c = i - t * nvec;
-            float v[8];
-            load_x8(a, t0 + t, p0 * 256 + 8 * c, v);
-            int m = 0;
+    if (u0 < u1)
+        locate();
+    auto load = [&](Step<FMT, NB> &s) {
+        if (lu >= u1)
+            return;
+        const uint8_t *code = wp + w8 * (BF ? 4096 : UNIT_BYTES) + lane * 16;
+        if constexpr (BF) {
 #pragma unroll
             for (int j = 0; j < 8; ++j)
-                m = max(m, __float_as_int(v[j]) & 0x7FFFFFFF);
-            // nvec is a multiple of 32: a warp's lanes hold one token
-            m = __reduce_max_sync(__activemask(), m);
-            if (lane == 0)
-                atomicMax(&xmax[t], m);
-        }
-        __syncthreads();
-    }
-    for (int i = tid; i < tv * nvec; i += THREADS) {
-        const int t = i / nvec, c = i - t * nvec;
-        float v[8];
-        load_x8(a, t0 + t, p0 * 256 + 8 * c, v);
-        uint32_t o[4];
-        if (BF) {
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const __nv_bfloat162 b = __floats2bfloat162_rn(v[2 * j], v[2 * j + 1]);
-                o[j] = *reinterpret_cast<const uint32_t *>(&b);
-            }
+                s.c[j] = ldg_stream(code + j * 512);
         } else {
-            const int m = xmax[t];
-            const int e = m == 0 ? 0 : (m >> 23) - 141;
-            float s = 0.f;
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const __half2 hh = __floats2half2_rn(scale_pow2(v[2 * j], -e), scale_pow2(v[2 * j + 1], -e));
-                o[j] = *reinterpret_cast<const uint32_t *>(&hh);
-                if (FMT == FMT_INT4) {
-                    const float2 f = __half22float2(hh);
-                    s += f.x + f.y;
+            for (int h = 0; h < 2; ++h) {
+                s.c[2 * h] = ldg_stream(code + h * CB);
+                s.c[2 * h + 1] = ldg_stream(code + h * CB + 512);
+            }
+            const uint8_t *sc = wp + CHUNK_MX_CODE_BYTES;
+            const int row = w8 * 8 + g;
+            if constexpr (FMT == FMT_MXFP4 && NB == 8) {
+                const uint8_t *p = sc + (q >> 1) * CB + row * 8 + (q & 1) * 2;
+                s.ea = __ldg(reinterpret_cast<const uint16_t *>(p));
+                s.eb = __ldg(reinterpret_cast<const uint16_t *>(p + 4));
+            } else if constexpr (FMT == FMT_MXFP4) {
+#pragma unroll
+                for (int h = 0; h < 2; ++h)
+                    s.e[h] = ldg_stream8(sc + h * CB + row * 8);
+            } else if constexpr (NB == 8) {
+                const uint8_t *p = sc + (q >> 1) * CB + row * 16 + (q & 1) * 4;
+                s.sa = __ldg(reinterpret_cast<const uint32_t *>(p));
+                s.sb = __ldg(reinterpret_cast<const uint32_t *>(p + 8));
+                const uint8_t *z = sc + (q >> 1) * CB + CHUNK_I4_SCALE_BYTES + row * 8 + (q & 1) * 2;
+                s.za = __ldg(reinterpret_cast<const uint16_t *>(z));
+                s.zb = __ldg(reinterpret_cast<const uint16_t *>(z + 4));
+            } else {
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    s.s[h] = ldg_stream(sc + h * CB + row * 16);
+                    s.z[h] = ldg_stream8(sc + h * CB + CHUNK_I4_SCALE_BYTES + row * 8);
                 }
             }
-            if (FMT == FMT_INT4) {
-                // four vectors (adjacent lanes) make a block
-                s += __shfl_xor_sync(__activemask(), s, 1);
-                s += __shfl_xor_sync(__activemask(), s, 2);
-                if ((lane & 3) == 0)
-                    xsum[(c >> 2) * tv + t] = s;
-            }
         }
-        // values 8c .. 8c+7 of the row: k step (c & 3) / 2 of the block, low or high eight
-        uint8_t *dst = xf + ((c >> 2) * tv + t) * 64 + ((c >> 1) & 1) * 8 + (c & 1) * 4;
+        ++lu;
+        wp += SC * CB;
+        if (++lp == P) {
+            lp = 0;
+            ++lr;
+            locate();
+        }
+    };
+    // ---- x: this CTA's columns of the tile's tokens as B fragments [block][token]
+    // [64 bytes].  An item is 256 values of one token, a vector of 8 per lane; a
+    // warp loads XB items at a time, the first before its weights.  FP16 operands
+    // take x * 2^-e, e from the item's largest |x| (in [2^14, 2^15) then): exact for
+    // BF16 and E4M3 values within 2^-29 of it.
+    constexpr int XB = 4;
+    const int items = (P * SB + 7) / 8 * TT;
+    const int k0 = p0 * SC * CHUNK_K;
+    const int kend = min(a.K, k0 + P * SC * CHUNK_K);
+    uint4 xr[XB];
+    auto load_items = [&](int i0) {
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
-            *reinterpret_cast<uint32_t *>(dst + j * 16) = o[j];
+        for (int b = 0; b < XB; ++b) {
+            const int i = i0 + b * WARPS, t = i % TT;
+            if (i < items && t < tv)
+                xr[b] = load_x8(a, t0 + t, k0 + (i / TT * 32 + lane) * 8, kend);
+        }
+    };
+    load_items(warp);
+    constexpr int DEPTH = BF ? 2 : 3;
+    Step<FMT, NB> st[DEPTH];
+#pragma unroll
+    for (int d = 0; d < DEPTH; ++d)
+        load(st[d]);
+    for (int i0 = warp; i0 < items; i0 += XB * WARPS) {
+#pragma unroll
+        for (int b = 0; b < XB; ++b) {
+            const int i = i0 + b * WARPS, t = i % TT;
+            if (i >= items || t >= tv)
+                continue;
+            const int c = i / TT * 32 + lane;  // vector of 8 values in this CTA's columns
+            uint32_t o[4];
+            if (BF) {
+                x8_bf16(a, xr[b], o);
+            } else {
+                const int e = x8_f16(a, xr[b], o);
+                if (lane == 0)
+                    xscale[i] = pow2f(e);
+                if (FMT == FMT_INT4) {
+                    float s = 0.f;
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        const float2 f = half_pair(o[j]);
+                        s += f.x + f.y;
+                    }
+                    // four vectors (adjacent lanes) make a block
+                    s += __shfl_xor_sync(0xffffffffu, s, 1);
+                    s += __shfl_xor_sync(0xffffffffu, s, 2);
+                    if ((lane & 3) == 0)
+                        xsum[(c >> 2) * TT + t] = s;
+                }
+            }
+            // values 8c .. 8c+7 of the row: k step (c & 3) / 2 of the block, low or high eight
+            uint8_t *dst = xf + ((c >> 2) * TT + t) * 64 + ((c >> 1) & 1) * 8 + (c & 1) * 4;
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                *reinterpret_cast<uint32_t *>(dst + j * 16) = o[j];
+        }
+        load_items(i0 + XB * WARPS);
     }
     __syncthreads();
 
@@ -310,179 +479,141 @@ __global__ void __launch_bounds__(THREADS) linear_kernel(const LinArgs a)
 #pragma unroll
         for (int j = 0; j < 4; ++j)
             acc[n][j] = 0.f;
-    // this lane's B column g: token and block (columns of tokens past tv repeat
-    // the last one; nothing reads their sums)
-    const int ctok = g / NB, cblk = g % NB;
-    auto compute = [&](const Step<FMT> &s, int pp) {
+    // B column g of the lane: token g / NB, block g % NB of a group; NB > 1: B of
+    // block i is zero in the lanes of the other columns, which never load it
+    uint32_t bx[NB][4];
+#pragma unroll
+    for (int i = 0; i < NB; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            bx[i][j] = 0u;
+    const uint32_t xb0 = smem_addr(xf) + (g / NB) * 64 + q * 16;
+    auto compute = [&](const Step<FMT, NB> &s, int p) {
         const uint32_t *cw = reinterpret_cast<const uint32_t *>(s.c);
-        const int blk0 = (pp - p0) * 8;
+        const uint32_t xb = xb0 + p * (SB * BLK_BYTES);
+        float sum[NT][4];  // of the step, in units of the tokens' powers of two
 #pragma unroll
-        for (int grp = 0; grp < 8 / NB; ++grp) {
+        for (int grp = 0; grp < SB / NB; ++grp) {
             float part[NT][4];
-            uint4 b[NT];
 #pragma unroll
-            for (int n = 0; n < NT; ++n) {
+            for (int n = 0; n < NT; ++n)
 #pragma unroll
                 for (int j = 0; j < 4; ++j)
                     part[n][j] = 0.f;
-                const int tok = min(8 * n + ctok, tv - 1);
-                b[n] = *reinterpret_cast<const uint4 *>(xf + ((blk0 + grp * NB + cblk) * tv + tok) * 64 + q * 16);
-            }
 #pragma unroll
             for (int i = 0; i < NB; ++i) {
                 const int blk = grp * NB + i;
                 uint32_t a0[4], a1[4];
-                if (BF) {
+                if constexpr (BF) {
 #pragma unroll
                     for (int j = 0; j < 4; ++j) {
-                        a0[j] = cw[(8 * blk + j) % (BF ? 64 : 16)];
-                        a1[j] = cw[(8 * blk + 4 + j) % (BF ? 64 : 16)];
+                        a0[j] = cw[8 * blk + j];
+                        a1[j] = cw[8 * blk + 4 + j];
                     }
-                } else if (FMT == FMT_MXFP4) {
-                    decode_e2m1(cw[2 * blk % 16], a0);
-                    decode_e2m1(cw[(2 * blk + 1) % 16], a1);
+                } else if constexpr (FMT == FMT_MXFP4) {
+                    decode_e2m1(cw[2 * blk], a0);
+                    decode_e2m1(cw[2 * blk + 1], a1);
                 } else {
-                    decode_u4(cw[2 * blk % 16], a0);
-                    decode_u4(cw[(2 * blk + 1) % 16], a1);
+                    decode_u4(cw[2 * blk], a0);
+                    decode_u4(cw[2 * blk + 1], a1);
                 }
 #pragma unroll
                 for (int n = 0; n < NT; ++n) {
-                    const bool on = NB == 1 || cblk == i;
-                    mma<BF>(BF ? acc[n] : part[n], a0, on ? b[n].x : 0u, on ? b[n].y : 0u);
-                    mma<BF>(BF ? acc[n] : part[n], a1, on ? b[n].z : 0u, on ? b[n].w : 0u);
+                    uint32_t *b = bx[i];
+                    lds16_if(NB == 1 || g % NB == i, xb + blk * BLK_BYTES + n * 512, b);
+                    mma<BF>(BF ? acc[n] : part[n], a0, b[0], b[1]);
+                    mma<BF>(BF ? acc[n] : part[n], a1, b[2], b[3]);
                 }
             }
-            if (BF)
-                continue;
-            // scales of this lane's columns 2q, 2q+1: blocks (of this group)
-            // NB = 8: 2q, 2q+1 (of both chunks); 4: 2(q&1), +1; 2: 0, 1; 1: the same block
-            const int h = NB == 8 ? 0 : grp * NB / 4;  // chunk (static; NB = 8 picks by lane)
-            float2 sa, sb, za = make_float2(0.f, 0.f), zb = za;
-            if (FMT == FMT_MXFP4) {
-                const bool hi = NB == 8 && q >= 2;
-                const uint32_t ra = hi ? s.s[1].x : s.s[h].x, rb = hi ? s.s[1].y : s.s[h].y;
-                // first byte of the pair inside the chunk's four
-                const int sh = NB >= 4 ? 16 * (q & 1) : NB == 2 ? 16 * (grp & 1) : 16 * ((grp & 3) >> 1);
-                sa = e8m0_pair(ra >> sh);
-                sb = e8m0_pair(rb >> sh);
-                if (NB == 1) {
-                    const float fa = (grp & 1) ? sa.y : sa.x, fb = (grp & 1) ? sb.y : sb.x;
-                    sa = make_float2(fa, fa);
-                    sb = make_float2(fb, fb);
-                }
-            } else {
-                const bool hi = NB == 8 && q >= 2;
-                const uint4 sv = hi ? s.s[1] : s.s[h];
-                const uint2 zv = hi ? s.z[1] : s.z[h];
-                const bool second = NB >= 4 ? (q & 1) : NB == 2 ? (grp & 1) : ((grp & 3) >> 1);
-                sa = half_pair(second ? sv.y : sv.x);
-                sb = half_pair(second ? sv.w : sv.z);
-                const uint32_t z0 = second ? zv.x >> 16 : zv.x, z1 = second ? zv.y >> 16 : zv.y;
-                za = make_float2((float)(z0 & 255u), (float)((z0 >> 8) & 255u));
-                zb = make_float2((float)(z1 & 255u), (float)((z1 >> 8) & 255u));
-                if (NB == 1) {
-                    const bool odd = grp & 1;
-                    const float fa = odd ? sa.y : sa.x, fb = odd ? sb.y : sb.x;
-                    const float ya = odd ? za.y : za.x, yb = odd ? zb.y : zb.x;
-                    sa = make_float2(fa, fa), sb = make_float2(fb, fb);
-                    za = make_float2(ya, ya), zb = make_float2(yb, yb);
+            if constexpr (!BF) {
+                const ColScales cs = col_scales<FMT, NB>(s, grp, q);
+#pragma unroll
+                for (int n = 0; n < NT; ++n) {
+                    if (FMT == FMT_INT4) {
+                        // sum q x - z sum x, then the group's scale
+                        const int c0 = 2 * q, c1 = 2 * q + 1;
+                        const float *xs = xsum + (p * SB + grp * NB) * TT + 8 * n;
+                        const float x0 = xs[(c0 % NB) * TT + c0 / NB], x1 = xs[(c1 % NB) * TT + c1 / NB];
+                        part[n][0] = fmaf(part[n][0], 16777216.f, -cs.za.x * x0);
+                        part[n][1] = fmaf(part[n][1], 16777216.f, -cs.za.y * x1);
+                        part[n][2] = fmaf(part[n][2], 1048576.f, -cs.zb.x * x0);
+                        part[n][3] = fmaf(part[n][3], 1048576.f, -cs.zb.y * x1);
+                    }
+                    sum[n][0] = grp ? fmaf(part[n][0], cs.a.x, sum[n][0]) : part[n][0] * cs.a.x;
+                    sum[n][1] = grp ? fmaf(part[n][1], cs.a.y, sum[n][1]) : part[n][1] * cs.a.y;
+                    sum[n][2] = grp ? fmaf(part[n][2], cs.b.x, sum[n][2]) : part[n][2] * cs.b.x;
+                    sum[n][3] = grp ? fmaf(part[n][3], cs.b.y, sum[n][3]) : part[n][3] * cs.b.y;
                 }
             }
+        }
+        if constexpr (!BF) {
 #pragma unroll
             for (int n = 0; n < NT; ++n) {
-                if (FMT == FMT_MXFP4) {
-                    acc[n][0] = fmaf(part[n][0], sa.x, acc[n][0]);
-                    acc[n][1] = fmaf(part[n][1], sa.y, acc[n][1]);
-                    acc[n][2] = fmaf(part[n][2], sb.x, acc[n][2]);
-                    acc[n][3] = fmaf(part[n][3], sb.y, acc[n][3]);
-                } else {
-                    // sum q x - z sum x, then the group's scale
-                    float xs[2];
-#pragma unroll
-                    for (int c = 0; c < 2; ++c) {
-                        const int col = 2 * q + c;
-                        const int tok = min(8 * n + col / NB, tv - 1);
-                        xs[c] = xsum[(blk0 + grp * NB + col % NB) * tv + tok];
-                    }
-                    acc[n][0] = fmaf(fmaf(part[n][0], 16777216.f, -za.x * xs[0]), sa.x, acc[n][0]);
-                    acc[n][1] = fmaf(fmaf(part[n][1], 16777216.f, -za.y * xs[1]), sa.y, acc[n][1]);
-                    acc[n][2] = fmaf(fmaf(part[n][2], 1048576.f, -zb.x * xs[0]), sb.x, acc[n][2]);
-                    acc[n][3] = fmaf(fmaf(part[n][3], 1048576.f, -zb.y * xs[1]), sb.y, acc[n][3]);
-                }
+                const float *xs = xscale + p * TT + 8 * n;
+                const float x0 = xs[2 * q / NB], x1 = xs[(2 * q + 1) / NB];
+                acc[n][0] = fmaf(sum[n][0], x0, acc[n][0]);
+                acc[n][1] = fmaf(sum[n][1], x1, acc[n][1]);
+                acc[n][2] = fmaf(sum[n][2], x0, acc[n][2]);
+                acc[n][3] = fmaf(sum[n][3], x1, acc[n][3]);
             }
         }
     };
-    for (; p < p1; p += DEPTH * a.kw) {
+    // partial sums of row group r (of the CTA): summed over the blocks side by side
+    auto flush = [&](int r) {
+        float *o = red + (size_t)(warp + r) * TT * 16;
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+            if (NB == 1) {
+                o[(8 * n + 2 * q) * 16 + g] = acc[n][0];
+                o[(8 * n + 2 * q + 1) * 16 + g] = acc[n][1];
+                o[(8 * n + 2 * q) * 16 + g + 8] = acc[n][2];
+                o[(8 * n + 2 * q + 1) * 16 + g + 8] = acc[n][3];
+            } else {
+                float r0 = acc[n][0] + acc[n][1], r1 = acc[n][2] + acc[n][3];
+                if (NB >= 4) {
+                    r0 += __shfl_xor_sync(0xffffffffu, r0, 1);
+                    r1 += __shfl_xor_sync(0xffffffffu, r1, 1);
+                }
+                if (NB == 8) {
+                    r0 += __shfl_xor_sync(0xffffffffu, r0, 2);
+                    r1 += __shfl_xor_sync(0xffffffffu, r1, 2);
+                }
+                const int tok = 2 * q / NB;
+                if (2 * q % NB == 0) {  // one of the lanes that share a token
+                    o[tok * 16 + g] = r0;
+                    o[tok * 16 + g + 8] = r1;
+                }
+            }
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                acc[n][j] = 0.f;
+        }
+    };
+    int r = P ? u0 / P : 0, p = P ? u0 % P : 0;
+    for (int u = u0; u < u1; u += DEPTH) {
 #pragma unroll
         for (int d = 0; d < DEPTH; ++d) {
-            const int pp = p + d * a.kw;
-            if (pp < p1)
-                compute(st[d], pp);
-            load(st[d], pp + DEPTH * a.kw);
-        }
-    }
-
-    // ---- sums over the blocks side by side, the warps of a row group, the cluster
-    const int rows = rgroups * 16;
-#pragma unroll
-    for (int n = 0; n < NT; ++n) {
-        float *o = red + (size_t)kwi * TT * rows + rwi * 16;
-        if (NB == 1) {
-            o[(8 * n + 2 * q) * rows + g] = acc[n][0];
-            o[(8 * n + 2 * q + 1) * rows + g] = acc[n][1];
-            o[(8 * n + 2 * q) * rows + g + 8] = acc[n][2];
-            o[(8 * n + 2 * q + 1) * rows + g + 8] = acc[n][3];
-        } else {
-            float r0 = acc[n][0] + acc[n][1], r1 = acc[n][2] + acc[n][3];
-            if (NB >= 4) {
-                r0 += __shfl_xor_sync(0xffffffffu, r0, 1);
-                r1 += __shfl_xor_sync(0xffffffffu, r1, 1);
+            if (u + d < u1) {
+                compute(st[d], p);
+                load(st[d]);
+                if (++p == P || u + d + 1 == u1) {
+                    flush(r);
+                    p = 0;
+                    ++r;
+                }
             }
-            if (NB == 8) {
-                r0 += __shfl_xor_sync(0xffffffffu, r0, 2);
-                r1 += __shfl_xor_sync(0xffffffffu, r1, 2);
-            }
-            const int tok = 2 * q / NB;  // equal values from the lanes that share a token
-            o[tok * rows + g] = r0;
-            o[tok * rows + g + 8] = r1;
         }
     }
     __syncthreads();
-    const int total = tv * rows;
-    const int row0 = tile * rows;
-    for (int i = tid; i < total; i += THREADS) {
-        float v = red[i];
-        for (int k = 1; k < a.kw; ++k)
-            v += red[(size_t)k * TT * rows + i];
-        if (!BF) {
-            const int m = xmax[i / rows];
-            v = scale_pow2(v, m == 0 ? 0 : (m >> 23) - 141);
-        }
-        red[i] = v;
-    }
-    if (csize > 1)
-        cluster_sync();
-    else
-        __syncthreads();
-    // rank r finishes every csize-th run of THREADS sums
-    for (int i = crank * THREADS + tid; i < total; i += csize * THREADS) {
-        float v;
-        if (csize > 1) {
-            v = 0.f;
-            const uint32_t local = (uint32_t)__cvta_generic_to_shared(red + i);
-            for (uint32_t r = 0; r < csize; ++r) {
-                uint32_t remote;
-                float f;
-                asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(remote) : "r"(local), "r"(r));
-                asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(f) : "r"(remote));
-                v += f;
-            }
-        } else {
-            v = red[i];
-        }
-        const int t = i / rows, n = row0 + (i - t * rows);
+
+    // ---- sums over the warps that share a row group, then over the cluster, in
+    // a fixed order
+    const int total = R * tv * 16;
+    auto store = [&](int i, float v) {
+        const int rt = i >> 4, rr = rt / tv;
+        const int n = (rg0 + rr) * 16 + (i & 15);
         if (n < a.N) {
-            const long long at = (t0 + t) * a.y_ld + n;
+            const long long at = (t0 + rt - rr * tv) * a.y_ld + n;
             if (a.y_f32) {
                 float *y = static_cast<float *>(a.y) + at;
                 *y = a.accumulate ? *y + v : v;
@@ -490,79 +621,159 @@ __global__ void __launch_bounds__(THREADS) linear_kernel(const LinArgs a)
                 static_cast<__nv_bfloat16 *>(a.y)[at] = __float2bfloat16_rn(v);
             }
         }
+    };
+    for (int i = tid; i < total; i += THREADS) {
+        const int rt = i >> 4, rr = rt / tv, t = rt - rr * tv;
+        float v = 0.f;
+        if (P) {
+            const int w1 = owner_of((rr + 1) * P - 1, units, nw);
+            for (int w = owner_of(rr * P, units, nw); w <= w1; ++w)
+                v += red[(size_t)((w + rr) * TT + t) * 16 + (i & 15)];
+        }
+        if (csize == 1)
+            store(i, v);
+        else
+            fin[i] = v;
     }
-    if (csize > 1)
-        cluster_sync();  // a CTA's sums stay in place until every rank has read them
+    if (csize == 1)
+        return;
+    cluster_sync();
+    // rank r finishes every csize-th run of THREADS sums
+    for (int i = crank * THREADS + tid; i < total; i += csize * THREADS) {
+        float v = 0.f;
+        const uint32_t local = (uint32_t)__cvta_generic_to_shared(fin + i);
+        for (uint32_t rk = 0; rk < csize; ++rk) {
+            uint32_t remote;
+            float f;
+            asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(remote) : "r"(local), "r"(rk));
+            asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(f) : "r"(remote));
+            v += f;
+        }
+        store(i, v);
+    }
+    cluster_sync();  // a CTA's sums stay in place until every rank has read them
 }
 
 // ------------------------------------------------------------------ host side
 
-// How a call is cut: kw warps of a CTA along K, a cluster of `cluster` CTAs
-// along K, and the shared memory of a CTA.
+// How a call is cut: a cluster of `cluster` CTAs along K, `rgroups` groups of 16
+// rows per cluster, and a CTA's shared memory.
 struct Cut {
-    int kw, cluster, smem, xs_off, red_off;
+    int cluster, rgroups, smem, xs_off, sum_off, red_off, fin_off;
 };
 
-Cut cut_of(int pairs, int tt, int tv, bool i4, int kw, int cluster)
+constexpr int SMEM_MAX = 220 * 1024;
+
+Cut cut_of(int n16, int steps, int step_blocks, int tt, int tv, bool i4, int cluster, int slots)
 {
     Cut c;
-    c.kw = kw;
     c.cluster = cluster;
-    const int blocks = (pairs + cluster - 1) / cluster * 8;
-    c.xs_off = blocks * tv * 64;
-    c.red_off = c.xs_off + 64 + (i4 ? blocks * tv * 4 : 0);
-    c.red_off = (c.red_off + 15) & ~15;
-    c.smem = c.red_off + tt * WARPS * 16 * 4;
+    const int segs = ((steps + cluster - 1) / cluster * step_blocks + 7) / 8;  // x is staged by 256 values
+    c.xs_off = segs * 8 * tt * 64;
+    c.sum_off = c.xs_off + segs * tt * 4;
+    c.red_off = (c.sum_off + (i4 ? segs * 8 * tt * 4 : 0) + 15) & ~15;
+    // one wave of clusters where the partial sums of its row groups fit
+    const int per = tt * 16 * 4, room = SMEM_MAX - c.red_off - WARPS * per;
+    c.rgroups = (n16 + slots - 1) / slots;
+    const int most = room > 0 ? room / (per + (cluster > 1 ? tv * 64 : 0)) : 0;
+    if (c.rgroups > most)
+        c.rgroups = most;
+    c.fin_off = c.red_off + (WARPS + c.rgroups) * per;
+    c.smem = c.fin_off + (cluster > 1 ? c.rgroups * tv * 64 : 0);
     return c;
 }
 
-constexpr int SMEM_MAX = 200 * 1024;
+// Clusters of `size` CTAs of a kernel that the current device runs at a time (one
+// CTA per SM: the register file holds one), looked up once per device.
+template <int FMT, int TB, int NT>
+int clusters_of(int size)
+{
+    const int sms = gemm::sm_count();
+    if (size == 1)
+        return sms;
+    static std::atomic<int> cached[gemm::MAX_DEVICES][4];
+    const int dev = gemm::current_device(), at = size == 2 ? 1 : size == 4 ? 2 : 3;
+    const bool cacheable = dev >= 0 && dev < gemm::MAX_DEVICES;
+    int n = cacheable ? cached[dev][at].load(std::memory_order_relaxed) : 0;
+    if (n > 0)
+        return n;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(sms / size * size);
+    cfg.blockDim = dim3(THREADS);
+    cudaLaunchAttribute at_cl;
+    at_cl.id = cudaLaunchAttributeClusterDimension;
+    at_cl.val.clusterDim.x = (unsigned)size;
+    at_cl.val.clusterDim.y = at_cl.val.clusterDim.z = 1;
+    cfg.attrs = &at_cl;
+    cfg.numAttrs = 1;
+    if (cudaOccupancyMaxActiveClusters(&n, linear_kernel<FMT, TB, NT>, &cfg) != cudaSuccess || n < 1) {
+        cudaGetLastError();
+        n = sms / size > 0 ? sms / size : 1;
+    }
+    if (cacheable)
+        cached[dev][at].store(n, std::memory_order_relaxed);
+    return n;
+}
 
 template <int FMT, int TB, int NT>
 cudaError_t launch_linear(const LinArgs &args, cudaStream_t st)
 {
     constexpr int TT = TB * NT;
+    constexpr int SC = step_chunks<FMT>;
     LinArgs a = args;
+    a.steps = (a.kchunks + SC - 1) / SC;
     const int n16 = (a.N + 15) / 16;
     const int tiles_y = (a.T + TT - 1) / TT;
     const int tv = a.T < TT ? a.T : TT;
-    // warps along K first within the CTA, then over a cluster where x would not
-    // fit or where the rows alone leave SMs idle
-    int kw = 8, cl = 1;
-    while (kw > 1 && (long long)((n16 * kw + 7) / 8) * tiles_y > 8ll * gemm::sm_count())
-        kw >>= 1;
-    Cut c = cut_of(a.pairs, TT, tv, FMT == FMT_INT4, kw, cl);
-    while (cl < 8 &&
-           (c.smem > 64 * 1024 || (long long)((n16 * kw + 7) / 8) * tiles_y * cl < 2ll * gemm::sm_count())) {
-        cl *= 2;
-        c = cut_of(a.pairs, TT, tv, FMT == FMT_INT4, kw, cl);
+    // The cluster size with the least estimated time, of those whose shared memory
+    // holds x: a CTA's steps (0.05 us each, more with several tokens), its items of x
+    // (1/16 of a warp's 0.25 us) and the cluster's barriers.
+    Cut best{};
+    double least = 0.;
+    for (int cl = 1; cl <= 8 && (cl == 1 || cl <= a.steps); cl *= 2) {
+        int slots = clusters_of<FMT, TB, NT>(cl) / tiles_y;
+        if (slots < 1)
+            slots = 1;
+        const Cut c = cut_of(n16, a.steps, SC * 4, TT, tv, FMT == FMT_INT4, cl, slots);
+        if (c.rgroups < 1)
+            continue;
+        const int grid = (n16 + c.rgroups - 1) / c.rgroups * tiles_y;
+        const int waves = (grid + slots * tiles_y - 1) / (slots * tiles_y);
+        const double steps = (double)((a.steps + cl - 1) / cl);
+        const double us = waves * (c.rgroups * steps * (0.05 + 0.003 * TT) + steps * SC * TT / 2 * 0.016 +
+                                   (cl > 1 ? 1.0 + 0.1 * cl : 0.));
+        if (best.rgroups < 1 || us < least) {
+            least = us;
+            best = c;
+        }
     }
     if constexpr (NT > 1) {
-        if (c.smem > SMEM_MAX)  // the longest rows: fewer tokens at a time
+        if (best.rgroups < 1)  // the longest rows: fewer tokens at a time
             return launch_linear<FMT, TB, 1>(args, st);
     }
-    if (c.smem > SMEM_MAX)
+    if (best.rgroups < 1)
         return cudaErrorInvalidValue;
-    a.kw = c.kw;
-    a.xs_off = c.xs_off;
-    a.red_off = c.red_off;
+    a.rgroups = best.rgroups;
+    a.xs_off = best.xs_off;
+    a.sum_off = best.sum_off;
+    a.red_off = best.red_off;
+    a.fin_off = best.fin_off;
     auto kern = linear_kernel<FMT, TB, NT>;
     static std::atomic<int> attr_set[gemm::MAX_DEVICES];
     cudaError_t e = gemm::smem_limit_once(attr_set, (const void *)kern, SMEM_MAX);
     if (e != cudaSuccess)
         return e;
-    const int rgroups = WARPS / c.kw;
     cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3((unsigned)((n16 + rgroups - 1) / rgroups * c.cluster), (unsigned)tiles_y);
+    cfg.gridDim = dim3((unsigned)((n16 + best.rgroups - 1) / best.rgroups * best.cluster), (unsigned)tiles_y);
     cfg.blockDim = dim3(THREADS);
-    cfg.dynamicSmemBytes = c.smem;
+    cfg.dynamicSmemBytes = best.smem;
     cfg.stream = st;
     cudaLaunchAttribute at;
     at.id = cudaLaunchAttributeClusterDimension;
-    at.val.clusterDim.x = (unsigned)c.cluster;
+    at.val.clusterDim.x = (unsigned)best.cluster;
     at.val.clusterDim.y = at.val.clusterDim.z = 1;
     cfg.attrs = &at;
-    cfg.numAttrs = 1;
+    cfg.numAttrs = best.cluster > 1;
     return cudaLaunchKernelEx(&cfg, kern, a);
 }
 
@@ -651,16 +862,19 @@ MoeStatus moe_linear_load(int N, int K, MoeWeightFormat wfmt, const MoeMx *w, vo
         destroy(l);
         return bad_cuda("cudaHostGetDevicePointer", e);
     }
-    if (cudaMalloc(&f.base, f.group_bytes) != cudaSuccess) {
+    // a step of two chunks may read one past a row tile's last (see linear_kernel)
+    const size_t bytes = f.group_bytes + f.chunk_bytes;
+    if (cudaMalloc(&f.base, bytes) != cudaSuccess) {
         cudaGetLastError();
-        snprintf(msg, sizeof msg, "device allocation of %zu bytes of weights failed", f.group_bytes);
+        snprintf(msg, sizeof msg, "device allocation of %zu bytes of weights failed", bytes);
         destroy(l);
         return bad(MOE_ENOMEM, msg);
     }
     const SrcMat src = {(const uint8_t *)w->codes, (const uint8_t *)(fmt == FMT_BF16 ? nullptr : w->scales),
                         fmt == FMT_BF16 ? (long long)K * 2 : K / 2, K / 32,
                         (const uint8_t *)(fmt == FMT_INT4 ? w->zeros : nullptr)};
-    if ((e = launch_repack(fmt, fmt == FMT_BF16 ? LAYOUT_FRAG : LAYOUT_FRAG_F16, false, src, src, f, 0, K, N,
+    if ((e = cudaMemsetAsync(f.base + f.group_bytes, 0, f.chunk_bytes, st)) != cudaSuccess ||
+        (e = launch_repack(fmt, fmt == FMT_BF16 ? LAYOUT_FRAG : LAYOUT_FRAG_F16, false, src, src, f, 0, K, N,
                            &l->err_dev[1], st)) != cudaSuccess ||
         (e = cudaStreamSynchronize(st)) != cudaSuccess) {
         destroy(l);
@@ -718,8 +932,6 @@ MoeStatus moe_linear_forward(MoeLinear *l, const void *x, MoeRowType x_type, lon
     a.N = l->N;
     a.K = l->K;
     a.kchunks = l->frag.kchunks;
-    a.chunk_bytes = l->frag.chunk_bytes;
-    a.pairs = (a.kchunks + 1) / 2;
     a.x = x;
     a.xscales = (const uint8_t *)x_scales;
     a.x_ld = x_ld;
