@@ -17,14 +17,17 @@
 
 #include "../../include/moe.h"
 #include "gemm_common.cuh"
-#include "moe_internal.cuh"
+#include "linear_internal.cuh"
 
 using namespace moe;
 
 struct MoeLinear {
     int N = 0, K = 0, fmt = 0;
-    WeightStore frag;         // FRAG / FRAG_F16 layout
-    int *err_host = nullptr;  // mapped pinned host memory: [0] device error flag, [1] a rejected scale at load
+    WeightStore frag;         // FRAG / FRAG_F16 layout (few tokens)
+    WeightStore tile;         // TILE, TILE_F16 or TILE_I4 layout (the tcgen05 GEMM)
+    int op = LIN_BF16;        // the GEMM's operands
+    int *err_host = nullptr;  // mapped pinned host memory: [0] device error flag, [1] a rejected scale
+                              // at load, [2] an MXFP4 row whose exponents span too widely for FP16 operands
     int *err_dev = nullptr;
 };
 
@@ -804,6 +807,10 @@ void destroy(MoeLinear *l)
 {
     if (l->frag.base)
         cudaFree(l->frag.base);
+    if (l->tile.base)
+        cudaFree(l->tile.base);
+    if (l->tile.row_base)
+        cudaFree(l->tile.row_base);
     if (l->err_host)
         cudaFreeHost(l->err_host);
     delete l;
@@ -862,20 +869,39 @@ MoeStatus moe_linear_load(int N, int K, MoeWeightFormat wfmt, const MoeMx *w, vo
         destroy(l);
         return bad_cuda("cudaHostGetDevicePointer", e);
     }
-    // a step of two chunks may read one past a row tile's last (see linear_kernel)
+    WeightStore &t = l->tile;
+    t = f;
+    // two copies, one for each kernel; a step of two chunks may read one past a row
+    // tile's last (see linear_kernel)
     const size_t bytes = f.group_bytes + f.chunk_bytes;
-    if (cudaMalloc(&f.base, bytes) != cudaSuccess) {
+    if (cudaMalloc(&f.base, bytes) != cudaSuccess || cudaMalloc(&t.base, t.group_bytes) != cudaSuccess ||
+        (fmt != FMT_BF16 && cudaMalloc(&t.row_base, (size_t)t.row_tiles * TILE_ROWS) != cudaSuccess)) {
         cudaGetLastError();
-        snprintf(msg, sizeof msg, "device allocation of %zu bytes of weights failed", bytes);
+        snprintf(msg, sizeof msg, "device allocation of %zu bytes of weights failed", bytes + t.group_bytes);
         destroy(l);
         return bad(MOE_ENOMEM, msg);
     }
     const SrcMat src = {(const uint8_t *)w->codes, (const uint8_t *)(fmt == FMT_BF16 ? nullptr : w->scales),
                         fmt == FMT_BF16 ? (long long)K * 2 : K / 2, K / 32,
                         (const uint8_t *)(fmt == FMT_INT4 ? w->zeros : nullptr)};
-    if ((e = cudaMemsetAsync(f.base + f.group_bytes, 0, f.chunk_bytes, st)) != cudaSuccess ||
+    if ((fmt != FMT_BF16 &&
+         (e = launch_row_base(fmt, false, src, src, t, 0, K, N, &l->err_dev[2], st)) != cudaSuccess) ||
+        (e = cudaMemsetAsync(f.base + f.group_bytes, 0, f.chunk_bytes, st)) != cudaSuccess ||
         (e = launch_repack(fmt, fmt == FMT_BF16 ? LAYOUT_FRAG : LAYOUT_FRAG_F16, false, src, src, f, 0, K, N,
                            &l->err_dev[1], st)) != cudaSuccess ||
+        (e = cudaStreamSynchronize(st)) != cudaSuccess) {
+        destroy(l);
+        return bad_cuda("repack", e);
+    }
+    int layout = LAYOUT_TILE;
+    if (fmt == FMT_INT4) {
+        l->op = LIN_I4;
+        layout = LAYOUT_TILE_I4;
+    } else if (fmt == FMT_MXFP4 && *(volatile int *)&l->err_host[2] == 0) {
+        l->op = LIN_F16;
+        layout = LAYOUT_TILE_F16;
+    }
+    if ((e = launch_repack(fmt, layout, false, src, src, t, 0, K, N, &l->err_dev[1], st)) != cudaSuccess ||
         (e = cudaStreamSynchronize(st)) != cudaSuccess) {
         destroy(l);
         return bad_cuda("repack", e);
@@ -889,7 +915,10 @@ MoeStatus moe_linear_load(int N, int K, MoeWeightFormat wfmt, const MoeMx *w, vo
     return MOE_OK;
 }
 
-size_t moe_linear_workspace_bytes(const MoeLinear *, int) { return 0; }
+size_t moe_linear_workspace_bytes(const MoeLinear *l, int T)
+{
+    return !l || T <= LINEAR_STREAM_MAX_T ? 0 : linear_gemm_workspace(l->K, T);
+}
 
 MoeStatus moe_linear_forward(MoeLinear *l, const void *x, MoeRowType x_type, long long x_ld, const void *x_scales,
                              int T, void *y, MoeRowType y_type, long long y_ld, int accumulate, void *workspace,
@@ -927,6 +956,30 @@ MoeStatus moe_linear_forward(MoeLinear *l, const void *x, MoeRowType x_type, lon
         return bad(MOE_EWORKSPACE, "moe_linear_forward: the workspace is smaller than moe_linear_workspace_bytes");
     if ((uintptr_t)workspace % 256)
         return bad(MOE_EWORKSPACE, "moe_linear_forward: the workspace must be 256-byte aligned");
+    cudaStream_t st = (cudaStream_t)cuda_stream;
+    if (T > LINEAR_STREAM_MAX_T) {
+        if (!workspace)
+            return bad(MOE_EWORKSPACE, "moe_linear_forward: NULL workspace");
+        LinearGemm g{};
+        g.w = &l->tile;
+        g.fmt = l->fmt;
+        g.op = l->op;
+        g.N = l->N;
+        g.K = l->K;
+        g.T = T;
+        g.x = x;
+        g.xscales = (const uint8_t *)x_scales;
+        g.x_ld = x_ld;
+        g.x_mx = x_type == MOE_ROWS_MXFP8;
+        g.y = y;
+        g.y_ld = y_ld;
+        g.y_f32 = y_type == MOE_ROWS_F32;
+        g.accumulate = accumulate != 0;
+        g.workspace = (uint8_t *)workspace;
+        g.err = l->err_dev;
+        const cudaError_t e = launch_linear_gemm(g, st);
+        return e == cudaSuccess ? MOE_OK : bad_cuda("linear layer launch", e);
+    }
     LinArgs a{};
     a.w = l->frag.base;
     a.N = l->N;
@@ -941,7 +994,6 @@ MoeStatus moe_linear_forward(MoeLinear *l, const void *x, MoeRowType x_type, lon
     a.y_ld = y_ld;
     a.y_f32 = y_type == MOE_ROWS_F32;
     a.accumulate = accumulate != 0;
-    cudaStream_t st = (cudaStream_t)cuda_stream;
     const cudaError_t e = l->fmt == FMT_MXFP4  ? launch_tokens<FMT_MXFP4>(a, st)
                           : l->fmt == FMT_INT4 ? launch_tokens<FMT_INT4>(a, st)
                                                : launch_tokens<FMT_BF16>(a, st);

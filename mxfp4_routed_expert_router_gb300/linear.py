@@ -66,7 +66,14 @@ class QuantLinear:
             out = torch.empty((T, self.N), dtype=torch.float32, device=self.device)
         elif tuple(out.shape) != (T, self.N):
             raise B.MoeError(B.MOE_EINVAL, f"out: shape {tuple(out.shape)} where ({T}, {self.N}) is needed")
-        B.moe_linear_forward(self.handle, x, x_scales, out, accumulate, stream=stream)
+        n = B.moe_linear_workspace_bytes(self.handle, T) if T > 16 else 0
+        ws = None
+        if n:
+            # from torch's allocator on each call: it keeps calls on several streams and captured calls apart
+            ws = torch.empty(n, dtype=torch.uint8, device=self.device)
+            if stream is not None:
+                ws.record_stream(torch.cuda.ExternalStream(stream) if isinstance(stream, int) else stream)
+        B.moe_linear_forward(self.handle, x, x_scales, out, accumulate, ws, n, stream)
         return out
 
     def sync(self, stream=None):
