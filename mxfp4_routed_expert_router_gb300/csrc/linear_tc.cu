@@ -15,9 +15,14 @@
 // share an SM (half of its tensor memory each), so that the hand-offs, the first
 // loads and the epilogue of one overlap the MMAs of the other.  A cluster of 1, 2,
 // 4 or 8 CTAs splits K; its partial tiles meet in shared memory and each rank
-// finishes a share of the tokens, in a fixed order.  Warps: 0 loads tiles and
-// prefetches weight chunks into L2, 1 issues the MMAs, 2-5 decode and then finish
-// the tile.  Every mbarrier wait is bounded (gemm_common.cuh).
+// finishes a share of the tokens, in a fixed order.  Warps: 0 loads token tiles, 1
+// issues the MMAs, 2 loads weight chunks, 4-11 decode (two groups of four, one per
+// tensor-memory lane quadrant, taking the stages in turn) and then finish the tile.
+// Weights and tokens come through rings of their own, as deep as the tile's size
+// leaves room for: with few tokens the weight stream is what bounds a call, and
+// its copies then run well ahead of the decoders.  The GEMM is launched while the
+// kernel that writes the token rows still runs and waits for it only before it
+// reads them.  Every mbarrier wait is bounded (gemm_common.cuh).
 #include <cuda.h>
 #include <cudaTypedefs.h>
 #include <cuda_bf16.h>
@@ -33,33 +38,37 @@ namespace {
 
 using namespace gemm;
 
-constexpr int N_WARPS = 6, THREADS = N_WARPS * 32;
-constexpr int WARP_LOAD = 0, WARP_MMA = 1;  // 2-5: decode
+constexpr int N_WARPS = 12, THREADS = N_WARPS * 32;
+constexpr int WARP_LOAD = 0, WARP_MMA = 1, WARP_WEIGHTS = 2, WARP_DEC = 4;  // (3 idles)
+constexpr int DEC_GROUPS = 2;         // group g decodes the stages of A slot g
 constexpr int NMAX = 128;             // tokens of a tile
 constexpr int A_STAGES = 2;           // A ring (tensor memory)
 constexpr int A_SLOT_COLS = 64;       // 128 16-bit values per lane
 constexpr int TMEM_COLS = 256;        // half of the SM's: accumulator and A ring
+static_assert(DEC_GROUPS == A_STAGES, "a group fills its own A slot");
 static_assert(NMAX + A_STAGES * A_SLOT_COLS <= TMEM_COLS, "tensor memory");
-constexpr int SLICE_BYTES = NMAX * HALF_K * 2;           // 16 KB: 128 token rows x 64 values, one swizzled tile
 constexpr int A_TILE_BYTES = TILE_ROWS * HALF_K * 2;     // BF16 weights: 16 KB
-constexpr int RING_BYTES = 96 * 1024;
-constexpr int RING_MAX = 6;
+// Shared memory: the token ring (slots of 64 values of K: a swizzled tile of
+// tile_tokens x 128 bytes, with BF16 weights the A tile after it), then the ring
+// of weight chunks.
+constexpr int RING_BYTES = 108 * 1024;
+constexpr int B_MAX = 12, W_MAX = 8;  // slots
 constexpr int BAR_OFF = RING_BYTES;
-constexpr int N_BARS = 2 * RING_MAX + 2 * A_STAGES + 1;
+constexpr int N_BARS = 2 * B_MAX + 2 * W_MAX + 2 * A_STAGES + 1;
 constexpr int MISC_OFF = BAR_OFF + N_BARS * 8;
-constexpr int TSC_OFF = MISC_OFF + 16;                   // token scales of the tile
+constexpr int TSC_OFF = MISC_OFF + 16;                   // the tile's token scales
 constexpr int SMEM_BYTES = TSC_OFF + NMAX * 4 + 1024;    // + alignment slack
 static_assert(2 * (SMEM_BYTES + 1024) <= 228 * 1024, "two CTAs per SM");
-static_assert(NMAX * TILE_ROWS * 4 <= RING_BYTES, "a partial tile fits in the ring");
-constexpr int PF_CHUNKS = 8;          // weight chunks prefetched into L2 ahead of the stage being loaded
+static_assert(NMAX * TILE_ROWS * 4 <= RING_BYTES, "a partial tile fits in the rings");
 
 struct Args {
     const uint8_t *w;
     const uint8_t *row_base;  // FP16 operands: power of two (+ 127) of each row
     const float *xscale;      // FP16 operands: power of two of each token
-    int N, T, kchunks, chunk_bytes;
+    int N, T, kchunks;
     int tile_tokens;          // tokens of a tile (a multiple of 16, at most NMAX), rows of a TMA box of B
     int ttiles;
+    int b_slots, w_slots, w_off;  // ring slots, the weight ring's offset (bytes)
     void *y;
     long long y_ld;
     int y_f32, accumulate;
@@ -171,22 +180,31 @@ __device__ __forceinline__ void cluster_sync()
     asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 
+__device__ __forceinline__ void store_y(const Args &a, long long at, float v)
+{
+    if (a.y_f32) {
+        float *y = static_cast<float *>(a.y) + at;
+        *y = a.accumulate ? *y + v : v;
+    } else {
+        static_cast<__nv_bfloat16 *>(a.y)[at] = __float2bfloat16_rn(v);
+    }
+}
+
 template <int OP, int WFMT>
 __global__ void __launch_bounds__(THREADS, 2)
     linear_tc_kernel(const __grid_constant__ Args a, const __grid_constant__ CUtensorMap map_b,
                      const __grid_constant__ CUtensorMap map_a)
 {
     constexpr bool AS = WFMT == FMT_BF16;                            // A by TMA into shared memory
-    constexpr int KST = (AS || OP == LIN_I4) ? HALF_K : CHUNK_K;     // K values per stage
-    constexpr int NSL = KST / HALF_K;                                // 64-wide slices per stage
+    constexpr int KST = (AS || OP == LIN_I4) ? HALF_K : CHUNK_K;     // K values per A stage
+    constexpr int NSL = KST / HALF_K;                                // token ring slots per A stage
     constexpr int NBLK = KST / 32;
-    constexpr int STAGE_BYTES = NSL * SLICE_BYTES + (AS ? A_TILE_BYTES : 0);
-    constexpr int RING = RING_BYTES / STAGE_BYTES;                   // 3 of 32 KB, or 6 of 16 KB
-    static_assert(RING >= 3 && RING <= RING_MAX, "ring");
+    constexpr int CB = WFMT == FMT_INT4 ? CHUNK_I4_BYTES : CHUNK_MX_BYTES;
     extern __shared__ uint8_t smem_dyn[];
-    uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_dyn) + 1023) & ~uintptr_t(1023));
-    uint64_t *b_full = reinterpret_cast<uint64_t *>(smem + BAR_OFF), *b_empty = b_full + RING_MAX;
-    uint64_t *a_full = b_empty + RING_MAX, *a_empty = a_full + A_STAGES, *acc_full = a_empty + A_STAGES;
+    uint8_t *smem = smem_dyn + ((1024u - (smem_addr(smem_dyn) & 1023u)) & 1023u);
+    uint64_t *b_full = reinterpret_cast<uint64_t *>(smem + BAR_OFF), *b_empty = b_full + B_MAX;
+    uint64_t *w_full = b_empty + B_MAX, *w_empty = w_full + W_MAX;
+    uint64_t *a_full = w_empty + W_MAX, *a_empty = a_full + A_STAGES, *acc_full = a_empty + A_STAGES;
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + MISC_OFF);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + MISC_OFF + 4);
     float *tsc = reinterpret_cast<float *>(smem + TSC_OFF);
@@ -199,13 +217,17 @@ __global__ void __launch_bounds__(THREADS, 2)
     const int tok0 = tt * a.tile_tokens, nvalid = min(a.tile_tokens, a.T - tok0);
     const int n_mma = (nvalid + 15) & ~15;
     const int c0 = (int)((long long)a.kchunks * crank / csize), c1 = (int)((long long)a.kchunks * (crank + 1) / csize);
-    const int nst = (c1 - c0) * (CHUNK_K / KST);
-    const uint8_t *wsrc = a.w + ((size_t)rt * a.kchunks + c0) * (size_t)a.chunk_bytes;
+    const int nst = (c1 - c0) * (CHUNK_K / KST), nsl = nst * NSL;  // A stages, token slots
+    const uint32_t slice_bytes = (uint32_t)a.tile_tokens * HALF_K * 2, slot_bytes = slice_bytes + (AS ? A_TILE_BYTES : 0);
 
     if (tid == 0) {
-        for (int i = 0; i < RING; ++i) {
+        for (int i = 0; i < a.b_slots; ++i) {
             mbar_init(&b_full[i], 1);
             mbar_init(&b_empty[i], 1);
+        }
+        for (int i = 0; i < a.w_slots; ++i) {
+            mbar_init(&w_full[i], 1);
+            mbar_init(&w_empty[i], KST == CHUNK_K ? 4 : 8);  // a chunk of two stages is read by both groups
         }
         for (int i = 0; i < A_STAGES; ++i) {
             mbar_init(&a_full[i], 4);
@@ -222,9 +244,6 @@ __global__ void __launch_bounds__(THREADS, 2)
                      : "memory");
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
     }
-    if (OP != LIN_BF16)
-        for (int i = tid; i < nvalid; i += THREADS)
-            tsc[i] = __ldg(a.xscale + tok0 + i);
     fence_before();
     __syncthreads();
     fence_after();
@@ -232,117 +251,141 @@ __global__ void __launch_bounds__(THREADS, 2)
     const uint32_t tmem_a = tmem + NMAX;
 
     if (warp == WARP_LOAD) {
-        // ---------------------------------------------------------- tiles -> ring
-        int pf = 0;
-        auto prefetch = [&]() {
-            if (pf < c1 - c0 && lane == 0 && !AS)
-                asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(wsrc + (size_t)pf * a.chunk_bytes),
-                             "r"((uint32_t)a.chunk_bytes)
-                             : "memory");
-            ++pf;
-        };
-        for (int i = 0; i < PF_CHUNKS; ++i)
-            prefetch();
-        const uint32_t bytes = (uint32_t)(NSL * a.tile_tokens * HALF_K * 2 + (AS ? A_TILE_BYTES : 0));
-        int st = 0;
-        for (; st < nst; ++st) {
-            const int slot = st % RING;
-            if (!mbar_wait_sleep_warp(&b_empty[slot], ((st / RING) & 1) ^ 1, abort_flag, a.err, lane))
+        // ---------------------------------------------------------- token tiles -> ring
+        asm volatile("griddepcontrol.wait;" ::: "memory");  // the token rows are written
+        int s = 0, slot = 0;
+        uint32_t ph = 0;
+        for (; s < nsl; ++s) {
+            if (!mbar_wait_sleep_warp(&b_empty[slot], ph ^ 1, abort_flag, a.err, lane))
                 break;
-            if (KST == CHUNK_K || (st & 1) == 0)
-                prefetch();
             if (lane == 0) {
-                uint8_t *dst = smem + slot * STAGE_BYTES;
-                const int k = c0 * CHUNK_K + st * KST;
-                mbar_arrive_expect_tx(&b_full[slot], bytes);
-#pragma unroll
-                for (int s = 0; s < NSL; ++s)
-                    tma_2d(dst + s * SLICE_BYTES, &map_b, k + s * HALF_K, tok0, &b_full[slot]);
+                uint8_t *dst = smem + slot * slot_bytes;
+                mbar_arrive_expect_tx(&b_full[slot], slot_bytes);
+                tma_2d(dst, &map_b, c0 * CHUNK_K + s * HALF_K, tok0, &b_full[slot]);
                 if (AS)  // the store seen as [row tiles * chunks * 2 halves * 128][64]
-                    tma_2d(dst + NSL * SLICE_BYTES, &map_a, 0, ((rt * a.kchunks + c0) * 2 + st) * TILE_ROWS,
-                           &b_full[slot]);
+                    tma_2d(dst + slice_bytes, &map_a, 0, ((rt * a.kchunks + c0) * 2 + s) * TILE_ROWS, &b_full[slot]);
+            }
+            if (++slot == a.b_slots) {
+                slot = 0;
+                ph ^= 1;
             }
         }
-        // every copy of an armed stage has landed before the CTA goes on (at once
-        // on the normal path; bounded after an abort)
+        // every copy of an armed slot has landed before the CTA goes on (at once on
+        // the normal path; bounded after an abort)
         if (lane == 0)
-            for (int s = st > RING ? st - RING : 0; s < st; ++s)
-                mbar_drain(&b_full[s % RING], (s / RING) & 1);
+            for (int i = s > a.b_slots ? s - a.b_slots : 0; i < s; ++i)
+                mbar_drain(&b_full[i % a.b_slots], (i / a.b_slots) & 1);
+        __syncwarp();
+    } else if (warp == WARP_WEIGHTS) {
+        // ---------------------------------------------------------- weight chunks -> ring
+        if (!AS) {
+            const uint8_t *src = a.w + ((size_t)rt * a.kchunks + c0) * (size_t)CB;
+            int c = 0, slot = 0;
+            uint32_t ph = 0;
+            for (; c < c1 - c0; ++c) {
+                if (!mbar_wait_sleep_warp(&w_empty[slot], ph ^ 1, abort_flag, a.err, lane))
+                    break;
+                if (lane == 0) {
+                    mbar_arrive_expect_tx(&w_full[slot], CB);
+                    bulk_g2s(smem + a.w_off + slot * CB, src + (size_t)c * CB, CB, &w_full[slot]);
+                }
+                if (++slot == a.w_slots) {
+                    slot = 0;
+                    ph ^= 1;
+                }
+            }
+            if (lane == 0)
+                for (int i = c > a.w_slots ? c - a.w_slots : 0; i < c; ++i)
+                    mbar_drain(&w_full[i % a.w_slots], (i / a.w_slots) & 1);
+        }
         __syncwarp();
     } else if (warp == WARP_MMA) {
         // ---------------------------------------------------------- MMAs (lane 0)
         if (lane == 0) {
             const uint64_t desc0 = sw128(smem_addr(smem));
             const uint32_t idesc = instr_desc(OP == LIN_BF16, n_mma);
-            for (int st = 0; st < nst; ++st) {
-                const int bs = st % RING, as = st % A_STAGES;
-                // a_full comes after the stage's B tiles too: its decoders wait for both
-                if (!(AS ? mbar_wait(&b_full[bs], (st / RING) & 1, abort_flag, a.err)
-                         : mbar_wait(&a_full[as], (st / A_STAGES) & 1, abort_flag, a.err)))
+            int slot = 0;
+            uint32_t ph = 0;
+            bool ok = true;
+            for (int st = 0; st < nst && ok; ++st) {
+                const int as = st % A_STAGES;
+                if (!AS && !(ok = mbar_wait(&a_full[as], (st / A_STAGES) & 1, abort_flag, a.err)))
                     break;
-                fence_after();
-                const uint64_t bd = desc0 + (uint64_t)((bs * STAGE_BYTES) >> 4);
                 const uint32_t at = tmem_a + as * A_SLOT_COLS;
-                if (AS) {
-                    mma64<true>(tmem, 0, bd + (uint64_t)((NSL * SLICE_BYTES) >> 4), bd, idesc, st);
-                } else if (OP == LIN_I4) {
-                    mma64<false>(tmem, at, 0, bd, idesc, st);
-                    mma64<false>(tmem, at + 32, 0, bd, idesc, 1u);
-                } else {
 #pragma unroll
-                    for (int s = 0; s < NSL; ++s)
-                        mma64<false>(tmem, at + 32 * s, 0, bd + (uint64_t)((s * SLICE_BYTES) >> 4), idesc,
-                                     st > 0 || s > 0);
+                for (int sl = 0; sl < NSL; ++sl) {
+                    if (!(ok = mbar_wait(&b_full[slot], ph, abort_flag, a.err)))
+                        break;
+                    fence_after();
+                    const uint64_t bd = desc0 + (uint64_t)((slot * slot_bytes) >> 4);
+                    if (AS) {
+                        mma64<true>(tmem, 0, bd + (uint64_t)(slice_bytes >> 4), bd, idesc, st);
+                    } else if (OP == LIN_I4) {
+                        mma64<false>(tmem, at, 0, bd, idesc, st);
+                        mma64<false>(tmem, at + 32, 0, bd, idesc, 1u);
+                    } else {
+                        mma64<false>(tmem, at + 32 * sl, 0, bd, idesc, st > 0 || sl > 0);
+                    }
+                    commit(&b_empty[slot]);
+                    if (++slot == a.b_slots) {
+                        slot = 0;
+                        ph ^= 1;
+                    }
                 }
-                commit(&b_empty[bs]);
                 if (!AS)
                     commit(&a_empty[as]);
             }
             // also after an abort: what was issued has completed before the tensor
-            // memory is freed and the ring reused
+            // memory is freed and the rings reused
             commit(acc_full);
             mbar_drain(acc_full, 0);
         }
         __syncwarp();
-    } else {
+    } else if (warp >= WARP_DEC) {
         // ---------------------------------------------------------- decode
-        const int q = warp & 3, r = 32 * q + lane;  // lane quadrant; row of the tile
+        const int q = warp & 3, grp = (warp - WARP_DEC) >> 2, r = 32 * q + lane;  // lane quadrant; row of the tile
         const uint32_t tlane = (uint32_t)(32 * q) << 16;
         bool ok = true;
         if (!AS) {
             const int rb = OP == LIN_BF16 ? 127 : (int)__ldg(a.row_base + rt * TILE_ROWS + r);
-            uint4 code[NBLK];
-            uint32_t sc[NBLK];
-            auto fetch = [&](int st) {
-                const uint8_t *ch = wsrc + (size_t)(st * KST / CHUNK_K) * a.chunk_bytes;
-                const int b0 = KST == CHUNK_K ? 0 : 2 * (st & 1);
+            constexpr int STEP = KST == CHUNK_K ? DEC_GROUPS : 1;  // chunks from one stage of the group to its next
+            int slot = KST == CHUNK_K ? grp : 0;
+            uint32_t ph = 0;
+            const bool second = KST < CHUNK_K && grp == 1;         // this group decodes the chunks' second halves
+            for (int st = grp; st < nst; st += DEC_GROUPS) {
+                if (!(ok = mbar_wait_warp(&w_full[slot], ph, abort_flag, a.err, lane)))
+                    break;
+                const uint8_t *ch = smem + a.w_off + slot * CB;
+                uint4 code[NBLK];
+                uint32_t sc[NBLK];
 #pragma unroll
                 for (int b = 0; b < NBLK; ++b) {
-                    const int blk = b0 + b;
+                    const int blk = (second ? 2 : 0) + b;
                     if (OP == LIN_I4) {
-                        code[b] = __ldg(reinterpret_cast<const uint4 *>(ch + (blk * TILE_ROWS + r) * 16));
-                        sc[b] = (uint32_t)__ldg(reinterpret_cast<const uint16_t *>(ch + CHUNK_MX_CODE_BYTES) +
-                                                blk * TILE_ROWS + r) |
-                                (uint32_t)__ldg(ch + CHUNK_MX_CODE_BYTES + CHUNK_I4_SCALE_BYTES + blk * TILE_ROWS + r)
-                                    << 16;
+                        code[b] = *reinterpret_cast<const uint4 *>(ch + (blk * TILE_ROWS + r) * 16);
+                        sc[b] = (uint32_t)*(reinterpret_cast<const uint16_t *>(ch + CHUNK_MX_CODE_BYTES) +
+                                            blk * TILE_ROWS + r) |
+                                (uint32_t)ch[CHUNK_MX_CODE_BYTES + CHUNK_I4_SCALE_BYTES + blk * TILE_ROWS + r] << 16;
                     } else if (OP == LIN_F16) {
-                        code[b] = __ldg(reinterpret_cast<const uint4 *>(ch + (blk * TILE_ROWS + r) * 16));
-                        sc[b] = __ldg(ch + CHUNK_MX_CODE_BYTES + blk * TILE_ROWS + r);
+                        code[b] = *reinterpret_cast<const uint4 *>(ch + (blk * TILE_ROWS + r) * 16);
+                        sc[b] = ch[CHUNK_MX_CODE_BYTES + blk * TILE_ROWS + r];
                     } else {
-                        code[b] = __ldg(reinterpret_cast<const uint4 *>(ch + (blk >> 1) * (CHUNK_MX_CODE_BYTES / 2) +
-                                                                        r * 32 + (blk & 1) * 16));
-                        sc[b] = __ldg(ch + CHUNK_MX_CODE_BYTES + r * 4 + blk);
+                        code[b] = *reinterpret_cast<const uint4 *>(ch + (blk >> 1) * (CHUNK_MX_CODE_BYTES / 2) +
+                                                                   r * 32 + (blk & 1) * 16);
+                        sc[b] = ch[CHUNK_MX_CODE_BYTES + r * 4 + blk];
                     }
                 }
-            };
-            if (nst > 0)
-                fetch(0);
-            for (int st = 0; st < nst; ++st) {
-                const int slot = st % A_STAGES;
-                if (!(ok = mbar_wait_warp(&a_empty[slot], ((st / A_STAGES) & 1) ^ 1, abort_flag, a.err, lane)))
+                __syncwarp();  // the stage's codes are in registers
+                if (lane == 0)
+                    mbar_arrive(&w_empty[slot]);
+                if ((slot += STEP) >= a.w_slots) {
+                    slot -= a.w_slots;
+                    ph ^= 1;
+                }
+                if (!(ok = mbar_wait_warp(&a_empty[grp], ((st / A_STAGES) & 1) ^ 1, abort_flag, a.err, lane)))
                     break;
                 fence_after();
-                const uint32_t dst = tmem_a + tlane + slot * A_SLOT_COLS;
+                const uint32_t dst = tmem_a + tlane + grp * A_SLOT_COLS;
 #pragma unroll
                 for (int b = 0; b < NBLK; ++b) {
                     const uint32_t w[4] = {code[b].x, code[b].y, code[b].z, code[b].w};
@@ -375,44 +418,56 @@ __global__ void __launch_bounds__(THREADS, 2)
                     }
                     tmem_st16(dst + b * 16, o);
                 }
-                if (st + 1 < nst)
-                    fetch(st + 1);
                 asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
                 fence_before();
-                if (!(ok = mbar_wait_warp(&b_full[st % RING], (st / RING) & 1, abort_flag, a.err, lane)))
-                    break;
+                __syncwarp();
                 if (lane == 0)
-                    mbar_arrive(&a_full[slot]);
+                    mbar_arrive(&a_full[grp]);
             }
         }
         // ---------------------------------------------------------- the tile's sums
+        asm volatile("griddepcontrol.wait;" ::: "memory");
+        if (OP != LIN_BF16) {  // (every warp writes the same values and reads its own)
+            for (int i = lane; i < nvalid; i += 32)
+                tsc[i] = __ldcg(a.xscale + tok0 + i);
+            __syncwarp();
+        }
         if (ok && mbar_wait_sleep_warp(acc_full, 0, abort_flag, a.err, lane)) {
             fence_after();
             const int n = rt * TILE_ROWS + r;
             const float wsc =
                 OP == LIN_BF16 ? 1.f : ldexpf(1.f, (int)__ldg(a.row_base + rt * TILE_ROWS + r) - 127);
-            float *part = reinterpret_cast<float *>(smem);  // [token][128]: the ring is free
-            for (int c = 0; c < n_mma; c += 16) {
+            float *part = reinterpret_cast<float *>(smem) + r;  // [token][128]: the rings are free
+            for (int c = 16 * grp; c < n_mma; c += 16 * DEC_GROUPS) {
                 float v[16];
-                if (nst > 0)
-                    tmem_ld16(tmem + tlane + c, v);
+                tmem_ld16(tmem + tlane + c, v);
+                if (csize > 1) {
 #pragma unroll
-                for (int j = 0; j < 16; ++j) {
-                    if (c + j >= nvalid)
-                        continue;
-                    const float f = nst > 0 ? v[j] * wsc : 0.f;
-                    if (csize > 1) {
-                        part[(c + j) * TILE_ROWS + r] = f;
-                    } else if (n < a.N) {
-                        const float o = OP == LIN_BF16 ? f : f * tsc[c + j];
-                        const long long at = (long long)(tok0 + c + j) * a.y_ld + n;
-                        if (a.y_f32) {
-                            float *y = static_cast<float *>(a.y) + at;
-                            *y = a.accumulate ? *y + o : o;
-                        } else {
-                            static_cast<__nv_bfloat16 *>(a.y)[at] = __float2bfloat16_rn(o);
-                        }
+                    for (int j = 0; j < 16; ++j)  // (columns past nvalid: inside the tile's room, not read)
+                        part[(c + j) * TILE_ROWS] = v[j] * wsc;
+                } else if (n < a.N) {
+                    const long long at = (long long)(tok0 + c) * a.y_ld + n;
+                    if (OP != LIN_BF16)
+#pragma unroll
+                        for (int j = 0; j < 16; ++j)
+                            v[j] *= wsc * tsc[c + j];
+                    if (a.accumulate) {  // all loads before the first store
+                        float old[16];
+#pragma unroll
+                        for (int j = 0; j < 16; ++j)
+                            old[j] = c + j < nvalid ? static_cast<const float *>(a.y)[at + j * a.y_ld] : 0.f;
+#pragma unroll
+                        for (int j = 0; j < 16; ++j)
+                            v[j] += old[j];
                     }
+#pragma unroll
+                    for (int j = 0; j < 16; ++j)
+                        if (c + j < nvalid) {
+                            if (a.y_f32)
+                                static_cast<float *>(a.y)[at + j * a.y_ld] = v[j];
+                            else
+                                static_cast<__nv_bfloat16 *>(a.y)[at + j * a.y_ld] = __float2bfloat16_rn(v[j]);
+                        }
                 }
             }
         }
@@ -426,30 +481,28 @@ __global__ void __launch_bounds__(THREADS, 2)
         if (!*abort_flag) {
             const uint32_t part = smem_addr(smem);
             for (int t = crank + csize * warp; t < nvalid; t += csize * N_WARPS) {
-                float s[4] = {0.f, 0.f, 0.f, 0.f};
                 const uint32_t local = part + (t * TILE_ROWS + lane * 4) * 4;
-                for (uint32_t rk = 0; rk < csize; ++rk) {
-                    uint32_t remote;
-                    float4 f;
-                    asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(remote) : "r"(local), "r"(rk));
-                    asm volatile("ld.shared::cluster.v4.f32 {%0,%1,%2,%3}, [%4];"
-                                 : "=f"(f.x), "=f"(f.y), "=f"(f.z), "=f"(f.w)
-                                 : "r"(remote));
-                    s[0] += f.x, s[1] += f.y, s[2] += f.z, s[3] += f.w;
-                }
+                float4 f[8];
+#pragma unroll
+                for (uint32_t rk = 0; rk < 8; ++rk)  // all ranks' loads in flight
+                    if (rk < csize) {
+                        uint32_t remote;
+                        asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(remote) : "r"(local), "r"(rk));
+                        asm volatile("ld.shared::cluster.v4.f32 {%0,%1,%2,%3}, [%4];"
+                                     : "=f"(f[rk].x), "=f"(f[rk].y), "=f"(f[rk].z), "=f"(f[rk].w)
+                                     : "r"(remote));
+                    }
+                float o[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                for (uint32_t rk = 0; rk < 8; ++rk)
+                    if (rk < csize)
+                        o[0] += f[rk].x, o[1] += f[rk].y, o[2] += f[rk].z, o[3] += f[rk].w;
+                const float ts = OP == LIN_BF16 ? 1.f : tsc[t];
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
                     const int n = rt * TILE_ROWS + lane * 4 + j;
-                    const float o = OP == LIN_BF16 ? s[j] : s[j] * tsc[t];
-                    if (n < a.N) {
-                        const long long at = (long long)(tok0 + t) * a.y_ld + n;
-                        if (a.y_f32) {
-                            float *y = static_cast<float *>(a.y) + at;
-                            *y = a.accumulate ? *y + o : o;
-                        } else {
-                            static_cast<__nv_bfloat16 *>(a.y)[at] = __float2bfloat16_rn(o);
-                        }
-                    }
+                    if (n < a.N)
+                        store_y(a, (long long)(tok0 + t) * a.y_ld + n, o[j] * ts);
                 }
             }
         }
@@ -466,11 +519,13 @@ __global__ void __launch_bounds__(THREADS, 2)
 // Token rows of the GEMM, one CTA per token: FP16 x * 2^-e (a power of two per
 // token: the largest |x| lands in [2^14, 2^15); exact within 2^-29 of it) with
 // scale[t] = 2^e, or BF16 (of MXFP8 rows).
-__global__ void __launch_bounds__(256) linear_rows_kernel(const void *x, const uint8_t *xscales, long long x_ld,
+__global__ void __launch_bounds__(1024) linear_rows_kernel(const void *x, const uint8_t *xscales, long long x_ld,
                                                           int x_mx, int K, int bf16, uint16_t *out, float *scale)
 {
-    __shared__ uint32_t red[8];
+    __shared__ uint32_t red[32];
     const long long t = blockIdx.x;
+    const int nt = blockDim.x;
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // the GEMM starts on the weights
     auto load = [&](int v, float f[8]) {
         if (x_mx) {
             const uint2 u = __ldg(reinterpret_cast<const uint2 *>(static_cast<const uint8_t *>(x) + t * x_ld) + v);
@@ -500,7 +555,7 @@ __global__ void __launch_bounds__(256) linear_rows_kernel(const void *x, const u
     float mul = 1.f;
     if (!bf16) {
         float m = 0.f;  // (NaN is left out and stays NaN in FP16)
-        for (int v = threadIdx.x; v < nv; v += 256) {
+        for (int v = threadIdx.x; v < nv; v += nt) {
             float f[8];
             load(v, f);
 #pragma unroll
@@ -512,15 +567,14 @@ __global__ void __launch_bounds__(256) linear_rows_kernel(const void *x, const u
             red[threadIdx.x >> 5] = b;
         __syncthreads();
         b = 0;
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
+        for (int i = 0; i < nt / 32; ++i)
             b = max(b, red[i]);
         const int e = max((int)(b >> 23) - 141, -126);
         mul = __int_as_float((127 - e) << 23);
         if (threadIdx.x == 0)
             scale[t] = __int_as_float((127 + e) << 23);
     }
-    for (int v = threadIdx.x; v < nv; v += 256) {
+    for (int v = threadIdx.x; v < nv; v += nt) {
         float f[8];
         uint32_t o[4];
         load(v, f);
@@ -558,7 +612,7 @@ cudaError_t rows_map(CUtensorMap *m, const void *base, long long rows, int cols,
 
 template <int OP, int WFMT>
 cudaError_t launch_cfg(const Args &a, const CUtensorMap &mb, const CUtensorMap &ma, int grid, int cluster,
-                       cudaStream_t st)
+                       bool after_rows, cudaStream_t st)
 {
     auto kern = linear_tc_kernel<OP, WFMT>;
     static std::atomic<int> attr_set[MAX_DEVICES];
@@ -570,12 +624,19 @@ cudaError_t launch_cfg(const Args &a, const CUtensorMap &mb, const CUtensorMap &
     cfg.blockDim = dim3(THREADS);
     cfg.dynamicSmemBytes = SMEM_BYTES;
     cfg.stream = st;
-    cudaLaunchAttribute at;
-    at.id = cudaLaunchAttributeClusterDimension;
-    at.val.clusterDim.x = (unsigned)cluster;
-    at.val.clusterDim.y = at.val.clusterDim.z = 1;
-    cfg.attrs = &at;
-    cfg.numAttrs = cluster > 1;
+    cudaLaunchAttribute at[2];
+    cfg.attrs = at;
+    if (cluster > 1) {
+        at[cfg.numAttrs].id = cudaLaunchAttributeClusterDimension;
+        at[cfg.numAttrs].val.clusterDim.x = (unsigned)cluster;
+        at[cfg.numAttrs].val.clusterDim.y = at[cfg.numAttrs].val.clusterDim.z = 1;
+        ++cfg.numAttrs;
+    }
+    if (after_rows) {
+        at[cfg.numAttrs].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        at[cfg.numAttrs].val.programmaticStreamSerializationAllowed = 1;
+        ++cfg.numAttrs;
+    }
     return cudaLaunchKernelEx(&cfg, kern, a, mb, ma);
 }
 
@@ -593,7 +654,6 @@ cudaError_t launch_linear_gemm(const LinearGemm &g, cudaStream_t st)
     a.N = g.N;
     a.T = g.T;
     a.kchunks = g.w->kchunks;
-    a.chunk_bytes = g.w->chunk_bytes;
     a.ttiles = (g.T + NMAX - 1) / NMAX;
     a.tile_tokens = ((g.T + a.ttiles - 1) / a.ttiles + 15) & ~15;
     a.ttiles = (g.T + a.tile_tokens - 1) / a.tile_tokens;
@@ -603,14 +663,27 @@ cudaError_t launch_linear_gemm(const LinearGemm &g, cudaStream_t st)
     a.accumulate = g.accumulate;
     a.err = g.err;
     const bool bf16 = g.op == LIN_BF16;
+    // the rings: enough token slots to cover their loads, the rest for weight chunks
+    const int slot_bytes = a.tile_tokens * HALF_K * 2 + (g.fmt == FMT_BF16 ? A_TILE_BYTES : 0);
+    if (g.fmt == FMT_BF16) {
+        a.b_slots = RING_BYTES / slot_bytes < B_MAX ? RING_BYTES / slot_bytes : B_MAX;
+        a.w_slots = 0;
+    } else {
+        a.b_slots = a.tile_tokens <= 32 ? B_MAX : a.tile_tokens <= 64 ? 8 : 5;
+        a.w_off = a.b_slots * slot_bytes;
+        a.w_slots = (RING_BYTES - a.w_off) / g.w->chunk_bytes;
+        if (a.w_slots > W_MAX)
+            a.w_slots = W_MAX;
+    }
     CUtensorMap mb, ma;
     cudaError_t e;
-    if (bf16 && !g.x_mx) {
+    const bool rows_written = !bf16 || g.x_mx;
+    if (!rows_written) {
         e = rows_map(&mb, g.x, g.T, g.K, g.x_ld * 2, a.tile_tokens);
     } else {
         uint16_t *rows = reinterpret_cast<uint16_t *>(g.workspace);
         float *scale = reinterpret_cast<float *>(g.workspace + align256((size_t)g.T * g.K * 2));
-        linear_rows_kernel<<<g.T, 256, 0, st>>>(g.x, g.xscales, g.x_ld, g.x_mx, g.K, bf16, rows, scale);
+        linear_rows_kernel<<<g.T, g.T <= 2 * sm_count() ? 1024 : 256, 0, st>>>(g.x, g.xscales, g.x_ld, g.x_mx, g.K, bf16, rows, scale);
         if ((e = cudaGetLastError()) != cudaSuccess)
             return e;
         a.xscale = scale;
@@ -632,11 +705,11 @@ cudaError_t launch_linear_gemm(const LinearGemm &g, cudaStream_t st)
         cluster *= 2;
     const int grid = (int)items * cluster;
     switch (g.op) {
-    case LIN_F16: return launch_cfg<LIN_F16, FMT_MXFP4>(a, mb, ma, grid, cluster, st);
-    case LIN_I4: return launch_cfg<LIN_I4, FMT_INT4>(a, mb, ma, grid, cluster, st);
+    case LIN_F16: return launch_cfg<LIN_F16, FMT_MXFP4>(a, mb, ma, grid, cluster, rows_written, st);
+    case LIN_I4: return launch_cfg<LIN_I4, FMT_INT4>(a, mb, ma, grid, cluster, rows_written, st);
     default:
-        return g.fmt == FMT_BF16 ? launch_cfg<LIN_BF16, FMT_BF16>(a, mb, ma, grid, cluster, st)
-                                 : launch_cfg<LIN_BF16, FMT_MXFP4>(a, mb, ma, grid, cluster, st);
+        return g.fmt == FMT_BF16 ? launch_cfg<LIN_BF16, FMT_BF16>(a, mb, ma, grid, cluster, rows_written, st)
+                                 : launch_cfg<LIN_BF16, FMT_MXFP4>(a, mb, ma, grid, cluster, rows_written, st);
     }
 }
 
