@@ -53,8 +53,10 @@ constexpr int A_TILE_BYTES = TILE_ROWS * HALF_K * 2;     // BF16 weights: 16 KB
 // of weight chunks.
 constexpr int RING_BYTES = 108 * 1024;
 constexpr int B_MAX = 12, W_MAX = 8;  // slots
+constexpr int DONE = 12;              // barriers of finished stages
+static_assert(DONE >= B_MAX, "see linear_tc_kernel");
 constexpr int BAR_OFF = RING_BYTES;
-constexpr int N_BARS = 2 * B_MAX + 2 * W_MAX + 2 * A_STAGES + 1;
+constexpr int N_BARS = B_MAX + 2 * W_MAX + A_STAGES + DONE + 1;
 constexpr int MISC_OFF = BAR_OFF + N_BARS * 8;
 constexpr int TSC_OFF = MISC_OFF + 16;                   // the tile's token scales
 constexpr int SMEM_BYTES = TSC_OFF + NMAX * 4 + 1024;    // + alignment slack
@@ -103,20 +105,24 @@ template <bool AS>
 __device__ __forceinline__ void mma64(uint32_t d, uint32_t a_tmem, uint64_t a_desc, uint64_t b, uint32_t idesc,
                                       uint32_t acc0)
 {
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {
-        const uint32_t acc = k ? 1u : acc0;
-        if (AS)
-            asm volatile("{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
-                         " tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(d),
-                         "l"(a_desc + 2 * k), "l"(b + 2 * k), "r"(idesc), "r"(acc)
-                         : "memory");
-        else
-            asm volatile("{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
-                         " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d),
-                         "r"(a_tmem + 8 * k), "l"(b + 2 * k), "r"(idesc), "r"(acc)
-                         : "memory");
-    }
+    if (AS)
+        asm volatile("{\n .reg .pred p, t;\n setp.ne.b32 p, %4, 0;\n setp.eq.b32 t, %4, %4;\n"
+                     " tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n"
+                     " tcgen05.mma.cta_group::1.kind::f16 [%0], %5, %6, %3, t;\n"
+                     " tcgen05.mma.cta_group::1.kind::f16 [%0], %7, %8, %3, t;\n"
+                     " tcgen05.mma.cta_group::1.kind::f16 [%0], %9, %10, %3, t;\n}\n" ::"r"(d),
+                     "l"(a_desc), "l"(b), "r"(idesc), "r"(acc0), "l"(a_desc + 2), "l"(b + 2), "l"(a_desc + 4),
+                     "l"(b + 4), "l"(a_desc + 6), "l"(b + 6)
+                     : "memory");
+    else
+        asm volatile("{\n .reg .pred p, t;\n setp.ne.b32 p, %4, 0;\n setp.eq.b32 t, %4, %4;\n"
+                     " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n"
+                     " tcgen05.mma.cta_group::1.kind::f16 [%0], [%5], %6, %3, t;\n"
+                     " tcgen05.mma.cta_group::1.kind::f16 [%0], [%7], %8, %3, t;\n"
+                     " tcgen05.mma.cta_group::1.kind::f16 [%0], [%9], %10, %3, t;\n}\n" ::"r"(d),
+                     "r"(a_tmem), "l"(b), "r"(idesc), "r"(acc0), "r"(a_tmem + 8), "l"(b + 2), "r"(a_tmem + 16),
+                     "l"(b + 4), "r"(a_tmem + 24), "l"(b + 6)
+                     : "memory");
 }
 
 // 16 tensor-memory columns of this warp's 32 lanes
@@ -202,9 +208,8 @@ __global__ void __launch_bounds__(THREADS, 2)
     constexpr int CB = WFMT == FMT_INT4 ? CHUNK_I4_BYTES : CHUNK_MX_BYTES;
     extern __shared__ uint8_t smem_dyn[];
     uint8_t *smem = smem_dyn + ((1024u - (smem_addr(smem_dyn) & 1023u)) & 1023u);
-    uint64_t *b_full = reinterpret_cast<uint64_t *>(smem + BAR_OFF), *b_empty = b_full + B_MAX;
-    uint64_t *w_full = b_empty + B_MAX, *w_empty = w_full + W_MAX;
-    uint64_t *a_full = w_empty + W_MAX, *a_empty = a_full + A_STAGES, *acc_full = a_empty + A_STAGES;
+    uint64_t *b_full = reinterpret_cast<uint64_t *>(smem + BAR_OFF), *w_full = b_full + B_MAX;
+    uint64_t *w_empty = w_full + W_MAX, *a_full = w_empty + W_MAX, *done = a_full + A_STAGES, *acc_full = done + DONE;
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + MISC_OFF);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + MISC_OFF + 4);
     float *tsc = reinterpret_cast<float *>(smem + TSC_OFF);
@@ -221,18 +226,16 @@ __global__ void __launch_bounds__(THREADS, 2)
     const uint32_t slice_bytes = (uint32_t)a.tile_tokens * HALF_K * 2, slot_bytes = slice_bytes + (AS ? A_TILE_BYTES : 0);
 
     if (tid == 0) {
-        for (int i = 0; i < a.b_slots; ++i) {
+        for (int i = 0; i < a.b_slots; ++i)
             mbar_init(&b_full[i], 1);
-            mbar_init(&b_empty[i], 1);
-        }
         for (int i = 0; i < a.w_slots; ++i) {
             mbar_init(&w_full[i], 1);
             mbar_init(&w_empty[i], KST == CHUNK_K ? 4 : 8);  // a chunk of two stages is read by both groups
         }
-        for (int i = 0; i < A_STAGES; ++i) {
+        for (int i = 0; i < A_STAGES; ++i)
             mbar_init(&a_full[i], 4);
-            mbar_init(&a_empty[i], 1);
-        }
+        for (int i = 0; i < DONE; ++i)
+            mbar_init(&done[i], 1);
         mbar_init(acc_full, 1);
         *abort_flag = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -247,6 +250,14 @@ __global__ void __launch_bounds__(THREADS, 2)
     fence_before();
     __syncthreads();
     fence_after();
+    // The MMAs of a stage are committed once, to the barrier of the stage (a commit
+    // costs the issuing thread about 250 cycles, an MMA 50): it frees the stage's A
+    // slot and its token slots.  Nobody waits for a stage whose barrier could have
+    // come round again, which takes the end of stage + DONE: the decoders' wait comes
+    // before they decode for stage + A_STAGES, and the loader's before it loads token
+    // slot NSL * stage + b_slots, the first of stage + DONE or an earlier one.
+    auto done_bar = [&](int st) { return &done[st % DONE]; };
+    auto done_par = [&](int st) { return (uint32_t)(st / DONE) & 1u; };
     const uint32_t tmem = *tmem_slot;
     const uint32_t tmem_a = tmem + NMAX;
 
@@ -254,9 +265,9 @@ __global__ void __launch_bounds__(THREADS, 2)
         // ---------------------------------------------------------- token tiles -> ring
         asm volatile("griddepcontrol.wait;" ::: "memory");  // the token rows are written
         int s = 0, slot = 0;
-        uint32_t ph = 0;
         for (; s < nsl; ++s) {
-            if (!mbar_wait_sleep_warp(&b_empty[slot], ph ^ 1, abort_flag, a.err, lane))
+            const int used = (s - a.b_slots) / NSL;  // the stage that the slot held before
+            if (s >= a.b_slots && !mbar_wait_sleep_warp(done_bar(used), done_par(used), abort_flag, a.err, lane))
                 break;
             if (lane == 0) {
                 uint8_t *dst = smem + slot * slot_bytes;
@@ -265,10 +276,8 @@ __global__ void __launch_bounds__(THREADS, 2)
                 if (AS)  // the store seen as [row tiles * chunks * 2 halves * 128][64]
                     tma_2d(dst + slice_bytes, &map_a, 0, ((rt * a.kchunks + c0) * 2 + s) * TILE_ROWS, &b_full[slot]);
             }
-            if (++slot == a.b_slots) {
+            if (++slot == a.b_slots)
                 slot = 0;
-                ph ^= 1;
-            }
         }
         // every copy of an armed slot has landed before the CTA goes on (at once on
         // the normal path; bounded after an abort)
@@ -326,14 +335,12 @@ __global__ void __launch_bounds__(THREADS, 2)
                     } else {
                         mma64<false>(tmem, at + 32 * sl, 0, bd, idesc, st > 0 || sl > 0);
                     }
-                    commit(&b_empty[slot]);
                     if (++slot == a.b_slots) {
                         slot = 0;
                         ph ^= 1;
                     }
                 }
-                if (!AS)
-                    commit(&a_empty[as]);
+                commit(done_bar(st));
             }
             // also after an abort: what was issued has completed before the tensor
             // memory is freed and the rings reused
@@ -382,7 +389,8 @@ __global__ void __launch_bounds__(THREADS, 2)
                     slot -= a.w_slots;
                     ph ^= 1;
                 }
-                if (!(ok = mbar_wait_warp(&a_empty[grp], ((st / A_STAGES) & 1) ^ 1, abort_flag, a.err, lane)))
+                if (st >= A_STAGES && !(ok = mbar_wait_warp(done_bar(st - A_STAGES), done_par(st - A_STAGES), abort_flag,
+                                                            a.err, lane)))
                     break;
                 fence_after();
                 const uint32_t dst = tmem_a + tlane + grp * A_SLOT_COLS;
