@@ -677,11 +677,15 @@ cudaError_t launch_linear_gemm(const LinearGemm &g, cudaStream_t st)
         a.b_slots = RING_BYTES / slot_bytes < B_MAX ? RING_BYTES / slot_bytes : B_MAX;
         a.w_slots = 0;
     } else {
-        a.b_slots = a.tile_tokens <= 32 ? B_MAX : a.tile_tokens <= 64 ? 8 : 5;
+        a.b_slots = a.tile_tokens <= 32 ? B_MAX : a.tile_tokens <= 64 ? 8 : 5;  // (leaves two chunks at least)
         a.w_off = a.b_slots * slot_bytes;
         a.w_slots = (RING_BYTES - a.w_off) / g.w->chunk_bytes;
         if (a.w_slots > W_MAX)
             a.w_slots = W_MAX;
+        // an even number, so that every load of a slot is waited for by one and the
+        // same decoder group: a group that skipped one could take the phase before
+        // it for the one that it waits for
+        a.w_slots &= ~1;
     }
     CUtensorMap mb, ma;
     cudaError_t e;
