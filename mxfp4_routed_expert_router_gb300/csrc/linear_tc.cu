@@ -40,13 +40,13 @@ using namespace gemm;
 
 constexpr int N_WARPS = 12, THREADS = N_WARPS * 32;
 constexpr int WARP_LOAD = 0, WARP_MMA = 1, WARP_WEIGHTS = 2, WARP_DEC = 4;  // (3 idles)
-constexpr int DEC_GROUPS = 2;         // group g decodes the stages of A slot g
+constexpr int DEC_GROUPS = 2;         // group g decodes the stages g, g + 2, ...
 constexpr int NMAX = 128;             // tokens of a tile
-constexpr int A_STAGES = 2;           // A ring (tensor memory)
+constexpr int A_MAX = 3;              // slots of the A ring (tensor memory): three with tiles of at most NHALF
+constexpr int NHALF = 64;             // tokens, two with larger ones
 constexpr int A_SLOT_COLS = 64;       // 128 16-bit values per lane
 constexpr int TMEM_COLS = 256;        // half of the SM's: accumulator and A ring
-static_assert(DEC_GROUPS == A_STAGES, "a group fills its own A slot");
-static_assert(NMAX + A_STAGES * A_SLOT_COLS <= TMEM_COLS, "tensor memory");
+static_assert(NMAX + 2 * A_SLOT_COLS <= TMEM_COLS && NHALF + A_MAX * A_SLOT_COLS <= TMEM_COLS, "tensor memory");
 constexpr int A_TILE_BYTES = TILE_ROWS * HALF_K * 2;     // BF16 weights: 16 KB
 // Shared memory: the token ring (slots of 64 values of K: a swizzled tile of
 // tile_tokens x 128 bytes, with BF16 weights the A tile after it), then the ring
@@ -56,7 +56,7 @@ constexpr int B_MAX = 12, W_MAX = 8;  // slots
 constexpr int DONE = 12;              // barriers of finished stages
 static_assert(DONE >= B_MAX, "see linear_tc_kernel");
 constexpr int BAR_OFF = RING_BYTES;
-constexpr int N_BARS = B_MAX + 2 * W_MAX + A_STAGES + DONE + 1;
+constexpr int N_BARS = B_MAX + 2 * W_MAX + A_MAX + DONE + 1;
 constexpr int MISC_OFF = BAR_OFF + N_BARS * 8;
 constexpr int TSC_OFF = MISC_OFF + 16;                   // the tile's token scales
 constexpr int SMEM_BYTES = TSC_OFF + NMAX * 4 + 1024;    // + alignment slack
@@ -209,7 +209,7 @@ __global__ void __launch_bounds__(THREADS, 2)
     extern __shared__ uint8_t smem_dyn[];
     uint8_t *smem = smem_dyn + ((1024u - (smem_addr(smem_dyn) & 1023u)) & 1023u);
     uint64_t *b_full = reinterpret_cast<uint64_t *>(smem + BAR_OFF), *w_full = b_full + B_MAX;
-    uint64_t *w_empty = w_full + W_MAX, *a_full = w_empty + W_MAX, *done = a_full + A_STAGES, *acc_full = done + DONE;
+    uint64_t *w_empty = w_full + W_MAX, *a_full = w_empty + W_MAX, *done = a_full + A_MAX, *acc_full = done + DONE;
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + MISC_OFF);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + MISC_OFF + 4);
     float *tsc = reinterpret_cast<float *>(smem + TSC_OFF);
@@ -232,7 +232,7 @@ __global__ void __launch_bounds__(THREADS, 2)
             mbar_init(&w_full[i], 1);
             mbar_init(&w_empty[i], KST == CHUNK_K ? 4 : 8);  // a chunk of two stages is read by both groups
         }
-        for (int i = 0; i < A_STAGES; ++i)
+        for (int i = 0; i < A_MAX; ++i)
             mbar_init(&a_full[i], 4);
         for (int i = 0; i < DONE; ++i)
             mbar_init(&done[i], 1);
@@ -250,16 +250,19 @@ __global__ void __launch_bounds__(THREADS, 2)
     fence_before();
     __syncthreads();
     fence_after();
-    // The MMAs of a stage are committed once, to the barrier of the stage (a commit
-    // costs the issuing thread about 250 cycles, an MMA 50): it frees the stage's A
-    // slot and its token slots.  Nobody waits for a stage whose barrier could have
+    // The MMAs of a stage are committed once, to the barrier of the stage: it frees
+    // the stage's A slot and its token slots.  Nobody waits for a stage whose barrier could have
     // come round again, which takes the end of stage + DONE: the decoders' wait comes
-    // before they decode for stage + A_STAGES, and the loader's before it loads token
-    // slot NSL * stage + b_slots, the first of stage + DONE or an earlier one.
+    // before they decode for stage + a_slots, and the loader's before it loads token
+    // slot NSL * stage + b_slots, the first of stage + DONE or an earlier one.  Nor
+    // does anybody skip a phase of a barrier that it waits for (it could take the
+    // older one for it): decoder groups take every other chunk, and the ring of chunks
+    // has an even number of slots.
     auto done_bar = [&](int st) { return &done[st % DONE]; };
     auto done_par = [&](int st) { return (uint32_t)(st / DONE) & 1u; };
     const uint32_t tmem = *tmem_slot;
-    const uint32_t tmem_a = tmem + NMAX;
+    const int a_slots = a.tile_tokens <= NHALF ? A_MAX : 2;
+    const uint32_t tmem_a = tmem + (a.tile_tokens <= NHALF ? NHALF : NMAX);
 
     if (warp == WARP_LOAD) {
         // ---------------------------------------------------------- token tiles -> ring
@@ -309,24 +312,30 @@ __global__ void __launch_bounds__(THREADS, 2)
         }
         __syncwarp();
     } else if (warp == WARP_MMA) {
-        // ---------------------------------------------------------- MMAs (lane 0)
-        if (lane == 0) {
-            const uint64_t desc0 = sw128(smem_addr(smem));
-            const uint32_t idesc = instr_desc(OP == LIN_BF16, n_mma);
-            int slot = 0;
-            uint32_t ph = 0;
-            bool ok = true;
-            for (int st = 0; st < nst && ok; ++st) {
-                const int as = st % A_STAGES;
-                if (!AS && !(ok = mbar_wait(&a_full[as], (st / A_STAGES) & 1, abort_flag, a.err)))
-                    break;
-                const uint32_t at = tmem_a + as * A_SLOT_COLS;
+        // ---------------------------------------------------------- MMAs
+        // The whole warp runs the loop and one elected lane issues: the operands are
+        // then computed in converged code (measured: 26 cycles an MMA against 49 from
+        // a loop that one lane runs).
+        uint32_t elected;
+        asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xFFFFFFFF;\n selp.u32 %0, 1, 0, p;\n}" : "=r"(elected));
+        auto wait = [&](uint64_t *bar, uint32_t par) {
+            return __all_sync(0xffffffffu, mbar_wait(bar, par, abort_flag, a.err)) != 0;
+        };
+        const uint64_t desc0 = sw128(smem_addr(smem)), bstep = (uint64_t)(slot_bytes >> 4);
+        const uint32_t idesc = instr_desc(OP == LIN_BF16, n_mma);
+        uint64_t bd = desc0;
+        uint32_t at = tmem_a, aph = 0, bph = 0;
+        int as = 0, ds = 0, slot = 0;
+        bool ok = true;
+        for (int st = 0; st < nst && ok; ++st) {
+            if (!AS && !(ok = wait(&a_full[as], aph)))
+                break;
 #pragma unroll
-                for (int sl = 0; sl < NSL; ++sl) {
-                    if (!(ok = mbar_wait(&b_full[slot], ph, abort_flag, a.err)))
-                        break;
-                    fence_after();
-                    const uint64_t bd = desc0 + (uint64_t)((slot * slot_bytes) >> 4);
+            for (int sl = 0; sl < NSL; ++sl) {
+                if (!(ok = wait(&b_full[slot], bph)))
+                    break;
+                fence_after();
+                if (elected) {
                     if (AS) {
                         mma64<true>(tmem, 0, bd + (uint64_t)(slice_bytes >> 4), bd, idesc, st);
                     } else if (OP == LIN_I4) {
@@ -335,15 +344,29 @@ __global__ void __launch_bounds__(THREADS, 2)
                     } else {
                         mma64<false>(tmem, at + 32 * sl, 0, bd, idesc, st > 0 || sl > 0);
                     }
-                    if (++slot == a.b_slots) {
-                        slot = 0;
-                        ph ^= 1;
-                    }
+                    if (sl == NSL - 1)
+                        commit(&done[ds]);
                 }
-                commit(done_bar(st));
+                __syncwarp();
+                bd += bstep;
+                if (++slot == a.b_slots) {
+                    slot = 0;
+                    bph ^= 1;
+                    bd = desc0;
+                }
             }
-            // also after an abort: what was issued has completed before the tensor
-            // memory is freed and the rings reused
+            if (++ds == DONE)
+                ds = 0;
+            at += A_SLOT_COLS;
+            if (++as == a_slots) {
+                as = 0;
+                aph ^= 1;
+                at = tmem_a;
+            }
+        }
+        // also after an abort: what was issued has completed before the tensor memory
+        // is freed and the rings reused
+        if (elected) {
             commit(acc_full);
             mbar_drain(acc_full, 0);
         }
@@ -359,6 +382,7 @@ __global__ void __launch_bounds__(THREADS, 2)
             int slot = KST == CHUNK_K ? grp : 0;
             uint32_t ph = 0;
             const bool second = KST < CHUNK_K && grp == 1;         // this group decodes the chunks' second halves
+            int as = grp;                                          // the stage's A slot
             for (int st = grp; st < nst; st += DEC_GROUPS) {
                 if (!(ok = mbar_wait_warp(&w_full[slot], ph, abort_flag, a.err, lane)))
                     break;
@@ -389,11 +413,11 @@ __global__ void __launch_bounds__(THREADS, 2)
                     slot -= a.w_slots;
                     ph ^= 1;
                 }
-                if (st >= A_STAGES && !(ok = mbar_wait_warp(done_bar(st - A_STAGES), done_par(st - A_STAGES), abort_flag,
-                                                            a.err, lane)))
+                const int prev = st - a_slots;  // the stage that the A slot held before
+                if (prev >= 0 && !(ok = mbar_wait_warp(done_bar(prev), done_par(prev), abort_flag, a.err, lane)))
                     break;
                 fence_after();
-                const uint32_t dst = tmem_a + tlane + grp * A_SLOT_COLS;
+                const uint32_t dst = tmem_a + tlane + as * A_SLOT_COLS;
 #pragma unroll
                 for (int b = 0; b < NBLK; ++b) {
                     const uint32_t w[4] = {code[b].x, code[b].y, code[b].z, code[b].w};
@@ -430,7 +454,9 @@ __global__ void __launch_bounds__(THREADS, 2)
                 fence_before();
                 __syncwarp();
                 if (lane == 0)
-                    mbar_arrive(&a_full[grp]);
+                    mbar_arrive(&a_full[as]);
+                if ((as += DEC_GROUPS) >= a_slots)
+                    as -= a_slots;
             }
         }
         // ---------------------------------------------------------- the tile's sums
@@ -677,15 +703,13 @@ cudaError_t launch_linear_gemm(const LinearGemm &g, cudaStream_t st)
         a.b_slots = RING_BYTES / slot_bytes < B_MAX ? RING_BYTES / slot_bytes : B_MAX;
         a.w_slots = 0;
     } else {
-        a.b_slots = a.tile_tokens <= 32 ? B_MAX : a.tile_tokens <= 64 ? 8 : 5;  // (leaves two chunks at least)
+        a.b_slots = a.tile_tokens <= 32 ? B_MAX : a.tile_tokens <= 64 ? 8 : a.tile_tokens <= 96 ? 6 : 4;
         a.w_off = a.b_slots * slot_bytes;
         a.w_slots = (RING_BYTES - a.w_off) / g.w->chunk_bytes;
         if (a.w_slots > W_MAX)
             a.w_slots = W_MAX;
-        // an even number, so that every load of a slot is waited for by one and the
-        // same decoder group: a group that skipped one could take the phase before
-        // it for the one that it waits for
-        a.w_slots &= ~1;
+        if (g.op != LIN_I4)
+            a.w_slots &= ~1;  // (see linear_tc_kernel; with INT4 both groups read every chunk)
     }
     CUtensorMap mb, ma;
     cudaError_t e;
