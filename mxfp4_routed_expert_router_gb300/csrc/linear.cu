@@ -319,24 +319,22 @@ __device__ __forceinline__ ColScales col_scales(const Step<FMT, NB> &s, int grp,
 __device__ __forceinline__ int owner_of(int u, int units, int n) { return ((u + 1) * n - 1) / units; }
 
 // One CTA: `rgroups` groups of 16 rows (fewer at the end), its K range (the
-// whole of K, or a share of a cluster's), up to TB * NT tokens.  x is staged
+// whole of K, or a share of a cluster's), up to TB tokens.  x is staged
 // once; then every warp streams its share of the CTA's steps with DEPTH of them
 // in flight and writes a partial sum for each row group that it touches.
-// blockIdx.x = row tile * cluster size + rank, blockIdx.y = token tile.
-template <int FMT, int TB, int NT>
+// blockIdx.x = row tile * cluster size + rank.
+template <int FMT, int TB>
 __global__ void __launch_bounds__(THREADS, 1) linear_kernel(const __grid_constant__ LinArgs a)
 {
     constexpr int NB = 8 / TB;         // blocks side by side in the columns of one n-tile
     constexpr bool BF = FMT == FMT_BF16;
-    constexpr int TT = TB * NT;        // tokens of a tile
     constexpr int SC = step_chunks<FMT>, SB = SC * 4;  // chunks and 32-value blocks of a step
-    constexpr int BLK_BYTES = TT * 64;                 // B fragments of a block
+    constexpr int BLK_BYTES = TB * 64;                 // B fragments of a block
     constexpr int CB = chunk_bytes<FMT>;
-    static_assert(NT == 1 || TB == 8, "several n-tiles hold 8 tokens each");
     extern __shared__ __align__(16) uint8_t smem[];
     uint8_t *xf = smem;                                              // B fragments
-    float *xscale = reinterpret_cast<float *>(smem + a.xs_off);      // [256 values][TT] powers of two
-    float *xsum = reinterpret_cast<float *>(smem + a.sum_off);       // INT4: [block][TT] sums of the FP16 values
+    float *xscale = reinterpret_cast<float *>(smem + a.xs_off);      // [256 values][TB] powers of two
+    float *xsum = reinterpret_cast<float *>(smem + a.sum_off);       // INT4: [block][TB] sums of the FP16 values
     float *red = reinterpret_cast<float *>(smem + a.red_off);        // [warp + row group][token][16]
     float *fin = reinterpret_cast<float *>(smem + a.fin_off);        // [row group][token][16] (clusters)
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, q = lane & 3;
@@ -348,8 +346,7 @@ __global__ void __launch_bounds__(THREADS, 1) linear_kernel(const __grid_constan
     const int R = min(a.rgroups, n16 - rg0);
     const int p0 = (int)((long long)a.steps * crank / csize), p1 = (int)((long long)a.steps * (crank + 1) / csize);
     const int P = p1 - p0;
-    const long long t0 = (long long)blockIdx.y * TT;
-    const int tv = min(TT, (int)(a.T - t0));  // tokens of this tile
+    const int tv = a.T;  // at most TB
     const int units = R * P, nw = min(WARPS, units);
     const int u0 = nw ? min(units, warp * units / nw) : 0, u1 = nw ? min(units, (warp + 1) * units / nw) : 0;
 
@@ -419,20 +416,20 @@ __global__ void __launch_bounds__(THREADS, 1) linear_kernel(const __grid_constan
     // take x * 2^-e, e from the item's largest |x| (in [2^14, 2^15) then): exact for
     // BF16 and E4M3 values within 2^-29 of it.
     constexpr int XB = 4;
-    const int items = (P * SB + 7) / 8 * TT;
+    const int items = (P * SB + 7) / 8 * TB;
     const int k0 = p0 * SC * CHUNK_K;
     const int kend = min(a.K, k0 + P * SC * CHUNK_K);
     uint4 xr[XB];
     auto load_items = [&](int i0) {
 #pragma unroll
         for (int b = 0; b < XB; ++b) {
-            const int i = i0 + b * WARPS, t = i % TT;
+            const int i = i0 + b * WARPS, t = i % TB;
             if (i < items && t < tv)
-                xr[b] = load_x8(a, t0 + t, k0 + (i / TT * 32 + lane) * 8, kend);
+                xr[b] = load_x8(a, t, k0 + (i / TB * 32 + lane) * 8, kend);
         }
     };
     load_items(warp);
-    constexpr int DEPTH = BF ? 2 : 3;
+    constexpr int DEPTH = FMT == FMT_MXFP4 ? 3 : 2;  // (three spill with INT4: 33 against 27 us at 7168 x 18432, 8 tokens)
     Step<FMT, NB> st[DEPTH];
 #pragma unroll
     for (int d = 0; d < DEPTH; ++d)
@@ -440,10 +437,10 @@ __global__ void __launch_bounds__(THREADS, 1) linear_kernel(const __grid_constan
     for (int i0 = warp; i0 < items; i0 += XB * WARPS) {
 #pragma unroll
         for (int b = 0; b < XB; ++b) {
-            const int i = i0 + b * WARPS, t = i % TT;
+            const int i = i0 + b * WARPS, t = i % TB;
             if (i >= items || t >= tv)
                 continue;
-            const int c = i / TT * 32 + lane;  // vector of 8 values in this CTA's columns
+            const int c = i / TB * 32 + lane;  // vector of 8 values in this CTA's columns
             uint32_t o[4];
             if (BF) {
                 x8_bf16(a, xr[b], o);
@@ -462,11 +459,11 @@ __global__ void __launch_bounds__(THREADS, 1) linear_kernel(const __grid_constan
                     s += __shfl_xor_sync(0xffffffffu, s, 1);
                     s += __shfl_xor_sync(0xffffffffu, s, 2);
                     if ((lane & 3) == 0)
-                        xsum[(c >> 2) * TT + t] = s;
+                        xsum[(c >> 2) * TB + t] = s;
                 }
             }
             // values 8c .. 8c+7 of the row: k step (c & 3) / 2 of the block, low or high eight
-            uint8_t *dst = xf + ((c >> 2) * TT + t) * 64 + ((c >> 1) & 1) * 8 + (c & 1) * 4;
+            uint8_t *dst = xf + ((c >> 2) * TB + t) * 64 + ((c >> 1) & 1) * 8 + (c & 1) * 4;
 #pragma unroll
             for (int j = 0; j < 4; ++j)
                 *reinterpret_cast<uint32_t *>(dst + j * 16) = o[j];
@@ -476,12 +473,7 @@ __global__ void __launch_bounds__(THREADS, 1) linear_kernel(const __grid_constan
     __syncthreads();
 
     // ---- weight stream
-    float acc[NT][4];
-#pragma unroll
-    for (int n = 0; n < NT; ++n)
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-            acc[n][j] = 0.f;
+    float acc[4] = {0.f, 0.f, 0.f, 0.f};
     // B column g of the lane: token g / NB, block g % NB of a group; NB > 1: B of
     // block i is zero in the lanes of the other columns, which never load it
     uint32_t bx[NB][4];
@@ -494,15 +486,10 @@ __global__ void __launch_bounds__(THREADS, 1) linear_kernel(const __grid_constan
     auto compute = [&](const Step<FMT, NB> &s, int p) {
         const uint32_t *cw = reinterpret_cast<const uint32_t *>(s.c);
         const uint32_t xb = xb0 + p * (SB * BLK_BYTES);
-        float sum[NT][4];  // of the step, in units of the tokens' powers of two
+        float sum[4];  // of the step, in units of the tokens' powers of two
 #pragma unroll
         for (int grp = 0; grp < SB / NB; ++grp) {
-            float part[NT][4];
-#pragma unroll
-            for (int n = 0; n < NT; ++n)
-#pragma unroll
-                for (int j = 0; j < 4; ++j)
-                    part[n][j] = 0.f;
+            float part[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
             for (int i = 0; i < NB; ++i) {
                 const int blk = grp * NB + i;
@@ -520,77 +507,65 @@ __global__ void __launch_bounds__(THREADS, 1) linear_kernel(const __grid_constan
                     decode_u4(cw[2 * blk], a0);
                     decode_u4(cw[2 * blk + 1], a1);
                 }
-#pragma unroll
-                for (int n = 0; n < NT; ++n) {
-                    uint32_t *b = bx[i];
-                    lds16_if(NB == 1 || g % NB == i, xb + blk * BLK_BYTES + n * 512, b);
-                    mma<BF>(BF ? acc[n] : part[n], a0, b[0], b[1]);
-                    mma<BF>(BF ? acc[n] : part[n], a1, b[2], b[3]);
-                }
+                uint32_t *b = bx[i];
+                lds16_if(NB == 1 || g % NB == i, xb + blk * BLK_BYTES, b);
+                mma<BF>(BF ? acc : part, a0, b[0], b[1]);
+                mma<BF>(BF ? acc : part, a1, b[2], b[3]);
             }
             if constexpr (!BF) {
                 const ColScales cs = col_scales<FMT, NB>(s, grp, q);
-#pragma unroll
-                for (int n = 0; n < NT; ++n) {
-                    if (FMT == FMT_INT4) {
-                        // sum q x - z sum x, then the group's scale
-                        const int c0 = 2 * q, c1 = 2 * q + 1;
-                        const float *xs = xsum + (p * SB + grp * NB) * TT + 8 * n;
-                        const float x0 = xs[(c0 % NB) * TT + c0 / NB], x1 = xs[(c1 % NB) * TT + c1 / NB];
-                        part[n][0] = fmaf(part[n][0], 16777216.f, -cs.za.x * x0);
-                        part[n][1] = fmaf(part[n][1], 16777216.f, -cs.za.y * x1);
-                        part[n][2] = fmaf(part[n][2], 1048576.f, -cs.zb.x * x0);
-                        part[n][3] = fmaf(part[n][3], 1048576.f, -cs.zb.y * x1);
-                    }
-                    sum[n][0] = grp ? fmaf(part[n][0], cs.a.x, sum[n][0]) : part[n][0] * cs.a.x;
-                    sum[n][1] = grp ? fmaf(part[n][1], cs.a.y, sum[n][1]) : part[n][1] * cs.a.y;
-                    sum[n][2] = grp ? fmaf(part[n][2], cs.b.x, sum[n][2]) : part[n][2] * cs.b.x;
-                    sum[n][3] = grp ? fmaf(part[n][3], cs.b.y, sum[n][3]) : part[n][3] * cs.b.y;
+                if (FMT == FMT_INT4) {
+                    // sum q x - z sum x, then the group's scale
+                    const int c0 = 2 * q, c1 = 2 * q + 1;
+                    const float *xs = xsum + (p * SB + grp * NB) * TB;
+                    const float x0 = xs[(c0 % NB) * TB + c0 / NB], x1 = xs[(c1 % NB) * TB + c1 / NB];
+                    part[0] = fmaf(part[0], 16777216.f, -cs.za.x * x0);
+                    part[1] = fmaf(part[1], 16777216.f, -cs.za.y * x1);
+                    part[2] = fmaf(part[2], 1048576.f, -cs.zb.x * x0);
+                    part[3] = fmaf(part[3], 1048576.f, -cs.zb.y * x1);
                 }
+                sum[0] = grp ? fmaf(part[0], cs.a.x, sum[0]) : part[0] * cs.a.x;
+                sum[1] = grp ? fmaf(part[1], cs.a.y, sum[1]) : part[1] * cs.a.y;
+                sum[2] = grp ? fmaf(part[2], cs.b.x, sum[2]) : part[2] * cs.b.x;
+                sum[3] = grp ? fmaf(part[3], cs.b.y, sum[3]) : part[3] * cs.b.y;
             }
         }
         if constexpr (!BF) {
-#pragma unroll
-            for (int n = 0; n < NT; ++n) {
-                const float *xs = xscale + p * TT + 8 * n;
-                const float x0 = xs[2 * q / NB], x1 = xs[(2 * q + 1) / NB];
-                acc[n][0] = fmaf(sum[n][0], x0, acc[n][0]);
-                acc[n][1] = fmaf(sum[n][1], x1, acc[n][1]);
-                acc[n][2] = fmaf(sum[n][2], x0, acc[n][2]);
-                acc[n][3] = fmaf(sum[n][3], x1, acc[n][3]);
-            }
+            const float *xs = xscale + p * TB;
+            const float x0 = xs[2 * q / NB], x1 = xs[(2 * q + 1) / NB];
+            acc[0] = fmaf(sum[0], x0, acc[0]);
+            acc[1] = fmaf(sum[1], x1, acc[1]);
+            acc[2] = fmaf(sum[2], x0, acc[2]);
+            acc[3] = fmaf(sum[3], x1, acc[3]);
         }
     };
     // partial sums of row group r (of the CTA): summed over the blocks side by side
     auto flush = [&](int r) {
-        float *o = red + (size_t)(warp + r) * TT * 16;
-#pragma unroll
-        for (int n = 0; n < NT; ++n) {
-            if (NB == 1) {
-                o[(8 * n + 2 * q) * 16 + g] = acc[n][0];
-                o[(8 * n + 2 * q + 1) * 16 + g] = acc[n][1];
-                o[(8 * n + 2 * q) * 16 + g + 8] = acc[n][2];
-                o[(8 * n + 2 * q + 1) * 16 + g + 8] = acc[n][3];
-            } else {
-                float r0 = acc[n][0] + acc[n][1], r1 = acc[n][2] + acc[n][3];
-                if (NB >= 4) {
-                    r0 += __shfl_xor_sync(0xffffffffu, r0, 1);
-                    r1 += __shfl_xor_sync(0xffffffffu, r1, 1);
-                }
-                if (NB == 8) {
-                    r0 += __shfl_xor_sync(0xffffffffu, r0, 2);
-                    r1 += __shfl_xor_sync(0xffffffffu, r1, 2);
-                }
-                const int tok = 2 * q / NB;
-                if (2 * q % NB == 0) {  // one of the lanes that share a token
-                    o[tok * 16 + g] = r0;
-                    o[tok * 16 + g + 8] = r1;
-                }
+        float *o = red + (size_t)(warp + r) * TB * 16;
+        if (NB == 1) {
+            o[(2 * q) * 16 + g] = acc[0];
+            o[(2 * q + 1) * 16 + g] = acc[1];
+            o[(2 * q) * 16 + g + 8] = acc[2];
+            o[(2 * q + 1) * 16 + g + 8] = acc[3];
+        } else {
+            float r0 = acc[0] + acc[1], r1 = acc[2] + acc[3];
+            if (NB >= 4) {
+                r0 += __shfl_xor_sync(0xffffffffu, r0, 1);
+                r1 += __shfl_xor_sync(0xffffffffu, r1, 1);
             }
-#pragma unroll
-            for (int j = 0; j < 4; ++j)
-                acc[n][j] = 0.f;
+            if (NB == 8) {
+                r0 += __shfl_xor_sync(0xffffffffu, r0, 2);
+                r1 += __shfl_xor_sync(0xffffffffu, r1, 2);
+            }
+            const int tok = 2 * q / NB;
+            if (2 * q % NB == 0) {  // one of the lanes that share a token
+                o[tok * 16 + g] = r0;
+                o[tok * 16 + g + 8] = r1;
+            }
         }
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            acc[j] = 0.f;
     };
     int r = P ? u0 / P : 0, p = P ? u0 % P : 0;
     for (int u = u0; u < u1; u += DEPTH) {
@@ -616,7 +591,7 @@ __global__ void __launch_bounds__(THREADS, 1) linear_kernel(const __grid_constan
         const int rt = i >> 4, rr = rt / tv;
         const int n = (rg0 + rr) * 16 + (i & 15);
         if (n < a.N) {
-            const long long at = (t0 + rt - rr * tv) * a.y_ld + n;
+            const long long at = (long long)(rt - rr * tv) * a.y_ld + n;
             if (a.y_f32) {
                 float *y = static_cast<float *>(a.y) + at;
                 *y = a.accumulate ? *y + v : v;
@@ -631,7 +606,7 @@ __global__ void __launch_bounds__(THREADS, 1) linear_kernel(const __grid_constan
         if (P) {
             const int w1 = owner_of((rr + 1) * P - 1, units, nw);
             for (int w = owner_of(rr * P, units, nw); w <= w1; ++w)
-                v += red[(size_t)((w + rr) * TT + t) * 16 + (i & 15)];
+                v += red[(size_t)((w + rr) * TB + t) * 16 + (i & 15)];
         }
         if (csize == 1)
             store(i, v);
@@ -688,7 +663,7 @@ Cut cut_of(int n16, int steps, int step_blocks, int tt, int tv, bool i4, int clu
 
 // Clusters of `size` CTAs of a kernel that the current device runs at a time (one
 // CTA per SM: the register file holds one), looked up once per device.
-template <int FMT, int TB, int NT>
+template <int FMT, int TB>
 int clusters_of(int size)
 {
     const int sms = gemm::sm_count();
@@ -709,7 +684,7 @@ int clusters_of(int size)
     at_cl.val.clusterDim.y = at_cl.val.clusterDim.z = 1;
     cfg.attrs = &at_cl;
     cfg.numAttrs = 1;
-    if (cudaOccupancyMaxActiveClusters(&n, linear_kernel<FMT, TB, NT>, &cfg) != cudaSuccess || n < 1) {
+    if (cudaOccupancyMaxActiveClusters(&n, linear_kernel<FMT, TB>, &cfg) != cudaSuccess || n < 1) {
         cudaGetLastError();
         n = sms / size > 0 ? sms / size : 1;
     }
@@ -718,41 +693,32 @@ int clusters_of(int size)
     return n;
 }
 
-template <int FMT, int TB, int NT>
+template <int FMT, int TB>
 cudaError_t launch_linear(const LinArgs &args, cudaStream_t st)
 {
-    constexpr int TT = TB * NT;
     constexpr int SC = step_chunks<FMT>;
     LinArgs a = args;
     a.steps = (a.kchunks + SC - 1) / SC;
     const int n16 = (a.N + 15) / 16;
-    const int tiles_y = (a.T + TT - 1) / TT;
-    const int tv = a.T < TT ? a.T : TT;
     // The cluster size with the least estimated time, of those whose shared memory
     // holds x: a CTA's steps (0.05 us each, more with several tokens), its items of x
     // (1/16 of a warp's 0.25 us) and the cluster's barriers.
     Cut best{};
     double least = 0.;
     for (int cl = 1; cl <= 8 && (cl == 1 || cl <= a.steps); cl *= 2) {
-        int slots = clusters_of<FMT, TB, NT>(cl) / tiles_y;
-        if (slots < 1)
-            slots = 1;
-        const Cut c = cut_of(n16, a.steps, SC * 4, TT, tv, FMT == FMT_INT4, cl, slots);
+        const int slots = clusters_of<FMT, TB>(cl);
+        const Cut c = cut_of(n16, a.steps, SC * 4, TB, a.T, FMT == FMT_INT4, cl, slots);
         if (c.rgroups < 1)
             continue;
-        const int grid = (n16 + c.rgroups - 1) / c.rgroups * tiles_y;
-        const int waves = (grid + slots * tiles_y - 1) / (slots * tiles_y);
+        const int grid = (n16 + c.rgroups - 1) / c.rgroups;
+        const int waves = (grid + slots - 1) / slots;
         const double steps = (double)((a.steps + cl - 1) / cl);
-        const double us = waves * (c.rgroups * steps * (0.05 + 0.003 * TT) + steps * SC * TT / 2 * 0.016 +
+        const double us = waves * (c.rgroups * steps * (0.05 + 0.003 * TB) + steps * SC * TB / 2 * 0.016 +
                                    (cl > 1 ? 1.0 + 0.1 * cl : 0.));
         if (best.rgroups < 1 || us < least) {
             least = us;
             best = c;
         }
-    }
-    if constexpr (NT > 1) {
-        if (best.rgroups < 1)  // the longest rows: fewer tokens at a time
-            return launch_linear<FMT, TB, 1>(args, st);
     }
     if (best.rgroups < 1)
         return cudaErrorInvalidValue;
@@ -761,13 +727,13 @@ cudaError_t launch_linear(const LinArgs &args, cudaStream_t st)
     a.sum_off = best.sum_off;
     a.red_off = best.red_off;
     a.fin_off = best.fin_off;
-    auto kern = linear_kernel<FMT, TB, NT>;
+    auto kern = linear_kernel<FMT, TB>;
     static std::atomic<int> attr_set[gemm::MAX_DEVICES];
     cudaError_t e = gemm::smem_limit_once(attr_set, (const void *)kern, SMEM_MAX);
     if (e != cudaSuccess)
         return e;
     cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3((unsigned)((n16 + best.rgroups - 1) / best.rgroups * best.cluster), (unsigned)tiles_y);
+    cfg.gridDim = dim3((unsigned)((n16 + best.rgroups - 1) / best.rgroups * best.cluster));
     cfg.blockDim = dim3(THREADS);
     cfg.dynamicSmemBytes = best.smem;
     cfg.stream = st;
@@ -785,13 +751,13 @@ cudaError_t launch_tokens(const LinArgs &a, cudaStream_t st)
 {
     if constexpr (FMT != FMT_BF16) {  // (BF16 weights have no scales to apply per block)
         if (a.T == 1)
-            return launch_linear<FMT, 1, 1>(a, st);
+            return launch_linear<FMT, 1>(a, st);
         if (a.T == 2)
-            return launch_linear<FMT, 2, 1>(a, st);
+            return launch_linear<FMT, 2>(a, st);
         if (a.T <= 4)
-            return launch_linear<FMT, 4, 1>(a, st);
+            return launch_linear<FMT, 4>(a, st);
     }
-    return a.T <= 8 ? launch_linear<FMT, 8, 1>(a, st) : launch_linear<FMT, 8, 2>(a, st);
+    return launch_linear<FMT, 8>(a, st);
 }
 
 MoeStatus bad(MoeStatus s, const char *msg) { return (MoeStatus)set_last_error(s, msg); }

@@ -7,8 +7,12 @@ namespace moe {
 
 // A call of at most this many tokens streams the FRAG store through the
 // warp-level MMAs (linear.cu); more tokens run on the tcgen05 GEMM
-// (linear_tc.cu).
-constexpr int LINEAR_STREAM_MAX_T = 16;
+// (linear_tc.cu).  Eight tokens fill the columns of a warp-level MMA.  Measured
+// (device time in us, this kernel and the GEMM): MXFP4 7168 x 7168 12.4 and 16.0
+// for 8 tokens, 17.7 (two MMAs per weight fragment) and 16.3 for 16; group-32 INT4
+// 7168 x 18432 33 and 46 for 8, 52 and 46 for 16; BF16 2048 x 7168 10.0 and 9.3 for
+// 8, 12.1 and 9.5 for 16.
+constexpr int LINEAR_STREAM_MAX_T = 8;
 
 // Operands of the tcgen05 GEMM: FP16 (MXFP4 whose exponents span at most
 // TILE_F16_MAX_SPREAD in every row), BF16 (BF16 weights, other MXFP4), FP16 hi +

@@ -44,6 +44,9 @@ class QuantLinear:
             self._dense("zeros", zeros, torch.uint8, (self.N, self.K // 32))
         self.device = codes.device
         self.handle = B.moe_linear_load(self.N, self.K, FORMATS[fmt], codes, scales, zeros, stream)
+        self._no_ws = 0  # the largest T that needs no workspace
+        while B.moe_linear_workspace_bytes(self.handle, self._no_ws + 1) == 0 and self._no_ws < 64:
+            self._no_ws += 1
 
     @staticmethod
     def _dense(name, t, dtype, shape):
@@ -66,9 +69,9 @@ class QuantLinear:
             out = torch.empty((T, self.N), dtype=torch.float32, device=self.device)
         elif tuple(out.shape) != (T, self.N):
             raise B.MoeError(B.MOE_EINVAL, f"out: shape {tuple(out.shape)} where ({T}, {self.N}) is needed")
-        n = B.moe_linear_workspace_bytes(self.handle, T) if T > 16 else 0
-        ws = None
-        if n:
+        n, ws = 0, None
+        if T > self._no_ws:
+            n = B.moe_linear_workspace_bytes(self.handle, T)
             # from torch's allocator on each call: it keeps calls on several streams and captured calls apart
             ws = torch.empty(n, dtype=torch.uint8, device=self.device)
             if stream is not None:
