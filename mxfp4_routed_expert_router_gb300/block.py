@@ -1,0 +1,70 @@
+"""A decoder layer's work around attention, with the operators of the library.
+
+``MoeBlock`` holds the pieces that a decoder layer runs beside attention itself:
+the norm and the 4-bit projection in front of attention, and behind it the output
+projection, the norm, the router, group-limited routing and the experts.  The
+residual stream is a float32 [T, H] tensor that is updated in place.  torch
+supplies memory and streams only; everything runs on its current stream.
+"""
+from __future__ import annotations
+
+import dataclasses
+from typing import Optional
+
+import torch
+
+from . import binding as B
+from .layer import MoeLayer
+from .linear import QuantLinear
+
+
+@dataclasses.dataclass(frozen=True)
+class Routing:
+    """How the router's logits choose experts (``moe_route_grouped``)."""
+
+    k: int
+    n_groups: int = 1
+    k_groups: int = 1
+    score: int = B.MOE_SCORE_SIGMOID
+    group_score: int = B.MOE_GROUP_TOP2
+    renormalize: bool = True
+    scale: float = 1.0
+
+
+class MoeBlock:
+    """* in_gain [H], in_proj: the norm and the projection in front of attention (``project_in``)
+    * out_proj: attention's output projection (rows of H values), or None when attention's output is added as it is
+    * gain [H], router (a [E, H] weight), bias [E] or None, routing, layer: the experts' side (``forward``)
+    """
+
+    def __init__(self, layer: MoeLayer, router: QuantLinear, routing: Routing, gain: Optional[torch.Tensor] = None,
+                 bias: Optional[torch.Tensor] = None, out_proj: Optional[QuantLinear] = None,
+                 in_proj: Optional[QuantLinear] = None, in_gain: Optional[torch.Tensor] = None, eps: float = 1e-6):
+        self.layer, self.router, self.routing = layer, router, routing
+        self.gain, self.bias, self.out_proj, self.in_proj, self.in_gain = gain, bias, out_proj, in_proj, in_gain
+        self.eps = eps
+
+    def project_in(self, residual: torch.Tensor) -> torch.Tensor:
+        """in_proj of the norm of the residual stream, as bfloat16 rows; the norm's rows are MXFP8 in between."""
+        T, H = residual.shape
+        q = torch.empty((T, H), dtype=torch.float8_e4m3fn, device=residual.device)
+        scales = torch.empty((T, H // 32), dtype=torch.uint8, device=residual.device)
+        out = torch.empty((T, self.in_proj.N), dtype=torch.bfloat16, device=residual.device)
+        B.moe_add_rmsnorm(residual, None, self.in_gain, self.eps, None, None, q, scales)
+        return self.in_proj.forward(q, scales, out=out)
+
+    def forward(self, attn: torch.Tensor, residual: torch.Tensor) -> torch.Tensor:
+        """Adds attention's output (bfloat16 rows; out_proj is applied to them) and then the experts' output for
+        the norm of the sum to the residual stream, in place."""
+        T, H = residual.shape
+        dev, r = residual.device, self.routing
+        E = self.router.N
+        delta = attn if self.out_proj is None else self.out_proj.forward(attn)
+        x = torch.empty((T, H), dtype=torch.bfloat16, device=dev)
+        B.moe_add_rmsnorm(residual, delta, self.gain, self.eps, residual, x)
+        logits = self.router.forward(x)
+        ids = torch.empty((T, r.k), dtype=torch.int32, device=dev)
+        w = torch.empty((T, r.k), dtype=torch.float32, device=dev)
+        B.moe_route_grouped(logits, self.bias, T, E, r.k, r.n_groups, r.k_groups, r.score, r.group_score,
+                            r.renormalize, r.scale, ids, w)
+        return self.layer.forward_routed(x, ids, w, out=residual, accumulate=True)

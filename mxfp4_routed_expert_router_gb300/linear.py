@@ -63,7 +63,8 @@ class QuantLinear:
         T = x.shape[0]
         if x_scales is not None and (tuple(x_scales.shape) != (T, self.K // 32) or not x_scales.is_contiguous()):
             raise B.MoeError(B.MOE_EINVAL, f"x_scales: a dense [{T}, {self.K // 32}] tensor is needed")
-        if out is None:
+        made = out is None
+        if made:
             if accumulate:
                 raise B.MoeError(B.MOE_EINVAL, "accumulate needs an out to add to")
             out = torch.empty((T, self.N), dtype=torch.float32, device=self.device)
@@ -74,8 +75,11 @@ class QuantLinear:
             n = B.moe_linear_workspace_bytes(self.handle, T)
             # from torch's allocator on each call: it keeps calls on several streams and captured calls apart
             ws = torch.empty(n, dtype=torch.uint8, device=self.device)
-            if stream is not None:
-                ws.record_stream(torch.cuda.ExternalStream(stream) if isinstance(stream, int) else stream)
+        if stream is not None and (made or n):
+            on = torch.cuda.ExternalStream(stream) if isinstance(stream, int) else stream
+            for t in (out if made else None, ws):
+                if t is not None:
+                    t.record_stream(on)
         B.moe_linear_forward(self.handle, x, x_scales, out, accumulate, ws, n, stream)
         return out
 
