@@ -15,7 +15,10 @@
 // more than 2 e apart is the FP64 order.  So route_fast selects on FP32 keys and
 // measures the gaps that its result rests on (after the last group that stays;
 // after each kept key); a row with a gap too small, equal keys or a value that is
-// not finite is done again on FP64 keys (route_exact).  The errors, with u = 2^-24:
+// not finite is done again on FP64 keys (route_exact).  Where only the order of
+// the kept keys is in doubt, FP64 keys of the experts that can be among them, one a
+// lane, decide it: a row in route_exact takes several us, which a call of thousands
+// of rows would wait for at its end.  The errors, with u = 2^-24:
 //   sigmoid: exp 2 ulp (4 u), addition and division (2 u): below 8 u of the score
 //   softmax: exp 4 u; its argument l - max rounded, |l - max| u (below 76 u for the
 //     scores above 1e-30 taken here; times exp(l - max), below 0.37 u of the
@@ -25,8 +28,10 @@
 //   key with a bias: the score's, and u |key| for the addition
 // Without a bias the error is relative to the key (REL), with one it is taken
 // from the row's largest score (ABS) and key.
-// Issue and latency bound (a row is 4 E bytes): FP64 for every row took 147 us
-// for 8192 rows of 256 experts in 8 groups, 4 kept, k = 8, and 15 us for one row.
+// Issue and latency bound (a row is 4 E bytes).  8192 rows of 256 experts in 8
+// groups, 4 kept, sigmoid scores with a bias, k = 8: 17 us (1.3 us of HBM time;
+// FP64 keys for every row took 147 us, for the whole of each unsure row 25 us); one
+// row 5.6 us (FP64: 15 us).
 #include <math.h>
 #include <stdio.h>
 
@@ -197,10 +202,10 @@ __device__ __forceinline__ float key_value32(uint32_t k)
     return k ? __uint_as_float((k >> 31) ? (k & 0x7FFFFFFFu) : ~k) : -INFINITY;
 }
 
-// One row on FP32 keys (a whole warp): writes the row and returns true when the
-// order is certain.
+// One row on FP32 keys (a whole warp; cand: 32 ints of its own in shared memory):
+// writes the row and returns true when the selection is certain.
 template <int SCORE, int NV>
-__device__ __forceinline__ bool route_fast(const RouteArgs &a, long long t)
+__device__ __forceinline__ bool route_fast(const RouteArgs &a, long long t, int *cand)
 {
     constexpr float U = 5.9604645e-8f;  // 2^-24
     constexpr float REL = (SCORE == MOE_SCORE_SOFTMAX ? 256.f : 8.f) * U;
@@ -302,7 +307,9 @@ __device__ __forceinline__ bool route_fast(const RouteArgs &a, long long t)
                 key[i] = 0u;
     }
 
-    int my_e = -1;
+    if (!sure)
+        return false;
+    int my_e = -1, taken = 0;
     uint32_t prev = 0u;
     for (int j = 0; j <= a.k; ++j) {
         uint32_t best = key[0];
@@ -332,9 +339,58 @@ __device__ __forceinline__ bool route_fast(const RouteArgs &a, long long t)
         e = __shfl_sync(0xffffffffu, grp * a.gs + sub + a.lg * e, src);
         if (lane == j)
             my_e = e;
+        taken = j + 1;
     }
-    if (!sure)
-        return false;
+    if (!sure) {
+        // Candidates: the experts taken, and the others whose key can reach the last
+        // taken one's (within twice the error).
+        const float last = key_value32(prev);
+        const uint32_t floor_key = order_key32(last - err_of(last));
+        if (lane < taken)
+            cand[lane] = my_e;
+        int n = taken;
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            const bool c = key[i] != 0u && key[i] >= floor_key;
+            const unsigned mask = __ballot_sync(0xffffffffu, c);
+            const int at = n + __popc(mask & ((1u << lane) - 1u));
+            if (c && at < 32)
+                cand[at] = grp * a.gs + sub + a.lg * i;
+            n += __popc(mask);
+        }
+        if (n > 32)
+            return false;
+        __syncwarp();
+        const int e = lane < n ? cand[lane] : 0;
+        double sum64 = 0.0;
+        if (SCORE == MOE_SCORE_SOFTMAX) {
+#pragma unroll 1
+            for (int i = 0; i < NV; ++i)
+                if (has_grp && sub + a.lg * i < a.gs && mine[a.lg * i] != -INFINITY)
+                    sum64 += exp((double)mine[a.lg * i] - (double)mx);
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1)
+                sum64 += __shfl_xor_sync(0xffffffffu, sum64, o);
+        }
+        u64 k64 = 0ull;
+        if (lane < n) {
+            const double l64 = (double)row[e];
+            const double s64 =
+                SCORE == MOE_SCORE_SOFTMAX ? exp(l64 - (double)mx) / sum64 : 1.0 / (1.0 + exp(-l64));
+            k64 = order_key(s64 + (a.bias ? (double)a.bias[e] : 0.0));
+        }
+        int rank = 0;
+        for (int j = 0; j < n; ++j) {
+            const u64 kj = __shfl_sync(0xffffffffu, k64, j);
+            const int ej = __shfl_sync(0xffffffffu, e, j);
+            rank += kj > k64 || (kj == k64 && ej < e);
+        }
+        __syncwarp();
+        if (lane < n && rank < taken)
+            cand[rank] = e;
+        __syncwarp();
+        my_e = lane < taken ? cand[lane] : -1;
+    }
     float s = 0.f;
     if (my_e >= 0)
         s = SCORE == MOE_SCORE_SOFTMAX ? expf(row[my_e] - mx) / inv : 1.f / (1.f + expf(-row[my_e]));
@@ -355,8 +411,9 @@ __device__ __forceinline__ bool route_fast(const RouteArgs &a, long long t)
 template <int SCORE, int NV>
 __global__ void __launch_bounds__(256) route_grouped_kernel(const __grid_constant__ RouteArgs a)
 {
+    __shared__ int cand[8][32];
     const long long t = ((long long)blockIdx.x * blockDim.x + threadIdx.x) >> 5;
-    if (t < a.T && !route_fast<SCORE, NV>(a, t))
+    if (t < a.T && !route_fast<SCORE, NV>(a, t, cand[threadIdx.x >> 5]))
         route_exact<SCORE, NV>(a, t);
 }
 

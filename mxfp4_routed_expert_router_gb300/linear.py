@@ -63,25 +63,29 @@ class QuantLinear:
         T = x.shape[0]
         if x_scales is not None and (tuple(x_scales.shape) != (T, self.K // 32) or not x_scales.is_contiguous()):
             raise B.MoeError(B.MOE_EINVAL, f"x_scales: a dense [{T}, {self.K // 32}] tensor is needed")
-        made = out is None
-        if made:
+        if out is None:
             if accumulate:
                 raise B.MoeError(B.MOE_EINVAL, "accumulate needs an out to add to")
-            out = torch.empty((T, self.N), dtype=torch.float32, device=self.device)
         elif tuple(out.shape) != (T, self.N):
             raise B.MoeError(B.MOE_EINVAL, f"out: shape {tuple(out.shape)} where ({T}, {self.N}) is needed")
-        n, ws = 0, None
-        if T > self._no_ws:
-            n = B.moe_linear_workspace_bytes(self.handle, T)
-            # from torch's allocator on each call: it keeps calls on several streams and captured calls apart
-            ws = torch.empty(n, dtype=torch.uint8, device=self.device)
-        if stream is not None and (made or n):
-            on = torch.cuda.ExternalStream(stream) if isinstance(stream, int) else stream
-            for t in (out if made else None, ws):
-                if t is not None:
-                    t.record_stream(on)
+        n = B.moe_linear_workspace_bytes(self.handle, T) if T > self._no_ws else 0
+        ws = None
+        if n or out is None:
+            # Allocated on each call, on the call's own stream: torch's allocator then keeps calls on several
+            # streams, and captured calls, apart.
+            if stream is None:
+                out, ws = self._allocate(T, n, out)
+            else:
+                on = torch.cuda.ExternalStream(stream) if isinstance(stream, int) else stream
+                with torch.cuda.stream(on):
+                    out, ws = self._allocate(T, n, out)
         B.moe_linear_forward(self.handle, x, x_scales, out, accumulate, ws, n, stream)
         return out
+
+    def _allocate(self, T: int, n: int, out):
+        if out is None:
+            out = torch.empty((T, self.N), dtype=torch.float32, device=self.device)
+        return out, torch.empty(n, dtype=torch.uint8, device=self.device) if n else None
 
     def sync(self, stream=None):
         B.moe_linear_sync_status(self.handle, stream)
