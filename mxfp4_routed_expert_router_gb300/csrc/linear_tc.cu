@@ -8,8 +8,8 @@
 // largest exponent, or to BF16 where a row's exponents span too widely; group-32
 // INT4 to an exact FP16 pair hi + lo.  BF16 weights come by TMA into shared
 // memory.  B: token rows by TMA, 128-byte-swizzled K-major tiles: the caller's
-// BF16 rows with BF16 operands, else FP16 rows x * 2^-e (a power of two per
-// token) that a first kernel writes.
+// BF16 rows with BF16 weights, else rows that a first kernel writes, with 4-bit
+// weights in FP16 times a power of two per token.
 //
 // A CTA computes one tile (128 rows x up to 128 tokens x its K range) and two CTAs
 // share an SM (half of its tensor memory each), so that the hand-offs, the first
@@ -48,8 +48,8 @@ constexpr int A_SLOT_COLS = 64;       // 128 16-bit values per lane
 constexpr int TMEM_COLS = 256;        // half of the SM's: accumulator and A ring
 static_assert(NMAX + 2 * A_SLOT_COLS <= TMEM_COLS && NHALF + A_MAX * A_SLOT_COLS <= TMEM_COLS, "tensor memory");
 constexpr int A_TILE_BYTES = TILE_ROWS * HALF_K * 2;     // BF16 weights: 16 KB
-// Shared memory: the token ring (slots of 64 values of K: a swizzled tile of
-// tile_tokens x 128 bytes, with BF16 weights the A tile after it), then the ring
+// Shared memory: the token ring (a slot holds a stage's one or two swizzled tiles
+// of tile_tokens x 128 bytes, with BF16 weights the A tile after it), then the ring
 // of weight chunks.
 constexpr int RING_BYTES = 108 * 1024;
 constexpr int B_MAX = 12, W_MAX = 8;  // slots
@@ -222,8 +222,9 @@ __global__ void __launch_bounds__(THREADS, 2)
     const int tok0 = tt * a.tile_tokens, nvalid = min(a.tile_tokens, a.T - tok0);
     const int n_mma = (nvalid + 15) & ~15;
     const int c0 = (int)((long long)a.kchunks * crank / csize), c1 = (int)((long long)a.kchunks * (crank + 1) / csize);
-    const int nst = (c1 - c0) * (CHUNK_K / KST), nsl = nst * NSL;  // A stages, token slots
-    const uint32_t slice_bytes = (uint32_t)a.tile_tokens * HALF_K * 2, slot_bytes = slice_bytes + (AS ? A_TILE_BYTES : 0);
+    const int nst = (c1 - c0) * (CHUNK_K / KST);  // stages
+    const uint32_t slice_bytes = (uint32_t)a.tile_tokens * HALF_K * 2;
+    const uint32_t slot_bytes = NSL * slice_bytes + (AS ? A_TILE_BYTES : 0);
 
     if (tid == 0) {
         for (int i = 0; i < a.b_slots; ++i)
@@ -253,13 +254,11 @@ __global__ void __launch_bounds__(THREADS, 2)
     // The MMAs of a stage are committed once, to the barrier of the stage: it frees
     // the stage's A slot and its token slots.  Nobody waits for a stage whose barrier could have
     // come round again, which takes the end of stage + DONE: the decoders' wait comes
-    // before they decode for stage + a_slots, and the loader's before it loads token
-    // slot NSL * stage + b_slots, the first of stage + DONE or an earlier one.  Nor
+    // before they decode for stage + a_slots, and the loader's before it loads for
+    // stage + b_slots, which is stage + DONE or an earlier one.  Nor
     // does anybody skip a phase of a barrier that it waits for (it could take the
     // older one for it): decoder groups take every other chunk, and the ring of chunks
     // has an even number of slots.
-    auto done_bar = [&](int st) { return &done[st % DONE]; };
-    auto done_par = [&](int st) { return (uint32_t)(st / DONE) & 1u; };
     const uint32_t tmem = *tmem_slot;
     const int a_slots = a.tile_tokens <= NHALF ? A_MAX : 2;
     const uint32_t tmem_a = tmem + (a.tile_tokens <= NHALF ? NHALF : NMAX);
@@ -267,17 +266,26 @@ __global__ void __launch_bounds__(THREADS, 2)
     if (warp == WARP_LOAD) {
         // ---------------------------------------------------------- token tiles -> ring
         asm volatile("griddepcontrol.wait;" ::: "memory");  // the token rows are written
-        int s = 0, slot = 0;
-        for (; s < nsl; ++s) {
-            const int used = (s - a.b_slots) / NSL;  // the stage that the slot held before
-            if (s >= a.b_slots && !mbar_wait_sleep_warp(done_bar(used), done_par(used), abort_flag, a.err, lane))
-                break;
+        int st = 0, slot = 0, ds = 0;
+        uint32_t dph = 0;
+        for (; st < nst; ++st) {
+            if (st >= a.b_slots) {  // the stage that the slot held before
+                if (!mbar_wait_sleep_warp(&done[ds], dph, abort_flag, a.err, lane))
+                    break;
+                if (++ds == DONE) {
+                    ds = 0;
+                    dph ^= 1;
+                }
+            }
             if (lane == 0) {
                 uint8_t *dst = smem + slot * slot_bytes;
                 mbar_arrive_expect_tx(&b_full[slot], slot_bytes);
-                tma_2d(dst, &map_b, c0 * CHUNK_K + s * HALF_K, tok0, &b_full[slot]);
-                if (AS)  // the store seen as [row tiles * chunks * 2 halves * 128][64]
-                    tma_2d(dst + slice_bytes, &map_a, 0, ((rt * a.kchunks + c0) * 2 + s) * TILE_ROWS, &b_full[slot]);
+                if (AS) {  // the store seen as [row tiles * chunks * 2 halves * 128][64]
+                    tma_2d(dst, &map_b, c0 * CHUNK_K + st * HALF_K, tok0, &b_full[slot]);
+                    tma_2d(dst + slice_bytes, &map_a, 0, ((rt * a.kchunks + c0) * 2 + st) * TILE_ROWS, &b_full[slot]);
+                } else {   // the rows seen as 64-value slices
+                    tma_3d(dst, &map_b, 0, tok0, c0 * 2 + st * NSL, &b_full[slot]);
+                }
             }
             if (++slot == a.b_slots)
                 slot = 0;
@@ -285,7 +293,7 @@ __global__ void __launch_bounds__(THREADS, 2)
         // every copy of an armed slot has landed before the CTA goes on (at once on
         // the normal path; bounded after an abort)
         if (lane == 0)
-            for (int i = s > a.b_slots ? s - a.b_slots : 0; i < s; ++i)
+            for (int i = st > a.b_slots ? st - a.b_slots : 0; i < st; ++i)
                 mbar_drain(&b_full[i % a.b_slots], (i / a.b_slots) & 1);
         __syncwarp();
     } else if (warp == WARP_WEIGHTS) {
@@ -321,42 +329,38 @@ __global__ void __launch_bounds__(THREADS, 2)
         auto wait = [&](uint64_t *bar, uint32_t par) {
             return __all_sync(0xffffffffu, mbar_wait(bar, par, abort_flag, a.err)) != 0;
         };
-        const uint64_t desc0 = sw128(smem_addr(smem)), bstep = (uint64_t)(slot_bytes >> 4);
+        const uint64_t desc0 = sw128(smem_addr(smem)), slice = (uint64_t)(slice_bytes >> 4);
         const uint32_t idesc = instr_desc(OP == LIN_BF16, n_mma);
         uint64_t bd = desc0;
         uint32_t at = tmem_a, aph = 0, bph = 0;
         int as = 0, ds = 0, slot = 0;
-        bool ok = true;
-        for (int st = 0; st < nst && ok; ++st) {
-            if (!AS && !(ok = wait(&a_full[as], aph)))
+        for (int st = 0; st < nst; ++st) {
+            if (!AS && !wait(&a_full[as], aph))
                 break;
-#pragma unroll
-            for (int sl = 0; sl < NSL; ++sl) {
-                if (!(ok = wait(&b_full[slot], bph)))
-                    break;
-                fence_after();
-                if (elected) {
-                    if (AS) {
-                        mma64<true>(tmem, 0, bd + (uint64_t)(slice_bytes >> 4), bd, idesc, st);
-                    } else if (OP == LIN_I4) {
-                        mma64<false>(tmem, at, 0, bd, idesc, st);
-                        mma64<false>(tmem, at + 32, 0, bd, idesc, 1u);
-                    } else {
-                        mma64<false>(tmem, at + 32 * sl, 0, bd, idesc, st > 0 || sl > 0);
-                    }
-                    if (sl == NSL - 1)
-                        commit(&done[ds]);
+            if (!wait(&b_full[slot], bph))
+                break;
+            fence_after();
+            if (elected) {
+                if (AS) {
+                    mma64<true>(tmem, 0, bd + slice, bd, idesc, st);
+                } else if (OP == LIN_I4) {
+                    mma64<false>(tmem, at, 0, bd, idesc, st);
+                    mma64<false>(tmem, at + 32, 0, bd, idesc, 1u);
+                } else {
+                    mma64<false>(tmem, at, 0, bd, idesc, st);
+                    mma64<false>(tmem, at + 32, 0, bd + slice, idesc, 1u);
                 }
-                __syncwarp();
-                bd += bstep;
-                if (++slot == a.b_slots) {
-                    slot = 0;
-                    bph ^= 1;
-                    bd = desc0;
-                }
+                commit(&done[ds]);
             }
+            __syncwarp();
             if (++ds == DONE)
                 ds = 0;
+            bd += (uint64_t)(slot_bytes >> 4);
+            if (++slot == a.b_slots) {
+                slot = 0;
+                bph ^= 1;
+                bd = desc0;
+            }
             at += A_SLOT_COLS;
             if (++as == a_slots) {
                 as = 0;
@@ -383,6 +387,8 @@ __global__ void __launch_bounds__(THREADS, 2)
             uint32_t ph = 0;
             const bool second = KST < CHUNK_K && grp == 1;         // this group decodes the chunks' second halves
             int as = grp;                                          // the stage's A slot
+            int ds = (grp + a_slots) & 1;                          // barrier of the stage that the slot held before
+            uint32_t dph = 0;
             for (int st = grp; st < nst; st += DEC_GROUPS) {
                 if (!(ok = mbar_wait_warp(&w_full[slot], ph, abort_flag, a.err, lane)))
                     break;
@@ -413,9 +419,14 @@ __global__ void __launch_bounds__(THREADS, 2)
                     slot -= a.w_slots;
                     ph ^= 1;
                 }
-                const int prev = st - a_slots;  // the stage that the A slot held before
-                if (prev >= 0 && !(ok = mbar_wait_warp(done_bar(prev), done_par(prev), abort_flag, a.err, lane)))
-                    break;
+                if (st >= a_slots) {
+                    if (!(ok = mbar_wait_warp(&done[ds], dph, abort_flag, a.err, lane)))
+                        break;
+                    if ((ds += DEC_GROUPS) >= DONE) {
+                        ds -= DONE;
+                        dph ^= 1;
+                    }
+                }
                 fence_after();
                 const uint32_t dst = tmem_a + tlane + as * A_SLOT_COLS;
 #pragma unroll
@@ -554,7 +565,8 @@ __global__ void __launch_bounds__(THREADS, 2)
 // token: the largest |x| lands in [2^14, 2^15); exact within 2^-29 of it) with
 // scale[t] = 2^e, or BF16 (of MXFP8 rows).
 __global__ void __launch_bounds__(1024) linear_rows_kernel(const void *x, const uint8_t *xscales, long long x_ld,
-                                                          int x_mx, int K, int bf16, uint16_t *out, float *scale)
+                                                          int x_mx, int K, int kpad, int bf16, uint16_t *out,
+                                                          float *scale)
 {
     __shared__ uint32_t red[32];
     const long long t = blockIdx.x;
@@ -608,10 +620,11 @@ __global__ void __launch_bounds__(1024) linear_rows_kernel(const void *x, const 
         if (threadIdx.x == 0)
             scale[t] = __int_as_float((127 + e) << 23);
     }
-    for (int v = threadIdx.x; v < nv; v += nt) {
-        float f[8];
+    for (int v = threadIdx.x; v < kpad / 8; v += nt) {
+        float f[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};  // (zeros up to a whole chunk)
         uint32_t o[4];
-        load(v, f);
+        if (v < nv)
+            load(v, f);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             if (bf16) {
@@ -622,7 +635,7 @@ __global__ void __launch_bounds__(1024) linear_rows_kernel(const void *x, const 
                 o[i] = *reinterpret_cast<const uint32_t *>(&p);
             }
         }
-        reinterpret_cast<uint4 *>(out + t * (long long)K)[v] = make_uint4(o[0], o[1], o[2], o[3]);
+        reinterpret_cast<uint4 *>(out + t * (long long)kpad)[v] = make_uint4(o[0], o[1], o[2], o[3]);
     }
 }
 
@@ -678,7 +691,11 @@ size_t align256(size_t n) { return (n + 255) & ~(size_t)255; }
 
 }  // namespace
 
-size_t linear_gemm_workspace(int K, int T) { return align256((size_t)T * K * 2) + align256((size_t)T * 4); }
+size_t linear_gemm_workspace(int K, int T)
+{
+    const size_t kpad = (size_t)((K + CHUNK_K - 1) & ~(CHUNK_K - 1));
+    return align256((size_t)T * kpad * 2) + align256((size_t)T * 4);
+}
 
 cudaError_t launch_linear_gemm(const LinearGemm &g, cudaStream_t st)
 {
@@ -698,12 +715,13 @@ cudaError_t launch_linear_gemm(const LinearGemm &g, cudaStream_t st)
     a.err = g.err;
     const bool bf16 = g.op == LIN_BF16;
     // the rings: enough token slots to cover their loads, the rest for weight chunks
-    const int slot_bytes = a.tile_tokens * HALF_K * 2 + (g.fmt == FMT_BF16 ? A_TILE_BYTES : 0);
+    const int nsl = g.fmt == FMT_BF16 || g.op == LIN_I4 ? 1 : 2;
+    const int slot_bytes = nsl * a.tile_tokens * HALF_K * 2 + (g.fmt == FMT_BF16 ? A_TILE_BYTES : 0);
     if (g.fmt == FMT_BF16) {
         a.b_slots = RING_BYTES / slot_bytes < B_MAX ? RING_BYTES / slot_bytes : B_MAX;
         a.w_slots = 0;
     } else {
-        a.b_slots = a.tile_tokens <= 32 ? B_MAX : a.tile_tokens <= 64 ? 8 : a.tile_tokens <= 96 ? 6 : 4;
+        a.b_slots = (a.tile_tokens <= 32 ? B_MAX : a.tile_tokens <= 64 ? 8 : a.tile_tokens <= 96 ? 6 : 4) / nsl;
         a.w_off = a.b_slots * slot_bytes;
         a.w_slots = (RING_BYTES - a.w_off) / g.w->chunk_bytes;
         if (a.w_slots > W_MAX)
@@ -713,17 +731,20 @@ cudaError_t launch_linear_gemm(const LinearGemm &g, cudaStream_t st)
     }
     CUtensorMap mb, ma;
     cudaError_t e;
-    const bool rows_written = !bf16 || g.x_mx;
+    const bool rows_written = g.fmt != FMT_BF16 || g.x_mx;
+    const int kpad = (g.K + CHUNK_K - 1) & ~(CHUNK_K - 1);
     if (!rows_written) {
         e = rows_map(&mb, g.x, g.T, g.K, g.x_ld * 2, a.tile_tokens);
     } else {
         uint16_t *rows = reinterpret_cast<uint16_t *>(g.workspace);
-        float *scale = reinterpret_cast<float *>(g.workspace + align256((size_t)g.T * g.K * 2));
-        linear_rows_kernel<<<g.T, g.T <= 2 * sm_count() ? 1024 : 256, 0, st>>>(g.x, g.xscales, g.x_ld, g.x_mx, g.K, bf16, rows, scale);
+        float *scale = reinterpret_cast<float *>(g.workspace + align256((size_t)g.T * kpad * 2));
+        linear_rows_kernel<<<g.T, g.T <= 2 * sm_count() ? 1024 : 256, 0, st>>>(g.x, g.xscales, g.x_ld, g.x_mx, g.K, kpad,
+                                                                            bf16, rows, scale);
         if ((e = cudaGetLastError()) != cudaSuccess)
             return e;
         a.xscale = scale;
-        e = rows_map(&mb, rows, g.T, g.K, (long long)g.K * 2, a.tile_tokens);
+        e = g.fmt == FMT_BF16 ? rows_map(&mb, rows, g.T, kpad, (long long)kpad * 2, a.tile_tokens)
+                              : make_map_3d(&mb, rows, g.T, kpad, a.tile_tokens, nsl);
     }
     if (e != cudaSuccess)
         return e;
