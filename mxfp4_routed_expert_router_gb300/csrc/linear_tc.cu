@@ -54,7 +54,7 @@ constexpr int A_TILE_BYTES = TILE_ROWS * HALF_K * 2;     // BF16 weights: 16 KB
 constexpr int RING_BYTES = 108 * 1024;
 constexpr int B_MAX = 12, W_MAX = 8;  // slots
 constexpr int DONE = 12;              // barriers of finished stages
-static_assert(DONE >= B_MAX, "see linear_tc_kernel");
+static_assert(DONE >= B_MAX, "see linear_tc_kernel");  // (B_MAX slots of one slice, half as many of two)
 constexpr int BAR_OFF = RING_BYTES;
 constexpr int N_BARS = B_MAX + 2 * W_MAX + A_MAX + DONE + 1;
 constexpr int MISC_OFF = BAR_OFF + N_BARS * 8;
@@ -203,7 +203,8 @@ __global__ void __launch_bounds__(THREADS, 2)
 {
     constexpr bool AS = WFMT == FMT_BF16;                            // A by TMA into shared memory
     constexpr int KST = (AS || OP == LIN_I4) ? HALF_K : CHUNK_K;     // K values per A stage
-    constexpr int NSL = KST / HALF_K;                                // token ring slots per A stage
+    constexpr int NSL = AS ? 1 : 2;                                  // 64-value token slices per slot of the token ring
+    constexpr int BST = NSL * HALF_K / KST;                          // stages per slot (INT4: two)
     constexpr int NBLK = KST / 32;
     constexpr int CB = WFMT == FMT_INT4 ? CHUNK_I4_BYTES : CHUNK_MX_BYTES;
     extern __shared__ uint8_t smem_dyn[];
@@ -252,13 +253,13 @@ __global__ void __launch_bounds__(THREADS, 2)
     __syncthreads();
     fence_after();
     // The MMAs of a stage are committed once, to the barrier of the stage: it frees
-    // the stage's A slot and its token slots.  Nobody waits for a stage whose barrier could have
-    // come round again, which takes the end of stage + DONE: the decoders' wait comes
-    // before they decode for stage + a_slots, and the loader's before it loads for
-    // stage + b_slots, which is stage + DONE or an earlier one.  Nor
-    // does anybody skip a phase of a barrier that it waits for (it could take the
-    // older one for it): decoder groups take every other chunk, and the ring of chunks
-    // has an even number of slots.
+    // the stage's A slot and its part of the token slot.  Nobody waits for a stage
+    // whose barrier could have come round again, which takes the end of stage + DONE:
+    // the decoders' wait comes before they decode for stage + a_slots, and the
+    // loader's before it loads for stage + BST * b_slots, which is stage + DONE or an
+    // earlier one.  Nor does anybody skip a phase of a barrier that it waits for (it
+    // could take the older one for it): decoder groups take every other chunk, and the
+    // ring of chunks has an even number of slots.
     const uint32_t tmem = *tmem_slot;
     const int a_slots = a.tile_tokens <= NHALF ? A_MAX : 2;
     const uint32_t tmem_a = tmem + (a.tile_tokens <= NHALF ? NHALF : NMAX);
@@ -266,14 +267,14 @@ __global__ void __launch_bounds__(THREADS, 2)
     if (warp == WARP_LOAD) {
         // ---------------------------------------------------------- token tiles -> ring
         asm volatile("griddepcontrol.wait;" ::: "memory");  // the token rows are written
-        int st = 0, slot = 0, ds = 0;
+        int it = 0, slot = 0, ds = BST - 1;
         uint32_t dph = 0;
-        for (; st < nst; ++st) {
-            if (st >= a.b_slots) {  // the stage that the slot held before
+        for (; it < nst / BST; ++it) {
+            if (it >= a.b_slots) {  // the last stage that the slot held before
                 if (!mbar_wait_sleep_warp(&done[ds], dph, abort_flag, a.err, lane))
                     break;
-                if (++ds == DONE) {
-                    ds = 0;
+                if ((ds += BST) >= DONE) {
+                    ds -= DONE;
                     dph ^= 1;
                 }
             }
@@ -281,10 +282,10 @@ __global__ void __launch_bounds__(THREADS, 2)
                 uint8_t *dst = smem + slot * slot_bytes;
                 mbar_arrive_expect_tx(&b_full[slot], slot_bytes);
                 if (AS) {  // the store seen as [row tiles * chunks * 2 halves * 128][64]
-                    tma_2d(dst, &map_b, c0 * CHUNK_K + st * HALF_K, tok0, &b_full[slot]);
-                    tma_2d(dst + slice_bytes, &map_a, 0, ((rt * a.kchunks + c0) * 2 + st) * TILE_ROWS, &b_full[slot]);
+                    tma_2d(dst, &map_b, c0 * CHUNK_K + it * HALF_K, tok0, &b_full[slot]);
+                    tma_2d(dst + slice_bytes, &map_a, 0, ((rt * a.kchunks + c0) * 2 + it) * TILE_ROWS, &b_full[slot]);
                 } else {   // the rows seen as 64-value slices
-                    tma_3d(dst, &map_b, 0, tok0, c0 * 2 + st * NSL, &b_full[slot]);
+                    tma_3d(dst, &map_b, 0, tok0, (c0 + it) * 2, &b_full[slot]);
                 }
             }
             if (++slot == a.b_slots)
@@ -293,7 +294,7 @@ __global__ void __launch_bounds__(THREADS, 2)
         // every copy of an armed slot has landed before the CTA goes on (at once on
         // the normal path; bounded after an abort)
         if (lane == 0)
-            for (int i = st > a.b_slots ? st - a.b_slots : 0; i < st; ++i)
+            for (int i = it > a.b_slots ? it - a.b_slots : 0; i < it; ++i)
                 mbar_drain(&b_full[i % a.b_slots], (i / a.b_slots) & 1);
         __syncwarp();
     } else if (warp == WARP_WEIGHTS) {
@@ -337,15 +338,16 @@ __global__ void __launch_bounds__(THREADS, 2)
         for (int st = 0; st < nst; ++st) {
             if (!AS && !wait(&a_full[as], aph))
                 break;
-            if (!wait(&b_full[slot], bph))
+            const int half = BST == 2 ? st & 1 : 0;
+            if (half == 0 && !wait(&b_full[slot], bph))
                 break;
             fence_after();
             if (elected) {
                 if (AS) {
                     mma64<true>(tmem, 0, bd + slice, bd, idesc, st);
                 } else if (OP == LIN_I4) {
-                    mma64<false>(tmem, at, 0, bd, idesc, st);
-                    mma64<false>(tmem, at + 32, 0, bd, idesc, 1u);
+                    mma64<false>(tmem, at, 0, bd + half * slice, idesc, st);
+                    mma64<false>(tmem, at + 32, 0, bd + half * slice, idesc, 1u);
                 } else {
                     mma64<false>(tmem, at, 0, bd, idesc, st);
                     mma64<false>(tmem, at + 32, 0, bd + slice, idesc, 1u);
@@ -355,11 +357,13 @@ __global__ void __launch_bounds__(THREADS, 2)
             __syncwarp();
             if (++ds == DONE)
                 ds = 0;
-            bd += (uint64_t)(slot_bytes >> 4);
-            if (++slot == a.b_slots) {
-                slot = 0;
-                bph ^= 1;
-                bd = desc0;
+            if (half == BST - 1) {
+                bd += (uint64_t)(slot_bytes >> 4);
+                if (++slot == a.b_slots) {
+                    slot = 0;
+                    bph ^= 1;
+                    bd = desc0;
+                }
             }
             at += A_SLOT_COLS;
             if (++as == a_slots) {
@@ -715,7 +719,7 @@ cudaError_t launch_linear_gemm(const LinearGemm &g, cudaStream_t st)
     a.err = g.err;
     const bool bf16 = g.op == LIN_BF16;
     // the rings: enough token slots to cover their loads, the rest for weight chunks
-    const int nsl = g.fmt == FMT_BF16 || g.op == LIN_I4 ? 1 : 2;
+    const int nsl = g.fmt == FMT_BF16 ? 1 : 2;
     const int slot_bytes = nsl * a.tile_tokens * HALF_K * 2 + (g.fmt == FMT_BF16 ? A_TILE_BYTES : 0);
     if (g.fmt == FMT_BF16) {
         a.b_slots = RING_BYTES / slot_bytes < B_MAX ? RING_BYTES / slot_bytes : B_MAX;
