@@ -274,3 +274,26 @@ def test_linear_refusals():
     e = torch.empty((0, 64), dtype=torch.bfloat16, device="cuda")
     assert lin.forward(e).shape == (0, 40)
     lin.free()
+
+
+@pytest.mark.parametrize("fmt", FMTS + ["mxfp4 wide"])
+@pytest.mark.parametrize("T", [9, 33, 65, 97, 128, 129, 300])
+def test_linear_gemm_ring_depths(fmt, T):
+    """The tcgen05 GEMM with one to many weight chunks per CTA, on every depth of its rings; rows of MXFP4 exponents
+    too wide for FP16 operands; results repeat bit for bit, from L2 and from HBM."""
+    _, Linear = _mods()
+    flush = torch.empty(160 << 20, dtype=torch.uint8, device="cuda")
+    wide = fmt.endswith("wide")
+    fmt = fmt.split()[0]
+    for N, K in ((130, 32), (260, 160), (100, 640), (513, 1504), (128, 3136), (1030, 4704)):
+        W = Weight(fmt, N, K, seed=K + T, **({"e_lo": 100, "e_hi": 140} if wide else {}))
+        lin = Linear(fmt, *W.args)
+        x, xd, _ = _x(np.random.default_rng(K), T, K, "bf16")
+        first = lin.forward(xd)
+        _check(first, x, W)
+        for i in range(6):
+            if i % 2:
+                flush.fill_(i)
+            assert torch.equal(lin.forward(xd), first)
+        lin.sync()
+        lin.free()
