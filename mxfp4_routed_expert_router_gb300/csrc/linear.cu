@@ -18,6 +18,7 @@
 #include "../../include/moe.h"
 #include "gemm_common.cuh"
 #include "linear_internal.cuh"
+#include "overlap.cuh"
 
 using namespace moe;
 
@@ -133,17 +134,18 @@ __device__ __forceinline__ int x_exponent(uint32_t max_bits) { return max((int)(
 __device__ __forceinline__ float pow2f(int e) { return __int_as_float(e < -126 ? 0x400000 : (127 + e) << 23); }
 
 // 8 values of token row t from column k (a multiple of 8; zeros from kend, a
-// multiple of 32) as they lie in memory: BF16, or E4M3 in x, y and the block's
+// multiple of 32; from L2, not through the read-only path: the kernel before may
+// have written them while this one had started) as they lie in memory: BF16, or E4M3 in x, y and the block's
 // E8M0 byte in z.
 __device__ __forceinline__ uint4 load_x8(const LinArgs &a, long long t, int k, int kend)
 {
     uint4 u = make_uint4(0, 0, 0, 0);
     if (k < kend) {
         if (a.x_mx) {
-            const uint2 c = __ldg(reinterpret_cast<const uint2 *>(static_cast<const uint8_t *>(a.x) + t * a.x_ld + k));
-            u = make_uint4(c.x, c.y, __ldg(a.xscales + t * (a.K / 32) + k / 32), 0);
+            const uint2 c = __ldcg(reinterpret_cast<const uint2 *>(static_cast<const uint8_t *>(a.x) + t * a.x_ld + k));
+            u = make_uint4(c.x, c.y, __ldcg(a.xscales + t * (a.K / 32) + k / 32), 0);
         } else {
-            u = __ldg(reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(a.x) + t * a.x_ld + k));
+            u = __ldcg(reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(a.x) + t * a.x_ld + k));
         }
     }
     return u;
@@ -338,6 +340,7 @@ __global__ void __launch_bounds__(THREADS, 1) linear_kernel(const __grid_constan
     float *red = reinterpret_cast<float *>(smem + a.red_off);        // [warp + row group][token][16]
     float *fin = reinterpret_cast<float *>(smem + a.fin_off);        // [row group][token][16] (clusters)
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, q = lane & 3;
+    overlap_trigger();
     uint32_t crank, csize;
     asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(crank));
     asm("mov.u32 %0, %%cluster_nctarank;" : "=r"(csize));
@@ -412,7 +415,7 @@ __global__ void __launch_bounds__(THREADS, 1) linear_kernel(const __grid_constan
     };
     // ---- x: this CTA's columns of the tile's tokens as B fragments [block][token]
     // [64 bytes].  An item is 256 values of one token, a vector of 8 per lane; a
-    // warp loads XB items at a time, the first before its weights.  FP16 operands
+    // warp loads XB items at a time.  FP16 operands
     // take x * 2^-e, e from the item's largest |x| (in [2^14, 2^15) then): exact for
     // BF16 and E4M3 values within 2^-29 of it.
     constexpr int XB = 4;
@@ -428,12 +431,13 @@ __global__ void __launch_bounds__(THREADS, 1) linear_kernel(const __grid_constan
                 xr[b] = load_x8(a, t, k0 + (i / TB * 32 + lane) * 8, kend);
         }
     };
-    load_items(warp);
     constexpr int DEPTH = FMT == FMT_MXFP4 ? 3 : 2;  // (three spill with INT4: 33 against 27 us at 7168 x 18432, 8 tokens)
     Step<FMT, NB> st[DEPTH];
 #pragma unroll
     for (int d = 0; d < DEPTH; ++d)
         load(st[d]);
+    overlap_wait();
+    load_items(warp);
     for (int i0 = warp; i0 < items; i0 += XB * WARPS) {
 #pragma unroll
         for (int b = 0; b < XB; ++b) {
@@ -732,18 +736,8 @@ cudaError_t launch_linear(const LinArgs &args, cudaStream_t st)
     cudaError_t e = gemm::smem_limit_once(attr_set, (const void *)kern, SMEM_MAX);
     if (e != cudaSuccess)
         return e;
-    cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3((unsigned)((n16 + best.rgroups - 1) / best.rgroups * best.cluster));
-    cfg.blockDim = dim3(THREADS);
-    cfg.dynamicSmemBytes = best.smem;
-    cfg.stream = st;
-    cudaLaunchAttribute at;
-    at.id = cudaLaunchAttributeClusterDimension;
-    at.val.clusterDim.x = (unsigned)best.cluster;
-    at.val.clusterDim.y = at.val.clusterDim.z = 1;
-    cfg.attrs = &at;
-    cfg.numAttrs = best.cluster > 1;
-    return cudaLaunchKernelEx(&cfg, kern, a);
+    return launch_overlapped(kern, (unsigned)((n16 + best.rgroups - 1) / best.rgroups * best.cluster), THREADS, best.smem,
+                             best.cluster, st, a);
 }
 
 template <int FMT>

@@ -20,9 +20,9 @@
 // tensor-memory lane quadrant, taking the stages in turn) and then finish the tile.
 // Weights and tokens come through rings of their own, as deep as the tile's size
 // leaves room for: with few tokens the weight stream is what bounds a call, and
-// its copies then run well ahead of the decoders.  The GEMM is launched while the
+// its copies then run well ahead of the decoders.  The GEMM starts while the
 // kernel that writes the token rows still runs and waits for it only before it
-// reads them.  Every mbarrier wait is bounded (gemm_common.cuh).
+// reads them (overlap.cuh).  Every mbarrier wait is bounded (gemm_common.cuh).
 #include <cuda.h>
 #include <cudaTypedefs.h>
 #include <cuda_bf16.h>
@@ -31,6 +31,7 @@
 #include "gemm_common.cuh"
 #include "linear_internal.cuh"
 #include "mx_decode.cuh"
+#include "overlap.cuh"
 
 namespace moe {
 
@@ -216,6 +217,7 @@ __global__ void __launch_bounds__(THREADS, 2)
     float *tsc = reinterpret_cast<float *>(smem + TSC_OFF);
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    overlap_trigger();
     uint32_t crank, csize;
     asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(crank));
     asm("mov.u32 %0, %%cluster_nctarank;" : "=r"(csize));
@@ -266,7 +268,7 @@ __global__ void __launch_bounds__(THREADS, 2)
 
     if (warp == WARP_LOAD) {
         // ---------------------------------------------------------- token tiles -> ring
-        asm volatile("griddepcontrol.wait;" ::: "memory");  // the token rows are written
+        overlap_wait();  // the token rows are written
         int it = 0, slot = 0, ds = BST - 1;
         uint32_t dph = 0;
         for (; it < nst / BST; ++it) {
@@ -475,7 +477,7 @@ __global__ void __launch_bounds__(THREADS, 2)
             }
         }
         // ---------------------------------------------------------- the tile's sums
-        asm volatile("griddepcontrol.wait;" ::: "memory");
+        overlap_wait();
         if (OP != LIN_BF16) {  // (every warp writes the same values and reads its own)
             for (int i = lane; i < nvalid; i += 32)
                 tsc[i] = __ldcg(a.xscale + tok0 + i);
@@ -575,11 +577,12 @@ __global__ void __launch_bounds__(1024) linear_rows_kernel(const void *x, const 
     __shared__ uint32_t red[32];
     const long long t = blockIdx.x;
     const int nt = blockDim.x;
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // the GEMM starts on the weights
+    overlap_trigger();  // the GEMM starts on the weights
+    overlap_wait();
     auto load = [&](int v, float f[8]) {
         if (x_mx) {
-            const uint2 u = __ldg(reinterpret_cast<const uint2 *>(static_cast<const uint8_t *>(x) + t * x_ld) + v);
-            const int e = __ldg(xscales + t * (K / 32) + v / 4);
+            const uint2 u = __ldcg(reinterpret_cast<const uint2 *>(static_cast<const uint8_t *>(x) + t * x_ld) + v);
+            const int e = __ldcg(xscales + t * (K / 32) + v / 4);
             const float s = e == 255 ? __int_as_float(0x7FC00000) : __int_as_float(e ? e << 23 : 0x400000);
             const uint32_t w[2] = {u.x, u.y};
 #pragma unroll
@@ -592,7 +595,7 @@ __global__ void __launch_bounds__(1024) linear_rows_kernel(const void *x, const 
                 f[2 * i + 1] = p.y * s;
             }
         } else {
-            const uint4 u = __ldg(reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(x) + t * x_ld) + v);
+            const uint4 u = __ldcg(reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(x) + t * x_ld) + v);
             const uint32_t w[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
@@ -663,32 +666,14 @@ cudaError_t rows_map(CUtensorMap *m, const void *base, long long rows, int cols,
 
 template <int OP, int WFMT>
 cudaError_t launch_cfg(const Args &a, const CUtensorMap &mb, const CUtensorMap &ma, int grid, int cluster,
-                       bool after_rows, cudaStream_t st)
+                       cudaStream_t st)
 {
     auto kern = linear_tc_kernel<OP, WFMT>;
     static std::atomic<int> attr_set[MAX_DEVICES];
     const cudaError_t e = smem_limit_once(attr_set, (const void *)kern, SMEM_BYTES);
     if (e != cudaSuccess)
         return e;
-    cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3((unsigned)grid);
-    cfg.blockDim = dim3(THREADS);
-    cfg.dynamicSmemBytes = SMEM_BYTES;
-    cfg.stream = st;
-    cudaLaunchAttribute at[2];
-    cfg.attrs = at;
-    if (cluster > 1) {
-        at[cfg.numAttrs].id = cudaLaunchAttributeClusterDimension;
-        at[cfg.numAttrs].val.clusterDim.x = (unsigned)cluster;
-        at[cfg.numAttrs].val.clusterDim.y = at[cfg.numAttrs].val.clusterDim.z = 1;
-        ++cfg.numAttrs;
-    }
-    if (after_rows) {
-        at[cfg.numAttrs].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-        at[cfg.numAttrs].val.programmaticStreamSerializationAllowed = 1;
-        ++cfg.numAttrs;
-    }
-    return cudaLaunchKernelEx(&cfg, kern, a, mb, ma);
+    return launch_overlapped(kern, (unsigned)grid, THREADS, SMEM_BYTES, cluster, st, a, mb, ma);
 }
 
 size_t align256(size_t n) { return (n + 255) & ~(size_t)255; }
@@ -742,9 +727,8 @@ cudaError_t launch_linear_gemm(const LinearGemm &g, cudaStream_t st)
     } else {
         uint16_t *rows = reinterpret_cast<uint16_t *>(g.workspace);
         float *scale = reinterpret_cast<float *>(g.workspace + align256((size_t)g.T * kpad * 2));
-        linear_rows_kernel<<<g.T, g.T <= 2 * sm_count() ? 1024 : 256, 0, st>>>(g.x, g.xscales, g.x_ld, g.x_mx, g.K, kpad,
-                                                                            bf16, rows, scale);
-        if ((e = cudaGetLastError()) != cudaSuccess)
+        if ((e = launch_overlapped(linear_rows_kernel, g.T, g.T <= 2 * sm_count() ? 1024 : 256, 0, 1, st, g.x, g.xscales,
+                                   g.x_ld, (int)g.x_mx, g.K, kpad, (int)bf16, rows, scale)) != cudaSuccess)
             return e;
         a.xscale = scale;
         e = g.fmt == FMT_BF16 ? rows_map(&mb, rows, g.T, kpad, (long long)kpad * 2, a.tile_tokens)
@@ -766,11 +750,11 @@ cudaError_t launch_linear_gemm(const LinearGemm &g, cudaStream_t st)
         cluster *= 2;
     const int grid = (int)items * cluster;
     switch (g.op) {
-    case LIN_F16: return launch_cfg<LIN_F16, FMT_MXFP4>(a, mb, ma, grid, cluster, rows_written, st);
-    case LIN_I4: return launch_cfg<LIN_I4, FMT_INT4>(a, mb, ma, grid, cluster, rows_written, st);
+    case LIN_F16: return launch_cfg<LIN_F16, FMT_MXFP4>(a, mb, ma, grid, cluster, st);
+    case LIN_I4: return launch_cfg<LIN_I4, FMT_INT4>(a, mb, ma, grid, cluster, st);
     default:
-        return g.fmt == FMT_BF16 ? launch_cfg<LIN_BF16, FMT_BF16>(a, mb, ma, grid, cluster, rows_written, st)
-                                 : launch_cfg<LIN_BF16, FMT_MXFP4>(a, mb, ma, grid, cluster, rows_written, st);
+        return g.fmt == FMT_BF16 ? launch_cfg<LIN_BF16, FMT_BF16>(a, mb, ma, grid, cluster, st)
+                                 : launch_cfg<LIN_BF16, FMT_MXFP4>(a, mb, ma, grid, cluster, st);
     }
 }
 

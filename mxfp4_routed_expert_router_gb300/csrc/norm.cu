@@ -18,6 +18,7 @@
 
 #include "../../include/moe.h"
 #include "moe_internal.cuh"
+#include "overlap.cuh"
 
 namespace moe {
 
@@ -97,6 +98,8 @@ __global__ void __launch_bounds__(1024) add_rmsnorm_kernel(const NormArgs a)
     const int nv = a.H / 8;
     const long long t = (long long)blockIdx.x * blockDim.y + threadIdx.y;
     const bool live = t < a.T;
+    overlap_trigger();
+    overlap_wait();
     float v[VPT][8];
     float ss = 0.f;
 #pragma unroll
@@ -211,12 +214,11 @@ cudaError_t launch_norm(const NormArgs &a, cudaStream_t st)
     const int threads = ((nv + vpt - 1) / vpt + 31) & ~31;
     const dim3 block(threads, 1);
     switch (vpt) {
-    case 1: add_rmsnorm_kernel<RES, DELTA, 1><<<a.T, block, 0, st>>>(a); break;
-    case 2: add_rmsnorm_kernel<RES, DELTA, 2><<<a.T, block, 0, st>>>(a); break;
-    case 4: add_rmsnorm_kernel<RES, DELTA, 4><<<a.T, block, 0, st>>>(a); break;
-    default: add_rmsnorm_kernel<RES, DELTA, 8><<<a.T, block, 0, st>>>(a); break;
+    case 1: return launch_overlapped(add_rmsnorm_kernel<RES, DELTA, 1>, a.T, block, 0, 1, st, a);
+    case 2: return launch_overlapped(add_rmsnorm_kernel<RES, DELTA, 2>, a.T, block, 0, 1, st, a);
+    case 4: return launch_overlapped(add_rmsnorm_kernel<RES, DELTA, 4>, a.T, block, 0, 1, st, a);
+    default: return launch_overlapped(add_rmsnorm_kernel<RES, DELTA, 8>, a.T, block, 0, 1, st, a);
     }
-    return cudaGetLastError();
 }
 
 bool rows_aligned(const void *p, long long ld, int size) { return (uintptr_t)p % 16 == 0 && ld * size % 16 == 0; }

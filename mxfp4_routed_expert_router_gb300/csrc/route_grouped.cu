@@ -37,6 +37,7 @@
 
 #include "../../include/moe.h"
 #include "moe_internal.cuh"
+#include "overlap.cuh"
 
 namespace moe {
 
@@ -412,6 +413,8 @@ template <int SCORE, int NV>
 __global__ void __launch_bounds__(256) route_grouped_kernel(const __grid_constant__ RouteArgs a)
 {
     __shared__ int cand[8][32];
+    overlap_trigger();
+    overlap_wait();
     const long long t = ((long long)blockIdx.x * blockDim.x + threadIdx.x) >> 5;
     if (t < a.T && !route_fast<SCORE, NV>(a, t, cand[threadIdx.x >> 5]))
         route_exact<SCORE, NV>(a, t);
@@ -424,10 +427,8 @@ cudaError_t launch(const RouteArgs &a, cudaStream_t st)
     const unsigned blocks = (unsigned)(((long long)a.T * 32 + threads - 1) / threads);
     const int nv = (a.gs + a.lg - 1) / a.lg;
 #define MOE_GROUPED_CASE(N)                                          \
-    if (nv <= N) {                                                   \
-        route_grouped_kernel<SCORE, N><<<blocks, threads, 0, st>>>(a); \
-        return cudaGetLastError();                                   \
-    }
+    if (nv <= N)                                                     \
+        return launch_overlapped(route_grouped_kernel<SCORE, N>, blocks, threads, 0, 1, st, a);
     MOE_GROUPED_CASE(4)
     MOE_GROUPED_CASE(8)
     MOE_GROUPED_CASE(16)

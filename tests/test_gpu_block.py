@@ -86,3 +86,63 @@ def test_block_in_a_graph_and_on_a_side_stream():
         g.replay()
         torch.cuda.synchronize()
         assert torch.equal(buf, want)
+
+
+@pytest.mark.parametrize("T", [1, 6, 20])
+def test_block_steps_without_waiting(T):
+    """Kernels of one step start while those of the step before still end: many steps enqueued at once, other work
+    between them, give what the same steps give one at a time."""
+    cfg, b, *_ = _block(70)
+    steps = 40
+    attn = [torch.randn((T, A), device="cuda").bfloat16() for _ in range(steps)]
+    res0 = torch.randn((T, H), device="cuda")
+    one, want = res0.clone(), []
+    for a in attn:
+        q = b.project_in(one)
+        torch.cuda.synchronize()
+        b.forward(a, one)
+        torch.cuda.synchronize()
+        want.append((q.clone(), one.clone()))
+        one.mul_(0.5)
+        torch.cuda.synchronize()
+    for _ in range(5):
+        res, got = res0.clone(), []
+        for a in attn:
+            q = b.project_in(res)
+            b.forward(a, res)
+            got.append((q, res.clone()))
+            res.mul_(0.5)
+        torch.cuda.synchronize()
+        for (q, r), (wq, wr) in zip(got, want):
+            assert torch.equal(q, wq) and torch.equal(r, wr)
+
+
+def test_operators_in_a_graph_beside_copies():
+    """Captured after and between copies and memsets, as a serving step is."""
+    cfg, b, *_ = _block(80)
+    T = 5
+    host_attn = torch.randn((T, A)).bfloat16().pin_memory()
+    host_res = torch.randn((T, H)).pin_memory()
+    attn, res = torch.zeros((T, A), device="cuda", dtype=torch.bfloat16), torch.zeros((T, H), device="cuda")
+    out = torch.empty((T, H), device="cuda")
+    b.project_in(res)
+    b.forward(attn, res)
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        attn.copy_(host_attn, non_blocking=True)
+        res.copy_(host_res, non_blocking=True)
+        q = b.project_in(res)
+        b.forward(attn, res)
+        out.copy_(res)
+        res.zero_()
+        q2 = b.project_in(out)
+    for i in range(4):
+        host_attn.copy_(torch.randn((T, A)).bfloat16())
+        host_res.copy_(torch.randn((T, H)))
+        g.replay()
+        torch.cuda.synchronize()
+        r = host_res.cuda()
+        assert torch.equal(b.project_in(r), q)
+        b.forward(host_attn.cuda(), r)
+        assert torch.equal(out, r) and torch.equal(b.project_in(r), q2) and not res.any()
