@@ -217,7 +217,6 @@ __global__ void __launch_bounds__(THREADS, 2)
     float *tsc = reinterpret_cast<float *>(smem + TSC_OFF);
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    overlap_trigger();
     uint32_t crank, csize;
     asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(crank));
     asm("mov.u32 %0, %%cluster_nctarank;" : "=r"(csize));
@@ -477,6 +476,7 @@ __global__ void __launch_bounds__(THREADS, 2)
             }
         }
         // ---------------------------------------------------------- the tile's sums
+        overlap_trigger();
         overlap_wait();
         if (OP != LIN_BF16) {  // (every warp writes the same values and reads its own)
             for (int i = lane; i < nvalid; i += 32)

@@ -98,7 +98,6 @@ __global__ void __launch_bounds__(1024) add_rmsnorm_kernel(const NormArgs a)
     const int nv = a.H / 8;
     const long long t = (long long)blockIdx.x * blockDim.y + threadIdx.y;
     const bool live = t < a.T;
-    overlap_trigger();
     overlap_wait();
     float v[VPT][8];
     float ss = 0.f;
@@ -151,6 +150,7 @@ __global__ void __launch_bounds__(1024) add_rmsnorm_kernel(const NormArgs a)
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1)
         ss += __shfl_xor_sync(0xffffffffu, ss, o);
+    overlap_trigger();
     const int nw = blockDim.x >> 5;  // warps of a row
     if (nw > 1) {
         if (lane == 0)
