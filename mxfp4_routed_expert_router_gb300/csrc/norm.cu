@@ -156,13 +156,21 @@ __global__ void __launch_bounds__(1024) add_rmsnorm_kernel(const NormArgs a)
         if (lane == 0)
             red[threadIdx.y * nw + (tid >> 5)] = ss;
         __syncthreads();
-        ss = 0.f;
-        for (int i = 0; i < nw; ++i)
-            ss += red[threadIdx.y * nw + i];
+        ss = lane < nw ? red[threadIdx.y * nw + lane] : 0.f;
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1)
+            ss += __shfl_xor_sync(0xffffffffu, ss, o);
     }
     if (!a.y && !a.q)
         return;
-    const float rinv = rsqrtf(ss / (float)a.H + a.eps);
+    // 1 / sqrt(x) as hi + lo (one Newton step, whose residual 1 - x hi^2 is taken
+    // exactly), so that n below rounds once: an E4M3 value next to a border falls on
+    // the side that the formula gives, but for the error of the mean
+    const float x = ss / (float)a.H + a.eps;
+    const float hi = rsqrtf(x);
+    const float xh = x * hi;
+    float lo = 0.5f * hi * (fmaf(-xh, hi, 1.f) - fmaf(x, hi, -xh) * hi);
+    lo = isfinite(lo) ? lo : 0.f;
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
         const int c = tid + i * (int)blockDim.x;
@@ -179,8 +187,11 @@ __global__ void __launch_bounds__(1024) add_rmsnorm_kernel(const NormArgs a)
                 g[j] = 1.f;
         }
 #pragma unroll
-        for (int j = 0; j < 8; ++j)
-            v[i][j] = v[i][j] * rinv * g[j];
+        for (int j = 0; j < 8; ++j) {
+            const float p = v[i][j] * hi;
+            const float rest = fmaf(v[i][j], lo, fmaf(v[i][j], hi, -p));
+            v[i][j] = fmaf(p, g[j], rest * g[j]);
+        }
         if (in && a.y)
             *reinterpret_cast<uint4 *>(a.y + t * a.y_ld + 8 * c) = bf16x8(v[i]);
         if (a.q) {
