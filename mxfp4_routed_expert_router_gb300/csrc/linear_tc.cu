@@ -24,9 +24,10 @@
 // kernel that writes the token rows still runs and waits for it only before it
 // reads them (overlap.cuh).  Every mbarrier wait is bounded (gemm_common.cuh).
 //
-// Bound by the tensor pipe for many tokens, by the decoders with INT4 weights (two
-// operands to make), and by the hand-offs between the roles for small tiles (a copy
-// without the decode and the MMAs still took 26 of 33 us at 17 tokens).  A tile is 128
+// Bound by the hand-offs between the roles (with few tokens a copy without the decode
+// and the MMAs still took 26 of 33 us; with 512 and with 2048 an SM takes 0.47 us per
+// 128 x 128 x 128 step, 0.70 of the tensor burst) and by the decoders with INT4
+// weights (two operands to make).  A tile is 128
 // tokens wide, as two CTAs share an SM's tensor memory (one CTA per SM with 256-wide
 // tiles leaves nothing to run during the hand-offs); an MMA of 64 columns or fewer
 // takes no longer than one of 64, so narrower tiles pay no less.
