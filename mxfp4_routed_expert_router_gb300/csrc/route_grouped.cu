@@ -272,6 +272,40 @@ __device__ __forceinline__ bool route_fast(const RouteArgs &a, long long t, int 
     const float err2 = 2.f * (ABS * __uint_as_float(sm) + U * __uint_as_float(km));
     auto err_of = [&](float c) { return a.bias ? err2 : 2.f * REL * c; };
 
+    // FP64 keys of up to 32 experts, one a lane (a warp's work; 0 for lanes without one)
+    auto keys64 = [&](int e, bool has) {
+        double sum64 = 0.0;
+        if (SCORE == MOE_SCORE_SOFTMAX) {
+#pragma unroll 1
+            for (int i = 0; i < NV; ++i)
+                if (has_grp && sub + a.lg * i < a.gs && mine[a.lg * i] != -INFINITY)
+                    sum64 += exp((double)mine[a.lg * i] - (double)mx);
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1)
+                sum64 += __shfl_xor_sync(0xffffffffu, sum64, o);
+        }
+        if (!has)
+            return (u64)0;
+        const double l64 = (double)row[e];
+        const double s64 = SCORE == MOE_SCORE_SOFTMAX ? exp(l64 - (double)mx) / sum64 : 1.0 / (1.0 + exp(-l64));
+        return order_key(s64 + (a.bias ? (double)a.bias[e] : 0.0));
+    };
+    // Adds to the n experts in cand those of this lane whose key is at least `floor`
+    // (0: none); returns their number, which may be above 32.
+    auto collect = [&](int n, uint32_t floor) {
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            const bool c = floor != 0u && key[i] >= floor;
+            const unsigned mask = __ballot_sync(0xffffffffu, c);
+            const int at = n + __popc(mask & ((1u << lane) - 1u));
+            if (c && at < 32)
+                cand[at] = grp * a.gs + sub + a.lg * i;
+            n += __popc(mask);
+        }
+        __syncwarp();
+        return n;
+    };
+
     bool sure = true;
     if (a.k_groups < a.n_groups) {
         for (int o = 1; o < a.lg; o <<= 1) {
@@ -292,7 +326,47 @@ __device__ __forceinline__ bool route_fast(const RouteArgs &a, long long t, int 
                 // the gap between the last group that stays and the next (sums of two keys, rounded)
                 if (m != 0u) {
                     const float x = key_value32(last), y = key_value32(m);
-                    sure = x - y > 2.f * err_of(x) + 4.f * U * (fabsf(x) + fabsf(y));
+                    const float tol = 1.01f * (2.f * err_of(x) + 4.f * U * (fabsf(x) + fabsf(y)));
+                    if (x - y <= tol) {
+                        // Groups above y + tol stay and groups below x - tol do not; the FP64
+                        // scores of those between decide.  A score is that of the experts whose
+                        // keys can be the largest, or the second largest, of the group.
+                        const float g = key_value32(gk);
+                        const bool in = has_grp && gk != 0u && g > y + tol;
+                        const bool open = has_grp && gk != 0u && !in && g >= x - tol;
+                        const int left = a.k_groups - __popc(__ballot_sync(0xffffffffu, in && sub == 0));
+                        const uint32_t low = a.top2 ? b2 : b1;
+                        const uint32_t floor =
+                            low == 0u ? 1u : order_key32(key_value32(low) - err_of(key_value32(b1)));
+                        const int n = collect(0, open ? floor : 0u);
+                        if (n > 32)
+                            return false;
+                        const int e = lane < n ? cand[lane] : 0, eg = lane < n ? e / a.gs : -1;
+                        const u64 k64 = keys64(e, lane < n);
+                        u64 g1 = 0ull, g2 = 0ull;
+                        bool repeats = false;  // an earlier lane stands for the group
+                        for (int j = 0; j < n; ++j) {
+                            const u64 kj = __shfl_sync(0xffffffffu, k64, j);
+                            if (__shfl_sync(0xffffffffu, eg, j) == eg) {
+                                g2 = max(g2, min(g1, kj));
+                                g1 = max(g1, kj);
+                                repeats = repeats || j < lane;
+                            }
+                        }
+                        const u64 g64 = a.top2 && g2 != 0ull ? order_key(key_value(g1) + key_value(g2)) : g1;
+                        int better = 0;
+                        for (int j = 0; j < n; ++j) {
+                            const u64 gj = __shfl_sync(0xffffffffu, g64, j);
+                            const int ej = __shfl_sync(0xffffffffu, repeats ? -1 : eg, j);
+                            better += ej >= 0 && (gj > g64 || (gj == g64 && ej < eg));
+                        }
+                        kept = in;
+                        for (int j = 0; j < n; ++j) {
+                            const int ej = __shfl_sync(0xffffffffu, better < left ? eg : -1, j);
+                            kept = kept || ej == grp;
+                        }
+                        __syncwarp();  // cand is written again
+                    }
                 }
                 break;
             }
@@ -308,8 +382,6 @@ __device__ __forceinline__ bool route_fast(const RouteArgs &a, long long t, int 
                 key[i] = 0u;
     }
 
-    if (!sure)
-        return false;
     int my_e = -1, taken = 0;
     uint32_t prev = 0u;
     for (int j = 0; j <= a.k; ++j) {
@@ -349,37 +421,11 @@ __device__ __forceinline__ bool route_fast(const RouteArgs &a, long long t, int 
         const uint32_t floor_key = order_key32(last - err_of(last));
         if (lane < taken)
             cand[lane] = my_e;
-        int n = taken;
-#pragma unroll
-        for (int i = 0; i < NV; ++i) {
-            const bool c = key[i] != 0u && key[i] >= floor_key;
-            const unsigned mask = __ballot_sync(0xffffffffu, c);
-            const int at = n + __popc(mask & ((1u << lane) - 1u));
-            if (c && at < 32)
-                cand[at] = grp * a.gs + sub + a.lg * i;
-            n += __popc(mask);
-        }
+        const int n = collect(taken, floor_key);
         if (n > 32)
             return false;
-        __syncwarp();
         const int e = lane < n ? cand[lane] : 0;
-        double sum64 = 0.0;
-        if (SCORE == MOE_SCORE_SOFTMAX) {
-#pragma unroll 1
-            for (int i = 0; i < NV; ++i)
-                if (has_grp && sub + a.lg * i < a.gs && mine[a.lg * i] != -INFINITY)
-                    sum64 += exp((double)mine[a.lg * i] - (double)mx);
-#pragma unroll
-            for (int o = 16; o > 0; o >>= 1)
-                sum64 += __shfl_xor_sync(0xffffffffu, sum64, o);
-        }
-        u64 k64 = 0ull;
-        if (lane < n) {
-            const double l64 = (double)row[e];
-            const double s64 =
-                SCORE == MOE_SCORE_SOFTMAX ? exp(l64 - (double)mx) / sum64 : 1.0 / (1.0 + exp(-l64));
-            k64 = order_key(s64 + (a.bias ? (double)a.bias[e] : 0.0));
-        }
+        const u64 k64 = keys64(e, lane < n);
         int rank = 0;
         for (int j = 0; j < n; ++j) {
             const u64 kj = __shfl_sync(0xffffffffu, k64, j);

@@ -114,6 +114,27 @@ def test_route_values_next_to_a_border(score, group_score):
     _run(logits, bias, 6, 4, 2, score, group_score, True, 1.0)
 
 
+@pytest.mark.parametrize("score", ["sigmoid", "softmax"])
+@pytest.mark.parametrize("group_score", ["max", "top2"])
+@pytest.mark.parametrize("n_groups,gs,k_groups", [(8, 16, 4), (4, 24, 1), (16, 5, 9), (32, 32, 16), (3, 2, 2)])
+def test_route_groups_next_to_a_border(score, group_score, n_groups, gs, k_groups):
+    """Group scores a few FP32 steps apart, or equal, around the last that stays: the groups are those of 64 bits.
+    A group's largest logit lies 0 to 3 steps above one value, its second is the same in all, so that scores are
+    equal or differ by an FP32 step of a key; the rest is far below."""
+    rng = np.random.default_rng(100 * n_groups + gs)
+    T, E = 150, n_groups * gs
+    logits = (rng.standard_normal((T, E)) - 6.0).astype(np.float32)
+    for t in range(T):
+        for g in range(n_groups):
+            at = g * gs + rng.permutation(gs)[:2]
+            far = rng.choice([0.0, 0.0, 0.0, 0.5, -0.5])  # some groups are out of the question, or in it for sure
+            logits[t, at[0]] = (np.float32(0.7 + far).view(np.int32) + rng.integers(0, 4)).astype(np.int32).view(np.float32)
+            logits[t, at[1]] = np.float32(0.4 + far)
+    bias = np.full(E, 0.125, np.float32)
+    _run(logits, bias, min(4, k_groups * gs), n_groups, k_groups, score, group_score, True, 1.0)
+    _run(logits, None, min(4, k_groups * gs), n_groups, k_groups, score, group_score, False, 1.0)
+
+
 def test_route_wide_logits_and_saturated_scores():
     rng = np.random.default_rng(12)
     logits = (rng.standard_normal((40, 128)) * 30).astype(np.float32)  # many sigmoids equal to 1 or near 0
