@@ -217,10 +217,17 @@ __device__ __forceinline__ bool route_fast(const RouteArgs &a, long long t, int 
     const bool has_grp = grp < a.n_groups;
     const float *mine = row + grp * a.gs + sub;
 
-    float l[NV];
+    float l[NV], bias[NV];  // every load before the first use
 #pragma unroll
     for (int i = 0; i < NV; ++i)
         l[i] = has_grp && sub + a.lg * i < a.gs ? mine[a.lg * i] : -INFINITY;
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
+        bias[i] = a.bias && has_grp && sub + a.lg * i < a.gs ? a.bias[grp * a.gs + sub + a.lg * i] : 0.f;
+    u64 on = 0ull;          // bit i: expert i of the lane is not switched off
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
+        on |= (u64)(l[i] != -INFINITY) << i;
     float mx = 0.f, inv = 1.f;
     if (SCORE == MOE_SCORE_SOFTMAX) {
         mx = l[0];
@@ -247,20 +254,16 @@ __device__ __forceinline__ bool route_fast(const RouteArgs &a, long long t, int 
     bool fine = true;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-        const int j = sub + a.lg * i;
-        key[i] = 0u;
-        if (has_grp && j < a.gs) {
-            const float lg = SCORE == MOE_SCORE_SOFTMAX ? mine[a.lg * i] : l[i];
-            if (lg != -INFINITY) {
-                const float s = SCORE == MOE_SCORE_SOFTMAX ? l[i] / inv : 1.f / (1.f + expf(-lg));
-                const float c = a.bias ? s + a.bias[grp * a.gs + j] : s;
-                // (a score below FP32's normal range has no relative accuracy)
-                fine = fine && isfinite(c) && s > 1e-30f;
-                smax = fmaxf(smax, s);
-                kmax = fmaxf(kmax, fabsf(c));
-                key[i] = order_key32(c);
-            }
-        }
+        const bool is_on = on >> i & 1;
+        // (a division of zero or by an infinity would take the slow path for the whole warp)
+        const float v = is_on ? l[i] : SCORE == MOE_SCORE_SOFTMAX ? inv : 0.f;
+        const float sc = SCORE == MOE_SCORE_SOFTMAX ? v / inv : 1.f / (1.f + expf(-v));
+        const float c = sc + bias[i];
+        // (a score below FP32's normal range has no relative accuracy)
+        fine = fine && (!is_on || (isfinite(c) && sc > 1e-30f));
+        smax = fmaxf(smax, is_on ? sc : 0.f);
+        kmax = fmaxf(kmax, is_on ? fabsf(c) : 0.f);
+        key[i] = is_on ? order_key32(c) : 0u;
         b2 = max(b2, min(b1, key[i]));
         b1 = max(b1, key[i]);
     }
