@@ -5,6 +5,7 @@ libmoe_gb300.so through ``binding``.
 """
 from __future__ import annotations
 
+import threading
 from typing import Optional
 
 import torch
@@ -12,6 +13,32 @@ import torch
 from . import binding as B
 
 FORMATS = {"mxfp4": B.MOE_W_MXFP4, "bf16": B.MOE_W_BF16, "int4g32": B.MOE_W_INT4G32}
+
+KEPT_WORKSPACE = 32 << 20  # largest workspace that stays with its stream
+
+
+class _Workspaces(threading.local):
+    """(device, stream) -> bytes that the layers' calls on that stream share; a thread has its own, as a call's
+    launches may lie between those of another thread's."""
+
+    def __init__(self):
+        self.of = {}
+
+
+_workspaces = _Workspaces()
+
+
+def _workspace(n: int, device: torch.device) -> torch.Tensor:
+    """At least n bytes for a call on torch's current stream.  Up to KEPT_WORKSPACE they stay with the stream for its
+    next call, which comes after this one there (an allocation between two launches costs as much as a launch).  A
+    captured call gets bytes of its graph's own, as a replay may run on another stream."""
+    if n > KEPT_WORKSPACE or torch.cuda.is_current_stream_capturing():
+        return torch.empty(n, dtype=torch.uint8, device=device)
+    key = (device.index, B._current_stream())
+    ws = _workspaces.of.get(key)
+    if ws is None or ws.numel() < n:
+        ws = _workspaces.of[key] = torch.empty(n, dtype=torch.uint8, device=device)
+    return ws
 
 
 class QuantLinear:
@@ -71,8 +98,7 @@ class QuantLinear:
         n = B.moe_linear_workspace_bytes(self.handle, T) if T > self._no_ws else 0
         ws = None
         if n or out is None:
-            # Allocated on each call, on the call's own stream: torch's allocator then keeps calls on several
-            # streams, and captured calls, apart.
+            # On the call's own stream: calls on several streams, and captured calls, then stay apart.
             if stream is None:
                 out, ws = self._allocate(T, n, out)
             else:
@@ -85,7 +111,7 @@ class QuantLinear:
     def _allocate(self, T: int, n: int, out):
         if out is None:
             out = torch.empty((T, self.N), dtype=torch.float32, device=self.device)
-        return out, torch.empty(n, dtype=torch.uint8, device=self.device) if n else None
+        return out, _workspace(n, self.device) if n else None
 
     def sync(self, stream=None):
         B.moe_linear_sync_status(self.handle, stream)

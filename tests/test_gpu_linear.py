@@ -6,6 +6,8 @@ additions, each off by at most 2^-23 of the terms so far: (K / 16 + 32) * 2^-23 
 sum |x||w| for every value (group-32 INT4 sums q and z apart: |s|(q + z) in place
 of |w|).  BF16 results round by 2^-8 of the value more.
 """
+import threading
+
 import numpy as np
 import pytest
 import torch
@@ -235,6 +237,69 @@ def test_linear_streams_graphs_and_freed_weights():
         g.replay()
         torch.cuda.synchronize()
         _check(out, x, W)
+    lin.free()
+
+
+def test_linear_calls_share_a_streams_workspace():
+    """Calls of several layers and sizes on one stream, without waiting, and a captured call replayed on another."""
+    _, Linear = _mods()
+    Ws = [Weight("mxfp4", 260, 512, seed=8), Weight("int4g32", 130, 1024, seed=9)]
+    lins = [Linear(W.fmt, *W.args) for W in Ws]
+    rng = np.random.default_rng(8)
+    calls = []  # sizes that grow, so that the workspace is replaced while calls are in flight
+    for T in (9, 40, 17, 300, 11, 700):
+        for W, lin in zip(Ws, lins):
+            x, xd, _ = _x(rng, T, W.K, "bf16")
+            calls.append((lin, W, x, xd, torch.empty((T, W.N), device="cuda")))
+    buf = [torch.zeros((50, W.K), dtype=torch.bfloat16, device="cuda") for W in Ws]
+    got = [torch.empty((50, W.N), device="cuda") for W in Ws]
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        for lin, b, o in zip(lins, buf, got):
+            lin.forward(b, out=o)
+    fresh = [_x(rng, 50, W.K, "bf16") for W in Ws]
+    for b, f in zip(buf, fresh):
+        b.copy_(f[1])
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    for _ in range(4):
+        with torch.cuda.stream(side):
+            g.replay()
+        for lin, _, _, xd, o in calls:
+            lin.forward(xd, out=o)
+    torch.cuda.synchronize()
+    for lin, W, x, _, o in calls:
+        _check(o, x, W)
+    for W, f, o in zip(Ws, fresh, got):
+        _check(o, f[0], W)
+    for lin in lins:
+        lin.free()
+
+
+def test_linear_threads_on_one_stream():
+    """Two threads whose calls interleave on the same stream do not share a workspace."""
+    _, Linear = _mods()
+    W = Weight("mxfp4", 200, 512, seed=10)
+    lin = Linear(W.fmt, *W.args)
+    rng = np.random.default_rng(10)
+    xs = [[_x(rng, T, 512, "bf16") for T in (20, 65, 9)] for _ in range(2)]
+    outs = [[torch.empty((x[0].shape[0], 200), device="cuda") for x in row] for row in xs]
+    torch.cuda.synchronize()
+
+    def work(i):
+        for _ in range(30):
+            for x, o in zip(xs[i], outs[i]):
+                lin.forward(x[1], out=o)
+
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(2)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    for row, out in zip(xs, outs):
+        for x, o in zip(row, out):
+            _check(o, x[0], W)
     lin.free()
 
 
