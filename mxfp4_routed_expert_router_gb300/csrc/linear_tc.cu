@@ -208,6 +208,28 @@ __device__ __forceinline__ void store_y(const Args &a, long long at, float v)
     }
 }
 
+// This CTA's tile and its rank in the cluster.  Read afresh where they are needed
+// again after the loops, so that no register holds them meanwhile.
+struct Tile {
+    int rt, tok0, nvalid, n_mma;
+    uint32_t crank, csize;
+};
+
+__device__ __forceinline__ Tile tile_here(const Args &a)
+{
+    Tile t;
+    uint32_t cta;
+    asm volatile("mov.u32 %0, %%ctaid.x;" : "=r"(cta));
+    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(t.crank));
+    asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(t.csize));
+    const int item = cta / t.csize;
+    t.rt = item / a.ttiles;
+    t.tok0 = (item - t.rt * a.ttiles) * a.tile_tokens;
+    t.nvalid = min(a.tile_tokens, a.T - t.tok0);
+    t.n_mma = (t.nvalid + 15) & ~15;
+    return t;
+}
+
 template <int OP, int WFMT>
 __global__ void __launch_bounds__(THREADS, 2)
     linear_tc_kernel(const __grid_constant__ Args a, const __grid_constant__ CUtensorMap map_b,
@@ -228,12 +250,9 @@ __global__ void __launch_bounds__(THREADS, 2)
     float *tsc = reinterpret_cast<float *>(smem + TSC_OFF);
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    uint32_t crank, csize;
-    asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(crank));
-    asm("mov.u32 %0, %%cluster_nctarank;" : "=r"(csize));
-    const int item = blockIdx.x / csize, rt = item / a.ttiles, tt = item - rt * a.ttiles;
-    const int tok0 = tt * a.tile_tokens, nvalid = min(a.tile_tokens, a.T - tok0);
-    const int n_mma = (nvalid + 15) & ~15;
+    const Tile at0 = tile_here(a);
+    const int rt = at0.rt, tok0 = at0.tok0, n_mma = at0.n_mma;
+    const uint32_t crank = at0.crank, csize = at0.csize;
     const int c0 = (int)((long long)a.kchunks * crank / csize), c1 = (int)((long long)a.kchunks * (crank + 1) / csize);
     const int nst = (c1 - c0) * (CHUNK_K / KST);  // stages
     const uint32_t slice_bytes = (uint32_t)a.tile_tokens * HALF_K * 2;
@@ -489,6 +508,9 @@ __global__ void __launch_bounds__(THREADS, 2)
         // ---------------------------------------------------------- the tile's sums
         overlap_trigger();
         overlap_wait();
+        const Tile at1 = tile_here(a);
+        const int rt = at1.rt, tok0 = at1.tok0, nvalid = at1.nvalid, n_mma = at1.n_mma;
+        const uint32_t csize = at1.csize;
         if (OP != LIN_BF16) {  // (every warp writes the same values and reads its own)
             for (int i = lane; i < nvalid; i += 32)
                 tsc[i] = __ldcg(a.xscale + tok0 + i);
@@ -537,7 +559,10 @@ __global__ void __launch_bounds__(THREADS, 2)
     }
 
     __syncwarp();
-    if (csize > 1) {
+    const Tile at2 = tile_here(a);
+    if (at2.csize > 1) {
+        const int rt = at2.rt, tok0 = at2.tok0, nvalid = at2.nvalid;
+        const uint32_t crank = at2.crank, csize = at2.csize;
         cluster_sync();
         // rank r finishes tokens r, r + csize, ... of the tile: a warp per token, four rows a lane
         if (!*abort_flag) {
