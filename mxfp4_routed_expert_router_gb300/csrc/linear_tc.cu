@@ -454,6 +454,38 @@ __global__ void __launch_bounds__(THREADS, 2)
                     slot -= a.w_slots;
                     ph ^= 1;
                 }
+                // The first block of the stage is decoded before the wait for its A slot, so that
+                // less lies between the end of the MMAs that used it and those that wait for it
+                // (INT4 7168 x 18432, 512 tokens: 221 -> 199 us; more blocks gain nothing more).
+                uint32_t o[16], lo[16];
+                auto decode = [&](int b, uint32_t *hi, uint32_t *rest) {
+                    const uint32_t w[4] = {code[b].x, code[b].y, code[b].z, code[b].w};
+                    if (OP == LIN_I4) {
+                        // relative to the row's base (the scale then lies below 2^12)
+                        const float sf = __half2float(__ushort_as_half((unsigned short)(sc[b] & 0xFFFFu))) *
+                                         __int_as_float((254 - rb) << 23);
+                        const uint32_t s2 = (uint32_t)__half_as_ushort(__float2half_rn(sf)) * 0x10001u;
+                        const uint32_t zz = (0x6400u + (sc[b] >> 16)) * 0x10001u;
+#pragma unroll
+                        for (int c = 0; c < 4; ++c)
+#pragma unroll
+                            for (int p = 0; p < 4; ++p)
+                                decode_i4(w[c] >> (4 * p), zz, s2, hi[4 * c + p], rest[4 * c + p]);
+                    } else if (OP == LIN_F16) {
+                        int d = (int)sc[b] - rb;
+                        d = d < -24 ? -24 : (d > 0 ? 0 : d);  // (blocks past K, whose codes are 0)
+                        const uint32_t s2 = f16x2_pow2(d);
+#pragma unroll
+                        for (int c = 0; c < 4; ++c)
+                            decode_e2m1(w[c], s2, hi + 4 * c);
+                    } else {
+                        const uint32_t s2 = e8m0_to_bf16x2(sc[b]);
+#pragma unroll
+                        for (int c = 0; c < 4; ++c)
+                            decode_word(w[c], s2, hi + 4 * c);
+                    }
+                };
+                decode(0, o, lo);
                 if (st >= a_slots) {
                     if (!(ok = mbar_wait_warp(&done[ds], dph, abort_flag, a.err, lane)))
                         break;
@@ -466,34 +498,10 @@ __global__ void __launch_bounds__(THREADS, 2)
                 const uint32_t dst = tmem_a + tlane + as * A_SLOT_COLS;
 #pragma unroll
                 for (int b = 0; b < NBLK; ++b) {
-                    const uint32_t w[4] = {code[b].x, code[b].y, code[b].z, code[b].w};
-                    uint32_t o[16];
-                    if (OP == LIN_I4) {
-                        // relative to the row's base (the scale then lies below 2^12)
-                        const float sf = __half2float(__ushort_as_half((unsigned short)(sc[b] & 0xFFFFu))) *
-                                         __int_as_float((254 - rb) << 23);
-                        const uint32_t s2 = (uint32_t)__half_as_ushort(__float2half_rn(sf)) * 0x10001u;
-                        const uint32_t zz = (0x6400u + (sc[b] >> 16)) * 0x10001u;
-                        uint32_t lo[16];
-#pragma unroll
-                        for (int c = 0; c < 4; ++c)
-#pragma unroll
-                            for (int p = 0; p < 4; ++p)
-                                decode_i4(w[c] >> (4 * p), zz, s2, o[4 * c + p], lo[4 * c + p]);
+                    if (b > 0)
+                        decode(b, o, lo);
+                    if (OP == LIN_I4)
                         tmem_st16(dst + 32 + b * 16, lo);
-                    } else if (OP == LIN_F16) {
-                        int d = (int)sc[b] - rb;
-                        d = d < -24 ? -24 : (d > 0 ? 0 : d);  // (blocks past K, whose codes are 0)
-                        const uint32_t s2 = f16x2_pow2(d);
-#pragma unroll
-                        for (int c = 0; c < 4; ++c)
-                            decode_e2m1(w[c], s2, o + 4 * c);
-                    } else {
-                        const uint32_t s2 = e8m0_to_bf16x2(sc[b]);
-#pragma unroll
-                        for (int c = 0; c < 4; ++c)
-                            decode_word(w[c], s2, o + 4 * c);
-                    }
                     tmem_st16(dst + b * 16, o);
                 }
                 asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
