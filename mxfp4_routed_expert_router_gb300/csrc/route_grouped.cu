@@ -23,11 +23,14 @@
 //   softmax: exp 4 u; its argument l - max rounded, |l - max| u (below 76 u for the
 //     scores above 1e-30 taken here; times exp(l - max), below 0.37 u of the
 //     largest); the sum of at most 64 terms a lane and 5 shuffles (69 u) of terms
-//     off by 4 u and on average |l - max| < 7 u; the division u: below 256 u of
-//     the score, and below 96 u of the row's largest score
+//     off by 4 u and on average |l - max| < 7 u; the division u: below 96 u of the
+//     row's largest score.  The sum is the same for every expert and turns no order
+//     around: without a bias a key counts as off by (5 + |l - max|) u of itself, with
+//     |l - max| from the key (err_of takes 8 + 1.1 |log|, which also holds for the sum
+//     of two keys: e |log e| of the lesser is below the greater's, or below 0.37)
 //   key with a bias: the score's, and u |key| for the addition
-// Without a bias the error is relative to the key (REL), with one it is taken
-// from the row's largest score (ABS) and key.
+// Without a bias the error is relative to the key, with one it is taken from the
+// row's largest score (ABS) and key.
 // Where the order of groups is in doubt, the same is done for the experts that can
 // make up the scores of the groups between the border's error bounds.
 // Issue bound for many rows (a row is 4 E bytes), latency bound for few: all of a
@@ -216,7 +219,7 @@ template <int SCORE, int NV>
 __device__ __forceinline__ bool route_fast(const RouteArgs &a, long long t, int *cand)
 {
     constexpr float U = 5.9604645e-8f;  // 2^-24
-    constexpr float REL = (SCORE == MOE_SCORE_SOFTMAX ? 256.f : 8.f) * U;
+    constexpr float REL = 8.f * U;
     constexpr float ABS = (SCORE == MOE_SCORE_SOFTMAX ? 96.f : 8.f) * U;
     const int lane = threadIdx.x & 31;
     const float *row = a.logits + t * a.E;
@@ -280,7 +283,11 @@ __device__ __forceinline__ bool route_fast(const RouteArgs &a, long long t, int 
     const uint32_t sm = __reduce_max_sync(0xffffffffu, __float_as_uint(smax));
     const uint32_t km = __reduce_max_sync(0xffffffffu, __float_as_uint(kmax));
     const float err2 = 2.f * (ABS * __uint_as_float(sm) + U * __uint_as_float(km));
-    auto err_of = [&](float c) { return a.bias ? err2 : 2.f * REL * c; };
+    auto err_of = [&](float c) {
+        if (a.bias)
+            return err2;
+        return SCORE == MOE_SCORE_SOFTMAX ? 2.f * U * c * (8.f + 1.1f * fabsf(__logf(c * inv))) : 2.f * REL * c;
+    };
 
     // FP64 keys of up to 32 experts, one a lane (a warp's work; 0 for lanes without one)
     auto keys64 = [&](int e, bool has) {
@@ -403,8 +410,10 @@ __device__ __forceinline__ bool route_fast(const RouteArgs &a, long long t, int 
         if (m == 0u)
             break;  // no expert is left: empty slots
         if (j > 0) {
-            const float x = key_value32(prev);
-            sure = sure && x - key_value32(m) > err_of(x);
+            const float x = key_value32(prev), gap = x - key_value32(m);
+            // (a gap that any softmax score's error allows for needs no logarithm)
+            if (SCORE != MOE_SCORE_SOFTMAX || a.bias || !(gap > 1024.f * U * x))
+                sure = sure && gap > err_of(x);
         }
         if (j == a.k)
             break;
