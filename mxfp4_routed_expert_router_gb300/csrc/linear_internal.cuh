@@ -9,10 +9,10 @@ namespace moe {
 // warp-level MMAs (linear.cu); more tokens run on the tcgen05 GEMM
 // (linear_tc.cu).  Eight tokens fill the columns of a warp-level MMA.  Measured
 // (device time in us, 8 tokens here and 9 in the GEMM): MXFP4 7168 x 7168 10.8 and
-// 12.2, 7168 x 18432 19.9 and 26.0; group-32 INT4 7168 x 18432 24.8 and 46.4; BF16
-// 256 x 7168 4.0 and 6.3, 2048 x 7168 7.9 and 7.4, 7168 x 7168 18.9 and 19.2.  Sixteen
+// 12.2, 7168 x 18432 19.9 and 26.5; group-32 INT4 7168 x 18432 24.8 and 45.3; BF16
+// 256 x 7168 4.0 and 6.3, 2048 x 7168 7.9 and 7.3, 7168 x 7168 18.9 and 18.8.  Sixteen
 // tokens here would take two MMAs per weight fragment: MXFP4 7168 x 7168 17.7 (the
-// GEMM 12.7), 36864 x 7168 55 (32.6); INT4 7168 x 18432 52 (46.5).
+// GEMM 12.7), 36864 x 7168 55 (32.3); INT4 7168 x 18432 52 (45.8).
 constexpr int LINEAR_STREAM_MAX_T = 8;
 
 // Operands of the tcgen05 GEMM: FP16 (MXFP4 whose exponents span at most

@@ -25,15 +25,15 @@
 // reads them (overlap.cuh).  Every mbarrier wait is bounded (gemm_common.cuh).
 //
 // Bound by the hand-offs between the roles (with few tokens a copy without the decode
-// and the MMAs still took 26 of 33 us; with 512 and with 2048 an SM takes 0.47 us per
-// 128 x 128 x 128 step, 0.70 of the tensor burst) and by the decoders with INT4
+// and the MMAs still took 26 of 33 us; with 512 and with 2048 an SM takes 0.44 us per
+// 128 x 128 x 128 step, 0.75 of the tensor burst) and by the decoders with INT4
 // weights (two operands to make).  A tile is 128
 // tokens wide, as two CTAs share an SM's tensor memory (one CTA per SM with 256-wide
 // tiles leaves nothing to run during the hand-offs); an MMA of 64 columns or fewer
 // takes no longer than one of 64, so narrower tiles pay no less.
-// Measured, us per call back to back: MXFP4 7168 x 7168, 9 tokens 12.2, 32 13.7, 128
-// 22.1, 512 53 (0.99 PFLOP/s), 2048 154 (1.36); group-32 INT4 21.4, 22.1, 31.9, 93;
-// BF16 19.2, 20.0, 26.2, 60.
+// Measured, us per call back to back: MXFP4 7168 x 7168, 9 tokens 12.2, 32 13.5, 128
+// 21.8, 512 50 (1.05 PFLOP/s), 2048 146 (1.44), 36864 x 7168 with 2048 717 (1.51);
+// group-32 INT4 7168 x 7168 20.7, 21.9, 30.3, 84, 244; BF16 18.8, 19.6, 25.9, 61, 166.
 #include <cuda.h>
 #include <cudaTypedefs.h>
 #include <cuda_bf16.h>
