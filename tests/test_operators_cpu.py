@@ -106,3 +106,40 @@ def test_wrappers_check_shapes_and_types(b):
         with pytest.raises(b.MoeError) as e:
             call()
         assert e.value.status == b.MOE_EINVAL
+
+
+def _refused(b, calls):
+    for i, call in enumerate(calls):
+        with pytest.raises(b.MoeError) as e:
+            call()
+        assert e.value.status == b.MOE_EINVAL, i
+
+
+def test_route_wrapper_checks_shapes_and_types(b, monkeypatch):
+    """Bare addresses reach the library only from tensors of the right type and size."""
+    import torch
+    T, E, k = 3, 16, 4
+    reached = []
+    monkeypatch.setattr(b, "_stream", lambda s: None)
+    monkeypatch.setattr(b.lib, "moe_route_grouped", lambda *a: reached.append(a) or 0)
+    good = dict(logits=torch.zeros(T, E), bias=torch.zeros(E), ids=torch.zeros((T, k), dtype=torch.int32),
+                w=torch.zeros(T, k))
+
+    def call(**kw):
+        v = {**good, **kw}
+        b.moe_route_grouped(v["logits"], v["bias"], T, E, k, 4, 2, b.MOE_SCORE_SIGMOID, b.MOE_GROUP_MAX, True, 1.0,
+                            v["ids"], v["w"])
+
+    _refused(b, [lambda kw=kw: call(**kw) for kw in (
+        dict(logits=good["logits"].bfloat16()), dict(logits=good["logits"].double()), dict(logits=torch.zeros(T, E - 1)),
+        dict(logits=torch.zeros(T - 1, E)), dict(logits=torch.zeros(E, T).t()), dict(logits=torch.zeros(T, 2 * E)[:, :E]),
+        dict(logits=torch.zeros(T, 2 * E)), dict(bias=torch.zeros(E, dtype=torch.bfloat16)), dict(bias=torch.zeros(E - 1)),
+        dict(bias=torch.zeros(2 * E)[::2]), dict(ids=good["ids"].long()), dict(ids=good["ids"].float()),
+        dict(ids=torch.zeros((T, k - 1), dtype=torch.int32)), dict(ids=torch.zeros(T * k - 1, dtype=torch.int32)),
+        dict(w=good["w"].half()), dict(w=torch.zeros(T, k - 1)), dict(w=torch.zeros(k, T).t()))])
+    assert not reached
+    call()
+    call(bias=None)
+    call(logits=torch.zeros(T + 2, E), ids=torch.zeros(T * k, dtype=torch.int32), w=torch.zeros(T + 1, k))
+    call(logits=256, bias=512, ids=1024, w=2048)  # plain addresses
+    assert len(reached) == 4 and reached[3][0] == 256
