@@ -384,6 +384,11 @@ def moe_linear_forward(handle: int, x, x_scales, y, accumulate: bool = False, wo
         raise MoeError(MOE_EINVAL, f"x {tuple(x.shape)} and y {tuple(y.shape)}: [T, K] and [T, N] are needed")
     xp, xt, xld = _rows(x, "x", x.shape)
     yp, yt, yld = _rows(y, "y", y.shape)
+    if x_scales is not None and not isinstance(x_scales, int) and (
+            x_scales.shape != (x.shape[0], x.shape[1] // 32) or x_scales.element_size() != 1 or
+            not x_scales.is_contiguous()):
+        raise MoeError(MOE_EINVAL, f"x_scales: dense bytes [{x.shape[0]}, {x.shape[1] // 32}] are needed, not "
+                                   f"{x_scales.dtype} {tuple(x_scales.shape)}")
     status = lib.moe_linear_forward(handle, xp, xt, xld, _ptr(x_scales), x.shape[0], yp, yt, yld, bool(accumulate),
                                     _ptr(workspace), ws_bytes, _stream(stream))
     if status:

@@ -143,3 +143,37 @@ def test_route_wrapper_checks_shapes_and_types(b, monkeypatch):
     call(logits=torch.zeros(T + 2, E), ids=torch.zeros(T * k, dtype=torch.int32), w=torch.zeros(T + 1, k))
     call(logits=256, bias=512, ids=1024, w=2048)  # plain addresses
     assert len(reached) == 4 and reached[3][0] == 256
+
+
+def test_linear_wrapper_checks_the_scales_of_x(b, monkeypatch):
+    """E8M0 scales are bytes: a wider type of the same shape would be read as other numbers."""
+    import torch
+    T, K = 3, 64
+    reached = []
+    monkeypatch.setattr(b, "_stream", lambda s: None)
+    monkeypatch.setattr(b.lib, "moe_linear_forward", lambda *a: reached.append(a) or 0)
+    x, y = torch.zeros(T, K).to(torch.float8_e4m3fn), torch.zeros(T, 8)
+    good = torch.zeros((T, K // 32), dtype=torch.uint8)
+    _refused(b, [lambda sc=sc: b.moe_linear_forward(1, x, sc, y) for sc in (
+        good.float(), good.to(torch.float16), good.int(), good[:2], good[:, :1], torch.zeros((2, T), dtype=torch.uint8).t(),
+        torch.zeros((T, 4), dtype=torch.uint8)[:, ::2], good.view(-1))])
+    assert not reached
+    for sc in (good, good.view(torch.float8_e8m0fnu), None):
+        b.moe_linear_forward(1, x, sc, y)
+    assert len(reached) == 3
+
+
+def test_quant_linear_checks_the_scales_of_x(b, monkeypatch):
+    import torch
+    from mxfp4_routed_expert_router_gb300.linear import QuantLinear
+    reached = []
+    monkeypatch.setattr(b, "_stream", lambda s: None)
+    monkeypatch.setattr(b.lib, "moe_linear_forward", lambda *a: reached.append(a) or 0)
+    lin = QuantLinear.__new__(QuantLinear)
+    lin.handle, lin.N, lin.K, lin._no_ws, lin.device = None, 8, 64, 8, torch.device("cpu")
+    x, out = torch.zeros(3, 64).to(torch.float8_e4m3fn), torch.zeros(3, 8)
+    _refused(b, [lambda dt=dt: lin.forward(x, torch.zeros((3, 2), dtype=dt), out=out)
+                 for dt in (torch.float32, torch.float16, torch.int64)])
+    assert not reached
+    lin.forward(x, torch.zeros((3, 2), dtype=torch.uint8), out=out)
+    assert len(reached) == 1
