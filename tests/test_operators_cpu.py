@@ -177,3 +177,72 @@ def test_quant_linear_checks_the_scales_of_x(b, monkeypatch):
     assert not reached
     lin.forward(x, torch.zeros((3, 2), dtype=torch.uint8), out=out)
     assert len(reached) == 1
+
+
+class _Calls:
+    """Stands for the library: records which entry points a block reaches."""
+
+    def __init__(self, b, monkeypatch):
+        self.names = []
+        monkeypatch.setattr(b, "_stream", lambda s: None)
+        for name in ("moe_add_rmsnorm", "moe_linear_forward", "moe_forward_routed"):
+            monkeypatch.setattr(b.lib, name, lambda *a, name=name: self.names.append((name, a)) or 0)
+        real = b.lib.moe_route_grouped  # (argument checks only: no tokens reach a kernel)
+        monkeypatch.setattr(b.lib, "moe_route_grouped",
+                            lambda *a: self.names.append(("moe_route_grouped", a)) or (real(*a) if a[2] == 0 else 0))
+        monkeypatch.setattr(b.lib, "moe_workspace_bytes", lambda h, T, k: 4096 * T)
+
+
+def _linear(N, K):
+    import torch
+    from mxfp4_routed_expert_router_gb300.linear import QuantLinear
+    lin = QuantLinear.__new__(QuantLinear)
+    lin.handle, lin.N, lin.K, lin._no_ws, lin.device = None, N, K, 1 << 20, torch.device("cpu")
+    return lin
+
+
+def _layer(H, E, k):
+    import types
+
+    import torch
+    from mxfp4_routed_expert_router_gb300.layer import MoeLayer
+    layer = MoeLayer.__new__(MoeLayer)
+    layer.handle, layer._ws, layer.dense, layer.device = None, None, False, torch.device("cpu")
+    layer.cfg, layer.config = types.SimpleNamespace(hidden=H, n_experts=E, k=k), types.SimpleNamespace(k_max=k)
+    return layer
+
+
+def test_block_refuses_rows_that_the_experts_cannot_take(b, monkeypatch):
+    """The residual stream goes to the experts as dense FP32 rows: any other is refused before it is touched."""
+    import torch
+    from mxfp4_routed_expert_router_gb300.block import MoeBlock, Routing
+    calls = _Calls(b, monkeypatch)
+    T, H, E = 5, 64, 16
+    block = MoeBlock(_layer(H, E, 4), _linear(E, H), Routing(4, 4, 2))
+    attn = torch.zeros((T, H), dtype=torch.bfloat16)
+    calls.names.clear()
+    good = torch.zeros(T, H)
+    _refused(b, [lambda r=r: block.forward(attn, r) for r in (
+        good.bfloat16(), good.double(), torch.zeros(T, 2 * H)[:, :H], torch.zeros(2 * T, H)[::2], torch.zeros(H, T).t(),
+        torch.zeros(T, 32), torch.zeros(T, 96), torch.zeros(T * H))])
+    assert not calls.names
+    block.forward(attn, good)
+    assert [n for n, _ in calls.names] == ["moe_add_rmsnorm", "moe_linear_forward", "moe_route_grouped",
+                                           "moe_forward_routed"]
+
+
+def test_block_refuses_parts_that_do_not_fit(b, monkeypatch):
+    import torch
+    from mxfp4_routed_expert_router_gb300.block import MoeBlock, Routing
+    _Calls(b, monkeypatch)
+    H, E = 64, 16
+    good = dict(layer=_layer(H, E, 4), router=_linear(E, H), routing=Routing(4, 4, 2), bias=torch.zeros(E),
+                out_proj=_linear(H, 96), in_proj=_linear(200, H))
+    MoeBlock(**good)
+    dense = _layer(H, E, 4)
+    dense.dense = True
+    _refused(b, [lambda kw=kw: MoeBlock(**{**good, **kw}) for kw in (
+        dict(bias=torch.zeros(E, dtype=torch.bfloat16)), dict(bias=torch.zeros(E + 1)), dict(bias=torch.zeros(2 * E)[::2]),
+        dict(router=_linear(E, 96)), dict(out_proj=_linear(96, H)), dict(in_proj=_linear(200, 96)),
+        dict(routing=Routing(5, 4, 2)), dict(routing=Routing(4, 3, 2)), dict(routing=Routing(4, 4, 5)),
+        dict(routing=Routing(0, 4, 2)), dict(routing=Routing(4, 4, 2, score=7)), dict(layer=dense))])
