@@ -15,7 +15,7 @@ import torch
 
 from . import binding as B
 from .layer import MoeLayer
-from .linear import QuantLinear
+from .linear import QuantLinear, stream_workspace
 
 
 @dataclasses.dataclass(frozen=True)
@@ -85,4 +85,7 @@ class MoeBlock:
         w = torch.empty((T, r.k), dtype=torch.float32, device=dev)
         B.moe_route_grouped(logits, self.bias, T, E, r.k, r.n_groups, r.k_groups, r.score, r.group_score,
                             r.renormalize, r.scale, ids, w)
-        return self.layer.forward_routed(x, ids, w, out=residual, accumulate=True)
+        # the stream's workspace, or the captured graph's own, not the layer's: that one is shared by all streams and
+        # replaced under a graph when more tokens come
+        ws = stream_workspace(max(256, B.moe_workspace_bytes(self.layer.handle, T, r.k)), dev)
+        return self.layer.forward_routed(x, ids, w, out=residual, accumulate=True, workspace=ws)

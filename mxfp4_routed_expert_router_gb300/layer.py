@@ -96,13 +96,16 @@ class MoeLayer:
         return out
 
     def forward_routed(self, x: torch.Tensor, topk_ids: torch.Tensor, topk_w: torch.Tensor,
-                       out: Optional[torch.Tensor] = None, accumulate: bool = False, routing=None, stream=None):
+                       out: Optional[torch.Tensor] = None, accumulate: bool = False, routing=None, stream=None,
+                       workspace: Optional[torch.Tensor] = None):
         """The layer for routing given as expert ids (int32 [T, k]) and weights (float32 [T, k]).
-        An id of -1 is an empty slot (it adds nothing; its weight is not read)."""
+        An id of -1 is an empty slot (it adds nothing; its weight is not read).
+        workspace: bytes for this call, as ``moe_workspace_bytes`` asks for; without it the layer's own, which calls on
+        several streams must not share and which a call of more tokens replaces (also under a captured call)."""
         T, k = topk_ids.shape
         if out is None:
             out = torch.empty((T, self.cfg.hidden), dtype=torch.float32, device=self.device)
-        ws, n = self.workspace(T, k)
+        ws, n = self.workspace(T, k) if workspace is None else (workspace, workspace.numel())
         B.moe_forward_routed(self.handle, x, topk_ids, topk_w, T, k, out, accumulate, ws, n, routing, stream)
         return out
 

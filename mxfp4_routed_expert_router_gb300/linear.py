@@ -18,8 +18,8 @@ KEPT_WORKSPACE = 32 << 20  # largest workspace that stays with its stream
 
 
 class _Workspaces(threading.local):
-    """(device, stream) -> bytes that the layers' calls on that stream share; a thread has its own, as a call's
-    launches may lie between those of another thread's."""
+    """(device, stream) -> bytes that the calls on that stream share; a thread has its own, as a call's launches may
+    lie between those of another thread's."""
 
     def __init__(self):
         self.of = {}
@@ -28,7 +28,7 @@ class _Workspaces(threading.local):
 _workspaces = _Workspaces()
 
 
-def _workspace(n: int, device: torch.device) -> torch.Tensor:
+def stream_workspace(n: int, device: torch.device) -> torch.Tensor:
     """At least n bytes for a call on torch's current stream.  Up to KEPT_WORKSPACE they stay with the stream for its
     next call, which comes after this one there (an allocation between two launches costs as much as a launch).  A
     captured call gets bytes of its graph's own, as a replay may run on another stream."""
@@ -109,7 +109,7 @@ class QuantLinear:
     def _allocate(self, T: int, n: int, out):
         if out is None:
             out = torch.empty((T, self.N), dtype=torch.float32, device=self.device)
-        return out, _workspace(n, self.device) if n else None
+        return out, stream_workspace(n, self.device) if n else None
 
     def sync(self, stream=None):
         B.moe_linear_sync_status(self.handle, stream)

@@ -146,3 +146,52 @@ def test_operators_in_a_graph_beside_copies():
         assert torch.equal(b.project_in(r), q)
         b.forward(host_attn.cuda(), r)
         assert torch.equal(out, r) and torch.equal(b.project_in(r), q2) and not res.any()
+
+
+def test_block_graph_outlives_larger_calls():
+    """A graph captured with one token is replayed after calls and captures of many, and after other tensors have
+    taken whatever memory those gave back."""
+    cfg, b, *_ = _block(90)
+    attn = {T: torch.randn((T, A), device="cuda").bfloat16() for T in (1, 24, 300)}
+    res = {T: torch.randn((T, H), device="cuda") for T in attn}
+    want, graphs, bufs = {}, {}, {}
+    for T in attn:
+        want[T] = b.forward(attn[T], res[T].clone()).clone()
+        bufs[T] = res[T].clone()
+        graphs[T] = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graphs[T]):
+            b.forward(attn[T], bufs[T])
+    torch.cuda.synchronize()
+    others = [torch.full((n,), 7, dtype=torch.uint8, device="cuda") for n in (1 << 12, 1 << 18, 1 << 22, 1 << 24, 1 << 24)]
+    for T in attn:
+        bufs[T].copy_(res[T])
+        graphs[T].replay()
+        torch.cuda.synchronize()
+        assert torch.equal(bufs[T], want[T])
+    assert all((o == 7).all() for o in others)
+
+
+def test_block_on_streams_at_a_time():
+    """One block on three streams without an order between them: each gets what it gets alone."""
+    cfg, b, *_ = _block(91)
+    sizes = (3, 24, 70)
+    attn = [torch.randn((T, A), device="cuda").bfloat16() for T in sizes]
+    res = [torch.randn((T, H), device="cuda") for T in sizes]
+    want = []
+    for a, r in zip(attn, res):
+        one = r.clone()
+        for _ in range(4):
+            b.forward(a, one)
+        torch.cuda.synchronize()
+        want.append(one)
+    streams = [torch.cuda.Stream() for _ in sizes]
+    got = [r.clone() for r in res]
+    torch.cuda.synchronize()
+    for i in range(4):
+        for s, a, g in zip(streams, attn, got):
+            with torch.cuda.stream(s):
+                b.forward(a, g)
+    torch.cuda.synchronize()
+    b.layer.sync()
+    for g, w in zip(got, want):
+        assert torch.equal(g, w)

@@ -183,8 +183,11 @@ class _Calls:
     """Stands for the library: records which entry points a block reaches."""
 
     def __init__(self, b, monkeypatch):
+        import torch
         self.names = []
         monkeypatch.setattr(b, "_stream", lambda s: None)
+        monkeypatch.setattr(b, "_current_stream", lambda: 11)
+        monkeypatch.setattr(torch.cuda, "is_current_stream_capturing", lambda: False)
         for name in ("moe_add_rmsnorm", "moe_linear_forward", "moe_forward_routed"):
             monkeypatch.setattr(b.lib, name, lambda *a, name=name: self.names.append((name, a)) or 0)
         real = b.lib.moe_route_grouped  # (argument checks only: no tokens reach a kernel)
@@ -246,3 +249,45 @@ def test_block_refuses_parts_that_do_not_fit(b, monkeypatch):
         dict(router=_linear(E, 96)), dict(out_proj=_linear(96, H)), dict(in_proj=_linear(200, 96)),
         dict(routing=Routing(5, 4, 2)), dict(routing=Routing(4, 3, 2)), dict(routing=Routing(4, 4, 5)),
         dict(routing=Routing(0, 4, 2)), dict(routing=Routing(4, 4, 2, score=7)), dict(layer=dense))])
+
+
+def test_block_workspaces_of_streams_and_captures(b, monkeypatch):
+    """The experts' workspace is the stream's, or the captured call's own: never one that calls on two streams share,
+    nor one that a later call of more tokens frees while a graph still holds its address."""
+    import gc
+
+    import torch
+    from mxfp4_routed_expert_router_gb300 import linear
+    from mxfp4_routed_expert_router_gb300.block import MoeBlock, Routing
+    calls = _Calls(b, monkeypatch)
+    now = dict(stream=11, capturing=False)
+    monkeypatch.setattr(b, "_current_stream", lambda: now["stream"])
+    monkeypatch.setattr(torch.cuda, "is_current_stream_capturing", lambda: now["capturing"])
+    monkeypatch.setattr(linear, "_workspaces", linear._Workspaces())
+    H, E = 64, 16
+    block = MoeBlock(_layer(H, E, 4), _linear(E, H), Routing(4, 4, 2))
+
+    kept = []  # captured calls' memory belongs to their graphs: here every tensor made while capturing lives on
+    empty = torch.empty
+    monkeypatch.setattr(linear.torch, "empty",
+                        lambda *a, **kw: (kept.append(empty(*a, **kw)) or kept[-1]) if now["capturing"] else empty(*a, **kw))
+
+    def ran(T, stream, capturing=False):
+        now.update(stream=stream, capturing=capturing)
+        calls.names.clear()
+        block.forward(torch.zeros((T, H), dtype=torch.bfloat16), torch.zeros(T, H))
+        at, size = [a for n, a in calls.names if n == "moe_forward_routed"][0][8:10]
+        assert at and size >= 4096 * T
+        return at, size
+
+    one, other = ran(3, 11), ran(3, 22)
+    assert one[0] != other[0], "two streams share the experts' workspace"
+    assert ran(2, 11)[0] == one[0], "the stream's calls share it"
+    graph = ran(1, 11, capturing=True)
+    mine = [t for t in kept if t.data_ptr() == graph[0]]
+    assert mine and graph[0] not in (one[0], other[0]), "a captured call has bytes of its graph's own"
+    bigger = ran(300, 11)
+    gc.collect()
+    assert bigger[0] != graph[0] and ran(3, 22) == other
+    assert block.layer._ws is None
+    calls.names.clear()
