@@ -70,7 +70,7 @@ static_assert(DONE >= B_MAX, "see linear_tc_kernel");  // (B_MAX slots of one sl
 constexpr int BAR_OFF = RING_BYTES;
 constexpr int N_BARS = B_MAX + 2 * W_MAX + A_MAX + DONE + 1;
 constexpr int MISC_OFF = BAR_OFF + N_BARS * 8;
-constexpr int TSC_OFF = MISC_OFF + 16;                   // the tile's token scales
+constexpr int TSC_OFF = MISC_OFF + 16;                   // exponents of the tile's tokens
 constexpr int SMEM_BYTES = TSC_OFF + NMAX * 4 + 1024;    // + alignment slack
 static_assert(2 * (SMEM_BYTES + 1024) <= 228 * 1024, "two CTAs per SM");
 static_assert(NMAX * TILE_ROWS * 4 <= RING_BYTES, "a partial tile fits in the rings");
@@ -78,7 +78,7 @@ static_assert(NMAX * TILE_ROWS * 4 <= RING_BYTES, "a partial tile fits in the ri
 struct Args {
     const uint8_t *w;
     const uint8_t *row_base;  // FP16 operands: power of two (+ 127) of each row
-    const float *xscale;      // FP16 operands: power of two of each token
+    const float *xscale;      // FP16 operands: power of two of each token (2^-126 .. 2^114)
     int N, T, kchunks;
     int tile_tokens;          // tokens of a tile (a multiple of 16, at most NMAX), rows of a TMA box of B
     int ttiles;
@@ -208,6 +208,16 @@ __device__ __forceinline__ void store_y(const Args &a, long long at, float v)
     }
 }
 
+// v * 2^e for a sum |v| < 2^47 of the MMAs and e = the row's exponent + the token's, -253 .. 241: neither power of two
+// may be applied alone (v * 2^row or their product can leave FP32's range where the result does not), so e is
+// split into one factor within the range and the rest of the same sign, which comes first.
+__device__ __forceinline__ float scale_pow2(float v, int e)
+{
+    e = max(e, -252);  // (v * 2^e is 0 there already)
+    const int c = min(max(e, -126), 127);
+    return v * __int_as_float((127 + e - c) << 23) * __int_as_float((127 + c) << 23);
+}
+
 // This CTA's tile and its rank in the cluster.  Read afresh where they are needed
 // again after the loops, so that no register holds them meanwhile.
 struct Tile {
@@ -247,7 +257,7 @@ __global__ void __launch_bounds__(THREADS, 2)
     uint64_t *w_empty = w_full + W_MAX, *a_full = w_empty + W_MAX, *done = a_full + A_MAX, *acc_full = done + DONE;
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + MISC_OFF);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + MISC_OFF + 4);
-    float *tsc = reinterpret_cast<float *>(smem + TSC_OFF);
+    int *tsc = reinterpret_cast<int *>(smem + TSC_OFF);  // exponents of the tile's tokens
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const Tile at0 = tile_here(a);
@@ -521,14 +531,13 @@ __global__ void __launch_bounds__(THREADS, 2)
         const uint32_t csize = at1.csize;
         if (OP != LIN_BF16) {  // (every warp writes the same values and reads its own)
             for (int i = lane; i < nvalid; i += 32)
-                tsc[i] = __ldcg(a.xscale + tok0 + i);
+                tsc[i] = (__float_as_int(__ldcg(a.xscale + tok0 + i)) >> 23) - 127;
             __syncwarp();
         }
         if (ok && mbar_wait_sleep_warp(acc_full, 0, abort_flag, a.err, lane)) {
             fence_after();
             const int n = rt * TILE_ROWS + r;
-            const float wsc =
-                OP == LIN_BF16 ? 1.f : ldexpf(1.f, (int)__ldg(a.row_base + rt * TILE_ROWS + r) - 127);
+            const int we = OP == LIN_BF16 ? 0 : (int)__ldg(a.row_base + rt * TILE_ROWS + r) - 127;
             float *part = reinterpret_cast<float *>(smem) + r;  // [token][128]: the rings are free
             for (int c = 16 * grp; c < n_mma; c += 16 * DEC_GROUPS) {
                 float v[16];
@@ -536,13 +545,13 @@ __global__ void __launch_bounds__(THREADS, 2)
                 if (csize > 1) {
 #pragma unroll
                     for (int j = 0; j < 16; ++j)  // (columns past nvalid: inside the tile's room, not read)
-                        part[(c + j) * TILE_ROWS] = v[j] * wsc;
+                        part[(c + j) * TILE_ROWS] = v[j];
                 } else if (n < a.N) {
                     const long long at = (long long)(tok0 + c) * a.y_ld + n;
                     if (OP != LIN_BF16)
 #pragma unroll
                         for (int j = 0; j < 16; ++j)
-                            v[j] *= wsc * tsc[c + j];
+                            v[j] = scale_pow2(v[j], we + tsc[c + j]);
                     if (a.accumulate) {  // all loads before the first store
                         float old[16];
 #pragma unroll
@@ -592,12 +601,16 @@ __global__ void __launch_bounds__(THREADS, 2)
                 for (uint32_t rk = 0; rk < 8; ++rk)
                     if (rk < csize)
                         o[0] += f[rk].x, o[1] += f[rk].y, o[2] += f[rk].z, o[3] += f[rk].w;
-                const float ts = OP == LIN_BF16 ? 1.f : tsc[t];
+                // row exponents (+ 127) of the lane's four rows
+                const uint32_t rb4 = OP == LIN_BF16 ? 0u : __ldg(reinterpret_cast<const uint32_t *>(a.row_base) +
+                                                                 rt * (TILE_ROWS / 4) + lane);
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
                     const int n = rt * TILE_ROWS + lane * 4 + j;
+                    if (OP != LIN_BF16)
+                        o[j] = scale_pow2(o[j], (int)(rb4 >> (8 * j) & 255u) - 127 + tsc[t]);
                     if (n < a.N)
-                        store_y(a, (long long)(tok0 + t) * a.y_ld + n, o[j] * ts);
+                        store_y(a, (long long)(tok0 + t) * a.y_ld + n, o[j]);
                 }
             }
         }

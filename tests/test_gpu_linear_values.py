@@ -10,7 +10,7 @@ import pytest
 import torch
 
 import test_gpu_linear as base
-from test_gpu_linear import FMTS, Weight, _x
+from test_gpu_linear import Weight
 
 pytestmark = pytest.mark.gpu
 
@@ -64,3 +64,67 @@ def test_values_are_written_and_numbers(test, args, monkeypatch):
     monkeypatch.setattr(base, "_check", close)
     monkeypatch.setattr(base, "_mods", lambda: (B, Filled))
     test(**args)
+
+
+def mx_weight(codes, scales):
+    W = Weight.__new__(Weight)
+    W.fmt, (W.N, W.K) = "mxfp4", (codes.shape[0], codes.shape[1] * 2)
+    W.args = (torch.from_numpy(codes).cuda(), torch.from_numpy(scales).cuda())
+    W.w = base.E2M1[base._nibbles(codes)] * np.repeat(2.0 ** (scales.astype(np.float64) - 127), 32, 1)
+    W.terms = np.abs(W.w)
+    return W
+
+
+def same_rows(T, row):
+    """T equal tokens, as values and as BF16 (which holds them exactly)."""
+    x = np.tile(row, (T, 1))
+    t = torch.from_numpy(x).to(torch.bfloat16)
+    assert np.array_equal(t.double().numpy(), x)
+    return x, t.cuda()
+
+
+@pytest.mark.parametrize("T,N", [(1, 64), (8, 64), (9, 64), (200, 10240)])
+def test_mxfp4_powers_of_row_and_token_leave_the_range(T, N):
+    """The row's power of two times the token's lies outside FP32's range; the sum times both does not.  With one tile
+    per CTA and with K split over a cluster."""
+    _, Linear = base._mods()
+    K = 1024
+    W = mx_weight(np.full((N, K // 2), 0x77, np.uint8), np.full((N, K // 32), 37, np.uint8))  # 6 * 2^-90 each
+    lin = Linear("mxfp4", *W.args)
+    x, xd = same_rows(T, np.full(K, 2.0 ** -46))
+    close(lin.forward(xd, out=nan_out(lin, T)), x, W)
+    half = nan_out(lin, T, torch.bfloat16)
+    close(lin.forward(xd, out=half), x, W, out_bf16=True)
+    lin.free()
+    # the token's largest value meets weights of zero only; a row of zeros stays zero
+    codes = np.full((N, K // 2), 0x11, np.uint8)  # 0.5 * 2^100
+    codes[:, 0] = 0x10
+    codes[N // 2] = 0
+    W = mx_weight(codes, np.full((N, K // 32), 227, np.uint8))
+    lin = Linear("mxfp4", *W.args)
+    row = np.full(K, 2.0 ** 15)
+    row[0] = 2.0 ** 43
+    x, xd = same_rows(T, row)
+    got = lin.forward(xd, out=nan_out(lin, T))
+    close(got, x, W)
+    assert torch.all(got[:, N // 2] == 0)
+    lin.sync()
+    lin.free()
+
+
+def check_scales(T, lo, hi, p):
+    _, Linear = base._mods()
+    W = Weight("mxfp4", 70, 512, seed=hi, e_lo=lo, e_hi=hi)
+    lin = Linear("mxfp4", *W.args)
+    t = torch.from_numpy(np.random.default_rng(hi).standard_normal((T, 512)).astype(np.float32)).to(torch.bfloat16)
+    xs = (t.double() * 2.0 ** p).to(torch.bfloat16)
+    close(lin.forward(xs.cuda(), out=nan_out(lin, T)), xs.double().numpy(), W)
+    lin.sync()
+    lin.free()
+
+
+@pytest.mark.parametrize("T", [9, 40, 200])
+@pytest.mark.parametrize("lo,hi,p", [(230, 240, -60), (245, 254, -60), (14, 20, 60), (0, 3, 100)])
+def test_mxfp4_scales_at_the_ends(T, lo, hi, p):
+    """Block scales far from one, undone by x: neither may leave FP32's range before the other is applied."""
+    check_scales(T, lo, hi, p)
