@@ -414,7 +414,7 @@ __global__ void row_base_i4_kernel(int gate_up, SrcMat gate, SrcMat up, uint8_t 
 // Row bases of a TILE_F16 store: one thread per tile row; rows past the
 // logical end get 127 (their codes are 0).
 __global__ void row_base_kernel(int gate_up, SrcMat gate, SrcMat up, uint8_t *dst, int row_tiles, int logical_rows,
-                                int K, int *wide)
+                                int K, int *wide, int *far)
 {
     // one warp per tile row; lanes read the row's scale bytes side by side
     const long long idx = (long long)blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5);
@@ -444,11 +444,13 @@ __global__ void row_base_kernel(int gate_up, SrcMat gate, SrcMat up, uint8_t *ds
         dst[idx] = (uint8_t)mx;
         if (mx - mn > TILE_F16_MAX_SPREAD)
             atomicOr(wide, 1);
+        if (far && (mx > LINEAR_STREAM_MAX_E8M0 || mn < LINEAR_STREAM_MIN_E8M0))
+            atomicOr(far, 1);
     }
 }
 
 cudaError_t launch_row_base(int fmt, bool gate_up, const SrcMat &gate, const SrcMat &up, const WeightStore &ws,
-                            int group, int I, int H, int *wide, cudaStream_t st)
+                            int group, int I, int H, int *wide, cudaStream_t st, int *far)
 {
     const int logical_rows = gate_up ? I : H;
     const long long total = (long long)ws.row_tiles * TILE_ROWS;
@@ -458,7 +460,7 @@ cudaError_t launch_row_base(int fmt, bool gate_up, const SrcMat &gate, const Src
     else
         row_base_kernel<<<(unsigned)((total + 7) / 8), 256, 0, st>>>(
             gate_up ? 1 : 0, gate, up, ws.row_base + (size_t)group * total, ws.row_tiles, logical_rows, ws.cols,
-            wide);
+            wide, far);
     return cudaGetLastError();
 }
 

@@ -38,8 +38,10 @@ struct MoeLinear {
     WeightStore frag;         // FRAG / FRAG_F16 layout (few tokens)
     WeightStore tile;         // TILE, TILE_F16 or TILE_I4 layout (the tcgen05 GEMM)
     int op = LIN_BF16;        // the GEMM's operands
+    bool stream = true;       // few tokens run on the weight stream (no MXFP4 scale outside its range)
     int *err_host = nullptr;  // mapped pinned host memory: [0] device error flag, [1] a rejected scale
-                              // at load, [2] an MXFP4 row whose exponents span too widely for FP16 operands
+                              // at load, [2] an MXFP4 row whose exponents span too widely for FP16 operands,
+                              // [3] a scale outside the weight stream's range
     int *err_dev = nullptr;
 };
 
@@ -774,6 +776,8 @@ MoeStatus bad_cuda(const char *what, cudaError_t e)
     return bad(MOE_ECUDA, msg);
 }
 
+bool on_stream(const MoeLinear *l, int T) { return T <= LINEAR_STREAM_MAX_T && l->stream; }
+
 void destroy(MoeLinear *l)
 {
     if (l->frag.base)
@@ -856,7 +860,7 @@ MoeStatus moe_linear_load(int N, int K, MoeWeightFormat wfmt, const MoeMx *w, vo
                         fmt == FMT_BF16 ? (long long)K * 2 : K / 2, K / 32,
                         (const uint8_t *)(fmt == FMT_INT4 ? w->zeros : nullptr)};
     if ((fmt != FMT_BF16 &&
-         (e = launch_row_base(fmt, false, src, src, t, 0, K, N, &l->err_dev[2], st)) != cudaSuccess) ||
+         (e = launch_row_base(fmt, false, src, src, t, 0, K, N, &l->err_dev[2], st, &l->err_dev[3])) != cudaSuccess) ||
         (e = cudaMemsetAsync(f.base + f.group_bytes, 0, f.chunk_bytes, st)) != cudaSuccess ||
         (e = launch_repack(fmt, fmt == FMT_BF16 ? LAYOUT_FRAG : LAYOUT_FRAG_F16, false, src, src, f, 0, K, N,
                            &l->err_dev[1], st)) != cudaSuccess ||
@@ -864,6 +868,7 @@ MoeStatus moe_linear_load(int N, int K, MoeWeightFormat wfmt, const MoeMx *w, vo
         destroy(l);
         return bad_cuda("repack", e);
     }
+    l->stream = *(volatile int *)&l->err_host[3] == 0;
     int layout = LAYOUT_TILE;
     if (fmt == FMT_INT4) {
         l->op = LIN_I4;
@@ -888,7 +893,7 @@ MoeStatus moe_linear_load(int N, int K, MoeWeightFormat wfmt, const MoeMx *w, vo
 
 size_t moe_linear_workspace_bytes(const MoeLinear *l, int T)
 {
-    return !l || T <= LINEAR_STREAM_MAX_T ? 0 : linear_gemm_workspace(l->K, T);
+    return !l || T <= 0 || on_stream(l, T) ? 0 : linear_gemm_workspace(l->K, T);
 }
 
 MoeStatus moe_linear_forward(MoeLinear *l, const void *x, MoeRowType x_type, long long x_ld, const void *x_scales,
@@ -928,7 +933,7 @@ MoeStatus moe_linear_forward(MoeLinear *l, const void *x, MoeRowType x_type, lon
     if ((uintptr_t)workspace % 256)
         return bad(MOE_EWORKSPACE, "moe_linear_forward: the workspace must be 256-byte aligned");
     cudaStream_t st = (cudaStream_t)cuda_stream;
-    if (T > LINEAR_STREAM_MAX_T) {
+    if (!on_stream(l, T)) {
         if (!workspace)
             return bad(MOE_EWORKSPACE, "moe_linear_forward: NULL workspace");
         LinearGemm g{};

@@ -218,9 +218,18 @@ cudaError_t launch_gather_rows(const Plan &p, const uint16_t *x, cudaStream_t st
 // row bases of a TILE_F16 store for one group: for every tile row, the
 // largest E8M0 exponent over the row's K; a row whose exponents span more than
 // TILE_F16_MAX_SPREAD sets *wide.  With fmt FMT_INT4, the TILE_I4 row base
-// (see above; wide is not used)
+// (see above; wide is not used).  For the linear layers, far (NULL: not asked
+// for) is set by an E8M0 byte outside LINEAR_STREAM_MIN_E8M0 ..
+// LINEAR_STREAM_MAX_E8M0.
 cudaError_t launch_row_base(int fmt, bool gate_up, const SrcMat &gate, const SrcMat &up, const WeightStore &ws,
-                            int group, int I, int H, int *wide, cudaStream_t st);
+                            int group, int I, int H, int *wide, cudaStream_t st, int *far = nullptr);
+
+// The weight stream of linear.cu applies a block's scale 2^s to a sum in units of
+// the token's power of two, before that power.  FP16 x lies below 2^15 and is a
+// multiple of 2^-24, a code is 0 or 0.5 to 6: a block's sum lies below 2^23 and is a
+// multiple of 2^-25, a step's eight blocks with their scales lie below 2^(26 + s).
+// With -100 <= s <= 100 neither overflows nor loses a bit to FP32's subnormals.
+constexpr int LINEAR_STREAM_MIN_E8M0 = 27, LINEAR_STREAM_MAX_E8M0 = 227;
 
 // For the h scales of the tcgen05 path with FP16 operands: out[group] = an
 // order-preserving integer key of max_n log2(|w_g,n| |w_u,n|) over the

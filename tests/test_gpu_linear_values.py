@@ -128,3 +128,47 @@ def check_scales(T, lo, hi, p):
 def test_mxfp4_scales_at_the_ends(T, lo, hi, p):
     """Block scales far from one, undone by x: neither may leave FP32's range before the other is applied."""
     check_scales(T, lo, hi, p)
+
+
+@pytest.mark.parametrize("T", [1, 2, 3, 4, 8, 9, 200])
+@pytest.mark.parametrize("lo,hi,p", [(230, 240, -60), (245, 254, -60), (0, 250, -30), (14, 20, 60), (0, 3, 100),
+                                     (27, 227, 0), (26, 60, 0), (200, 228, -30)])
+def test_mxfp4_scales_at_the_ends_few_tokens(T, lo, hi, p):
+    """The same for few tokens, and with scales from end to end of the format in a row."""
+    check_scales(T, lo, hi, p)
+
+
+@pytest.mark.parametrize("T", [1, 5, 8])
+def test_mxfp4_scales_at_the_ends_rows_and_outputs(T):
+    """Few tokens with scales that the weight stream does not take: both types of x and y, strides, accumulation, a
+    graph; the workspace that the call then needs is asked for."""
+    B, Linear = base._mods()
+    N, K = 203, 608
+    W = Weight("mxfp4", N, K, seed=T, e_lo=228, e_hi=240)
+    lin = Linear("mxfp4", *W.args)
+    rng = np.random.default_rng(T)
+    codes = torch.from_numpy(rng.standard_normal((T, K + 32)).astype(np.float32)).to(torch.float8_e4m3fn)
+    sc = rng.integers(20, 26, (T, K // 32), dtype=np.uint8)
+    v = codes[:, :K].float().numpy().astype(np.float64) * np.repeat(2.0 ** (sc.astype(np.float64) - 127), 32, 1)
+    t = torch.from_numpy(rng.standard_normal((T, K + 32)) * 2.0 ** -104).to(torch.bfloat16)
+    for x, xd, xs in ((v, codes.cuda()[:, :K], torch.from_numpy(sc).cuda()), (t.double().numpy()[:, :K], t.cuda()[:, :K], None)):
+        buf = torch.full((T, N + 3), float("nan"), device="cuda")
+        close(lin.forward(xd, xs, out=buf[:, :N]), x, W)
+        assert torch.isnan(buf[:, N:]).all()
+        close(lin.forward(xd, xs, out=nan_out(lin, T, torch.bfloat16)), x, W, out_bf16=True)
+        acc = torch.randn((T, N), device="cuda")
+        before = acc.cpu().numpy().astype(np.float64)
+        close(lin.forward(xd, xs, out=acc, accumulate=True), x, W, base=before)
+        out = nan_out(lin, T)
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            lin.forward(xd, xs, out=out)
+        g.replay()
+        torch.cuda.synchronize()
+        close(out, x, W)
+    assert B.moe_linear_workspace_bytes(lin.handle, T) > 0 and B.moe_linear_workspace_bytes(lin.handle, 0) == 0
+    with pytest.raises(B.MoeError) as e:
+        B.moe_linear_forward(lin.handle, t.cuda()[:, :K], None, out)
+    assert e.value.status == B.MOE_EWORKSPACE
+    lin.sync()
+    lin.free()
