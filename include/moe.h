@@ -478,15 +478,17 @@ typedef struct MoeLinear MoeLinear;
 MoeStatus moe_linear_load(int N, int K, MoeWeightFormat fmt, const MoeMx *w, void *cuda_stream, MoeLinear **out);
 
 /* Bytes of device workspace moe_linear_forward needs for T tokens (0 for few
- * tokens unless an MXFP4 scale lies outside 2^-100 .. 2^100, for a NULL handle
- * and for T <= 0). */
+ * tokens unless an MXFP4 scale lies outside 2^-100 .. 2^100, for INT4
+ * weights that run in slices of few, for a NULL handle and for T <= 0). */
 size_t moe_linear_workspace_bytes(const MoeLinear *l, int T);
 
 /* y[t][n] = sum_k x[t][k] w[n][k] for T tokens.  Products accumulate in FP32;
  * 4-bit weights decode exactly, and x keeps its value as long as it is within
  * 2^-24 of the largest |x| of its token.  MXFP8 values of 2^128 and more count as
  * infinite; so may MXFP4 weights of 2^128 and more (scale bytes 253 and 254) where
- * the scales of a row span more than 2^23.
+ * the scales of a row span more than 2^23.  INT4 weights with a group scale of
+ * 4096 or more and one with bits below 2^-20 in one row run 8 tokens at a time
+ * (slower for many tokens, as exact).
  *  x         BF16 or MXFP8 rows of K values (x_scales [T][K/32] for MXFP8, else NULL)
  *  y         F32 or BF16 rows of N values; F32 rows are overwritten, or added
  *            to when accumulate != 0 (BF16 rows cannot accumulate)

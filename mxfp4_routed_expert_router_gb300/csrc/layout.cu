@@ -387,7 +387,7 @@ __global__ void repack_tile_i4_kernel(int gate_up, SrcMat gate, SrcMat up, uint8
 // floor(log2 max|s|) - TILE_I4_BASE_SHIFT over the row's nonzero FP16 scales
 // (127 for a row with none, or past the logical end).
 __global__ void row_base_i4_kernel(int gate_up, SrcMat gate, SrcMat up, uint8_t *dst, int row_tiles, int logical_rows,
-                                   int K)
+                                   int K, int *far)
 {
     const long long idx = (long long)blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5);
     const int lane = threadIdx.x & 31;
@@ -397,8 +397,9 @@ __global__ void row_base_i4_kernel(int gate_up, SrcMat gate, SrcMat up, uint8_t 
     int srow;
     const SrcMat *src = tile_row_source(gate_up, &gate, &up, tile, r, logical_rows, &srow);
     int mx = -1000;
+    const uint16_t *sc = nullptr;
     if (srow >= 0) {
-        const uint16_t *sc = reinterpret_cast<const uint16_t *>(src->scales) + (long long)srow * src->scale_stride;
+        sc = reinterpret_cast<const uint16_t *>(src->scales) + (long long)srow * src->scale_stride;
         for (int b = lane; b < K / 32; b += 32) {
             const float s = fabsf(__half2float(__ushort_as_half(sc[b])));
             if (s > 0.f && s <= 65504.f)
@@ -409,6 +410,16 @@ __global__ void row_base_i4_kernel(int gate_up, SrcMat gate, SrcMat up, uint8_t 
         mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, o));
     if (lane == 0)
         dst[idx] = (uint8_t)(mx == -1000 ? 127 : mx - TILE_I4_BASE_SHIFT + 127);
+    if (far && mx > TILE_I4_BASE_SHIFT) {  // (a base below one makes the scales larger: no bit is lost)
+        const float down = ldexpf(1.f, TILE_I4_BASE_SHIFT - mx);
+        bool lost = false;
+        for (int b = lane; b < K / 32; b += 32) {
+            const float s = __half2float(__ushort_as_half(sc[b])) * down;
+            lost = lost || __half2float(__float2half_rn(s)) != s;  // (Inf and NaN are refused elsewhere)
+        }
+        if (lost)
+            atomicOr(far, 1);
+    }
 }
 
 // Row bases of a TILE_F16 store: one thread per tile row; rows past the
@@ -456,7 +467,8 @@ cudaError_t launch_row_base(int fmt, bool gate_up, const SrcMat &gate, const Src
     const long long total = (long long)ws.row_tiles * TILE_ROWS;
     if (fmt == FMT_INT4)
         row_base_i4_kernel<<<(unsigned)((total + 7) / 8), 256, 0, st>>>(
-            gate_up ? 1 : 0, gate, up, ws.row_base + (size_t)group * total, ws.row_tiles, logical_rows, ws.cols);
+            gate_up ? 1 : 0, gate, up, ws.row_base + (size_t)group * total, ws.row_tiles, logical_rows, ws.cols,
+            far);
     else
         row_base_kernel<<<(unsigned)((total + 7) / 8), 256, 0, st>>>(
             gate_up ? 1 : 0, gate, up, ws.row_base + (size_t)group * total, ws.row_tiles, logical_rows, ws.cols,

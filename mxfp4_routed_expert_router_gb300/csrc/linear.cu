@@ -39,9 +39,10 @@ struct MoeLinear {
     WeightStore tile;         // TILE, TILE_F16 or TILE_I4 layout (the tcgen05 GEMM)
     int op = LIN_BF16;        // the GEMM's operands
     bool stream = true;       // few tokens run on the weight stream (no MXFP4 scale outside its range)
+    bool gemm = true;         // more run on the GEMM (INT4: every scale exact relative to its row's base)
     int *err_host = nullptr;  // mapped pinned host memory: [0] device error flag, [1] a rejected scale
                               // at load, [2] an MXFP4 row whose exponents span too widely for FP16 operands,
-                              // [3] a scale outside the weight stream's range
+                              // [3] a scale that one of the two kernels does not take (launch_row_base)
     int *err_dev = nullptr;
 };
 
@@ -776,7 +777,8 @@ MoeStatus bad_cuda(const char *what, cudaError_t e)
     return bad(MOE_ECUDA, msg);
 }
 
-bool on_stream(const MoeLinear *l, int T) { return T <= LINEAR_STREAM_MAX_T && l->stream; }
+// Whether T tokens run on the weight stream: few of them, or, without the GEMM, any number in slices of few.
+bool on_stream(const MoeLinear *l, int T) { return (T <= LINEAR_STREAM_MAX_T && l->stream) || !l->gemm; }
 
 void destroy(MoeLinear *l)
 {
@@ -868,7 +870,8 @@ MoeStatus moe_linear_load(int N, int K, MoeWeightFormat wfmt, const MoeMx *w, vo
         destroy(l);
         return bad_cuda("repack", e);
     }
-    l->stream = *(volatile int *)&l->err_host[3] == 0;
+    if (*(volatile int *)&l->err_host[3])
+        (fmt == FMT_INT4 ? l->gemm : l->stream) = false;
     int layout = LAYOUT_TILE;
     if (fmt == FMT_INT4) {
         l->op = LIN_I4;
@@ -961,20 +964,22 @@ MoeStatus moe_linear_forward(MoeLinear *l, const void *x, MoeRowType x_type, lon
     a.N = l->N;
     a.K = l->K;
     a.kchunks = l->frag.kchunks;
-    a.x = x;
-    a.xscales = (const uint8_t *)x_scales;
     a.x_ld = x_ld;
     a.x_mx = x_type == MOE_ROWS_MXFP8;
-    a.T = T;
-    a.y = y;
     a.y_ld = y_ld;
     a.y_f32 = y_type == MOE_ROWS_F32;
     a.accumulate = accumulate != 0;
-    const cudaError_t e = l->fmt == FMT_MXFP4  ? launch_tokens<FMT_MXFP4>(a, st)
-                          : l->fmt == FMT_INT4 ? launch_tokens<FMT_INT4>(a, st)
-                                               : launch_tokens<FMT_BF16>(a, st);
-    if (e != cudaSuccess)
-        return bad_cuda("linear layer launch", e);
+    for (int t = 0; t < T; t += LINEAR_STREAM_MAX_T) {  // (once, but for INT4 weights that the GEMM does not take)
+        a.T = T - t < LINEAR_STREAM_MAX_T ? T - t : LINEAR_STREAM_MAX_T;
+        a.x = (const uint8_t *)x + t * x_ld * (a.x_mx ? 1 : 2);
+        a.xscales = a.x_mx ? (const uint8_t *)x_scales + (long long)t * (l->K / 32) : nullptr;
+        a.y = (uint8_t *)y + t * y_ld * (a.y_f32 ? 4 : 2);
+        const cudaError_t e = l->fmt == FMT_MXFP4  ? launch_tokens<FMT_MXFP4>(a, st)
+                              : l->fmt == FMT_INT4 ? launch_tokens<FMT_INT4>(a, st)
+                                                   : launch_tokens<FMT_BF16>(a, st);
+        if (e != cudaSuccess)
+            return bad_cuda("linear layer launch", e);
+    }
     return MOE_OK;
 }
 

@@ -7,7 +7,9 @@ namespace moe {
 
 // A call of at most this many tokens streams the FRAG store through the
 // warp-level MMAs (linear.cu); more tokens, and MXFP4 weights with scales outside
-// LINEAR_STREAM_MIN_E8M0 .. MAX_E8M0, run on the tcgen05 GEMM (linear_tc.cu).  Eight tokens fill the columns of a warp-level MMA.  Measured
+// LINEAR_STREAM_MIN_E8M0 .. MAX_E8M0, run on the tcgen05 GEMM (linear_tc.cu).  INT4
+// weights whose scales the GEMM's FP16 operands do not hold run here in slices of
+// this many tokens, each of which reads the weights once.  Eight tokens fill the columns of a warp-level MMA.  Measured
 // (device time in us, 8 tokens here and 9 in the GEMM): MXFP4 7168 x 7168 10.8 and
 // 12.2, 7168 x 18432 19.9 and 26.5; group-32 INT4 7168 x 18432 24.8 and 45.3; BF16
 // 256 x 7168 4.0 and 6.3, 2048 x 7168 7.9 and 7.3, 7168 x 7168 18.9 and 18.8.  Sixteen

@@ -471,7 +471,8 @@ __global__ void __launch_bounds__(THREADS, 2)
                 auto decode = [&](int b, uint32_t *hi, uint32_t *rest) {
                     const uint32_t w[4] = {code[b].x, code[b].y, code[b].z, code[b].w};
                     if (OP == LIN_I4) {
-                        // relative to the row's base (the scale then lies below 2^12)
+                        // relative to the row's base (the scale then lies below 2^12, and is exact:
+                        // launch_row_base keeps weights where one is not away from this kernel)
                         const float sf = __half2float(__ushort_as_half((unsigned short)(sc[b] & 0xFFFFu))) *
                                          __int_as_float((254 - rb) << 23);
                         const uint32_t s2 = (uint32_t)__half_as_ushort(__float2half_rn(sf)) * 0x10001u;

@@ -220,7 +220,8 @@ cudaError_t launch_gather_rows(const Plan &p, const uint16_t *x, cudaStream_t st
 // TILE_F16_MAX_SPREAD sets *wide.  With fmt FMT_INT4, the TILE_I4 row base
 // (see above; wide is not used).  For the linear layers, far (NULL: not asked
 // for) is set by an E8M0 byte outside LINEAR_STREAM_MIN_E8M0 ..
-// LINEAR_STREAM_MAX_E8M0.
+// LINEAR_STREAM_MAX_E8M0, or by an INT4 scale that FP16 does not hold relative to
+// its row's base (a largest scale of 2^12 or more beside one with bits below 2^-20).
 cudaError_t launch_row_base(int fmt, bool gate_up, const SrcMat &gate, const SrcMat &up, const WeightStore &ws,
                             int group, int I, int H, int *wide, cudaStream_t st, int *far = nullptr);
 

@@ -10,7 +10,7 @@ import pytest
 import torch
 
 import test_gpu_linear as base
-from test_gpu_linear import Weight
+from test_gpu_linear import Weight, _x
 
 pytestmark = pytest.mark.gpu
 
@@ -170,5 +170,45 @@ def test_mxfp4_scales_at_the_ends_rows_and_outputs(T):
     with pytest.raises(B.MoeError) as e:
         B.moe_linear_forward(lin.handle, t.cuda()[:, :K], None, out)
     assert e.value.status == B.MOE_EWORKSPACE
+    lin.sync()
+    lin.free()
+
+
+def i4_weight(N, K, large, small, seed):
+    """Random codes and zero points; every row's first block has the large scale, the others small ones."""
+    rng = np.random.default_rng(seed)
+    codes = rng.integers(0, 256, (N, K // 2), dtype=np.uint8)
+    zeros = rng.integers(0, 16, (N, K // 32), dtype=np.uint8)
+    scales = (small * (1 + rng.random((N, K // 32)))).astype(np.float16)
+    scales[::2, 0] = large  # (every other row: rows with and without one in a tile)
+    W = Weight.__new__(Weight)
+    W.fmt, W.N, W.K = "int4g32", N, K
+    W.args = tuple(torch.from_numpy(a).cuda() for a in (codes, scales, zeros))
+    s, z = (np.repeat(a.astype(np.float64), 32, 1) for a in (scales, zeros))
+    W.w, W.terms = s * (base._nibbles(codes) - z), np.abs(s) * (base._nibbles(codes) + z)
+    return W
+
+
+@pytest.mark.parametrize("T", [1, 2, 3, 8, 9, 16, 17, 40, 200])
+@pytest.mark.parametrize("large,small", [(65504.0, 2.0 ** -24), (60000.0, 1e-5), (8192.0, 6e-8), (4096.0, 6e-8), (4094.0, 6e-8)])
+def test_int4_scales_far_apart_in_a_row(T, large, small):
+    """FP16's largest and smallest group scales in one row; x is zero where the large one is, so that only the blocks
+    with small ones count."""
+    _, Linear = base._mods()
+    N, K = 133, 320
+    W = i4_weight(N, K, large, small, T)
+    lin = Linear("int4g32", *W.args)
+    rng = np.random.default_rng(T)
+    for xt in ("bf16", "mxfp8"):
+        x, xd, sc = _x(rng, T, K, xt, 32)
+        xd[:, :32] = 0
+        x[:, :32] = 0
+        close(lin.forward(xd, sc, out=nan_out(lin, T)), x, W)
+        buf = torch.full((T, N + 5), float("nan"), dtype=torch.bfloat16, device="cuda")
+        close(lin.forward(xd, sc, out=buf[:, :N]), x, W, out_bf16=True)
+        assert torch.isnan(buf[:, N:].float()).all()
+        acc = torch.randn((T, N), device="cuda")
+        before = acc.cpu().numpy().astype(np.float64)
+        close(lin.forward(xd, sc, out=acc, accumulate=True), x, W, base=before)
     lin.sync()
     lin.free()
