@@ -1,7 +1,13 @@
-"""Every value of moe_linear_forward on the GPU: none unwritten and none NaN that is not one.
+"""Every value of moe_linear_forward on the GPU: none unwritten, none NaN that is not one, none lost at the ends of
+the formats or to long sums.
 
 Tolerances are those of test_gpu_linear (FP32 accumulation of exact products); a
 value that is not a number is outside them, and outputs start as NaN.
+
+F32 rows are also held to an error of 1.5e-5 of the output's norm: an MMA's sum
+loses at most half a last place on average (2^-24, times 0.72 over the mantissas),
+always towards zero; a random walk's running sum is 2/3 of its last on average, and
+a chain has at most 512 MMAs: 512 * 0.72 * 2^-24 * 2/3 = 1.5e-5.
 """
 import inspect
 
@@ -210,5 +216,39 @@ def test_int4_scales_far_apart_in_a_row(T, large, small):
         acc = torch.randn((T, N), device="cuda")
         before = acc.cpu().numpy().astype(np.float64)
         close(lin.forward(xd, sc, out=acc, accumulate=True), x, W, base=before)
+    lin.sync()
+    lin.free()
+
+
+@pytest.mark.parametrize("fmt", ["mxfp4", "int4g32", "bf16"])
+@pytest.mark.parametrize("T,N,K", [(640, 4096, 18432), (9, 512, 18432), (130, 20480, 7168), (640, 4096, 65536)])
+def test_f32_rows_of_long_sums(fmt, T, N, K):
+    """Long K with so many tiles that nothing else splits it (and with few)."""
+    if K == 65536 and fmt == "int4g32":
+        pytest.skip("1024 MMAs a chain: a cluster of 8 is the most")
+    _, Linear = base._mods()
+    g = torch.Generator(device="cuda")
+    g.manual_seed(K + T)
+    if fmt == "bf16":
+        args = ((0.02 * torch.randn((N, K), generator=g, device="cuda")).bfloat16(),)
+        w = args[0].double()
+    else:
+        codes = torch.randint(0, 256, (N, K // 2), generator=g, device="cuda", dtype=torch.uint8)
+        w = torch.stack((codes & 15, codes >> 4), -1).view(N, K).long()
+        if fmt == "mxfp4":
+            sc = torch.randint(117, 122, (N, K // 32), generator=g, device="cuda", dtype=torch.uint8)
+            args = (codes, sc)
+            w = torch.from_numpy(base.E2M1).cuda()[w] * torch.exp2(sc.double() - 127).repeat_interleave(32, 1)
+        else:
+            sc = torch.exp2(torch.rand((N, K // 32), generator=g, device="cuda") * 4 - 11).half()
+            z = torch.randint(6, 11, (N, K // 32), generator=g, device="cuda", dtype=torch.uint8)
+            args = (codes, sc, z)
+            w = (w - z.double().repeat_interleave(32, 1)) * sc.double().repeat_interleave(32, 1)
+    x = torch.randn((T, K), generator=g, device="cuda").bfloat16()
+    lin = Linear(fmt, *args)
+    ref = x.double() @ w.T
+    got = lin.forward(x, out=nan_out(lin, T)).double()
+    err = float((got - ref).norm() / ref.norm())
+    assert err <= 1.5e-5, err
     lin.sync()
     lin.free()
