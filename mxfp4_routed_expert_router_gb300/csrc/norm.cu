@@ -36,7 +36,7 @@ struct NormArgs {
     const void *gain;
     int gain_type;
     float eps;
-    int T, H;
+    int H;
     void *sum;
     long long sum_ld;
     uint16_t *y;
@@ -94,23 +94,22 @@ __device__ __forceinline__ uint32_t e4m3x2(float lo, float hi)
     return r;
 }
 
-// One row per blockDim.x threads, blockDim.y rows per CTA; VPT vectors of 8
-// values per thread.  RES and DELTA are row types (DELTA -1: none).
+// One row per CTA, VPT vectors of 8 values per thread.  RES and DELTA are row
+// types (DELTA -1: none).
 template <int RES, int DELTA, int VPT>
 __global__ void __launch_bounds__(1024) add_rmsnorm_kernel(const NormArgs a)
 {
     __shared__ float red[32];
     const int tid = threadIdx.x, lane = tid & 31;
     const int nv = a.H / 8;
-    const long long t = (long long)blockIdx.x * blockDim.y + threadIdx.y;
-    const bool live = t < a.T;
+    const long long t = blockIdx.x;
     overlap_wait();
     float v[VPT][8];
     float ss = 0.f;
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
         const int c = tid + i * (int)blockDim.x;
-        if (live && c < nv) {
+        if (c < nv) {
             load8<RES>(a.res, t * a.res_ld + 8 * c, v[i]);
             if (DELTA >= 0) {
                 float d[8];
@@ -128,7 +127,7 @@ __global__ void __launch_bounds__(1024) add_rmsnorm_kernel(const NormArgs a)
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
         const int c = tid + i * (int)blockDim.x;
-        const bool in = live && c < nv;
+        const bool in = c < nv;
         if (RES == MOE_ROWS_BF16 && DELTA >= 0) {
             // the norm is that of what the stream holds
             const uint4 u = bf16x8(v[i]);
@@ -160,9 +159,9 @@ __global__ void __launch_bounds__(1024) add_rmsnorm_kernel(const NormArgs a)
     const int nw = blockDim.x >> 5;  // warps of a row
     if (nw > 1) {
         if (lane == 0)
-            red[threadIdx.y * nw + (tid >> 5)] = ss;
+            red[tid >> 5] = ss;
         __syncthreads();
-        ss = lane < nw ? red[threadIdx.y * nw + lane] : 0.f;
+        ss = lane < nw ? red[lane] : 0.f;
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1)
             ss += __shfl_xor_sync(0xffffffffu, ss, o);
@@ -180,9 +179,9 @@ __global__ void __launch_bounds__(1024) add_rmsnorm_kernel(const NormArgs a)
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
         const int c = tid + i * (int)blockDim.x;
-        const bool in = live && c < nv;
+        const bool in = c < nv;
         float g[8];
-        if (a.gain && c < nv) {
+        if (a.gain && in) {
             if (a.gain_type == MOE_ROWS_BF16)
                 load8<MOE_ROWS_BF16>(a.gain, 8 * c, g);
             else
@@ -224,17 +223,16 @@ __global__ void __launch_bounds__(1024) add_rmsnorm_kernel(const NormArgs a)
 }
 
 template <int RES, int DELTA>
-cudaError_t launch_norm(const NormArgs &a, cudaStream_t st)
+cudaError_t launch_norm(const NormArgs &a, int T, cudaStream_t st)
 {
     const int nv = a.H / 8;
     const int vpt = nv <= 1024 ? 1 : nv <= 2048 ? 2 : nv <= 4096 ? 4 : 8;
     const int threads = ((nv + vpt - 1) / vpt + 31) & ~31;
-    const dim3 block(threads, 1);
     switch (vpt) {
-    case 1: return launch_overlapped(add_rmsnorm_kernel<RES, DELTA, 1>, a.T, block, 0, 1, st, a);
-    case 2: return launch_overlapped(add_rmsnorm_kernel<RES, DELTA, 2>, a.T, block, 0, 1, st, a);
-    case 4: return launch_overlapped(add_rmsnorm_kernel<RES, DELTA, 4>, a.T, block, 0, 1, st, a);
-    default: return launch_overlapped(add_rmsnorm_kernel<RES, DELTA, 8>, a.T, block, 0, 1, st, a);
+    case 1: return launch_overlapped(add_rmsnorm_kernel<RES, DELTA, 1>, T, threads, 0, 1, st, a);
+    case 2: return launch_overlapped(add_rmsnorm_kernel<RES, DELTA, 2>, T, threads, 0, 1, st, a);
+    case 4: return launch_overlapped(add_rmsnorm_kernel<RES, DELTA, 4>, T, threads, 0, 1, st, a);
+    default: return launch_overlapped(add_rmsnorm_kernel<RES, DELTA, 8>, T, threads, 0, 1, st, a);
     }
 }
 
@@ -290,7 +288,6 @@ extern "C" MoeStatus moe_add_rmsnorm(const void *residual, MoeRowType residual_t
     a.gain = gain;
     a.gain_type = gain_type;
     a.eps = eps;
-    a.T = T;
     a.H = H;
     a.sum = sum;
     a.sum_ld = sum_ld;
@@ -304,9 +301,9 @@ extern "C" MoeStatus moe_add_rmsnorm(const void *residual, MoeRowType residual_t
     const int d = delta ? (int)delta_type : -1;
     cudaError_t e;
     if (residual_type == MOE_ROWS_BF16)
-        e = d < 0 ? launch_norm<B, -1>(a, st) : d == B ? launch_norm<B, B>(a, st) : launch_norm<B, F>(a, st);
+        e = d < 0 ? launch_norm<B, -1>(a, T, st) : d == B ? launch_norm<B, B>(a, T, st) : launch_norm<B, F>(a, T, st);
     else
-        e = d < 0 ? launch_norm<F, -1>(a, st) : d == B ? launch_norm<F, B>(a, st) : launch_norm<F, F>(a, st);
+        e = d < 0 ? launch_norm<F, -1>(a, T, st) : d == B ? launch_norm<F, B>(a, T, st) : launch_norm<F, F>(a, T, st);
     if (e != cudaSuccess) {
         snprintf(msg, sizeof msg, "RMS norm launch: %s", cudaGetErrorString(e));
         return bad(MOE_ECUDA, msg);
