@@ -493,7 +493,8 @@ size_t moe_linear_workspace_bytes(const MoeLinear *l, int T);
  *  y         F32 or BF16 rows of N values; F32 rows are overwritten, or added
  *            to when accumulate != 0 (BF16 rows cannot accumulate)
  *  workspace >= moe_linear_workspace_bytes(l, T) bytes, 256-byte aligned;
- *            contents on entry do not matter; may be NULL when that is 0
+ *            contents on entry do not matter; may be NULL when that is 0, and
+ *            for BF16 weights on BF16 rows, which use none
  * Rows of x start on 16-byte boundaries; rows of y on boundaries of their
  * elements.  Several streams may use one handle at a time, each with a
  * workspace of its own.  T == 0 enqueues nothing.

@@ -931,13 +931,15 @@ MoeStatus moe_linear_forward(MoeLinear *l, const void *x, MoeRowType x_type, lon
         return bad(MOE_EINVAL, "moe_linear_forward: rows of x must start on 16-byte boundaries");
     if ((uintptr_t)y % (y_type == MOE_ROWS_F32 ? 4 : 2))
         return bad(MOE_EINVAL, "moe_linear_forward: y is misaligned");
-    if (ws_bytes < moe_linear_workspace_bytes(l, T))
+    // (the GEMM reads the caller's BF16 rows as they are with BF16 weights, else rows that it writes first)
+    const bool rows = l->fmt != FMT_BF16 || x_type == MOE_ROWS_MXFP8;
+    if (rows && ws_bytes < moe_linear_workspace_bytes(l, T))
         return bad(MOE_EWORKSPACE, "moe_linear_forward: the workspace is smaller than moe_linear_workspace_bytes");
     if ((uintptr_t)workspace % 256)
         return bad(MOE_EWORKSPACE, "moe_linear_forward: the workspace must be 256-byte aligned");
     cudaStream_t st = (cudaStream_t)cuda_stream;
     if (!on_stream(l, T)) {
-        if (!workspace)
+        if (rows && !workspace)
             return bad(MOE_EWORKSPACE, "moe_linear_forward: NULL workspace");
         LinearGemm g{};
         g.w = &l->tile;

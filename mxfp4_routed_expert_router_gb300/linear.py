@@ -93,7 +93,9 @@ class QuantLinear:
                 raise B.MoeError(B.MOE_EINVAL, "accumulate needs an out to add to")
         elif tuple(out.shape) != (T, self.N):
             raise B.MoeError(B.MOE_EINVAL, f"out: shape {tuple(out.shape)} where ({T}, {self.N}) is needed")
-        n = B.moe_linear_workspace_bytes(self.handle, T) if T > self._no_ws else 0
+        n = 0
+        if T > self._no_ws and not (self.fmt == "bf16" and x.dtype == torch.bfloat16):  # (these rows go in as they are)
+            n = B.moe_linear_workspace_bytes(self.handle, T)
         ws = None
         if n or out is None:
             # On the call's own stream: calls on several streams, and captured calls, then stay apart.

@@ -252,3 +252,23 @@ def test_f32_rows_of_long_sums(fmt, T, N, K):
     assert err <= 1.5e-5, err
     lin.sync()
     lin.free()
+
+
+@pytest.mark.parametrize("T", [1, 9, 300])
+def test_bf16_weights_on_bf16_rows_use_no_workspace(T):
+    B, Linear = base._mods()
+    N, K = 130, 224
+    W = Weight("bf16", N, K, seed=T)
+    lin = Linear("bf16", *W.args)
+    x, xd, _ = _x(np.random.default_rng(T), T, K, "bf16", 8)
+    out = nan_out(lin, T)
+    B.moe_linear_forward(lin.handle, xd, None, out)
+    close(out, x, W)
+    q, qd, sc = _x(np.random.default_rng(T), T, K, "mxfp8")
+    if T > 8:  # rows that are converted need it
+        with pytest.raises(B.MoeError) as e:
+            B.moe_linear_forward(lin.handle, qd, sc, out)
+        assert e.value.status == B.MOE_EWORKSPACE
+    close(lin.forward(qd, sc, out=out), q, W)
+    lin.sync()
+    lin.free()
