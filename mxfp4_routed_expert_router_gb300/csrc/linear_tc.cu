@@ -54,7 +54,7 @@ constexpr int N_WARPS = 12, THREADS = N_WARPS * 32;
 constexpr int WARP_LOAD = 0, WARP_MMA = 1, WARP_WEIGHTS = 2, WARP_DEC = 4;  // (3 idles)
 constexpr int DEC_GROUPS = 2;         // group g decodes the stages g, g + 2, ...
 constexpr int NMAX = 128;             // tokens of a tile
-constexpr int CHAIN_F32 = 512;        // MMAs into one accumulator for F32 rows (see launch_linear_gemm)
+constexpr int CHAIN_F32 = 512, CHAIN_F32_MX = 1152;  // MMAs into one accumulator for F32 rows (see launch_linear_gemm)
 constexpr int A_MAX = 3;              // slots of the A ring (tensor memory): three with tiles of at most NHALF
 constexpr int NHALF = 64;             // tokens, two with larger ones
 constexpr int A_SLOT_COLS = 64;       // 128 16-bit values per lane
@@ -810,10 +810,12 @@ cudaError_t launch_linear_gemm(const LinearGemm &g, cudaStream_t st)
     // An MMA adds to its FP32 accumulator by truncation, half of a last place on average and always towards zero, so
     // that a long chain drifts: error against 64 bits at K = 18432 in one chain 2.1e-5 of the norm (BF16), 4.0e-5
     // (INT4, two MMAs per 16 values) where an FP32 sum is 2e-6 off.  BF16 rows round by 100 times that; for F32 rows K
-    // is split further, as far as a cluster goes, and the parts add up rounded to nearest (INT4 512 x 7168 x 18432
-    // 199 -> 224 us, BF16 142 -> 174).
+    // is split further, as far as a cluster goes, and the parts add up rounded to nearest: 5e-6 (INT4 512 x 7168 x
+    // 18432 199 -> 224 us, BF16 142 -> 174).  MXFP4's products have 10 bits and lose less: 3.4e-6 with scales within
+    // 2^4 of each other, 1.5e-5 at most, at K = 18432, which is left whole (114 us; 164 in four parts).
     const int chain = g.w->kchunks * (CHUNK_K / 16) * (g.op == LIN_I4 ? 2 : 1);
-    while (g.y_f32 && cluster < 8 && chain > CHAIN_F32 * cluster && cluster * 2 <= a.kchunks)
+    const int chain_most = g.op == LIN_F16 ? CHAIN_F32_MX : CHAIN_F32;
+    while (g.y_f32 && cluster < 8 && chain > chain_most * cluster && cluster * 2 <= a.kchunks)
         cluster *= 2;
     const int grid = (int)items * cluster;
     switch (g.op) {

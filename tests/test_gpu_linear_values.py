@@ -7,7 +7,9 @@ value that is not a number is outside them, and outputs start as NaN.
 F32 rows are also held to an error of 1.5e-5 of the output's norm: an MMA's sum
 loses at most half a last place on average (2^-24, times 0.72 over the mantissas),
 always towards zero; a random walk's running sum is 2/3 of its last on average, and
-a chain has at most 512 MMAs: 512 * 0.72 * 2^-24 * 2/3 = 1.5e-5.
+a chain has at most 512 MMAs: 512 * 0.72 * 2^-24 * 2/3 = 1.5e-5.  (1152 with MXFP4
+weights, whose products of 10 bits fit the accumulator's last places until the sum
+has grown: the same bound.)
 """
 import inspect
 
