@@ -334,32 +334,37 @@ def moe_add_rmsnorm(residual, delta, gain, eps: float, sum=None, y=None, q=None,
         _check(status)
 
 
-def _dense(t, name: str, dtype: str, rows: int, cols: int):
+_DTYPES = []  # torch.float32, torch.int32: filled by the first call that needs them
+
+
+def _dtypes():
+    if not _DTYPES:
+        import torch
+        _DTYPES.extend((torch.float32, torch.int32))
+    return _DTYPES
+
+
+def _dense(t, name: str, dtype, rows: int, cols: int):
     """Address of a dense tensor of `rows` rows (or more, or flat) of `cols` values; None and plain addresses pass."""
     if t is None or isinstance(t, int):
         return t
-    if _DTYPES.get(t.dtype) != dtype:
-        if not _DTYPES:
-            import torch
-            _DTYPES.update({torch.float32: "float32", torch.int32: "int32"})
-            return _dense(t, name, dtype, rows, cols)
-        raise MoeError(MOE_EINVAL, f"{name}: {dtype} is needed, not {t.dtype}")
-    if t.numel() < rows * cols or not t.is_contiguous() or (t.dim() == 2 and t.shape[1] != cols):
-        raise MoeError(MOE_EINVAL, f"{name}: shape {tuple(t.shape)} where a dense [{rows}, {cols}] is needed")
+    n = rows * cols
+    if t.dtype is not dtype or not t.is_contiguous() or (
+            (size := t.numel()) != n and (size < n or (t.dim() == 2 and t.shape[1] != cols))):
+        raise MoeError(MOE_EINVAL, f"{name}: a dense {dtype} tensor [{rows}, {cols}] is needed, not {t.dtype} "
+                                   f"{tuple(t.shape)}")
     return t.data_ptr()
-
-
-_DTYPES = {}
 
 
 def moe_route_grouped(router_logits, bias, T: int, E: int, k: int, n_groups: int, k_groups: int, score: int,
                       group_score: int, renormalize: bool, scale: float, topk_ids, topk_w, stream=None) -> None:
     """Group-limited routing (see include/moe.h); the outputs feed moe_forward_routed.  router_logits float32 [T, E],
     bias float32 [E] or None, topk_ids int32 and topk_w float32 [T, k], all dense; longer buffers may be given."""
-    status = lib.moe_route_grouped(_dense(router_logits, "router_logits", "float32", T, E),
-                                   _dense(bias, "bias", "float32", 1, E), T, E, k, n_groups, k_groups, score,
-                                   group_score, bool(renormalize), scale, _dense(topk_ids, "topk_ids", "int32", T, k),
-                                   _dense(topk_w, "topk_w", "float32", T, k), _stream(stream))
+    f32, i32 = _DTYPES or _dtypes()
+    status = lib.moe_route_grouped(_dense(router_logits, "router_logits", f32, T, E), _dense(bias, "bias", f32, 1, E),
+                                   T, E, k, n_groups, k_groups, score, group_score, bool(renormalize), scale,
+                                   _dense(topk_ids, "topk_ids", i32, T, k), _dense(topk_w, "topk_w", f32, T, k),
+                                   _stream(stream))
     if status:
         _check(status)
 
