@@ -348,9 +348,8 @@ def _dense(t, name: str, dtype, rows: int, cols: int):
     """Address of a dense tensor of `rows` rows (or more, or flat) of `cols` values; None and plain addresses pass."""
     if t is None or isinstance(t, int):
         return t
-    n = rows * cols
-    if t.dtype is not dtype or not t.is_contiguous() or (
-            (size := t.numel()) != n and (size < n or (t.dim() == 2 and t.shape[1] != cols))):
+    if t.dtype is not dtype or not t.is_contiguous() or t.numel() < rows * cols or (
+            t.dim() > 1 and t.size(-1) != cols):
         raise MoeError(MOE_EINVAL, f"{name}: a dense {dtype} tensor [{rows}, {cols}] is needed, not {t.dtype} "
                                    f"{tuple(t.shape)}")
     return t.data_ptr()

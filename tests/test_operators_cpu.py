@@ -133,7 +133,8 @@ def test_route_wrapper_checks_shapes_and_types(b, monkeypatch):
     _refused(b, [lambda kw=kw: call(**kw) for kw in (
         dict(logits=good["logits"].bfloat16()), dict(logits=good["logits"].double()), dict(logits=torch.zeros(T, E - 1)),
         dict(logits=torch.zeros(T - 1, E)), dict(logits=torch.zeros(E, T).t()), dict(logits=torch.zeros(T, 2 * E)[:, :E]),
-        dict(logits=torch.zeros(T, 2 * E)), dict(bias=torch.zeros(E, dtype=torch.bfloat16)), dict(bias=torch.zeros(E - 1)),
+        dict(logits=torch.zeros(T, 2 * E)),
+        dict(logits=torch.zeros(E, T)), dict(bias=torch.zeros(E, dtype=torch.bfloat16)), dict(bias=torch.zeros(E - 1)),
         dict(bias=torch.zeros(2 * E)[::2]), dict(ids=good["ids"].long()), dict(ids=good["ids"].float()),
         dict(ids=torch.zeros((T, k - 1), dtype=torch.int32)), dict(ids=torch.zeros(T * k - 1, dtype=torch.int32)),
         dict(w=good["w"].half()), dict(w=torch.zeros(T, k - 1)), dict(w=torch.zeros(k, T).t()))])
