@@ -417,7 +417,9 @@ typedef enum { MOE_ROWS_BF16 = 0, MOE_ROWS_F32 = 1, MOE_ROWS_MXFP8 = 2 } MoeRowT
  *   y = BF16 of n;   q, q_scales = MXFP8 of n
  * The mean and n are FP32.  An MXFP8 block takes the smallest power of two that
  * brings its largest |n| to 448 or below, so that nothing saturates; a block of
- * zeros takes byte 0.  A non-finite n becomes the E4M3 NaN (0x7F).
+ * zeros takes byte 0.  A non-finite n becomes the E4M3 NaN (0x7F); beside an
+ * infinite one the rest of its block may lose its bits.  Where gain is infinite, or
+ * eps and mean(s^2) are both 0, y is an infinity or NaN.
  *  residual   BF16 or F32 rows;  delta  BF16 or F32 rows, or NULL (nothing is added)
  *  gain       [H] BF16 or F32 (gain_type), or NULL (ones)
  *  sum        receives s in residual's type, or NULL; may be residual itself
@@ -470,25 +472,27 @@ MoeStatus moe_route_grouped(const float *router_logits, const float *bias, int T
  * formats: 4-bit for projections, BF16 for the router's own product.
  * moe_linear_load copies the weights into the library's own layouts, as
  * moe_load_weights does (synchronous; the caller's buffers can be freed when it
- * returns).  N in 1 .. 1048576; K a multiple of 32 in 32 .. 65536.
+ * returns): two copies, one for few tokens and one for many.  N in 1 .. 1048576;
+ * K a multiple of 32 in 32 .. 65536.
  * Errors: MOE_EINVAL (NULL pointers, unknown format, N, INT4 scales not 2-byte
  * aligned), MOE_EDIMS (K), MOE_ESCALE, MOE_ENOMEM, MOE_ECUDA.  *out is set only
  * on MOE_OK. */
 typedef struct MoeLinear MoeLinear;
 MoeStatus moe_linear_load(int N, int K, MoeWeightFormat fmt, const MoeMx *w, void *cuda_stream, MoeLinear **out);
 
-/* Bytes of device workspace moe_linear_forward needs for T tokens (0 for few
- * tokens unless an MXFP4 scale lies outside 2^-100 .. 2^100, for INT4
- * weights that run in slices of few, for a NULL handle and for T <= 0). */
+/* Bytes of device workspace moe_linear_forward needs for T tokens: 0 for a NULL
+ * handle, for T <= 0, for few tokens (unless an MXFP4 scale lies outside
+ * 2^-100 .. 2^100) and for INT4 weights that run a few tokens at a time. */
 size_t moe_linear_workspace_bytes(const MoeLinear *l, int T);
 
 /* y[t][n] = sum_k x[t][k] w[n][k] for T tokens.  Products accumulate in FP32;
  * 4-bit weights decode exactly, and x keeps its value as long as it is within
- * 2^-24 of the largest |x| of its token.  MXFP8 values of 2^128 and more count as
- * infinite; so may MXFP4 weights of 2^128 and more (scale bytes 253 and 254) where
+ * 2^-24 of the largest |x| of its token.  MXFP8 values of 2^128 and more may
+ * count as infinite, and so may MXFP4 weights of 2^128 and more (scale bytes 253 and 254) where
  * the scales of a row span more than 2^23.  INT4 weights with a group scale of
  * 4096 or more and one with bits below 2^-20 in one row run 8 tokens at a time
- * (slower for many tokens, as exact).
+ * (slower for many tokens, as exact).  A token with an infinity or a NaN gives
+ * results that are not finite, and touches no other token's.
  *  x         BF16 or MXFP8 rows of K values (x_scales [T][K/32] for MXFP8, else NULL)
  *  y         F32 or BF16 rows of N values; F32 rows are overwritten, or added
  *            to when accumulate != 0 (BF16 rows cannot accumulate)

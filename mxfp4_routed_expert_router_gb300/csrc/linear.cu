@@ -15,10 +15,12 @@
 // (launch_linear); partial sums meet in a fixed order.
 // Bound by HBM for large weights, by the start of the stream (launch, x, the first
 // steps' latency: about 3 us) for small ones, and by the decode with more tokens.
-// Measured, us per call back to back (share of a plain copy's bandwidth): MXFP4, one
-// token, 36864 x 7168 23.9 (0.87), 7168 x 18432 14.3 (0.73), 7168 x 7168 7.7 (0.52);
-// eight tokens 31.9, 19.9, 10.8; group-32 INT4, one token, 27.2, 15.9, 8.3; BF16, one
-// token, 7168 x 7168 17.4 (0.87), 256 x 7168 3.3.
+// Measured, us per call back to back, over weight copies of 420 MB in all so that none
+// stays in L2 (share of a plain copy's bandwidth): MXFP4, one token, 36864 x 7168 23.8
+// (0.87), 7168 x 18432 15.1 (0.69), 7168 x 7168 7.7 (0.52; two copies, which stay in L2,
+// take as long: the start bounds this size, not HBM); eight tokens 31.8, 21.2, 10.8;
+// group-32 INT4, one token, 27.9, 16.5, 8.4; BF16, one token, 7168 x 7168 17.3 (0.88),
+// 256 x 7168 3.4.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_fp8.h>

@@ -10,11 +10,12 @@ namespace moe {
 // LINEAR_STREAM_MIN_E8M0 .. MAX_E8M0, run on the tcgen05 GEMM (linear_tc.cu).  INT4
 // weights whose scales the GEMM's FP16 operands do not hold run here in slices of
 // this many tokens, each of which reads the weights once.  Eight tokens fill the columns of a warp-level MMA.  Measured
-// (device time in us, 8 tokens here and 9 in the GEMM): MXFP4 7168 x 7168 10.8 and
-// 12.2, 7168 x 18432 19.9 and 26.5; group-32 INT4 7168 x 18432 24.8 and 45.3; BF16
-// 256 x 7168 4.0 and 6.3, 2048 x 7168 7.9 and 7.3, 7168 x 7168 18.9 and 18.8.  Sixteen
-// tokens here would take two MMAs per weight fragment: MXFP4 7168 x 7168 17.7 (the
-// GEMM 12.7), 36864 x 7168 55 (32.3); INT4 7168 x 18432 52 (45.8).
+// (device time in us, weights from HBM, 8 tokens here and 9 in the GEMM): MXFP4
+// 7168 x 7168 10.8 and 14.1, 7168 x 18432 21.2 and 26.4; group-32 INT4 7168 x 18432
+// 25.0 and 46 (F32 rows 51); BF16 256 x 7168 3.8 and 6.6, 2048 x 7168 8.4 and 8.7,
+// 7168 x 7168 19.0 and 19.0.  Sixteen tokens here would take two MMAs per weight
+// fragment (measured with the weights in L2): MXFP4 7168 x 7168 17.7 (the GEMM 13.0),
+// 36864 x 7168 55 (33); INT4 7168 x 18432 52 (46, F32 rows 52).
 constexpr int LINEAR_STREAM_MAX_T = 8;
 
 // Operands of the tcgen05 GEMM: FP16 (MXFP4 whose exponents span at most

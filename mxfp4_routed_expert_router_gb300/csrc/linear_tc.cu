@@ -24,16 +24,22 @@
 // kernel that writes the token rows still runs and waits for it only before it
 // reads them (overlap.cuh).  Every mbarrier wait is bounded (gemm_common.cuh).
 //
-// Bound by the hand-offs between the roles (with few tokens a copy without the decode
-// and the MMAs still took 26 of 33 us; with 512 and with 2048 an SM takes 0.44 us per
-// 128 x 128 x 128 step, 0.75 of the tensor burst) and by the decoders with INT4
-// weights (two operands to make).  A tile is 128
-// tokens wide, as two CTAs share an SM's tensor memory (one CTA per SM with 256-wide
-// tiles leaves nothing to run during the hand-offs); an MMA of 64 columns or fewer
-// takes no longer than one of 64, so narrower tiles pay no less.
-// Measured, us per call back to back: MXFP4 7168 x 7168, 9 tokens 12.2, 32 13.5, 128
-// 21.8, 512 50 (1.05 PFLOP/s), 2048 146 (1.44), 36864 x 7168 with 2048 717 (1.51);
-// group-32 INT4 7168 x 7168 20.7, 21.9, 30.3, 84, 244; BF16 18.8, 19.6, 25.9, 61, 166.
+// No unit is at its peak: with 512 and 2048 tokens of 7168 x 7168 the tensor pipe is
+// active 0.4 to 0.66 of the time, L2 0.3 to 0.6 of its throughput, the path from L2 to
+// the SMs 0.26 to 0.54, DRAM below 0.25.  BF16 weights, which have no decoder to wait
+// for, are slower than MXFP4 ones: a 128 x 128 tile draws 16 KB of A and 16 KB of B
+// per 64 of K from L2 (0.82 GB for 512 tokens, 3.3 GB for 2048; MXFP4 0.52 and 2.1 GB)
+// through a ring of three such stages, so the latency of those loads is the likelier
+// bound, with the tiles' balance (224 of them on 152 SMs) for 512 tokens.  With few
+// tokens the roles' hand-offs bound it (a copy of the kernel without the decode and the
+// MMAs still took 26 of 33 us), with INT4 weights the decoders (two operands to make).
+// A tile is 128 tokens wide, as two CTAs share an SM's tensor memory (one CTA per SM with
+// 256-wide tiles leaves nothing to run meanwhile); an MMA of 64 columns or fewer takes
+// no longer than one of 64, so narrower tiles pay no less.
+// Measured, us per call back to back with F32 rows, weights from HBM (linear.cu): MXFP4
+// 7168 x 7168, 9 tokens 14.1, 32 14.8, 128 23.1, 512 49.8 (1.06 PFLOP/s), 2048 148
+// (1.42), 36864 x 7168 with 2048 743 (1.46); group-32 INT4 7168 x 7168 21.8, 22.4, 31.1,
+// 85, 284 (BF16 rows, which need no split of K, 244); BF16 19.0, 19.8, 26.1, 61, 166.
 #include <cuda.h>
 #include <cudaTypedefs.h>
 #include <cuda_bf16.h>
@@ -467,7 +473,7 @@ __global__ void __launch_bounds__(THREADS, 2)
                 }
                 // The first block of the stage is decoded before the wait for its A slot, so that
                 // less lies between the end of the MMAs that used it and those that wait for it
-                // (INT4 7168 x 18432, 512 tokens: 221 -> 199 us; more blocks gain nothing more).
+                // (INT4 7168 x 18432, 512 tokens, K whole: 221 -> 199 us; more blocks gain nothing more).
                 uint32_t o[16], lo[16];
                 auto decode = [&](int b, uint32_t *hi, uint32_t *rest) {
                     const uint32_t w[4] = {code[b].x, code[b].y, code[b].z, code[b].w};

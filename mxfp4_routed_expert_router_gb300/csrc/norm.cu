@@ -14,9 +14,11 @@
 // has vectors (up to 1024, then two, four or eight vectors a thread): a row of 7168
 // is 28 warps of one vector each, two rows to an SM.
 //
-// Measured, FP32 residual and delta, sum, y and q: 8192 rows of 7168 values 129.5 us
-// (882 MB, 6.8 TB/s: the rate of a plain copy); 176 rows 5.0 us; one row of BF16 2.4 us,
-// launch included.
+// Measured, FP32 residual and delta, sum, y and q: 8192 rows of 7168 values 128 us
+// (882 MB, 6.9 TB/s: the rate of a plain copy), of BF16 94 us (529 MB, 5.6 TB/s: the
+// instructions show); 176 rows 5.9 us from HBM, 5.2 from L2; one row of BF16 2.5 us, launch
+// included.  Above 32768 values a thread's eight vectors do not fit 64 registers: 120 to
+// 476 bytes are spilled (64 rows of 40960 BF16 values: 14.7 us, 24 MB).
 #include <cuda_bf16.h>
 #include <cuda_fp8.h>
 #include <math.h>
