@@ -515,6 +515,125 @@ MoeStatus moe_linear_sync_status(MoeLinear *l, void *cuda_stream);
 /* Release the handle and its weight copies (waits for the device; NULL is a no-op). */
 void moe_linear_free(MoeLinear *l);
 
+/* ---- Attention ----
+ *
+ * What lies between a decoder layer's input projection and its output
+ * projection: rotary embedding and the write of new keys and values into a
+ * paged cache (moe_kv_append), attention of one new token per sequence over
+ * that cache (moe_attention_decode) and causal attention within whole prompts
+ * (moe_attention_prompt).  No handle: what a kernel finds wrong in its device
+ * inputs it records in a flag of the device, which moe_attention_status reads.
+ * No counterpart in the papers.
+ *
+ * Heads: n_heads query heads share n_kv_heads key and value heads, n_heads a
+ * multiple of n_kv_heads; query head h reads key head h / (n_heads /
+ * n_kv_heads).  A head has head_dim values, 64 or 128; a row of n heads holds
+ * them side by side, and "rows" below are BF16 with a stride ld in elements. */
+
+/* One layer's keys and values in pages of page_size tokens (a power of two in
+ * 16 .. 256), the caller's memory:
+ *   k, v                [n_pages][n_kv_heads][page_size][head_dim], BF16 or, with
+ *                       MOE_ROWS_MXFP8, E4M3 bytes
+ *   k_scales, v_scales  MXFP8: E8M0 bytes [n_pages][n_kv_heads][page_size][head_dim / 32]
+ *                       (values as in MXFP8 rows above); else NULL
+ * All are dense and 16-byte aligned, n_pages * page_size is below 2^31.  The row
+ * of a token, its slot, is page * page_size + offset. */
+typedef struct {
+    void *k, *v;
+    void *k_scales, *v_scales;
+    MoeRowType type;
+    int n_pages, page_size, n_kv_heads, head_dim;
+} MoeKvCache;
+
+/* Planes that a rotation turns: values (i, i + rot_dim / 2), or neighbours (2 i, 2 i + 1). */
+typedef enum { MOE_ROPE_HALVES = 0, MOE_ROPE_PAIRS = 1 } MoeRope;
+
+/* For T tokens whose row of qkv holds n_heads query heads, then n_kv_heads key
+ * heads, then n_kv_heads value heads: turns the first rot_dim values of every
+ * query and key head by the token's position,
+ *   (a, b) -> (a cos - b sin, b cos + a sin),
+ * writes the keys and the values into the cache and the queries to q_out.
+ *  slots      [T] the token's row of the cache; -1: the token (padding) is not
+ *             written into it.  Any other slot outside the cache is treated as
+ *             -1 and recorded (moe_attention_status).  Two tokens of a call must
+ *             not have the same slot: its row would hold parts of both.
+ *  rope       float [n_positions][rot_dim]: rot_dim / 2 cosines, then as many
+ *             sines; NULL: nothing is turned, positions and rot_dim are not read
+ *  positions  [T] rows of rope.  A token whose position lies outside gets NaN
+ *             for what would be turned (recorded unless its slot is -1).
+ *  q_out      BF16 rows of n_heads heads, or NULL; may be qkv itself (in place)
+ *  k_out      BF16 rows of the turned keys, or NULL; may be the keys of qkv in place
+ * Arithmetic is FP32, rounded once to BF16.  MXFP8 blocks are those of
+ * moe_add_rmsnorm, rounded once from the turned value (not from its BF16): a
+ * non-finite value becomes the E4M3 NaN.
+ * rot_dim is a multiple of 16 in 16 .. head_dim.  Rows and rope start on 16-byte
+ * boundaries.  T == 0 enqueues nothing.
+ * Errors: MOE_EINVAL (a bad cache, T outside [0, 2^24], n_heads outside
+ * [1, 1024], an unknown style, NULL or misaligned pointers, ld too small),
+ * MOE_EDIMS (head_dim, page_size, rot_dim, n_positions), MOE_ECUDA. */
+MoeStatus moe_kv_append(const MoeKvCache *cache, const void *qkv, long long qkv_ld, int T, int n_heads,
+                        const int32_t *slots, const int32_t *positions, const float *rope, int n_positions,
+                        int rot_dim, MoeRope style, void *q_out, long long q_ld, void *k_out, long long k_ld,
+                        void *cuda_stream);
+
+/* Attention of one token for each of B sequences over the lens[b] tokens that
+ * the cache holds of sequence b (its own among them, where it has been
+ * appended):
+ *   out_h = sum_t p_t v_t,  p = softmax over t < lens[b] of scale * (q_h . k_t)
+ *  q           BF16 rows of n_heads heads, row b for sequence b
+ *  page_table  [B][max_pages]: token t of sequence b lies in page
+ *              page_table[b][t / page_size], at offset t % page_size; entries past
+ *              a sequence's last page are not read
+ *  lens        [B]; a sequence of 0 tokens gives zeros
+ *  out         BF16 rows of n_heads heads
+ *  workspace   >= moe_attention_decode_workspace_bytes(...) bytes, 256-byte
+ *              aligned; contents on entry do not matter
+ * Rows of the cache at and past lens[b], and pages of other sequences, may hold
+ * anything.  A sequence with a negative length, one above max_pages * page_size,
+ * or a page outside the cache gives NaN, and this is recorded
+ * (moe_attention_status).  Scores, softmax and sums are FP32; probabilities
+ * round to BF16 (with MXFP8 to FP16) for the product with v, MXFP8 queries to
+ * FP16 with a power of two per head.  Results do not change from call to call.
+ * Rows start on 16-byte boundaries.  B == 0 enqueues nothing.
+ * Errors: MOE_EINVAL (a bad cache, B outside [0, 65536], n_heads no multiple of
+ * n_kv_heads or above 1024, max_pages < 1 or max_pages * page_size >= 2^31, scale
+ * not finite or not above 0, NULL or misaligned pointers, ld too small), MOE_EDIMS,
+ * MOE_EWORKSPACE, MOE_ECUDA. */
+MoeStatus moe_attention_decode(const MoeKvCache *cache, const void *q, long long q_ld, int B, int n_heads,
+                               const int32_t *page_table, int max_pages, const int32_t *lens, float scale, void *out,
+                               long long out_ld, void *workspace, size_t ws_bytes, void *cuda_stream);
+
+/* Bytes of workspace that moe_attention_decode needs on the current device; 0 for arguments that it refuses. */
+size_t moe_attention_decode_workspace_bytes(int B, int n_heads, int n_kv_heads, int head_dim);
+
+/* Causal attention within each of n_seqs prompts packed one behind the other
+ * into T rows: sequence s has the rows offsets[s] .. offsets[s + 1] - 1, and
+ *   out_i = sum over j <= i of the same sequence of p_j v_j,
+ *   p = softmax over these j of scale * (q_i . k_j)      for every query head
+ *  q, k, v   BF16 rows of n_heads, n_kv_heads and n_kv_heads heads (they may lie
+ *            side by side in wider rows)
+ *  offsets   [n_seqs + 1] ascending, within 0 .. T; offsets beyond are cut to T
+ *  out       BF16 rows of n_heads heads; rows that no sequence holds stay as they
+ *            were
+ * A sequence may be empty.  A value that is not finite reaches only rows that
+ * may see it.  Scores, softmax and sums are FP32; probabilities round to BF16
+ * for the product with v.  n_heads / n_kv_heads is at most 64.
+ * Rows start on 16-byte boundaries.  T == 0 or n_seqs == 0 enqueues nothing.
+ * Errors: MOE_EINVAL (T outside [0, 2^24], n_seqs outside [0, 65536], n_heads no
+ * multiple of n_kv_heads or above 1024, more than 64 heads to a key head, scale
+ * not finite or not above 0, NULL or misaligned pointers, ld too small), MOE_EDIMS (head_dim),
+ * MOE_ECUDA. */
+MoeStatus moe_attention_prompt(const void *q, long long q_ld, const void *k, long long k_ld, const void *v,
+                               long long v_ld, int T, const int32_t *offsets, int n_seqs, int n_heads, int n_kv_heads,
+                               int head_dim, float scale, void *out, long long out_ld, void *cuda_stream);
+
+/* Wait for `cuda_stream`, then report whether a kernel of this section recorded
+ * an error on the current device since the last report: a slot, position,
+ * length or page out of range, or a wait that ran out (the call's rows are NaN
+ * or were not written).  The report clears it.
+ * Returns MOE_OK, MOE_EDEVICE or MOE_ECUDA. */
+MoeStatus moe_attention_status(void *cuda_stream);
+
 /* Human-readable description of the last non-OK status returned on the
  * calling thread (thread-local, never NULL). */
 const char *moe_last_error(void);

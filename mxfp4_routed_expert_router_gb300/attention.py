@@ -1,0 +1,138 @@
+"""Attention of a decoder layer: a paged key-value cache with its writer and its reader, and attention within prompts.
+
+torch is used only for device memory and streams; everything runs in
+libmoe_gb300.so through ``binding``.
+"""
+from __future__ import annotations
+
+from typing import Optional
+
+import torch
+
+from . import binding as B
+from .linear import stream_workspace
+
+
+def rope_table(n_positions: int, rot_dim: int, theta: float = 10000.0, device="cuda") -> torch.Tensor:
+    """Cosines and sines for ``KvCache.append``: float32 [n_positions, rot_dim], angle = position * theta^(-2 i / rot_dim)
+    for plane i, taken in 64 bits (a far position's angle loses its fraction in 32)."""
+    i = torch.arange(rot_dim // 2, device=device, dtype=torch.float64)
+    angle = torch.arange(n_positions, device=device, dtype=torch.float64).unsqueeze(1) * theta ** (-2 * i / rot_dim)
+    return torch.cat((angle.cos(), angle.sin()), 1).float()
+
+
+class KvCache:
+    """One layer's keys and values in pages: k, v [n_pages, n_kv_heads, page_size, head_dim], bfloat16, or
+    float8_e4m3fn with k_scales, v_scales uint8 [n_pages, n_kv_heads, page_size, head_dim / 32] (MXFP8).
+
+    The tensors are the caller's (``empty`` makes them) and stay with the cache.  The slot of a token is
+    page * page_size + offset.
+    """
+
+    def __init__(self, k: torch.Tensor, v: torch.Tensor, k_scales: Optional[torch.Tensor] = None,
+                 v_scales: Optional[torch.Tensor] = None):
+        if k.dim() != 4 or k.shape != v.shape or k.dtype != v.dtype or k.dtype not in (torch.bfloat16,
+                                                                                     torch.float8_e4m3fn):
+            raise B.MoeError(B.MOE_EINVAL, "k, v: bfloat16 or float8_e4m3fn [n_pages, n_kv_heads, page_size, head_dim] "
+                                           f"tensors are needed, not {k.dtype} {tuple(k.shape)} and {v.dtype} "
+                                           f"{tuple(v.shape)}")
+        mx = k.dtype == torch.float8_e4m3fn
+        if mx != (k_scales is not None) or mx != (v_scales is not None):
+            raise B.MoeError(B.MOE_EINVAL, "k_scales, v_scales: MXFP8 needs both, bfloat16 none")
+        n_pages, n_kv, page, dim = k.shape
+        for name, t in (("k_scales", k_scales), ("v_scales", v_scales)):
+            if t is not None and (t.dtype != torch.uint8 or t.shape != (n_pages, n_kv, page, dim // 32)):
+                raise B.MoeError(B.MOE_EINVAL, f"{name}: uint8 {(n_pages, n_kv, page, dim // 32)} is needed, not "
+                                               f"{t.dtype} {tuple(t.shape)}")
+        tensors = [t for t in (k, v, k_scales, v_scales) if t is not None]
+        if any(not t.is_contiguous() or not t.is_cuda or t.device != k.device for t in tensors):
+            raise B.MoeError(B.MOE_EINVAL, "a cache's tensors must be dense and on one CUDA device")
+        self.k, self.v, self.k_scales, self.v_scales = k, v, k_scales, v_scales
+        self.device = k.device
+        self.page_size, self.n_kv_heads, self.head_dim = page, n_kv, dim
+        self.c = B.MoeKvCache(k.data_ptr(), v.data_ptr(), B._ptr(k_scales), B._ptr(v_scales),
+                              B.MOE_ROWS_MXFP8 if mx else B.MOE_ROWS_BF16, n_pages, page, n_kv, dim)
+
+    @classmethod
+    def empty(cls, n_pages: int, n_kv_heads: int, page_size: int = 64, head_dim: int = 128, fmt: str = "bf16",
+              device="cuda") -> "KvCache":
+        """A cache of zeros; fmt: "bf16" or "mxfp8"."""
+        if fmt not in ("bf16", "mxfp8"):
+            raise B.MoeError(B.MOE_EINVAL, f"unknown cache format {fmt!r}")
+        shape = (n_pages, n_kv_heads, page_size, head_dim)
+        ty = torch.bfloat16 if fmt == "bf16" else torch.float8_e4m3fn
+        parts = [torch.zeros(shape, dtype=ty, device=device) for _ in range(2)]
+        if fmt == "mxfp8":
+            parts += [torch.zeros(shape[:3] + (head_dim // 32,), dtype=torch.uint8, device=device) for _ in range(2)]
+        return cls(*parts)
+
+    def append(self, qkv: torch.Tensor, n_heads: int, slots: torch.Tensor, positions: Optional[torch.Tensor] = None,
+               rope: Optional[torch.Tensor] = None, pairs: bool = False, q_out: Optional[torch.Tensor] = None,
+               k_out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+        """Turns queries and keys of qkv (bfloat16 [T, (n_heads + 2 n_kv_heads) * head_dim]) by their positions, writes
+        keys and values to their slots (-1: nowhere) and returns the queries, [T, n_heads, head_dim].  rope: a table
+        as ``rope_table`` makes (None: nothing is turned), planes of a head's halves or, with pairs, of neighbours.
+        k_out: also receives the turned keys, [T, n_kv_heads, head_dim]."""
+        self._here(qkv)
+        if q_out is None:
+            with _on(stream):
+                q_out = torch.empty((qkv.shape[0], n_heads, self.head_dim), dtype=torch.bfloat16, device=self.device)
+        B.moe_kv_append(self.c, qkv, n_heads, slots, positions, rope, B.MOE_ROPE_PAIRS if pairs else B.MOE_ROPE_HALVES,
+                        q_out, k_out, stream)
+        return q_out
+
+    def decode(self, q: torch.Tensor, page_table: torch.Tensor, lens: torch.Tensor, scale: Optional[float] = None,
+               out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+        """Attention of one token for each of B sequences (q bfloat16 [B, n_heads, head_dim]) over their lens[b] tokens
+        in the pages page_table[b] (int32 [B, max_pages]).  scale: 1 / sqrt(head_dim) by default."""
+        self._here(q)
+        if q.dim() != 3:
+            raise B.MoeError(B.MOE_EINVAL, f"q: shape {tuple(q.shape)} where [B, n_heads, head_dim] is needed")
+        n = B.moe_attention_decode_workspace_bytes(q.shape[0], q.shape[1], self.n_kv_heads, self.head_dim)
+        if stream is None:
+            ws = stream_workspace(n, self.device) if n else None
+            out = torch.empty_like(q, memory_format=torch.contiguous_format) if out is None else out
+        else:
+            with _on(stream):
+                ws = stream_workspace(n, self.device) if n else None
+                out = torch.empty_like(q, memory_format=torch.contiguous_format) if out is None else out
+        B.moe_attention_decode(self.c, q, page_table, lens, self.head_dim ** -0.5 if scale is None else scale, out, ws,
+                               n, stream)
+        return out
+
+    def _here(self, t: torch.Tensor) -> None:
+        if t.device != self.device:
+            raise B.MoeError(B.MOE_EINVAL, f"a tensor on {t.device} and a cache on {self.device}")
+
+
+def prompt(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, offsets: torch.Tensor, scale: Optional[float] = None,
+           out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """Causal attention within packed prompts: q bfloat16 [T, n_heads, head_dim], k, v [T, n_kv_heads, head_dim] (views
+    of wider rows will do), offsets int32 [n_seqs + 1].  Rows that no sequence holds are left as they are in out (of
+    an out made here they hold anything)."""
+    if out is None:
+        with _on(stream):
+            out = torch.empty(q.shape, dtype=torch.bfloat16, device=q.device)
+    B.moe_attention_prompt(q, k, v, offsets, q.shape[-1] ** -0.5 if scale is None else scale, out, stream)
+    return out
+
+
+def sync(stream=None) -> None:
+    """Waits for the stream and raises if an attention kernel on the current device recorded an error."""
+    B.moe_attention_status(stream)
+
+
+class _on:
+    """torch.cuda.stream for a stream, its address, or None (the current one)."""
+
+    def __init__(self, stream):
+        self.guard = None if stream is None else torch.cuda.stream(
+            torch.cuda.ExternalStream(stream) if isinstance(stream, int) else stream)
+
+    def __enter__(self):
+        if self.guard is not None:
+            self.guard.__enter__()
+
+    def __exit__(self, *exc):
+        if self.guard is not None:
+            self.guard.__exit__(*exc)

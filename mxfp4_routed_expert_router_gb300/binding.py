@@ -22,6 +22,7 @@ MOE_W_MXFP4, MOE_W_BF16, MOE_W_INT4G32 = 0, 1, 2
 MOE_ROWS_BF16, MOE_ROWS_F32, MOE_ROWS_MXFP8 = 0, 1, 2
 MOE_SCORE_SOFTMAX, MOE_SCORE_SIGMOID = 0, 1
 MOE_GROUP_MAX, MOE_GROUP_TOP2 = 0, 1
+MOE_ROPE_HALVES, MOE_ROPE_PAIRS = 0, 1
 
 # every symbol include/moe.h declares
 EXPORTED = ("moe_load_weights", "moe_workspace_bytes", "moe_forward", "moe_forward_routed", "moe_set_expert_range",
@@ -29,7 +30,8 @@ EXPORTED = ("moe_load_weights", "moe_workspace_bytes", "moe_forward", "moe_forwa
             "moe_profile_read", "moe_route_static", "moe_route_static_status", "moe_graph_create",
             "moe_graph_launch", "moe_graph_free", "moe_debug_expire_next_wait", "moe_last_error", "moe_free",
             "moe_add_rmsnorm", "moe_route_grouped", "moe_linear_load", "moe_linear_workspace_bytes",
-            "moe_linear_forward", "moe_linear_sync_status", "moe_linear_free")
+            "moe_linear_forward", "moe_linear_sync_status", "moe_linear_free", "moe_kv_append", "moe_attention_decode",
+            "moe_attention_decode_workspace_bytes", "moe_attention_prompt", "moe_attention_status")
 STAGES = ("routing", "grouping", "gate_up", "down", "combine", "layer")
 
 
@@ -52,6 +54,12 @@ class MoeMx(ctypes.Structure):
 class MoeHostIO(ctypes.Structure):
     _fields_ = [("x_host", ctypes.c_void_p), ("logits_host", ctypes.c_void_p), ("ids_host", ctypes.c_void_p),
                 ("w_host", ctypes.c_void_p), ("out_host", ctypes.c_void_p)]
+
+
+class MoeKvCache(ctypes.Structure):
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("k_scales", ctypes.c_void_p),
+                ("v_scales", ctypes.c_void_p), ("type", ctypes.c_int), ("n_pages", ctypes.c_int),
+                ("page_size", ctypes.c_int), ("n_kv_heads", ctypes.c_int), ("head_dim", ctypes.c_int)]
 
 
 class MoeRoutingOut(ctypes.Structure):
@@ -114,6 +122,17 @@ def _load():
     L.moe_linear_sync_status.restype = ci
     L.moe_linear_free.argtypes = [vp]
     L.moe_linear_free.restype = None
+    cache = ctypes.POINTER(MoeKvCache)
+    L.moe_kv_append.argtypes = [cache, vp, ll, ci, ci, vp, vp, vp, ci, ci, ci, vp, ll, vp, ll, vp]
+    L.moe_kv_append.restype = ci
+    L.moe_attention_decode.argtypes = [cache, vp, ll, ci, ci, vp, ci, vp, cf, vp, ll, vp, sz, vp]
+    L.moe_attention_decode.restype = ci
+    L.moe_attention_decode_workspace_bytes.argtypes = [ci, ci, ci, ci]
+    L.moe_attention_decode_workspace_bytes.restype = sz
+    L.moe_attention_prompt.argtypes = [vp, ll, vp, ll, vp, ll, ci, vp, ci, ci, ci, ci, cf, vp, ll, vp]
+    L.moe_attention_prompt.restype = ci
+    L.moe_attention_status.argtypes = [vp]
+    L.moe_attention_status.restype = ci
     L.moe_last_error.argtypes = []
     L.moe_last_error.restype = ctypes.c_char_p
     L.moe_free.argtypes = [vp]
@@ -405,6 +424,121 @@ def moe_linear_sync_status(handle: int, stream=None) -> None:
 
 def moe_linear_free(handle: int) -> None:
     lib.moe_linear_free(handle)
+
+
+def _heads(t, name: str, rows: int, heads: int, dim: int):
+    """Address and row stride of a bfloat16 tensor [rows, heads, dim] whose rows are dense; (None, 0) for None."""
+    import torch
+    if t is None:
+        return None, 0
+    if t.dtype is not torch.bfloat16 or t.shape != (rows, heads, dim):
+        raise MoeError(MOE_EINVAL, f"{name}: bfloat16 [{rows}, {heads}, {dim}] is needed, not {t.dtype} "
+                                   f"{tuple(t.shape)}")
+    ld, step, one = t.stride()
+    if (one != 1 and dim > 1) or (step != dim and heads > 1):
+        raise MoeError(MOE_EINVAL, f"{name}: the heads of a row must lie side by side")
+    return t.data_ptr(), (ld if rows > 1 else heads * dim)
+
+
+def _vector(t, name: str, n: int):
+    """Address of a dense int32 vector of n values."""
+    import torch
+    if t.dtype is not torch.int32 or t.shape != (n,) or not t.is_contiguous():
+        raise MoeError(MOE_EINVAL, f"{name}: a dense int32 vector of {n} values is needed, not {t.dtype} "
+                                   f"{tuple(t.shape)}")
+    return t.data_ptr()
+
+
+def _on_device(*tensors) -> None:
+    """All tensors on torch's current GPU."""
+    import torch
+    dev = torch.cuda.current_device() if tensors[0].is_cuda else -1
+    for t in tensors:
+        if t is not None and t.get_device() != dev or dev < 0:
+            raise MoeError(MOE_EINVAL, "every tensor must lie on the current CUDA device")
+
+
+def moe_kv_append(cache: MoeKvCache, qkv, n_heads: int, slots, positions=None, rope=None,
+                  style: int = MOE_ROPE_HALVES, q_out=None, k_out=None, stream=None) -> None:
+    """Rotary embedding and the write into a paged cache (see include/moe.h).  qkv: bfloat16 [T, (n_heads +
+    2 n_kv_heads) * head_dim]; slots, positions: int32 [T]; rope: float32 [n_positions, rot_dim] or None; q_out:
+    bfloat16 [T, n_heads, head_dim], k_out: [T, n_kv_heads, head_dim], or None."""
+    f32, _ = _DTYPES or _dtypes()
+    D, kv = cache.head_dim, cache.n_kv_heads
+    if qkv.dim() != 2 or _row_type(qkv.dtype) != MOE_ROWS_BF16:
+        raise MoeError(MOE_EINVAL, "qkv: bfloat16 rows are needed")
+    T = qkv.shape[0]
+    p, _, ld = _rows(qkv, "qkv", (T, (n_heads + 2 * kv) * D))
+    sp = _vector(slots, "slots", T)
+    pp = rp = n_pos = rot = 0
+    if rope is not None:
+        if rope.dim() != 2 or rope.dtype is not f32 or not rope.is_contiguous():
+            raise MoeError(MOE_EINVAL, "rope: a dense float32 [n_positions, rot_dim] tensor is needed")
+        if positions is None:
+            raise MoeError(MOE_EINVAL, "positions: rope needs them")
+        n_pos, rot = rope.shape
+        rp, pp = rope.data_ptr(), _vector(positions, "positions", T)
+    qo, qld = _heads(q_out, "q_out", T, n_heads, D)
+    ko, kld = _heads(k_out, "k_out", T, kv, D)
+    _on_device(qkv, slots, rope, positions if rope is not None else None, q_out, k_out)
+    status = lib.moe_kv_append(ctypes.byref(cache), p, ld, T, n_heads, sp, pp, rp, n_pos, rot, style, qo, qld, ko, kld,
+                               _stream(stream))
+    if status:
+        _check(status)
+
+
+def moe_attention_decode_workspace_bytes(B: int, n_heads: int, n_kv_heads: int, head_dim: int) -> int:
+    return int(lib.moe_attention_decode_workspace_bytes(B, n_heads, n_kv_heads, head_dim))
+
+
+def moe_attention_decode(cache: MoeKvCache, q, page_table, lens, scale: float, out, workspace, ws_bytes: int,
+                         stream=None) -> None:
+    """Attention of one token per sequence over a paged cache (see include/moe.h).  q, out: bfloat16 [B, n_heads,
+    head_dim]; page_table: dense int32 [B, max_pages]; lens: int32 [B]."""
+    _, i32 = _DTYPES or _dtypes()
+    if q.dim() != 3:
+        raise MoeError(MOE_EINVAL, "q: a [B, n_heads, head_dim] tensor is needed")
+    B, heads, D = q.shape
+    qp, qld = _heads(q, "q", B, heads, cache.head_dim)
+    op, old = _heads(out, "out", B, heads, cache.head_dim)
+    if page_table.dim() != 2 or page_table.shape[0] != B or page_table.dtype is not i32 or \
+            not page_table.is_contiguous():
+        raise MoeError(MOE_EINVAL, f"page_table: a dense int32 [{B}, max_pages] tensor is needed")
+    lp = _vector(lens, "lens", B)
+    _on_device(q, page_table, lens, out)
+    status = lib.moe_attention_decode(ctypes.byref(cache), qp, qld, B, heads, page_table.data_ptr(),
+                                      page_table.shape[1], lp, scale, op, old, _ptr(workspace), ws_bytes,
+                                      _stream(stream))
+    if status:
+        _check(status)
+
+
+def moe_attention_prompt(q, k, v, offsets, scale: float, out, stream=None) -> None:
+    """Causal attention within packed prompts (see include/moe.h).  q, out: bfloat16 [T, n_heads, head_dim]; k, v:
+    bfloat16 [T, n_kv_heads, head_dim]; offsets: int32 [n_seqs + 1]."""
+    if q.dim() != 3 or k.dim() != 3:
+        raise MoeError(MOE_EINVAL, "q, k: [T, heads, head_dim] tensors are needed")
+    T, heads, D = q.shape
+    kv = k.shape[1]
+    qp, qld = _heads(q, "q", T, heads, D)
+    kp, kld = _heads(k, "k", T, kv, D)
+    vp, vld = _heads(v, "v", T, kv, D)
+    op, old = _heads(out, "out", T, heads, D)
+    if offsets.dim() != 1 or offsets.shape[0] < 1:
+        raise MoeError(MOE_EINVAL, "offsets: an int32 vector of n_seqs + 1 values is needed")
+    n = offsets.shape[0] - 1
+    off = _vector(offsets, "offsets", n + 1)
+    _on_device(q, k, v, offsets, out)
+    status = lib.moe_attention_prompt(qp, qld, kp, kld, vp, vld, T, off, n, heads, kv, D, scale, op, old,
+                                      _stream(stream))
+    if status:
+        _check(status)
+
+
+def moe_attention_status(stream=None) -> None:
+    """Raise MoeError(MOE_EDEVICE) if an attention kernel recorded an error on the current device since the last
+    report."""
+    _check(lib.moe_attention_status(_stream(stream)))
 
 
 def routing_out(topk_ids=None, topk_w=None, expert_offsets=None, sorted_slot=None, slot_pos=None) -> MoeRoutingOut:

@@ -1,0 +1,973 @@
+// attention_decode.cu -- attention of one new token per sequence over a paged key-value cache (moe_attention_decode,
+// include/moe.h).
+//
+//   out_h = sum_t p_t v_t / sum_t p_t,   p_t = 2^(s_t - m),  s_t = scale * log2(e) * (q_h . k_t)
+//
+// The cache is read once and nothing else counts: 4 * head_dim bytes a token and key head, for 4 * head_dim flops a
+// query head.  So this is a stream, like the weight stream of linear.cu: a CTA per SM whose loader warp brings tiles
+// of 64 tokens (keys and values of one key head, by TMA through the page table) into a ring of up to 200 KB of shared
+// memory, and four warps that take 16 tokens of every tile each.  Two warp-level MMAs per 16 x 16 values of a tile do
+// the work of all query heads that share the key head, eight at a time:
+//   S^T[16 tokens, 8 heads] = K Q^T,    O^T[16 values, 8 heads] += V^T P^T
+// With tokens as the rows of the first product and values as the rows of the second, keys come out of shared memory as
+// they lie there (16 bytes a lane, which pair with the same 16 bytes of q), values by one byte permutation per pair of
+// tokens, and P moves from one to the other by a transposition of 8 x 8 (movmatrix).  The tiles carry TMA's 128-byte
+// (8-bit heads of 64: 64-byte) swizzle, so that neither read meets a bank twice.
+//
+// The work of all sequences and key heads, tile by tile, is one long list that the CTAs share evenly whatever the
+// lengths (which only the device knows): a CTA takes the tiles [c * share, (c + 1) * share).  What it finishes alone it
+// writes; of a sequence and head that other CTAs have a part of it leaves the running maximum, sum and vector in the
+// workspace, and a second kernel joins the parts in their order.
+//
+// MXFP8 caches (half the bytes): E4M3 values become FP16 exactly.  A block's power of two is applied to the FP32 sums
+// of its 32 values (keys), or to P (values): P, relative to the largest of the 16 tokens' powers in the block, in FP16,
+// tokens more than 2^8 below it in a further pass, so that no token's probability loses its bits to FP16's range.
+#include <math.h>
+#include <stdio.h>
+
+#include "attention_internal.cuh"
+#include "gemm_common.cuh"
+#include "mx_encode.cuh"
+#include "overlap.cuh"
+
+namespace moe {
+
+namespace {
+
+using namespace gemm;
+
+constexpr int TILE = 64;             // tokens of a tile
+constexpr int WARPS = 4;             // that compute, 16 tokens of a tile each
+constexpr int THREADS = (WARPS + 1) * 32;
+constexpr int MAX_STAGES = 16;
+constexpr int MIN_SHARE = 2;         // tiles of a CTA, unless there are fewer
+
+struct DecodeArgs {
+    const uint16_t *q;
+    long long q_ld;
+    const int32_t *table;
+    int max_pages;
+    const int32_t *lens;
+    long long cap;                   // tokens that a row of the table holds
+    int B, heads, kv, group;         // group: query heads of a key head
+    int chunks, units;               // chunks of up to 8 NT heads of a group; units = kv * chunks
+    int n_pages, page_log2;
+    const uint8_t *ks, *vs;
+    float scale;                     // times log2(e)
+    uint16_t *out;
+    long long out_ld;
+    float *part_o, *part_ml;         // parts: [2 * CTAs][8 NT][D], [2 * CTAs][8 NT][2]
+    int ctas;
+    int *err;
+};
+
+template <int D, int NT, bool MX> struct Geo {
+    static constexpr int ROW_B = D * (MX ? 1 : 2);
+    static constexpr int TILE_B = TILE * ROW_B;
+    static constexpr int SC_B = MX ? TILE * D / 32 : 0;
+    static constexpr int MERGE_B = WARPS * NT * 8 * D * 4;
+    static constexpr int FIT = (222 * 1024 - MERGE_B) / (2 * (TILE_B + SC_B));
+    static constexpr int STAGES = FIT < MAX_STAGES ? FIT : MAX_STAGES;
+    static constexpr int SC_OFF = STAGES * 2 * TILE_B;
+    static constexpr int MERGE_OFF = SC_OFF + STAGES * 2 * SC_B;
+    static constexpr int ML_OFF = MERGE_OFF + MERGE_B;                 // [WARPS][8 NT][2]
+    static constexpr int BAR_OFF = ML_OFF + WARPS * NT * 8 * 2 * 4;
+    static constexpr int BAD_OFF = BAR_OFF + 2 * MAX_STAGES * 8;       // a stage holds a page outside the cache
+    static constexpr int SCAN_OFF = BAD_OFF + MAX_STAGES * 4;          // long long [THREADS + 4]
+    static constexpr int SMEM = SCAN_OFF + (THREADS + 4) * 8 + 1024;   // + alignment slack
+    static_assert(SMEM <= 227 * 1024, "shared memory");
+    static_assert(TILE_B % 1024 == 0 && SC_OFF % 16 == 0 && SC_B % 16 == 0 && BAR_OFF % 8 == 0, "alignment");
+};
+
+// Tiles of sequence b: 0 for an empty one and for a length that the table cannot hold.
+__device__ __forceinline__ int tiles_of(const DecodeArgs &a, int b)
+{
+    const int n = __ldcg(a.lens + b);
+    return n > 0 && n <= a.cap ? (n + TILE - 1) / TILE : 0;
+}
+
+__device__ __forceinline__ long long share_of(const DecodeArgs &a, long long total)
+{
+    const long long s = (total + a.ctas - 1) / a.ctas;
+    return s < MIN_SHARE ? MIN_SHARE : s;
+}
+
+__device__ __forceinline__ float ex2(float x)
+{
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+template <bool F16>
+__device__ __forceinline__ void mma16816(float c[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                         uint32_t b1)
+{
+    if (F16)
+        asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+            : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+            : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+    else
+        asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+            : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+            : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+__device__ __forceinline__ uint32_t transpose8x8(uint32_t v)
+{
+    uint32_t r;
+    asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
+    return r;
+}
+
+__device__ __forceinline__ uint32_t f16_pair(float a, float b)
+{
+    const __half2 p = __floats2half2_rn(a, b);
+    return *reinterpret_cast<const uint32_t *>(&p);
+}
+
+__device__ __forceinline__ uint32_t e4m3x2_to_f16x2(uint32_t v)
+{
+    uint32_t h;
+    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"((uint16_t)v));
+    return h;
+}
+
+// 2^(byte - 127), NaN for 255
+__device__ __forceinline__ float e8m0(uint32_t byte)
+{
+    return byte == 255 ? __int_as_float(0x7FC00000) : __int_as_float(byte ? byte << 23 : 0x400000);
+}
+
+__device__ __forceinline__ uint4 lds128(uint32_t a)
+{
+    uint4 v;
+    asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a));
+    return v;
+}
+
+__device__ __forceinline__ uint2 lds64(uint32_t a)
+{
+    uint2 v;
+    asm volatile("ld.shared.v2.b32 {%0,%1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(a));
+    return v;
+}
+
+__device__ __forceinline__ uint32_t lds32(uint32_t a)
+{
+    uint32_t v;
+    asm volatile("ld.shared.b32 %0, [%1];" : "=r"(v) : "r"(a));
+    return v;
+}
+
+__device__ __forceinline__ uint32_t lds16(uint32_t a)
+{
+    uint16_t v;
+    asm volatile("ld.shared.b16 %0, [%1];" : "=h"(v) : "r"(a));
+    return v;
+}
+
+__device__ __forceinline__ void tma_4d(void *dst, const CUtensorMap *map, int x, int y, int z, int w, uint64_t *bar)
+{
+    asm volatile(
+        "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, "
+        "%5}], [%6];" ::"r"(smem_addr(dst)),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(w), "r"(smem_addr(bar))
+        : "memory");
+}
+
+// What one warp of those that compute holds of a sequence and key head: per lane (g, q) = (lane / 4, lane % 4) the
+// vector's values of heads 2q and 2q + 1, their maximum (of log2 scores) and its own part of their sum.
+template <int D, int NT> struct State {
+    float o[D / 16][NT][4];
+    float m[NT][2], l[NT][2];
+};
+
+// ---------------------------------------------------------------- BF16
+
+// q as the B operand: lane (g, q) has of head g the 16-byte pieces 8 h + 2q and 8 h + 2q + 1 of each 64 values h
+template <int D, int NT>
+__device__ __forceinline__ void load_q(const DecodeArgs &a, const uint16_t *q, int heads, int g, int qd,
+                                       uint32_t (&qf)[NT][D / 8])
+{
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int c = 0; c < D / 32; ++c) {
+            uint4 u = make_uint4(0, 0, 0, 0);
+            if (8 * nt + g < heads)
+                u = __ldcg(reinterpret_cast<const uint4 *>(q + (8 * nt + g) * D) + 8 * (c / 2) + 2 * qd + (c & 1));
+            qf[nt][4 * c] = u.x, qf[nt][4 * c + 1] = u.y, qf[nt][4 * c + 2] = u.z, qf[nt][4 * c + 3] = u.w;
+        }
+}
+
+// Scores' maximum over the 16 tokens, per head; s turns into scaled scores, -inf past the sequence
+template <int NT>
+__device__ __forceinline__ void tile_max(float (&s)[NT][4], const float (&mul)[NT][2], bool in0, bool in1,
+                                         float (&mt)[NT][2])
+{
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+        s[nt][0] = in0 ? s[nt][0] * mul[nt][0] : -INFINITY;
+        s[nt][1] = in0 ? s[nt][1] * mul[nt][1] : -INFINITY;
+        s[nt][2] = in1 ? s[nt][2] * mul[nt][0] : -INFINITY;
+        s[nt][3] = in1 ? s[nt][3] * mul[nt][1] : -INFINITY;
+        mt[nt][0] = fmaxf(s[nt][0], s[nt][2]);
+        mt[nt][1] = fmaxf(s[nt][1], s[nt][3]);
+    }
+#pragma unroll
+    for (int o = 4; o < 32; o <<= 1)
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+            mt[nt][0] = fmaxf(mt[nt][0], __shfl_xor_sync(0xffffffffu, mt[nt][0], o));
+            mt[nt][1] = fmaxf(mt[nt][1], __shfl_xor_sync(0xffffffffu, mt[nt][1], o));
+        }
+}
+
+__device__ __forceinline__ float finite_base(float m) { return m == -INFINITY ? 0.f : m; }
+
+// 16 tokens of a BF16 tile.  kb, vb: shared addresses of the warp's block of rows (of `rows` rows), r0 its first row
+// there; n of the 16 tokens belong to the sequence.
+template <int D, int NT>
+__device__ __forceinline__ void tile_bf16(State<D, NT> &st, const uint32_t (&qf)[NT][D / 8], uint32_t kb, uint32_t vb,
+                                          int rows, int r0, int n, const float (&mul)[NT][2], int g, int qd)
+{
+    float sa[NT][4], sb[NT][4];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            sa[nt][i] = sb[nt][i] = 0.f;
+#pragma unroll
+    for (int c = 0; c < D / 32; ++c) {
+        const uint32_t at = kb + (c / 2) * rows * 128 + (r0 + g) * 128 + (((2 * qd + (c & 1)) ^ g) << 4);
+        const uint4 k0 = lds128(at), k1 = lds128(at + 8 * 128);
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+            mma16816<false>(sa[nt], k0.x, k1.x, k0.y, k1.y, qf[nt][4 * c], qf[nt][4 * c + 1]);
+            mma16816<false>(sb[nt], k0.z, k1.z, k0.w, k1.w, qf[nt][4 * c + 2], qf[nt][4 * c + 3]);
+        }
+    }
+    float mt[NT][2];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            sa[nt][i] += sb[nt][i];
+    tile_max<NT>(sa, mul, g < n, g + 8 < n, mt);
+    bool grown = false;
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+        grown |= mt[nt][0] > st.m[nt][0] || mt[nt][1] > st.m[nt][1];
+    if (__any_sync(0xffffffffu, grown)) {
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const float m = fmaxf(st.m[nt][h], mt[nt][h]), f = ex2(st.m[nt][h] - finite_base(m));
+                st.m[nt][h] = m;
+                st.l[nt][h] *= f;
+#pragma unroll
+                for (int i = 0; i < D / 16; ++i) {
+                    st.o[i][nt][h] *= f;
+                    st.o[i][nt][2 + h] *= f;
+                }
+            }
+        }
+    }
+    uint32_t pf[NT][2];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+        const float b0 = finite_base(st.m[nt][0]), b1 = finite_base(st.m[nt][1]);
+        const float p0 = ex2(sa[nt][0] - b0), p1 = ex2(sa[nt][1] - b1);
+        const float p2 = ex2(sa[nt][2] - b0), p3 = ex2(sa[nt][3] - b1);
+        st.l[nt][0] += p0 + p2;
+        st.l[nt][1] += p1 + p3;
+        // rounded to BF16 for the product (2^-9 of each, of random sign): v is BF16, and an MMA's operands share a type
+        pf[nt][0] = transpose8x8(bf16_pair(p0, p1));
+        pf[nt][1] = transpose8x8(bf16_pair(p2, p3));
+    }
+#pragma unroll
+    for (int h = 0; h < D / 64; ++h) {
+        uint4 w[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int t = 2 * qd + (i & 1) + 8 * (i >> 1);
+            w[i] = lds128(vb + h * rows * 128 + (r0 + t) * 128 + ((g ^ (t & 7)) << 4));
+            if (t >= n)  // what lies there may be anything: 0 * inf is not 0
+                w[i] = make_uint4(0, 0, 0, 0);
+        }
+        const uint32_t w0[4] = {w[0].x, w[0].y, w[0].z, w[0].w}, w1[4] = {w[1].x, w[1].y, w[1].z, w[1].w};
+        const uint32_t w2[4] = {w[2].x, w[2].y, w[2].z, w[2].w}, w3[4] = {w[3].x, w[3].y, w[3].z, w[3].w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const uint32_t a0 = __byte_perm(w0[i], w1[i], 0x5410), a1 = __byte_perm(w0[i], w1[i], 0x7632);
+            const uint32_t a2 = __byte_perm(w2[i], w3[i], 0x5410), a3 = __byte_perm(w2[i], w3[i], 0x7632);
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+                mma16816<false>(st.o[4 * h + i][nt], a0, a1, a2, a3, pf[nt][0], pf[nt][1]);
+        }
+    }
+}
+
+// ---------------------------------------------------------------- MXFP8
+
+// q in FP16 with a power of two per head (the largest |q| lands in [2^14, 2^15)): lane (g, q) has of head g the values
+// 32 b + 8 q .. + 7 of each block b.  e: the powers of heads 2q and 2q + 1.
+template <int D, int NT>
+__device__ __forceinline__ void load_q_f16(const DecodeArgs &a, const uint16_t *q, int heads, int g, int qd,
+                                           uint32_t (&qf)[NT][D / 8], float (&mul)[NT][2])
+{
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+        uint32_t w[D / 8];
+        float m = 0.f;  // (NaN is left out and stays NaN in FP16)
+#pragma unroll
+        for (int b = 0; b < D / 32; ++b) {
+            uint4 u = make_uint4(0, 0, 0, 0);
+            if (8 * nt + g < heads)
+                u = __ldcg(reinterpret_cast<const uint4 *>(q + (8 * nt + g) * D) + 4 * b + qd);
+            w[4 * b] = u.x, w[4 * b + 1] = u.y, w[4 * b + 2] = u.z, w[4 * b + 3] = u.w;
+        }
+#pragma unroll
+        for (int i = 0; i < D / 8; ++i)
+            m = fmaxf(m, fmaxf(fabsf(__uint_as_float(w[i] << 16)), fabsf(__uint_as_float(w[i] & 0xFFFF0000u))));
+        m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 1));
+        m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 2));
+        const int e = max((int)(__float_as_uint(m) >> 23) - 141, -126);
+        const float by = __int_as_float((127 - e) << 23);
+#pragma unroll
+        for (int i = 0; i < D / 8; ++i)
+            qf[nt][i] = f16_pair(__uint_as_float(w[i] << 16) * by, __uint_as_float(w[i] & 0xFFFF0000u) * by);
+        mul[nt][0] = a.scale * __int_as_float((127 + __shfl_sync(0xffffffffu, e, 8 * qd)) << 23);
+        mul[nt][1] = a.scale * __int_as_float((127 + __shfl_sync(0xffffffffu, e, 8 * qd + 4)) << 23);
+    }
+}
+
+// A row's byte in a swizzled tile
+template <int D> __device__ __forceinline__ uint32_t row8(int r, int byte)
+{
+    return D == 128 ? r * 128 + (byte ^ ((r & 7) << 4)) : r * 64 + (byte ^ (((r >> 1) & 3) << 4));
+}
+
+template <int D> __device__ __forceinline__ uint32_t scales_of(uint32_t base, int t)
+{
+    return D == 128 ? lds32(base + t * 4) : lds16(base + t * 2);
+}
+
+// 16 tokens of an MXFP8 tile.  kb, vb, r0 as above; ksb, vsb: the scales of the warp's 16 tokens.
+template <int D, int NT>
+__device__ __forceinline__ void tile_mx(State<D, NT> &st, const uint32_t (&qf)[NT][D / 8], uint32_t kb, uint32_t vb,
+                                        uint32_t ksb, uint32_t vsb, int r0, int n, const float (&mul)[NT][2], int g,
+                                        int qd)
+{
+    constexpr int NB = D / 32;
+    float s[NT][4];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            s[nt][i] = 0.f;
+    const uint32_t k0s = scales_of<D>(ksb, g), k1s = scales_of<D>(ksb, g + 8);
+#pragma unroll
+    for (int b = 0; b < NB; ++b) {
+        const uint2 k0 = lds64(kb + row8<D>(r0 + g, 32 * b + 8 * qd));
+        const uint2 k1 = lds64(kb + row8<D>(r0 + g + 8, 32 * b + 8 * qd));
+        const uint32_t x0 = e4m3x2_to_f16x2(k0.x), x1 = e4m3x2_to_f16x2(k0.x >> 16);
+        const uint32_t x2 = e4m3x2_to_f16x2(k0.y), x3 = e4m3x2_to_f16x2(k0.y >> 16);
+        const uint32_t y0 = e4m3x2_to_f16x2(k1.x), y1 = e4m3x2_to_f16x2(k1.x >> 16);
+        const uint32_t y2 = e4m3x2_to_f16x2(k1.y), y3 = e4m3x2_to_f16x2(k1.y >> 16);
+        const float e0 = e8m0((k0s >> (8 * b)) & 255), e1 = e8m0((k1s >> (8 * b)) & 255);
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+            float c[4] = {0.f, 0.f, 0.f, 0.f};
+            mma16816<true>(c, x0, y0, x1, y1, qf[nt][4 * b], qf[nt][4 * b + 1]);
+            mma16816<true>(c, x2, y2, x3, y3, qf[nt][4 * b + 2], qf[nt][4 * b + 3]);
+            s[nt][0] = fmaf(c[0], e0, s[nt][0]);
+            s[nt][1] = fmaf(c[1], e0, s[nt][1]);
+            s[nt][2] = fmaf(c[2], e1, s[nt][2]);
+            s[nt][3] = fmaf(c[3], e1, s[nt][3]);
+        }
+    }
+    float mt[NT][2];
+    const bool in0 = g < n, in1 = g + 8 < n;
+    tile_max<NT>(s, mul, in0, in1, mt);
+    // P relative to the tile's own maximum, in FP16; f brings the tile's product to the running one
+    float f[NT][2], alpha[NT][2], p[NT][4];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const float m = fmaxf(st.m[nt][h], mt[nt][h]), base = finite_base(m);
+            alpha[nt][h] = ex2(st.m[nt][h] - base);
+            f[nt][h] = ex2(mt[nt][h] - base);
+            st.m[nt][h] = m;
+            const float tb = finite_base(mt[nt][h]);
+            p[nt][h] = ex2(s[nt][h] - tb);
+            p[nt][2 + h] = ex2(s[nt][2 + h] - tb);
+            st.l[nt][h] = fmaf(st.l[nt][h], alpha[nt][h], f[nt][h] * (p[nt][h] + p[nt][2 + h]));
+#pragma unroll
+            for (int i = 0; i < D / 16; ++i) {
+                st.o[i][nt][h] *= alpha[nt][h];
+                st.o[i][nt][2 + h] *= alpha[nt][h];
+            }
+        }
+    }
+    const uint32_t v0s = scales_of<D>(vsb, g), v1s = scales_of<D>(vsb, g + 8);
+    uint32_t todo0 = in0 ? (D == 128 ? 0xFFFFFFFFu : 0xFFFFu) : 0u, todo1 = in1 ? (D == 128 ? 0xFFFFFFFFu : 0xFFFFu) : 0u;
+    do {
+        uint32_t top = __vmaxu4(v0s & todo0, v1s & todo1);  // per block, the largest power left
+        top = __vmaxu4(top, __shfl_xor_sync(0xffffffffu, top, 4));
+        top = __vmaxu4(top, __shfl_xor_sync(0xffffffffu, top, 8));
+        top = __vmaxu4(top, __shfl_xor_sync(0xffffffffu, top, 16));
+#pragma unroll
+        for (int b = 0; b < NB; ++b) {
+            const uint32_t mask = 255u << (8 * b);
+            const int R = (top >> (8 * b)) & 255;
+            const int d0 = R - (int)((v0s >> (8 * b)) & 255), d1 = R - (int)((v1s >> (8 * b)) & 255);
+            const bool u0 = (todo0 & mask) && d0 <= 8, u1 = (todo1 & mask) && d1 <= 8;
+            const float w0 = u0 ? __int_as_float((127 - d0) << 23) : 0.f, w1 = u1 ? __int_as_float((127 - d1) << 23) : 0.f;
+            todo0 &= u0 ? ~mask : ~0u;
+            todo1 &= u1 ? ~mask : ~0u;
+            const float er = e8m0(R);
+            uint32_t w[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int t = 2 * qd + (i & 1) + 8 * (i >> 1);
+                w[i] = lds32(vb + row8<D>(r0 + t, 32 * b + 4 * g));
+                if (t >= n)  // what lies there may be NaN: 0 * NaN is not 0
+                    w[i] = 0;
+            }
+            uint32_t pf[NT][2];
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+                pf[nt][0] = transpose8x8(f16_pair(p[nt][0] * w0, p[nt][1] * w0));
+                pf[nt][1] = transpose8x8(f16_pair(p[nt][2] * w1, p[nt][3] * w1));
+            }
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                const uint32_t lo = __byte_perm(w[0], w[1], j ? 0x7362 : 0x5140);
+                const uint32_t hi = __byte_perm(w[2], w[3], j ? 0x7362 : 0x5140);
+                const uint32_t a0 = e4m3x2_to_f16x2(lo), a1 = e4m3x2_to_f16x2(lo >> 16);
+                const uint32_t a2 = e4m3x2_to_f16x2(hi), a3 = e4m3x2_to_f16x2(hi >> 16);
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt) {
+                    float c[4] = {0.f, 0.f, 0.f, 0.f};
+                    mma16816<true>(c, a0, a1, a2, a3, pf[nt][0], pf[nt][1]);
+                    const float f0 = f[nt][0] * er, f1 = f[nt][1] * er;
+                    float *o = st.o[2 * b + j][nt];
+                    o[0] = fmaf(c[0], f0, o[0]);
+                    o[1] = fmaf(c[1], f1, o[1]);
+                    o[2] = fmaf(c[2], f0, o[2]);
+                    o[3] = fmaf(c[3], f1, o[3]);
+                }
+            }
+        }
+    } while (__any_sync(0xffffffffu, todo0 | todo1));
+}
+
+// ---------------------------------------------------------------- kernel
+
+// A place in the list of tiles: sequence b (its tiles start at `base` times units, `nt` of them per unit), unit u, tile t.
+struct Place {
+    long long base;
+    int b, nt, u, t;
+};
+
+__device__ __forceinline__ void next_sequence(const DecodeArgs &a, Place &p)
+{
+    p.base += p.nt;
+    p.u = p.t = 0;
+    do
+        p.nt = ++p.b < a.B ? tiles_of(a, p.b) : 1;
+    while (p.nt == 0);
+}
+
+template <int D, int NT, bool MX>
+__global__ void __launch_bounds__(THREADS, 1)
+    decode_kernel(const __grid_constant__ DecodeArgs a, const __grid_constant__ CUtensorMap map_k,
+                  const __grid_constant__ CUtensorMap map_v)
+{
+    using G = Geo<D, NT, MX>;
+    extern __shared__ uint8_t smem_dyn[];
+    uint8_t *smem = smem_dyn + ((1024u - (smem_addr(smem_dyn) & 1023u)) & 1023u);
+    uint64_t *full = reinterpret_cast<uint64_t *>(smem + G::BAR_OFF), *empty = full + MAX_STAGES;
+    int *bad = reinterpret_cast<int *>(smem + G::BAD_OFF);
+    long long *scan = reinterpret_cast<long long *>(smem + G::SCAN_OFF);
+    __shared__ Place first;
+    __shared__ int abort_word;
+    volatile int *abort_flag = &abort_word;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+
+    if (tid == 0) {
+        for (int i = 0; i < G::STAGES; ++i) {
+            mbar_init(&full[i], 1);
+            mbar_init(&empty[i], WARPS);
+        }
+        abort_word = 0;
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+        fence_proxy_async();
+    }
+    overlap_trigger();
+    overlap_wait();
+
+    // the list: every thread sums the tiles of some consecutive sequences
+    const int per = (a.B + THREADS - 1) / THREADS;
+    long long sum = 0;
+    for (int b = tid * per; b < min(a.B, (tid + 1) * per); ++b)
+        sum += tiles_of(a, b);
+    long long incl = sum;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const long long v = __shfl_up_sync(0xffffffffu, incl, o);
+        incl += lane >= o ? v : 0;
+    }
+    if (lane == 31)
+        scan[warp] = incl;
+    __syncthreads();
+    long long pre = incl - sum, total = 0;
+    for (int w = 0; w < WARPS + 1; ++w) {
+        pre += w < warp ? scan[w] : 0;
+        total += scan[w];
+    }
+    total *= a.units;
+    const long long share = share_of(a, total);
+    const long long start = min(total, (long long)blockIdx.x * share), end = min(total, start + share);
+    if (start < end && pre * a.units <= start && start < (pre + sum) * a.units) {
+        Place p;
+        p.b = tid * per;
+        p.base = pre;
+        p.nt = tiles_of(a, p.b);
+        while (start >= (p.base + p.nt) * a.units) {
+            p.base += p.nt;
+            p.nt = tiles_of(a, ++p.b);
+        }
+        const long long in = start - p.base * a.units;
+        p.u = (int)(in / p.nt);
+        p.t = (int)(in - (long long)p.u * p.nt);
+        first = p;
+    }
+    // sequences without tiles: zeros, or NaN where the length cannot be
+    for (int b = blockIdx.x; b < a.B; b += gridDim.x) {
+        const int n = __ldcg(a.lens + b);
+        if (n > 0 && n <= a.cap)
+            continue;
+        if (n != 0 && tid == 0)
+            atomicCAS(a.err, 0, DEV_ERR_BOUNDS);
+        const uint32_t v = n == 0 ? 0u : 0x7FC07FC0u;
+        for (int i = tid; i < a.heads * D / 8; i += THREADS)
+            reinterpret_cast<uint4 *>(a.out + b * a.out_ld)[i] = make_uint4(v, v, v, v);
+    }
+    __syncthreads();
+    if (start >= end)
+        return;
+    Place at = first;
+    const int page = 1 << a.page_log2, rows = min(page, TILE);  // rows of a TMA box
+
+    if (warp == WARPS) {
+        // ------------------------------------------------------ tiles -> ring
+        // (a lane per page of a tile; the next tile's page numbers are on their way while this one's slot is awaited)
+        const int pages = TILE / rows;
+        auto entry = [&](const Place &p) {  // the lane's page: -1 none, -2 outside the cache
+            const int i = ((p.t * TILE) >> a.page_log2) + lane;
+            if (lane >= pages || ((long long)i << a.page_log2) >= __ldcg(a.lens + p.b))
+                return -1;
+            const int id = __ldcg(a.table + (long long)p.b * a.max_pages + i);
+            return id >= 0 && id < a.n_pages ? id : -2;
+        };
+        int slot = 0, it = 0;
+        uint32_t ph = 0;
+        int id = entry(at);
+        for (long long cur = start; cur < end; ++cur) {
+            const Place here = at;
+            if (++at.t == at.nt) {
+                at.t = 0;
+                if (++at.u == a.units && cur + 1 < end)
+                    next_sequence(a, at);
+            }
+            const int id_next = cur + 1 < end ? entry(at) : -1;
+            if (!mbar_wait_sleep_warp(&empty[slot], ph ^ 1, abort_flag, a.err, lane))
+                break;
+            const uint32_t got = __ballot_sync(0xffffffffu, id != -1), wrong = __ballot_sync(0xffffffffu, id == -2);
+            if (lane == 0) {
+                if (wrong)
+                    atomicCAS(a.err, 0, DEV_ERR_BOUNDS);
+                bad[slot] = wrong != 0;
+                mbar_arrive_expect_tx(&full[slot], __popc(got) * 2 * rows * (G::ROW_B + (MX ? D / 32 : 0)));
+            }
+            __syncwarp();
+            if (id != -1) {
+                const int pg = id < 0 ? 0 : id;  // (any page will do for one outside: the result is NaN)
+                const int kvh = here.u / a.chunks, off = (here.t * TILE) & (page - 1);
+                uint8_t *dk = smem + slot * 2 * G::TILE_B + lane * rows * G::ROW_B, *dv = dk + G::TILE_B;
+                tma_4d(dk, &map_k, 0, kvh * page + off, 0, pg, &full[slot]);
+                tma_4d(dv, &map_v, 0, kvh * page + off, 0, pg, &full[slot]);
+                if (MX) {
+                    const long long row = (((long long)pg * a.kv + kvh) << a.page_log2) + off;
+                    uint8_t *ds = smem + G::SC_OFF + slot * 2 * G::SC_B + lane * rows * (D / 32);
+                    bulk_g2s(ds, a.ks + row * (D / 32), rows * (D / 32), &full[slot]);
+                    bulk_g2s(ds + G::SC_B, a.vs + row * (D / 32), rows * (D / 32), &full[slot]);
+                }
+            }
+            id = id_next;
+            ++it;
+            if (++slot == G::STAGES) {
+                slot = 0;
+                ph ^= 1;
+            }
+        }
+        // every copy has landed before the CTA ends (bounded)
+        if (lane == 0)
+            for (int i = it > G::STAGES ? it - G::STAGES : 0; i < it; ++i)
+                mbar_drain(&full[i % G::STAGES], (i / G::STAGES) & 1);
+        __syncwarp();
+        return;
+    }
+
+    // ---------------------------------------------------------- products
+    const int g = lane >> 2, qd = lane & 3;
+    const int block = 16 * warp / rows, r0 = 16 * warp % rows;  // the warp's rows of a tile
+    float *merge = reinterpret_cast<float *>(smem + G::MERGE_OFF), *ml = reinterpret_cast<float *>(smem + G::ML_OFF);
+    const uint32_t ring = smem_addr(smem);
+    int slot = 0, part = 0;
+    uint32_t ph = 0;
+    bool alive = true;
+    State<D, NT> st;
+    uint32_t qf[NT][D / 8];
+    float mul[NT][2];
+    for (long long cur = start; cur < end;) {
+        const int t0 = at.t, t1 = (int)min((long long)at.nt, t0 + (end - cur));
+        const int kvh = at.u / a.chunks, chunk = at.u - kvh * a.chunks;
+        const int h0 = chunk * 8 * NT, heads = min(8 * NT, a.group - h0);
+        const long long head = (long long)kvh * a.group + h0;
+        const int len = __ldcg(a.lens + at.b);
+        const uint16_t *q = a.q + at.b * a.q_ld + head * D;
+        if (MX) {
+            load_q_f16<D, NT>(a, q, heads, g, qd, qf, mul);
+        } else {
+            load_q<D, NT>(a, q, heads, g, qd, qf);
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+                mul[nt][0] = mul[nt][1] = a.scale;
+        }
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                st.m[nt][h] = -INFINITY;
+                st.l[nt][h] = 0.f;
+            }
+#pragma unroll
+            for (int i = 0; i < D / 16; ++i)
+#pragma unroll
+                for (int c = 0; c < 4; ++c)
+                    st.o[i][nt][c] = 0.f;
+        }
+        bool wrong = false;
+        for (int t = t0; t < t1; ++t) {
+            // (after a wait that ran out the warp only keeps to the others' barriers; the rows become NaN)
+            alive = alive && __all_sync(0xffffffffu, mbar_wait(&full[slot], ph, abort_flag, a.err)) != 0;
+            wrong |= !alive || bad[slot] != 0;
+            const int n = min(16, len - t * TILE - 16 * warp);
+            if (alive && n > 0) {
+                const uint32_t kb = ring + slot * 2 * G::TILE_B + block * rows * G::ROW_B, vb = kb + G::TILE_B;
+                if constexpr (MX) {
+                    const uint32_t ksb = ring + G::SC_OFF + slot * 2 * G::SC_B + 16 * warp * (D / 32);
+                    tile_mx<D, NT>(st, qf, kb, vb, ksb, ksb + G::SC_B, r0, n, mul, g, qd);
+                } else {
+                    tile_bf16<D, NT>(st, qf, kb, vb, rows, r0, n, mul, g, qd);
+                }
+            }
+            __syncwarp();
+            if (lane == 0 && alive)
+                mbar_arrive(&empty[slot]);
+            if (++slot == G::STAGES) {
+                slot = 0;
+                ph ^= 1;
+            }
+        }
+        // the four warps' parts
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                float l = st.l[nt][h];
+#pragma unroll
+                for (int o = 4; o < 32; o <<= 1)
+                    l += __shfl_xor_sync(0xffffffffu, l, o);
+                if (wrong)
+                    l = __int_as_float(0x7FC00000);
+                if (g == 0)
+                    *reinterpret_cast<float2 *>(ml + ((warp * NT + nt) * 8 + 2 * qd + h) * 2) = make_float2(st.m[nt][h], l);
+            }
+        asm volatile("bar.sync 1, %0;" ::"n"(WARPS * 32) : "memory");
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const int hd = nt * 8 + 2 * qd + h;
+                float m = -INFINITY;
+#pragma unroll
+                for (int w = 0; w < WARPS; ++w)
+                    m = fmaxf(m, ml[(w * NT * 8 + hd) * 2]);
+                const float f = ex2(st.m[nt][h] - finite_base(m));
+                float *o = merge + (warp * NT * 8 + hd) * D;
+                if constexpr (MX) {  // values 16 (i / 2) ..: block i / 2 of 32, 4 g + 2 (i & 1) and the next
+#pragma unroll
+                    for (int i = 0; i < D / 16; ++i)
+                        *reinterpret_cast<float2 *>(o + 32 * (i / 2) + 4 * g + 2 * (i & 1)) =
+                            make_float2(st.o[i][nt][h] * f, st.o[i][nt][2 + h] * f);
+                } else {  // 64 (i / 4) + 8 g + 2 (i & 3) and the next
+#pragma unroll
+                    for (int i = 0; i < D / 16; ++i)
+                        *reinterpret_cast<float2 *>(o + 64 * (i / 4) + 8 * g + 2 * (i & 3)) =
+                            make_float2(st.o[i][nt][h] * f, st.o[i][nt][2 + h] * f);
+                }
+            }
+        asm volatile("bar.sync 1, %0;" ::"n"(WARPS * 32) : "memory");
+        const bool whole = t0 == 0 && t1 == at.nt;
+        for (int i = tid; i < NT * D; i += WARPS * 32) {
+            const int hd = i / (D / 8), d = i % (D / 8) * 8;
+            if (hd >= heads)
+                continue;
+            float m = -INFINITY, l = 0.f, v[8] = {};
+#pragma unroll
+            for (int w = 0; w < WARPS; ++w)
+                m = fmaxf(m, ml[(w * NT * 8 + hd) * 2]);
+#pragma unroll
+            for (int w = 0; w < WARPS; ++w) {
+                const float2 x = *reinterpret_cast<const float2 *>(ml + (w * NT * 8 + hd) * 2);
+                l = fmaf(x.y, ex2(x.x - finite_base(m)), l);
+                const float4 *o = reinterpret_cast<const float4 *>(merge + (w * NT * 8 + hd) * D + d);
+                const float4 o0 = o[0], o1 = o[1];
+                v[0] += o0.x, v[1] += o0.y, v[2] += o0.z, v[3] += o0.w;
+                v[4] += o1.x, v[5] += o1.y, v[6] += o1.z, v[7] += o1.w;
+            }
+            if (whole) {
+                const float inv = 1.f / l;
+#pragma unroll
+                for (int k = 0; k < 8; ++k)
+                    v[k] *= inv;
+                *reinterpret_cast<uint4 *>(a.out + at.b * a.out_ld + (head + hd) * D + d) = bf16x8(v);
+            } else {
+                const long long s = (2ll * blockIdx.x + part) * 8 * NT + hd;
+                float4 *o = reinterpret_cast<float4 *>(a.part_o + s * D + d);
+                o[0] = make_float4(v[0], v[1], v[2], v[3]);
+                o[1] = make_float4(v[4], v[5], v[6], v[7]);
+                if (d == 0)
+                    *reinterpret_cast<float2 *>(a.part_ml + 2 * s) = make_float2(m, l);
+            }
+        }
+        part = 1;  // of a CTA's stretches only the first and the last can be parts
+        cur += t1 - t0;
+        at.t = 0;
+        if (++at.u == a.units && cur < end)
+            next_sequence(a, at);
+    }
+}
+
+// Joins the parts of one sequence's query head, a thread per value.
+template <int D, int NT>
+__global__ void __launch_bounds__(D) join_kernel(const DecodeArgs a)
+{
+    __shared__ long long red[2][D / 32];
+    const int b = blockIdx.x, h = blockIdx.y, d = threadIdx.x, lane = d & 31;
+    overlap_trigger();
+    overlap_wait();
+    long long before = 0, total = 0;
+    for (int i = d; i < a.B; i += D) {
+        const int n = tiles_of(a, i);
+        total += n;
+        before += i < b ? n : 0;
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+        before += __shfl_xor_sync(0xffffffffu, before, o);
+        total += __shfl_xor_sync(0xffffffffu, total, o);
+    }
+    if (lane == 0) {
+        red[0][d >> 5] = before;
+        red[1][d >> 5] = total;
+    }
+    __syncthreads();
+    before = total = 0;
+#pragma unroll
+    for (int w = 0; w < D / 32; ++w) {
+        before += red[0][w];
+        total += red[1][w];
+    }
+    const int nt = tiles_of(a, b);
+    if (nt == 0)
+        return;
+    const int kvh = h / a.group, hh = h - kvh * a.group, chunk = hh / (8 * NT);
+    const long long share = share_of(a, total * a.units);
+    const long long s = before * a.units + (long long)(kvh * a.chunks + chunk) * nt, e = s + nt;
+    const int c0 = (int)(s / share), c1 = (int)((e - 1) / share);
+    if (c0 == c1)
+        return;  // written by its CTA
+    const int hd = hh - chunk * 8 * NT;
+    // CTA c's stretch of this unit is its first one if the CTA's tiles start inside the unit
+    auto slot = [&](int c) { return (2ll * c + (c * share >= s ? 0 : 1)) * 8 * NT + hd; };
+    float m = -INFINITY;
+    for (int c = c0; c <= c1; ++c)
+        m = fmaxf(m, __ldcg(a.part_ml + 2 * slot(c)));
+    const float base = finite_base(m);
+    float l = 0.f, v = 0.f;
+#pragma unroll 4
+    for (int c = c0; c <= c1; ++c) {
+        const long long at = slot(c);
+        const float2 x = __ldcg(reinterpret_cast<const float2 *>(a.part_ml + 2 * at));
+        const float f = ex2(x.x - base);
+        l = fmaf(x.y, f, l);
+        v = fmaf(__ldcg(a.part_o + at * D + d), f, v);
+    }
+    a.out[b * a.out_ld + (long long)h * D + d] = __bfloat16_as_ushort(__float2bfloat16_rn(v / l));
+}
+
+// ---------------------------------------------------------------- host side
+
+MoeStatus bad(MoeStatus s, const char *msg) { return (MoeStatus)set_last_error(s, msg); }
+
+int head_tiles(int group) { return group <= 8 ? 1 : 2; }
+
+// pages as {values of 128 bytes, rows of a page's heads, halves of a row, pages}
+cudaError_t cache_map(CUtensorMap *m, const void *base, const MoeKvCache *c)
+{
+    auto enc = tensor_map_encoder();
+    if (!enc)
+        return cudaErrorNotSupported;
+    const bool mx = c->type == MOE_ROWS_MXFP8;
+    const int size = mx ? 1 : 2, inner = mx ? c->head_dim : 64, parts = c->head_dim / inner;
+    const long long row = (long long)c->head_dim * size, rows = (long long)c->n_kv_heads * c->page_size;
+    const cuuint64_t dims[4] = {(cuuint64_t)inner, (cuuint64_t)rows, (cuuint64_t)parts, (cuuint64_t)c->n_pages};
+    const cuuint64_t strides[3] = {(cuuint64_t)row, (cuuint64_t)(parts > 1 ? 128 : row), (cuuint64_t)(rows * row)};
+    const cuuint32_t box[4] = {(cuuint32_t)inner, (cuuint32_t)(c->page_size < TILE ? c->page_size : TILE),
+                               (cuuint32_t)parts, 1};
+    const cuuint32_t step[4] = {1, 1, 1, 1};
+    const CUresult r = enc(m, mx ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4,
+                           const_cast<void *>(base), dims, strides, box, step, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                           inner * size == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+                           CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
+}
+
+template <int D, int NT, bool MX>
+cudaError_t launch_decode(const DecodeArgs &a, const CUtensorMap &mk, const CUtensorMap &mv, cudaStream_t st)
+{
+    using G = Geo<D, NT, MX>;
+    auto kern = decode_kernel<D, NT, MX>;
+    static std::atomic<int> attr_set[MAX_DEVICES];
+    cudaError_t e = smem_limit_once(attr_set, (const void *)kern, G::SMEM);
+    if (e != cudaSuccess)
+        return e;
+    if ((e = launch_overlapped(kern, (unsigned)a.ctas, THREADS, G::SMEM, 1, st, a, mk, mv)) != cudaSuccess)
+        return e;
+    if (a.cap <= TILE)  // one tile a sequence and head: nothing is ever shared
+        return cudaSuccess;
+    return launch_overlapped(join_kernel<D, NT>, dim3((unsigned)a.B, (unsigned)a.heads), D, 0, 1, st, a);
+}
+
+size_t part_bytes(int heads_of_part, int D) { return (size_t)2 * sm_count() * heads_of_part * (D + 2) * 4; }
+
+bool heads_fit(int n_heads, int n_kv_heads)
+{
+    return n_heads >= 1 && n_heads <= ATTN_MAX_HEADS && n_kv_heads >= 1 && n_heads % n_kv_heads == 0;
+}
+
+}  // namespace
+
+}  // namespace moe
+
+using namespace moe;
+
+extern "C" size_t moe_attention_decode_workspace_bytes(int B, int n_heads, int n_kv_heads, int head_dim)
+{
+    if (B < 1 || B > 65536 || !heads_fit(n_heads, n_kv_heads) || (head_dim != 64 && head_dim != 128))
+        return 0;
+    return part_bytes(8 * head_tiles(n_heads / n_kv_heads), head_dim);
+}
+
+extern "C" MoeStatus moe_attention_decode(const MoeKvCache *cache, const void *q, long long q_ld, int B, int n_heads,
+                                          const int32_t *page_table, int max_pages, const int32_t *lens, float scale,
+                                          void *out, long long out_ld, void *workspace, size_t ws_bytes,
+                                          void *cuda_stream)
+{
+    char msg[160];
+    const MoeStatus s = check_kv_cache(cache);
+    if (s != MOE_OK)
+        return s;
+    const int D = cache->head_dim;
+    if (B < 0 || B > 65536) {
+        snprintf(msg, sizeof msg, "B = %d out of range [0, 65536]", B);
+        return bad(MOE_EINVAL, msg);
+    }
+    if (!heads_fit(n_heads, cache->n_kv_heads)) {
+        snprintf(msg, sizeof msg, "n_heads (%d) must be a multiple of the cache's %d heads and at most %d", n_heads,
+                 cache->n_kv_heads, ATTN_MAX_HEADS);
+        return bad(MOE_EINVAL, msg);
+    }
+    if (max_pages < 1 || (long long)max_pages * cache->page_size > 0x7FFFFFFFll)
+        return bad(MOE_EINVAL, "moe_attention_decode: max_pages below 1, or 2^31 tokens and more");
+    if (!(scale > 0.f) || !isfinite(scale * 1.4427f))
+        return bad(MOE_EINVAL, "moe_attention_decode: scale must be finite and above 0");
+    if (B == 0)
+        return MOE_OK;
+    if (!q || !page_table || !lens || !out)
+        return bad(MOE_EINVAL, "moe_attention_decode: NULL q, page_table, lens or out");
+    if (q_ld < (long long)n_heads * D || out_ld < (long long)n_heads * D)
+        return bad(MOE_EINVAL, "moe_attention_decode: a row stride is below the row's values");
+    if (!rows_16b(q, q_ld) || !rows_16b(out, out_ld) || (uintptr_t)page_table % 4 || (uintptr_t)lens % 4)
+        return bad(MOE_EINVAL, "moe_attention_decode: rows must start on 16-byte boundaries, page_table and lens on "
+                               "4-byte ones");
+    const int group = n_heads / cache->n_kv_heads, nt = head_tiles(group);
+    const size_t need = part_bytes(8 * nt, D);
+    if (!workspace || ws_bytes < need || (uintptr_t)workspace % 256) {
+        snprintf(msg, sizeof msg, "moe_attention_decode: workspace of %zu bytes, 256-byte aligned, is needed", need);
+        return bad(MOE_EWORKSPACE, msg);
+    }
+    DecodeArgs a{};
+    CUtensorMap mk, mv;
+    cudaError_t e = attention_error_flag(&a.err);
+    if (e == cudaSuccess)
+        e = cache_map(&mk, cache->k, cache);
+    if (e == cudaSuccess)
+        e = cache_map(&mv, cache->v, cache);
+    if (e == cudaSuccess) {
+        a.q = static_cast<const uint16_t *>(q);
+        a.q_ld = q_ld;
+        a.table = page_table;
+        a.max_pages = max_pages;
+        a.lens = lens;
+        a.cap = (long long)max_pages * cache->page_size;
+        a.B = B;
+        a.heads = n_heads;
+        a.kv = cache->n_kv_heads;
+        a.group = group;
+        a.chunks = (group + 8 * nt - 1) / (8 * nt);
+        a.units = a.kv * a.chunks;
+        a.n_pages = cache->n_pages;
+        while ((1 << a.page_log2) < cache->page_size)
+            ++a.page_log2;
+        a.ks = static_cast<const uint8_t *>(cache->k_scales);
+        a.vs = static_cast<const uint8_t *>(cache->v_scales);
+        a.scale = scale * 1.44269504088896340736f;
+        a.out = static_cast<uint16_t *>(out);
+        a.out_ld = out_ld;
+        a.ctas = gemm::sm_count();
+        a.part_o = static_cast<float *>(workspace);
+        a.part_ml = a.part_o + (size_t)2 * a.ctas * 8 * nt * D;
+        cudaStream_t st = (cudaStream_t)cuda_stream;
+        const bool mx = cache->type == MOE_ROWS_MXFP8;
+        if (D == 128)
+            e = nt == 1 ? (mx ? launch_decode<128, 1, true>(a, mk, mv, st) : launch_decode<128, 1, false>(a, mk, mv, st))
+                        : (mx ? launch_decode<128, 2, true>(a, mk, mv, st) : launch_decode<128, 2, false>(a, mk, mv, st));
+        else
+            e = nt == 1 ? (mx ? launch_decode<64, 1, true>(a, mk, mv, st) : launch_decode<64, 1, false>(a, mk, mv, st))
+                        : (mx ? launch_decode<64, 2, true>(a, mk, mv, st) : launch_decode<64, 2, false>(a, mk, mv, st));
+    }
+    if (e != cudaSuccess) {
+        snprintf(msg, sizeof msg, "decode attention launch: %s", cudaGetErrorString(e));
+        return bad(MOE_ECUDA, msg);
+    }
+    return MOE_OK;
+}

@@ -1,0 +1,679 @@
+// attention_prompt.cu -- causal attention within packed prompts (moe_attention_prompt, include/moe.h) on the
+// 5th-generation tensor cores.
+//
+//   S = Q K^T,  P = 2^(scale log2(e) S - m),  O = sum of P V over the key tiles,  out = O / sum of P
+// with m a row's running maximum: one pass over the keys, nothing of S or P leaves the SM.
+//
+// A CTA has 256 rows as two tiles of 128: 128 / group tokens (rounded down) of a tile times the `group` query heads of
+// one key head, so that short sequences fill tiles too and a key tile is loaded once for all heads that read it.  It
+// goes over the keys of its sequence in tiles of 128 up to its last token.  Warps: 0-3 and 4-7 the softmax of either
+// tile (a thread per row), 8 issues the MMAs, 9 loads by TMA, 10 and 11 look after values that no row may see (below).
+// Tensor memory: S of both tiles (128 columns each; P overwrites its tile's S as BF16) and O of both.  MMAs go in the
+// order S0 S1 | PV0 S0' | PV1 S1' | ..., so that one tile's softmax runs under the other tile's products, and a tile's
+// next S, which comes after its PV in the same queue, says that this PV is done: O may then be touched without a wait.
+// The maximum in use is kept until a row exceeds it by 2^8 (P is then up to 2^8, in BF16's and FP32's range alike):
+// rescaling O in tensor memory, which would be needed in every tile, becomes rare.
+//
+// Bound by the tensor pipe for long prompts: 512 flops per key, row and 128 values, of which the tile's exponentials
+// (128 a row) take about as long as half of its MMAs.
+//
+// Masked values: P is 0 there, but 0 * inf is not.  Two warps clear the rows of V past the sequence's end, and values
+// that are not finite in tiles that some row must not see in full; rows that may see such a value get it added at the
+// end.  CTAs are numbered from the last rows of the longest sequences down, so that the short ones fill the gaps.
+#include <math.h>
+#include <stdio.h>
+
+#include "attention_internal.cuh"
+#include "gemm_common.cuh"
+#include "mx_encode.cuh"
+#include "overlap.cuh"
+
+namespace moe {
+
+namespace {
+
+using namespace gemm;
+
+constexpr int BM = 128, BN = 128;    // rows of a tile, keys of a tile
+constexpr int THREADS = 384;
+constexpr int WARP_MMA = 8, WARP_LOAD = 9, WARP_GUARD = 10;
+constexpr int GUARDS = 2;
+constexpr int MASKED = 3;            // key tiles that 256 rows' tokens can lie in
+constexpr int TMEM_COLS = 512;
+constexpr float GROWTH = 8.f;        // log2 by which a row's maximum may exceed the one in use
+
+struct PromptArgs {
+    const int32_t *offsets;
+    int n_seqs, T;
+    int heads, kv, group, tile_tokens;  // tokens of a tile
+    const uint16_t *v;
+    long long v_ld;
+    float scale;                        // times log2(e)
+    uint16_t *out;
+    long long out_ld;
+    int *err;
+};
+
+template <int D> struct PGeo {
+    static constexpr int TILE_B = 128 * D * 2;              // 128 rows
+    static constexpr int SLOTS = D == 128 ? 5 : 8;          // key and value tiles
+    static_assert(SLOTS >= 2 * MASKED - 1, "see the loader");
+    static constexpr int RING_OFF = 2 * TILE_B;
+    static constexpr int BAR_OFF = RING_OFF + SLOTS * TILE_B;
+    static constexpr int N_BARS = 1 + 2 * SLOTS + 2 * MASKED + 6 + 1;
+    static constexpr int SMEM = BAR_OFF + N_BARS * 8 + 1024;  // + alignment slack
+    static_assert(SMEM <= 226 * 1024, "shared memory");
+};
+
+__device__ __forceinline__ float ex2(float x)
+{
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+__device__ __forceinline__ void fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
+
+__device__ __forceinline__ void commit(uint64_t *bar)
+{
+    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_addr(bar))
+                 : "memory");
+}
+
+// K-major operand, 128-byte swizzle, 8-row groups 1024 bytes apart
+__device__ __forceinline__ uint64_t desc_k(uint32_t saddr)
+{
+    return (uint64_t)((saddr & 0x3FFFFu) >> 4) | (1ull << 16) | (64ull << 32) | (1ull << 46) | (2ull << 61);
+}
+
+// The other major: 64 values of N side by side in 128 bytes, rows of K 128 bytes apart (8-row groups 1024), the next 64
+// values of N a tile half (16 KB) on
+__device__ __forceinline__ uint64_t desc_n(uint32_t saddr)
+{
+    return (uint64_t)((saddr & 0x3FFFFu) >> 4) | (1024ull << 16) | (64ull << 32) | (1ull << 46) | (2ull << 61);
+}
+
+// kind::f16, BF16 operands, FP32 accumulator, M = 128
+constexpr uint32_t instr_desc(int n, bool b_n_major)
+{
+    return (1u << 4) | (1u << 7) | (1u << 10) | (b_n_major ? 1u << 16 : 0u) | ((uint32_t)(n >> 3) << 17) |
+           ((uint32_t)(BM >> 4) << 24);
+}
+
+__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc)
+{
+    asm volatile("{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
+                 " tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(d),
+                 "l"(a), "l"(b), "r"(idesc), "r"(acc)
+                 : "memory");
+}
+
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t acc)
+{
+    asm volatile("{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
+                 " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d),
+                 "r"(a), "l"(b), "r"(idesc), "r"(acc)
+                 : "memory");
+}
+
+#define MOE_R8(r, o) "=r"(r[o]), "=r"(r[o + 1]), "=r"(r[o + 2]), "=r"(r[o + 3]), "=r"(r[o + 4]), "=r"(r[o + 5]), \
+                     "=r"(r[o + 6]), "=r"(r[o + 7])
+#define MOE_I8(r, o) "r"(r[o]), "r"(r[o + 1]), "r"(r[o + 2]), "r"(r[o + 3]), "r"(r[o + 4]), "r"(r[o + 5]), \
+                     "r"(r[o + 6]), "r"(r[o + 7])
+
+// 32 columns of this warp's 32 lanes (the load still has to be waited for)
+__device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t *r)
+{
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,"
+                 "%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+                 : MOE_R8(r, 0), MOE_R8(r, 8), MOE_R8(r, 16), MOE_R8(r, 24)
+                 : "r"(taddr));
+}
+
+__device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t *r)
+{
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+                 "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(taddr),
+                 MOE_I8(r, 0), MOE_I8(r, 8), MOE_I8(r, 16), MOE_I8(r, 24)
+                 : "memory");
+}
+
+__device__ __forceinline__ void wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
+__device__ __forceinline__ void wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+__device__ __forceinline__ void tma_4d(void *dst, const CUtensorMap *map, int x, int y, int z, int w, uint64_t *bar)
+{
+    asm volatile(
+        "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, "
+        "%5}], [%6];" ::"r"(smem_addr(dst)),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(w), "r"(smem_addr(bar))
+        : "memory");
+}
+
+// ---------------------------------------------------------------- which rows
+
+struct Span {
+    int start, len;
+};
+
+__device__ __forceinline__ Span sequence(const PromptArgs &a, int b)
+{
+    const int s = min(max(__ldcg(a.offsets + b), 0), a.T), e = min(max(__ldcg(a.offsets + b + 1), s), a.T);
+    return {s, e - s};
+}
+
+// A CTA's work: tokens from tok0 (within the sequence) on and a key head; len == 0: none
+struct Item {
+    int start, len, tok0, kvh;
+};
+
+__device__ __forceinline__ int block_sum(int v, int *red)
+{
+    v = __reduce_add_sync(0xffffffffu, v);
+    __syncthreads();
+    if ((threadIdx.x & 31) == 0)
+        red[threadIdx.x >> 5] = v;
+    __syncthreads();
+    int s = 0;
+#pragma unroll
+    for (int w = 0; w < THREADS / 32; ++w)
+        s += red[w];
+    return s;
+}
+
+// Item i of the list that holds, from the highest level down, the level-th CTA of every sequence that has one.  Every
+// thread of the CTA takes part.
+__device__ __forceinline__ Item find_item(const PromptArgs &a, int i, int *red, Item *found)
+{
+    const int per_cta = 2 * a.tile_tokens, tid = threadIdx.x;
+    const int chunk = (a.n_seqs + THREADS - 1) / THREADS, b0 = min(a.n_seqs, tid * chunk);
+    const int b1 = min(a.n_seqs, b0 + chunk);
+    auto above = [&](int level) {  // CTAs at this level and above
+        int s = 0;
+        for (int b = b0; b < b1; ++b)
+            s += max(0, (sequence(a, b).len + per_cta - 1) / per_cta - level);
+        return block_sum(s, red) * a.kv;
+    };
+    int lo = 0, hi = (a.T + per_cta - 1) / per_cta;  // above(lo) > i >= above(hi)
+    if (above(0) <= i)
+        return {0, 0, 0, 0};
+    int over = 0;  // above(hi)
+    while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1, n = above(mid);
+        if (n > i) {
+            lo = mid;
+        } else {
+            hi = mid;
+            over = n;
+        }
+    }
+    const int rank = (i - over) / a.kv, kvh = (i - over) - rank * a.kv;
+    // the rank-th sequence with more than lo CTAs
+    int mine = 0;
+    for (int b = b0; b < b1; ++b)
+        mine += sequence(a, b).len > lo * per_cta;
+    int incl = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int n = __shfl_up_sync(0xffffffffu, incl, o);
+        incl += (tid & 31) >= o ? n : 0;
+    }
+    __syncthreads();
+    if ((tid & 31) == 31)
+        red[tid >> 5] = incl;
+    __syncthreads();
+    int pre = incl - mine;
+    for (int w = 0; w < (tid >> 5); ++w)
+        pre += red[w];
+    if (tid == 0)
+        *found = {0, 0, 0, 0};  // (stays where offsets that do not ascend have no such sequence)
+    __syncthreads();
+    if (pre <= rank && rank < pre + mine) {
+        for (int b = b0; b < b1; ++b) {
+            const Span s = sequence(a, b);
+            if (s.len > lo * per_cta && pre++ == rank) {
+                *found = {s.start, s.len, lo * per_cta, kvh};
+                break;
+            }
+        }
+    }
+    __syncthreads();
+    return *found;
+}
+
+// ---------------------------------------------------------------- kernel
+
+template <int D>
+__global__ void __launch_bounds__(THREADS, 1)
+    prompt_kernel(const __grid_constant__ PromptArgs a, const __grid_constant__ CUtensorMap map_q,
+                  const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v)
+{
+    using G = PGeo<D>;
+    extern __shared__ uint8_t smem_dyn[];
+    __shared__ int red[THREADS / 32];
+    __shared__ Item found;
+    __shared__ uint32_t tmem_word;
+    __shared__ int abort_word, odd_word;  // odd: a value that is not finite has been cleared
+    volatile int *abort_flag = &abort_word;
+    uint8_t *smem = smem_dyn + ((1024u - (smem_addr(smem_dyn) & 1023u)) & 1023u);
+    uint64_t *q_full = reinterpret_cast<uint64_t *>(smem + G::BAR_OFF), *full = q_full + 1, *empty = full + G::SLOTS;
+    uint64_t *v_land = empty + G::SLOTS, *v_clear = v_land + MASKED, *s_full = v_clear + MASKED, *p_full = s_full + 2;
+    uint64_t *o_full = p_full + 2, *end_bar = o_full + 2;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+
+    overlap_wait();
+    const Item item = find_item(a, blockIdx.x, red, &found);
+    if (item.len == 0)
+        return;
+    if (tid == 0) {
+        mbar_init(q_full, 1);
+        for (int i = 0; i < G::SLOTS; ++i) {
+            mbar_init(&full[i], 1);
+            mbar_init(&empty[i], 1);
+        }
+        for (int i = 0; i < MASKED; ++i) {
+            mbar_init(&v_land[i], 1);
+            mbar_init(&v_clear[i], GUARDS);
+        }
+        for (int t = 0; t < 2; ++t) {
+            mbar_init(&s_full[t], 1);
+            mbar_init(&p_full[t], 4);
+            mbar_init(&o_full[t], 1);
+        }
+        mbar_init(end_bar, 1);
+        abort_word = odd_word = 0;
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+        fence_proxy_async();
+    }
+    if (warp == WARP_MMA) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_addr(&tmem_word)),
+                     "r"(TMEM_COLS)
+                     : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    }
+    fence_before();
+    __syncthreads();
+    fence_after();
+    // (only now: a kernel that starts here may want tensor memory too, and waits for this one's end while it holds it)
+    overlap_trigger();
+    const uint32_t tmem = tmem_word;
+    // key tiles of either row tile; those from `masked` on hold keys that some row must not see
+    const int last = item.len - 1;
+    const int n0 = min(last, item.tok0 + a.tile_tokens - 1) / BN + 1;
+    const int n1 = item.tok0 + a.tile_tokens > last ? 0 : min(last, item.tok0 + 2 * a.tile_tokens - 1) / BN + 1;
+    const int n = max(n0, n1), masked = item.tok0 / BN;
+
+    if (warp == WARP_LOAD) {
+        // ------------------------------------------------------ tiles -> shared memory
+        if (lane == 0) {
+            const int rows = a.group * a.tile_tokens, both = n1 > 0 ? 2 : 1;
+            mbar_arrive_expect_tx(q_full, both * rows * D * 2);
+            for (int t = 0; t < both; ++t)
+                for (int h = 0; h < D / 64; ++h)
+                    tma_4d(smem + t * G::TILE_B + h * (BM * 128), &map_q, 0, item.kvh * a.group,
+                           item.start + item.tok0 + t * a.tile_tokens, h, q_full);
+        }
+        // K0 V0 K1 V1 ...  The values of the masked tiles land on barriers of their own, where the guards wait for them
+        // (a waiter that skipped phases of a slot's barrier could take an older one for its own); no slot of these last
+        // tiles is used again.
+        int slot = 0, it = 0;
+        uint32_t ph = 0;
+        for (; it < 2 * n; ++it) {
+            const int j = it >> 1;
+            const bool is_v = it & 1;
+            if (!mbar_wait_sleep_warp(&empty[slot], ph ^ 1, abort_flag, a.err, lane))
+                break;
+            if (lane == 0) {
+                uint64_t *bar = is_v && j >= masked ? &v_land[j - masked] : &full[slot];
+                mbar_arrive_expect_tx(bar, G::TILE_B);
+                tma_4d(smem + G::RING_OFF + slot * G::TILE_B, is_v ? &map_v : &map_k, 0, item.kvh, item.start + j * BN, 0,
+                       bar);
+            }
+            if (++slot == G::SLOTS) {
+                slot = 0;
+                ph ^= 1;
+            }
+        }
+        // every copy has landed before the CTA ends (at once on the normal path; bounded)
+        if (lane == 0) {
+            mbar_drain(q_full, 0);
+            for (int i = it > G::SLOTS ? it - G::SLOTS : 0; i < it; ++i) {
+                if ((i & 1) && (i >> 1) >= masked)
+                    mbar_drain(&v_land[(i >> 1) - masked], 0);
+                else
+                    mbar_drain(&full[i % G::SLOTS], (i / G::SLOTS) & 1);
+            }
+        }
+        __syncwarp();
+    } else if (warp >= WARP_GUARD) {
+        // ------------------------------------------------------ values that no row, or not every row, may see
+        for (int j = masked; j < n; ++j) {
+            if (!mbar_wait_sleep_warp(&v_land[j - masked], 0, abort_flag, a.err, lane))
+                break;
+            uint8_t *tile = smem + G::RING_OFF + (2 * j + 1) % G::SLOTS * G::TILE_B;
+            const int held = item.len - j * BN;  // rows of the tile within the sequence
+            bool odd = false;
+            for (int i = (warp - WARP_GUARD) * 32 + lane; i < G::TILE_B / 16; i += GUARDS * 32) {
+                uint4 *p = reinterpret_cast<uint4 *>(tile) + i;
+                uint4 v = *p;
+                if (i / 8 % BN >= held) {
+                    *p = make_uint4(0, 0, 0, 0);
+                    continue;
+                }
+                uint32_t *w = reinterpret_cast<uint32_t *>(&v);
+                bool bad = false;
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    if ((w[k] & 0x7F80u) == 0x7F80u) {
+                        w[k] &= 0xFFFF0000u;
+                        bad = true;
+                    }
+                    if ((w[k] & 0x7F800000u) == 0x7F800000u) {
+                        w[k] &= 0xFFFFu;
+                        bad = true;
+                    }
+                }
+                if (bad) {
+                    *p = v;
+                    odd = true;
+                }
+            }
+            if (odd)
+                odd_word = 1;
+            __threadfence_block();
+            fence_proxy_async();
+            __syncwarp();
+            if (lane == 0)
+                mbar_arrive(&v_clear[j - masked]);
+        }
+        __syncwarp();
+    } else if (warp == WARP_MMA) {
+        // ------------------------------------------------------ MMAs: the warp runs the loop, one elected lane issues
+        uint32_t elected;
+        asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xFFFFFFFF;\n selp.u32 %0, 1, 0, p;\n}" : "=r"(elected));
+        auto wait = [&](uint64_t *bar, uint32_t par) {
+            return __all_sync(0xffffffffu, mbar_wait(bar, par, abort_flag, a.err)) != 0;
+        };
+        const uint64_t dq = desc_k(smem_addr(smem)), dk = desc_k(smem_addr(smem + G::RING_OFF));
+        const uint64_t dv = desc_n(smem_addr(smem + G::RING_OFF));
+        constexpr uint64_t TILE16 = G::TILE_B / 16, HALF16 = BM * 128 / 16;
+        auto scores = [&](int t, int slot) {  // S of row tile t and the keys in the slot
+            if (elected) {
+#pragma unroll
+                for (int k = 0; k < D / 16; ++k) {
+                    const uint64_t o = (k / 4) * HALF16 + (k % 4) * 2;
+                    mma_ss(tmem + t * BN, dq + t * TILE16 + o, dk + slot * TILE16 + o, instr_desc(BN, false), k > 0);
+                }
+                commit(&s_full[t]);
+            }
+            __syncwarp();
+        };
+        bool ok = wait(q_full, 0) && wait(&full[0], 0);
+        fence_after();
+        if (ok) {
+            scores(0, 0);
+            if (n1 > 0)
+                scores(1, 0);
+            if (elected)
+                commit(&empty[0]);
+            __syncwarp();
+        }
+        int it = 1;  // the value tile's place in the loader's order
+        for (int j = 0; ok && j < n; ++j, it += 2) {
+            const int vs = it % G::SLOTS, ks = (it + 1) % G::SLOTS;
+            const uint32_t vph = (it / G::SLOTS) & 1, kph = ((it + 1) / G::SLOTS) & 1;
+            if (!(ok = j >= masked ? wait(&v_clear[j - masked], 0) : wait(&full[vs], vph)))
+                break;
+            if (j + 1 < n && !(ok = wait(&full[ks], kph)))
+                break;
+#pragma unroll
+            for (int t = 0; t < 2; ++t) {
+                const int nt = t ? n1 : n0;
+                if (j >= nt)
+                    continue;
+                if (!(ok = ok && wait(&p_full[t], j & 1)))
+                    break;
+                fence_after();
+                if (elected) {
+#pragma unroll
+                    for (int k = 0; k < BN / 16; ++k)
+                        mma_ts(tmem + 2 * BN + t * D, tmem + t * BN + 8 * k, dv + vs * TILE16 + k * (16 * 128 / 16),
+                               instr_desc(D, true), j > 0 || k > 0);
+                    if (j + 1 == nt)
+                        commit(&o_full[t]);
+                }
+                __syncwarp();
+                if (j + 1 < nt)
+                    scores(t, ks);
+            }
+            if (elected) {
+                commit(&empty[vs]);
+                if (j + 1 < n)
+                    commit(&empty[ks]);
+            }
+            __syncwarp();
+        }
+        // also after an abort: what was issued has completed before the tensor memory is freed
+        if (elected) {
+            commit(end_bar);
+            mbar_drain(end_bar, 0);
+        }
+        __syncwarp();
+    } else {
+        // ------------------------------------------------------ softmax: a thread per row
+        const int t = warp >> 2, row = (warp & 3) * 32 + lane, nt = t ? n1 : n0;
+        const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
+        const uint32_t ts = tmem + lanes + t * BN, to = tmem + lanes + 2 * BN + t * D;
+        const int tok = item.tok0 + t * a.tile_tokens + row / a.group;  // within the sequence
+        const bool valid = row < a.group * a.tile_tokens && tok < item.len;
+        const int sees = valid ? tok + 1 : 0x40000000;  // keys that the row sees
+        float m = -INFINITY, l = 0.f;                   // m: of scaled scores, the one in use
+        bool ok = true;
+        for (int j = 0; j < nt; ++j) {
+            if (!(ok = __all_sync(0xffffffffu, mbar_wait(&s_full[t], j & 1, abort_flag, a.err)) != 0))
+                break;
+            fence_after();
+            uint32_t s[BN];
+#pragma unroll
+            for (int c = 0; c < BN; c += 32)
+                tmem_ld32(ts + c, s + c);
+            wait_ld();
+            if (j >= masked) {
+                const int vis = sees - j * BN;
+#pragma unroll
+                for (int c = 0; c < BN; ++c)
+                    s[c] = c < vis ? s[c] : 0xFF800000u;
+            }
+            float mx = __uint_as_float(s[0]);
+#pragma unroll
+            for (int c = 1; c < BN; ++c)
+                mx = fmaxf(mx, __uint_as_float(s[c]));
+            mx *= a.scale;
+            const bool grown = mx > m + GROWTH && valid;
+            if (j == 0) {
+                m = mx;
+            } else if (__any_sync(0xffffffffu, grown)) {
+                const float next = grown ? mx : m, f = ex2(m - (next == -INFINITY ? 0.f : next));
+                m = next;
+                l *= f;
+#pragma unroll 1
+                for (int c = 0; c < D; c += 32) {
+                    uint32_t o[32];
+                    tmem_ld32(to + c, o);
+                    wait_ld();
+#pragma unroll
+                    for (int i = 0; i < 32; ++i)
+                        o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
+                    tmem_st32(to + c, o);
+                }
+            }
+            const float base = m == -INFINITY ? 0.f : m;
+            float sum[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int c = 0; c < BN; c += 64) {
+                uint32_t p[32];
+#pragma unroll
+                for (int i = 0; i < 32; ++i) {
+                    const float p0 = ex2(fmaf(__uint_as_float(s[c + 2 * i]), a.scale, -base));
+                    const float p1 = ex2(fmaf(__uint_as_float(s[c + 2 * i + 1]), a.scale, -base));
+                    sum[i & 3] += p0 + p1;
+                    // rounded to BF16 for the product (2^-9 of each, of random sign): v is BF16, and an MMA's
+                    // operands share a type
+                    p[i] = bf16_pair(p0, p1);
+                }
+                tmem_st32(ts + c / 2, p);
+            }
+            l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+            wait_st();
+            fence_before();
+            __syncwarp();
+            if (lane == 0)
+                mbar_arrive(&p_full[t]);
+        }
+        ok = ok && nt > 0 && __all_sync(0xffffffffu, mbar_wait(&o_full[t], 0, abort_flag, a.err)) != 0;
+        if (ok) {
+            fence_after();
+            const float inv = 1.f / l;
+            const bool odd = *static_cast<volatile int *>(&odd_word) != 0;
+            const int at = item.start + tok;
+            uint16_t *out = a.out + at * a.out_ld + (long long)(item.kvh * a.group + row % a.group) * D;
+#pragma unroll 1
+            for (int c = 0; c < D; c += 32) {
+                uint32_t o[32];
+                tmem_ld32(to + c, o);
+                wait_ld();
+                if (valid) {
+                    float v[32];
+#pragma unroll
+                    for (int i = 0; i < 32; ++i)
+                        v[i] = __uint_as_float(o[i]) * inv;
+                    if (odd) {  // what the guards cleared, for the rows that see it
+                        for (int k = masked * BN; k <= tok; ++k) {
+                            const uint16_t *p = a.v + (item.start + k) * a.v_ld + (long long)item.kvh * D + c;
+#pragma unroll
+                            for (int i = 0; i < 32; ++i) {
+                                const float x = __uint_as_float((uint32_t)__ldcg(p + i) << 16);
+                                v[i] += isfinite(x) ? 0.f : x;
+                            }
+                        }
+                    }
+#pragma unroll
+                    for (int i = 0; i < 32; i += 8)
+                        *reinterpret_cast<uint4 *>(out + c + i) = bf16x8(v + i);
+                }
+            }
+            fence_before();
+        }
+    }
+    __syncthreads();
+    if (warp == WARP_MMA) {
+        fence_after();
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(TMEM_COLS) : "memory");
+    }
+}
+
+// ---------------------------------------------------------------- host side
+
+MoeStatus bad(MoeStatus s, const char *msg) { return (MoeStatus)set_last_error(s, msg); }
+
+// rows as {64 values, heads, rows, 64-value parts of a head}, boxes of {64, box_heads, box_rows, parts}
+cudaError_t rows_map(CUtensorMap *m, const void *base, long long ld, int T, int heads, int D, int box_heads,
+                     int box_rows, int box_parts)
+{
+    auto enc = tensor_map_encoder();
+    if (!enc)
+        return cudaErrorNotSupported;
+    const cuuint64_t dims[4] = {64, (cuuint64_t)heads, (cuuint64_t)T, (cuuint64_t)(D / 64)};
+    const cuuint64_t strides[3] = {(cuuint64_t)D * 2, (cuuint64_t)ld * 2, 128};
+    const cuuint32_t box[4] = {64, (cuuint32_t)box_heads, (cuuint32_t)box_rows, (cuuint32_t)box_parts};
+    const cuuint32_t step[4] = {1, 1, 1, 1};
+    const CUresult r = enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void *>(base), dims, strides, box, step,
+                           CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                           CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
+}
+
+template <int D>
+cudaError_t launch_prompt(const PromptArgs &a, const void *q, long long q_ld, const void *k, long long k_ld,
+                          cudaStream_t st)
+{
+    auto kern = prompt_kernel<D>;
+    static std::atomic<int> attr_set[MAX_DEVICES];
+    CUtensorMap mq, mk, mv;
+    cudaError_t e = smem_limit_once(attr_set, (const void *)kern, PGeo<D>::SMEM);
+    if (e == cudaSuccess)
+        e = rows_map(&mq, q, q_ld, a.T, a.heads, D, a.group, a.tile_tokens, 1);
+    if (e == cudaSuccess)
+        e = rows_map(&mk, k, k_ld, a.T, a.kv, D, 1, BN, D / 64);
+    if (e == cudaSuccess)
+        e = rows_map(&mv, a.v, a.v_ld, a.T, a.kv, D, 1, BN, D / 64);
+    if (e != cudaSuccess)
+        return e;
+    // at most this many: every sequence rounds up to whole CTAs
+    const long long grid = ((long long)a.T / (2 * a.tile_tokens) + a.n_seqs) * a.kv;
+    return launch_overlapped(kern, (unsigned)grid, THREADS, PGeo<D>::SMEM, 1, st, a, mq, mk, mv);
+}
+
+}  // namespace
+
+}  // namespace moe
+
+using namespace moe;
+
+extern "C" MoeStatus moe_attention_prompt(const void *q, long long q_ld, const void *k, long long k_ld, const void *v,
+                                          long long v_ld, int T, const int32_t *offsets, int n_seqs, int n_heads,
+                                          int n_kv_heads, int head_dim, float scale, void *out, long long out_ld,
+                                          void *cuda_stream)
+{
+    char msg[160];
+    const int D = head_dim;
+    if (T < 0 || T > (1 << 24) || n_seqs < 0 || n_seqs > 65536) {
+        snprintf(msg, sizeof msg, "T = %d or n_seqs = %d out of range [0, 2^24], [0, 65536]", T, n_seqs);
+        return bad(MOE_EINVAL, msg);
+    }
+    if (D != 64 && D != 128) {
+        snprintf(msg, sizeof msg, "moe_attention_prompt: head_dim (%d) must be 64 or 128", D);
+        return bad(MOE_EDIMS, msg);
+    }
+    if (n_heads < 1 || n_heads > ATTN_MAX_HEADS || n_kv_heads < 1 || n_heads % n_kv_heads || n_heads / n_kv_heads > 64) {
+        snprintf(msg, sizeof msg, "n_heads (%d) must be 1 to 64 times n_kv_heads (%d) and at most %d", n_heads,
+                 n_kv_heads, ATTN_MAX_HEADS);
+        return bad(MOE_EINVAL, msg);
+    }
+    if (!(scale > 0.f) || !isfinite(scale * 1.4427f))
+        return bad(MOE_EINVAL, "moe_attention_prompt: scale must be finite and above 0");
+    if (T == 0 || n_seqs == 0)
+        return MOE_OK;
+    if (!q || !k || !v || !offsets || !out)
+        return bad(MOE_EINVAL, "moe_attention_prompt: NULL q, k, v, offsets or out");
+    const long long wq = (long long)n_heads * D, wk = (long long)n_kv_heads * D;
+    if (q_ld < wq || out_ld < wq || k_ld < wk || v_ld < wk)
+        return bad(MOE_EINVAL, "moe_attention_prompt: a row stride is below the row's values");
+    if (!rows_16b(q, q_ld) || !rows_16b(k, k_ld) || !rows_16b(v, v_ld) || !rows_16b(out, out_ld) ||
+        (uintptr_t)offsets % 4)
+        return bad(MOE_EINVAL, "moe_attention_prompt: rows must start on 16-byte boundaries, offsets on 4-byte ones");
+    PromptArgs a{};
+    cudaError_t e = attention_error_flag(&a.err);
+    if (e == cudaSuccess) {
+        a.offsets = offsets;
+        a.n_seqs = n_seqs;
+        a.T = T;
+        a.heads = n_heads;
+        a.kv = n_kv_heads;
+        a.group = n_heads / n_kv_heads;
+        a.tile_tokens = BM / a.group;
+        a.v = static_cast<const uint16_t *>(v);
+        a.v_ld = v_ld;
+        a.scale = scale * 1.44269504088896340736f;
+        a.out = static_cast<uint16_t *>(out);
+        a.out_ld = out_ld;
+        cudaStream_t st = (cudaStream_t)cuda_stream;
+        e = D == 128 ? launch_prompt<128>(a, q, q_ld, k, k_ld, st) : launch_prompt<64>(a, q, q_ld, k, k_ld, st);
+    }
+    if (e != cudaSuccess) {
+        snprintf(msg, sizeof msg, "prompt attention launch: %s", cudaGetErrorString(e));
+        return bad(MOE_ECUDA, msg);
+    }
+    return MOE_OK;
+}

@@ -19,13 +19,12 @@
 // instructions show); 176 rows 5.9 us from HBM, 5.2 from L2; one row of BF16 2.5 us, launch
 // included.  Above 32768 values a thread's eight vectors do not fit 64 registers: 120 to
 // 476 bytes are spilled (64 rows of 40960 BF16 values: 14.7 us, 24 MB).
-#include <cuda_bf16.h>
-#include <cuda_fp8.h>
 #include <math.h>
 #include <stdio.h>
 
 #include "../../include/moe.h"
 #include "moe_internal.cuh"
+#include "mx_encode.cuh"
 #include "overlap.cuh"
 
 namespace moe {
@@ -67,33 +66,6 @@ __device__ __forceinline__ void load8(const void *p, long long at, float v[8])
         v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w;
         v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
     }
-}
-
-__device__ __forceinline__ uint32_t bf16_pair(float a, float b)
-{
-    const __nv_bfloat162 p = __floats2bfloat162_rn(a, b);
-    return *reinterpret_cast<const uint32_t *>(&p);
-}
-
-__device__ __forceinline__ uint4 bf16x8(const float v[8])
-{
-    return make_uint4(bf16_pair(v[0], v[1]), bf16_pair(v[2], v[3]), bf16_pair(v[4], v[5]), bf16_pair(v[6], v[7]));
-}
-
-// E8M0 byte of a block whose largest value is amax = 1.m * 2^(E - 127): the
-// smallest p with amax <= 448 * 2^p = 1.75 * 2^(p + 8), as p + 127.
-__device__ __forceinline__ int mx_scale_byte(float amax)
-{
-    const uint32_t b = __float_as_uint(amax);
-    const int byte = (int)(b >> 23) - 8 + ((b & 0x7FFFFFu) > 0x600000u);
-    return byte < 0 ? 0 : byte;  // at most 247
-}
-
-__device__ __forceinline__ uint32_t e4m3x2(float lo, float hi)
-{
-    uint16_t r;
-    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
-    return r;
 }
 
 // One row per CTA, VPT vectors of 8 values per thread.  RES and DELTA are row
