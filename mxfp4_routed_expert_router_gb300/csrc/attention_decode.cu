@@ -37,8 +37,7 @@ namespace {
 using namespace gemm;
 
 constexpr int TILE = 64;             // tokens of a tile
-constexpr int WARPS = 4;             // that compute, 16 tokens of a tile each
-constexpr int THREADS = (WARPS + 1) * 32;
+constexpr int TEAM = 4;              // warps that share a tile, 16 tokens each; teams take the tiles in turn
 constexpr int MAX_STAGES = 16;
 constexpr int MIN_SHARE = 2;         // tiles of a CTA, unless there are fewer
 
@@ -62,20 +61,24 @@ struct DecodeArgs {
 };
 
 template <int D, int NT, bool MX> struct Geo {
+    static constexpr int TEAMS = 2;
+    static constexpr int WARPS = TEAM * TEAMS;       // that compute
+    static constexpr int THREADS = (WARPS + 1) * 32;
     static constexpr int ROW_B = D * (MX ? 1 : 2);
     static constexpr int TILE_B = TILE * ROW_B;
     static constexpr int SC_B = MX ? TILE * D / 32 : 0;
-    static constexpr int MERGE_B = WARPS * NT * 8 * D * 4;
+    static constexpr int MERGE_B = TEAM * NT * 8 * D * 4;
     static constexpr int FIT = (222 * 1024 - MERGE_B) / (2 * (TILE_B + SC_B));
-    static constexpr int STAGES = FIT < MAX_STAGES ? FIT : MAX_STAGES;
+    // a multiple of the teams: a slot then is one team's, which so sees every phase of its barriers
+    static constexpr int STAGES = (FIT < MAX_STAGES ? FIT : MAX_STAGES) / TEAMS * TEAMS;
     static constexpr int SC_OFF = STAGES * 2 * TILE_B;
     static constexpr int MERGE_OFF = SC_OFF + STAGES * 2 * SC_B;
-    static constexpr int ML_OFF = MERGE_OFF + MERGE_B;                 // [WARPS][8 NT][2]
-    static constexpr int BAR_OFF = ML_OFF + WARPS * NT * 8 * 2 * 4;
+    static constexpr int ML_B = WARPS * NT * 8 * 2 * 4;
+    static constexpr int ML_OFF = MERGE_OFF + MERGE_B;                 // [2][WARPS][8 NT][2]
+    static constexpr int BAR_OFF = ML_OFF + 2 * ML_B;
     static constexpr int BAD_OFF = BAR_OFF + 2 * MAX_STAGES * 8;       // a stage holds a page outside the cache
-    static constexpr int SCAN_OFF = BAD_OFF + MAX_STAGES * 4;          // long long [THREADS + 4]
-    static constexpr int SMEM = SCAN_OFF + (THREADS + 4) * 8 + 1024;   // + alignment slack
-    static_assert(SMEM <= 227 * 1024, "shared memory");
+    static constexpr int SMEM = BAD_OFF + MAX_STAGES * 4 + 1024;       // + alignment slack
+    static_assert(SMEM <= 226 * 1024, "shared memory");
     static_assert(TILE_B % 1024 == 0 && SC_OFF % 16 == 0 && SC_B % 16 == 0 && BAR_OFF % 8 == 0, "alignment");
 };
 
@@ -226,6 +229,31 @@ __device__ __forceinline__ void tile_max(float (&s)[NT][4], const float (&mul)[N
 
 __device__ __forceinline__ float finite_base(float m) { return m == -INFINITY ? 0.f : m; }
 
+// The running maxima with those of 16 more tokens
+template <int D, int NT> __device__ __forceinline__ void grow(State<D, NT> &st, const float (&mt)[NT][2])
+{
+    bool grown = false;
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+        grown |= mt[nt][0] > st.m[nt][0] || mt[nt][1] > st.m[nt][1];
+    if (!__any_sync(0xffffffffu, grown))
+        return;
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const float m = fmaxf(st.m[nt][h], mt[nt][h]), f = ex2(st.m[nt][h] - finite_base(m));
+            st.m[nt][h] = m;
+            st.l[nt][h] *= f;
+#pragma unroll
+            for (int i = 0; i < D / 16; ++i) {
+                st.o[i][nt][h] *= f;
+                st.o[i][nt][2 + h] *= f;
+            }
+        }
+    }
+}
+
 // 16 tokens of a BF16 tile.  kb, vb: shared addresses of the warp's block of rows (of `rows` rows), r0 its first row
 // there; n of the 16 tokens belong to the sequence.
 template <int D, int NT>
@@ -255,26 +283,7 @@ __device__ __forceinline__ void tile_bf16(State<D, NT> &st, const uint32_t (&qf)
         for (int i = 0; i < 4; ++i)
             sa[nt][i] += sb[nt][i];
     tile_max<NT>(sa, mul, g < n, g + 8 < n, mt);
-    bool grown = false;
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt)
-        grown |= mt[nt][0] > st.m[nt][0] || mt[nt][1] > st.m[nt][1];
-    if (__any_sync(0xffffffffu, grown)) {
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                const float m = fmaxf(st.m[nt][h], mt[nt][h]), f = ex2(st.m[nt][h] - finite_base(m));
-                st.m[nt][h] = m;
-                st.l[nt][h] *= f;
-#pragma unroll
-                for (int i = 0; i < D / 16; ++i) {
-                    st.o[i][nt][h] *= f;
-                    st.o[i][nt][2 + h] *= f;
-                }
-            }
-        }
-    }
+    grow<D, NT>(st, mt);
     uint32_t pf[NT][2];
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
@@ -294,8 +303,12 @@ __device__ __forceinline__ void tile_bf16(State<D, NT> &st, const uint32_t (&qf)
         for (int i = 0; i < 4; ++i) {
             const int t = 2 * qd + (i & 1) + 8 * (i >> 1);
             w[i] = lds128(vb + h * rows * 128 + (r0 + t) * 128 + ((g ^ (t & 7)) << 4));
-            if (t >= n)  // what lies there may be anything: 0 * inf is not 0
-                w[i] = make_uint4(0, 0, 0, 0);
+        }
+        if (n < 16) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i)  // what lies past the end may be anything: 0 * inf is not 0
+                if (2 * qd + (i & 1) + 8 * (i >> 1) >= n)
+                    w[i] = make_uint4(0, 0, 0, 0);
         }
         const uint32_t w0[4] = {w[0].x, w[0].y, w[0].z, w[0].w}, w1[4] = {w[1].x, w[1].y, w[1].z, w[1].w};
         const uint32_t w2[4] = {w[2].x, w[2].y, w[2].z, w[2].w}, w3[4] = {w[3].x, w[3].y, w[3].z, w[3].w};
@@ -355,6 +368,12 @@ template <int D> __device__ __forceinline__ uint32_t scales_of(uint32_t base, in
     return D == 128 ? lds32(base + t * 4) : lds16(base + t * 2);
 }
 
+// Whether a byte of x is 0 or 255
+__device__ __forceinline__ bool has_edge_byte(uint32_t x)
+{
+    return (((x - 0x01010101u) & ~x) | ((~x - 0x01010101u) & x)) & 0x80808080u;
+}
+
 // 16 tokens of an MXFP8 tile.  kb, vb, r0 as above; ksb, vsb: the scales of the warp's 16 tokens.
 template <int D, int NT>
 __device__ __forceinline__ void tile_mx(State<D, NT> &st, const uint32_t (&qf)[NT][D / 8], uint32_t kb, uint32_t vb,
@@ -362,6 +381,7 @@ __device__ __forceinline__ void tile_mx(State<D, NT> &st, const uint32_t (&qf)[N
                                         int qd)
 {
     constexpr int NB = D / 32;
+    constexpr uint32_t SCALES = D == 128 ? 0xFFFFFFFFu : 0xFFFFu;
     float s[NT][4];
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
@@ -369,6 +389,23 @@ __device__ __forceinline__ void tile_mx(State<D, NT> &st, const uint32_t (&qf)[N
         for (int i = 0; i < 4; ++i)
             s[nt][i] = 0.f;
     const uint32_t k0s = scales_of<D>(ksb, g), k1s = scales_of<D>(ksb, g + 8);
+    const uint32_t v0s = scales_of<D>(vsb, g), v1s = scales_of<D>(vsb, g + 8);
+    // 2^(byte - 127) is the byte in the exponent's place, unless it is 0 or 255
+    const bool plain = !__any_sync(0xffffffffu, has_edge_byte(k0s | (0x01010101u & ~SCALES)) ||
+                                                    has_edge_byte(k1s | (0x01010101u & ~SCALES)));
+    float e0[NB], e1[NB];
+#pragma unroll
+    for (int b = 0; b < NB; ++b) {
+        e0[b] = __uint_as_float(((k0s >> (8 * b)) & 255) << 23);
+        e1[b] = __uint_as_float(((k1s >> (8 * b)) & 255) << 23);
+    }
+    if (!plain) {
+#pragma unroll
+        for (int b = 0; b < NB; ++b) {
+            e0[b] = e8m0((k0s >> (8 * b)) & 255);
+            e1[b] = e8m0((k1s >> (8 * b)) & 255);
+        }
+    }
 #pragma unroll
     for (int b = 0; b < NB; ++b) {
         const uint2 k0 = lds64(kb + row8<D>(r0 + g, 32 * b + 8 * qd));
@@ -377,53 +414,40 @@ __device__ __forceinline__ void tile_mx(State<D, NT> &st, const uint32_t (&qf)[N
         const uint32_t x2 = e4m3x2_to_f16x2(k0.y), x3 = e4m3x2_to_f16x2(k0.y >> 16);
         const uint32_t y0 = e4m3x2_to_f16x2(k1.x), y1 = e4m3x2_to_f16x2(k1.x >> 16);
         const uint32_t y2 = e4m3x2_to_f16x2(k1.y), y3 = e4m3x2_to_f16x2(k1.y >> 16);
-        const float e0 = e8m0((k0s >> (8 * b)) & 255), e1 = e8m0((k1s >> (8 * b)) & 255);
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
             float c[4] = {0.f, 0.f, 0.f, 0.f};
             mma16816<true>(c, x0, y0, x1, y1, qf[nt][4 * b], qf[nt][4 * b + 1]);
             mma16816<true>(c, x2, y2, x3, y3, qf[nt][4 * b + 2], qf[nt][4 * b + 3]);
-            s[nt][0] = fmaf(c[0], e0, s[nt][0]);
-            s[nt][1] = fmaf(c[1], e0, s[nt][1]);
-            s[nt][2] = fmaf(c[2], e1, s[nt][2]);
-            s[nt][3] = fmaf(c[3], e1, s[nt][3]);
+            s[nt][0] = fmaf(c[0], e0[b], s[nt][0]);
+            s[nt][1] = fmaf(c[1], e0[b], s[nt][1]);
+            s[nt][2] = fmaf(c[2], e1[b], s[nt][2]);
+            s[nt][3] = fmaf(c[3], e1[b], s[nt][3]);
         }
     }
     float mt[NT][2];
     const bool in0 = g < n, in1 = g + 8 < n;
     tile_max<NT>(s, mul, in0, in1, mt);
+    grow<D, NT>(st, mt);
     // P relative to the tile's own maximum, in FP16; f brings the tile's product to the running one
-    float f[NT][2], alpha[NT][2], p[NT][4];
+    float f[NT][2], p[NT][4];
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-            const float m = fmaxf(st.m[nt][h], mt[nt][h]), base = finite_base(m);
-            alpha[nt][h] = ex2(st.m[nt][h] - base);
-            f[nt][h] = ex2(mt[nt][h] - base);
-            st.m[nt][h] = m;
             const float tb = finite_base(mt[nt][h]);
+            f[nt][h] = ex2(mt[nt][h] - finite_base(st.m[nt][h]));
             p[nt][h] = ex2(s[nt][h] - tb);
             p[nt][2 + h] = ex2(s[nt][2 + h] - tb);
-            st.l[nt][h] = fmaf(st.l[nt][h], alpha[nt][h], f[nt][h] * (p[nt][h] + p[nt][2 + h]));
-#pragma unroll
-            for (int i = 0; i < D / 16; ++i) {
-                st.o[i][nt][h] *= alpha[nt][h];
-                st.o[i][nt][2 + h] *= alpha[nt][h];
-            }
+            st.l[nt][h] = fmaf(f[nt][h], p[nt][h] + p[nt][2 + h], st.l[nt][h]);
         }
     }
-    const uint32_t v0s = scales_of<D>(vsb, g), v1s = scales_of<D>(vsb, g + 8);
-    uint32_t todo0 = in0 ? (D == 128 ? 0xFFFFFFFFu : 0xFFFFu) : 0u, todo1 = in1 ? (D == 128 ? 0xFFFFFFFFu : 0xFFFFu) : 0u;
+    uint32_t todo0 = in0 ? SCALES : 0u, todo1 = in1 ? SCALES : 0u;
     do {
-        uint32_t top = __vmaxu4(v0s & todo0, v1s & todo1);  // per block, the largest power left
-        top = __vmaxu4(top, __shfl_xor_sync(0xffffffffu, top, 4));
-        top = __vmaxu4(top, __shfl_xor_sync(0xffffffffu, top, 8));
-        top = __vmaxu4(top, __shfl_xor_sync(0xffffffffu, top, 16));
 #pragma unroll
         for (int b = 0; b < NB; ++b) {
             const uint32_t mask = 255u << (8 * b);
-            const int R = (top >> (8 * b)) & 255;
+            const int R = __reduce_max_sync(0xffffffffu, max(v0s & todo0 & mask, v1s & todo1 & mask)) >> (8 * b);
             const int d0 = R - (int)((v0s >> (8 * b)) & 255), d1 = R - (int)((v1s >> (8 * b)) & 255);
             const bool u0 = (todo0 & mask) && d0 <= 8, u1 = (todo1 & mask) && d1 <= 8;
             const float w0 = u0 ? __int_as_float((127 - d0) << 23) : 0.f, w1 = u1 ? __int_as_float((127 - d1) << 23) : 0.f;
@@ -432,11 +456,12 @@ __device__ __forceinline__ void tile_mx(State<D, NT> &st, const uint32_t (&qf)[N
             const float er = e8m0(R);
             uint32_t w[4];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const int t = 2 * qd + (i & 1) + 8 * (i >> 1);
-                w[i] = lds32(vb + row8<D>(r0 + t, 32 * b + 4 * g));
-                if (t >= n)  // what lies there may be NaN: 0 * NaN is not 0
-                    w[i] = 0;
+            for (int i = 0; i < 4; ++i)
+                w[i] = lds32(vb + row8<D>(r0 + 2 * qd + (i & 1) + 8 * (i >> 1), 32 * b + 4 * g));
+            if (n < 16) {
+#pragma unroll
+                for (int i = 0; i < 4; ++i)  // what lies past the end may be NaN: 0 * NaN is not 0
+                    w[i] = 2 * qd + (i & 1) + 8 * (i >> 1) < n ? w[i] : 0;
             }
             uint32_t pf[NT][2];
 #pragma unroll
@@ -468,23 +493,32 @@ __device__ __forceinline__ void tile_mx(State<D, NT> &st, const uint32_t (&qf)[N
 
 // ---------------------------------------------------------------- kernel
 
-// A place in the list of tiles: sequence b (its tiles start at `base` times units, `nt` of them per unit), unit u, tile t.
+// A place in the list of tiles: sequence b of `len` tokens (its tiles start at `base` times units, `nt` of them per
+// unit), unit u, tile t.  ahead: the length of the sequence after it, asked for early.
 struct Place {
     long long base;
-    int b, nt, u, t;
+    int b, len, nt, u, t, ahead;
 };
+
+__device__ __forceinline__ void enter_sequence(const DecodeArgs &a, Place &p, int len)
+{
+    p.len = len;
+    p.nt = len > 0 && len <= a.cap ? (len + TILE - 1) / TILE : 0;
+    p.ahead = p.b + 1 < a.B ? __ldcg(a.lens + p.b + 1) : 0;
+}
 
 __device__ __forceinline__ void next_sequence(const DecodeArgs &a, Place &p)
 {
     p.base += p.nt;
     p.u = p.t = 0;
-    do
-        p.nt = ++p.b < a.B ? tiles_of(a, p.b) : 1;
-    while (p.nt == 0);
+    do {
+        ++p.b;
+        enter_sequence(a, p, p.ahead);
+    } while (p.nt == 0 && p.b < a.B);
 }
 
 template <int D, int NT, bool MX>
-__global__ void __launch_bounds__(THREADS, 1)
+__global__ void __launch_bounds__(Geo<D, NT, MX>::THREADS, 1)
     decode_kernel(const __grid_constant__ DecodeArgs a, const __grid_constant__ CUtensorMap map_k,
                   const __grid_constant__ CUtensorMap map_v)
 {
@@ -493,7 +527,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     uint8_t *smem = smem_dyn + ((1024u - (smem_addr(smem_dyn) & 1023u)) & 1023u);
     uint64_t *full = reinterpret_cast<uint64_t *>(smem + G::BAR_OFF), *empty = full + MAX_STAGES;
     int *bad = reinterpret_cast<int *>(smem + G::BAD_OFF);
-    long long *scan = reinterpret_cast<long long *>(smem + G::SCAN_OFF);
+    __shared__ long long scan[G::WARPS + 1];
     __shared__ Place first;
     __shared__ int abort_word;
     volatile int *abort_flag = &abort_word;
@@ -502,7 +536,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     if (tid == 0) {
         for (int i = 0; i < G::STAGES; ++i) {
             mbar_init(&full[i], 1);
-            mbar_init(&empty[i], WARPS);
+            mbar_init(&empty[i], TEAM);
         }
         abort_word = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -512,7 +546,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     overlap_wait();
 
     // the list: every thread sums the tiles of some consecutive sequences
-    const int per = (a.B + THREADS - 1) / THREADS;
+    const int per = (a.B + G::THREADS - 1) / G::THREADS;
     long long sum = 0;
     for (int b = tid * per; b < min(a.B, (tid + 1) * per); ++b)
         sum += tiles_of(a, b);
@@ -526,7 +560,7 @@ __global__ void __launch_bounds__(THREADS, 1)
         scan[warp] = incl;
     __syncthreads();
     long long pre = incl - sum, total = 0;
-    for (int w = 0; w < WARPS + 1; ++w) {
+    for (int w = 0; w < G::WARPS + 1; ++w) {
         pre += w < warp ? scan[w] : 0;
         total += scan[w];
     }
@@ -542,6 +576,7 @@ __global__ void __launch_bounds__(THREADS, 1)
             p.base += p.nt;
             p.nt = tiles_of(a, ++p.b);
         }
+        enter_sequence(a, p, __ldcg(a.lens + p.b));
         const long long in = start - p.base * a.units;
         p.u = (int)(in / p.nt);
         p.t = (int)(in - (long long)p.u * p.nt);
@@ -555,7 +590,7 @@ __global__ void __launch_bounds__(THREADS, 1)
         if (n != 0 && tid == 0)
             atomicCAS(a.err, 0, DEV_ERR_BOUNDS);
         const uint32_t v = n == 0 ? 0u : 0x7FC07FC0u;
-        for (int i = tid; i < a.heads * D / 8; i += THREADS)
+        for (int i = tid; i < a.heads * D / 8; i += G::THREADS)
             reinterpret_cast<uint4 *>(a.out + b * a.out_ld)[i] = make_uint4(v, v, v, v);
     }
     __syncthreads();
@@ -564,31 +599,32 @@ __global__ void __launch_bounds__(THREADS, 1)
     Place at = first;
     const int page = 1 << a.page_log2, rows = min(page, TILE);  // rows of a TMA box
 
-    if (warp == WARPS) {
+    if (warp == G::WARPS) {
         // ------------------------------------------------------ tiles -> ring
-        // (a lane per page of a tile; the next tile's page numbers are on their way while this one's slot is awaited)
+        // A lane per page of a tile.  The table is read 32 pages at a time, a block ahead: a tile's pages then cost a
+        // shuffle, where a load per tile would hold the loader up for as long as the tile's bytes take.
         const int pages = TILE / rows;
-        auto entry = [&](const Place &p) {  // the lane's page: -1 none, -2 outside the cache
-            const int i = ((p.t * TILE) >> a.page_log2) + lane;
-            if (lane >= pages || ((long long)i << a.page_log2) >= __ldcg(a.lens + p.b))
-                return -1;
-            const int id = __ldcg(a.table + (long long)p.b * a.max_pages + i);
-            return id >= 0 && id < a.n_pages ? id : -2;
+        auto block = [&](int b, int k, int len) {  // the lane's entry of block k
+            const int i = 32 * k + lane;
+            return (long long)i << a.page_log2 < len ? __ldcg(a.table + (long long)b * a.max_pages + i) : 0;
         };
         int slot = 0, it = 0;
         uint32_t ph = 0;
-        int id = entry(at);
+        int held_b = -1, held_k = 0, held = 0, ahead = 0;
         for (long long cur = start; cur < end; ++cur) {
-            const Place here = at;
-            if (++at.t == at.nt) {
-                at.t = 0;
-                if (++at.u == a.units && cur + 1 < end)
-                    next_sequence(a, at);
+            const int pg0 = (at.t * TILE) >> a.page_log2, k = pg0 >> 5;
+            if (at.b != held_b || k != held_k) {
+                held = at.b == held_b && k == held_k + 1 ? ahead : block(at.b, k, at.len);
+                ahead = block(at.b, k + 1, at.len);
+                held_b = at.b;
+                held_k = k;
             }
-            const int id_next = cur + 1 < end ? entry(at) : -1;
+            const int id = __shfl_sync(0xffffffffu, held, (pg0 & 31) + min(lane, pages - 1));
+            const bool mine = lane < pages && (long long)(pg0 + lane) << a.page_log2 < at.len;
+            const bool outside = id < 0 || id >= a.n_pages;
             if (!mbar_wait_sleep_warp(&empty[slot], ph ^ 1, abort_flag, a.err, lane))
                 break;
-            const uint32_t got = __ballot_sync(0xffffffffu, id != -1), wrong = __ballot_sync(0xffffffffu, id == -2);
+            const uint32_t got = __ballot_sync(0xffffffffu, mine), wrong = __ballot_sync(0xffffffffu, mine && outside);
             if (lane == 0) {
                 if (wrong)
                     atomicCAS(a.err, 0, DEV_ERR_BOUNDS);
@@ -596,9 +632,9 @@ __global__ void __launch_bounds__(THREADS, 1)
                 mbar_arrive_expect_tx(&full[slot], __popc(got) * 2 * rows * (G::ROW_B + (MX ? D / 32 : 0)));
             }
             __syncwarp();
-            if (id != -1) {
-                const int pg = id < 0 ? 0 : id;  // (any page will do for one outside: the result is NaN)
-                const int kvh = here.u / a.chunks, off = (here.t * TILE) & (page - 1);
+            if (mine) {
+                const int pg = outside ? 0 : id;  // (any page will do for one outside: the result is NaN)
+                const int kvh = at.u / a.chunks, off = (at.t * TILE) & (page - 1);
                 uint8_t *dk = smem + slot * 2 * G::TILE_B + lane * rows * G::ROW_B, *dv = dk + G::TILE_B;
                 tma_4d(dk, &map_k, 0, kvh * page + off, 0, pg, &full[slot]);
                 tma_4d(dv, &map_v, 0, kvh * page + off, 0, pg, &full[slot]);
@@ -609,7 +645,11 @@ __global__ void __launch_bounds__(THREADS, 1)
                     bulk_g2s(ds + G::SC_B, a.vs + row * (D / 32), rows * (D / 32), &full[slot]);
                 }
             }
-            id = id_next;
+            if (++at.t == at.nt) {
+                at.t = 0;
+                if (++at.u == a.units)
+                    next_sequence(a, at);
+            }
             ++it;
             if (++slot == G::STAGES) {
                 slot = 0;
@@ -625,13 +665,13 @@ __global__ void __launch_bounds__(THREADS, 1)
     }
 
     // ---------------------------------------------------------- products
-    const int g = lane >> 2, qd = lane & 3;
-    const int block = 16 * warp / rows, r0 = 16 * warp % rows;  // the warp's rows of a tile
-    float *merge = reinterpret_cast<float *>(smem + G::MERGE_OFF), *ml = reinterpret_cast<float *>(smem + G::ML_OFF);
+    const int g = lane >> 2, qd = lane & 3, team = warp / TEAM, w4 = warp % TEAM;
+    const int block = 16 * w4 / rows, r0 = 16 * w4 % rows;  // the warp's rows of a tile
+    float *merge = reinterpret_cast<float *>(smem + G::MERGE_OFF);
     const uint32_t ring = smem_addr(smem);
-    int slot = 0, part = 0;
+    int slot = 0, part = 0, turn = 0;
     uint32_t ph = 0;
-    bool alive = true;
+    bool alive = true, odd = false;
     State<D, NT> st;
     uint32_t qf[NT][D / 8];
     float mul[NT][2];
@@ -640,7 +680,6 @@ __global__ void __launch_bounds__(THREADS, 1)
         const int kvh = at.u / a.chunks, chunk = at.u - kvh * a.chunks;
         const int h0 = chunk * 8 * NT, heads = min(8 * NT, a.group - h0);
         const long long head = (long long)kvh * a.group + h0;
-        const int len = __ldcg(a.lens + at.b);
         const uint16_t *q = a.q + at.b * a.q_ld + head * D;
         if (MX) {
             load_q_f16<D, NT>(a, q, heads, g, qd, qf, mul);
@@ -665,28 +704,35 @@ __global__ void __launch_bounds__(THREADS, 1)
         }
         bool wrong = false;
         for (int t = t0; t < t1; ++t) {
-            // (after a wait that ran out the warp only keeps to the others' barriers; the rows become NaN)
-            alive = alive && __all_sync(0xffffffffu, mbar_wait(&full[slot], ph, abort_flag, a.err)) != 0;
-            wrong |= !alive || bad[slot] != 0;
-            const int n = min(16, len - t * TILE - 16 * warp);
-            if (alive && n > 0) {
-                const uint32_t kb = ring + slot * 2 * G::TILE_B + block * rows * G::ROW_B, vb = kb + G::TILE_B;
-                if constexpr (MX) {
-                    const uint32_t ksb = ring + G::SC_OFF + slot * 2 * G::SC_B + 16 * warp * (D / 32);
-                    tile_mx<D, NT>(st, qf, kb, vb, ksb, ksb + G::SC_B, r0, n, mul, g, qd);
-                } else {
-                    tile_bf16<D, NT>(st, qf, kb, vb, rows, r0, n, mul, g, qd);
+            if (turn == team) {
+                // (after a wait that ran out the warp only keeps to the others' barriers; the rows become NaN)
+                alive = alive && __all_sync(0xffffffffu, mbar_wait(&full[slot], ph, abort_flag, a.err)) != 0;
+                wrong |= !alive || bad[slot] != 0;
+                const int n = min(16, at.len - t * TILE - 16 * w4);
+                if (alive && n > 0) {
+                    const uint32_t kb = ring + slot * 2 * G::TILE_B + block * rows * G::ROW_B, vb = kb + G::TILE_B;
+                    if constexpr (MX) {
+                        const uint32_t ksb = ring + G::SC_OFF + slot * 2 * G::SC_B + 16 * w4 * (D / 32);
+                        tile_mx<D, NT>(st, qf, kb, vb, ksb, ksb + G::SC_B, r0, n, mul, g, qd);
+                    } else {
+                        tile_bf16<D, NT>(st, qf, kb, vb, rows, r0, n, mul, g, qd);
+                    }
                 }
+                __syncwarp();
+                if (lane == 0 && alive)
+                    mbar_arrive(&empty[slot]);
             }
-            __syncwarp();
-            if (lane == 0 && alive)
-                mbar_arrive(&empty[slot]);
+            if (++turn == G::TEAMS)
+                turn = 0;
             if (++slot == G::STAGES) {
                 slot = 0;
                 ph ^= 1;
             }
         }
-        // the four warps' parts
+        // The warps' parts: all come to the common maximum, then a team adds what the team above it has left.
+        // (maxima and sums lie in one of two places in turn: a warp may be one stretch ahead of the others' reads)
+        float *ml = reinterpret_cast<float *>(smem + G::ML_OFF + (odd ? G::ML_B : 0));
+        odd = !odd;
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -700,44 +746,77 @@ __global__ void __launch_bounds__(THREADS, 1)
                 if (g == 0)
                     *reinterpret_cast<float2 *>(ml + ((warp * NT + nt) * 8 + 2 * qd + h) * 2) = make_float2(st.m[nt][h], l);
             }
-        asm volatile("bar.sync 1, %0;" ::"n"(WARPS * 32) : "memory");
+        asm volatile("bar.sync 1, %0;" ::"n"(G::WARPS * 32) : "memory");
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
-                const int hd = nt * 8 + 2 * qd + h;
                 float m = -INFINITY;
 #pragma unroll
-                for (int w = 0; w < WARPS; ++w)
-                    m = fmaxf(m, ml[(w * NT * 8 + hd) * 2]);
+                for (int w = 0; w < G::WARPS; ++w)
+                    m = fmaxf(m, ml[((w * NT + nt) * 8 + 2 * qd + h) * 2]);
                 const float f = ex2(st.m[nt][h] - finite_base(m));
-                float *o = merge + (warp * NT * 8 + hd) * D;
-                if constexpr (MX) {  // values 16 (i / 2) ..: block i / 2 of 32, 4 g + 2 (i & 1) and the next
 #pragma unroll
-                    for (int i = 0; i < D / 16; ++i)
-                        *reinterpret_cast<float2 *>(o + 32 * (i / 2) + 4 * g + 2 * (i & 1)) =
-                            make_float2(st.o[i][nt][h] * f, st.o[i][nt][2 + h] * f);
-                } else {  // 64 (i / 4) + 8 g + 2 (i & 3) and the next
-#pragma unroll
-                    for (int i = 0; i < D / 16; ++i)
-                        *reinterpret_cast<float2 *>(o + 64 * (i / 4) + 8 * g + 2 * (i & 3)) =
-                            make_float2(st.o[i][nt][h] * f, st.o[i][nt][2 + h] * f);
+                for (int i = 0; i < D / 16; ++i) {
+                    st.o[i][nt][h] *= f;
+                    st.o[i][nt][2 + h] *= f;
                 }
             }
-        asm volatile("bar.sync 1, %0;" ::"n"(WARPS * 32) : "memory");
+#pragma unroll
+        for (int from = G::TEAMS - 1; from >= 0; --from) {
+            if (team == from) {
+                float4 *mine = reinterpret_cast<float4 *>(merge + w4 * NT * 8 * D) + lane;
+                if (from < G::TEAMS - 1) {
+#pragma unroll
+                    for (int i = 0; i < D / 16; ++i)
+#pragma unroll
+                        for (int nt = 0; nt < NT; ++nt) {
+                            const float4 x = mine[(i * NT + nt) * 32];
+                            st.o[i][nt][0] += x.x, st.o[i][nt][1] += x.y, st.o[i][nt][2] += x.z, st.o[i][nt][3] += x.w;
+                        }
+                }
+                __syncwarp();
+                if (from > 0) {
+#pragma unroll
+                    for (int i = 0; i < D / 16; ++i)
+#pragma unroll
+                        for (int nt = 0; nt < NT; ++nt)
+                            mine[(i * NT + nt) * 32] =
+                                make_float4(st.o[i][nt][0], st.o[i][nt][1], st.o[i][nt][2], st.o[i][nt][3]);
+                } else {
+                    // the first team's in the order of heads and values: MMA i has a head's values 4 g + 2 (i & 1) and
+                    // the next of 32 (MXFP8), 8 g + 2 (i & 3) and the next of 64
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                        for (int h = 0; h < 2; ++h) {
+                            float *o = merge + (w4 * NT * 8 + nt * 8 + 2 * qd + h) * D;
+#pragma unroll
+                            for (int i = 0; i < D / 16; ++i)
+                                *reinterpret_cast<float2 *>(o + (MX ? 32 * (i / 2) + 4 * g + 2 * (i & 1)
+                                                                    : 64 * (i / 4) + 8 * g + 2 * (i & 3))) =
+                                    make_float2(st.o[i][nt][h], st.o[i][nt][2 + h]);
+                        }
+                }
+            }
+            asm volatile("bar.sync 1, %0;" ::"n"(G::WARPS * 32) : "memory");
+        }
         const bool whole = t0 == 0 && t1 == at.nt;
-        for (int i = tid; i < NT * D; i += WARPS * 32) {
+        for (int i = tid; i < NT * D; i += G::WARPS * 32) {
             const int hd = i / (D / 8), d = i % (D / 8) * 8;
             if (hd >= heads)
                 continue;
             float m = -INFINITY, l = 0.f, v[8] = {};
 #pragma unroll
-            for (int w = 0; w < WARPS; ++w)
+            for (int w = 0; w < G::WARPS; ++w)
                 m = fmaxf(m, ml[(w * NT * 8 + hd) * 2]);
 #pragma unroll
-            for (int w = 0; w < WARPS; ++w) {
+            for (int w = 0; w < G::WARPS; ++w) {
                 const float2 x = *reinterpret_cast<const float2 *>(ml + (w * NT * 8 + hd) * 2);
                 l = fmaf(x.y, ex2(x.x - finite_base(m)), l);
+            }
+#pragma unroll
+            for (int w = 0; w < TEAM; ++w) {
                 const float4 *o = reinterpret_cast<const float4 *>(merge + (w * NT * 8 + hd) * D + d);
                 const float4 o0 = o[0], o1 = o[1];
                 v[0] += o0.x, v[1] += o0.y, v[2] += o0.z, v[3] += o0.w;
@@ -761,7 +840,7 @@ __global__ void __launch_bounds__(THREADS, 1)
         part = 1;  // of a CTA's stretches only the first and the last can be parts
         cur += t1 - t0;
         at.t = 0;
-        if (++at.u == a.units && cur < end)
+        if (++at.u == a.units)
             next_sequence(a, at);
     }
 }
@@ -860,7 +939,7 @@ cudaError_t launch_decode(const DecodeArgs &a, const CUtensorMap &mk, const CUte
     cudaError_t e = smem_limit_once(attr_set, (const void *)kern, G::SMEM);
     if (e != cudaSuccess)
         return e;
-    if ((e = launch_overlapped(kern, (unsigned)a.ctas, THREADS, G::SMEM, 1, st, a, mk, mv)) != cudaSuccess)
+    if ((e = launch_overlapped(kern, (unsigned)a.ctas, G::THREADS, G::SMEM, 1, st, a, mk, mv)) != cudaSuccess)
         return e;
     if (a.cap <= TILE)  // one tile a sequence and head: nothing is ever shared
         return cudaSuccess;
