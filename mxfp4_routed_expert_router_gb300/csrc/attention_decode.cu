@@ -39,7 +39,7 @@ using namespace gemm;
 constexpr int TILE = 64;             // tokens of a tile
 constexpr int TEAM = 4;              // warps that share a tile, 16 tokens each; teams take the tiles in turn
 constexpr int MAX_STAGES = 16;
-constexpr int MIN_SHARE = 2;         // tiles of a CTA, unless there are fewer
+constexpr int MIN_SHARE = 2;         // tiles of a CTA at least
 
 struct DecodeArgs {
     const uint16_t *q;
@@ -63,10 +63,13 @@ struct DecodeArgs {
 template <int D, int NT, bool MX> struct Geo {
     static constexpr int TEAMS = 2;
     static constexpr int WARPS = TEAM * TEAMS;       // that compute
-    static constexpr int THREADS = (WARPS + 1) * 32;
+    static constexpr int LOADERS = 2 * TEAMS;        // one for a team's keys, one for its values
+    static constexpr int THREADS = (WARPS + LOADERS) * 32;
     static constexpr int ROW_B = D * (MX ? 1 : 2);
     static constexpr int TILE_B = TILE * ROW_B;
     static constexpr int SC_B = MX ? TILE * D / 32 : 0;
+    // what starting and ending a sequence and head costs, in tiles (0.7 us; a tile's bytes take 0.73 us per 32 KB)
+    static constexpr int START = TILE_B >= 16384 ? 1 : TILE_B >= 8192 ? 2 : 4;
     static constexpr int MERGE_B = TEAM * NT * 8 * D * 4;
     static constexpr int FIT = (222 * 1024 - MERGE_B) / (2 * (TILE_B + SC_B));
     // a multiple of the teams: a slot then is one team's, which so sees every phase of its barriers
@@ -89,10 +92,18 @@ __device__ __forceinline__ int tiles_of(const DecodeArgs &a, int b)
     return n > 0 && n <= a.cap ? (n + TILE - 1) / TILE : 0;
 }
 
-__device__ __forceinline__ long long share_of(const DecodeArgs &a, long long total)
+// The places of the list that a CTA takes, of `total` in all.  A unit (a key head of a sequence, or a chunk of its
+// query heads) has START places for its beginning and end before one place per tile.
+template <int START> __device__ __forceinline__ long long share_of(const DecodeArgs &a, long long total)
 {
     const long long s = (total + a.ctas - 1) / a.ctas;
-    return s < MIN_SHARE ? MIN_SHARE : s;
+    return s < START + MIN_SHARE ? START + MIN_SHARE : s;
+}
+
+template <int START> __device__ __forceinline__ int places_of(const DecodeArgs &a, int b)
+{
+    const int nt = tiles_of(a, b);
+    return nt ? nt + START : 0;
 }
 
 __device__ __forceinline__ float ex2(float x)
@@ -368,6 +379,13 @@ template <int D> __device__ __forceinline__ uint32_t scales_of(uint32_t base, in
     return D == 128 ? lds32(base + t * 4) : lds16(base + t * 2);
 }
 
+// The powers of two in use for the blocks of values: E8M0 bytes, and as floats
+template <int D> struct Powers {
+    uint32_t bytes;
+    bool narrow;  // all in 16 .. 240
+    float power[D / 32];
+};
+
 // Whether a byte of x is 0 or 255
 __device__ __forceinline__ bool has_edge_byte(uint32_t x)
 {
@@ -377,8 +395,8 @@ __device__ __forceinline__ bool has_edge_byte(uint32_t x)
 // 16 tokens of an MXFP8 tile.  kb, vb, r0 as above; ksb, vsb: the scales of the warp's 16 tokens.
 template <int D, int NT>
 __device__ __forceinline__ void tile_mx(State<D, NT> &st, const uint32_t (&qf)[NT][D / 8], uint32_t kb, uint32_t vb,
-                                        uint32_t ksb, uint32_t vsb, int r0, int n, const float (&mul)[NT][2], int g,
-                                        int qd)
+                                        uint32_t ksb, uint32_t vsb, int r0, int n, const float (&mul)[NT][2],
+                                        Powers<D> &ref, int g, int qd)
 {
     constexpr int NB = D / 32;
     constexpr uint32_t SCALES = D == 128 ? 0xFFFFFFFFu : 0xFFFFu;
@@ -389,7 +407,7 @@ __device__ __forceinline__ void tile_mx(State<D, NT> &st, const uint32_t (&qf)[N
         for (int i = 0; i < 4; ++i)
             s[nt][i] = 0.f;
     const uint32_t k0s = scales_of<D>(ksb, g), k1s = scales_of<D>(ksb, g + 8);
-    const uint32_t v0s = scales_of<D>(vsb, g), v1s = scales_of<D>(vsb, g + 8);
+    uint32_t v0s = scales_of<D>(vsb, g), v1s = scales_of<D>(vsb, g + 8);
     // 2^(byte - 127) is the byte in the exponent's place, unless it is 0 or 255
     const bool plain = !__any_sync(0xffffffffu, has_edge_byte(k0s | (0x01010101u & ~SCALES)) ||
                                                     has_edge_byte(k1s | (0x01010101u & ~SCALES)));
@@ -442,18 +460,44 @@ __device__ __forceinline__ void tile_mx(State<D, NT> &st, const uint32_t (&qf)[N
             st.l[nt][h] = fmaf(f[nt][h], p[nt][h] + p[nt][2 + h], st.l[nt][h]);
         }
     }
+    // A block's powers relative to the one in use (kept from step to step while it fits): P, at most 1, takes what a
+    // token's power is away from it, 2^-8 to 2^7, and keeps eight bits and more in FP16 for a token that counts.  The
+    // usual case is that all 16 tokens fit in all blocks: then no byte of `away`, power - (ref - 8), borrows from the
+    // next or has a high half (ref lies in 16 .. 240, so that a byte which borrows shows it).
+    v0s = in0 ? v0s : ref.bytes;
+    v1s = in1 ? v1s : ref.bytes;
+    const uint32_t away0 = v0s - (ref.bytes - (0x08080808u & SCALES)), away1 = v1s - (ref.bytes - (0x08080808u & SCALES));
+    const bool fits = __all_sync(0xffffffffu, ref.narrow && ((away0 | away1) & 0xF0F0F0F0u) == 0);
+    uint32_t w0s = away0 + 0x77777777u, w1s = away1 + 0x77777777u;  // 127 + power - ref in each byte
     uint32_t todo0 = in0 ? SCALES : 0u, todo1 = in1 ? SCALES : 0u;
     do {
+        if (!fits) {  // the largest power left, and the tokens within 2^8 of it
+            ref.bytes = 0;
+            ref.narrow = true;
+            w0s = w1s = 0;
+#pragma unroll
+            for (int b = 0; b < NB; ++b) {
+                const uint32_t mask = 255u << (8 * b);
+                const uint32_t top = __reduce_max_sync(0xffffffffu, max(v0s & todo0 & mask, v1s & todo1 & mask));
+                ref.bytes |= top;
+                const int R = top >> (8 * b), d0 = R - (int)((v0s >> (8 * b)) & 255), d1 = R - (int)((v1s >> (8 * b)) & 255);
+                ref.narrow = ref.narrow && R >= 16 && R <= 240;
+                ref.power[b] = e8m0(R);
+                if ((todo0 & mask) && d0 <= 8) {  // (a byte of 0 makes a factor of 0: another pass takes the token)
+                    w0s |= (uint32_t)(127 - d0) << (8 * b);
+                    todo0 &= ~mask;
+                }
+                if ((todo1 & mask) && d1 <= 8) {
+                    w1s |= (uint32_t)(127 - d1) << (8 * b);
+                    todo1 &= ~mask;
+                }
+            }
+        }
 #pragma unroll
         for (int b = 0; b < NB; ++b) {
-            const uint32_t mask = 255u << (8 * b);
-            const int R = __reduce_max_sync(0xffffffffu, max(v0s & todo0 & mask, v1s & todo1 & mask)) >> (8 * b);
-            const int d0 = R - (int)((v0s >> (8 * b)) & 255), d1 = R - (int)((v1s >> (8 * b)) & 255);
-            const bool u0 = (todo0 & mask) && d0 <= 8, u1 = (todo1 & mask) && d1 <= 8;
-            const float w0 = u0 ? __int_as_float((127 - d0) << 23) : 0.f, w1 = u1 ? __int_as_float((127 - d1) << 23) : 0.f;
-            todo0 &= u0 ? ~mask : ~0u;
-            todo1 &= u1 ? ~mask : ~0u;
-            const float er = e8m0(R);
+            const float w0 = __uint_as_float(((w0s >> (8 * b)) & 255) << 23);
+            const float w1 = __uint_as_float(((w1s >> (8 * b)) & 255) << 23);
+            const float er = ref.power[b];
             uint32_t w[4];
 #pragma unroll
             for (int i = 0; i < 4; ++i)
@@ -488,33 +532,46 @@ __device__ __forceinline__ void tile_mx(State<D, NT> &st, const uint32_t (&qf)[N
                 }
             }
         }
-    } while (__any_sync(0xffffffffu, todo0 | todo1));
+    } while (!fits && __any_sync(0xffffffffu, todo0 | todo1));
 }
 
 // ---------------------------------------------------------------- kernel
 
-// A place in the list of tiles: sequence b of `len` tokens (its tiles start at `base` times units, `nt` of them per
-// unit), unit u, tile t.  ahead: the length of the sequence after it, asked for early.
-struct Place {
-    long long base;
-    int b, len, nt, u, t, ahead;
+// A stretch of the list: tiles t0 .. t1 - 1 of unit u of sequence b, which has `len` tokens in `nt` tiles; the unit's
+// places start at v.  ahead: the length of the sequence after it, asked for early.
+struct Stretch {
+    long long v;
+    int b, len, nt, u, t0, t1, ahead;
 };
 
-__device__ __forceinline__ void enter_sequence(const DecodeArgs &a, Place &p, int len)
+__device__ __forceinline__ void enter_sequence(const DecodeArgs &a, Stretch &p, int len)
 {
     p.len = len;
     p.nt = len > 0 && len <= a.cap ? (len + TILE - 1) / TILE : 0;
     p.ahead = p.b + 1 < a.B ? __ldcg(a.lens + p.b + 1) : 0;
 }
 
-__device__ __forceinline__ void next_sequence(const DecodeArgs &a, Place &p)
+template <int START> __device__ __forceinline__ void cut(Stretch &p, long long end)
 {
-    p.base += p.nt;
-    p.u = p.t = 0;
-    do {
-        ++p.b;
-        enter_sequence(a, p, p.ahead);
-    } while (p.nt == 0 && p.b < a.B);
+    p.t1 = (int)max(0ll, min((long long)p.nt, end - p.v - START));
+}
+
+// The next stretch of a CTA whose places end at `end`; false where there is none.
+template <int START> __device__ __forceinline__ bool advance(const DecodeArgs &a, Stretch &p, long long end)
+{
+    p.v += p.nt + START;
+    if (p.t1 < p.nt || p.v + START >= end)
+        return false;
+    if (++p.u == a.units) {
+        p.u = 0;
+        do {
+            ++p.b;
+            enter_sequence(a, p, p.ahead);
+        } while (p.nt == 0 && p.b < a.B);
+    }
+    p.t0 = 0;
+    cut<START>(p, end);
+    return true;
 }
 
 template <int D, int NT, bool MX>
@@ -527,15 +584,15 @@ __global__ void __launch_bounds__(Geo<D, NT, MX>::THREADS, 1)
     uint8_t *smem = smem_dyn + ((1024u - (smem_addr(smem_dyn) & 1023u)) & 1023u);
     uint64_t *full = reinterpret_cast<uint64_t *>(smem + G::BAR_OFF), *empty = full + MAX_STAGES;
     int *bad = reinterpret_cast<int *>(smem + G::BAD_OFF);
-    __shared__ long long scan[G::WARPS + 1];
-    __shared__ Place first;
+    __shared__ long long scan[G::THREADS / 32];
+    __shared__ Stretch first;
     __shared__ int abort_word;
     volatile int *abort_flag = &abort_word;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
 
     if (tid == 0) {
         for (int i = 0; i < G::STAGES; ++i) {
-            mbar_init(&full[i], 1);
+            mbar_init(&full[i], 2);
             mbar_init(&empty[i], TEAM);
         }
         abort_word = 0;
@@ -549,7 +606,7 @@ __global__ void __launch_bounds__(Geo<D, NT, MX>::THREADS, 1)
     const int per = (a.B + G::THREADS - 1) / G::THREADS;
     long long sum = 0;
     for (int b = tid * per; b < min(a.B, (tid + 1) * per); ++b)
-        sum += tiles_of(a, b);
+        sum += places_of<G::START>(a, b);
     long long incl = sum;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -560,26 +617,27 @@ __global__ void __launch_bounds__(Geo<D, NT, MX>::THREADS, 1)
         scan[warp] = incl;
     __syncthreads();
     long long pre = incl - sum, total = 0;
-    for (int w = 0; w < G::WARPS + 1; ++w) {
+    for (int w = 0; w < G::THREADS / 32; ++w) {
         pre += w < warp ? scan[w] : 0;
         total += scan[w];
     }
     total *= a.units;
-    const long long share = share_of(a, total);
+    const long long share = share_of<G::START>(a, total);
     const long long start = min(total, (long long)blockIdx.x * share), end = min(total, start + share);
     if (start < end && pre * a.units <= start && start < (pre + sum) * a.units) {
-        Place p;
+        Stretch p;
         p.b = tid * per;
-        p.base = pre;
-        p.nt = tiles_of(a, p.b);
-        while (start >= (p.base + p.nt) * a.units) {
-            p.base += p.nt;
-            p.nt = tiles_of(a, ++p.b);
+        long long base = pre;
+        int n = places_of<G::START>(a, p.b);
+        while (start >= (base + n) * a.units) {
+            base += n;
+            n = places_of<G::START>(a, ++p.b);
         }
         enter_sequence(a, p, __ldcg(a.lens + p.b));
-        const long long in = start - p.base * a.units;
-        p.u = (int)(in / p.nt);
-        p.t = (int)(in - (long long)p.u * p.nt);
+        p.u = (int)((start - base * a.units) / n);
+        p.v = base * a.units + (long long)p.u * n;
+        p.t0 = (int)max(0ll, start - p.v - G::START);
+        cut<G::START>(p, end);
         first = p;
     }
     // sequences without tiles: zeros, or NaN where the length cannot be
@@ -594,72 +652,79 @@ __global__ void __launch_bounds__(Geo<D, NT, MX>::THREADS, 1)
             reinterpret_cast<uint4 *>(a.out + b * a.out_ld)[i] = make_uint4(v, v, v, v);
     }
     __syncthreads();
-    if (start >= end)
+    if (start >= end || first.t1 <= first.t0)  // (a last CTA may have no more than a unit's START places)
         return;
-    Place at = first;
+    Stretch at = first;
     const int page = 1 << a.page_log2, rows = min(page, TILE);  // rows of a TMA box
 
-    if (warp == G::WARPS) {
+    if (warp >= G::WARPS) {
         // ------------------------------------------------------ tiles -> ring
-        // A lane per page of a tile.  The table is read 32 pages at a time, a block ahead: a tile's pages then cost a
-        // shuffle, where a load per tile would hold the loader up for as long as the tile's bytes take.
-        const int pages = TILE / rows;
+        // A warp for each team's keys and one for its values: a copy costs its issuer about as long whatever its size,
+        // and small pages take several.  A lane per page of a tile.  The table is read 32 pages at a time, a block
+        // ahead: a tile's pages then cost a shuffle, where a load per tile would hold the loader up.
+        const int team = (warp - G::WARPS) >> 1, pages = TILE / rows;
+        const bool is_v = (warp - G::WARPS) & 1;
+        const CUtensorMap *map = is_v ? &map_v : &map_k;
+        const uint8_t *scales = is_v ? a.vs : a.ks;
         auto block = [&](int b, int k, int len) {  // the lane's entry of block k
             const int i = 32 * k + lane;
             return (long long)i << a.page_log2 < len ? __ldcg(a.table + (long long)b * a.max_pages + i) : 0;
         };
-        int slot = 0, it = 0;
+        int slot = 0, turn = 0, it = 0;
         uint32_t ph = 0;
         int held_b = -1, held_k = 0, held = 0, ahead = 0;
-        for (long long cur = start; cur < end; ++cur) {
-            const int pg0 = (at.t * TILE) >> a.page_log2, k = pg0 >> 5;
-            if (at.b != held_b || k != held_k) {
-                held = at.b == held_b && k == held_k + 1 ? ahead : block(at.b, k, at.len);
-                ahead = block(at.b, k + 1, at.len);
-                held_b = at.b;
-                held_k = k;
-            }
-            const int id = __shfl_sync(0xffffffffu, held, (pg0 & 31) + min(lane, pages - 1));
-            const bool mine = lane < pages && (long long)(pg0 + lane) << a.page_log2 < at.len;
-            const bool outside = id < 0 || id >= a.n_pages;
-            if (!mbar_wait_sleep_warp(&empty[slot], ph ^ 1, abort_flag, a.err, lane))
-                break;
-            const uint32_t got = __ballot_sync(0xffffffffu, mine), wrong = __ballot_sync(0xffffffffu, mine && outside);
-            if (lane == 0) {
-                if (wrong)
-                    atomicCAS(a.err, 0, DEV_ERR_BOUNDS);
-                bad[slot] = wrong != 0;
-                mbar_arrive_expect_tx(&full[slot], __popc(got) * 2 * rows * (G::ROW_B + (MX ? D / 32 : 0)));
-            }
-            __syncwarp();
-            if (mine) {
-                const int pg = outside ? 0 : id;  // (any page will do for one outside: the result is NaN)
-                const int kvh = at.u / a.chunks, off = (at.t * TILE) & (page - 1);
-                uint8_t *dk = smem + slot * 2 * G::TILE_B + lane * rows * G::ROW_B, *dv = dk + G::TILE_B;
-                tma_4d(dk, &map_k, 0, kvh * page + off, 0, pg, &full[slot]);
-                tma_4d(dv, &map_v, 0, kvh * page + off, 0, pg, &full[slot]);
-                if (MX) {
-                    const long long row = (((long long)pg * a.kv + kvh) << a.page_log2) + off;
-                    uint8_t *ds = smem + G::SC_OFF + slot * 2 * G::SC_B + lane * rows * (D / 32);
-                    bulk_g2s(ds, a.ks + row * (D / 32), rows * (D / 32), &full[slot]);
-                    bulk_g2s(ds + G::SC_B, a.vs + row * (D / 32), rows * (D / 32), &full[slot]);
+        bool more = true;
+        for (int t = at.t0; more; ++it) {
+            if (turn == team) {
+                const int pg0 = (t * TILE) >> a.page_log2, k = pg0 >> 5;
+                if (at.b != held_b || k != held_k) {
+                    held = at.b == held_b && k == held_k + 1 ? ahead : block(at.b, k, at.len);
+                    ahead = block(at.b, k + 1, at.len);
+                    held_b = at.b;
+                    held_k = k;
+                }
+                const int id = __shfl_sync(0xffffffffu, held, (pg0 & 31) + min(lane, pages - 1));
+                const bool mine = lane < pages && (long long)(pg0 + lane) << a.page_log2 < at.len;
+                const bool outside = id < 0 || id >= a.n_pages;
+                if (!mbar_wait_sleep_warp(&empty[slot], ph ^ 1, abort_flag, a.err, lane))
+                    break;
+                const uint32_t got = __ballot_sync(0xffffffffu, mine), wrong = __ballot_sync(0xffffffffu, mine && outside);
+                if (lane == 0) {
+                    if (wrong)
+                        atomicCAS(a.err, 0, DEV_ERR_BOUNDS);
+                    if (!is_v)
+                        bad[slot] = wrong != 0;
+                    mbar_arrive_expect_tx(&full[slot], __popc(got) * rows * (G::ROW_B + (MX ? D / 32 : 0)));
+                }
+                __syncwarp();
+                if (mine) {
+                    const int pg = outside ? 0 : id;  // (any page will do for one outside: the result is NaN)
+                    const int kvh = at.u / a.chunks, off = (t * TILE) & (page - 1);
+                    tma_4d(smem + (2 * slot + is_v) * G::TILE_B + lane * rows * G::ROW_B, map, 0, kvh * page + off, 0, pg,
+                           &full[slot]);
+                    if (MX) {
+                        const long long row = (((long long)pg * a.kv + kvh) << a.page_log2) + off;
+                        bulk_g2s(smem + G::SC_OFF + (2 * slot + is_v) * G::SC_B + lane * rows * (D / 32),
+                                 scales + row * (D / 32), rows * (D / 32), &full[slot]);
+                    }
                 }
             }
-            if (++at.t == at.nt) {
-                at.t = 0;
-                if (++at.u == a.units)
-                    next_sequence(a, at);
+            if (++t == at.t1) {
+                more = advance<G::START>(a, at, end);
+                t = 0;
             }
-            ++it;
+            if (++turn == G::TEAMS)
+                turn = 0;
             if (++slot == G::STAGES) {
                 slot = 0;
                 ph ^= 1;
             }
         }
-        // every copy has landed before the CTA ends (bounded)
+        // every copy has landed before the CTA ends (bounded; slots whose other half never came run the limit out)
         if (lane == 0)
             for (int i = it > G::STAGES ? it - G::STAGES : 0; i < it; ++i)
-                mbar_drain(&full[i % G::STAGES], (i / G::STAGES) & 1);
+                if (i % G::TEAMS == team && !mbar_drain(&full[i % G::STAGES], (i / G::STAGES) & 1))
+                    break;
         __syncwarp();
         return;
     }
@@ -671,12 +736,15 @@ __global__ void __launch_bounds__(Geo<D, NT, MX>::THREADS, 1)
     const uint32_t ring = smem_addr(smem);
     int slot = 0, part = 0, turn = 0;
     uint32_t ph = 0;
+    Powers<D> ref;
+    ref.bytes = 0;
+    ref.narrow = false;
     bool alive = true, odd = false;
     State<D, NT> st;
     uint32_t qf[NT][D / 8];
     float mul[NT][2];
-    for (long long cur = start; cur < end;) {
-        const int t0 = at.t, t1 = (int)min((long long)at.nt, t0 + (end - cur));
+    do {
+        const int t0 = at.t0, t1 = at.t1;
         const int kvh = at.u / a.chunks, chunk = at.u - kvh * a.chunks;
         const int h0 = chunk * 8 * NT, heads = min(8 * NT, a.group - h0);
         const long long head = (long long)kvh * a.group + h0;
@@ -713,7 +781,7 @@ __global__ void __launch_bounds__(Geo<D, NT, MX>::THREADS, 1)
                     const uint32_t kb = ring + slot * 2 * G::TILE_B + block * rows * G::ROW_B, vb = kb + G::TILE_B;
                     if constexpr (MX) {
                         const uint32_t ksb = ring + G::SC_OFF + slot * 2 * G::SC_B + 16 * w4 * (D / 32);
-                        tile_mx<D, NT>(st, qf, kb, vb, ksb, ksb + G::SC_B, r0, n, mul, g, qd);
+                        tile_mx<D, NT>(st, qf, kb, vb, ksb, ksb + G::SC_B, r0, n, mul, ref, g, qd);
                     } else {
                         tile_bf16<D, NT>(st, qf, kb, vb, rows, r0, n, mul, g, qd);
                     }
@@ -838,15 +906,11 @@ __global__ void __launch_bounds__(Geo<D, NT, MX>::THREADS, 1)
             }
         }
         part = 1;  // of a CTA's stretches only the first and the last can be parts
-        cur += t1 - t0;
-        at.t = 0;
-        if (++at.u == a.units)
-            next_sequence(a, at);
-    }
+    } while (advance<G::START>(a, at, end));
 }
 
 // Joins the parts of one sequence's query head, a thread per value.
-template <int D, int NT>
+template <int D, int NT, int START>
 __global__ void __launch_bounds__(D) join_kernel(const DecodeArgs a)
 {
     __shared__ long long red[2][D / 32];
@@ -855,7 +919,7 @@ __global__ void __launch_bounds__(D) join_kernel(const DecodeArgs a)
     overlap_wait();
     long long before = 0, total = 0;
     for (int i = d; i < a.B; i += D) {
-        const int n = tiles_of(a, i);
+        const int n = places_of<START>(a, i);
         total += n;
         before += i < b ? n : 0;
     }
@@ -879,13 +943,13 @@ __global__ void __launch_bounds__(D) join_kernel(const DecodeArgs a)
     if (nt == 0)
         return;
     const int kvh = h / a.group, hh = h - kvh * a.group, chunk = hh / (8 * NT);
-    const long long share = share_of(a, total * a.units);
-    const long long s = before * a.units + (long long)(kvh * a.chunks + chunk) * nt, e = s + nt;
-    const int c0 = (int)(s / share), c1 = (int)((e - 1) / share);
+    const long long share = share_of<START>(a, total * a.units);
+    const long long s = before * a.units + (long long)(kvh * a.chunks + chunk) * (nt + START);  // the unit's places
+    const int c0 = (int)((s + START) / share), c1 = (int)((s + START + nt - 1) / share);
     if (c0 == c1)
         return;  // written by its CTA
     const int hd = hh - chunk * 8 * NT;
-    // CTA c's stretch of this unit is its first one if the CTA's tiles start inside the unit
+    // CTA c's stretch of this unit is its first one if the CTA's places start inside the unit
     auto slot = [&](int c) { return (2ll * c + (c * share >= s ? 0 : 1)) * 8 * NT + hd; };
     float m = -INFINITY;
     for (int c = c0; c <= c1; ++c)
@@ -943,7 +1007,7 @@ cudaError_t launch_decode(const DecodeArgs &a, const CUtensorMap &mk, const CUte
         return e;
     if (a.cap <= TILE)  // one tile a sequence and head: nothing is ever shared
         return cudaSuccess;
-    return launch_overlapped(join_kernel<D, NT>, dim3((unsigned)a.B, (unsigned)a.heads), D, 0, 1, st, a);
+    return launch_overlapped(join_kernel<D, NT, G::START>, dim3((unsigned)a.B, (unsigned)a.heads), D, 0, 1, st, a);
 }
 
 size_t part_bytes(int heads_of_part, int D) { return (size_t)2 * sm_count() * heads_of_part * (D + 2) * 4; }
