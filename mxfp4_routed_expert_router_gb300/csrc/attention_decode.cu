@@ -20,8 +20,8 @@
 // workspace, and a second kernel joins the parts in their order.
 //
 // MXFP8 caches (half the bytes): E4M3 values become FP16 exactly.  A block's power of two is applied to the FP32 sums
-// of its 32 values (keys), or to P (values): P, relative to the largest of the 16 tokens' powers in the block, in FP16,
-// tokens more than 2^8 below it in a further pass, so that no token's probability loses its bits to FP16's range.
+// of its 32 values (keys), or to P (values), relative to a power that the vector's block is kept in; tokens whose powers
+// lie too far from it for FP16 are taken one by one in FP32.
 #include <math.h>
 #include <stdio.h>
 
@@ -368,171 +368,203 @@ __device__ __forceinline__ void load_q_f16(const DecodeArgs &a, const uint16_t *
     }
 }
 
-// A row's byte in a swizzled tile
-template <int D> __device__ __forceinline__ uint32_t row8(int r, int byte)
+// {2^(b0 - 127), 2^(b1 - 127)} of two E8M0 bytes as floats, NaN for 255
+__device__ __forceinline__ float2 e8m0x2(uint32_t bytes)
 {
-    return D == 128 ? r * 128 + (byte ^ ((r & 7) << 4)) : r * 64 + (byte ^ (((r >> 1) & 3) << 4));
+    uint32_t r;
+    asm("cvt.rn.bf16x2.ue8m0x2 %0, %1;" : "=r"(r) : "h"((uint16_t)bytes));
+    return make_float2(__uint_as_float(r << 16), __uint_as_float(r & 0xFFFF0000u));
 }
 
-template <int D> __device__ __forceinline__ uint32_t scales_of(uint32_t base, int t)
+__device__ __forceinline__ uint32_t mul_f16x2(uint32_t a, uint32_t b)
 {
-    return D == 128 ? lds32(base + t * 4) : lds16(base + t * 2);
+    uint32_t r;
+    asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
 }
 
-// The powers of two in use for the blocks of values: E8M0 bytes, and as floats
-template <int D> struct Powers {
+// The scales of tokens t and t + 1 (t even)
+template <int D> __device__ __forceinline__ uint2 scales_of_two(uint32_t base, int t)
+{
+    if (D == 128)
+        return lds64(base + t * 4);
+    const uint32_t v = lds32(base + t * 2);
+    return make_uint2(v & 0xFFFFu, v >> 16);
+}
+
+// The powers of two in use for the blocks of values, as E8M0 bytes: a state's vector is relative to them
+struct Powers {
     uint32_t bytes;
     bool narrow;  // all in 16 .. 240
-    float power[D / 32];
 };
 
-// Whether a byte of x is 0 or 255
-__device__ __forceinline__ bool has_edge_byte(uint32_t x)
-{
-    return (((x - 0x01010101u) & ~x) | ((~x - 0x01010101u) & x)) & 0x80808080u;
-}
-
-// 16 tokens of an MXFP8 tile.  kb, vb, r0 as above; ksb, vsb: the scales of the warp's 16 tokens.
+// 16 tokens' values where their blocks' powers lie far from those in use: a token at a time in FP32.
 template <int D, int NT>
-__device__ __forceinline__ void tile_mx(State<D, NT> &st, const uint32_t (&qf)[NT][D / 8], uint32_t kb, uint32_t vb,
-                                        uint32_t ksb, uint32_t vsb, int r0, int n, const float (&mul)[NT][2],
-                                        Powers<D> &ref, int g, int qd)
+__device__ __forceinline__ void values_apart(State<D, NT> &st, const float (&p)[NT][4], uint32_t vb, uint32_t vsb, int r0, int n,
+                                          Powers &ref, int lane)
 {
     constexpr int NB = D / 32;
+    const int g = lane >> 2, qd = lane & 3;
+    uint32_t now = 0;
+    ref.narrow = true;
+#pragma unroll
+    for (int b = 0; b < NB; ++b) {  // what is in use grows to the largest of these tokens', and the vector follows
+        const uint32_t mine = lane < n ? ((D == 128 ? lds32(vsb + lane * 4) : lds16(vsb + lane * 2)) >> (8 * b)) & 255 : 0;
+        const uint32_t was = (ref.bytes >> (8 * b)) & 255, top = max(was, __reduce_max_sync(0xffffffffu, mine));
+        now |= top << (8 * b);
+        ref.narrow = ref.narrow && top >= 16 && top <= 240;
+        const float f = ex2((float)((int)was - (int)top));
+#pragma unroll
+        for (int i = 2 * b; i < 2 * b + 2; ++i)
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int c = 0; c < 4; ++c)
+                    st.o[i][nt][c] *= f;
+    }
+    ref.bytes = now;
+#pragma unroll 1
+    for (int t = 0; t < n; ++t) {
+        const uint32_t scales = D == 128 ? lds32(vsb + t * 4) : lds16(vsb + t * 2);
+        float pt[NT][2];
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+                pt[nt][h] = __shfl_sync(0xffffffffu, t < 8 ? p[nt][h] : p[nt][2 + h], 4 * (t & 7) + qd);
+        const int r = r0 + t;
+#pragma unroll
+        for (int b = 0; b < NB; ++b) {
+            const float f = ex2((float)((int)((scales >> (8 * b)) & 255) - (int)((now >> (8 * b)) & 255)));
+            const int byte = 32 * b + 4 * g;
+            const uint32_t w = lds32(vb + (D == 128 ? r * 128 + (byte ^ ((r & 7) << 4))
+                                                    : r * 64 + (byte ^ (((r >> 1) & 3) << 4))));
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                const uint32_t x = e4m3x2_to_f16x2(j ? w >> 16 : w);
+                const float2 v = __half22float2(*reinterpret_cast<const __half2 *>(&x));
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        st.o[2 * b + j][nt][h] = fmaf(pt[nt][h] * f, v.x, st.o[2 * b + j][nt][h]);
+                        st.o[2 * b + j][nt][2 + h] = fmaf(pt[nt][h] * f, v.y, st.o[2 * b + j][nt][2 + h]);
+                    }
+            }
+        }
+    }
+}
+
+// 16 tokens of an MXFP8 tile.  kb, vb: shared addresses of the warp's 16 rows (a multiple of 16 into a tile that starts
+// on 1024 bytes); ksb, vsb: their scales.
+template <int D, int NT>
+__device__ __forceinline__ void tile_mx(State<D, NT> &st, const uint32_t (&qf)[NT][D / 8], uint32_t kb, uint32_t vb,
+                                        uint32_t ksb, uint32_t vsb, int n, const float (&mul)[NT][2], Powers &ref, int lane)
+{
+    constexpr int NB = D / 32, ROW = D;
     constexpr uint32_t SCALES = D == 128 ? 0xFFFFFFFFu : 0xFFFFu;
+    const int g = lane >> 2, qd = lane & 3;
     float s[NT][4];
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
         for (int i = 0; i < 4; ++i)
             s[nt][i] = 0.f;
-    const uint32_t k0s = scales_of<D>(ksb, g), k1s = scales_of<D>(ksb, g + 8);
-    uint32_t v0s = scales_of<D>(vsb, g), v1s = scales_of<D>(vsb, g + 8);
-    // 2^(byte - 127) is the byte in the exponent's place, unless it is 0 or 255
-    const bool plain = !__any_sync(0xffffffffu, has_edge_byte(k0s | (0x01010101u & ~SCALES)) ||
-                                                    has_edge_byte(k1s | (0x01010101u & ~SCALES)));
-    float e0[NB], e1[NB];
+    const uint32_t k0s = D == 128 ? lds32(ksb + g * 4) : lds16(ksb + g * 2);
+    const uint32_t k1s = D == 128 ? lds32(ksb + g * 4 + 32) : lds16(ksb + g * 2 + 16);
+    // 8 bytes of row g, and of row g + 8: the swizzle is an exclusive or on bits 4 .. 6 of a row's byte, as is the step
+    // from block to block
+    const uint32_t ka = kb + g * ROW + ((8 * qd) ^ (D == 128 ? g << 4 : ((g >> 1) & 3) << 4));
 #pragma unroll
     for (int b = 0; b < NB; ++b) {
-        e0[b] = __uint_as_float(((k0s >> (8 * b)) & 255) << 23);
-        e1[b] = __uint_as_float(((k1s >> (8 * b)) & 255) << 23);
-    }
-    if (!plain) {
-#pragma unroll
-        for (int b = 0; b < NB; ++b) {
-            e0[b] = e8m0((k0s >> (8 * b)) & 255);
-            e1[b] = e8m0((k1s >> (8 * b)) & 255);
-        }
-    }
-#pragma unroll
-    for (int b = 0; b < NB; ++b) {
-        const uint2 k0 = lds64(kb + row8<D>(r0 + g, 32 * b + 8 * qd));
-        const uint2 k1 = lds64(kb + row8<D>(r0 + g + 8, 32 * b + 8 * qd));
+        const uint2 k0 = lds64(ka ^ (32 * b)), k1 = lds64((ka ^ (32 * b)) + 8 * ROW);
         const uint32_t x0 = e4m3x2_to_f16x2(k0.x), x1 = e4m3x2_to_f16x2(k0.x >> 16);
         const uint32_t x2 = e4m3x2_to_f16x2(k0.y), x3 = e4m3x2_to_f16x2(k0.y >> 16);
         const uint32_t y0 = e4m3x2_to_f16x2(k1.x), y1 = e4m3x2_to_f16x2(k1.x >> 16);
         const uint32_t y2 = e4m3x2_to_f16x2(k1.y), y3 = e4m3x2_to_f16x2(k1.y >> 16);
+        const float2 e0 = e8m0x2(k0s >> (16 * (b / 2))), e1 = e8m0x2(k1s >> (16 * (b / 2)));
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
             float c[4] = {0.f, 0.f, 0.f, 0.f};
             mma16816<true>(c, x0, y0, x1, y1, qf[nt][4 * b], qf[nt][4 * b + 1]);
             mma16816<true>(c, x2, y2, x3, y3, qf[nt][4 * b + 2], qf[nt][4 * b + 3]);
-            s[nt][0] = fmaf(c[0], e0[b], s[nt][0]);
-            s[nt][1] = fmaf(c[1], e0[b], s[nt][1]);
-            s[nt][2] = fmaf(c[2], e1[b], s[nt][2]);
-            s[nt][3] = fmaf(c[3], e1[b], s[nt][3]);
+            s[nt][0] = fmaf(c[0], b & 1 ? e0.y : e0.x, s[nt][0]);
+            s[nt][1] = fmaf(c[1], b & 1 ? e0.y : e0.x, s[nt][1]);
+            s[nt][2] = fmaf(c[2], b & 1 ? e1.y : e1.x, s[nt][2]);
+            s[nt][3] = fmaf(c[3], b & 1 ? e1.y : e1.x, s[nt][3]);
         }
     }
     float mt[NT][2];
-    const bool in0 = g < n, in1 = g + 8 < n;
-    tile_max<NT>(s, mul, in0, in1, mt);
+    tile_max<NT>(s, mul, g < n, g + 8 < n, mt);
     grow<D, NT>(st, mt);
-    // P relative to the tile's own maximum, in FP16; f brings the tile's product to the running one
-    float f[NT][2], p[NT][4];
+    float p[NT][4];
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
+        const float b0 = finite_base(st.m[nt][0]), b1 = finite_base(st.m[nt][1]);
+        p[nt][0] = ex2(s[nt][0] - b0), p[nt][1] = ex2(s[nt][1] - b1);
+        p[nt][2] = ex2(s[nt][2] - b0), p[nt][3] = ex2(s[nt][3] - b1);
+        st.l[nt][0] += p[nt][0] + p[nt][2];
+        st.l[nt][1] += p[nt][1] + p[nt][3];
+    }
+    // P rounds to FP16 and takes, per block, what the token's power is away from the one in use: 2^-4 to 2^3, exact but
+    // for numbers below FP16's normal range.  A probability so is off by 2^-12 of itself or 2^-25 of the largest, times
+    // 2^4 at most in units of the token's values.  The usual case is that all 16 tokens fit in all blocks: then no byte
+    // of `away`, power - (ref - 4), borrows from the next or has more than three bits (ref lies in 16 .. 240, so that a
+    // byte which borrows shows it).
+    const uint2 v01 = scales_of_two<D>(vsb, 2 * qd), v89 = scales_of_two<D>(vsb, 2 * qd + 8);
+    uint32_t away[4] = {v01.x, v01.y, v89.x, v89.y};
+    if (n < 16) {
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            const float tb = finite_base(mt[nt][h]);
-            f[nt][h] = ex2(mt[nt][h] - finite_base(st.m[nt][h]));
-            p[nt][h] = ex2(s[nt][h] - tb);
-            p[nt][2 + h] = ex2(s[nt][2 + h] - tb);
-            st.l[nt][h] = fmaf(f[nt][h], p[nt][h] + p[nt][2 + h], st.l[nt][h]);
+        for (int i = 0; i < 4; ++i)
+            away[i] = 2 * qd + (i & 1) + 8 * (i >> 1) < n ? away[i] : ref.bytes;
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        away[i] -= ref.bytes - (0x04040404u & SCALES);
+    if (!__all_sync(0xffffffffu, ref.narrow && ((away[0] | away[1] | away[2] | away[3]) & 0xF8F8F8F8u) == 0)) {
+        values_apart<D, NT>(st, p, vb, vsb, 0, n, ref, lane);
+        return;
+    }
+    uint32_t pt[NT][2];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+        pt[nt][0] = transpose8x8(f16_pair(p[nt][0], p[nt][1]));
+        pt[nt][1] = transpose8x8(f16_pair(p[nt][2], p[nt][3]));
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        away[i] = (away[i] << 2) + 0x2C2C2C2Cu;  // 15 + power - ref, where FP16 has its exponent in the upper byte
+    // 4 bytes of row 2 q, and of the rows 1, 8 and 9 on: the next row flips bit 4 of the swizzle (with 64-byte rows it
+    // has the same one)
+    const uint32_t va = vb + 2 * qd * ROW + ((4 * g) ^ (D == 128 ? (2 * qd) << 4 : qd << 4));
+#pragma unroll
+    for (int b = 0; b < NB; ++b) {
+        const uint32_t v0 = va ^ (32 * b), v1 = D == 128 ? (v0 + ROW) ^ 16 : v0 + ROW;
+        uint32_t w[4] = {lds32(v0), lds32(v1), lds32(v0 + 8 * ROW), lds32(v1 + 8 * ROW)};
+        if (n < 16) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i)  // what lies past the end may be NaN: 0 * NaN is not 0
+                w[i] = 2 * qd + (i & 1) + 8 * (i >> 1) < n ? w[i] : 0;
+        }
+        const uint32_t f01 = __byte_perm(away[0], away[1], b * 0x1111 + 0x4400) & 0xFF00FF00u;
+        const uint32_t f89 = __byte_perm(away[2], away[3], b * 0x1111 + 0x4400) & 0xFF00FF00u;
+        uint32_t pf[NT][2];
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+            pf[nt][0] = mul_f16x2(pt[nt][0], f01);
+            pf[nt][1] = mul_f16x2(pt[nt][1], f89);
+        }
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            const uint32_t lo = __byte_perm(w[0], w[1], j ? 0x7362 : 0x5140);
+            const uint32_t hi = __byte_perm(w[2], w[3], j ? 0x7362 : 0x5140);
+            const uint32_t a0 = e4m3x2_to_f16x2(lo), a1 = e4m3x2_to_f16x2(lo >> 16);
+            const uint32_t a2 = e4m3x2_to_f16x2(hi), a3 = e4m3x2_to_f16x2(hi >> 16);
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+                mma16816<true>(st.o[2 * b + j][nt], a0, a1, a2, a3, pf[nt][0], pf[nt][1]);
         }
     }
-    // A block's powers relative to the one in use (kept from step to step while it fits): P, at most 1, takes what a
-    // token's power is away from it, 2^-8 to 2^7, and keeps eight bits and more in FP16 for a token that counts.  The
-    // usual case is that all 16 tokens fit in all blocks: then no byte of `away`, power - (ref - 8), borrows from the
-    // next or has a high half (ref lies in 16 .. 240, so that a byte which borrows shows it).
-    v0s = in0 ? v0s : ref.bytes;
-    v1s = in1 ? v1s : ref.bytes;
-    const uint32_t away0 = v0s - (ref.bytes - (0x08080808u & SCALES)), away1 = v1s - (ref.bytes - (0x08080808u & SCALES));
-    const bool fits = __all_sync(0xffffffffu, ref.narrow && ((away0 | away1) & 0xF0F0F0F0u) == 0);
-    uint32_t w0s = away0 + 0x77777777u, w1s = away1 + 0x77777777u;  // 127 + power - ref in each byte
-    uint32_t todo0 = in0 ? SCALES : 0u, todo1 = in1 ? SCALES : 0u;
-    do {
-        if (!fits) {  // the largest power left, and the tokens within 2^8 of it
-            ref.bytes = 0;
-            ref.narrow = true;
-            w0s = w1s = 0;
-#pragma unroll
-            for (int b = 0; b < NB; ++b) {
-                const uint32_t mask = 255u << (8 * b);
-                const uint32_t top = __reduce_max_sync(0xffffffffu, max(v0s & todo0 & mask, v1s & todo1 & mask));
-                ref.bytes |= top;
-                const int R = top >> (8 * b), d0 = R - (int)((v0s >> (8 * b)) & 255), d1 = R - (int)((v1s >> (8 * b)) & 255);
-                ref.narrow = ref.narrow && R >= 16 && R <= 240;
-                ref.power[b] = e8m0(R);
-                if ((todo0 & mask) && d0 <= 8) {  // (a byte of 0 makes a factor of 0: another pass takes the token)
-                    w0s |= (uint32_t)(127 - d0) << (8 * b);
-                    todo0 &= ~mask;
-                }
-                if ((todo1 & mask) && d1 <= 8) {
-                    w1s |= (uint32_t)(127 - d1) << (8 * b);
-                    todo1 &= ~mask;
-                }
-            }
-        }
-#pragma unroll
-        for (int b = 0; b < NB; ++b) {
-            const float w0 = __uint_as_float(((w0s >> (8 * b)) & 255) << 23);
-            const float w1 = __uint_as_float(((w1s >> (8 * b)) & 255) << 23);
-            const float er = ref.power[b];
-            uint32_t w[4];
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-                w[i] = lds32(vb + row8<D>(r0 + 2 * qd + (i & 1) + 8 * (i >> 1), 32 * b + 4 * g));
-            if (n < 16) {
-#pragma unroll
-                for (int i = 0; i < 4; ++i)  // what lies past the end may be NaN: 0 * NaN is not 0
-                    w[i] = 2 * qd + (i & 1) + 8 * (i >> 1) < n ? w[i] : 0;
-            }
-            uint32_t pf[NT][2];
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt) {
-                pf[nt][0] = transpose8x8(f16_pair(p[nt][0] * w0, p[nt][1] * w0));
-                pf[nt][1] = transpose8x8(f16_pair(p[nt][2] * w1, p[nt][3] * w1));
-            }
-#pragma unroll
-            for (int j = 0; j < 2; ++j) {
-                const uint32_t lo = __byte_perm(w[0], w[1], j ? 0x7362 : 0x5140);
-                const uint32_t hi = __byte_perm(w[2], w[3], j ? 0x7362 : 0x5140);
-                const uint32_t a0 = e4m3x2_to_f16x2(lo), a1 = e4m3x2_to_f16x2(lo >> 16);
-                const uint32_t a2 = e4m3x2_to_f16x2(hi), a3 = e4m3x2_to_f16x2(hi >> 16);
-#pragma unroll
-                for (int nt = 0; nt < NT; ++nt) {
-                    float c[4] = {0.f, 0.f, 0.f, 0.f};
-                    mma16816<true>(c, a0, a1, a2, a3, pf[nt][0], pf[nt][1]);
-                    const float f0 = f[nt][0] * er, f1 = f[nt][1] * er;
-                    float *o = st.o[2 * b + j][nt];
-                    o[0] = fmaf(c[0], f0, o[0]);
-                    o[1] = fmaf(c[1], f1, o[1]);
-                    o[2] = fmaf(c[2], f0, o[2]);
-                    o[3] = fmaf(c[3], f1, o[3]);
-                }
-            }
-        }
-    } while (!fits && __any_sync(0xffffffffu, todo0 | todo1));
 }
 
 // ---------------------------------------------------------------- kernel
@@ -736,9 +768,7 @@ __global__ void __launch_bounds__(Geo<D, NT, MX>::THREADS, 1)
     const uint32_t ring = smem_addr(smem);
     int slot = 0, part = 0, turn = 0;
     uint32_t ph = 0;
-    Powers<D> ref;
-    ref.bytes = 0;
-    ref.narrow = false;
+    Powers ref{0, false};
     bool alive = true, odd = false;
     State<D, NT> st;
     uint32_t qf[NT][D / 8];
@@ -781,7 +811,8 @@ __global__ void __launch_bounds__(Geo<D, NT, MX>::THREADS, 1)
                     const uint32_t kb = ring + slot * 2 * G::TILE_B + block * rows * G::ROW_B, vb = kb + G::TILE_B;
                     if constexpr (MX) {
                         const uint32_t ksb = ring + G::SC_OFF + slot * 2 * G::SC_B + 16 * w4 * (D / 32);
-                        tile_mx<D, NT>(st, qf, kb, vb, ksb, ksb + G::SC_B, r0, n, mul, ref, g, qd);
+                        tile_mx<D, NT>(st, qf, kb + r0 * G::ROW_B, vb + r0 * G::ROW_B, ksb, ksb + G::SC_B, n, mul, ref,
+                                       lane);
                     } else {
                         tile_bf16<D, NT>(st, qf, kb, vb, rows, r0, n, mul, g, qd);
                     }
@@ -826,6 +857,11 @@ __global__ void __launch_bounds__(Geo<D, NT, MX>::THREADS, 1)
                 const float f = ex2(st.m[nt][h] - finite_base(m));
 #pragma unroll
                 for (int i = 0; i < D / 16; ++i) {
+                    if (MX) {
+                        const float power = e8m0((ref.bytes >> (8 * (i / 2))) & 255);
+                        st.o[i][nt][h] *= power;
+                        st.o[i][nt][2 + h] *= power;
+                    }
                     st.o[i][nt][h] *= f;
                     st.o[i][nt][2 + h] *= f;
                 }
