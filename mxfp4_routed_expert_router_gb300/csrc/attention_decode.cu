@@ -6,7 +6,8 @@
 // The cache is read once and nothing else counts: 4 * head_dim bytes a token and key head, for 4 * head_dim flops a
 // query head.  So this is a stream, like the weight stream of linear.cu: a CTA per SM whose loader warp brings tiles
 // of 64 tokens (keys and values of one key head, by TMA through the page table) into a ring of up to 200 KB of shared
-// memory, and four warps that take 16 tokens of every tile each.  Two warp-level MMAs per 16 x 16 values of a tile do
+// memory, and two
+// teams of four warps that take the tiles in turn.  Two warp-level MMAs per 16 x 16 values of a tile do
 // the work of all query heads that share the key head, eight at a time:
 //   S^T[16 tokens, 8 heads] = K Q^T,    O^T[16 values, 8 heads] += V^T P^T
 // With tokens as the rows of the first product and values as the rows of the second, keys come out of shared memory as
@@ -36,8 +37,7 @@ namespace {
 
 using namespace gemm;
 
-constexpr int TILE = 64;             // tokens of a tile
-constexpr int TEAM = 4;              // warps that share a tile, 16 tokens each; teams take the tiles in turn
+constexpr int TEAM = 4;              // warps that share a tile, 16 tokens of each 64; teams take the tiles in turn
 constexpr int MAX_STAGES = 16;
 constexpr int MIN_SHARE = 2;         // tiles of a CTA at least
 
@@ -66,10 +66,13 @@ template <int D, int NT, bool MX> struct Geo {
     static constexpr int LOADERS = 2 * TEAMS;        // one for a team's keys, one for its values
     static constexpr int THREADS = (WARPS + LOADERS) * 32;
     static constexpr int ROW_B = D * (MX ? 1 : 2);
+    // tokens of a tile: 64 in BF16, 128 where they have half the bytes or fewer (waiting, arming and asking for a tile
+    // cost about 180 instructions per warp and tile, as many as 16 tokens' keys)
+    static constexpr int TILE = ROW_B >= 256 ? 64 : 128;
     static constexpr int TILE_B = TILE * ROW_B;
     static constexpr int SC_B = MX ? TILE * D / 32 : 0;
     // what starting and ending a sequence and head costs, in tiles (0.7 us; a tile's bytes take 0.73 us per 32 KB)
-    static constexpr int START = TILE_B >= 16384 ? 1 : TILE_B >= 8192 ? 2 : 4;
+    static constexpr int START = TILE_B >= 16384 ? 1 : 2;
     static constexpr int MERGE_B = TEAM * NT * 8 * D * 4;
     static constexpr int FIT = (222 * 1024 - MERGE_B) / (2 * (TILE_B + SC_B));
     // a multiple of the teams: a slot then is one team's, which so sees every phase of its barriers
@@ -85,25 +88,24 @@ template <int D, int NT, bool MX> struct Geo {
     static_assert(TILE_B % 1024 == 0 && SC_OFF % 16 == 0 && SC_B % 16 == 0 && BAR_OFF % 8 == 0, "alignment");
 };
 
-// Tiles of sequence b: 0 for an empty one and for a length that the table cannot hold.
-__device__ __forceinline__ int tiles_of(const DecodeArgs &a, int b)
+// Tiles of a sequence of n tokens: 0 for an empty one and for a length that the table cannot hold.
+template <class G> __device__ __forceinline__ int tiles_of(const DecodeArgs &a, int n)
 {
-    const int n = __ldcg(a.lens + b);
-    return n > 0 && n <= a.cap ? (n + TILE - 1) / TILE : 0;
+    return n > 0 && n <= a.cap ? (n + G::TILE - 1) / G::TILE : 0;
 }
 
 // The places of the list that a CTA takes, of `total` in all.  A unit (a key head of a sequence, or a chunk of its
 // query heads) has START places for its beginning and end before one place per tile.
-template <int START> __device__ __forceinline__ long long share_of(const DecodeArgs &a, long long total)
+template <class G> __device__ __forceinline__ long long share_of(const DecodeArgs &a, long long total)
 {
     const long long s = (total + a.ctas - 1) / a.ctas;
-    return s < START + MIN_SHARE ? START + MIN_SHARE : s;
+    return s < G::START + MIN_SHARE ? G::START + MIN_SHARE : s;
 }
 
-template <int START> __device__ __forceinline__ int places_of(const DecodeArgs &a, int b)
+template <class G> __device__ __forceinline__ int places_of(const DecodeArgs &a, int b)
 {
-    const int nt = tiles_of(a, b);
-    return nt ? nt + START : 0;
+    const int nt = tiles_of<G>(a, __ldcg(a.lens + b));
+    return nt ? nt + G::START : 0;
 }
 
 __device__ __forceinline__ float ex2(float x)
@@ -576,33 +578,33 @@ struct Stretch {
     int b, len, nt, u, t0, t1, ahead;
 };
 
-__device__ __forceinline__ void enter_sequence(const DecodeArgs &a, Stretch &p, int len)
+template <class G> __device__ __forceinline__ void enter_sequence(const DecodeArgs &a, Stretch &p, int len)
 {
     p.len = len;
-    p.nt = len > 0 && len <= a.cap ? (len + TILE - 1) / TILE : 0;
+    p.nt = tiles_of<G>(a, len);
     p.ahead = p.b + 1 < a.B ? __ldcg(a.lens + p.b + 1) : 0;
 }
 
-template <int START> __device__ __forceinline__ void cut(Stretch &p, long long end)
+template <class G> __device__ __forceinline__ void cut(Stretch &p, long long end)
 {
-    p.t1 = (int)max(0ll, min((long long)p.nt, end - p.v - START));
+    p.t1 = (int)max(0ll, min((long long)p.nt, end - p.v - G::START));
 }
 
 // The next stretch of a CTA whose places end at `end`; false where there is none.
-template <int START> __device__ __forceinline__ bool advance(const DecodeArgs &a, Stretch &p, long long end)
+template <class G> __device__ __forceinline__ bool advance(const DecodeArgs &a, Stretch &p, long long end)
 {
-    p.v += p.nt + START;
-    if (p.t1 < p.nt || p.v + START >= end)
+    p.v += p.nt + G::START;
+    if (p.t1 < p.nt || p.v + G::START >= end)
         return false;
     if (++p.u == a.units) {
         p.u = 0;
         do {
             ++p.b;
-            enter_sequence(a, p, p.ahead);
+            enter_sequence<G>(a, p, p.ahead);
         } while (p.nt == 0 && p.b < a.B);
     }
     p.t0 = 0;
-    cut<START>(p, end);
+    cut<G>(p, end);
     return true;
 }
 
@@ -638,7 +640,7 @@ __global__ void __launch_bounds__(Geo<D, NT, MX>::THREADS, 1)
     const int per = (a.B + G::THREADS - 1) / G::THREADS;
     long long sum = 0;
     for (int b = tid * per; b < min(a.B, (tid + 1) * per); ++b)
-        sum += places_of<G::START>(a, b);
+        sum += places_of<G>(a, b);
     long long incl = sum;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -654,22 +656,22 @@ __global__ void __launch_bounds__(Geo<D, NT, MX>::THREADS, 1)
         total += scan[w];
     }
     total *= a.units;
-    const long long share = share_of<G::START>(a, total);
+    const long long share = share_of<G>(a, total);
     const long long start = min(total, (long long)blockIdx.x * share), end = min(total, start + share);
     if (start < end && pre * a.units <= start && start < (pre + sum) * a.units) {
         Stretch p;
         p.b = tid * per;
         long long base = pre;
-        int n = places_of<G::START>(a, p.b);
+        int n = places_of<G>(a, p.b);
         while (start >= (base + n) * a.units) {
             base += n;
-            n = places_of<G::START>(a, ++p.b);
+            n = places_of<G>(a, ++p.b);
         }
-        enter_sequence(a, p, __ldcg(a.lens + p.b));
+        enter_sequence<G>(a, p, __ldcg(a.lens + p.b));
         p.u = (int)((start - base * a.units) / n);
         p.v = base * a.units + (long long)p.u * n;
         p.t0 = (int)max(0ll, start - p.v - G::START);
-        cut<G::START>(p, end);
+        cut<G>(p, end);
         first = p;
     }
     // sequences without tiles: zeros, or NaN where the length cannot be
@@ -687,14 +689,14 @@ __global__ void __launch_bounds__(Geo<D, NT, MX>::THREADS, 1)
     if (start >= end || first.t1 <= first.t0)  // (a last CTA may have no more than a unit's START places)
         return;
     Stretch at = first;
-    const int page = 1 << a.page_log2, rows = min(page, TILE);  // rows of a TMA box
+    const int page = 1 << a.page_log2, rows = min(page, G::TILE);  // rows of a TMA box
 
     if (warp >= G::WARPS) {
         // ------------------------------------------------------ tiles -> ring
         // A warp for each team's keys and one for its values: a copy costs its issuer about as long whatever its size,
         // and small pages take several.  A lane per page of a tile.  The table is read 32 pages at a time, a block
         // ahead: a tile's pages then cost a shuffle, where a load per tile would hold the loader up.
-        const int team = (warp - G::WARPS) >> 1, pages = TILE / rows;
+        const int team = (warp - G::WARPS) >> 1, pages = G::TILE / rows;
         const bool is_v = (warp - G::WARPS) & 1;
         const CUtensorMap *map = is_v ? &map_v : &map_k;
         const uint8_t *scales = is_v ? a.vs : a.ks;
@@ -702,13 +704,13 @@ __global__ void __launch_bounds__(Geo<D, NT, MX>::THREADS, 1)
             const int i = 32 * k + lane;
             return (long long)i << a.page_log2 < len ? __ldcg(a.table + (long long)b * a.max_pages + i) : 0;
         };
-        int slot = 0, turn = 0, it = 0;
+        int slot = team, own = team, n0 = 0;  // the team's next tile, and the stretch's first, in the CTA's count
         uint32_t ph = 0;
         int held_b = -1, held_k = 0, held = 0, ahead = 0;
-        bool more = true;
-        for (int t = at.t0; more; ++it) {
-            if (turn == team) {
-                const int pg0 = (t * TILE) >> a.page_log2, k = pg0 >> 5;
+        bool ok = true;
+        do {
+            for (int t = at.t0 + (own - n0); t < at.t1; t += G::TEAMS) {
+                const int pg0 = (t * G::TILE) >> a.page_log2, k = pg0 >> 5;
                 if (at.b != held_b || k != held_k) {
                     held = at.b == held_b && k == held_k + 1 ? ahead : block(at.b, k, at.len);
                     ahead = block(at.b, k + 1, at.len);
@@ -718,7 +720,7 @@ __global__ void __launch_bounds__(Geo<D, NT, MX>::THREADS, 1)
                 const int id = __shfl_sync(0xffffffffu, held, (pg0 & 31) + min(lane, pages - 1));
                 const bool mine = lane < pages && (long long)(pg0 + lane) << a.page_log2 < at.len;
                 const bool outside = id < 0 || id >= a.n_pages;
-                if (!mbar_wait_sleep_warp(&empty[slot], ph ^ 1, abort_flag, a.err, lane))
+                if (!(ok = mbar_wait_sleep_warp(&empty[slot], ph ^ 1, abort_flag, a.err, lane)))
                     break;
                 const uint32_t got = __ballot_sync(0xffffffffu, mine), wrong = __ballot_sync(0xffffffffu, mine && outside);
                 if (lane == 0) {
@@ -731,7 +733,7 @@ __global__ void __launch_bounds__(Geo<D, NT, MX>::THREADS, 1)
                 __syncwarp();
                 if (mine) {
                     const int pg = outside ? 0 : id;  // (any page will do for one outside: the result is NaN)
-                    const int kvh = at.u / a.chunks, off = (t * TILE) & (page - 1);
+                    const int kvh = at.u / a.chunks, off = (t * G::TILE) & (page - 1);
                     tma_4d(smem + (2 * slot + is_v) * G::TILE_B + lane * rows * G::ROW_B, map, 0, kvh * page + off, 0, pg,
                            &full[slot]);
                     if (MX) {
@@ -740,22 +742,18 @@ __global__ void __launch_bounds__(Geo<D, NT, MX>::THREADS, 1)
                                  scales + row * (D / 32), rows * (D / 32), &full[slot]);
                     }
                 }
+                own += G::TEAMS;
+                if ((slot += G::TEAMS) >= G::STAGES) {
+                    slot = team;
+                    ph ^= 1;
+                }
             }
-            if (++t == at.t1) {
-                more = advance<G::START>(a, at, end);
-                t = 0;
-            }
-            if (++turn == G::TEAMS)
-                turn = 0;
-            if (++slot == G::STAGES) {
-                slot = 0;
-                ph ^= 1;
-            }
-        }
+            n0 += at.t1 - at.t0;
+        } while (ok && advance<G>(a, at, end));
         // every copy has landed before the CTA ends (bounded; slots whose other half never came run the limit out)
         if (lane == 0)
-            for (int i = it > G::STAGES ? it - G::STAGES : 0; i < it; ++i)
-                if (i % G::TEAMS == team && !mbar_drain(&full[i % G::STAGES], (i / G::STAGES) & 1))
+            for (int i = max(team, own - G::STAGES); i < own; i += G::TEAMS)
+                if (!mbar_drain(&full[i % G::STAGES], (i / G::STAGES) & 1))
                     break;
         __syncwarp();
         return;
@@ -763,10 +761,9 @@ __global__ void __launch_bounds__(Geo<D, NT, MX>::THREADS, 1)
 
     // ---------------------------------------------------------- products
     const int g = lane >> 2, qd = lane & 3, team = warp / TEAM, w4 = warp % TEAM;
-    const int block = 16 * w4 / rows, r0 = 16 * w4 % rows;  // the warp's rows of a tile
     float *merge = reinterpret_cast<float *>(smem + G::MERGE_OFF);
     const uint32_t ring = smem_addr(smem);
-    int slot = 0, part = 0, turn = 0;
+    int slot = team, own = team, n0 = 0, part = 0;
     uint32_t ph = 0;
     Powers ref{0, false};
     bool alive = true, odd = false;
@@ -801,33 +798,35 @@ __global__ void __launch_bounds__(Geo<D, NT, MX>::THREADS, 1)
                     st.o[i][nt][c] = 0.f;
         }
         bool wrong = false;
-        for (int t = t0; t < t1; ++t) {
-            if (turn == team) {
-                // (after a wait that ran out the warp only keeps to the others' barriers; the rows become NaN)
-                alive = alive && __all_sync(0xffffffffu, mbar_wait(&full[slot], ph, abort_flag, a.err)) != 0;
-                wrong |= !alive || bad[slot] != 0;
-                const int n = min(16, at.len - t * TILE - 16 * w4);
-                if (alive && n > 0) {
-                    const uint32_t kb = ring + slot * 2 * G::TILE_B + block * rows * G::ROW_B, vb = kb + G::TILE_B;
-                    if constexpr (MX) {
-                        const uint32_t ksb = ring + G::SC_OFF + slot * 2 * G::SC_B + 16 * w4 * (D / 32);
-                        tile_mx<D, NT>(st, qf, kb + r0 * G::ROW_B, vb + r0 * G::ROW_B, ksb, ksb + G::SC_B, n, mul, ref,
-                                       lane);
-                    } else {
-                        tile_bf16<D, NT>(st, qf, kb, vb, rows, r0, n, mul, g, qd);
-                    }
+        for (int t = t0 + (own - n0); t < t1; t += G::TEAMS) {
+            // (after a wait that ran out the warp only keeps to the others' barriers; the rows become NaN)
+            alive = alive && __all_sync(0xffffffffu, mbar_wait(&full[slot], ph, abort_flag, a.err)) != 0;
+            wrong |= !alive || bad[slot] != 0;
+            const uint32_t tile = ring + slot * 2 * G::TILE_B;
+#pragma unroll 1
+            for (int r = 16 * w4; r < G::TILE; r += 16 * TEAM) {
+                const int n = min(16, at.len - t * G::TILE - r);
+                if (!alive || n <= 0)
+                    break;
+                const int block = r / rows, r0 = r % rows;  // (a tile is blocks of `rows` rows, one or a part of a page)
+                const uint32_t kb = tile + block * rows * G::ROW_B, vb = kb + G::TILE_B;
+                if constexpr (MX) {
+                    const uint32_t ksb = ring + G::SC_OFF + slot * 2 * G::SC_B + r * (D / 32);
+                    tile_mx<D, NT>(st, qf, kb + r0 * G::ROW_B, vb + r0 * G::ROW_B, ksb, ksb + G::SC_B, n, mul, ref, lane);
+                } else {
+                    tile_bf16<D, NT>(st, qf, kb, vb, rows, r0, n, mul, g, qd);
                 }
-                __syncwarp();
-                if (lane == 0 && alive)
-                    mbar_arrive(&empty[slot]);
             }
-            if (++turn == G::TEAMS)
-                turn = 0;
-            if (++slot == G::STAGES) {
-                slot = 0;
+            __syncwarp();
+            if (lane == 0 && alive)
+                mbar_arrive(&empty[slot]);
+            own += G::TEAMS;
+            if ((slot += G::TEAMS) >= G::STAGES) {
+                slot = team;
                 ph ^= 1;
             }
         }
+        n0 += t1 - t0;
         // The warps' parts: all come to the common maximum, then a team adds what the team above it has left.
         // (maxima and sums lie in one of two places in turn: a warp may be one stretch ahead of the others' reads)
         float *ml = reinterpret_cast<float *>(smem + G::ML_OFF + (odd ? G::ML_B : 0));
@@ -942,11 +941,11 @@ __global__ void __launch_bounds__(Geo<D, NT, MX>::THREADS, 1)
             }
         }
         part = 1;  // of a CTA's stretches only the first and the last can be parts
-    } while (advance<G::START>(a, at, end));
+    } while (advance<G>(a, at, end));
 }
 
 // Joins the parts of one sequence's query head, a thread per value.
-template <int D, int NT, int START>
+template <int D, int NT, class G>
 __global__ void __launch_bounds__(D) join_kernel(const DecodeArgs a)
 {
     __shared__ long long red[2][D / 32];
@@ -955,7 +954,7 @@ __global__ void __launch_bounds__(D) join_kernel(const DecodeArgs a)
     overlap_wait();
     long long before = 0, total = 0;
     for (int i = d; i < a.B; i += D) {
-        const int n = places_of<START>(a, i);
+        const int n = places_of<G>(a, i);
         total += n;
         before += i < b ? n : 0;
     }
@@ -975,13 +974,13 @@ __global__ void __launch_bounds__(D) join_kernel(const DecodeArgs a)
         before += red[0][w];
         total += red[1][w];
     }
-    const int nt = tiles_of(a, b);
+    const int nt = tiles_of<G>(a, __ldcg(a.lens + b));
     if (nt == 0)
         return;
     const int kvh = h / a.group, hh = h - kvh * a.group, chunk = hh / (8 * NT);
-    const long long share = share_of<START>(a, total * a.units);
-    const long long s = before * a.units + (long long)(kvh * a.chunks + chunk) * (nt + START);  // the unit's places
-    const int c0 = (int)((s + START) / share), c1 = (int)((s + START + nt - 1) / share);
+    const long long share = share_of<G>(a, total * a.units);
+    const long long s = before * a.units + (long long)(kvh * a.chunks + chunk) * (nt + G::START);  // the unit's places
+    const int c0 = (int)((s + G::START) / share), c1 = (int)((s + G::START + nt - 1) / share);
     if (c0 == c1)
         return;  // written by its CTA
     const int hd = hh - chunk * 8 * NT;
@@ -1010,7 +1009,7 @@ MoeStatus bad(MoeStatus s, const char *msg) { return (MoeStatus)set_last_error(s
 int head_tiles(int group) { return group <= 8 ? 1 : 2; }
 
 // pages as {values of 128 bytes, rows of a page's heads, halves of a row, pages}
-cudaError_t cache_map(CUtensorMap *m, const void *base, const MoeKvCache *c)
+cudaError_t cache_map(CUtensorMap *m, const void *base, const MoeKvCache *c, int tile)
 {
     auto enc = tensor_map_encoder();
     if (!enc)
@@ -1020,7 +1019,7 @@ cudaError_t cache_map(CUtensorMap *m, const void *base, const MoeKvCache *c)
     const long long row = (long long)c->head_dim * size, rows = (long long)c->n_kv_heads * c->page_size;
     const cuuint64_t dims[4] = {(cuuint64_t)inner, (cuuint64_t)rows, (cuuint64_t)parts, (cuuint64_t)c->n_pages};
     const cuuint64_t strides[3] = {(cuuint64_t)row, (cuuint64_t)(parts > 1 ? 128 : row), (cuuint64_t)(rows * row)};
-    const cuuint32_t box[4] = {(cuuint32_t)inner, (cuuint32_t)(c->page_size < TILE ? c->page_size : TILE),
+    const cuuint32_t box[4] = {(cuuint32_t)inner, (cuuint32_t)(c->page_size < tile ? c->page_size : tile),
                                (cuuint32_t)parts, 1};
     const cuuint32_t step[4] = {1, 1, 1, 1};
     const CUresult r = enc(m, mx ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4,
@@ -1031,19 +1030,24 @@ cudaError_t cache_map(CUtensorMap *m, const void *base, const MoeKvCache *c)
 }
 
 template <int D, int NT, bool MX>
-cudaError_t launch_decode(const DecodeArgs &a, const CUtensorMap &mk, const CUtensorMap &mv, cudaStream_t st)
+cudaError_t launch_decode(const DecodeArgs &a, const MoeKvCache *cache, cudaStream_t st)
 {
     using G = Geo<D, NT, MX>;
+    CUtensorMap mk, mv;
     auto kern = decode_kernel<D, NT, MX>;
     static std::atomic<int> attr_set[MAX_DEVICES];
     cudaError_t e = smem_limit_once(attr_set, (const void *)kern, G::SMEM);
+    if (e == cudaSuccess)
+        e = cache_map(&mk, cache->k, cache, G::TILE);
+    if (e == cudaSuccess)
+        e = cache_map(&mv, cache->v, cache, G::TILE);
     if (e != cudaSuccess)
         return e;
     if ((e = launch_overlapped(kern, (unsigned)a.ctas, G::THREADS, G::SMEM, 1, st, a, mk, mv)) != cudaSuccess)
         return e;
-    if (a.cap <= TILE)  // one tile a sequence and head: nothing is ever shared
+    if (a.cap <= G::TILE)  // one tile a sequence and head: nothing is ever shared
         return cudaSuccess;
-    return launch_overlapped(join_kernel<D, NT, G::START>, dim3((unsigned)a.B, (unsigned)a.heads), D, 0, 1, st, a);
+    return launch_overlapped(join_kernel<D, NT, G>, dim3((unsigned)a.B, (unsigned)a.heads), D, 0, 1, st, a);
 }
 
 size_t part_bytes(int heads_of_part, int D) { return (size_t)2 * sm_count() * heads_of_part * (D + 2) * 4; }
@@ -1105,12 +1109,7 @@ extern "C" MoeStatus moe_attention_decode(const MoeKvCache *cache, const void *q
         return bad(MOE_EWORKSPACE, msg);
     }
     DecodeArgs a{};
-    CUtensorMap mk, mv;
     cudaError_t e = attention_error_flag(&a.err);
-    if (e == cudaSuccess)
-        e = cache_map(&mk, cache->k, cache);
-    if (e == cudaSuccess)
-        e = cache_map(&mv, cache->v, cache);
     if (e == cudaSuccess) {
         a.q = static_cast<const uint16_t *>(q);
         a.q_ld = q_ld;
@@ -1138,11 +1137,11 @@ extern "C" MoeStatus moe_attention_decode(const MoeKvCache *cache, const void *q
         cudaStream_t st = (cudaStream_t)cuda_stream;
         const bool mx = cache->type == MOE_ROWS_MXFP8;
         if (D == 128)
-            e = nt == 1 ? (mx ? launch_decode<128, 1, true>(a, mk, mv, st) : launch_decode<128, 1, false>(a, mk, mv, st))
-                        : (mx ? launch_decode<128, 2, true>(a, mk, mv, st) : launch_decode<128, 2, false>(a, mk, mv, st));
+            e = nt == 1 ? (mx ? launch_decode<128, 1, true>(a, cache, st) : launch_decode<128, 1, false>(a, cache, st))
+                        : (mx ? launch_decode<128, 2, true>(a, cache, st) : launch_decode<128, 2, false>(a, cache, st));
         else
-            e = nt == 1 ? (mx ? launch_decode<64, 1, true>(a, mk, mv, st) : launch_decode<64, 1, false>(a, mk, mv, st))
-                        : (mx ? launch_decode<64, 2, true>(a, mk, mv, st) : launch_decode<64, 2, false>(a, mk, mv, st));
+            e = nt == 1 ? (mx ? launch_decode<64, 1, true>(a, cache, st) : launch_decode<64, 1, false>(a, cache, st))
+                        : (mx ? launch_decode<64, 2, true>(a, cache, st) : launch_decode<64, 2, false>(a, cache, st));
     }
     if (e != cudaSuccess) {
         snprintf(msg, sizeof msg, "decode attention launch: %s", cudaGetErrorString(e));
