@@ -19,7 +19,8 @@
 //
 // Masked values: P is 0 there, but 0 * inf is not.  Two warps clear the rows of V past the sequence's end, and values
 // that are not finite in tiles that some row must not see in full; rows that may see such a value get it added at the
-// end.  CTAs are numbered from the last rows of the longest sequences down, so that the short ones fill the gaps.
+// end.  A CTA per SM goes over its items (two tiles of a key head) one after the other, without a gap: the next item's
+// tiles are on their way and its first S is computed while the last one's rows are written.
 #include <math.h>
 #include <stdio.h>
 
@@ -38,7 +39,6 @@ constexpr int BM = 128, BN = 128;    // rows of a tile, keys of a tile
 constexpr int THREADS = 384;
 constexpr int WARP_MMA = 8, WARP_LOAD = 9, WARP_GUARD = 10;
 constexpr int GUARDS = 2;
-constexpr int MASKED = 3;            // key tiles that 256 rows' tokens can lie in
 constexpr int TMEM_COLS = 512;
 constexpr float GROWTH = 8.f;        // log2 by which a row's maximum may exceed the one in use
 
@@ -57,10 +57,9 @@ struct PromptArgs {
 template <int D> struct PGeo {
     static constexpr int TILE_B = 128 * D * 2;              // 128 rows
     static constexpr int SLOTS = D == 128 ? 5 : 8;          // key and value tiles
-    static_assert(SLOTS >= 2 * MASKED - 1, "see the loader");
     static constexpr int RING_OFF = 2 * TILE_B;
     static constexpr int BAR_OFF = RING_OFF + SLOTS * TILE_B;
-    static constexpr int N_BARS = 1 + 2 * SLOTS + 2 * MASKED + 6 + 1;
+    static constexpr int N_BARS = 4 * SLOTS + 6 + 2 + 4 + 1;
     static constexpr int SMEM = BAR_OFF + N_BARS * 8 + 1024;  // + alignment slack
     static_assert(SMEM <= 226 * 1024, "shared memory");
 };
@@ -70,6 +69,57 @@ __device__ __forceinline__ float ex2(float x)
     float y;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
+}
+
+// Two floats in one register pair: one instruction for both
+__device__ __forceinline__ uint64_t pack2(float x, float y)
+{
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(x), "f"(y));
+    return r;
+}
+
+__device__ __forceinline__ float2 unpack2(uint64_t v)
+{
+    float2 r;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
+    return r;
+}
+
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c)
+{
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b)
+{
+    uint64_t r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+
+__device__ __forceinline__ float max3(float a, float b, float c)
+{
+    float r;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+    return r;
+}
+
+// The largest of a row's 128 scores
+__device__ __forceinline__ float row_max(const uint32_t (&s)[BN])
+{
+    float m[4] = {__uint_as_float(s[0]), __uint_as_float(s[1]), __uint_as_float(s[2]), __uint_as_float(s[3])};
+#pragma unroll
+    for (int c = 4; c + 8 <= BN; c += 8)
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            m[i] = max3(m[i], __uint_as_float(s[c + 2 * i]), __uint_as_float(s[c + 2 * i + 1]));
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        m[i] = fmaxf(m[i], __uint_as_float(s[BN - 4 + i]));
+    return fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3]));
 }
 
 __device__ __forceinline__ void fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
@@ -163,83 +213,108 @@ __device__ __forceinline__ Span sequence(const PromptArgs &a, int b)
     return {s, e - s};
 }
 
-// A CTA's work: tokens from tok0 (within the sequence) on and a key head; len == 0: none
+// One piece of work: the two tiles from token tok0 (within the sequence) on, of a key head; len == 0: no more
 struct Item {
     int start, len, tok0, kvh;
 };
 
-__device__ __forceinline__ int block_sum(int v, int *red)
-{
-    v = __reduce_add_sync(0xffffffffu, v);
-    __syncthreads();
-    if ((threadIdx.x & 31) == 0)
-        red[threadIdx.x >> 5] = v;
-    __syncthreads();
-    int s = 0;
-#pragma unroll
-    for (int w = 0; w < THREADS / 32; ++w)
-        s += red[w];
-    return s;
-}
+// The list of all items holds, from the highest level down, the level-th item of every sequence that has one: the
+// rows that see most keys come first.  One warp walks it for its CTA.
+struct Walk {
+    static constexpr int KEPT = 4;  // sequences of a lane whose items it keeps
+    int kept[KEPT];
+    int level, here;                // items at this level and above
 
-// Item i of the list that holds, from the highest level down, the level-th CTA of every sequence that has one.  Every
-// thread of the CTA takes part.
-__device__ __forceinline__ Item find_item(const PromptArgs &a, int i, int *red, Item *found)
-{
-    const int per_cta = 2 * a.tile_tokens, tid = threadIdx.x;
-    const int chunk = (a.n_seqs + THREADS - 1) / THREADS, b0 = min(a.n_seqs, tid * chunk);
-    const int b1 = min(a.n_seqs, b0 + chunk);
-    auto above = [&](int level) {  // CTAs at this level and above
+    __device__ __forceinline__ int items(const PromptArgs &a, int b) const
+    {
+        const int per = 2 * a.tile_tokens;
+        return b < a.n_seqs ? (sequence(a, b).len + per - 1) / per : 0;
+    }
+
+    __device__ __forceinline__ int above(const PromptArgs &a, int at_level, int lane) const
+    {
         int s = 0;
-        for (int b = b0; b < b1; ++b)
-            s += max(0, (sequence(a, b).len + per_cta - 1) / per_cta - level);
-        return block_sum(s, red) * a.kv;
-    };
-    int lo = 0, hi = (a.T + per_cta - 1) / per_cta;  // above(lo) > i >= above(hi)
-    if (above(0) <= i)
-        return {0, 0, 0, 0};
-    int over = 0;  // above(hi)
-    while (hi - lo > 1) {
-        const int mid = (lo + hi) >> 1, n = above(mid);
-        if (n > i) {
-            lo = mid;
-        } else {
-            hi = mid;
-            over = n;
-        }
-    }
-    const int rank = (i - over) / a.kv, kvh = (i - over) - rank * a.kv;
-    // the rank-th sequence with more than lo CTAs
-    int mine = 0;
-    for (int b = b0; b < b1; ++b)
-        mine += sequence(a, b).len > lo * per_cta;
-    int incl = mine;
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        const int n = __shfl_up_sync(0xffffffffu, incl, o);
-        incl += (tid & 31) >= o ? n : 0;
+        for (int i = 0; i < KEPT; ++i)
+            s += max(0, kept[i] - at_level);
+        for (int b = lane + 32 * KEPT; b < a.n_seqs; b += 32)
+            s += max(0, items(a, b) - at_level);
+        return __reduce_add_sync(0xffffffffu, s) * a.kv;
     }
-    __syncthreads();
-    if ((tid & 31) == 31)
-        red[tid >> 5] = incl;
-    __syncthreads();
-    int pre = incl - mine;
-    for (int w = 0; w < (tid >> 5); ++w)
-        pre += red[w];
-    if (tid == 0)
-        *found = {0, 0, 0, 0};  // (stays where offsets that do not ascend have no such sequence)
-    __syncthreads();
-    if (pre <= rank && rank < pre + mine) {
-        for (int b = b0; b < b1; ++b) {
-            const Span s = sequence(a, b);
-            if (s.len > lo * per_cta && pre++ == rank) {
-                *found = {s.start, s.len, lo * per_cta, kvh};
-                break;
+
+    __device__ __forceinline__ void begin(const PromptArgs &a, int lane)
+    {
+#pragma unroll
+        for (int i = 0; i < KEPT; ++i)
+            kept[i] = items(a, lane + 32 * i);
+        level = a.T / (2 * a.tile_tokens) + 1;
+        here = 0;
+    }
+
+    // Item i of the list; i grows from call to call.
+    __device__ __forceinline__ Item at(const PromptArgs &a, int i, int lane)
+    {
+        int over = 0;  // items above the level that i is in
+        if (i >= here) {
+            int lo = 0, hi = level;  // above(lo) > i >= above(hi)
+            int n = above(a, 0, lane);
+            if (n <= i)
+                return {0, 0, 0, 0};
+            here = n;
+            over = above(a, hi, lane);
+            while (hi - lo > 1) {
+                const int mid = (lo + hi) >> 1;
+                n = above(a, mid, lane);
+                if (n > i) {
+                    lo = mid;
+                    here = n;
+                } else {
+                    hi = mid;
+                    over = n;
+                }
             }
+            level = lo;
+        } else {
+            over = above(a, level + 1, lane);
         }
+        const int rank = (i - over) / a.kv, kvh = (i - over) - rank * a.kv;
+        // the rank-th sequence with more than `level` items
+        int seen = 0;
+        for (int b0 = 0, k = 0; b0 < a.n_seqs; b0 += 32, ++k) {
+            int n = 0;
+#pragma unroll
+            for (int j = 0; j < KEPT; ++j)
+                n = k == j ? kept[j] : n;
+            if (k >= KEPT)
+                n = items(a, b0 + lane);
+            uint32_t with = __ballot_sync(0xffffffffu, n > level);
+            const int count = __popc(with);
+            if (count > 0 && rank < seen + count) {
+                for (int j = rank - seen; j > 0; --j)
+                    with &= with - 1;
+                const Span q = sequence(a, b0 + __ffs(with) - 1);
+                return {q.start, q.len, level * 2 * a.tile_tokens, kvh};
+            }
+            seen += count;
+        }
+        return {0, 0, 0, 0};  // (not reached: offsets do not change during the call)
     }
-    __syncthreads();
-    return *found;
+};
+
+// Key tiles of an item's two row tiles; those from `masked` on hold keys that some row must not see.
+struct Tiles {
+    int n0, n1, n, masked;
+};
+
+__device__ __forceinline__ Tiles tiles_of(const PromptArgs &a, const Item &item)
+{
+    const int last = item.len - 1, second = item.tok0 + a.tile_tokens;
+    Tiles t;
+    t.n0 = min(last, second - 1) / BN + 1;
+    t.n1 = second > last ? 0 : min(last, second + a.tile_tokens - 1) / BN + 1;
+    t.n = max(t.n0, t.n1);
+    t.masked = item.tok0 / BN;
+    return t;
 }
 
 // ---------------------------------------------------------------- kernel
@@ -251,28 +326,21 @@ __global__ void __launch_bounds__(THREADS, 1)
 {
     using G = PGeo<D>;
     extern __shared__ uint8_t smem_dyn[];
-    __shared__ int red[THREADS / 32];
-    __shared__ Item found;
+    __shared__ Item items[2];
     __shared__ uint32_t tmem_word;
-    __shared__ int abort_word, odd_word;  // odd: a value that is not finite has been cleared
+    __shared__ int abort_word, odd_word;  // odd: a value that is not finite has been cleared, in this item or an earlier
     volatile int *abort_flag = &abort_word;
     uint8_t *smem = smem_dyn + ((1024u - (smem_addr(smem_dyn) & 1023u)) & 1023u);
-    uint64_t *q_full = reinterpret_cast<uint64_t *>(smem + G::BAR_OFF), *full = q_full + 1, *empty = full + G::SLOTS;
-    uint64_t *v_land = empty + G::SLOTS, *v_clear = v_land + MASKED, *s_full = v_clear + MASKED, *p_full = s_full + 2;
-    uint64_t *o_full = p_full + 2, *end_bar = o_full + 2;
+    uint64_t *full = reinterpret_cast<uint64_t *>(smem + G::BAR_OFF), *empty = full + G::SLOTS;
+    uint64_t *v_land = empty + G::SLOTS, *v_clear = v_land + G::SLOTS, *s_full = v_clear + G::SLOTS, *p_full = s_full + 2;
+    uint64_t *o_full = p_full + 2, *q_full = o_full + 2, *q_empty = q_full + 1, *item_full = q_empty + 1;
+    uint64_t *item_empty = item_full + 2, *end_bar = item_empty + 2;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
 
-    overlap_wait();
-    const Item item = find_item(a, blockIdx.x, red, &found);
-    if (item.len == 0)
-        return;
     if (tid == 0) {
-        mbar_init(q_full, 1);
         for (int i = 0; i < G::SLOTS; ++i) {
             mbar_init(&full[i], 1);
             mbar_init(&empty[i], 1);
-        }
-        for (int i = 0; i < MASKED; ++i) {
             mbar_init(&v_land[i], 1);
             mbar_init(&v_clear[i], GUARDS);
         }
@@ -280,12 +348,19 @@ __global__ void __launch_bounds__(THREADS, 1)
             mbar_init(&s_full[t], 1);
             mbar_init(&p_full[t], 4);
             mbar_init(&o_full[t], 1);
+            mbar_init(&item_full[t], 1);
+            mbar_init(&item_empty[t], THREADS / 32 - 1);
         }
+        mbar_init(q_full, 1);
+        mbar_init(q_empty, 1);
         mbar_init(end_bar, 1);
         abort_word = odd_word = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
         fence_proxy_async();
     }
+    // (a kernel that started before this one's end may hold tensor memory while it waits for that end: this one takes
+    // its own only when nothing is left before it, and lets the next one start only then)
+    overlap_wait();
     if (warp == WARP_MMA) {
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_addr(&tmem_word)),
                      "r"(TMEM_COLS)
@@ -295,97 +370,144 @@ __global__ void __launch_bounds__(THREADS, 1)
     fence_before();
     __syncthreads();
     fence_after();
-    // (only now: a kernel that starts here may want tensor memory too, and waits for this one's end while it holds it)
     overlap_trigger();
     const uint32_t tmem = tmem_word;
-    // key tiles of either row tile; those from `masked` on hold keys that some row must not see
-    const int last = item.len - 1;
-    const int n0 = min(last, item.tok0 + a.tile_tokens - 1) / BN + 1;
-    const int n1 = item.tok0 + a.tile_tokens > last ? 0 : min(last, item.tok0 + 2 * a.tile_tokens - 1) / BN + 1;
-    const int n = max(n0, n1), masked = item.tok0 / BN;
+
+    // the CTA's next item, for every warp but the loader's: i counts them
+    auto next_item = [&](int i, Item &item) {
+        if (!__all_sync(0xffffffffu, mbar_wait(&item_full[i & 1], (i >> 1) & 1, abort_flag, a.err)))
+            return false;
+        item = items[i & 1];
+        __syncwarp();
+        if (lane == 0)
+            mbar_arrive(&item_empty[i & 1]);
+        return item.len > 0;
+    };
 
     if (warp == WARP_LOAD) {
-        // ------------------------------------------------------ tiles -> shared memory
-        if (lane == 0) {
-            const int rows = a.group * a.tile_tokens, both = n1 > 0 ? 2 : 1;
-            mbar_arrive_expect_tx(q_full, both * rows * D * 2);
-            for (int t = 0; t < both; ++t)
-                for (int h = 0; h < D / 64; ++h)
-                    tma_4d(smem + t * G::TILE_B + h * (BM * 128), &map_q, 0, item.kvh * a.group,
-                           item.start + item.tok0 + t * a.tile_tokens, h, q_full);
-        }
-        // K0 V0 K1 V1 ...  The values of the masked tiles land on barriers of their own, where the guards wait for them
-        // (a waiter that skipped phases of a slot's barrier could take an older one for its own); no slot of these last
-        // tiles is used again.
-        int slot = 0, it = 0;
-        uint32_t ph = 0;
-        for (; it < 2 * n; ++it) {
-            const int j = it >> 1;
-            const bool is_v = it & 1;
-            if (!mbar_wait_sleep_warp(&empty[slot], ph ^ 1, abort_flag, a.err, lane))
+        // ------------------------------------------------------ items, and tiles -> shared memory
+        // Items go to the CTAs forth and back, so that none has the longest of every round.  K0 V0 K1 V1 ... of an item;
+        // the values of masked tiles land on another barrier of their slot, where the guards wait for them.  Everyone who
+        // waits for a slot's barrier so waits for each of its phases, and none comes before the slot was free again: no
+        // phase can pass unseen.
+        Walk walk;
+        walk.begin(a, lane);
+        int slot = 0;
+        uint32_t ph = 0, slot_parity = 0, land_parity = 0, armed = 0, armed_land = 0;
+        bool ok = true;
+        const int ctas = (int)gridDim.x, cta = (int)blockIdx.x;
+        for (int i = 0; ok; ++i) {
+            const Item item = walk.at(a, i & 1 ? (i + 1) * ctas - 1 - cta : i * ctas + cta, lane);
+            if (!(ok = mbar_wait_sleep_warp(&item_empty[i & 1], ((i >> 1) & 1) ^ 1, abort_flag, a.err, lane)))
                 break;
             if (lane == 0) {
-                uint64_t *bar = is_v && j >= masked ? &v_land[j - masked] : &full[slot];
-                mbar_arrive_expect_tx(bar, G::TILE_B);
-                tma_4d(smem + G::RING_OFF + slot * G::TILE_B, is_v ? &map_v : &map_k, 0, item.kvh, item.start + j * BN, 0,
-                       bar);
+                items[i & 1] = item;
+                mbar_arrive(&item_full[i & 1]);
             }
-            if (++slot == G::SLOTS) {
-                slot = 0;
-                ph ^= 1;
+            if (item.len == 0)
+                break;
+            const Tiles tl = tiles_of(a, item);
+            for (int it = 0; it < 2 * tl.n; ++it) {
+                const int j = it >> 1;
+                const bool is_v = it & 1;
+                if (!(ok = mbar_wait_sleep_warp(&empty[slot], ph ^ 1, abort_flag, a.err, lane)))
+                    break;
+                const bool land = is_v && j >= tl.masked;
+                if (lane == 0) {
+                    uint64_t *bar = land ? &v_land[slot] : &full[slot];
+                    mbar_arrive_expect_tx(bar, G::TILE_B);
+                    tma_4d(smem + G::RING_OFF + slot * G::TILE_B, is_v ? &map_v : &map_k, 0, item.kvh, item.start + j * BN,
+                           0, bar);
+                }
+                if (land) {
+                    land_parity ^= 1u << slot;
+                    armed_land |= 1u << slot;
+                } else {
+                    slot_parity ^= 1u << slot;
+                    armed |= 1u << slot;
+                }
+                if (++slot == G::SLOTS) {
+                    slot = 0;
+                    ph ^= 1;
+                }
+                if (it == 1) {  // (the queries' place is free later than the first tiles')
+                    if (!(ok = mbar_wait_sleep_warp(q_empty, (i & 1) ^ 1, abort_flag, a.err, lane)))
+                        break;
+                    if (lane == 0) {
+                        const int rows = a.group * a.tile_tokens, both = tl.n1 > 0 ? 2 : 1;
+                        mbar_arrive_expect_tx(q_full, both * rows * D * 2);
+                        for (int t = 0; t < both; ++t)
+                            for (int h = 0; h < D / 64; ++h)
+                                tma_4d(smem + t * G::TILE_B + h * (BM * 128), &map_q, 0, item.kvh * a.group,
+                                       item.start + item.tok0 + t * a.tile_tokens, h, q_full);
+                    }
+                }
             }
         }
-        // every copy has landed before the CTA ends (at once on the normal path; bounded)
-        if (lane == 0) {
+        // every copy has landed before the CTA ends (at once on the normal path, where the MMAs have read them; bounded)
+        if (lane == 0 && !ok) {
+            for (int i = 0; i < G::SLOTS; ++i)
+                if (armed >> i & 1)
+                    mbar_drain(&full[i], (slot_parity >> i & 1) ^ 1);
+            for (int i = 0; i < G::SLOTS; ++i)
+                if (armed_land >> i & 1)
+                    mbar_drain(&v_land[i], (land_parity >> i & 1) ^ 1);
             mbar_drain(q_full, 0);
-            for (int i = it > G::SLOTS ? it - G::SLOTS : 0; i < it; ++i) {
-                if ((i & 1) && (i >> 1) >= masked)
-                    mbar_drain(&v_land[(i >> 1) - masked], 0);
-                else
-                    mbar_drain(&full[i % G::SLOTS], (i / G::SLOTS) & 1);
-            }
+            mbar_drain(q_full, 1);
         }
         __syncwarp();
     } else if (warp >= WARP_GUARD) {
         // ------------------------------------------------------ values that no row, or not every row, may see
-        for (int j = masked; j < n; ++j) {
-            if (!mbar_wait_sleep_warp(&v_land[j - masked], 0, abort_flag, a.err, lane))
-                break;
-            uint8_t *tile = smem + G::RING_OFF + (2 * j + 1) % G::SLOTS * G::TILE_B;
-            const int held = item.len - j * BN;  // rows of the tile within the sequence
-            bool odd = false;
-            for (int i = (warp - WARP_GUARD) * 32 + lane; i < G::TILE_B / 16; i += GUARDS * 32) {
-                uint4 *p = reinterpret_cast<uint4 *>(tile) + i;
-                uint4 v = *p;
-                if (i / 8 % BN >= held) {
-                    *p = make_uint4(0, 0, 0, 0);
-                    continue;
-                }
-                uint32_t *w = reinterpret_cast<uint32_t *>(&v);
-                bool bad = false;
+        Item item;
+        int slot = 0;              // of the item's first key tile
+        uint32_t land_parity = 0;
+        for (int i = 0; next_item(i, item); ++i) {
+            const Tiles tl = tiles_of(a, item);
+            bool ok = true;
+            for (int j = tl.masked; j < tl.n; ++j) {
+                const int at = (slot + 2 * j + 1) % G::SLOTS;
+                if (!(ok = mbar_wait_sleep_warp(&v_land[at], land_parity >> at & 1, abort_flag, a.err, lane)))
+                    break;
+                land_parity ^= 1u << at;
+                uint8_t *tile = smem + G::RING_OFF + at * G::TILE_B;
+                const int held = item.len - j * BN;  // rows of the tile within the sequence
+                bool odd = false;
+                for (int c = (warp - WARP_GUARD) * 32 + lane; c < G::TILE_B / 16; c += GUARDS * 32) {
+                    uint4 *p = reinterpret_cast<uint4 *>(tile) + c;
+                    uint4 v = *p;
+                    if (c / 8 % BN >= held) {
+                        *p = make_uint4(0, 0, 0, 0);
+                        continue;
+                    }
+                    uint32_t *w = reinterpret_cast<uint32_t *>(&v);
+                    bool bad = false;
 #pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    if ((w[k] & 0x7F80u) == 0x7F80u) {
-                        w[k] &= 0xFFFF0000u;
-                        bad = true;
+                    for (int k = 0; k < 4; ++k) {
+                        if ((w[k] & 0x7F80u) == 0x7F80u) {
+                            w[k] &= 0xFFFF0000u;
+                            bad = true;
+                        }
+                        if ((w[k] & 0x7F800000u) == 0x7F800000u) {
+                            w[k] &= 0xFFFFu;
+                            bad = true;
+                        }
                     }
-                    if ((w[k] & 0x7F800000u) == 0x7F800000u) {
-                        w[k] &= 0xFFFFu;
-                        bad = true;
+                    if (bad) {
+                        *p = v;
+                        odd = true;
                     }
                 }
-                if (bad) {
-                    *p = v;
-                    odd = true;
-                }
+                if (odd)
+                    odd_word = 1;
+                __threadfence_block();
+                fence_proxy_async();
+                __syncwarp();
+                if (lane == 0)
+                    mbar_arrive(&v_clear[at]);
             }
-            if (odd)
-                odd_word = 1;
-            __threadfence_block();
-            fence_proxy_async();
-            __syncwarp();
-            if (lane == 0)
-                mbar_arrive(&v_clear[j - masked]);
+            if (!ok)
+                break;
+            slot = (slot + 2 * tl.n) % G::SLOTS;
         }
         __syncwarp();
     } else if (warp == WARP_MMA) {
@@ -398,61 +520,88 @@ __global__ void __launch_bounds__(THREADS, 1)
         const uint64_t dq = desc_k(smem_addr(smem)), dk = desc_k(smem_addr(smem + G::RING_OFF));
         const uint64_t dv = desc_n(smem_addr(smem + G::RING_OFF));
         constexpr uint64_t TILE16 = G::TILE_B / 16, HALF16 = BM * 128 / 16;
-        auto scores = [&](int t, int slot) {  // S of row tile t and the keys in the slot
+        uint32_t slot_parity = 0, clear_parity = 0, p_parity = 0;
+        int slot = 0;
+        auto wait_slot = [&](int at) {
+            if (!wait(&full[at], slot_parity >> at & 1))
+                return false;
+            slot_parity ^= 1u << at;
+            return true;
+        };
+        auto scores = [&](int t, int at) {  // S of row tile t and the keys in the slot
             if (elected) {
 #pragma unroll
                 for (int k = 0; k < D / 16; ++k) {
                     const uint64_t o = (k / 4) * HALF16 + (k % 4) * 2;
-                    mma_ss(tmem + t * BN, dq + t * TILE16 + o, dk + slot * TILE16 + o, instr_desc(BN, false), k > 0);
+                    mma_ss(tmem + t * BN, dq + t * TILE16 + o, dk + at * TILE16 + o, instr_desc(BN, false), k > 0);
                 }
                 commit(&s_full[t]);
             }
             __syncwarp();
         };
-        bool ok = wait(q_full, 0) && wait(&full[0], 0);
-        fence_after();
-        if (ok) {
-            scores(0, 0);
-            if (n1 > 0)
-                scores(1, 0);
-            if (elected)
-                commit(&empty[0]);
+        Item item;
+        for (int i = 0; next_item(i, item); ++i) {
+            const Tiles tl = tiles_of(a, item);
+            bool ok = wait(q_full, i & 1) && wait_slot(slot);
+            if (!ok)
+                break;
+            fence_after();
+            // (P of the item before lies in these columns: its products come before these in the queue)
+            scores(0, slot);
+            if (tl.n1 > 0)
+                scores(1, slot);
+            if (elected) {
+                commit(&empty[slot]);
+                if (tl.n == 1)
+                    commit(q_empty);
+            }
             __syncwarp();
-        }
-        int it = 1;  // the value tile's place in the loader's order
-        for (int j = 0; ok && j < n; ++j, it += 2) {
-            const int vs = it % G::SLOTS, ks = (it + 1) % G::SLOTS;
-            const uint32_t vph = (it / G::SLOTS) & 1, kph = ((it + 1) / G::SLOTS) & 1;
-            if (!(ok = j >= masked ? wait(&v_clear[j - masked], 0) : wait(&full[vs], vph)))
-                break;
-            if (j + 1 < n && !(ok = wait(&full[ks], kph)))
-                break;
-#pragma unroll
-            for (int t = 0; t < 2; ++t) {
-                const int nt = t ? n1 : n0;
-                if (j >= nt)
-                    continue;
-                if (!(ok = ok && wait(&p_full[t], j & 1)))
+            for (int j = 0; j < tl.n; ++j) {
+                const int vs = slot + 1 < G::SLOTS ? slot + 1 : 0, ks = vs + 1 < G::SLOTS ? vs + 1 : 0;
+                if (j >= tl.masked) {
+                    if (!(ok = wait(&v_clear[vs], clear_parity >> vs & 1)))
+                        break;
+                    clear_parity ^= 1u << vs;
+                } else if (!(ok = wait_slot(vs))) {
                     break;
-                fence_after();
-                if (elected) {
+                }
+                if (j + 1 < tl.n && !(ok = wait_slot(ks)))
+                    break;
 #pragma unroll
-                    for (int k = 0; k < BN / 16; ++k)
-                        mma_ts(tmem + 2 * BN + t * D, tmem + t * BN + 8 * k, dv + vs * TILE16 + k * (16 * 128 / 16),
-                               instr_desc(D, true), j > 0 || k > 0);
-                    if (j + 1 == nt)
-                        commit(&o_full[t]);
+                for (int t = 0; t < 2; ++t) {
+                    const int nt = t ? tl.n1 : tl.n0;
+                    if (j >= nt || !ok)
+                        continue;
+                    if (!(ok = wait(&p_full[t], p_parity >> t & 1)))
+                        continue;
+                    p_parity ^= 1u << t;
+                    fence_after();
+                    if (elected) {
+#pragma unroll
+                        for (int k = 0; k < BN / 16; ++k)
+                            mma_ts(tmem + 2 * BN + t * D, tmem + t * BN + 8 * k, dv + vs * TILE16 + k * (16 * 128 / 16),
+                                   instr_desc(D, true), j > 0 || k > 0);
+                        if (j + 1 == nt)
+                            commit(&o_full[t]);
+                    }
+                    __syncwarp();
+                    if (j + 1 < nt)
+                        scores(t, ks);
+                }
+                if (!ok)
+                    break;
+                if (elected) {
+                    commit(&empty[vs]);
+                    if (j + 1 < tl.n)
+                        commit(&empty[ks]);
+                    if (j + 2 == tl.n)
+                        commit(q_empty);
                 }
                 __syncwarp();
-                if (j + 1 < nt)
-                    scores(t, ks);
+                slot = ks;  // (after the last tile: the next item's first)
             }
-            if (elected) {
-                commit(&empty[vs]);
-                if (j + 1 < n)
-                    commit(&empty[ks]);
-            }
-            __syncwarp();
+            if (!ok)
+                break;
         }
         // also after an abort: what was issued has completed before the tensor memory is freed
         if (elected) {
@@ -462,82 +611,91 @@ __global__ void __launch_bounds__(THREADS, 1)
         __syncwarp();
     } else {
         // ------------------------------------------------------ softmax: a thread per row
-        const int t = warp >> 2, row = (warp & 3) * 32 + lane, nt = t ? n1 : n0;
+        const int t = warp >> 2, row = (warp & 3) * 32 + lane, in_tile = row / a.group, head = row - in_tile * a.group;
         const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
         const uint32_t ts = tmem + lanes + t * BN, to = tmem + lanes + 2 * BN + t * D;
-        const int tok = item.tok0 + t * a.tile_tokens + row / a.group;  // within the sequence
-        const bool valid = row < a.group * a.tile_tokens && tok < item.len;
-        const int sees = valid ? tok + 1 : 0x40000000;  // keys that the row sees
-        float m = -INFINITY, l = 0.f;                   // m: of scaled scores, the one in use
-        bool ok = true;
-        for (int j = 0; j < nt; ++j) {
-            if (!(ok = __all_sync(0xffffffffu, mbar_wait(&s_full[t], j & 1, abort_flag, a.err)) != 0))
-                break;
-            fence_after();
-            uint32_t s[BN];
+        uint32_t s_parity = 0, o_parity = 0;
+        Item item;
+        for (int i = 0; next_item(i, item); ++i) {
+            const Tiles tl = tiles_of(a, item);
+            const int nt = t ? tl.n1 : tl.n0;
+            if (nt == 0)
+                continue;
+            const int tok = item.tok0 + t * a.tile_tokens + in_tile;  // within the sequence
+            const bool valid = in_tile < a.tile_tokens && tok < item.len;
+            const int sees = valid ? tok + 1 : 0x40000000;  // keys that the row sees
+            float m = -INFINITY, l = 0.f;                   // m: of scaled scores, the one in use
+            bool ok = true;
+            for (int j = 0; j < nt; ++j) {
+                if (!(ok = __all_sync(0xffffffffu, mbar_wait(&s_full[t], s_parity, abort_flag, a.err)) != 0))
+                    break;
+                s_parity ^= 1;
+                fence_after();
+                uint32_t s[BN];
 #pragma unroll
-            for (int c = 0; c < BN; c += 32)
-                tmem_ld32(ts + c, s + c);
-            wait_ld();
-            if (j >= masked) {
-                const int vis = sees - j * BN;
+                for (int c = 0; c < BN; c += 32)
+                    tmem_ld32(ts + c, s + c);
+                wait_ld();
+                if (j >= tl.masked) {
+                    const int vis = sees - j * BN;
 #pragma unroll
-                for (int c = 0; c < BN; ++c)
-                    s[c] = c < vis ? s[c] : 0xFF800000u;
-            }
-            float mx = __uint_as_float(s[0]);
-#pragma unroll
-            for (int c = 1; c < BN; ++c)
-                mx = fmaxf(mx, __uint_as_float(s[c]));
-            mx *= a.scale;
-            const bool grown = mx > m + GROWTH && valid;
-            if (j == 0) {
-                m = mx;
-            } else if (__any_sync(0xffffffffu, grown)) {
-                const float next = grown ? mx : m, f = ex2(m - (next == -INFINITY ? 0.f : next));
-                m = next;
-                l *= f;
+                    for (int c = 0; c < BN; ++c)
+                        s[c] = c < vis ? s[c] : 0xFF800000u;
+                }
+                const float mx = a.scale * row_max(s);
+                const bool grown = mx > m + GROWTH && valid;
+                if (j == 0) {
+                    m = mx;
+                } else if (__any_sync(0xffffffffu, grown)) {
+                    const float next = grown ? mx : m, f = ex2(m - (next == -INFINITY ? 0.f : next));
+                    m = next;
+                    l *= f;
 #pragma unroll 1
-                for (int c = 0; c < D; c += 32) {
-                    uint32_t o[32];
-                    tmem_ld32(to + c, o);
-                    wait_ld();
+                    for (int c = 0; c < D; c += 32) {
+                        uint32_t o[32];
+                        tmem_ld32(to + c, o);
+                        wait_ld();
 #pragma unroll
-                    for (int i = 0; i < 32; ++i)
-                        o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
-                    tmem_st32(to + c, o);
+                        for (int k = 0; k < 32; ++k)
+                            o[k] = __float_as_uint(__uint_as_float(o[k]) * f);
+                        tmem_st32(to + c, o);
+                    }
                 }
-            }
-            const float base = m == -INFINITY ? 0.f : m;
-            float sum[4] = {0.f, 0.f, 0.f, 0.f};
+                const float base = m == -INFINITY ? 0.f : m;
+                const uint64_t mul2 = pack2(a.scale, a.scale), base2 = pack2(-base, -base);
+                uint64_t sum[4] = {0, 0, 0, 0};
 #pragma unroll
-            for (int c = 0; c < BN; c += 64) {
-                uint32_t p[32];
+                for (int c = 0; c < BN; c += 64) {
+                    uint32_t p[32];
 #pragma unroll
-                for (int i = 0; i < 32; ++i) {
-                    const float p0 = ex2(fmaf(__uint_as_float(s[c + 2 * i]), a.scale, -base));
-                    const float p1 = ex2(fmaf(__uint_as_float(s[c + 2 * i + 1]), a.scale, -base));
-                    sum[i & 3] += p0 + p1;
-                    // rounded to BF16 for the product (2^-9 of each, of random sign): v is BF16, and an MMA's
-                    // operands share a type
-                    p[i] = bf16_pair(p0, p1);
+                    for (int k = 0; k < 32; ++k) {
+                        const float2 x = unpack2(fma2(pack2(__uint_as_float(s[c + 2 * k]), __uint_as_float(s[c + 2 * k + 1])),
+                                                      mul2, base2));
+                        const float p0 = ex2(x.x), p1 = ex2(x.y);
+                        sum[k & 3] = add2(sum[k & 3], pack2(p0, p1));
+                        // rounded to BF16 for the product (2^-9 of each, of random sign): v is BF16, and an MMA's
+                        // operands share a type
+                        p[k] = bf16_pair(p0, p1);
+                    }
+                    tmem_st32(ts + c / 2, p);
                 }
-                tmem_st32(ts + c / 2, p);
+                const float2 sums = unpack2(add2(add2(sum[0], sum[1]), add2(sum[2], sum[3])));
+                l += sums.x + sums.y;
+                wait_st();
+                fence_before();
+                __syncwarp();
+                if (lane == 0)
+                    mbar_arrive(&p_full[t]);
             }
-            l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
-            wait_st();
-            fence_before();
-            __syncwarp();
-            if (lane == 0)
-                mbar_arrive(&p_full[t]);
-        }
-        ok = ok && nt > 0 && __all_sync(0xffffffffu, mbar_wait(&o_full[t], 0, abort_flag, a.err)) != 0;
-        if (ok) {
+            ok = ok && __all_sync(0xffffffffu, mbar_wait(&o_full[t], o_parity, abort_flag, a.err)) != 0;
+            if (!ok)
+                break;
+            o_parity ^= 1;
             fence_after();
             const float inv = 1.f / l;
             const bool odd = *static_cast<volatile int *>(&odd_word) != 0;
-            const int at = item.start + tok;
-            uint16_t *out = a.out + at * a.out_ld + (long long)(item.kvh * a.group + row % a.group) * D;
+            const long long at = item.start + tok;
+            uint16_t *out = a.out + at * a.out_ld + (long long)(item.kvh * a.group + head) * D;
 #pragma unroll 1
             for (int c = 0; c < D; c += 32) {
                 uint32_t o[32];
@@ -546,24 +704,24 @@ __global__ void __launch_bounds__(THREADS, 1)
                 if (valid) {
                     float v[32];
 #pragma unroll
-                    for (int i = 0; i < 32; ++i)
-                        v[i] = __uint_as_float(o[i]) * inv;
+                    for (int k = 0; k < 32; ++k)
+                        v[k] = __uint_as_float(o[k]) * inv;
                     if (odd) {  // what the guards cleared, for the rows that see it
-                        for (int k = masked * BN; k <= tok; ++k) {
-                            const uint16_t *p = a.v + (item.start + k) * a.v_ld + (long long)item.kvh * D + c;
+                        for (int r = tl.masked * BN; r <= tok; ++r) {
+                            const uint16_t *p = a.v + (item.start + r) * a.v_ld + (long long)item.kvh * D + c;
 #pragma unroll
-                            for (int i = 0; i < 32; ++i) {
-                                const float x = __uint_as_float((uint32_t)__ldcg(p + i) << 16);
-                                v[i] += isfinite(x) ? 0.f : x;
+                            for (int k = 0; k < 32; ++k) {
+                                const float x = __uint_as_float((uint32_t)__ldcg(p + k) << 16);
+                                v[k] += isfinite(x) ? 0.f : x;
                             }
                         }
                     }
 #pragma unroll
-                    for (int i = 0; i < 32; i += 8)
-                        *reinterpret_cast<uint4 *>(out + c + i) = bf16x8(v + i);
+                    for (int k = 0; k < 32; k += 8)
+                        *reinterpret_cast<uint4 *>(out + c + k) = bf16x8(v + k);
                 }
             }
-            fence_before();
+            fence_before();  // (the next item's first product into O waits for its P, which comes after this)
         }
     }
     __syncthreads();
@@ -610,8 +768,9 @@ cudaError_t launch_prompt(const PromptArgs &a, const void *q, long long q_ld, co
         e = rows_map(&mv, a.v, a.v_ld, a.T, a.kv, D, 1, BN, D / 64);
     if (e != cudaSuccess)
         return e;
-    // at most this many: every sequence rounds up to whole CTAs
-    const long long grid = ((long long)a.T / (2 * a.tile_tokens) + a.n_seqs) * a.kv;
+    // a CTA per SM, or per item where there are fewer (at most: every sequence rounds up to whole items)
+    const long long items = ((long long)a.T / (2 * a.tile_tokens) + a.n_seqs) * a.kv;
+    const long long grid = items < sm_count() ? items : sm_count();
     return launch_overlapped(kern, (unsigned)grid, THREADS, PGeo<D>::SMEM, 1, st, a, mq, mk, mv);
 }
 

@@ -47,6 +47,8 @@ CASES = [
     ([128], 2, 2, 64), ([255, 256, 257], 4, 4, 64), ([1, 0, 3, 0, 0, 200, 1], 7, 1, 128), ([513], 64, 8, 128),
     ([1000, 24], 12, 4, 64), ([1025], 6, 6, 128), ([1] * 70, 16, 2, 64), ([300, 1, 700], 40, 8, 128),
     ([640, 513], 48, 1, 64), ([2500], 2, 1, 128), ([40 * i % 300 for i in range(30)], 5, 1, 64), ([37] * 400, 2, 1, 64),
+    ([130 * i % 777 for i in range(60)], 14, 2, 128), ([1 + 211 * i % 1500 for i in range(15)], 56, 8, 128),
+    ([90 * i % 400 for i in range(200)], 8, 8, 64),
 ]
 
 
