@@ -51,6 +51,7 @@ struct PromptArgs {
     float scale;                        // times log2(e)
     uint16_t *out;
     long long out_ld;
+    bool wide_out;                      // rows of out start on 32-byte boundaries
     int *err;
 };
 
@@ -301,6 +302,45 @@ struct Walk {
     }
 };
 
+// 32 bytes of a row
+__device__ __forceinline__ void st256(uint16_t *p, const uint32_t (&w)[8])
+{
+    asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(p), "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3]),
+                 "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+                 : "memory");
+}
+
+__device__ __forceinline__ void st128x2(uint16_t *p, const uint32_t (&w)[8])
+{
+    reinterpret_cast<uint4 *>(p)[0] = make_uint4(w[0], w[1], w[2], w[3]);
+    reinterpret_cast<uint4 *>(p)[1] = make_uint4(w[4], w[5], w[6], w[7]);
+}
+
+// Adds to a row's sums, per value, what is not finite among the values of the tokens first .. last: what the sum over
+// all of them would be (a probability is above 0).
+template <int D>
+__device__ __noinline__ void add_cleared_to(const uint16_t *v, long long ld, int n, float *sums)
+{
+    for (int r = 0; r < n; ++r)
+        for (int k = 0; k < D; ++k) {
+            const float x = __uint_as_float((uint32_t)__ldcg(v + r * ld + k) << 16);
+            sums[k] += isfinite(x) ? 0.f : x;
+        }
+}
+
+template <int D>
+__device__ __forceinline__ void add_cleared(const PromptArgs &a, const Item &item, int first, int last, uint32_t (&o)[D])
+{
+    float sums[D];
+#pragma unroll
+    for (int k = 0; k < D; ++k)
+        sums[k] = 0.f;
+    add_cleared_to<D>(a.v + (item.start + first) * a.v_ld + (long long)item.kvh * D, a.v_ld, last - first + 1, sums);
+#pragma unroll
+    for (int k = 0; k < D; ++k)
+        o[k] = __float_as_uint(__uint_as_float(o[k]) + sums[k]);
+}
+
 // Key tiles of an item's two row tiles; those from `masked` on hold keys that some row must not see.
 struct Tiles {
     int n0, n1, n, masked;
@@ -471,30 +511,40 @@ __global__ void __launch_bounds__(THREADS, 1)
                 land_parity ^= 1u << at;
                 uint8_t *tile = smem + G::RING_OFF + at * G::TILE_B;
                 const int held = item.len - j * BN;  // rows of the tile within the sequence
+                const int me = (warp - WARP_GUARD) * 32 + lane;
                 bool odd = false;
-                for (int c = (warp - WARP_GUARD) * 32 + lane; c < G::TILE_B / 16; c += GUARDS * 32) {
-                    uint4 *p = reinterpret_cast<uint4 *>(tile) + c;
-                    uint4 v = *p;
-                    if (c / 8 % BN >= held) {
-                        *p = make_uint4(0, 0, 0, 0);
-                        continue;
-                    }
-                    uint32_t *w = reinterpret_cast<uint32_t *>(&v);
-                    bool bad = false;
+                // (rows past the end: a sequence's last tile alone has any)
+                for (int h = 0; h < D / 64; ++h)
+                    for (int c = max(0, held) * 8 + me; c < BN * 8; c += GUARDS * 32)
+                        reinterpret_cast<uint4 *>(tile)[h * BN * 8 + c] = make_uint4(0, 0, 0, 0);
+                __syncwarp();  // (both guards may write the same zeros: what one reads as it was it leaves)
+#pragma unroll 1
+                for (int c = me; c < G::TILE_B / 16; c += 8 * GUARDS * 32) {
+                    uint4 v[8];
 #pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        if ((w[k] & 0x7F80u) == 0x7F80u) {
-                            w[k] &= 0xFFFF0000u;
-                            bad = true;
+                    for (int k = 0; k < 8; ++k)
+                        v[k] = reinterpret_cast<const uint4 *>(tile)[c + k * GUARDS * 32];
+                    uint32_t any = 0;  // an exponent of ones carries into the sign's place
+#pragma unroll
+                    for (int k = 0; k < 8; ++k)
+                        any |= ((v[k].x & 0x7F807F80u) + 0x00800080u) | ((v[k].y & 0x7F807F80u) + 0x00800080u) |
+                               ((v[k].z & 0x7F807F80u) + 0x00800080u) | ((v[k].w & 0x7F807F80u) + 0x00800080u);
+                    if (!(any & 0x80008000u))
+                        continue;
+#pragma unroll 1
+                    for (int k = 0; k < 8; ++k) {
+                        uint32_t *w = reinterpret_cast<uint32_t *>(tile) + 4 * (c + k * GUARDS * 32);
+                        if ((c + k * GUARDS * 32) / 8 % BN >= held)
+                            continue;  // (already, or about to be, zeros)
+                        for (int i = 0; i < 4; ++i) {
+                            const uint32_t x = w[i];
+                            const uint32_t clear = ((x & 0x7F80u) == 0x7F80u ? 0xFFFFu : 0u) |
+                                                   ((x & 0x7F800000u) == 0x7F800000u ? 0xFFFF0000u : 0u);
+                            if (clear) {
+                                w[i] = x & ~clear;
+                                odd = true;
+                            }
                         }
-                        if ((w[k] & 0x7F800000u) == 0x7F800000u) {
-                            w[k] &= 0xFFFFu;
-                            bad = true;
-                        }
-                    }
-                    if (bad) {
-                        *p = v;
-                        odd = true;
                     }
                 }
                 if (odd)
@@ -695,30 +745,26 @@ __global__ void __launch_bounds__(THREADS, 1)
             const float inv = 1.f / l;
             const bool odd = *static_cast<volatile int *>(&odd_word) != 0;
             const long long at = item.start + tok;
+            const bool wide = a.wide_out;
             uint16_t *out = a.out + at * a.out_ld + (long long)(item.kvh * a.group + head) * D;
-#pragma unroll 1
-            for (int c = 0; c < D; c += 32) {
-                uint32_t o[32];
-                tmem_ld32(to + c, o);
-                wait_ld();
-                if (valid) {
-                    float v[32];
+            uint32_t o[D];
 #pragma unroll
-                    for (int k = 0; k < 32; ++k)
-                        v[k] = __uint_as_float(o[k]) * inv;
-                    if (odd) {  // what the guards cleared, for the rows that see it
-                        for (int r = tl.masked * BN; r <= tok; ++r) {
-                            const uint16_t *p = a.v + (item.start + r) * a.v_ld + (long long)item.kvh * D + c;
+            for (int c = 0; c < D; c += 32)
+                tmem_ld32(to + c, o + c);
+            wait_ld();
+            if (odd && valid)  // what the guards cleared, for the rows that see it
+                add_cleared<D>(a, item, tl.masked * BN, tok, o);
+            if (valid) {
 #pragma unroll
-                            for (int k = 0; k < 32; ++k) {
-                                const float x = __uint_as_float((uint32_t)__ldcg(p + k) << 16);
-                                v[k] += isfinite(x) ? 0.f : x;
-                            }
-                        }
-                    }
+                for (int c = 0; c < D; c += 16) {
+                    uint32_t w[8];
 #pragma unroll
-                    for (int k = 0; k < 32; k += 8)
-                        *reinterpret_cast<uint4 *>(out + c + k) = bf16x8(v + k);
+                    for (int k = 0; k < 8; ++k)
+                        w[k] = bf16_pair(__uint_as_float(o[c + 2 * k]) * inv, __uint_as_float(o[c + 2 * k + 1]) * inv);
+                    if (wide)
+                        st256(out + c, w);
+                    else
+                        st128x2(out + c, w);
                 }
             }
             fence_before();  // (the next item's first product into O waits for its P, which comes after this)
@@ -827,6 +873,7 @@ extern "C" MoeStatus moe_attention_prompt(const void *q, long long q_ld, const v
         a.scale = scale * 1.44269504088896340736f;
         a.out = static_cast<uint16_t *>(out);
         a.out_ld = out_ld;
+        a.wide_out = (uintptr_t)out % 32 == 0 && out_ld % 16 == 0;
         cudaStream_t st = (cudaStream_t)cuda_stream;
         e = D == 128 ? launch_prompt<128>(a, q, q_ld, k, k_ld, st) : launch_prompt<64>(a, q, q_ld, k, k_ld, st);
     }
