@@ -40,6 +40,9 @@ constexpr int THREADS = 384;
 constexpr int WARP_MMA = 8, WARP_LOAD = 9, WARP_GUARD = 10;
 constexpr int GUARDS = 2;
 constexpr int TMEM_COLS = 512;
+// Registers: 168 a thread at launch; the warps that do not compute rows give some of theirs to those that do.
+constexpr int SOFTMAX_REGS = 208, OTHER_REGS = 80;
+static_assert(256 * SOFTMAX_REGS + 128 * OTHER_REGS <= 168 * THREADS, "the launch's registers");
 constexpr float GROWTH = 8.f;        // log2 by which a row's maximum may exceed the one in use
 
 struct PromptArgs {
@@ -202,6 +205,42 @@ __device__ __forceinline__ void tma_4d(void *dst, const CUtensorMap *map, int x,
         : "memory");
 }
 
+// Bounded waits (gemm_common.cuh) without calls: a function's registers are the launch's, which the warps here have
+// shared out anew.
+__device__ __forceinline__ bool wait_for(uint64_t *bar, uint32_t parity, volatile int *abort_flag, int *err)
+{
+    if (mbar_try_wait(bar, parity))
+        return true;
+    const uint64_t t0 = global_ns();
+#pragma unroll 1
+    for (uint32_t i = 1;; ++i) {
+        if (mbar_try_wait(bar, parity))
+            return true;
+        if ((i & 7u) == 0) {
+            if (*abort_flag)
+                return false;
+            if (global_ns() - t0 > WAIT_LIMIT_NS) {
+                atomicCAS(err, 0, DEV_ERR_WAIT_TIMEOUT);
+                *abort_flag = 1;
+                return false;
+            }
+        }
+    }
+}
+
+__device__ __forceinline__ bool wait_for_warp(uint64_t *bar, uint32_t parity, volatile int *abort_flag, int *err)
+{
+    return __all_sync(0xffffffffu, wait_for(bar, parity, abort_flag, err)) != 0;
+}
+
+__device__ __forceinline__ void drain(uint64_t *bar, uint32_t parity)
+{
+    const uint64_t t0 = global_ns();
+#pragma unroll 1
+    while (!mbar_try_wait(bar, parity) && global_ns() - t0 <= WAIT_LIMIT_NS) {
+    }
+}
+
 // ---------------------------------------------------------------- which rows
 
 struct Span {
@@ -316,29 +355,20 @@ __device__ __forceinline__ void st128x2(uint16_t *p, const uint32_t (&w)[8])
     reinterpret_cast<uint4 *>(p)[1] = make_uint4(w[4], w[5], w[6], w[7]);
 }
 
-// Adds to a row's sums, per value, what is not finite among the values of the tokens first .. last: what the sum over
-// all of them would be (a probability is above 0).
-template <int D>
-__device__ __noinline__ void add_cleared_to(const uint16_t *v, long long ld, int n, float *sums)
+// Adds to a row's sums what is not finite among the n values of a place in v and on, per value: what the sum over all
+// of them would be (a probability is above 0).
+template <int D> __device__ __forceinline__ void add_cleared(const uint16_t *v, long long ld, int n, uint32_t (&o)[D])
 {
-    for (int r = 0; r < n; ++r)
-        for (int k = 0; k < D; ++k) {
-            const float x = __uint_as_float((uint32_t)__ldcg(v + r * ld + k) << 16);
-            sums[k] += isfinite(x) ? 0.f : x;
+#pragma unroll 1
+    for (int r = 0; r < n; ++r) {
+#pragma unroll
+        for (int c = 0; c < D; c += 2) {
+            const uint32_t w = __ldcg(reinterpret_cast<const uint32_t *>(v + r * ld + c));
+            const float x = __uint_as_float(w << 16), y = __uint_as_float(w & 0xFFFF0000u);
+            o[c] = isfinite(x) ? o[c] : __float_as_uint(__uint_as_float(o[c]) + x);
+            o[c + 1] = isfinite(y) ? o[c + 1] : __float_as_uint(__uint_as_float(o[c + 1]) + y);
         }
-}
-
-template <int D>
-__device__ __forceinline__ void add_cleared(const PromptArgs &a, const Item &item, int first, int last, uint32_t (&o)[D])
-{
-    float sums[D];
-#pragma unroll
-    for (int k = 0; k < D; ++k)
-        sums[k] = 0.f;
-    add_cleared_to<D>(a.v + (item.start + first) * a.v_ld + (long long)item.kvh * D, a.v_ld, last - first + 1, sums);
-#pragma unroll
-    for (int k = 0; k < D; ++k)
-        o[k] = __float_as_uint(__uint_as_float(o[k]) + sums[k]);
+    }
 }
 
 // Key tiles of an item's two row tiles; those from `masked` on hold keys that some row must not see.
@@ -415,7 +445,7 @@ __global__ void __launch_bounds__(THREADS, 1)
 
     // the CTA's next item, for every warp but the loader's: i counts them
     auto next_item = [&](int i, Item &item) {
-        if (!__all_sync(0xffffffffu, mbar_wait(&item_full[i & 1], (i >> 1) & 1, abort_flag, a.err)))
+        if (!wait_for_warp(&item_full[i & 1], (i >> 1) & 1, abort_flag, a.err))
             return false;
         item = items[i & 1];
         __syncwarp();
@@ -425,6 +455,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     };
 
     if (warp == WARP_LOAD) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(OTHER_REGS));
         // ------------------------------------------------------ items, and tiles -> shared memory
         // Items go to the CTAs forth and back, so that none has the longest of every round.  K0 V0 K1 V1 ... of an item;
         // the values of masked tiles land on another barrier of their slot, where the guards wait for them.  Everyone who
@@ -438,7 +469,7 @@ __global__ void __launch_bounds__(THREADS, 1)
         const int ctas = (int)gridDim.x, cta = (int)blockIdx.x;
         for (int i = 0; ok; ++i) {
             const Item item = walk.at(a, i & 1 ? (i + 1) * ctas - 1 - cta : i * ctas + cta, lane);
-            if (!(ok = mbar_wait_sleep_warp(&item_empty[i & 1], ((i >> 1) & 1) ^ 1, abort_flag, a.err, lane)))
+            if (!(ok = wait_for_warp(&item_empty[i & 1], ((i >> 1) & 1) ^ 1, abort_flag, a.err)))
                 break;
             if (lane == 0) {
                 items[i & 1] = item;
@@ -450,7 +481,7 @@ __global__ void __launch_bounds__(THREADS, 1)
             for (int it = 0; it < 2 * tl.n; ++it) {
                 const int j = it >> 1;
                 const bool is_v = it & 1;
-                if (!(ok = mbar_wait_sleep_warp(&empty[slot], ph ^ 1, abort_flag, a.err, lane)))
+                if (!(ok = wait_for_warp(&empty[slot], ph ^ 1, abort_flag, a.err)))
                     break;
                 const bool land = is_v && j >= tl.masked;
                 if (lane == 0) {
@@ -471,7 +502,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                     ph ^= 1;
                 }
                 if (it == 1) {  // (the queries' place is free later than the first tiles')
-                    if (!(ok = mbar_wait_sleep_warp(q_empty, (i & 1) ^ 1, abort_flag, a.err, lane)))
+                    if (!(ok = wait_for_warp(q_empty, (i & 1) ^ 1, abort_flag, a.err)))
                         break;
                     if (lane == 0) {
                         const int rows = a.group * a.tile_tokens, both = tl.n1 > 0 ? 2 : 1;
@@ -488,15 +519,16 @@ __global__ void __launch_bounds__(THREADS, 1)
         if (lane == 0 && !ok) {
             for (int i = 0; i < G::SLOTS; ++i)
                 if (armed >> i & 1)
-                    mbar_drain(&full[i], (slot_parity >> i & 1) ^ 1);
+                    drain(&full[i], (slot_parity >> i & 1) ^ 1);
             for (int i = 0; i < G::SLOTS; ++i)
                 if (armed_land >> i & 1)
-                    mbar_drain(&v_land[i], (land_parity >> i & 1) ^ 1);
-            mbar_drain(q_full, 0);
-            mbar_drain(q_full, 1);
+                    drain(&v_land[i], (land_parity >> i & 1) ^ 1);
+            drain(q_full, 0);
+            drain(q_full, 1);
         }
         __syncwarp();
     } else if (warp >= WARP_GUARD) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(OTHER_REGS));
         // ------------------------------------------------------ values that no row, or not every row, may see
         Item item;
         int slot = 0;              // of the item's first key tile
@@ -506,7 +538,7 @@ __global__ void __launch_bounds__(THREADS, 1)
             bool ok = true;
             for (int j = tl.masked; j < tl.n; ++j) {
                 const int at = (slot + 2 * j + 1) % G::SLOTS;
-                if (!(ok = mbar_wait_sleep_warp(&v_land[at], land_parity >> at & 1, abort_flag, a.err, lane)))
+                if (!(ok = wait_for_warp(&v_land[at], land_parity >> at & 1, abort_flag, a.err)))
                     break;
                 land_parity ^= 1u << at;
                 uint8_t *tile = smem + G::RING_OFF + at * G::TILE_B;
@@ -561,11 +593,12 @@ __global__ void __launch_bounds__(THREADS, 1)
         }
         __syncwarp();
     } else if (warp == WARP_MMA) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(OTHER_REGS));
         // ------------------------------------------------------ MMAs: the warp runs the loop, one elected lane issues
         uint32_t elected;
         asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xFFFFFFFF;\n selp.u32 %0, 1, 0, p;\n}" : "=r"(elected));
         auto wait = [&](uint64_t *bar, uint32_t par) {
-            return __all_sync(0xffffffffu, mbar_wait(bar, par, abort_flag, a.err)) != 0;
+            return wait_for_warp(bar, par, abort_flag, a.err);
         };
         const uint64_t dq = desc_k(smem_addr(smem)), dk = desc_k(smem_addr(smem + G::RING_OFF));
         const uint64_t dv = desc_n(smem_addr(smem + G::RING_OFF));
@@ -656,10 +689,11 @@ __global__ void __launch_bounds__(THREADS, 1)
         // also after an abort: what was issued has completed before the tensor memory is freed
         if (elected) {
             commit(end_bar);
-            mbar_drain(end_bar, 0);
+            drain(end_bar, 0);
         }
         __syncwarp();
     } else {
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(SOFTMAX_REGS));
         // ------------------------------------------------------ softmax: a thread per row
         const int t = warp >> 2, row = (warp & 3) * 32 + lane, in_tile = row / a.group, head = row - in_tile * a.group;
         const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
@@ -677,7 +711,7 @@ __global__ void __launch_bounds__(THREADS, 1)
             float m = -INFINITY, l = 0.f;                   // m: of scaled scores, the one in use
             bool ok = true;
             for (int j = 0; j < nt; ++j) {
-                if (!(ok = __all_sync(0xffffffffu, mbar_wait(&s_full[t], s_parity, abort_flag, a.err)) != 0))
+                if (!(ok = wait_for_warp(&s_full[t], s_parity, abort_flag, a.err)))
                     break;
                 s_parity ^= 1;
                 fence_after();
@@ -737,7 +771,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                 if (lane == 0)
                     mbar_arrive(&p_full[t]);
             }
-            ok = ok && __all_sync(0xffffffffu, mbar_wait(&o_full[t], o_parity, abort_flag, a.err)) != 0;
+            ok = ok && wait_for_warp(&o_full[t], o_parity, abort_flag, a.err);
             if (!ok)
                 break;
             o_parity ^= 1;
@@ -753,7 +787,8 @@ __global__ void __launch_bounds__(THREADS, 1)
                 tmem_ld32(to + c, o + c);
             wait_ld();
             if (odd && valid)  // what the guards cleared, for the rows that see it
-                add_cleared<D>(a, item, tl.masked * BN, tok, o);
+                add_cleared<D>(a.v + (item.start + tl.masked * BN) * a.v_ld + (long long)item.kvh * D, a.v_ld,
+                               tok - tl.masked * BN + 1, o);
             if (valid) {
 #pragma unroll
                 for (int c = 0; c < D; c += 16) {
