@@ -114,16 +114,18 @@ __device__ __forceinline__ float max3(float a, float b, float c)
 // The largest of a row's 128 scores
 __device__ __forceinline__ float row_max(const uint32_t (&s)[BN])
 {
-    float m[4] = {__uint_as_float(s[0]), __uint_as_float(s[1]), __uint_as_float(s[2]), __uint_as_float(s[3])};
+    float m[8];
 #pragma unroll
-    for (int c = 4; c + 8 <= BN; c += 8)
+    for (int i = 0; i < 8; ++i)
+        m[i] = fmaxf(__uint_as_float(s[2 * i]), __uint_as_float(s[2 * i + 1]));
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
+    for (int c = 16; c < BN; c += 16)
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
             m[i] = max3(m[i], __uint_as_float(s[c + 2 * i]), __uint_as_float(s[c + 2 * i + 1]));
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-        m[i] = fmaxf(m[i], __uint_as_float(s[BN - 4 + i]));
-    return fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3]));
+    m[0] = max3(m[0], m[1], m[2]);
+    m[3] = max3(m[3], m[4], m[5]);
+    return max3(max3(m[0], m[3], m[6]), m[7], m[7]);
 }
 
 __device__ __forceinline__ void fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
@@ -262,7 +264,7 @@ struct Item {
 // rows that see most keys come first.  One warp walks it for its CTA.
 struct Walk {
     static constexpr int KEPT = 4;  // sequences of a lane whose items it keeps
-    int kept[KEPT];
+    int kept[KEPT], starts[KEPT], lens[KEPT];
     int level, here;                // items at this level and above
 
     __device__ __forceinline__ int items(const PromptArgs &a, int b) const
@@ -285,8 +287,12 @@ struct Walk {
     __device__ __forceinline__ void begin(const PromptArgs &a, int lane)
     {
 #pragma unroll
-        for (int i = 0; i < KEPT; ++i)
-            kept[i] = items(a, lane + 32 * i);
+        for (int i = 0; i < KEPT; ++i) {
+            const Span q = lane + 32 * i < a.n_seqs ? sequence(a, lane + 32 * i) : Span{0, 0};
+            starts[i] = q.start;
+            lens[i] = q.len;
+            kept[i] = (q.len + 2 * a.tile_tokens - 1) / (2 * a.tile_tokens);
+        }
         level = a.T / (2 * a.tile_tokens) + 1;
         here = 0;
     }
@@ -332,7 +338,15 @@ struct Walk {
             if (count > 0 && rank < seen + count) {
                 for (int j = rank - seen; j > 0; --j)
                     with &= with - 1;
-                const Span q = sequence(a, b0 + __ffs(with) - 1);
+                const int from = __ffs(with) - 1;
+                Span q = {0, 0};
+#pragma unroll
+                for (int j = 0; j < KEPT; ++j)
+                    q = k == j ? Span{starts[j], lens[j]} : q;
+                q.start = __shfl_sync(0xffffffffu, q.start, from);
+                q.len = __shfl_sync(0xffffffffu, q.len, from);
+                if (k >= KEPT)
+                    q = sequence(a, b0 + from);
                 return {q.start, q.len, level * 2 * a.tile_tokens, kvh};
             }
             seen += count;
@@ -467,6 +481,16 @@ __global__ void __launch_bounds__(THREADS, 1)
         uint32_t ph = 0, slot_parity = 0, land_parity = 0, armed = 0, armed_land = 0;
         bool ok = true;
         const int ctas = (int)gridDim.x, cta = (int)blockIdx.x;
+        auto load_q = [&](const Item &item, const Tiles &tl) {
+            if (lane == 0) {
+                const int rows = a.group * a.tile_tokens, both = tl.n1 > 0 ? 2 : 1;
+                mbar_arrive_expect_tx(q_full, both * rows * D * 2);
+                for (int t = 0; t < both; ++t)
+                    for (int h = 0; h < D / 64; ++h)
+                        tma_4d(smem + t * G::TILE_B + h * (BM * 128), &map_q, 0, item.kvh * a.group,
+                               item.start + item.tok0 + t * a.tile_tokens, h, q_full);
+            }
+        };
         for (int i = 0; ok; ++i) {
             const Item item = walk.at(a, i & 1 ? (i + 1) * ctas - 1 - cta : i * ctas + cta, lane);
             if (!(ok = wait_for_warp(&item_empty[i & 1], ((i >> 1) & 1) ^ 1, abort_flag, a.err)))
@@ -478,6 +502,8 @@ __global__ void __launch_bounds__(THREADS, 1)
             if (item.len == 0)
                 break;
             const Tiles tl = tiles_of(a, item);
+            if (i == 0)
+                load_q(item, tl);
             for (int it = 0; it < 2 * tl.n; ++it) {
                 const int j = it >> 1;
                 const bool is_v = it & 1;
@@ -501,17 +527,10 @@ __global__ void __launch_bounds__(THREADS, 1)
                     slot = 0;
                     ph ^= 1;
                 }
-                if (it == 1) {  // (the queries' place is free later than the first tiles')
+                if (it == 1 && i > 0) {  // (the queries' place is free later than the first tiles')
                     if (!(ok = wait_for_warp(q_empty, (i & 1) ^ 1, abort_flag, a.err)))
                         break;
-                    if (lane == 0) {
-                        const int rows = a.group * a.tile_tokens, both = tl.n1 > 0 ? 2 : 1;
-                        mbar_arrive_expect_tx(q_full, both * rows * D * 2);
-                        for (int t = 0; t < both; ++t)
-                            for (int h = 0; h < D / 64; ++h)
-                                tma_4d(smem + t * G::TILE_B + h * (BM * 128), &map_q, 0, item.kvh * a.group,
-                                       item.start + item.tok0 + t * a.tile_tokens, h, q_full);
-                    }
+                    load_q(item, tl);
                 }
             }
         }
