@@ -31,6 +31,8 @@ namespace {
 
 __device__ int g_error;
 
+constexpr int THREADS = 256;
+
 struct AppendArgs {
     const uint16_t *qkv;
     long long ld;
@@ -77,7 +79,7 @@ __device__ __forceinline__ float turn_odd(float x, float c, float y, float s)
 }
 
 template <int D, bool MX, int HPT>
-__global__ void __launch_bounds__(512) kv_append_kernel(const AppendArgs a)
+__global__ void __launch_bounds__(THREADS) kv_append_kernel(const AppendArgs a)
 {
     constexpr int C = D / 16;  // threads of a head
     overlap_trigger();
@@ -91,46 +93,42 @@ __global__ void __launch_bounds__(512) kv_append_kernel(const AppendArgs a)
     // the thread's places: 8 values from `one`, 8 from `two`
     const bool halves = turned && !a.pairs;
     const int one = halves ? 8 * c : 16 * c, two = halves ? a.rot / 2 + 8 * c : 16 * c + 8;
-    float cs[8], sn[8];
-    int slot = -1;
-    if (here) {
-        slot = __ldcg(a.slots + t);
-        if (slot != -1 && (slot < 0 || slot >= a.n_slots)) {
-            if (j == 0)
-                atomicCAS(a.err, 0, DEV_ERR_BOUNDS);
-            slot = -1;
-        }
-        if (turned) {
-            const int pos = __ldcg(a.positions + t);
-            if (pos >= 0 && pos < a.n_positions) {
-                const float4 *p = reinterpret_cast<const float4 *>(a.rope + (long long)pos * a.rot + 8 * c);
-                const float4 *q = reinterpret_cast<const float4 *>(a.rope + (long long)pos * a.rot + a.rot / 2 + 8 * c);
-                const float4 c0 = __ldcg(p), c1 = __ldcg(p + 1), s0 = __ldcg(q), s1 = __ldcg(q + 1);
-                cs[0] = c0.x, cs[1] = c0.y, cs[2] = c0.z, cs[3] = c0.w;
-                cs[4] = c1.x, cs[5] = c1.y, cs[6] = c1.z, cs[7] = c1.w;
-                sn[0] = s0.x, sn[1] = s0.y, sn[2] = s0.z, sn[3] = s0.w;
-                sn[4] = s1.x, sn[5] = s1.y, sn[6] = s1.z, sn[7] = s1.w;
-            } else {
-                if (j == 0 && slot != -1)  // (a row of padding may have any position)
-                    atomicCAS(a.err, 0, DEV_ERR_BOUNDS);
-#pragma unroll
-                for (int i = 0; i < 8; ++i)
-                    cs[i] = sn[i] = __int_as_float(0x7FC00000);
-            }
-        }
-    }
+    // all that the thread reads is asked for before anything is looked at; the cosines wait for the position alone
     uint4 u[HPT][2];
+    int slot = -1, pos = 0;
+    if (here) {
+        pos = turned ? __ldcg(a.positions + t) : 0;
+        slot = __ldcg(a.slots + t);
+    }
 #pragma unroll
     for (int i = 0; i < HPT; ++i) {
         const int h = hs + i * a.slots_of_head;
+        u[i][0] = u[i][1] = make_uint4(0, 0, 0, 0);
         if (here && h < a.units) {
             const uint16_t *p = a.qkv + t * a.ld + (long long)h * D;
             u[i][0] = __ldcg(reinterpret_cast<const uint4 *>(p + one));
             u[i][1] = __ldcg(reinterpret_cast<const uint4 *>(p + two));
-        } else {
-            u[i][0] = u[i][1] = make_uint4(0, 0, 0, 0);
         }
     }
+    float cs[8], sn[8];
+    const bool known = pos >= 0 && pos < a.n_positions;
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+        cs[i] = sn[i] = __int_as_float(0x7FC00000);
+    if (here && turned && known) {
+        const float4 *p = reinterpret_cast<const float4 *>(a.rope + (long long)pos * a.rot + 8 * c);
+        const float4 *q = reinterpret_cast<const float4 *>(a.rope + (long long)pos * a.rot + a.rot / 2 + 8 * c);
+        const float4 c0 = __ldcg(p), c1 = __ldcg(p + 1), s0 = __ldcg(q), s1 = __ldcg(q + 1);
+        cs[0] = c0.x, cs[1] = c0.y, cs[2] = c0.z, cs[3] = c0.w;
+        cs[4] = c1.x, cs[5] = c1.y, cs[6] = c1.z, cs[7] = c1.w;
+        sn[0] = s0.x, sn[1] = s0.y, sn[2] = s0.z, sn[3] = s0.w;
+        sn[4] = s1.x, sn[5] = s1.y, sn[6] = s1.z, sn[7] = s1.w;
+    }
+    const bool outside = slot != -1 && (slot < 0 || slot >= a.n_slots);
+    if (here && j == 0 && (outside || (slot != -1 && turned && !known)))  // (a row of padding may have any position)
+        atomicCAS(a.err, 0, DEV_ERR_BOUNDS);
+    if (outside)
+        slot = -1;
 #pragma unroll
     for (int i = 0; i < HPT; ++i) {
         const int h = hs + i * a.slots_of_head;
@@ -217,8 +215,8 @@ cudaError_t launch_append(AppendArgs &a, cudaStream_t st)
     const bool many = (long long)a.T * a.units * C >= 2048ll * gemm::sm_count();
     a.slots_of_head = many ? (a.units + MANY - 1) / MANY : a.units;
     a.per_token = a.slots_of_head * C;
-    a.tokens = a.per_token >= 512 ? 1 : 512 / a.per_token;
-    const int n = a.per_token * a.tokens, threads = n >= 512 ? 512 : (n + 31) & ~31;
+    a.tokens = a.per_token >= THREADS ? 1 : THREADS / a.per_token;
+    const int n = a.per_token * a.tokens, threads = n >= THREADS ? THREADS : (n + 31) & ~31;
     const dim3 grid((unsigned)((a.T + a.tokens - 1) / a.tokens), (unsigned)((n + threads - 1) / threads));
     return many ? launch_overlapped(kv_append_kernel<D, MX, MANY>, grid, threads, 0, 1, st, a)
                 : launch_overlapped(kv_append_kernel<D, MX, 1>, grid, threads, 0, 1, st, a);
