@@ -48,7 +48,7 @@ class KvCache:
         if any(not t.is_contiguous() or not t.is_cuda or t.device != k.device for t in tensors):
             raise B.MoeError(B.MOE_EINVAL, "a cache's tensors must be dense and on one CUDA device")
         self.k, self.v, self.k_scales, self.v_scales = k, v, k_scales, v_scales
-        self.device = k.device
+        self.device, self._ordinal = k.device, k.get_device()
         self.page_size, self.n_kv_heads, self.head_dim = page, n_kv, dim
         self.c = B.MoeKvCache(k.data_ptr(), v.data_ptr(), B._ptr(k_scales), B._ptr(v_scales),
                               B.MOE_ROWS_MXFP8 if mx else B.MOE_ROWS_BF16, n_pages, page, n_kv, dim)
@@ -101,7 +101,7 @@ class KvCache:
         return out
 
     def _here(self, t: torch.Tensor) -> None:
-        if t.device != self.device:
+        if t.get_device() != self._ordinal:
             raise B.MoeError(B.MOE_EINVAL, f"a tensor on {t.device} and a cache on {self.device}")
 
 
@@ -115,6 +115,52 @@ def prompt(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, offsets: torch.Ten
             out = torch.empty(q.shape, dtype=torch.bfloat16, device=q.device)
     B.moe_attention_prompt(q, k, v, offsets, q.shape[-1] ** -0.5 if scale is None else scale, out, stream)
     return out
+
+
+class Attention:
+    """A decoder layer's attention on the rows of its input projection (bfloat16 [T, (n_heads + 2 n_kv_heads) *
+    head_dim]: queries, keys and values side by side), over a cache of its own.
+
+    rope: a table as ``rope_table`` makes, or None (nothing is turned); scale: 1 / sqrt(head_dim) by default.  Both
+    calls turn the queries and keys of the rows in place, write keys and values to their slots (int32 [T]; -1: padding)
+    and return bfloat16 [T, n_heads * head_dim]; positions (int32 [T]) are needed with rope.
+    """
+
+    def __init__(self, n_heads: int, cache: KvCache, rope: Optional[torch.Tensor] = None, pairs: bool = False,
+                 scale: Optional[float] = None):
+        if n_heads < 1 or n_heads % cache.n_kv_heads:
+            raise B.MoeError(B.MOE_EINVAL, f"n_heads: {n_heads} is no multiple of the cache's {cache.n_kv_heads} heads")
+        if rope is not None and (rope.dim() != 2 or rope.dtype != torch.float32 or not rope.is_contiguous() or
+                                 rope.device != cache.device):
+            raise B.MoeError(B.MOE_EINVAL, "rope: a dense float32 [n_positions, rot_dim] tensor beside the cache is "
+                                           "needed")
+        self.n_heads, self.cache, self.rope, self.pairs = n_heads, cache, rope, pairs
+        self.scale = cache.head_dim ** -0.5 if scale is None else scale
+        self.row = (n_heads + 2 * cache.n_kv_heads) * cache.head_dim  # values of a row of the projection
+
+    def _append(self, qkv: torch.Tensor, slots, positions, k_too: bool):
+        n, kv, dim = self.n_heads, self.cache.n_kv_heads, self.cache.head_dim
+        if qkv.dim() != 2 or qkv.shape[1] != self.row or qkv.stride(1) != 1:
+            raise B.MoeError(B.MOE_EINVAL, f"qkv: shape {tuple(qkv.shape)} where [T, {self.row}] is needed")
+        rows = qkv.unflatten(1, (n + 2 * kv, dim))
+        q, k, v = rows[:, :n], rows[:, n:n + kv], rows[:, n + kv:]
+        self.cache.append(qkv, n, slots, positions, self.rope, self.pairs, q, k if k_too else None)
+        return q, k, v
+
+    def decode(self, qkv: torch.Tensor, slots: torch.Tensor, positions: Optional[torch.Tensor],
+               page_table: torch.Tensor, lens: torch.Tensor) -> torch.Tensor:
+        """One new token for each sequence; lens (int32 [T]) counts it.  A row without a sequence has slot -1 and
+        length 0, and gives zeros."""
+        q, _, _ = self._append(qkv, slots, positions, False)
+        return self.cache.decode(q, page_table, lens, self.scale).flatten(1)
+
+    def prompt(self, qkv: torch.Tensor, slots: torch.Tensor, positions: Optional[torch.Tensor],
+               offsets: torch.Tensor) -> torch.Tensor:
+        """Whole prompts, packed: sequence s has the rows offsets[s] .. offsets[s + 1] - 1 (int32 [n_seqs + 1]).  Rows
+        of no sequence give zeros."""
+        q, k, v = self._append(qkv, slots, positions, True)
+        out = torch.zeros((q.shape[0], self.n_heads, self.cache.head_dim), dtype=torch.bfloat16, device=qkv.device)
+        return prompt(q, k, v, offsets, self.scale, out).flatten(1)
 
 
 def sync(stream=None) -> None:

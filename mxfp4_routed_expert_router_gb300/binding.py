@@ -426,36 +426,49 @@ def moe_linear_free(handle: int) -> None:
     lib.moe_linear_free(handle)
 
 
-def _heads(t, name: str, rows: int, heads: int, dim: int):
+_ATTN = []  # torch.bfloat16, torch.int32, torch.float32, the current device's ordinal: filled by the first call
+
+
+def _attn():
+    if not _ATTN:
+        import torch
+        _ATTN.extend((torch.bfloat16, torch.int32, torch.float32,
+                      getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)))
+    return _ATTN
+
+
+def _heads(t, name: str, bf16, rows: int, heads: int, dim: int, dev: int):
     """Address and row stride of a bfloat16 tensor [rows, heads, dim] whose rows are dense; (None, 0) for None."""
-    import torch
     if t is None:
         return None, 0
-    if t.dtype is not torch.bfloat16 or t.shape != (rows, heads, dim):
+    if t.dtype is not bf16 or t.shape != (rows, heads, dim):
         raise MoeError(MOE_EINVAL, f"{name}: bfloat16 [{rows}, {heads}, {dim}] is needed, not {t.dtype} "
                                    f"{tuple(t.shape)}")
     ld, step, one = t.stride()
     if (one != 1 and dim > 1) or (step != dim and heads > 1):
         raise MoeError(MOE_EINVAL, f"{name}: the heads of a row must lie side by side")
+    if t.get_device() != dev:
+        _elsewhere(name, t, dev)
     return t.data_ptr(), (ld if rows > 1 else heads * dim)
 
 
-def _vector(t, name: str, n: int):
+def _vector(t, name: str, i32, n: int, dev: int):
     """Address of a dense int32 vector of n values."""
-    import torch
-    if t.dtype is not torch.int32 or t.shape != (n,) or not t.is_contiguous():
+    if t.dtype is not i32 or t.shape != (n,) or not t.is_contiguous():
         raise MoeError(MOE_EINVAL, f"{name}: a dense int32 vector of {n} values is needed, not {t.dtype} "
                                    f"{tuple(t.shape)}")
+    if t.get_device() != dev:
+        _elsewhere(name, t, dev)
     return t.data_ptr()
 
 
-def _on_device(*tensors) -> None:
-    """All tensors on torch's current GPU."""
-    import torch
-    dev = torch.cuda.current_device() if tensors[0].is_cuda else -1
-    for t in tensors:
-        if t is not None and t.get_device() != dev or dev < 0:
-            raise MoeError(MOE_EINVAL, "every tensor must lie on the current CUDA device")
+def _elsewhere(name: str, t, dev: int):
+    raise MoeError(MOE_EINVAL, f"{name}: a tensor on {t.device} where CUDA device {max(dev, 0)} is the current one")
+
+
+def _gpu_of(t) -> int:
+    """The current device's ordinal for a CUDA tensor, -2 (no tensor's) for one in host memory."""
+    return _ATTN[3]() if t.is_cuda else -2
 
 
 def moe_kv_append(cache: MoeKvCache, qkv, n_heads: int, slots, positions=None, rope=None,
@@ -463,24 +476,26 @@ def moe_kv_append(cache: MoeKvCache, qkv, n_heads: int, slots, positions=None, r
     """Rotary embedding and the write into a paged cache (see include/moe.h).  qkv: bfloat16 [T, (n_heads +
     2 n_kv_heads) * head_dim]; slots, positions: int32 [T]; rope: float32 [n_positions, rot_dim] or None; q_out:
     bfloat16 [T, n_heads, head_dim], k_out: [T, n_kv_heads, head_dim], or None."""
-    f32, _ = _DTYPES or _dtypes()
+    bf16, i32, f32, _ = _ATTN or _attn()
     D, kv = cache.head_dim, cache.n_kv_heads
-    if qkv.dim() != 2 or _row_type(qkv.dtype) != MOE_ROWS_BF16:
+    if qkv.dim() != 2 or qkv.dtype is not bf16:
         raise MoeError(MOE_EINVAL, "qkv: bfloat16 rows are needed")
-    T = qkv.shape[0]
+    T, dev = qkv.shape[0], _gpu_of(qkv)
     p, _, ld = _rows(qkv, "qkv", (T, (n_heads + 2 * kv) * D))
-    sp = _vector(slots, "slots", T)
+    if qkv.get_device() != dev:
+        _elsewhere("qkv", qkv, dev)
+    sp = _vector(slots, "slots", i32, T, dev)
     pp = rp = n_pos = rot = 0
     if rope is not None:
-        if rope.dim() != 2 or rope.dtype is not f32 or not rope.is_contiguous():
-            raise MoeError(MOE_EINVAL, "rope: a dense float32 [n_positions, rot_dim] tensor is needed")
+        if rope.dim() != 2 or rope.dtype is not f32 or not rope.is_contiguous() or rope.get_device() != dev:
+            raise MoeError(MOE_EINVAL, "rope: a dense float32 [n_positions, rot_dim] tensor on the current device is "
+                                       "needed")
         if positions is None:
             raise MoeError(MOE_EINVAL, "positions: rope needs them")
         n_pos, rot = rope.shape
-        rp, pp = rope.data_ptr(), _vector(positions, "positions", T)
-    qo, qld = _heads(q_out, "q_out", T, n_heads, D)
-    ko, kld = _heads(k_out, "k_out", T, kv, D)
-    _on_device(qkv, slots, rope, positions if rope is not None else None, q_out, k_out)
+        rp, pp = rope.data_ptr(), _vector(positions, "positions", i32, T, dev)
+    qo, qld = _heads(q_out, "q_out", bf16, T, n_heads, D, dev)
+    ko, kld = _heads(k_out, "k_out", bf16, T, kv, D, dev)
     status = lib.moe_kv_append(ctypes.byref(cache), p, ld, T, n_heads, sp, pp, rp, n_pos, rot, style, qo, qld, ko, kld,
                                _stream(stream))
     if status:
@@ -495,17 +510,17 @@ def moe_attention_decode(cache: MoeKvCache, q, page_table, lens, scale: float, o
                          stream=None) -> None:
     """Attention of one token per sequence over a paged cache (see include/moe.h).  q, out: bfloat16 [B, n_heads,
     head_dim]; page_table: dense int32 [B, max_pages]; lens: int32 [B]."""
-    _, i32 = _DTYPES or _dtypes()
+    bf16, i32, _, _ = _ATTN or _attn()
     if q.dim() != 3:
         raise MoeError(MOE_EINVAL, "q: a [B, n_heads, head_dim] tensor is needed")
     B, heads, D = q.shape
-    qp, qld = _heads(q, "q", B, heads, cache.head_dim)
-    op, old = _heads(out, "out", B, heads, cache.head_dim)
+    dev = _gpu_of(q)
+    qp, qld = _heads(q, "q", bf16, B, heads, cache.head_dim, dev)
+    op, old = _heads(out, "out", bf16, B, heads, cache.head_dim, dev)
     if page_table.dim() != 2 or page_table.shape[0] != B or page_table.dtype is not i32 or \
-            not page_table.is_contiguous():
-        raise MoeError(MOE_EINVAL, f"page_table: a dense int32 [{B}, max_pages] tensor is needed")
-    lp = _vector(lens, "lens", B)
-    _on_device(q, page_table, lens, out)
+            not page_table.is_contiguous() or page_table.get_device() != dev:
+        raise MoeError(MOE_EINVAL, f"page_table: a dense int32 [{B}, max_pages] tensor on the current device is needed")
+    lp = _vector(lens, "lens", i32, B, dev)
     status = lib.moe_attention_decode(ctypes.byref(cache), qp, qld, B, heads, page_table.data_ptr(),
                                       page_table.shape[1], lp, scale, op, old, _ptr(workspace), ws_bytes,
                                       _stream(stream))
@@ -516,19 +531,19 @@ def moe_attention_decode(cache: MoeKvCache, q, page_table, lens, scale: float, o
 def moe_attention_prompt(q, k, v, offsets, scale: float, out, stream=None) -> None:
     """Causal attention within packed prompts (see include/moe.h).  q, out: bfloat16 [T, n_heads, head_dim]; k, v:
     bfloat16 [T, n_kv_heads, head_dim]; offsets: int32 [n_seqs + 1]."""
+    bf16, i32, _, _ = _ATTN or _attn()
     if q.dim() != 3 or k.dim() != 3:
         raise MoeError(MOE_EINVAL, "q, k: [T, heads, head_dim] tensors are needed")
     T, heads, D = q.shape
-    kv = k.shape[1]
-    qp, qld = _heads(q, "q", T, heads, D)
-    kp, kld = _heads(k, "k", T, kv, D)
-    vp, vld = _heads(v, "v", T, kv, D)
-    op, old = _heads(out, "out", T, heads, D)
+    kv, dev = k.shape[1], _gpu_of(q)
+    qp, qld = _heads(q, "q", bf16, T, heads, D, dev)
+    kp, kld = _heads(k, "k", bf16, T, kv, D, dev)
+    vp, vld = _heads(v, "v", bf16, T, kv, D, dev)
+    op, old = _heads(out, "out", bf16, T, heads, D, dev)
     if offsets.dim() != 1 or offsets.shape[0] < 1:
         raise MoeError(MOE_EINVAL, "offsets: an int32 vector of n_seqs + 1 values is needed")
     n = offsets.shape[0] - 1
-    off = _vector(offsets, "offsets", n + 1)
-    _on_device(q, k, v, offsets, out)
+    off = _vector(offsets, "offsets", i32, n + 1, dev)
     status = lib.moe_attention_prompt(qp, qld, kp, kld, vp, vld, T, off, n, heads, kv, D, scale, op, old,
                                       _stream(stream))
     if status:
