@@ -41,6 +41,12 @@ constexpr int TEAM = 4;              // warps that share a tile, 16 tokens of ea
 constexpr int MAX_STAGES = 16;
 constexpr int MIN_SHARE = 2;         // tiles of a CTA at least
 
+// A unit that starts in a CTA (as its first stretch or its last: part 0 or 1) and ends in CTA `last`; of the CTAs
+// between it is the first stretch.  heads == 0: there is none.
+struct alignas(16) Split {
+    int b, head, heads_part, last;  // heads_part: heads * 2 + part
+};
+
 struct DecodeArgs {
     const uint16_t *q;
     long long q_ld;
@@ -56,6 +62,7 @@ struct DecodeArgs {
     uint16_t *out;
     long long out_ld;
     float *part_o, *part_ml;         // parts: [2 * CTAs][8 NT][D], [2 * CTAs][8 NT][2]
+    Split *splits;                   // [CTAs]: what starts in a CTA and goes on in the next
     int ctas;
     int *err;
 };
@@ -686,6 +693,8 @@ __global__ void __launch_bounds__(Geo<D, NT, MX>::THREADS, 1)
             reinterpret_cast<uint4 *>(a.out + b * a.out_ld)[i] = make_uint4(v, v, v, v);
     }
     __syncthreads();
+    if (tid == 0)
+        a.splits[blockIdx.x] = {0, 0, 0, 0};  // (until the last stretch shows one)
     if (start >= end || first.t1 <= first.t0)  // (a last CTA may have no more than a unit's START places)
         return;
     Stretch at = first;
@@ -905,6 +914,8 @@ __global__ void __launch_bounds__(Geo<D, NT, MX>::THREADS, 1)
             asm volatile("bar.sync 1, %0;" ::"n"(G::WARPS * 32) : "memory");
         }
         const bool whole = t0 == 0 && t1 == at.nt;
+        if (t0 == 0 && !whole && tid == 0)
+            a.splits[blockIdx.x] = {at.b, (int)head, heads * 2 + part, (int)((at.v + G::START + at.nt - 1) / share)};
         for (int i = tid; i < NT * D; i += G::WARPS * 32) {
             const int hd = i / (D / 8), d = i % (D / 8) * 8;
             if (hd >= heads)
@@ -944,62 +955,67 @@ __global__ void __launch_bounds__(Geo<D, NT, MX>::THREADS, 1)
     } while (advance<G>(a, at, end));
 }
 
-// Joins the parts of one sequence's query head, a thread per value.
-template <int D, int NT, class G>
-__global__ void __launch_bounds__(D) join_kernel(const DecodeArgs a)
+// Joins the parts of a query head of the unit that starts in CTA blockIdx.x and goes on in others; in the order of the
+// parts, four warps taking them in turn.
+template <int D, int NT>
+__global__ void __launch_bounds__(128) join_kernel(const DecodeArgs a)
 {
-    __shared__ long long red[2][D / 32];
-    const int b = blockIdx.x, h = blockIdx.y, d = threadIdx.x, lane = d & 31;
+    constexpr int V = D / 32, WARPS = 4;  // values of a lane
+    __shared__ float red[WARPS][D + 2];
+    const int c0 = blockIdx.x, hd = blockIdx.y, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     overlap_trigger();
     overlap_wait();
-    long long before = 0, total = 0;
-    for (int i = d; i < a.B; i += D) {
-        const int n = places_of<G>(a, i);
-        total += n;
-        before += i < b ? n : 0;
+    const int4 w = __ldcg(reinterpret_cast<const int4 *>(a.splits) + c0);
+    const Split s{w.x, w.y, w.z, w.w};
+    if (hd >= s.heads_part >> 1)
+        return;
+    float m = -INFINITY, l = 0.f, v[V];
+#pragma unroll
+    for (int i = 0; i < V; ++i)
+        v[i] = 0.f;
+#pragma unroll 4
+    for (int c = c0 + warp; c <= s.last; c += WARPS) {
+        const long long at = (2ll * c + (c == c0 ? s.heads_part & 1 : 0)) * 8 * NT + hd;
+        const float2 x = __ldcg(reinterpret_cast<const float2 *>(a.part_ml + 2 * at));
+        float o[V];
+        if constexpr (V == 4) {
+            const float4 u = __ldcg(reinterpret_cast<const float4 *>(a.part_o + at * D) + lane);
+            o[0] = u.x, o[1] = u.y, o[2] = u.z, o[3] = u.w;
+        } else {
+            const float2 u = __ldcg(reinterpret_cast<const float2 *>(a.part_o + at * D) + lane);
+            o[0] = u.x, o[1] = u.y;
+        }
+        const float next = fmaxf(m, x.x), base = finite_base(next), f = ex2(m - base), g = ex2(x.x - base);
+        m = next;
+        l = fmaf(l, f, x.y * g);
+#pragma unroll
+        for (int i = 0; i < V; ++i)
+            v[i] = fmaf(v[i], f, o[i] * g);
     }
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-        before += __shfl_xor_sync(0xffffffffu, before, o);
-        total += __shfl_xor_sync(0xffffffffu, total, o);
-    }
+    for (int i = 0; i < V; ++i)
+        red[warp][lane * V + i] = v[i];
     if (lane == 0) {
-        red[0][d >> 5] = before;
-        red[1][d >> 5] = total;
+        red[warp][D] = m;
+        red[warp][D + 1] = l;
     }
     __syncthreads();
-    before = total = 0;
-#pragma unroll
-    for (int w = 0; w < D / 32; ++w) {
-        before += red[0][w];
-        total += red[1][w];
-    }
-    const int nt = tiles_of<G>(a, __ldcg(a.lens + b));
-    if (nt == 0)
+    const int d = threadIdx.x;
+    if (d >= D)
         return;
-    const int kvh = h / a.group, hh = h - kvh * a.group, chunk = hh / (8 * NT);
-    const long long share = share_of<G>(a, total * a.units);
-    const long long s = before * a.units + (long long)(kvh * a.chunks + chunk) * (nt + G::START);  // the unit's places
-    const int c0 = (int)((s + G::START) / share), c1 = (int)((s + G::START + nt - 1) / share);
-    if (c0 == c1)
-        return;  // written by its CTA
-    const int hd = hh - chunk * 8 * NT;
-    // CTA c's stretch of this unit is its first one if the CTA's places start inside the unit
-    auto slot = [&](int c) { return (2ll * c + (c * share >= s ? 0 : 1)) * 8 * NT + hd; };
-    float m = -INFINITY;
-    for (int c = c0; c <= c1; ++c)
-        m = fmaxf(m, __ldcg(a.part_ml + 2 * slot(c)));
-    const float base = finite_base(m);
-    float l = 0.f, v = 0.f;
-#pragma unroll 4
-    for (int c = c0; c <= c1; ++c) {
-        const long long at = slot(c);
-        const float2 x = __ldcg(reinterpret_cast<const float2 *>(a.part_ml + 2 * at));
-        const float f = ex2(x.x - base);
-        l = fmaf(x.y, f, l);
-        v = fmaf(__ldcg(a.part_o + at * D + d), f, v);
+    m = -INFINITY;
+#pragma unroll
+    for (int i = 0; i < WARPS; ++i)
+        m = fmaxf(m, red[i][D]);
+    float sum = 0.f;
+    l = 0.f;
+#pragma unroll
+    for (int i = 0; i < WARPS; ++i) {
+        const float f = ex2(red[i][D] - finite_base(m));
+        l = fmaf(red[i][D + 1], f, l);
+        sum = fmaf(red[i][d], f, sum);
     }
-    a.out[b * a.out_ld + (long long)h * D + d] = __bfloat16_as_ushort(__float2bfloat16_rn(v / l));
+    a.out[s.b * a.out_ld + (long long)(s.head + hd) * D + d] = __bfloat16_as_ushort(__float2bfloat16_rn(sum / l));
 }
 
 // ---------------------------------------------------------------- host side
@@ -1047,10 +1063,13 @@ cudaError_t launch_decode(const DecodeArgs &a, const MoeKvCache *cache, cudaStre
         return e;
     if (a.cap <= G::TILE)  // one tile a sequence and head: nothing is ever shared
         return cudaSuccess;
-    return launch_overlapped(join_kernel<D, NT, G>, dim3((unsigned)a.B, (unsigned)a.heads), D, 0, 1, st, a);
+    return launch_overlapped(join_kernel<D, NT>, dim3((unsigned)a.ctas, 8 * NT), 128, 0, 1, st, a);
 }
 
-size_t part_bytes(int heads_of_part, int D) { return (size_t)2 * sm_count() * heads_of_part * (D + 2) * 4; }
+size_t part_bytes(int heads_of_part, int D)
+{
+    return (size_t)sm_count() * (2 * heads_of_part * (D + 2) * 4 + sizeof(Split));
+}
 
 bool heads_fit(int n_heads, int n_kv_heads)
 {
@@ -1134,6 +1153,7 @@ extern "C" MoeStatus moe_attention_decode(const MoeKvCache *cache, const void *q
         a.ctas = gemm::sm_count();
         a.part_o = static_cast<float *>(workspace);
         a.part_ml = a.part_o + (size_t)2 * a.ctas * 8 * nt * D;
+        a.splits = reinterpret_cast<Split *>(a.part_ml + (size_t)2 * a.ctas * 8 * nt * 2);
         cudaStream_t st = (cudaStream_t)cuda_stream;
         const bool mx = cache->type == MOE_ROWS_MXFP8;
         if (D == 128)
