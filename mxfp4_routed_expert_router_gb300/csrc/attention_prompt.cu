@@ -8,9 +8,11 @@
 // one key head, so that short sequences fill tiles too and a key tile is loaded once for all heads that read it.  It
 // goes over the keys of its sequence in tiles of 128 up to its last token.  Warps: 0-3 and 4-7 the softmax of either
 // tile (a thread per row), 8 issues the MMAs, 9 loads by TMA, 10 and 11 look after values that no row may see (below).
-// Tensor memory: S of both tiles (128 columns each; P overwrites its tile's S as BF16) and O of both.  MMAs go in the
-// order S0 S1 | PV0 S0' | PV1 S1' | ..., so that one tile's softmax runs under the other tile's products, and a tile's
-// next S, which comes after its PV in the same queue, says that this PV is done: O may then be touched without a wait.
+// Tensor memory: S of both tiles (128 columns each; P overwrites its tile's S as BF16, but for heads of 64) and O of
+// both.  MMAs go in the order S0 S1 | PV0 S0' | PV1 S1' | ..., so that one tile's softmax runs under the other tile's
+// products, and a tile's next S, which comes after its PV in the same queue, says that this PV is done: O may then be
+// touched without a wait.  Heads of 64, whose products take half as long as the softmax, leave room for P of its own:
+// S0' S1' | PV0 PV1, with S' under the softmax of S.
 // The maximum in use is kept until a row exceeds it by 2^8 (P is then up to 2^8, in BF16's and FP32's range alike):
 // rescaling O in tensor memory, which would be needed in every tile, becomes rare.
 //
@@ -60,10 +62,16 @@ struct PromptArgs {
 
 template <int D> struct PGeo {
     static constexpr int TILE_B = 128 * D * 2;              // 128 rows
+    // Tensor memory: S, P and O of the two tiles.  With heads of 64 there is room for P beside S, so that a tile's next
+    // S need not wait for the product that reads its P.
+    static constexpr bool APART = D == 64;
+    static constexpr int P_COL = APART ? 2 * BN : 0, P_STEP = APART ? BN / 2 : BN;
+    static constexpr int O_COL = APART ? 3 * BN : 2 * BN;
+    static_assert(O_COL + 2 * D <= TMEM_COLS, "tensor memory");
     static constexpr int SLOTS = D == 128 ? 5 : 8;          // key and value tiles
     static constexpr int RING_OFF = 2 * TILE_B;
     static constexpr int BAR_OFF = RING_OFF + SLOTS * TILE_B;
-    static constexpr int N_BARS = 4 * SLOTS + 6 + 2 + 4 + 1;
+    static constexpr int N_BARS = 4 * SLOTS + 8 + 2 + 4 + 1;
     static constexpr int SMEM = BAR_OFF + N_BARS * 8 + 1024;  // + alignment slack
     static_assert(SMEM <= 226 * 1024, "shared memory");
 };
@@ -417,7 +425,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     uint8_t *smem = smem_dyn + ((1024u - (smem_addr(smem_dyn) & 1023u)) & 1023u);
     uint64_t *full = reinterpret_cast<uint64_t *>(smem + G::BAR_OFF), *empty = full + G::SLOTS;
     uint64_t *v_land = empty + G::SLOTS, *v_clear = v_land + G::SLOTS, *s_full = v_clear + G::SLOTS, *p_full = s_full + 2;
-    uint64_t *o_full = p_full + 2, *q_full = o_full + 2, *q_empty = q_full + 1, *item_full = q_empty + 1;
+    uint64_t *s_free = p_full + 2, *o_full = s_free + 2, *q_full = o_full + 2, *q_empty = q_full + 1, *item_full = q_empty + 1;
     uint64_t *item_empty = item_full + 2, *end_bar = item_empty + 2;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
 
@@ -431,6 +439,7 @@ __global__ void __launch_bounds__(THREADS, 1)
         for (int t = 0; t < 2; ++t) {
             mbar_init(&s_full[t], 1);
             mbar_init(&p_full[t], 4);
+            mbar_init(&s_free[t], 4);
             mbar_init(&o_full[t], 1);
             mbar_init(&item_full[t], 1);
             mbar_init(&item_empty[t], THREADS / 32 - 1);
@@ -622,7 +631,7 @@ __global__ void __launch_bounds__(THREADS, 1)
         const uint64_t dq = desc_k(smem_addr(smem)), dk = desc_k(smem_addr(smem + G::RING_OFF));
         const uint64_t dv = desc_n(smem_addr(smem + G::RING_OFF));
         constexpr uint64_t TILE16 = G::TILE_B / 16, HALF16 = BM * 128 / 16;
-        uint32_t slot_parity = 0, clear_parity = 0, p_parity = 0;
+        uint32_t slot_parity = 0, clear_parity = 0, p_parity = 0, s_parity = 3;
         int slot = 0;
         auto wait_slot = [&](int at) {
             if (!wait(&full[at], slot_parity >> at & 1))
@@ -641,6 +650,16 @@ __global__ void __launch_bounds__(THREADS, 1)
             }
             __syncwarp();
         };
+        auto next_scores = [&](int t, int at) {  // with P apart: once the tile's rows have their last S in registers
+            if (G::APART) {
+                if (!wait(&s_free[t], s_parity >> t & 1))
+                    return false;
+                s_parity ^= 1u << t;
+                fence_after();
+            }
+            scores(t, at);
+            return true;
+        };
         Item item;
         for (int i = 0; next_item(i, item); ++i) {
             const Tiles tl = tiles_of(a, item);
@@ -648,10 +667,9 @@ __global__ void __launch_bounds__(THREADS, 1)
             if (!ok)
                 break;
             fence_after();
-            // (P of the item before lies in these columns: its products come before these in the queue)
-            scores(0, slot);
-            if (tl.n1 > 0)
-                scores(1, slot);
+            // (P of the item before, where it lies in these columns, has its products before these in the queue)
+            if (!(ok = next_scores(0, slot) && (tl.n1 == 0 || next_scores(1, slot))))
+                break;
             if (elected) {
                 commit(&empty[slot]);
                 if (tl.n == 1)
@@ -667,8 +685,21 @@ __global__ void __launch_bounds__(THREADS, 1)
                 } else if (!(ok = wait_slot(vs))) {
                     break;
                 }
-                if (j + 1 < tl.n && !(ok = wait_slot(ks)))
-                    break;
+                if (j + 1 < tl.n) {
+                    if (!(ok = wait_slot(ks)))
+                        break;
+                    if (G::APART) {
+                        fence_after();
+                        if (!(ok = (j + 1 >= tl.n0 || next_scores(0, ks)) && (j + 1 >= tl.n1 || next_scores(1, ks))))
+                            break;
+                        if (elected) {
+                            commit(&empty[ks]);
+                            if (j + 2 == tl.n)
+                                commit(q_empty);
+                        }
+                        __syncwarp();
+                    }
+                }
 #pragma unroll
                 for (int t = 0; t < 2; ++t) {
                     const int nt = t ? tl.n1 : tl.n0;
@@ -681,22 +712,22 @@ __global__ void __launch_bounds__(THREADS, 1)
                     if (elected) {
 #pragma unroll
                         for (int k = 0; k < BN / 16; ++k)
-                            mma_ts(tmem + 2 * BN + t * D, tmem + t * BN + 8 * k, dv + vs * TILE16 + k * (16 * 128 / 16),
+                            mma_ts(tmem + G::O_COL + t * D, tmem + G::P_COL + t * G::P_STEP + 8 * k, dv + vs * TILE16 + k * (16 * 128 / 16),
                                    instr_desc(D, true), j > 0 || k > 0);
-                        if (j + 1 == nt)
+                        if (G::APART || j + 1 == nt)
                             commit(&o_full[t]);
                     }
                     __syncwarp();
-                    if (j + 1 < nt)
+                    if (!G::APART && j + 1 < nt)
                         scores(t, ks);
                 }
                 if (!ok)
                     break;
                 if (elected) {
                     commit(&empty[vs]);
-                    if (j + 1 < tl.n)
+                    if (!G::APART && j + 1 < tl.n)
                         commit(&empty[ks]);
-                    if (j + 2 == tl.n)
+                    if (!G::APART && j + 2 == tl.n)
                         commit(q_empty);
                 }
                 __syncwarp();
@@ -716,7 +747,8 @@ __global__ void __launch_bounds__(THREADS, 1)
         // ------------------------------------------------------ softmax: a thread per row
         const int t = warp >> 2, row = (warp & 3) * 32 + lane, in_tile = row / a.group, head = row - in_tile * a.group;
         const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
-        const uint32_t ts = tmem + lanes + t * BN, to = tmem + lanes + 2 * BN + t * D;
+        const uint32_t ts = tmem + lanes + t * BN, to = tmem + lanes + G::O_COL + t * D;
+        const uint32_t tp = tmem + lanes + G::P_COL + t * G::P_STEP;
         uint32_t s_parity = 0, o_parity = 0;
         Item item;
         for (int i = 0; next_item(i, item); ++i) {
@@ -739,6 +771,12 @@ __global__ void __launch_bounds__(THREADS, 1)
                 for (int c = 0; c < BN; c += 32)
                     tmem_ld32(ts + c, s + c);
                 wait_ld();
+                if (G::APART) {
+                    fence_before();
+                    __syncwarp();
+                    if (lane == 0)
+                        mbar_arrive(&s_free[t]);
+                }
                 if (j >= tl.masked) {
                     const int vis = sees - j * BN;
 #pragma unroll
@@ -746,6 +784,13 @@ __global__ void __launch_bounds__(THREADS, 1)
                         s[c] = c < vis ? s[c] : 0xFF800000u;
                 }
                 const float mx = a.scale * row_max(s);
+                if (G::APART && j > 0) {  // the product before is done: O may be touched and P overwritten (with S and P
+                                          // in one place that a new S is there says so)
+                    if (!(ok = wait_for_warp(&o_full[t], o_parity, abort_flag, a.err)))
+                        break;
+                    o_parity ^= 1;
+                    fence_after();
+                }
                 const bool grown = mx > m + GROWTH && valid;
                 if (j == 0) {
                     m = mx;
@@ -780,7 +825,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                         // operands share a type
                         p[k] = bf16_pair(p0, p1);
                     }
-                    tmem_st32(ts + c / 2, p);
+                    tmem_st32(tp + c / 2, p);
                 }
                 const float2 sums = unpack2(add2(add2(sum[0], sum[1]), add2(sum[2], sum[3])));
                 l += sums.x + sums.y;
