@@ -12,7 +12,7 @@
 // both.  MMAs go in the order S0 S1 | PV0 S0' | PV1 S1' | ..., so that one tile's softmax runs under the other tile's
 // products, and a tile's next S, which comes after its PV in the same queue, says that this PV is done: O may then be
 // touched without a wait.  Heads of 64, whose products take half as long as the softmax, leave room for P of its own:
-// S0' S1' | PV0 PV1, with S' under the softmax of S.
+// S0' PV0 | S1' PV1, with S' under the softmax of S.
 // The maximum in use is kept until a row exceeds it by 2^8 (P is then up to 2^8, in BF16's and FP32's range alike):
 // rescaling O in tensor memory, which would be needed in every tile, becomes rare.
 //
@@ -685,25 +685,15 @@ __global__ void __launch_bounds__(THREADS, 1)
                 } else if (!(ok = wait_slot(vs))) {
                     break;
                 }
-                if (j + 1 < tl.n) {
-                    if (!(ok = wait_slot(ks)))
-                        break;
-                    if (G::APART) {
-                        fence_after();
-                        if (!(ok = (j + 1 >= tl.n0 || next_scores(0, ks)) && (j + 1 >= tl.n1 || next_scores(1, ks))))
-                            break;
-                        if (elected) {
-                            commit(&empty[ks]);
-                            if (j + 2 == tl.n)
-                                commit(q_empty);
-                        }
-                        __syncwarp();
-                    }
-                }
+                if (j + 1 < tl.n && !(ok = wait_slot(ks)))
+                    break;
 #pragma unroll
                 for (int t = 0; t < 2; ++t) {
                     const int nt = t ? tl.n1 : tl.n0;
                     if (j >= nt || !ok)
+                        continue;
+                    // (the first tile's P comes before the second's next S: the two tiles' softmaxes so run in turns)
+                    if (G::APART && j + 1 < nt && !(ok = next_scores(t, ks)))
                         continue;
                     if (!(ok = wait(&p_full[t], p_parity >> t & 1)))
                         continue;
@@ -725,9 +715,9 @@ __global__ void __launch_bounds__(THREADS, 1)
                     break;
                 if (elected) {
                     commit(&empty[vs]);
-                    if (!G::APART && j + 1 < tl.n)
+                    if (j + 1 < tl.n)
                         commit(&empty[ks]);
-                    if (!G::APART && j + 2 == tl.n)
+                    if (j + 2 == tl.n)
                         commit(q_empty);
                 }
                 __syncwarp();
