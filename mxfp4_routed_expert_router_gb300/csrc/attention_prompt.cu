@@ -364,14 +364,14 @@ struct Walk {
 };
 
 // 32 bytes of a row
-__device__ __forceinline__ void st256(uint16_t *p, const uint32_t (&w)[8])
+__device__ __forceinline__ void st256(uint16_t *p, const uint32_t *w)
 {
     asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(p), "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3]),
                  "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
                  : "memory");
 }
 
-__device__ __forceinline__ void st128x2(uint16_t *p, const uint32_t (&w)[8])
+__device__ __forceinline__ void st128x2(uint16_t *p, const uint32_t *w)
 {
     reinterpret_cast<uint4 *>(p)[0] = make_uint4(w[0], w[1], w[2], w[3]);
     reinterpret_cast<uint4 *>(p)[1] = make_uint4(w[4], w[5], w[6], w[7]);
@@ -379,12 +379,12 @@ __device__ __forceinline__ void st128x2(uint16_t *p, const uint32_t (&w)[8])
 
 // Adds to a row's sums what is not finite among the n values of a place in v and on, per value: what the sum over all
 // of them would be (a probability is above 0).
-template <int D> __device__ __forceinline__ void add_cleared(const uint16_t *v, long long ld, int n, uint32_t (&o)[D])
+template <int W> __device__ __forceinline__ void add_cleared(const uint16_t *v, long long ld, int n, uint32_t (&o)[W])
 {
 #pragma unroll 1
     for (int r = 0; r < n; ++r) {
 #pragma unroll
-        for (int c = 0; c < D; c += 2) {
+        for (int c = 0; c < W; c += 2) {
             const uint32_t w = __ldcg(reinterpret_cast<const uint32_t *>(v + r * ld + c));
             const float x = __uint_as_float(w << 16), y = __uint_as_float(w & 0xFFFF0000u);
             o[c] = isfinite(x) ? o[c] : __float_as_uint(__uint_as_float(o[c]) + x);
@@ -835,25 +835,26 @@ __global__ void __launch_bounds__(THREADS, 1)
             const long long at = item.start + tok;
             const bool wide = a.wide_out;
             uint16_t *out = a.out + at * a.out_ld + (long long)(item.kvh * a.group + head) * D;
-            uint32_t o[D];
+            // (a loop: code that runs once an item is not in the instruction cache, and unrolled it takes longer to come
+            // than to run)
+#pragma unroll 1
+            for (int c = 0; c < D; c += 32) {
+                uint32_t o[32];
+                tmem_ld32(to + c, o);
+                wait_ld();
+                if (odd && valid)  // what the guards cleared, for the rows that see it
+                    add_cleared<32>(a.v + (item.start + tl.masked * BN) * a.v_ld + (long long)item.kvh * D + c, a.v_ld,
+                                    tok - tl.masked * BN + 1, o);
+                uint32_t w[16];
 #pragma unroll
-            for (int c = 0; c < D; c += 32)
-                tmem_ld32(to + c, o + c);
-            wait_ld();
-            if (odd && valid)  // what the guards cleared, for the rows that see it
-                add_cleared<D>(a.v + (item.start + tl.masked * BN) * a.v_ld + (long long)item.kvh * D, a.v_ld,
-                               tok - tl.masked * BN + 1, o);
-            if (valid) {
-#pragma unroll
-                for (int c = 0; c < D; c += 16) {
-                    uint32_t w[8];
-#pragma unroll
-                    for (int k = 0; k < 8; ++k)
-                        w[k] = bf16_pair(__uint_as_float(o[c + 2 * k]) * inv, __uint_as_float(o[c + 2 * k + 1]) * inv);
-                    if (wide)
-                        st256(out + c, w);
-                    else
-                        st128x2(out + c, w);
+                for (int k = 0; k < 16; ++k)
+                    w[k] = bf16_pair(__uint_as_float(o[2 * k]) * inv, __uint_as_float(o[2 * k + 1]) * inv);
+                if (valid && wide) {
+                    st256(out + c, w);
+                    st256(out + c + 16, w + 8);
+                } else if (valid) {
+                    st128x2(out + c, w);
+                    st128x2(out + c + 16, w + 8);
                 }
             }
             fence_before();  // (the next item's first product into O waits for its P, which comes after this)
