@@ -660,15 +660,24 @@ __global__ void __launch_bounds__(THREADS, 1)
             scores(t, at);
             return true;
         };
-        Item item;
-        for (int i = 0; next_item(i, item); ++i) {
-            const Tiles tl = tiles_of(a, item);
-            bool ok = wait(q_full, i & 1) && wait_slot(slot);
-            if (!ok)
-                break;
+        // The first tile's first S of an item, as soon as the queries and keys are there.  It comes before the last P of
+        // the second tile of the item before: the two tiles' softmaxes keep to their turns from item to item.  (The
+        // queries' place is free once the second tile's last S has been issued, a round earlier.)
+        auto begin = [&](int i, int at) {
+            if (!wait(q_full, i & 1) || !wait_slot(at))
+                return false;
             fence_after();
+            return next_scores(0, at);
+        };
+        Item item;
+        bool ok = true, more = next_item(0, item);
+        if (more)
+            more = begin(0, 0);
+        for (int i = 0; more; ++i) {
+            const Tiles tl = tiles_of(a, item);
+            more = false;
             // (P of the item before, where it lies in these columns, has its products before these in the queue)
-            if (!(ok = next_scores(0, slot) && (tl.n1 == 0 || next_scores(1, slot))))
+            if (tl.n1 > 0 && !next_scores(1, slot))
                 break;
             if (elected) {
                 commit(&empty[slot]);
@@ -690,6 +699,8 @@ __global__ void __launch_bounds__(THREADS, 1)
 #pragma unroll
                 for (int t = 0; t < 2; ++t) {
                     const int nt = t ? tl.n1 : tl.n0;
+                    if (t == 1 && ok && j + 1 == tl.n && next_item(i + 1, item))
+                        more = ok = begin(i + 1, ks);
                     if (j >= nt || !ok)
                         continue;
                     // (the first tile's P comes before the second's next S: the two tiles' softmaxes so run in turns)
@@ -723,8 +734,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                 __syncwarp();
                 slot = ks;  // (after the last tile: the next item's first)
             }
-            if (!ok)
-                break;
+            more = more && ok;
         }
         // also after an abort: what was issued has completed before the tensor memory is freed
         if (elected) {
