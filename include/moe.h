@@ -588,12 +588,15 @@ MoeStatus moe_kv_append(const MoeKvCache *cache, const void *qkv, long long qkv_
  *  out         BF16 rows of n_heads heads
  *  workspace   >= moe_attention_decode_workspace_bytes(...) bytes, 256-byte
  *              aligned; contents on entry do not matter
+ *              (calls that may run at a time need workspaces of their own)
  * Rows of the cache at and past lens[b], and pages of other sequences, may hold
  * anything.  A sequence with a negative length, one above max_pages * page_size,
  * or a page outside the cache gives NaN, and this is recorded
  * (moe_attention_status).  Scores, softmax and sums are FP32; probabilities
  * round to BF16 (with MXFP8 to FP16) for the product with v, MXFP8 queries to
- * FP16 with a power of two per head.  Results do not change from call to call.
+ * FP16 with a power of two per head.  (MXFP8 blocks of v whose powers of two lie
+ * more than 2^100 apart within a sequence may lose the smaller ones.)  Results do
+ * not change from call to call.
  * Rows start on 16-byte boundaries.  B == 0 enqueues nothing.
  * Errors: MOE_EINVAL (a bad cache, B outside [0, 65536], n_heads no multiple of
  * n_kv_heads or above 1024, max_pages < 1 or max_pages * page_size >= 2^31, scale
@@ -613,6 +616,7 @@ size_t moe_attention_decode_workspace_bytes(int B, int n_heads, int n_kv_heads, 
  *  q, k, v   BF16 rows of n_heads, n_kv_heads and n_kv_heads heads (they may lie
  *            side by side in wider rows)
  *  offsets   [n_seqs + 1] ascending, within 0 .. T; offsets beyond are cut to T
+ *            (where they do not ascend, rows may be left out)
  *  out       BF16 rows of n_heads heads; rows that no sequence holds stay as they
  *            were
  * A sequence may be empty.  A value that is not finite reaches only rows that

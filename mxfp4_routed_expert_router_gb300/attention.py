@@ -49,6 +49,7 @@ class KvCache:
             raise B.MoeError(B.MOE_EINVAL, "a cache's tensors must be dense and on one CUDA device")
         self.k, self.v, self.k_scales, self.v_scales = k, v, k_scales, v_scales
         self.device, self._ordinal = k.device, k.get_device()
+        self._workspace = {}  # n_heads -> bytes that ``decode`` needs
         self.page_size, self.n_kv_heads, self.head_dim = page, n_kv, dim
         self.c = B.MoeKvCache(k.data_ptr(), v.data_ptr(), B._ptr(k_scales), B._ptr(v_scales),
                               B.MOE_ROWS_MXFP8 if mx else B.MOE_ROWS_BF16, n_pages, page, n_kv, dim)
@@ -88,7 +89,10 @@ class KvCache:
         self._here(q)
         if q.dim() != 3:
             raise B.MoeError(B.MOE_EINVAL, f"q: shape {tuple(q.shape)} where [B, n_heads, head_dim] is needed")
-        n = B.moe_attention_decode_workspace_bytes(q.shape[0], q.shape[1], self.n_kv_heads, self.head_dim)
+        n = self._workspace.get(q.shape[1])
+        if n is None:  # (the same for every number of sequences)
+            n = self._workspace[q.shape[1]] = B.moe_attention_decode_workspace_bytes(1, q.shape[1], self.n_kv_heads,
+                                                                                     self.head_dim)
         if stream is None:
             ws = stream_workspace(n, self.device) if n else None
             out = torch.empty_like(q, memory_format=torch.contiguous_format) if out is None else out

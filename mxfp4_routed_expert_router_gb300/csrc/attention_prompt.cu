@@ -49,7 +49,7 @@ constexpr float GROWTH = 8.f;        // log2 by which a row's maximum may exceed
 
 struct PromptArgs {
     const int32_t *offsets;
-    int n_seqs, T;
+    int n_seqs, T, max_items;
     int heads, kv, group, tile_tokens;  // tokens of a tile
     const uint16_t *v;
     long long v_ld;
@@ -281,15 +281,17 @@ struct Walk {
         return b < a.n_seqs ? (sequence(a, b).len + per - 1) / per : 0;
     }
 
+    // (Cut where no call with ascending offsets comes: T and n_seqs allow less than MOST items of a key head.)
     __device__ __forceinline__ int above(const PromptArgs &a, int at_level, int lane) const
     {
+        constexpr int MOST = 1 << 25;
         int s = 0;
 #pragma unroll
         for (int i = 0; i < KEPT; ++i)
             s += max(0, kept[i] - at_level);
         for (int b = lane + 32 * KEPT; b < a.n_seqs; b += 32)
-            s += max(0, items(a, b) - at_level);
-        return __reduce_add_sync(0xffffffffu, s) * a.kv;
+            s = min(MOST, s + max(0, items(a, b) - at_level));
+        return (int)min(0x7FFFFFFFll, (long long)__reduce_add_sync(0xffffffffu, min(MOST, s)) * a.kv);
     }
 
     __device__ __forceinline__ void begin(const PromptArgs &a, int lane)
@@ -305,10 +307,13 @@ struct Walk {
         here = 0;
     }
 
-    // Item i of the list; i grows from call to call.
+    // Item i of the list; i grows from call to call.  (Offsets that do not ascend may name more items than the rows have
+    // room for: those are left out.)
     __device__ __forceinline__ Item at(const PromptArgs &a, int i, int lane)
     {
         int over = 0;  // items above the level that i is in
+        if (i >= a.max_items)
+            return {0, 0, 0, 0};
         if (i >= here) {
             int lo = 0, hi = level;  // above(lo) > i >= above(hi)
             int n = above(a, 0, lane);
@@ -899,7 +904,7 @@ cudaError_t rows_map(CUtensorMap *m, const void *base, long long ld, int T, int 
 }
 
 template <int D>
-cudaError_t launch_prompt(const PromptArgs &a, const void *q, long long q_ld, const void *k, long long k_ld,
+cudaError_t launch_prompt(PromptArgs &a, const void *q, long long q_ld, const void *k, long long k_ld,
                           cudaStream_t st)
 {
     auto kern = prompt_kernel<D>;
@@ -917,6 +922,7 @@ cudaError_t launch_prompt(const PromptArgs &a, const void *q, long long q_ld, co
     // a CTA per SM, or per item where there are fewer (at most: every sequence rounds up to whole items)
     const long long items = ((long long)a.T / (2 * a.tile_tokens) + a.n_seqs) * a.kv;
     const long long grid = items < sm_count() ? items : sm_count();
+    a.max_items = (int)items;
     return launch_overlapped(kern, (unsigned)grid, THREADS, PGeo<D>::SMEM, 1, st, a, mq, mk, mv);
 }
 

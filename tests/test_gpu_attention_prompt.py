@@ -152,7 +152,7 @@ def test_offsets_that_do_not_fit_stay_in_bounds():
     want = A.prompt(q, k, v, torch.tensor([0, 200, 240], dtype=torch.int32, device="cuda"))
     got = A.prompt(q, k, v, torch.tensor([-5, 200, 2 ** 31 - 1], dtype=torch.int32, device="cuda"))
     assert torch.equal(got, want)
-    for bad in ([200, 100, 50], [0, 2 ** 31 - 1, -2 ** 31, 100], [-1, -1], [240, 240], [500, 600]):
+    for bad in ([0, 240] * 150, [200, 100, 50], [0, 2 ** 31 - 1, -2 ** 31, 100], [-1, -1], [240, 240], [500, 600]):
         out = torch.full_like(q, 3.0, memory_format=torch.contiguous_format)
         A.prompt(q, k, v, torch.tensor(bad, dtype=torch.int32, device="cuda"), out=out)
         torch.cuda.synchronize()
