@@ -23,6 +23,12 @@
 // MXFP8 caches (half the bytes): E4M3 values become FP16 exactly.  A block's power of two is applied to the FP32 sums
 // of its 32 values (keys), or to P (values), relative to a power that the vector's block is kept in; tokens whose powers
 // lie too far from it for FP16 are taken one by one in FP32.
+//
+// Measured (device time among other calls; 64 query heads on 8 key heads of 128 if not said otherwise): one sequence of
+// 131072 tokens 84 us (537 MB, 0.94 of a plain copy's rate); 88 sequences of 0 to 8192 (56 on 8) 221 us (1.49 GB, 0.99);
+// 176 of 1 to 8192 in MXFP8 267 us (1.53 GB, 0.84: the ALU pipe is 54 % busy, half of it turning E4M3 into FP16); 15 of 1
+// to 4096, 32 heads of 64 unshared, pages of 16 tokens, 49 us (245 MB, 0.73: 2 KB a copy; without any arithmetic 47.5);
+// one of 1000 tokens (56 on 8) 8.4 us, a chain of latencies: lengths, page numbers, tiles, parts, join.
 #include <math.h>
 #include <stdio.h>
 

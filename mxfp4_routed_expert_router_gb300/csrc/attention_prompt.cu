@@ -16,8 +16,15 @@
 // The maximum in use is kept until a row exceeds it by 2^8 (P is then up to 2^8, in BF16's and FP32's range alike):
 // rescaling O in tensor memory, which would be needed in every tile, becomes rare.
 //
-// Bound by the tensor pipe for long prompts: 512 flops per key, row and 128 values, of which the tile's exponentials
-// (128 a row) take about as long as half of its MMAs.
+// Measured (device time): 8192 rows, 64 heads on 8 of 128, 670 to 706 us (1.1 TFLOP: 1,640 to 1,560 TFLOP/s, 0.87 to
+// 0.83 of a cuBLAS burst, by how far the card's power limit has brought the clock down; 4 key heads with pauses 1,700).
+// A key tile takes 2,900 cycles for 2,048 of MMAs: a tile's softmax (load 150, maximum 400, exponentials 900, store
+// 110) and its own products (1,024 and 250 of latency) follow each other, and two tiles fill a third of each other's
+// gaps.  Tried without gain: P announced by halves; the exponentials with the old maximum while the new one is found;
+// two threads to a row (16 warps, a barrier of two per tile: 704 us for 673); rows that leave by TMA or, over shared
+// memory, by whole lines.  A new item costs 2 to 3 us beside its key tiles, so that short prompts get less (15 prompts
+// of 1 to 3001 rows, 56 heads on 8: 500 to 510 us for 650 GFLOP).  Heads of 64: 8192 rows, 32 heads on 4, 250 us, bound by
+// the softmax (exponentials: 49 % of their pipe).
 //
 // Masked values: P is 0 there, but 0 * inf is not.  Two warps clear the rows of V past the sequence's end, and values
 // that are not finite in tiles that some row must not see in full; rows that may see such a value get it added at the

@@ -12,6 +12,10 @@
 // give an MXFP8 block its largest value by shuffles.  With many tokens a thread takes the same 16 places of 4 heads, for
 // which the cosines and sines (64 bytes, twice the bytes of a head's values) are loaded once.
 //
+// Measured (device time among other calls): one token of 56 + 16 heads of 128 1.5 us; 176 tokens of 64 + 16 heads into
+// an MXFP8 cache 4.2 us; 8192 tokens of 64 + 16 heads, keys as rows too, 59 us (357 MB, 0.89 of a plain copy's rate; with
+// each load waiting for the one before 74 us; 512 threads a CTA 68; 2 or 8 heads a thread 81 or 61).
+//
 // MXFP8 keys round once, from the exact turned value: products and sum are held as two floats (a BF16 value times a
 // float leaves a float's rounding error, which an FMA gives) and the pair becomes a float rounded to odd, which no
 // later rounding to four bits takes to the wrong side of a border.
