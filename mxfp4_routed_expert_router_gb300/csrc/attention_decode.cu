@@ -70,6 +70,7 @@ struct DecodeArgs {
     float *part_o, *part_ml;         // parts: [2 * CTAs][8 NT][D], [2 * CTAs][8 NT][2]
     Split *splits;                   // [CTAs]: what starts in a CTA and goes on in the next
     int ctas;
+    bool whole;                      // a unit is its first place's CTA's alone
     int *err;
 };
 
@@ -598,16 +599,16 @@ template <class G> __device__ __forceinline__ void enter_sequence(const DecodeAr
     p.ahead = p.b + 1 < a.B ? __ldcg(a.lens + p.b + 1) : 0;
 }
 
-template <class G> __device__ __forceinline__ void cut(Stretch &p, long long end)
+template <class G> __device__ __forceinline__ void cut(const DecodeArgs &a, Stretch &p, long long end)
 {
-    p.t1 = (int)max(0ll, min((long long)p.nt, end - p.v - G::START));
+    p.t1 = a.whole ? p.nt : (int)max(0ll, min((long long)p.nt, end - p.v - G::START));
 }
 
 // The next stretch of a CTA whose places end at `end`; false where there is none.
 template <class G> __device__ __forceinline__ bool advance(const DecodeArgs &a, Stretch &p, long long end)
 {
     p.v += p.nt + G::START;
-    if (p.t1 < p.nt || p.v + G::START >= end)
+    if (p.t1 < p.nt || p.v + (a.whole ? 0 : G::START) >= end)
         return false;
     if (++p.u == a.units) {
         p.u = 0;
@@ -617,7 +618,7 @@ template <class G> __device__ __forceinline__ bool advance(const DecodeArgs &a, 
         } while (p.nt == 0 && p.b < a.B);
     }
     p.t0 = 0;
-    cut<G>(p, end);
+    cut<G>(a, p, end);
     return true;
 }
 
@@ -684,7 +685,9 @@ __global__ void __launch_bounds__(Geo<D, NT, MX>::THREADS, 1)
         p.u = (int)((start - base * a.units) / n);
         p.v = base * a.units + (long long)p.u * n;
         p.t0 = (int)max(0ll, start - p.v - G::START);
-        cut<G>(p, end);
+        cut<G>(a, p, end);
+        if (a.whole && start > p.v && !advance<G>(a, p, end))
+            p.t0 = p.t1 = 0;  // (the CTA's places are the rest of another's unit)
         first = p;
     }
     // sequences without tiles: zeros, or NaN where the length cannot be
@@ -701,7 +704,7 @@ __global__ void __launch_bounds__(Geo<D, NT, MX>::THREADS, 1)
     __syncthreads();
     if (tid == 0)
         a.splits[blockIdx.x] = {0, 0, 0, 0};  // (until the last stretch shows one)
-    if (start >= end || first.t1 <= first.t0)  // (a last CTA may have no more than a unit's START places)
+    if (start >= end || first.t1 <= first.t0)  // (a CTA may have no more than a unit's START places)
         return;
     Stretch at = first;
     const int page = 1 << a.page_log2, rows = min(page, G::TILE);  // rows of a TMA box
@@ -1052,10 +1055,16 @@ cudaError_t cache_map(CUtensorMap *m, const void *base, const MoeKvCache *c, int
 }
 
 template <int D, int NT, bool MX>
-cudaError_t launch_decode(const DecodeArgs &a, const MoeKvCache *cache, cudaStream_t st)
+cudaError_t launch_decode(DecodeArgs &a, const MoeKvCache *cache, cudaStream_t st)
 {
     using G = Geo<D, NT, MX>;
     CUtensorMap mk, mv;
+    // Short sequences are not shared between CTAs, which saves the join (2 us, and 3 us of the host's time for its launch).
+    // Measured, shared and whole (us in a graph; calls from Python): 56 heads on 8 of 128, one sequence of 512 tokens 7.4
+    // and 7.3 (11.9 and 9.5), of 1000 8.6 and 10.2, in MXFP8 11.7 and 13.2; 16 of 1 to 1000 15.6 and 13.2; 16 of 1 to 256
+    // 10.7 and 8.8; 88 of 1 to 256 25.1 and 24.7, of 1 to 500 31.4 and 31.6.
+    const long long units = (long long)a.B * a.units;
+    a.whole = a.cap <= (units > a.ctas ? 256 : 2 * units > a.ctas ? 1024 : 512);
     auto kern = decode_kernel<D, NT, MX>;
     static std::atomic<int> attr_set[MAX_DEVICES];
     cudaError_t e = smem_limit_once(attr_set, (const void *)kern, G::SMEM);
@@ -1067,7 +1076,7 @@ cudaError_t launch_decode(const DecodeArgs &a, const MoeKvCache *cache, cudaStre
         return e;
     if ((e = launch_overlapped(kern, (unsigned)a.ctas, G::THREADS, G::SMEM, 1, st, a, mk, mv)) != cudaSuccess)
         return e;
-    if (a.cap <= G::TILE)  // one tile a sequence and head: nothing is ever shared
+    if (a.whole)  // nothing is shared
         return cudaSuccess;
     return launch_overlapped(join_kernel<D, NT>, dim3((unsigned)a.ctas, 8 * NT), 128, 0, 1, st, a);
 }

@@ -48,6 +48,8 @@ CASES = [
     ([0, 0, 300, 0], 6, 2, 128, 128), ([5000], 16, 1, 128, 256), ([3, 4097, 1, 900], 32, 32, 64, 16),
     ([700] * 40, 40, 8, 128, 64), ([20000, 3], 64, 4, 128, 64), ([333, 100], 48, 2, 64, 32),
     ([37 * i % 500 for i in range(200)], 8, 2, 64, 32), ([1] * 300, 4, 4, 128, 16), ([257], 40, 1, 64, 256),
+    ([256, 0, 1, 255] * 60, 4, 2, 64, 64), ([512, 400], 12, 2, 128, 32), ([513, 400], 12, 2, 128, 16),
+    ([1024, 7, 0, 700] * 5, 20, 5, 64, 128), ([256] * 160, 8, 1, 128, 64), ([3] * 1500, 2, 1, 64, 16),
 ]
 
 
