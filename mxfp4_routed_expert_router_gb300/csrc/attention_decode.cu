@@ -43,12 +43,13 @@ namespace {
 
 using namespace gemm;
 
-constexpr int TEAM = 4;              // warps that share a tile, 16 tokens of each 64; teams take the tiles in turn
+constexpr int TEAM = 4;              // warps that share a tile, 16 tokens of each 64
+constexpr int TEAMS = 2;             // of a CTA, each with tiles of its own
 constexpr int MAX_STAGES = 16;
-constexpr int MIN_SHARE = 2;         // tiles of a CTA at least
+constexpr int MIN_SHARE = 2;         // tiles of a team at least
 
-// A unit that starts in a CTA (as its first stretch or its last: part 0 or 1) and ends in CTA `last`; of the CTAs
-// between it is the first stretch.  heads == 0: there is none.
+// A unit that starts with a worker (as its first stretch or its last: part 0 or 1) and ends with worker `last`; of the
+// workers between it is the first stretch.  heads == 0: there is none.
 struct alignas(16) Split {
     int b, head, heads_part, last;  // heads_part: heads * 2 + part
 };
@@ -67,15 +68,14 @@ struct DecodeArgs {
     float scale;                     // times log2(e)
     uint16_t *out;
     long long out_ld;
-    float *part_o, *part_ml;         // parts: [2 * CTAs][8 NT][D], [2 * CTAs][8 NT][2]
-    Split *splits;                   // [CTAs]: what starts in a CTA and goes on in the next
-    int ctas;
-    bool whole;                      // a unit is its first place's CTA's alone
+    float *part_o, *part_ml;         // parts: [2 * workers][8 NT][D], [2 * workers][8 NT][2]
+    Split *splits;                   // [workers]: what starts with one and goes on with the next
+    int ctas, workers;               // the workers are the CTAs' teams, all first ones first
+    bool whole;                      // a unit is its first place's worker's alone
     int *err;
 };
 
 template <int D, int NT, bool MX> struct Geo {
-    static constexpr int TEAMS = 2;
     static constexpr int WARPS = TEAM * TEAMS;       // that compute
     static constexpr int LOADERS = 2 * TEAMS;        // one for a team's keys, one for its values
     static constexpr int THREADS = (WARPS + LOADERS) * 32;
@@ -87,14 +87,14 @@ template <int D, int NT, bool MX> struct Geo {
     static constexpr int SC_B = MX ? TILE * D / 32 : 0;
     // what starting and ending a sequence and head costs, in tiles (0.7 us; a tile's bytes take 0.73 us per 32 KB)
     static constexpr int START = TILE_B >= 16384 ? 1 : 2;
-    static constexpr int MERGE_B = TEAM * NT * 8 * D * 4;
+    static constexpr int MERGE_B = TEAMS * 2 * NT * 8 * D * 4;         // two partial vectors of a team's heads
     static constexpr int FIT = (222 * 1024 - MERGE_B) / (2 * (TILE_B + SC_B));
     // a multiple of the teams: a slot then is one team's, which so sees every phase of its barriers
     static constexpr int STAGES = (FIT < MAX_STAGES ? FIT : MAX_STAGES) / TEAMS * TEAMS;
     static constexpr int SC_OFF = STAGES * 2 * TILE_B;
     static constexpr int MERGE_OFF = SC_OFF + STAGES * 2 * SC_B;
     static constexpr int ML_B = WARPS * NT * 8 * 2 * 4;
-    static constexpr int ML_OFF = MERGE_OFF + MERGE_B;                 // [2][WARPS][8 NT][2]
+    static constexpr int ML_OFF = MERGE_OFF + MERGE_B;                 // [2][TEAMS][TEAM][8 NT][2]
     static constexpr int BAR_OFF = ML_OFF + 2 * ML_B;
     static constexpr int BAD_OFF = BAR_OFF + 2 * MAX_STAGES * 8;       // a stage holds a page outside the cache
     static constexpr int SMEM = BAD_OFF + MAX_STAGES * 4 + 1024;       // + alignment slack
@@ -108,11 +108,11 @@ template <class G> __device__ __forceinline__ int tiles_of(const DecodeArgs &a, 
     return n > 0 && n <= a.cap ? (n + G::TILE - 1) / G::TILE : 0;
 }
 
-// The places of the list that a CTA takes, of `total` in all.  A unit (a key head of a sequence, or a chunk of its
+// The places of the list that a worker takes, of `total` in all.  A unit (a key head of a sequence, or a chunk of its
 // query heads) has START places for its beginning and end before one place per tile.
 template <class G> __device__ __forceinline__ long long share_of(const DecodeArgs &a, long long total)
 {
-    const long long s = (total + a.ctas - 1) / a.ctas;
+    const long long s = (total + a.workers - 1) / a.workers;
     return s < G::START + MIN_SHARE ? G::START + MIN_SHARE : s;
 }
 
@@ -604,7 +604,7 @@ template <class G> __device__ __forceinline__ void cut(const DecodeArgs &a, Stre
     p.t1 = a.whole ? p.nt : (int)max(0ll, min((long long)p.nt, end - p.v - G::START));
 }
 
-// The next stretch of a CTA whose places end at `end`; false where there is none.
+// The next stretch of a worker whose places end at `end`; false where there is none.
 template <class G> __device__ __forceinline__ bool advance(const DecodeArgs &a, Stretch &p, long long end)
 {
     p.v += p.nt + G::START;
@@ -633,7 +633,7 @@ __global__ void __launch_bounds__(Geo<D, NT, MX>::THREADS, 1)
     uint64_t *full = reinterpret_cast<uint64_t *>(smem + G::BAR_OFF), *empty = full + MAX_STAGES;
     int *bad = reinterpret_cast<int *>(smem + G::BAD_OFF);
     __shared__ long long scan[G::THREADS / 32];
-    __shared__ Stretch first;
+    __shared__ Stretch first[TEAMS];
     __shared__ int abort_word;
     volatile int *abort_flag = &abort_word;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -671,24 +671,31 @@ __global__ void __launch_bounds__(Geo<D, NT, MX>::THREADS, 1)
     }
     total *= a.units;
     const long long share = share_of<G>(a, total);
-    const long long start = min(total, (long long)blockIdx.x * share), end = min(total, start + share);
-    if (start < end && pre * a.units <= start && start < (pre + sum) * a.units) {
-        Stretch p;
-        p.b = tid * per;
-        long long base = pre;
-        int n = places_of<G>(a, p.b);
-        while (start >= (base + n) * a.units) {
-            base += n;
-            n = places_of<G>(a, ++p.b);
+    auto end_of = [&](int team) { return min(total, ((long long)team * gridDim.x + blockIdx.x + 1) * share); };
+    if (tid < TEAMS)
+        first[tid].t0 = first[tid].t1 = 0;
+    __syncthreads();
+#pragma unroll 1
+    for (int k = 0; k < TEAMS; ++k) {
+        const long long start = min(total, ((long long)k * gridDim.x + blockIdx.x) * share), end = end_of(k);
+        if (start < end && pre * a.units <= start && start < (pre + sum) * a.units) {
+            Stretch p;
+            p.b = tid * per;
+            long long base = pre;
+            int n = places_of<G>(a, p.b);
+            while (start >= (base + n) * a.units) {
+                base += n;
+                n = places_of<G>(a, ++p.b);
+            }
+            enter_sequence<G>(a, p, __ldcg(a.lens + p.b));
+            p.u = (int)((start - base * a.units) / n);
+            p.v = base * a.units + (long long)p.u * n;
+            p.t0 = (int)max(0ll, start - p.v - G::START);
+            cut<G>(a, p, end);
+            if (a.whole && start > p.v && !advance<G>(a, p, end))
+                p.t0 = p.t1 = 0;  // (the worker's places are the rest of another's unit)
+            first[k] = p;
         }
-        enter_sequence<G>(a, p, __ldcg(a.lens + p.b));
-        p.u = (int)((start - base * a.units) / n);
-        p.v = base * a.units + (long long)p.u * n;
-        p.t0 = (int)max(0ll, start - p.v - G::START);
-        cut<G>(a, p, end);
-        if (a.whole && start > p.v && !advance<G>(a, p, end))
-            p.t0 = p.t1 = 0;  // (the CTA's places are the rest of another's unit)
-        first = p;
     }
     // sequences without tiles: zeros, or NaN where the length cannot be
     for (int b = blockIdx.x; b < a.B; b += gridDim.x) {
@@ -702,11 +709,13 @@ __global__ void __launch_bounds__(Geo<D, NT, MX>::THREADS, 1)
             reinterpret_cast<uint4 *>(a.out + b * a.out_ld)[i] = make_uint4(v, v, v, v);
     }
     __syncthreads();
-    if (tid == 0)
-        a.splits[blockIdx.x] = {0, 0, 0, 0};  // (until the last stretch shows one)
-    if (start >= end || first.t1 <= first.t0)  // (a CTA may have no more than a unit's START places)
+    const int team = warp < G::WARPS ? warp / TEAM : (warp - G::WARPS) >> 1, worker = team * gridDim.x + blockIdx.x;
+    const long long end = end_of(team);
+    if (warp % TEAM == 0 && warp < G::WARPS && lane == 0)
+        a.splits[worker] = {0, 0, 0, 0};  // (until the last stretch shows one)
+    if (first[team].t1 <= first[team].t0)  // (none left, or no more than a unit's START places)
         return;
-    Stretch at = first;
+    Stretch at = first[team];
     const int page = 1 << a.page_log2, rows = min(page, G::TILE);  // rows of a TMA box
 
     if (warp >= G::WARPS) {
@@ -714,7 +723,7 @@ __global__ void __launch_bounds__(Geo<D, NT, MX>::THREADS, 1)
         // A warp for each team's keys and one for its values: a copy costs its issuer about as long whatever its size,
         // and small pages take several.  A lane per page of a tile.  The table is read 32 pages at a time, a block
         // ahead: a tile's pages then cost a shuffle, where a load per tile would hold the loader up.
-        const int team = (warp - G::WARPS) >> 1, pages = G::TILE / rows;
+        const int pages = G::TILE / rows;
         const bool is_v = (warp - G::WARPS) & 1;
         const CUtensorMap *map = is_v ? &map_v : &map_k;
         const uint8_t *scales = is_v ? a.vs : a.ks;
@@ -722,12 +731,12 @@ __global__ void __launch_bounds__(Geo<D, NT, MX>::THREADS, 1)
             const int i = 32 * k + lane;
             return (long long)i << a.page_log2 < len ? __ldcg(a.table + (long long)b * a.max_pages + i) : 0;
         };
-        int slot = team, own = team, n0 = 0;  // the team's next tile, and the stretch's first, in the CTA's count
+        int slot = team, n = 0;  // (every TEAMS-th slot is the team's); tiles so far
         uint32_t ph = 0;
         int held_b = -1, held_k = 0, held = 0, ahead = 0;
         bool ok = true;
         do {
-            for (int t = at.t0 + (own - n0); t < at.t1; t += G::TEAMS) {
+            for (int t = at.t0; t < at.t1; ++t) {
                 const int pg0 = (t * G::TILE) >> a.page_log2, k = pg0 >> 5;
                 if (at.b != held_b || k != held_k) {
                     held = at.b == held_b && k == held_k + 1 ? ahead : block(at.b, k, at.len);
@@ -760,28 +769,28 @@ __global__ void __launch_bounds__(Geo<D, NT, MX>::THREADS, 1)
                                  scales + row * (D / 32), rows * (D / 32), &full[slot]);
                     }
                 }
-                own += G::TEAMS;
-                if ((slot += G::TEAMS) >= G::STAGES) {
+                ++n;
+                if ((slot += TEAMS) >= G::STAGES) {
                     slot = team;
                     ph ^= 1;
                 }
             }
-            n0 += at.t1 - at.t0;
         } while (ok && advance<G>(a, at, end));
         // every copy has landed before the CTA ends (bounded; slots whose other half never came run the limit out)
         if (lane == 0)
-            for (int i = max(team, own - G::STAGES); i < own; i += G::TEAMS)
-                if (!mbar_drain(&full[i % G::STAGES], (i / G::STAGES) & 1))
+            for (int i = max(0, n - G::STAGES / TEAMS); i < n; ++i)
+                if (!mbar_drain(&full[team + i % (G::STAGES / TEAMS) * TEAMS], i / (G::STAGES / TEAMS) & 1))
                     break;
         __syncwarp();
         return;
     }
 
     // ---------------------------------------------------------- products
-    const int g = lane >> 2, qd = lane & 3, team = warp / TEAM, w4 = warp % TEAM;
-    float *merge = reinterpret_cast<float *>(smem + G::MERGE_OFF);
+    const int g = lane >> 2, qd = lane & 3, w4 = warp % TEAM;
+    float *merge = reinterpret_cast<float *>(smem + G::MERGE_OFF) + team * 2 * NT * 8 * D;
+    auto team_sync = [&] { asm volatile("barrier.cta.sync.aligned %0, %1;" ::"r"(1 + team), "n"(TEAM * 32) : "memory"); };
     const uint32_t ring = smem_addr(smem);
-    int slot = team, own = team, n0 = 0, part = 0;
+    int slot = team, part = 0;
     uint32_t ph = 0;
     Powers ref{0, false};
     bool alive = true, odd = false;
@@ -816,7 +825,7 @@ __global__ void __launch_bounds__(Geo<D, NT, MX>::THREADS, 1)
                     st.o[i][nt][c] = 0.f;
         }
         bool wrong = false;
-        for (int t = t0 + (own - n0); t < t1; t += G::TEAMS) {
+        for (int t = t0; t < t1; ++t) {
             // (after a wait that ran out the warp only keeps to the others' barriers; the rows become NaN)
             alive = alive && __all_sync(0xffffffffu, mbar_wait(&full[slot], ph, abort_flag, a.err)) != 0;
             wrong |= !alive || bad[slot] != 0;
@@ -838,16 +847,15 @@ __global__ void __launch_bounds__(Geo<D, NT, MX>::THREADS, 1)
             __syncwarp();
             if (lane == 0 && alive)
                 mbar_arrive(&empty[slot]);
-            own += G::TEAMS;
-            if ((slot += G::TEAMS) >= G::STAGES) {
+            if ((slot += TEAMS) >= G::STAGES) {
                 slot = team;
                 ph ^= 1;
             }
         }
-        n0 += t1 - t0;
-        // The warps' parts: all come to the common maximum, then a team adds what the team above it has left.
+        // The warps' parts: all come to the common maximum, the third's and the fourth's vectors go to the first and the
+        // second, and the two sums meet in memory.
         // (maxima and sums lie in one of two places in turn: a warp may be one stretch ahead of the others' reads)
-        float *ml = reinterpret_cast<float *>(smem + G::ML_OFF + (odd ? G::ML_B : 0));
+        float *ml = reinterpret_cast<float *>(smem + G::ML_OFF + (odd ? G::ML_B : 0)) + team * TEAM * NT * 8 * 2;
         odd = !odd;
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
@@ -860,16 +868,16 @@ __global__ void __launch_bounds__(Geo<D, NT, MX>::THREADS, 1)
                 if (wrong)
                     l = __int_as_float(0x7FC00000);
                 if (g == 0)
-                    *reinterpret_cast<float2 *>(ml + ((warp * NT + nt) * 8 + 2 * qd + h) * 2) = make_float2(st.m[nt][h], l);
+                    *reinterpret_cast<float2 *>(ml + ((w4 * NT + nt) * 8 + 2 * qd + h) * 2) = make_float2(st.m[nt][h], l);
             }
-        asm volatile("bar.sync 1, %0;" ::"n"(G::WARPS * 32) : "memory");
+        team_sync();
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
                 float m = -INFINITY;
 #pragma unroll
-                for (int w = 0; w < G::WARPS; ++w)
+                for (int w = 0; w < TEAM; ++w)
                     m = fmaxf(m, ml[((w * NT + nt) * 8 + 2 * qd + h) * 2]);
                 const float f = ex2(st.m[nt][h] - finite_base(m));
 #pragma unroll
@@ -883,63 +891,57 @@ __global__ void __launch_bounds__(Geo<D, NT, MX>::THREADS, 1)
                     st.o[i][nt][2 + h] *= f;
                 }
             }
+        float4 *mine = reinterpret_cast<float4 *>(merge + (w4 & 1) * NT * 8 * D) + lane;
+        if (w4 >= 2) {
 #pragma unroll
-        for (int from = G::TEAMS - 1; from >= 0; --from) {
-            if (team == from) {
-                float4 *mine = reinterpret_cast<float4 *>(merge + w4 * NT * 8 * D) + lane;
-                if (from < G::TEAMS - 1) {
+            for (int i = 0; i < D / 16; ++i)
 #pragma unroll
-                    for (int i = 0; i < D / 16; ++i)
-#pragma unroll
-                        for (int nt = 0; nt < NT; ++nt) {
-                            const float4 x = mine[(i * NT + nt) * 32];
-                            st.o[i][nt][0] += x.x, st.o[i][nt][1] += x.y, st.o[i][nt][2] += x.z, st.o[i][nt][3] += x.w;
-                        }
-                }
-                __syncwarp();
-                if (from > 0) {
-#pragma unroll
-                    for (int i = 0; i < D / 16; ++i)
-#pragma unroll
-                        for (int nt = 0; nt < NT; ++nt)
-                            mine[(i * NT + nt) * 32] =
-                                make_float4(st.o[i][nt][0], st.o[i][nt][1], st.o[i][nt][2], st.o[i][nt][3]);
-                } else {
-                    // the first team's in the order of heads and values: MMA i has a head's values 4 g + 2 (i & 1) and
-                    // the next of 32 (MXFP8), 8 g + 2 (i & 3) and the next of 64
-#pragma unroll
-                    for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                        for (int h = 0; h < 2; ++h) {
-                            float *o = merge + (w4 * NT * 8 + nt * 8 + 2 * qd + h) * D;
-#pragma unroll
-                            for (int i = 0; i < D / 16; ++i)
-                                *reinterpret_cast<float2 *>(o + (MX ? 32 * (i / 2) + 4 * g + 2 * (i & 1)
-                                                                    : 64 * (i / 4) + 8 * g + 2 * (i & 3))) =
-                                    make_float2(st.o[i][nt][h], st.o[i][nt][2 + h]);
-                        }
-                }
-            }
-            asm volatile("bar.sync 1, %0;" ::"n"(G::WARPS * 32) : "memory");
+                for (int nt = 0; nt < NT; ++nt)
+                    mine[(i * NT + nt) * 32] = make_float4(st.o[i][nt][0], st.o[i][nt][1], st.o[i][nt][2], st.o[i][nt][3]);
         }
+        team_sync();
+        if (w4 < 2) {
+#pragma unroll
+            for (int i = 0; i < D / 16; ++i)
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt) {
+                    const float4 x = mine[(i * NT + nt) * 32];
+                    st.o[i][nt][0] += x.x, st.o[i][nt][1] += x.y, st.o[i][nt][2] += x.z, st.o[i][nt][3] += x.w;
+                }
+            __syncwarp();
+            // in the order of heads and values: MMA i has a head's values 4 g + 2 (i & 1) and the next of 32 (MXFP8),
+            // 8 g + 2 (i & 3) and the next of 64
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    float *o = merge + (w4 * NT * 8 + nt * 8 + 2 * qd + h) * D;
+#pragma unroll
+                    for (int i = 0; i < D / 16; ++i)
+                        *reinterpret_cast<float2 *>(o + (MX ? 32 * (i / 2) + 4 * g + 2 * (i & 1)
+                                                            : 64 * (i / 4) + 8 * g + 2 * (i & 3))) =
+                            make_float2(st.o[i][nt][h], st.o[i][nt][2 + h]);
+                }
+        }
+        team_sync();
         const bool whole = t0 == 0 && t1 == at.nt;
-        if (t0 == 0 && !whole && tid == 0)
-            a.splits[blockIdx.x] = {at.b, (int)head, heads * 2 + part, (int)((at.v + G::START + at.nt - 1) / share)};
-        for (int i = tid; i < NT * D; i += G::WARPS * 32) {
+        if (t0 == 0 && !whole && w4 == 0 && lane == 0)
+            a.splits[worker] = {at.b, (int)head, heads * 2 + part, (int)((at.v + G::START + at.nt - 1) / share)};
+        for (int i = w4 * 32 + lane; i < NT * D; i += TEAM * 32) {
             const int hd = i / (D / 8), d = i % (D / 8) * 8;
             if (hd >= heads)
                 continue;
             float m = -INFINITY, l = 0.f, v[8] = {};
 #pragma unroll
-            for (int w = 0; w < G::WARPS; ++w)
+            for (int w = 0; w < TEAM; ++w)
                 m = fmaxf(m, ml[(w * NT * 8 + hd) * 2]);
 #pragma unroll
-            for (int w = 0; w < G::WARPS; ++w) {
+            for (int w = 0; w < TEAM; ++w) {
                 const float2 x = *reinterpret_cast<const float2 *>(ml + (w * NT * 8 + hd) * 2);
                 l = fmaf(x.y, ex2(x.x - finite_base(m)), l);
             }
 #pragma unroll
-            for (int w = 0; w < TEAM; ++w) {
+            for (int w = 0; w < 2; ++w) {
                 const float4 *o = reinterpret_cast<const float4 *>(merge + (w * NT * 8 + hd) * D + d);
                 const float4 o0 = o[0], o1 = o[1];
                 v[0] += o0.x, v[1] += o0.y, v[2] += o0.z, v[3] += o0.w;
@@ -952,7 +954,7 @@ __global__ void __launch_bounds__(Geo<D, NT, MX>::THREADS, 1)
                     v[k] *= inv;
                 *reinterpret_cast<uint4 *>(a.out + at.b * a.out_ld + (head + hd) * D + d) = bf16x8(v);
             } else {
-                const long long s = (2ll * blockIdx.x + part) * 8 * NT + hd;
+                const long long s = (2ll * worker + part) * 8 * NT + hd;
                 float4 *o = reinterpret_cast<float4 *>(a.part_o + s * D + d);
                 o[0] = make_float4(v[0], v[1], v[2], v[3]);
                 o[1] = make_float4(v[4], v[5], v[6], v[7]);
@@ -960,11 +962,11 @@ __global__ void __launch_bounds__(Geo<D, NT, MX>::THREADS, 1)
                     *reinterpret_cast<float2 *>(a.part_ml + 2 * s) = make_float2(m, l);
             }
         }
-        part = 1;  // of a CTA's stretches only the first and the last can be parts
+        part = 1;  // of a worker's stretches only the first and the last can be parts
     } while (advance<G>(a, at, end));
 }
 
-// Joins the parts of a query head of the unit that starts in CTA blockIdx.x and goes on in others; in the order of the
+// Joins the parts of a query head of the unit that starts with worker blockIdx.x and goes on with others; in the order of the
 // parts, four warps taking them in turn.
 template <int D, int NT>
 __global__ void __launch_bounds__(128) join_kernel(const DecodeArgs a)
@@ -1064,7 +1066,7 @@ cudaError_t launch_decode(DecodeArgs &a, const MoeKvCache *cache, cudaStream_t s
     // and 7.3 (11.9 and 9.5), of 1000 8.6 and 10.2, in MXFP8 11.7 and 13.2; 16 of 1 to 1000 15.6 and 13.2; 16 of 1 to 256
     // 10.7 and 8.8; 88 of 1 to 256 25.1 and 24.7, of 1 to 500 31.4 and 31.6.
     const long long units = (long long)a.B * a.units;
-    a.whole = a.cap <= (units > a.ctas ? 256 : 2 * units > a.ctas ? 1024 : 512);
+    a.whole = a.cap <= (units > a.workers ? 256 : 2 * units > a.workers ? 1024 : 512);
     auto kern = decode_kernel<D, NT, MX>;
     static std::atomic<int> attr_set[MAX_DEVICES];
     cudaError_t e = smem_limit_once(attr_set, (const void *)kern, G::SMEM);
@@ -1078,12 +1080,12 @@ cudaError_t launch_decode(DecodeArgs &a, const MoeKvCache *cache, cudaStream_t s
         return e;
     if (a.whole)  // nothing is shared
         return cudaSuccess;
-    return launch_overlapped(join_kernel<D, NT>, dim3((unsigned)a.ctas, 8 * NT), 128, 0, 1, st, a);
+    return launch_overlapped(join_kernel<D, NT>, dim3((unsigned)a.workers, 8 * NT), 128, 0, 1, st, a);
 }
 
 size_t part_bytes(int heads_of_part, int D)
 {
-    return (size_t)sm_count() * (2 * heads_of_part * (D + 2) * 4 + sizeof(Split));
+    return (size_t)TEAMS * sm_count() * (2 * heads_of_part * (D + 2) * 4 + sizeof(Split));
 }
 
 bool heads_fit(int n_heads, int n_kv_heads)
@@ -1166,9 +1168,10 @@ extern "C" MoeStatus moe_attention_decode(const MoeKvCache *cache, const void *q
         a.out = static_cast<uint16_t *>(out);
         a.out_ld = out_ld;
         a.ctas = gemm::sm_count();
+        a.workers = TEAMS * a.ctas;
         a.part_o = static_cast<float *>(workspace);
-        a.part_ml = a.part_o + (size_t)2 * a.ctas * 8 * nt * D;
-        a.splits = reinterpret_cast<Split *>(a.part_ml + (size_t)2 * a.ctas * 8 * nt * 2);
+        a.part_ml = a.part_o + (size_t)2 * a.workers * 8 * nt * D;
+        a.splits = reinterpret_cast<Split *>(a.part_ml + (size_t)2 * a.workers * 8 * nt * 2);
         cudaStream_t st = (cudaStream_t)cuda_stream;
         const bool mx = cache->type == MOE_ROWS_MXFP8;
         if (D == 128)
