@@ -4,31 +4,32 @@
 //   out_h = sum_t p_t v_t / sum_t p_t,   p_t = 2^(s_t - m),  s_t = scale * log2(e) * (q_h . k_t)
 //
 // The cache is read once and nothing else counts: 4 * head_dim bytes a token and key head, for 4 * head_dim flops a
-// query head.  So this is a stream, like the weight stream of linear.cu: a CTA per SM whose loader warp brings tiles
-// of 64 tokens (keys and values of one key head, by TMA through the page table) into a ring of up to 200 KB of shared
-// memory, and two
-// teams of four warps that take the tiles in turn.  Two warp-level MMAs per 16 x 16 values of a tile do
-// the work of all query heads that share the key head, eight at a time:
+// query head.  So this is a stream, like the weight stream of linear.cu: a CTA per SM with a ring of up to 200 KB of
+// shared memory, and two teams in it that share the ring's slots and nothing else: two warps that load tiles of 64 or 128
+// tokens (keys, and values, of one key head, by TMA through the page table) and four that take 16 tokens of each 64.  Two
+// warp-level MMAs per 16 x 16 values of a tile do the work of all query heads that share the key head, eight at a time:
 //   S^T[16 tokens, 8 heads] = K Q^T,    O^T[16 values, 8 heads] += V^T P^T
 // With tokens as the rows of the first product and values as the rows of the second, keys come out of shared memory as
 // they lie there (16 bytes a lane, which pair with the same 16 bytes of q), values by one byte permutation per pair of
 // tokens, and P moves from one to the other by a transposition of 8 x 8 (movmatrix).  The tiles carry TMA's 128-byte
 // (8-bit heads of 64: 64-byte) swizzle, so that neither read meets a bank twice.
 //
-// The work of all sequences and key heads, tile by tile, is one long list that the CTAs share evenly whatever the
-// lengths (which only the device knows): a CTA takes the tiles [c * share, (c + 1) * share).  What it finishes alone it
-// writes; of a sequence and head that other CTAs have a part of it leaves the running maximum, sum and vector in the
-// workspace, and a second kernel joins the parts in their order.
+// The work of all sequences and key heads, tile by tile, is one long list that the workers (the teams of all CTAs) share
+// evenly whatever the lengths (which only the device knows): worker w takes the places [w * share, (w + 1) * share).  What
+// it finishes alone it writes; of a sequence and head that other workers have a part of it leaves the running maximum, sum
+// and vector in the workspace, and a second kernel joins the parts in their order.  (Both teams on one list, each taking
+// every other tile, left the SM idle while a sequence's end was written and the next one's start loaded: 88 sequences of
+// 1 to 256 tokens 24.8 us for 18.9, the MXFP8 case below 267 for 249.)
 //
 // MXFP8 caches (half the bytes): E4M3 values become FP16 exactly.  A block's power of two is applied to the FP32 sums
 // of its 32 values (keys), or to P (values), relative to a power that the vector's block is kept in; tokens whose powers
 // lie too far from it for FP16 are taken one by one in FP32.
 //
 // Measured (device time among other calls; 64 query heads on 8 key heads of 128 if not said otherwise): one sequence of
-// 131072 tokens 84 us (537 MB, 0.94 of a plain copy's rate); 88 sequences of 0 to 8192 (56 on 8) 221 us (1.49 GB, 0.99);
-// 176 of 1 to 8192 in MXFP8 267 us (1.53 GB, 0.84: the ALU pipe is 54 % busy, half of it turning E4M3 into FP16); 15 of 1
-// to 4096, 32 heads of 64 unshared, pages of 16 tokens, 49 us (245 MB, 0.73: 2 KB a copy; without any arithmetic 47.5);
-// one of 1000 tokens (56 on 8) 8.4 us, a chain of latencies: lengths, page numbers, tiles, parts, join.
+// 131072 tokens 87 us (537 MB, 0.91 of a plain copy's rate; 81 without the join); 88 sequences of 0 to 8192 (56 on 8)
+// 222 us (1.49 GB, 0.99); 176 of 1 to 8192 in MXFP8 249 us (1.53 GB, 0.90); 15 of 1 to 4096, 32 heads of 64 unshared,
+// pages of 16 tokens, 44 us (245 MB, 0.83: 2 KB a copy); one of 1000 tokens (56 on 8) 8.4 us, a chain of latencies:
+// lengths, page numbers, tiles, parts, join.
 #include <math.h>
 #include <stdio.h>
 
@@ -1061,12 +1062,11 @@ cudaError_t launch_decode(DecodeArgs &a, const MoeKvCache *cache, cudaStream_t s
 {
     using G = Geo<D, NT, MX>;
     CUtensorMap mk, mv;
-    // Short sequences are not shared between CTAs, which saves the join (2 us, and 3 us of the host's time for its launch).
-    // Measured, shared and whole (us in a graph; calls from Python): 56 heads on 8 of 128, one sequence of 512 tokens 7.4
-    // and 7.3 (11.9 and 9.5), of 1000 8.6 and 10.2, in MXFP8 11.7 and 13.2; 16 of 1 to 1000 15.6 and 13.2; 16 of 1 to 256
-    // 10.7 and 8.8; 88 of 1 to 256 25.1 and 24.7, of 1 to 500 31.4 and 31.6.
-    const long long units = (long long)a.B * a.units;
-    a.whole = a.cap <= (units > a.workers ? 256 : 2 * units > a.workers ? 1024 : 512);
+    // Short sequences are not shared between workers, which saves the join (2 us, and 3 us of the host's time for its
+    // launch).  Measured, shared and whole (us in a graph; calls from Python): 56 heads on 8 of 128, one sequence of 256
+    // tokens 8.0 and 6.2 (11.9 and 9.8), of 512 7.7 and 8.6 (12.5 and 9.9), of 1000 8.4 and 13.2 (12.3 and 13.6); 88 of 1
+    // to 256 20.5 and 19.0, of 1 to 500 26.0 and 24.9; 32 of 1 to 500 16.0 and 15.9, of 1 to 1000 19.8 and 20.5.
+    a.whole = a.cap <= 512;
     auto kern = decode_kernel<D, NT, MX>;
     static std::atomic<int> attr_set[MAX_DEVICES];
     cudaError_t e = smem_limit_once(attr_set, (const void *)kern, G::SMEM);
