@@ -6,7 +6,8 @@
 // The cache is read once and nothing else counts: 4 * head_dim bytes a token and key head, for 4 * head_dim flops a
 // query head.  So this is a stream, like the weight stream of linear.cu: a CTA per SM with a ring of up to 200 KB of
 // shared memory, and two teams in it that share the ring's slots and nothing else: two warps that load tiles of 64 or 128
-// tokens (keys, and values, of one key head, by TMA through the page table) and four that take 16 tokens of each 64.  Two
+// tokens (keys, and values, of one key head, by TMA through the page table; a stretch's queries ahead of its first tile,
+// 222 -> 218 us for the 88 sequences below) and four that take 16 tokens of each 64.  Two
 // warp-level MMAs per 16 x 16 values of a tile do the work of all query heads that share the key head, eight at a time:
 //   S^T[16 tokens, 8 heads] = K Q^T,    O^T[16 values, 8 heads] += V^T P^T
 // With tokens as the rows of the first product and values as the rows of the second, keys come out of shared memory as
@@ -26,8 +27,8 @@
 // lie too far from it for FP16 are taken one by one in FP32.
 //
 // Measured (device time among other calls; 64 query heads on 8 key heads of 128 if not said otherwise): one sequence of
-// 131072 tokens 87 us (537 MB, 0.91 of a plain copy's rate; 81 without the join); 88 sequences of 0 to 8192 (56 on 8)
-// 222 us (1.49 GB, 0.99); 176 of 1 to 8192 in MXFP8 249 us (1.53 GB, 0.90); 15 of 1 to 4096, 32 heads of 64 unshared,
+// 131072 tokens 85 us (537 MB, 0.93 of a plain copy's rate; 80 without the join); 88 sequences of 0 to 8192 (56 on 8)
+// 218 us (1.49 GB, 1.00); 176 of 1 to 8192 in MXFP8 246 us (1.53 GB, 0.92); 15 of 1 to 4096, 32 heads of 64 unshared,
 // pages of 16 tokens, 44 us (245 MB, 0.83: 2 KB a copy); one of 1000 tokens (56 on 8) 8.4 us, a chain of latencies:
 // lengths, page numbers, tiles, parts, join.
 #include <math.h>
@@ -89,18 +90,21 @@ template <int D, int NT, bool MX> struct Geo {
     // what starting and ending a sequence and head costs, in tiles (0.7 us; a tile's bytes take 0.73 us per 32 KB)
     static constexpr int START = TILE_B >= 16384 ? 1 : 2;
     static constexpr int MERGE_B = TEAMS * 2 * NT * 8 * D * 4;         // two partial vectors of a team's heads
-    static constexpr int FIT = (222 * 1024 - MERGE_B) / (2 * (TILE_B + SC_B));
+    static constexpr int Q_B = NT * 8 * D * 2;                         // the queries of a stretch
+    static constexpr int ML_B = WARPS * NT * 8 * 2 * 4;
+    static constexpr int FIT = (224 * 1024 - MERGE_B - 2 * ML_B - 2 * TEAMS * Q_B) / (2 * (TILE_B + SC_B));
     // a multiple of the teams: a slot then is one team's, which so sees every phase of its barriers
     static constexpr int STAGES = (FIT < MAX_STAGES ? FIT : MAX_STAGES) / TEAMS * TEAMS;
     static constexpr int SC_OFF = STAGES * 2 * TILE_B;
     static constexpr int MERGE_OFF = SC_OFF + STAGES * 2 * SC_B;
-    static constexpr int ML_B = WARPS * NT * 8 * 2 * 4;
     static constexpr int ML_OFF = MERGE_OFF + MERGE_B;                 // [2][TEAMS][TEAM][8 NT][2]
-    static constexpr int BAR_OFF = ML_OFF + 2 * ML_B;
-    static constexpr int BAD_OFF = BAR_OFF + 2 * MAX_STAGES * 8;       // a stage holds a page outside the cache
+    static constexpr int Q_OFF = ML_OFF + 2 * ML_B;                    // [TEAMS][2]
+    static constexpr int BAR_OFF = Q_OFF + 2 * TEAMS * Q_B;
+    static constexpr int BAD_OFF = BAR_OFF + (2 * MAX_STAGES + 4 * TEAMS) * 8;       // a stage holds a page outside the cache
     static constexpr int SMEM = BAD_OFF + MAX_STAGES * 4 + 1024;       // + alignment slack
     static_assert(SMEM <= 226 * 1024, "shared memory");
-    static_assert(TILE_B % 1024 == 0 && SC_OFF % 16 == 0 && SC_B % 16 == 0 && BAR_OFF % 8 == 0, "alignment");
+    static_assert(TILE_B % 1024 == 0 && SC_OFF % 16 == 0 && SC_B % 16 == 0 && Q_OFF % 16 == 0 && BAR_OFF % 8 == 0,
+                  "alignment");
 };
 
 // Tiles of a sequence of n tokens: 0 for an empty one and for a length that the table cannot hold.
@@ -216,10 +220,10 @@ template <int D, int NT> struct State {
 
 // ---------------------------------------------------------------- BF16
 
-// q as the B operand: lane (g, q) has of head g the 16-byte pieces 8 h + 2q and 8 h + 2q + 1 of each 64 values h
+// q (in shared memory) as the B operand: lane (g, q) has of head g the 16-byte pieces 8 h + 2q and 8 h + 2q + 1 of each
+// 64 values h
 template <int D, int NT>
-__device__ __forceinline__ void load_q(const DecodeArgs &a, const uint16_t *q, int heads, int g, int qd,
-                                       uint32_t (&qf)[NT][D / 8])
+__device__ __forceinline__ void load_q(uint32_t q, int heads, int g, int qd, uint32_t (&qf)[NT][D / 8])
 {
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
@@ -227,7 +231,7 @@ __device__ __forceinline__ void load_q(const DecodeArgs &a, const uint16_t *q, i
         for (int c = 0; c < D / 32; ++c) {
             uint4 u = make_uint4(0, 0, 0, 0);
             if (8 * nt + g < heads)
-                u = __ldcg(reinterpret_cast<const uint4 *>(q + (8 * nt + g) * D) + 8 * (c / 2) + 2 * qd + (c & 1));
+                u = lds128(q + (8 * nt + g) * (D * 2) + (8 * (c / 2) + 2 * qd + (c & 1)) * 16);
             qf[nt][4 * c] = u.x, qf[nt][4 * c + 1] = u.y, qf[nt][4 * c + 2] = u.z, qf[nt][4 * c + 3] = u.w;
         }
 }
@@ -356,8 +360,8 @@ __device__ __forceinline__ void tile_bf16(State<D, NT> &st, const uint32_t (&qf)
 // q in FP16 with a power of two per head (the largest |q| lands in [2^14, 2^15)): lane (g, q) has of head g the values
 // 32 b + 8 q .. + 7 of each block b.  e: the powers of heads 2q and 2q + 1.
 template <int D, int NT>
-__device__ __forceinline__ void load_q_f16(const DecodeArgs &a, const uint16_t *q, int heads, int g, int qd,
-                                           uint32_t (&qf)[NT][D / 8], float (&mul)[NT][2])
+__device__ __forceinline__ void load_q_f16(float scale, uint32_t q, int heads, int g, int qd, uint32_t (&qf)[NT][D / 8],
+                                           float (&mul)[NT][2])
 {
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
@@ -367,7 +371,7 @@ __device__ __forceinline__ void load_q_f16(const DecodeArgs &a, const uint16_t *
         for (int b = 0; b < D / 32; ++b) {
             uint4 u = make_uint4(0, 0, 0, 0);
             if (8 * nt + g < heads)
-                u = __ldcg(reinterpret_cast<const uint4 *>(q + (8 * nt + g) * D) + 4 * b + qd);
+                u = lds128(q + (8 * nt + g) * (D * 2) + (4 * b + qd) * 16);
             w[4 * b] = u.x, w[4 * b + 1] = u.y, w[4 * b + 2] = u.z, w[4 * b + 3] = u.w;
         }
 #pragma unroll
@@ -380,8 +384,8 @@ __device__ __forceinline__ void load_q_f16(const DecodeArgs &a, const uint16_t *
 #pragma unroll
         for (int i = 0; i < D / 8; ++i)
             qf[nt][i] = f16_pair(__uint_as_float(w[i] << 16) * by, __uint_as_float(w[i] & 0xFFFF0000u) * by);
-        mul[nt][0] = a.scale * __int_as_float((127 + __shfl_sync(0xffffffffu, e, 8 * qd)) << 23);
-        mul[nt][1] = a.scale * __int_as_float((127 + __shfl_sync(0xffffffffu, e, 8 * qd + 4)) << 23);
+        mul[nt][0] = scale * __int_as_float((127 + __shfl_sync(0xffffffffu, e, 8 * qd)) << 23);
+        mul[nt][1] = scale * __int_as_float((127 + __shfl_sync(0xffffffffu, e, 8 * qd + 4)) << 23);
     }
 }
 
@@ -632,6 +636,7 @@ __global__ void __launch_bounds__(Geo<D, NT, MX>::THREADS, 1)
     extern __shared__ uint8_t smem_dyn[];
     uint8_t *smem = smem_dyn + ((1024u - (smem_addr(smem_dyn) & 1023u)) & 1023u);
     uint64_t *full = reinterpret_cast<uint64_t *>(smem + G::BAR_OFF), *empty = full + MAX_STAGES;
+    uint64_t *q_full = empty + MAX_STAGES, *q_empty = q_full + 2 * TEAMS;  // [TEAMS][2]
     int *bad = reinterpret_cast<int *>(smem + G::BAD_OFF);
     __shared__ long long scan[G::THREADS / 32];
     __shared__ Stretch first[TEAMS];
@@ -643,6 +648,10 @@ __global__ void __launch_bounds__(Geo<D, NT, MX>::THREADS, 1)
         for (int i = 0; i < G::STAGES; ++i) {
             mbar_init(&full[i], 2);
             mbar_init(&empty[i], TEAM);
+        }
+        for (int i = 0; i < 2 * TEAMS; ++i) {
+            mbar_init(&q_full[i], 1);
+            mbar_init(&q_empty[i], TEAM);
         }
         abort_word = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -735,15 +744,29 @@ __global__ void __launch_bounds__(Geo<D, NT, MX>::THREADS, 1)
         int slot = team, n = 0;  // (every TEAMS-th slot is the team's); tiles so far
         uint32_t ph = 0;
         int held_b = -1, held_k = 0, held = 0, ahead = 0;
+        int q_armed = -1;
         bool ok = true;
-        do {
+        for (int k = 0;; ++k) {  // stretches
+            if (!is_v) {
+                const int kvh = at.u / a.chunks, h0 = (at.u - kvh * a.chunks) * 8 * NT, heads = min(8 * NT, a.group - h0);
+                uint64_t *bar = &q_full[2 * team + (k & 1)];
+                if (!(ok = mbar_wait_sleep_warp(&q_empty[2 * team + (k & 1)], ((k >> 1) & 1) ^ 1, abort_flag, a.err, lane)))
+                    break;
+                if (lane == 0) {
+                    mbar_arrive_expect_tx(bar, heads * D * 2);
+                    bulk_g2s(smem + G::Q_OFF + (2 * team + (k & 1)) * G::Q_B,
+                             a.q + at.b * a.q_ld + ((long long)kvh * a.group + h0) * D, heads * D * 2, bar);
+                    q_armed = k;
+                }
+                __syncwarp();
+            }
             for (int t = at.t0; t < at.t1; ++t) {
-                const int pg0 = (t * G::TILE) >> a.page_log2, k = pg0 >> 5;
-                if (at.b != held_b || k != held_k) {
-                    held = at.b == held_b && k == held_k + 1 ? ahead : block(at.b, k, at.len);
-                    ahead = block(at.b, k + 1, at.len);
+                const int pg0 = (t * G::TILE) >> a.page_log2, bk = pg0 >> 5;
+                if (at.b != held_b || bk != held_k) {
+                    held = at.b == held_b && bk == held_k + 1 ? ahead : block(at.b, bk, at.len);
+                    ahead = block(at.b, bk + 1, at.len);
                     held_b = at.b;
-                    held_k = k;
+                    held_k = bk;
                 }
                 const int id = __shfl_sync(0xffffffffu, held, (pg0 & 31) + min(lane, pages - 1));
                 const bool mine = lane < pages && (long long)(pg0 + lane) << a.page_log2 < at.len;
@@ -776,12 +799,17 @@ __global__ void __launch_bounds__(Geo<D, NT, MX>::THREADS, 1)
                     ph ^= 1;
                 }
             }
-        } while (ok && advance<G>(a, at, end));
+            if (!ok || !advance<G>(a, at, end))
+                break;
+        }
         // every copy has landed before the CTA ends (bounded; slots whose other half never came run the limit out)
         if (lane == 0)
             for (int i = max(0, n - G::STAGES / TEAMS); i < n; ++i)
                 if (!mbar_drain(&full[team + i % (G::STAGES / TEAMS) * TEAMS], i / (G::STAGES / TEAMS) & 1))
                     break;
+        if (lane == 0)
+            for (int k = max(0, q_armed - 1); k <= q_armed; ++k)
+                mbar_drain(&q_full[2 * team + (k & 1)], (k >> 1) & 1);
         __syncwarp();
         return;
     }
@@ -798,16 +826,17 @@ __global__ void __launch_bounds__(Geo<D, NT, MX>::THREADS, 1)
     State<D, NT> st;
     uint32_t qf[NT][D / 8];
     float mul[NT][2];
-    do {
+    for (int k = 0;; ++k) {  // stretches
         const int t0 = at.t0, t1 = at.t1;
         const int kvh = at.u / a.chunks, chunk = at.u - kvh * a.chunks;
         const int h0 = chunk * 8 * NT, heads = min(8 * NT, a.group - h0);
         const long long head = (long long)kvh * a.group + h0;
-        const uint16_t *q = a.q + at.b * a.q_ld + head * D;
+        alive = alive && __all_sync(0xffffffffu, mbar_wait(&q_full[2 * team + (k & 1)], (k >> 1) & 1, abort_flag, a.err)) != 0;
+        const uint32_t q = ring + G::Q_OFF + (2 * team + (k & 1)) * G::Q_B;
         if (MX) {
-            load_q_f16<D, NT>(a, q, heads, g, qd, qf, mul);
+            load_q_f16<D, NT>(a.scale, q, heads, g, qd, qf, mul);
         } else {
-            load_q<D, NT>(a, q, heads, g, qd, qf);
+            load_q<D, NT>(q, heads, g, qd, qf);
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
                 mul[nt][0] = mul[nt][1] = a.scale;
@@ -825,7 +854,10 @@ __global__ void __launch_bounds__(Geo<D, NT, MX>::THREADS, 1)
                 for (int c = 0; c < 4; ++c)
                     st.o[i][nt][c] = 0.f;
         }
-        bool wrong = false;
+        __syncwarp();
+        if (lane == 0 && alive)
+            mbar_arrive(&q_empty[2 * team + (k & 1)]);
+        bool wrong = !alive;
         for (int t = t0; t < t1; ++t) {
             // (after a wait that ran out the warp only keeps to the others' barriers; the rows become NaN)
             alive = alive && __all_sync(0xffffffffu, mbar_wait(&full[slot], ph, abort_flag, a.err)) != 0;
@@ -964,7 +996,9 @@ __global__ void __launch_bounds__(Geo<D, NT, MX>::THREADS, 1)
             }
         }
         part = 1;  // of a worker's stretches only the first and the last can be parts
-    } while (advance<G>(a, at, end));
+        if (!advance<G>(a, at, end))
+            break;
+    }
 }
 
 // Joins the parts of a query head of the unit that starts with worker blockIdx.x and goes on with others; in the order of the
