@@ -29,7 +29,7 @@
 // Measured (device time among other calls; 64 query heads on 8 key heads of 128 if not said otherwise): one sequence of
 // 131072 tokens 85 us (537 MB, 0.93 of a plain copy's rate; 80 without the join); 88 sequences of 0 to 8192 (56 on 8)
 // 218 us (1.49 GB, 1.00); 176 of 1 to 8192 in MXFP8 246 us (1.53 GB, 0.92); 15 of 1 to 4096, 32 heads of 64 unshared,
-// pages of 16 tokens, 44 us (245 MB, 0.83: 2 KB a copy); one of 1000 tokens (56 on 8) 8.4 us, a chain of latencies:
+// pages of 16 tokens, 44 us (245 MB, 0.83: 2 KB a copy); one of 1000 tokens (56 on 8) 7.9 us, a chain of latencies:
 // lengths, page numbers, tiles, parts, join.
 #include <math.h>
 #include <stdio.h>
@@ -48,7 +48,9 @@ using namespace gemm;
 constexpr int TEAM = 4;              // warps that share a tile, 16 tokens of each 64
 constexpr int TEAMS = 2;             // of a CTA, each with tiles of its own
 constexpr int MAX_STAGES = 16;
-constexpr int MIN_SHARE = 2;         // tiles of a team at least
+// Tiles of a worker at least: shared 1 (one sequence of 1000 tokens 7.9 us, with 2 8.5), whole 2 (16 of 1 to 256 tokens 8.3
+// us, with 1 9.0).
+constexpr int MIN_SHARE = 1, MIN_WHOLE = 2;
 
 // A unit that starts with a worker (as its first stretch or its last: part 0 or 1) and ends with worker `last`; of the
 // workers between it is the first stretch.  heads == 0: there is none.
@@ -118,7 +120,8 @@ template <class G> __device__ __forceinline__ int tiles_of(const DecodeArgs &a, 
 template <class G> __device__ __forceinline__ long long share_of(const DecodeArgs &a, long long total)
 {
     const long long s = (total + a.workers - 1) / a.workers;
-    return s < G::START + MIN_SHARE ? G::START + MIN_SHARE : s;
+    const int least = G::START + (a.whole ? MIN_WHOLE : MIN_SHARE);
+    return s < least ? least : s;
 }
 
 template <class G> __device__ __forceinline__ int places_of(const DecodeArgs &a, int b)
@@ -1098,7 +1101,7 @@ cudaError_t launch_decode(DecodeArgs &a, const MoeKvCache *cache, cudaStream_t s
     CUtensorMap mk, mv;
     // Short sequences are not shared between workers, which saves the join (2 us, and 3 us of the host's time for its
     // launch).  Measured, shared and whole (us in a graph; calls from Python): 56 heads on 8 of 128, one sequence of 256
-    // tokens 8.0 and 6.2 (11.9 and 9.8), of 512 7.7 and 8.6 (12.5 and 9.9), of 1000 8.4 and 13.2 (12.3 and 13.6); 88 of 1
+    // tokens 8.0 and 6.2 (11.9 and 9.8), of 512 7.7 and 8.6 (12.5 and 9.9), of 1000 7.9 and 13.2 (12.3 and 13.6); 88 of 1
     // to 256 20.5 and 19.0, of 1 to 500 26.0 and 24.9; 32 of 1 to 500 16.0 and 15.9, of 1 to 1000 19.8 and 20.5.
     a.whole = a.cap <= 512;
     auto kern = decode_kernel<D, NT, MX>;
