@@ -280,7 +280,8 @@ struct Item {
 struct Walk {
     static constexpr int KEPT = 4;  // sequences of a lane whose items it keeps
     int kept[KEPT], starts[KEPT], lens[KEPT];
-    int level, here;                // items at this level and above
+    int level, here, over;          // the level it is at; items at this level and above, and above it
+    int b0, seen;                   // sequences looked at, and those of them that have an item at this level
 
     __device__ __forceinline__ int items(const PromptArgs &a, int b) const
     {
@@ -311,23 +312,26 @@ struct Walk {
             kept[i] = (q.len + 2 * a.tile_tokens - 1) / (2 * a.tile_tokens);
         }
         level = a.T / (2 * a.tile_tokens) + 1;
-        here = 0;
+        here = over = b0 = seen = 0;
     }
 
     // Item i of the list; i grows from call to call.  (Offsets that do not ascend may name more items than the rows have
     // room for: those are left out.)
     __device__ __forceinline__ Item at(const PromptArgs &a, int i, int lane)
     {
-        int over = 0;  // items above the level that i is in
         if (i >= a.max_items)
             return {0, 0, 0, 0};
-        if (i >= here) {
-            int lo = 0, hi = level;  // above(lo) > i >= above(hi)
-            int n = above(a, 0, lane);
-            if (n <= i)
-                return {0, 0, 0, 0};
+        if (i >= here) {  // down in steps that double, then between the last two: above(lo) > i >= above(hi)
+            int hi = level, lo = level, n = here;
+            for (int step = 1; n <= i; step *= 2) {
+                if (lo == 0)
+                    return {0, 0, 0, 0};
+                hi = lo;
+                over = n;
+                lo = max(0, hi - step);
+                n = above(a, lo, lane);
+            }
             here = n;
-            over = above(a, hi, lane);
             while (hi - lo > 1) {
                 const int mid = (lo + hi) >> 1;
                 n = above(a, mid, lane);
@@ -340,13 +344,14 @@ struct Walk {
                 }
             }
             level = lo;
-        } else {
-            over = above(a, level + 1, lane);
+            b0 = seen = 0;
         }
         const int rank = (i - over) / a.kv, kvh = (i - over) - rank * a.kv;
-        // the rank-th sequence with more than `level` items
-        int seen = 0;
-        for (int b0 = 0, k = 0; b0 < a.n_seqs; b0 += 32, ++k) {
+        // the rank-th sequence with more than `level` items; ranks of a level grow from call to call
+        for (;; b0 += 32) {
+            if (b0 >= a.n_seqs)
+                break;
+            const int k = b0 >> 5;
             int n = 0;
 #pragma unroll
             for (int j = 0; j < KEPT; ++j)

@@ -49,6 +49,7 @@ CASES = [
     ([640, 513], 48, 1, 64), ([2500], 2, 1, 128), ([40 * i % 300 for i in range(30)], 5, 1, 64), ([37] * 400, 2, 1, 64),
     ([130 * i % 777 for i in range(60)], 14, 2, 128), ([1 + 211 * i % 1500 for i in range(15)], 56, 8, 128),
     ([90 * i % 400 for i in range(200)], 8, 8, 64),
+    ([i % 41 for i in range(1500)], 8, 1, 64), ([3] * 3000, 4, 2, 128), ([2] * 200 + [900] + [0, 50] * 100, 16, 2, 64),
 ]
 
 
