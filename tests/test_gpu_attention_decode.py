@@ -207,3 +207,32 @@ def test_no_sequences_and_tables_wider_than_needed():
     c, q, table, n = make([10, 200], 8, 2, 64, 16, "bf16", 71, width=4000)
     check(c.decode(q, table, n), expected(c, q, table, [10, 200], 0.125))
     assert c.decode(q[:0], table[:0], n[:0]).shape == (0, 8, 64)
+
+
+@pytest.mark.parametrize("fmt,n_pages", [("bf16", 40000), ("mxfp8", 80000)])
+def test_a_cache_whose_offsets_pass_32_bits(fmt, n_pages):
+    """5 GB of keys and as much of values: tokens written to and read from its last pages, and its first ones."""
+    from mxfp4_routed_expert_router_gb300 import attention as A
+    kv, heads, page, D = 8, 16, 64, 128
+    c = A.KvCache.empty(n_pages, kv, page, D, fmt)
+    assert c.k.numel() * c.k.element_size() > 2 ** 32
+    lens = [130, 70]
+    pages = [[n_pages - 1, 0, n_pages - 3], [n_pages - 2, 1, 2]]
+    table = torch.tensor(pages, dtype=torch.int32, device="cuda")
+    slots = [pages[s][i // page] * page + i % page for s, n in enumerate(lens) for i in range(n)]
+    g = torch.Generator(device="cuda")
+    g.manual_seed(1)
+    x = torch.randn((200, (heads + 2 * kv) * D), generator=g, device="cuda").bfloat16()
+    q = c.append(x, heads, torch.tensor(slots, dtype=torch.int32, device="cuda"))
+    used = torch.unique(table).long()
+    small = A.KvCache(*[t.view(torch.uint8)[used].view(t.dtype).contiguous() if t is not None else None
+                        for t in (c.k, c.v, c.k_scales, c.v_scales)])
+    local = torch.searchsorted(used, table.long()).int()
+    n = torch.tensor(lens, dtype=torch.int32, device="cuda")
+    got = c.decode(q[[129, 199]].contiguous(), table, n)
+    check(got, expected(small, q[[129, 199]], local, lens, D ** -0.5))
+    assert torch.equal(small.decode(q[[129, 199]].contiguous(), local, n), got)
+    if fmt == "bf16":
+        at = torch.tensor(slots, device="cuda")
+        v = x.view(200, -1, D)[:, heads + kv:]
+        assert torch.equal(c.v[at // page, :, at % page], v)

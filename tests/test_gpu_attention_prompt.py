@@ -166,3 +166,23 @@ def test_no_rows_and_no_sequences():
     out = torch.full_like(q, 3.0, memory_format=torch.contiguous_format)
     A.prompt(q, k, v, off[:1], out=out)
     assert torch.all(out == 3.0)
+
+
+def test_rows_whose_offsets_pass_32_bits():
+    """More than 2^31 values before the prompts: only their rows are read and written."""
+    from mxfp4_routed_expert_router_gb300 import attention as A
+    heads, kv, D, T = 64, 8, 128, 270000
+    assert T * heads * D > 2 ** 31
+    x = torch.zeros((T, heads + 2 * kv, D), dtype=torch.bfloat16, device="cuda")
+    lens = [300, 5]
+    first = T - 310
+    g = torch.Generator(device="cuda")
+    g.manual_seed(5)
+    x[first:] = torch.randn((310, heads + 2 * kv, D), generator=g, device="cuda").bfloat16()
+    q, k, v = x[:, :heads], x[:, heads:heads + kv], x[:, heads + kv:]
+    out = torch.full((T, heads, D), 2.0, dtype=torch.bfloat16, device="cuda")
+    A.prompt(q, k, v, torch.tensor([first, first + 300, first + 305], dtype=torch.int32, device="cuda"), out=out)
+    A.sync()
+    want = expected(q[first:], k[first:], v[first:], lens, D ** -0.5)
+    check(out[first:first + 305], (want[0][:305], want[1][:305]))
+    assert torch.all(out[first - 1000:first] == 2.0) and torch.all(out[first + 305:] == 2.0)
