@@ -48,11 +48,12 @@ class KvCache:
         if any(not t.is_contiguous() or not t.is_cuda or t.device != k.device for t in tensors):
             raise B.MoeError(B.MOE_EINVAL, "a cache's tensors must be dense and on one CUDA device")
         self.k, self.v, self.k_scales, self.v_scales = k, v, k_scales, v_scales
-        self.device, self._ordinal = k.device, k.get_device()
+        self.device = k.device
         self._workspace = {}  # n_heads -> bytes that ``decode`` needs
         self.page_size, self.n_kv_heads, self.head_dim = page, n_kv, dim
         self.c = B.MoeKvCache(k.data_ptr(), v.data_ptr(), B._ptr(k_scales), B._ptr(v_scales),
                               B.MOE_ROWS_MXFP8 if mx else B.MOE_ROWS_BF16, n_pages, page, n_kv, dim)
+        self.c.device = k.get_device()
 
     @classmethod
     def empty(cls, n_pages: int, n_kv_heads: int, page_size: int = 64, head_dim: int = 128, fmt: str = "bf16",
@@ -74,7 +75,6 @@ class KvCache:
         keys and values to their slots (-1: nowhere) and returns the queries, [T, n_heads, head_dim].  rope: a table
         as ``rope_table`` makes (None: nothing is turned), planes of a head's halves or, with pairs, of neighbours.
         k_out: also receives the turned keys, [T, n_kv_heads, head_dim]."""
-        self._here(qkv)
         if q_out is None:
             with _on(stream):
                 q_out = torch.empty((qkv.shape[0], n_heads, self.head_dim), dtype=torch.bfloat16, device=self.device)
@@ -86,7 +86,6 @@ class KvCache:
                out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
         """Attention of one token for each of B sequences (q bfloat16 [B, n_heads, head_dim]) over their lens[b] tokens
         in the pages page_table[b] (int32 [B, max_pages]).  scale: 1 / sqrt(head_dim) by default."""
-        self._here(q)
         if q.dim() != 3:
             raise B.MoeError(B.MOE_EINVAL, f"q: shape {tuple(q.shape)} where [B, n_heads, head_dim] is needed")
         n = self._workspace.get(q.shape[1])
@@ -103,10 +102,6 @@ class KvCache:
         B.moe_attention_decode(self.c, q, page_table, lens, self.head_dim ** -0.5 if scale is None else scale, out, ws,
                                n, stream)
         return out
-
-    def _here(self, t: torch.Tensor) -> None:
-        if t.get_device() != self._ordinal:
-            raise B.MoeError(B.MOE_EINVAL, f"a tensor on {t.device} and a cache on {self.device}")
 
 
 def prompt(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, offsets: torch.Tensor, scale: Optional[float] = None,

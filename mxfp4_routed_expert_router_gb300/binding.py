@@ -60,6 +60,7 @@ class MoeKvCache(ctypes.Structure):
     _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("k_scales", ctypes.c_void_p),
                 ("v_scales", ctypes.c_void_p), ("type", ctypes.c_int), ("n_pages", ctypes.c_int),
                 ("page_size", ctypes.c_int), ("n_kv_heads", ctypes.c_int), ("head_dim", ctypes.c_int)]
+    device = -1  # ordinal of the device that it lies on, where its maker tells (not passed on)
 
 
 class MoeRoutingOut(ctypes.Structure):
@@ -444,11 +445,13 @@ def _heads(t, name: str, bf16, rows: int, heads: int, dim: int, dev: int):
     if t.dtype is not bf16 or t.shape != (rows, heads, dim):
         raise MoeError(MOE_EINVAL, f"{name}: bfloat16 [{rows}, {heads}, {dim}] is needed, not {t.dtype} "
                                    f"{tuple(t.shape)}")
+    if t.get_device() != dev:
+        _elsewhere(name, t, dev)
+    if t.is_contiguous():
+        return t.data_ptr(), heads * dim
     ld, step, one = t.stride()
     if (one != 1 and dim > 1) or (step != dim and heads > 1):
         raise MoeError(MOE_EINVAL, f"{name}: the heads of a row must lie side by side")
-    if t.get_device() != dev:
-        _elsewhere(name, t, dev)
     return t.data_ptr(), (ld if rows > 1 else heads * dim)
 
 
@@ -466,9 +469,14 @@ def _elsewhere(name: str, t, dev: int):
     raise MoeError(MOE_EINVAL, f"{name}: a tensor on {t.device} where CUDA device {max(dev, 0)} is the current one")
 
 
-def _gpu_of(t) -> int:
-    """The current device's ordinal for a CUDA tensor, -2 (no tensor's) for one in host memory."""
-    return _ATTN[3]() if t.is_cuda else -2
+def _gpu_of(t, cache=None) -> int:
+    """The current device's ordinal for a CUDA tensor (and a cache there), -2 (no tensor's) for one in host memory."""
+    dev = _ATTN[3]() if t.is_cuda else -2
+    if cache is not None and cache.device != dev:  # (-1: a struct that tells no device)
+        if cache.device >= 0:
+            raise MoeError(MOE_EINVAL, f"a tensor on {t.device} and a cache on CUDA device {cache.device}, with device "
+                                       f"{max(dev, 0)} current")
+    return dev
 
 
 def moe_kv_append(cache: MoeKvCache, qkv, n_heads: int, slots, positions=None, rope=None,
@@ -480,7 +488,7 @@ def moe_kv_append(cache: MoeKvCache, qkv, n_heads: int, slots, positions=None, r
     D, kv = cache.head_dim, cache.n_kv_heads
     if qkv.dim() != 2 or qkv.dtype is not bf16:
         raise MoeError(MOE_EINVAL, "qkv: bfloat16 rows are needed")
-    T, dev = qkv.shape[0], _gpu_of(qkv)
+    T, dev = qkv.shape[0], _gpu_of(qkv, cache)
     p, _, ld = _rows(qkv, "qkv", (T, (n_heads + 2 * kv) * D))
     if qkv.get_device() != dev:
         _elsewhere("qkv", qkv, dev)
@@ -514,7 +522,7 @@ def moe_attention_decode(cache: MoeKvCache, q, page_table, lens, scale: float, o
     if q.dim() != 3:
         raise MoeError(MOE_EINVAL, "q: a [B, n_heads, head_dim] tensor is needed")
     B, heads, D = q.shape
-    dev = _gpu_of(q)
+    dev = _gpu_of(q, cache)
     qp, qld = _heads(q, "q", bf16, B, heads, cache.head_dim, dev)
     op, old = _heads(out, "out", bf16, B, heads, cache.head_dim, dev)
     if page_table.dim() != 2 or page_table.shape[0] != B or page_table.dtype is not i32 or \
