@@ -416,11 +416,43 @@ template <int D> __device__ __forceinline__ uint2 scales_of_two(uint32_t base, i
     return make_uint2(v & 0xFFFFu, v >> 16);
 }
 
-// The powers of two in use for the blocks of values, as E8M0 bytes: a state's vector is relative to them
+// The powers of two in use for the blocks of values, as E8M0 bytes: a state's vector is relative to them.  They are a
+// stretch's own: the largest of its first 16 tokens', and later of others that lie too far from them; but 2^53 at most, so
+// that the power of an infinity (2^120 from the cache's writer) does not put the other tokens' products below FP32's
+// range.  (A product of P and a value relative to 2^53 is below 2^(127 - 53 + 9): sums have 2^45 to spare.)
+constexpr int MOST_POWER = 180;
+
 struct Powers {
     uint32_t bytes;
-    bool narrow;  // all in 16 .. 240
+    bool narrow;  // none below 16
+    bool fresh;   // nothing is relative to them yet
 };
+
+// The lane's token's scale bytes of values, 0 past the end
+template <int D> __device__ __forceinline__ uint32_t value_scales(uint32_t vsb, int n, int lane)
+{
+    return lane >= n ? 0u : D == 128 ? lds32(vsb + lane * 4) : lds16(vsb + lane * 2);
+}
+
+// The largest power of block b among the lanes' tokens' (that of NaN counts for none: its products are NaN anyway)
+__device__ __forceinline__ uint32_t largest_power(uint32_t mine, int b)
+{
+    const uint32_t power = (mine >> (8 * b)) & 255;
+    return min((uint32_t)MOST_POWER, __reduce_max_sync(0xffffffffu, power == 255 ? 0u : power));
+}
+
+// The first tokens' powers
+template <int D> __device__ __forceinline__ void start_powers(Powers &ref, uint32_t vsb, int n, int lane)
+{
+    const uint32_t mine = value_scales<D>(vsb, n, lane);
+    ref = {0, true, false};
+#pragma unroll
+    for (int b = 0; b < D / 32; ++b) {
+        const uint32_t top = largest_power(mine, b);
+        ref.bytes |= top << (8 * b);
+        ref.narrow = ref.narrow && top >= 16;
+    }
+}
 
 // 16 tokens' values where their blocks' powers lie far from those in use: a token at a time in FP32.
 template <int D, int NT>
@@ -429,14 +461,14 @@ __device__ __forceinline__ void values_apart(State<D, NT> &st, const float (&p)[
 {
     constexpr int NB = D / 32;
     const int g = lane >> 2, qd = lane & 3;
+    const uint32_t mine = value_scales<D>(vsb, n, lane);
     uint32_t now = 0;
     ref.narrow = true;
 #pragma unroll
     for (int b = 0; b < NB; ++b) {  // what is in use grows to the largest of these tokens', and the vector follows
-        const uint32_t mine = lane < n ? ((D == 128 ? lds32(vsb + lane * 4) : lds16(vsb + lane * 2)) >> (8 * b)) & 255 : 0;
-        const uint32_t was = (ref.bytes >> (8 * b)) & 255, top = max(was, __reduce_max_sync(0xffffffffu, mine));
+        const uint32_t was = (ref.bytes >> (8 * b)) & 255, top = max(was, largest_power(mine, b));
         now |= top << (8 * b);
-        ref.narrow = ref.narrow && top >= 16 && top <= 240;
+        ref.narrow = ref.narrow && top >= 16;
         const float f = ex2((float)((int)was - (int)top));
 #pragma unroll
         for (int i = 2 * b; i < 2 * b + 2; ++i)
@@ -459,7 +491,8 @@ __device__ __forceinline__ void values_apart(State<D, NT> &st, const float (&p)[
         const int r = r0 + t;
 #pragma unroll
         for (int b = 0; b < NB; ++b) {
-            const float f = ex2((float)((int)((scales >> (8 * b)) & 255) - (int)((now >> (8 * b)) & 255)));
+            const int power = (scales >> (8 * b)) & 255;
+            const float f = power == 255 ? __int_as_float(0x7FC00000) : ex2((float)(power - (int)((now >> (8 * b)) & 255)));
             const int byte = 32 * b + 4 * g;
             const uint32_t w = lds32(vb + (D == 128 ? r * 128 + (byte ^ ((r & 7) << 4))
                                                     : r * 64 + (byte ^ (((r >> 1) & 3) << 4))));
@@ -533,21 +566,30 @@ __device__ __forceinline__ void tile_mx(State<D, NT> &st, const uint32_t (&qf)[N
     // P rounds to FP16 and takes, per block, what the token's power is away from the one in use: 2^-4 to 2^3, exact but
     // for numbers below FP16's normal range.  A probability so is off by 2^-12 of itself or 2^-25 of the largest, times
     // 2^4 at most in units of the token's values.  The usual case is that all 16 tokens fit in all blocks: then no byte
-    // of `away`, power - (ref - 4), borrows from the next or has more than three bits (ref lies in 16 .. 240, so that a
-    // byte which borrows shows it).
+    // of `away`, power - (ref - 4), borrows from the next or has more than three bits (ref lies in 16 .. MOST_POWER, so
+    // that a byte which borrows shows it, and that of NaN does not fit).
     const uint2 v01 = scales_of_two<D>(vsb, 2 * qd), v89 = scales_of_two<D>(vsb, 2 * qd + 8);
-    uint32_t away[4] = {v01.x, v01.y, v89.x, v89.y};
-    if (n < 16) {
+    uint32_t away[4];
+    auto fit = [&] {
+        away[0] = v01.x, away[1] = v01.y, away[2] = v89.x, away[3] = v89.y;
+        if (n < 16) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                away[i] = 2 * qd + (i & 1) + 8 * (i >> 1) < n ? away[i] : ref.bytes;
+        }
 #pragma unroll
         for (int i = 0; i < 4; ++i)
-            away[i] = 2 * qd + (i & 1) + 8 * (i >> 1) < n ? away[i] : ref.bytes;
-    }
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-        away[i] -= ref.bytes - (0x04040404u & SCALES);
-    if (!__all_sync(0xffffffffu, ref.narrow && ((away[0] | away[1] | away[2] | away[3]) & 0xF8F8F8F8u) == 0)) {
-        values_apart<D, NT>(st, p, vb, vsb, 0, n, ref, lane);
-        return;
+            away[i] -= ref.bytes - (0x04040404u & SCALES);
+        return __all_sync(0xffffffffu, ref.narrow && ((away[0] | away[1] | away[2] | away[3]) & 0xF8F8F8F8u) == 0) != 0;
+    };
+    if (!fit()) {
+        const bool fresh = ref.fresh;
+        if (fresh)
+            start_powers<D>(ref, vsb, n, lane);
+        if (!fresh || !fit()) {
+            values_apart<D, NT>(st, p, vb, vsb, 0, n, ref, lane);
+            return;
+        }
     }
     uint32_t pt[NT][2];
 #pragma unroll
@@ -824,7 +866,7 @@ __global__ void __launch_bounds__(Geo<D, NT, MX>::THREADS, 1)
     const uint32_t ring = smem_addr(smem);
     int slot = team, part = 0;
     uint32_t ph = 0;
-    Powers ref{0, false};
+    Powers ref;
     bool alive = true, odd = false;
     State<D, NT> st;
     uint32_t qf[NT][D / 8];
@@ -857,6 +899,7 @@ __global__ void __launch_bounds__(Geo<D, NT, MX>::THREADS, 1)
                 for (int c = 0; c < 4; ++c)
                     st.o[i][nt][c] = 0.f;
         }
+        ref = {0, false, true};
         __syncwarp();
         if (lane == 0 && alive)
             mbar_arrive(&q_empty[2 * team + (k & 1)]);
