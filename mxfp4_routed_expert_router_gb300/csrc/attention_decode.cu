@@ -419,7 +419,7 @@ template <int D> __device__ __forceinline__ uint2 scales_of_two(uint32_t base, i
 // The powers of two in use for the blocks of values, as E8M0 bytes: a state's vector is relative to them.  They are a
 // stretch's own: the largest of its first 16 tokens', and later of others that lie too far from them; but 2^53 at most, so
 // that the power of an infinity (2^120 from the cache's writer) does not put the other tokens' products below FP32's
-// range.  (A product of P and a value relative to 2^53 is below 2^(127 - 53 + 9): sums have 2^45 to spare.)
+// range.  (A product of P, up to 2^12, and a value relative to 2^53 is below 2^(12 + 127 - 53 + 9): sums have 2^33 to spare.)
 constexpr int MOST_POWER = 180;
 
 struct Powers {
@@ -512,6 +512,9 @@ __device__ __forceinline__ void values_apart(State<D, NT> &st, const float (&p)[
     }
 }
 
+// log2 of the largest P, and so of what sums and vectors of MXFP8 tiles are scaled by: times 2^3 (below) it is 2^15
+constexpr float RAISED = 12.f;
+
 // 16 tokens of an MXFP8 tile.  kb, vb: shared addresses of the warp's 16 rows (a multiple of 16 into a tile that starts
 // on 1024 bytes); ksb, vsb: their scales.
 template <int D, int NT>
@@ -558,14 +561,15 @@ __device__ __forceinline__ void tile_mx(State<D, NT> &st, const uint32_t (&qf)[N
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
         const float b0 = finite_base(st.m[nt][0]), b1 = finite_base(st.m[nt][1]);
-        p[nt][0] = ex2(s[nt][0] - b0), p[nt][1] = ex2(s[nt][1] - b1);
-        p[nt][2] = ex2(s[nt][2] - b0), p[nt][3] = ex2(s[nt][3] - b1);
+        p[nt][0] = ex2(s[nt][0] - b0 + RAISED), p[nt][1] = ex2(s[nt][1] - b1 + RAISED);
+        p[nt][2] = ex2(s[nt][2] - b0 + RAISED), p[nt][3] = ex2(s[nt][3] - b1 + RAISED);
         st.l[nt][0] += p[nt][0] + p[nt][2];
         st.l[nt][1] += p[nt][1] + p[nt][3];
     }
-    // P rounds to FP16 and takes, per block, what the token's power is away from the one in use: 2^-4 to 2^3, exact but
-    // for numbers below FP16's normal range.  A probability so is off by 2^-12 of itself or 2^-25 of the largest, times
-    // 2^4 at most in units of the token's values.  The usual case is that all 16 tokens fit in all blocks: then no byte
+    // P, at most 2^RAISED, rounds to FP16 and takes, per block, what the token's power is away from the one in use: 2^-4 to
+    // 2^3, exact but for numbers below FP16's normal range.  A probability so is off by 2^-11 of itself or 2^-37 of the
+    // largest, times 2^4 at most in units of the token's values.  (With P at most 1 and 2^-25, 131,072 tokens that lay 2^-23
+    // below a maximum lost most of their share.)  The usual case is that all 16 tokens fit in all blocks: then no byte
     // of `away`, power - (ref - 4), borrows from the next or has more than three bits (ref lies in 16 .. MOST_POWER, so
     // that a byte which borrows shows it, and that of NaN does not fit).
     const uint2 v01 = scales_of_two<D>(vsb, 2 * qd), v89 = scales_of_two<D>(vsb, 2 * qd + 8);
@@ -864,6 +868,7 @@ __global__ void __launch_bounds__(Geo<D, NT, MX>::THREADS, 1)
     float *merge = reinterpret_cast<float *>(smem + G::MERGE_OFF) + team * 2 * NT * 8 * D;
     auto team_sync = [&] { asm volatile("barrier.cta.sync.aligned %0, %1;" ::"r"(1 + team), "n"(TEAM * 32) : "memory"); };
     const uint32_t ring = smem_addr(smem);
+    constexpr float LOWERED = 1.f / (1 << (int)RAISED);
     int slot = team, part = 0;
     uint32_t ph = 0;
     Powers ref;
@@ -944,6 +949,7 @@ __global__ void __launch_bounds__(Geo<D, NT, MX>::THREADS, 1)
 #pragma unroll
                 for (int o = 4; o < 32; o <<= 1)
                     l += __shfl_xor_sync(0xffffffffu, l, o);
+                l *= MX ? LOWERED : 1.f;
                 if (wrong)
                     l = __int_as_float(0x7FC00000);
                 if (g == 0)
@@ -958,16 +964,16 @@ __global__ void __launch_bounds__(Geo<D, NT, MX>::THREADS, 1)
 #pragma unroll
                 for (int w = 0; w < TEAM; ++w)
                     m = fmaxf(m, ml[((w * NT + nt) * 8 + 2 * qd + h) * 2]);
-                const float f = ex2(st.m[nt][h] - finite_base(m));
+                const float f = ex2(st.m[nt][h] - finite_base(m)) * (MX ? LOWERED : 1.f);
 #pragma unroll
                 for (int i = 0; i < D / 16; ++i) {
+                    st.o[i][nt][h] *= f;
+                    st.o[i][nt][2 + h] *= f;
                     if (MX) {
                         const float power = e8m0((ref.bytes >> (8 * (i / 2))) & 255);
                         st.o[i][nt][h] *= power;
                         st.o[i][nt][2 + h] *= power;
                     }
-                    st.o[i][nt][h] *= f;
-                    st.o[i][nt][2 + h] *= f;
                 }
             }
         float4 *mine = reinterpret_cast<float4 *>(merge + (w4 & 1) * NT * 8 * D) + lane;
