@@ -122,7 +122,8 @@ class Attention:
 
     rope: a table as ``rope_table`` makes, or None (nothing is turned); scale: 1 / sqrt(head_dim) by default.  Both
     calls turn the queries and keys of the rows in place, write keys and values to their slots (int32 [T]; -1: padding)
-    and return bfloat16 [T, n_heads * head_dim]; positions (int32 [T]) are needed with rope.
+    and return bfloat16 [T, n_heads * head_dim]; positions (int32 [T]) are needed with rope.  A call that is refused has
+    touched neither the rows nor the cache.
     """
 
     def __init__(self, n_heads: int, cache: KvCache, rope: Optional[torch.Tensor] = None, pairs: bool = False,
@@ -135,29 +136,33 @@ class Attention:
                                            "needed")
         self.n_heads, self.cache, self.rope, self.pairs = n_heads, cache, rope, pairs
         self.scale = cache.head_dim ** -0.5 if scale is None else scale
+        B.check_attention(cache.c, n_heads, self.scale)
         self.row = (n_heads + 2 * cache.n_kv_heads) * cache.head_dim  # values of a row of the projection
 
-    def _append(self, qkv: torch.Tensor, slots, positions, k_too: bool):
+    def _heads_of(self, qkv: torch.Tensor):
+        """Views of the rows' queries, keys and values."""
         n, kv, dim = self.n_heads, self.cache.n_kv_heads, self.cache.head_dim
         if qkv.dim() != 2 or qkv.shape[1] != self.row or qkv.stride(1) != 1:
             raise B.MoeError(B.MOE_EINVAL, f"qkv: shape {tuple(qkv.shape)} where [T, {self.row}] is needed")
         rows = qkv.unflatten(1, (n + 2 * kv, dim))
-        q, k, v = rows[:, :n], rows[:, n:n + kv], rows[:, n + kv:]
-        self.cache.append(qkv, n, slots, positions, self.rope, self.pairs, q, k if k_too else None)
-        return q, k, v
+        return rows[:, :n], rows[:, n:n + kv], rows[:, n + kv:]
 
     def decode(self, qkv: torch.Tensor, slots: torch.Tensor, positions: Optional[torch.Tensor],
                page_table: torch.Tensor, lens: torch.Tensor) -> torch.Tensor:
         """One new token for each sequence; lens (int32 [T]) counts it.  A row without a sequence has slot -1 and
         length 0, and gives zeros."""
-        q, _, _ = self._append(qkv, slots, positions, False)
+        q, _, _ = self._heads_of(qkv)
+        B.check_decode(self.cache.c, qkv, page_table, lens)
+        self.cache.append(qkv, self.n_heads, slots, positions, self.rope, self.pairs, q)
         return self.cache.decode(q, page_table, lens, self.scale).flatten(1)
 
     def prompt(self, qkv: torch.Tensor, slots: torch.Tensor, positions: Optional[torch.Tensor],
                offsets: torch.Tensor) -> torch.Tensor:
         """Whole prompts, packed: sequence s has the rows offsets[s] .. offsets[s + 1] - 1 (int32 [n_seqs + 1]).  Rows
         of no sequence give zeros."""
-        q, k, v = self._append(qkv, slots, positions, True)
+        q, k, v = self._heads_of(qkv)
+        B.check_prompt(self.cache.c, qkv, self.n_heads, offsets)
+        self.cache.append(qkv, self.n_heads, slots, positions, self.rope, self.pairs, q, k)
         out = torch.zeros((q.shape[0], self.n_heads, self.cache.head_dim), dtype=torch.bfloat16, device=qkv.device)
         return prompt(q, k, v, offsets, self.scale, out).flatten(1)
 

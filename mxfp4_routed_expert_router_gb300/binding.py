@@ -465,6 +465,22 @@ def _vector(t, name: str, i32, n: int, dev: int):
     return t.data_ptr()
 
 
+def _sequences(page_table, lens, i32, n: int, dev: int):
+    """Addresses of a page table and of the lengths of n sequences."""
+    if page_table.dim() != 2 or page_table.shape[0] != n or page_table.dtype is not i32 or \
+            not page_table.is_contiguous() or page_table.get_device() != dev:
+        raise MoeError(MOE_EINVAL, f"page_table: a dense int32 [{n}, max_pages] tensor on the current device is needed")
+    return page_table.data_ptr(), _vector(lens, "lens", i32, n, dev)
+
+
+def _offsets(offsets, i32, dev: int):
+    """Address of the offsets of packed prompts, and the number of these."""
+    if offsets.dim() != 1 or offsets.shape[0] < 1:
+        raise MoeError(MOE_EINVAL, "offsets: an int32 vector of n_seqs + 1 values is needed")
+    n = offsets.shape[0] - 1
+    return _vector(offsets, "offsets", i32, n + 1, dev), n
+
+
 def _elsewhere(name: str, t, dev: int):
     raise MoeError(MOE_EINVAL, f"{name}: a tensor on {t.device} where CUDA device {max(dev, 0)} is the current one")
 
@@ -525,15 +541,37 @@ def moe_attention_decode(cache: MoeKvCache, q, page_table, lens, scale: float, o
     dev = _gpu_of(q, cache)
     qp, qld = _heads(q, "q", bf16, B, heads, cache.head_dim, dev)
     op, old = _heads(out, "out", bf16, B, heads, cache.head_dim, dev)
-    if page_table.dim() != 2 or page_table.shape[0] != B or page_table.dtype is not i32 or \
-            not page_table.is_contiguous() or page_table.get_device() != dev:
-        raise MoeError(MOE_EINVAL, f"page_table: a dense int32 [{B}, max_pages] tensor on the current device is needed")
-    lp = _vector(lens, "lens", i32, B, dev)
-    status = lib.moe_attention_decode(ctypes.byref(cache), qp, qld, B, heads, page_table.data_ptr(),
-                                      page_table.shape[1], lp, scale, op, old, _ptr(workspace), ws_bytes,
-                                      _stream(stream))
+    tp, lp = _sequences(page_table, lens, i32, B, dev)
+    status = lib.moe_attention_decode(ctypes.byref(cache), qp, qld, B, heads, tp, page_table.shape[1], lp, scale, op, old,
+                                      _ptr(workspace), ws_bytes, _stream(stream))
     if status:
         _check(status)
+
+
+def check_attention(cache: MoeKvCache, n_heads: int, scale: float) -> None:
+    """Raise what moe_attention_decode would for a cache, a number of query heads or a scale that do not fit."""
+    status = lib.moe_attention_decode(ctypes.byref(cache), None, 0, 0, n_heads, None, 1, None, scale, None, 0, None, 0,
+                                      None)  # (no sequences: it checks these and enqueues nothing)
+    if status:
+        _check(status)
+
+
+def check_decode(cache: MoeKvCache, rows, page_table, lens) -> None:
+    """Raise what moe_attention_decode would for a page table or lengths that do not fit these rows, and touch nothing."""
+    n = rows.shape[0]
+    _sequences(page_table, lens, (_ATTN or _attn())[1], n, _gpu_of(rows, cache))
+    pages = page_table.shape[1]
+    if n > 65536 or pages < 1 or pages * cache.page_size >= 1 << 31:
+        raise MoeError(MOE_EINVAL, f"{n} sequences of up to {pages} pages: at most 65536, and 1 page or more and fewer "
+                                   "than 2^31 tokens, are possible")
+
+
+def check_prompt(cache: MoeKvCache, rows, n_heads: int, offsets) -> None:
+    """Raise what moe_attention_prompt would for offsets or a number of heads that do not fit, and touch nothing."""
+    _, n = _offsets(offsets, (_ATTN or _attn())[1], _gpu_of(rows, cache))
+    if n > 65536 or n_heads > 64 * cache.n_kv_heads:
+        raise MoeError(MOE_EINVAL, f"{n} sequences, {n_heads} heads on {cache.n_kv_heads}: at most 65536, and 64 heads to "
+                                   "a key head, are possible")
 
 
 def moe_attention_prompt(q, k, v, offsets, scale: float, out, stream=None) -> None:
@@ -548,10 +586,7 @@ def moe_attention_prompt(q, k, v, offsets, scale: float, out, stream=None) -> No
     kp, kld = _heads(k, "k", bf16, T, kv, D, dev)
     vp, vld = _heads(v, "v", bf16, T, kv, D, dev)
     op, old = _heads(out, "out", bf16, T, heads, D, dev)
-    if offsets.dim() != 1 or offsets.shape[0] < 1:
-        raise MoeError(MOE_EINVAL, "offsets: an int32 vector of n_seqs + 1 values is needed")
-    n = offsets.shape[0] - 1
-    off = _vector(offsets, "offsets", i32, n + 1, dev)
+    off, n = _offsets(offsets, i32, dev)
     status = lib.moe_attention_prompt(qp, qld, kp, kld, vp, vld, T, off, n, heads, kv, D, scale, op, old,
                                       _stream(stream))
     if status:
