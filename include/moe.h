@@ -522,7 +522,7 @@ void moe_linear_free(MoeLinear *l);
  * paged cache (moe_kv_append), attention of one new token per sequence over
  * that cache (moe_attention_decode) and causal attention within whole prompts
  * (moe_attention_prompt).  No handle: what a kernel finds wrong in its device
- * inputs it records in a flag of the device, which moe_attention_status reads.
+ * inputs it records on the device, of which moe_attention_status tells.
  * No counterpart in the papers.
  *
  * Heads: n_heads query heads share n_kv_heads key and value heads, n_heads a
@@ -632,10 +632,13 @@ MoeStatus moe_attention_prompt(const void *q, long long q_ld, const void *k, lon
                                int head_dim, float scale, void *out, long long out_ld, void *cuda_stream);
 
 /* Wait for `cuda_stream`, then report whether a kernel of this section recorded
- * an error on the current device since the last report: a slot, position,
- * length or page out of range, or a wait that ran out (the call's rows are NaN
- * or were not written).  The report clears it.
- * Returns MOE_OK, MOE_EDEVICE or MOE_ECUDA. */
+ * an error on the current device since the last report on this stream (at its
+ * first: since the process started): a slot, position, length or page out of
+ * range, or a wait that ran out (the call's rows are NaN or were not written).
+ * Kernels of all streams count, as a captured call may be replayed on any: after
+ * an error each stream's next report tells of it once, and none is lost.  Not
+ * while the stream is being captured.
+ * Returns MOE_OK, MOE_EDEVICE, MOE_ENOMEM or MOE_ECUDA. */
 MoeStatus moe_attention_status(void *cuda_stream);
 
 /* Human-readable description of the last non-OK status returned on the

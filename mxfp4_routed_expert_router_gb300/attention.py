@@ -168,7 +168,8 @@ class Attention:
 
 
 def sync(stream=None) -> None:
-    """Waits for the stream and raises if an attention kernel on the current device recorded an error."""
+    """Waits for the stream and raises if an attention kernel on the current device, on whatever stream, recorded an error
+    since the last time on this stream."""
     B.moe_attention_status(stream)
 
 

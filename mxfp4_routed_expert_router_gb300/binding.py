@@ -594,8 +594,8 @@ def moe_attention_prompt(q, k, v, offsets, scale: float, out, stream=None) -> No
 
 
 def moe_attention_status(stream=None) -> None:
-    """Raise MoeError(MOE_EDEVICE) if an attention kernel recorded an error on the current device since the last
-    report."""
+    """Raise MoeError(MOE_EDEVICE) if an attention kernel recorded an error on the current device, on whatever stream,
+    since the last report on this one."""
     _check(lib.moe_attention_status(_stream(stream)))
 
 

@@ -12,7 +12,7 @@ namespace moe {
 constexpr int ATTN_MAX_HEADS = 1024;
 
 // The attention operators have no handle: kernels record what goes wrong in one flag per device (the first error
-// stays until moe_attention_status reads it).  Its address on the current device, or an error.
+// stays until moe_attention_status takes it).  Its address on the current device, or an error.
 cudaError_t attention_error_flag(int **flag);
 
 // MOE_OK, or the status (with its message set) of what is wrong with a cache.

@@ -23,6 +23,10 @@
 #include <stdio.h>
 
 #include <atomic>
+#include <exception>
+#include <map>
+#include <mutex>
+#include <utility>
 
 #include "attention_internal.cuh"
 #include "gemm_common.cuh"
@@ -33,7 +37,21 @@ namespace moe {
 
 namespace {
 
-__device__ int g_error;
+__device__ int g_error;  // what a kernel recorded first since it was last taken
+__device__ int g_taken;  // (a report's copy of it)
+
+// Takes what is recorded in one step: what another stream's kernel records meanwhile comes before it or stays.
+__global__ void take_error_kernel(int *flag, int *taken) { *taken = atomicExch(flag, 0); }
+
+// Every stream hears of every error of its device: kernels do not know whose they are (a captured call's replay may run
+// on any stream), and the stream that asks first must not keep an error from the one whose rows it spoilt.
+struct Reports {
+    std::mutex mu;
+    unsigned long long count[gemm::MAX_DEVICES] = {};          // errors taken, per device
+    int code[gemm::MAX_DEVICES] = {};                          // the last one
+    std::map<std::pair<int, void *>, unsigned long long> seen;  // (device, stream) -> the count of its last report
+};
+Reports g_reports;
 
 constexpr int THREADS = 256;
 
@@ -356,14 +374,41 @@ extern "C" MoeStatus moe_kv_append(const MoeKvCache *cache, const void *qkv, lon
 extern "C" MoeStatus moe_attention_status(void *cuda_stream)
 {
     char msg[160];
-    int *flag = nullptr, got = 0;
+    cudaStream_t st = (cudaStream_t)cuda_stream;
+    int *flag = nullptr, dev = 0, got = 0;
     cudaError_t e = attention_error_flag(&flag);
     if (e == cudaSuccess)
-        e = cudaStreamSynchronize((cudaStream_t)cuda_stream);
+        e = cudaGetDevice(&dev);
     if (e == cudaSuccess)
-        e = cudaMemcpy(&got, flag, sizeof got, cudaMemcpyDeviceToHost);
-    if (e == cudaSuccess && got)
-        e = cudaMemset(flag, 0, sizeof got);
+        e = cudaStreamSynchronize(st);
+    try {
+        std::lock_guard<std::mutex> lock(g_reports.mu);
+        unsigned long long &seen = g_reports.seen[{dev, cuda_stream}];
+        void *taken = nullptr;
+        if (e == cudaSuccess)
+            e = cudaGetSymbolAddress(&taken, g_taken);
+        if (e == cudaSuccess) {
+            cudaLaunchConfig_t cfg{};
+            cfg.gridDim = cfg.blockDim = 1;
+            cfg.stream = st;
+            e = cudaLaunchKernelEx(&cfg, take_error_kernel, flag, static_cast<int *>(taken));
+        }
+        if (e == cudaSuccess)
+            e = cudaMemcpyAsync(&got, taken, sizeof got, cudaMemcpyDeviceToHost, st);
+        if (e == cudaSuccess)
+            e = cudaStreamSynchronize(st);
+        if (e == cudaSuccess) {
+            if (got) {
+                ++g_reports.count[dev];
+                g_reports.code[dev] = got;
+            }
+            got = seen != g_reports.count[dev] ? g_reports.code[dev] : 0;
+            seen = g_reports.count[dev];
+        }
+    } catch (const std::exception &x) {
+        snprintf(msg, sizeof msg, "moe_attention_status: %s", x.what());
+        return bad(MOE_ENOMEM, msg);
+    }
     if (e != cudaSuccess) {
         snprintf(msg, sizeof msg, "moe_attention_status: %s", cudaGetErrorString(e));
         return bad(MOE_ECUDA, msg);
