@@ -593,10 +593,11 @@ MoeStatus moe_kv_append(const MoeKvCache *cache, const void *qkv, long long qkv_
  * anything.  A sequence with a negative length, one above max_pages * page_size,
  * or a page outside the cache gives NaN, and this is recorded
  * (moe_attention_status).  Scores, softmax and sums are FP32; probabilities
- * round to BF16 (with MXFP8 to FP16, relative to 2^-12 of the largest) for the
- * product with v, MXFP8 queries to FP16 with a power of two per head.  (MXFP8
- * blocks of v whose powers of two lie more than 2^100 apart within a sequence may
- * lose the smaller ones.)  Results do not change from call to call.
+ * enter the product with v as the sum of two BF16 numbers (2^-15 of them; with
+ * MXFP8 as FP16, relative to 2^-12 of the largest), MXFP8 queries that with keys
+ * as FP16 with a power of two per head.  (MXFP8 blocks of v whose powers of two
+ * lie more than 2^100 apart within a sequence may lose the smaller ones.)
+ * Results do not change from call to call.
  * Rows start on 16-byte boundaries.  B == 0 enqueues nothing.
  * Errors: MOE_EINVAL (a bad cache, B outside [0, 65536], n_heads no multiple of
  * n_kv_heads or above 1024, max_pages < 1 or max_pages * page_size >= 2^31, scale

@@ -9,7 +9,7 @@
 // tokens (keys, and values, of one key head, by TMA through the page table; a stretch's queries ahead of its first tile,
 // 222 -> 218 us for the 88 sequences below) and four that take 16 tokens of each 64.  Two
 // warp-level MMAs per 16 x 16 values of a tile do the work of all query heads that share the key head, eight at a time:
-//   S^T[16 tokens, 8 heads] = K Q^T,    O^T[16 values, 8 heads] += V^T P^T
+//   S^T[16 tokens, 8 heads] = K Q^T,    O^T[16 values, 8 heads] += V^T P^T    (BF16: P as two numbers, two MMAs)
 // With tokens as the rows of the first product and values as the rows of the second, keys come out of shared memory as
 // they lie there (16 bytes a lane, which pair with the same 16 bytes of q), values by one byte permutation per pair of
 // tokens, and P moves from one to the other by a transposition of 8 x 8 (movmatrix).  The tiles carry TMA's 128-byte
@@ -149,6 +149,17 @@ __device__ __forceinline__ void mma16816(float c[4], uint32_t a0, uint32_t a1, u
         asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
             : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
             : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// a and b, 0 or more, as two BF16 numbers each: what the first, their upper half, leaves goes into the second, which is
+// above 0 wherever the first is (a zero or a negative number times an infinite value would make NaN of it).  Their sum is
+// off by 2^-15 of a or b.
+__device__ __forceinline__ void bf16_in_two(float a, float b, uint32_t &first, uint32_t &second)
+{
+    constexpr float LEAST = 1.f / (1 << 17);
+    first = __byte_perm(__float_as_uint(a), __float_as_uint(b), 0x7632);
+    second = bf16_pair(fmaxf(a - __uint_as_float(__float_as_uint(a) & 0xFFFF0000u), a * LEAST),
+                       fmaxf(b - __uint_as_float(__float_as_uint(b) & 0xFFFF0000u), b * LEAST));
 }
 
 __device__ __forceinline__ uint32_t transpose8x8(uint32_t v)
@@ -319,7 +330,7 @@ __device__ __forceinline__ void tile_bf16(State<D, NT> &st, const uint32_t (&qf)
             sa[nt][i] += sb[nt][i];
     tile_max<NT>(sa, mul, g < n, g + 8 < n, mt);
     grow<D, NT>(st, mt);
-    uint32_t pf[NT][2];
+    uint32_t pf[NT][2], rest[NT][2];
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
         const float b0 = finite_base(st.m[nt][0]), b1 = finite_base(st.m[nt][1]);
@@ -327,9 +338,16 @@ __device__ __forceinline__ void tile_bf16(State<D, NT> &st, const uint32_t (&qf)
         const float p2 = ex2(sa[nt][2] - b0), p3 = ex2(sa[nt][3] - b1);
         st.l[nt][0] += p0 + p2;
         st.l[nt][1] += p1 + p3;
-        // rounded to BF16 for the product (2^-9 of each, of random sign): v is BF16, and an MMA's operands share a type
-        pf[nt][0] = transpose8x8(bf16_pair(p0, p1));
-        pf[nt][1] = transpose8x8(bf16_pair(p2, p3));
+        // v is BF16, and an MMA's operands share a type: P goes in as two BF16 numbers, in a product each.  (The tensor pipe
+        // has room: it stood at 8 % with one product, which put outputs off by up to another BF16 rounding.)
+        uint32_t first[2], second[2];
+        bf16_in_two(p0, p1, first[0], second[0]);
+        bf16_in_two(p2, p3, first[1], second[1]);
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            pf[nt][i] = transpose8x8(first[i]);
+            rest[nt][i] = transpose8x8(second[i]);
+        }
     }
 #pragma unroll
     for (int h = 0; h < D / 64; ++h) {
@@ -352,8 +370,10 @@ __device__ __forceinline__ void tile_bf16(State<D, NT> &st, const uint32_t (&qf)
             const uint32_t a0 = __byte_perm(w0[i], w1[i], 0x5410), a1 = __byte_perm(w0[i], w1[i], 0x7632);
             const uint32_t a2 = __byte_perm(w2[i], w3[i], 0x5410), a3 = __byte_perm(w2[i], w3[i], 0x7632);
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
+            for (int nt = 0; nt < NT; ++nt) {
                 mma16816<false>(st.o[4 * h + i][nt], a0, a1, a2, a3, pf[nt][0], pf[nt][1]);
+                mma16816<false>(st.o[4 * h + i][nt], a0, a1, a2, a3, rest[nt][0], rest[nt][1]);
+            }
         }
     }
 }
