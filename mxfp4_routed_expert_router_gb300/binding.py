@@ -354,13 +354,13 @@ def moe_add_rmsnorm(residual, delta, gain, eps: float, sum=None, y=None, q=None,
         _check(status)
 
 
-_DTYPES = []  # torch.float32, torch.int32: filled by the first call that needs them
+_DTYPES = ()  # torch.float32, torch.int32: set by the first call that needs them (or by several threads' at once)
 
 
 def _dtypes():
-    if not _DTYPES:
-        import torch
-        _DTYPES.extend((torch.float32, torch.int32))
+    global _DTYPES
+    import torch
+    _DTYPES = (torch.float32, torch.int32)
     return _DTYPES
 
 
@@ -427,14 +427,16 @@ def moe_linear_free(handle: int) -> None:
     lib.moe_linear_free(handle)
 
 
-_ATTN = []  # torch.bfloat16, torch.int32, torch.float32, the current device's ordinal: filled by the first call
+# torch.bfloat16, torch.int32, torch.float32, the current device's ordinal: set by the first call (or by several threads'
+# at once)
+_ATTN = ()
 
 
 def _attn():
-    if not _ATTN:
-        import torch
-        _ATTN.extend((torch.bfloat16, torch.int32, torch.float32,
-                      getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)))
+    global _ATTN
+    import torch
+    _ATTN = (torch.bfloat16, torch.int32, torch.float32,
+             getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device))
     return _ATTN
 
 
