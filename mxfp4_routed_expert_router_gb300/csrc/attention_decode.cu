@@ -489,7 +489,8 @@ __device__ __forceinline__ void values_apart(State<D, NT> &st, const float (&p)[
         const uint32_t was = (ref.bytes >> (8 * b)) & 255, top = max(was, largest_power(mine, b));
         now |= top << (8 * b);
         ref.narrow = ref.narrow && top >= 16;
-        const float f = ex2((float)((int)was - (int)top));
+        const bool nan = __any_sync(0xffffffffu, ((mine >> (8 * b)) & 255) == 255);  // (and so all of the block)
+        const float f = nan ? __int_as_float(0x7FC00000) : ex2((float)((int)was - (int)top));
 #pragma unroll
         for (int i = 2 * b; i < 2 * b + 2; ++i)
 #pragma unroll
@@ -511,8 +512,7 @@ __device__ __forceinline__ void values_apart(State<D, NT> &st, const float (&p)[
         const int r = r0 + t;
 #pragma unroll
         for (int b = 0; b < NB; ++b) {
-            const int power = (scales >> (8 * b)) & 255;
-            const float f = power == 255 ? __int_as_float(0x7FC00000) : ex2((float)(power - (int)((now >> (8 * b)) & 255)));
+            const float f = ex2((float)((int)((scales >> (8 * b)) & 255) - (int)((now >> (8 * b)) & 255)));
             const int byte = 32 * b + 4 * g;
             const uint32_t w = lds32(vb + (D == 128 ? r * 128 + (byte ^ ((r & 7) << 4))
                                                     : r * 64 + (byte ^ (((r >> 1) & 3) << 4))));
