@@ -596,8 +596,9 @@ MoeStatus moe_kv_append(const MoeKvCache *cache, const void *qkv, long long qkv_
  * enter the product with v as the sum of two BF16 numbers (2^-15 of them; with
  * MXFP8 as FP16, relative to 2^-12 of the largest), MXFP8 queries that with keys
  * as FP16 with a power of two per head.  (MXFP8 blocks of v whose powers of two
- * lie more than 2^100 apart within a sequence may lose the smaller ones.)
- * Results do not change from call to call.
+ * lie more than 2^100 apart within a sequence may lose the smaller ones, and MXFP8
+ * keys of 2^90 and more may give infinite scores.)  A sequence's result does not
+ * depend on what others hold, and does not change from call to call.
  * Rows start on 16-byte boundaries.  B == 0 enqueues nothing.
  * Errors: MOE_EINVAL (a bad cache, B outside [0, 65536], n_heads no multiple of
  * n_kv_heads or above 1024, max_pages < 1 or max_pages * page_size >= 2^31, scale

@@ -24,13 +24,19 @@
 //
 // MXFP8 caches (half the bytes): E4M3 values become FP16 exactly.  A block's power of two is applied to the FP32 sums
 // of its 32 values (keys), or to P (values), relative to a power that the vector's block is kept in; tokens whose powers
-// lie too far from it for FP16 are taken one by one in FP32.
+// lie too far from it for FP16 are taken one by one in FP32.  That power is a stretch's own (kept from one to the next it
+// let a sequence's largest values reach the sums of others; the 176 sequences below, with v of 2^6 from head to head, then
+// took 645 us for 247).  With one token in 64 that lies 2^5 above the rest most tokens of every fourth warp go one by one,
+// and the others wait for it: 1002 us.
 //
 // Measured (device time among other calls; 64 query heads on 8 key heads of 128 if not said otherwise): one sequence of
 // 131072 tokens 85 us (537 MB, 0.93 of a plain copy's rate; 80 without the join); 88 sequences of 0 to 8192 (56 on 8)
 // 218 us (1.49 GB, 1.00); 176 of 1 to 8192 in MXFP8 246 us (1.53 GB, 0.92); 15 of 1 to 4096, 32 heads of 64 unshared,
-// pages of 16 tokens, 44 us (245 MB, 0.83: 2 KB a copy); one of 1000 tokens (56 on 8) 7.9 us, a chain of latencies:
-// lengths, page numbers, tiles, parts, join.
+// pages of 16 tokens, 44 us (245 MB, 0.82: 2 KB a copy); one of 1000 tokens (56 on 8) 8.1 us, a chain of latencies:
+// lengths, page numbers, tiles, parts, join.  Up to 16 query heads to a key head take two products of eight: 88 sequences
+// of 0 to 8192, 64 heads on 4, 133 us (0.82) in BF16 and 103 (0.55) in MXFP8, 96 on 8 248 (0.88) and 189 (0.60); heads of
+// 128 then spill 32 and 68 bytes a thread.  Beyond 16 the cache is read once for each 16: 32 sequences of 4096, 40 heads on
+// 1, 41.6 us (0.24) and 36.7 (0.14).
 #include <math.h>
 #include <stdio.h>
 
@@ -1168,10 +1174,12 @@ cudaError_t launch_decode(DecodeArgs &a, const MoeKvCache *cache, cudaStream_t s
 {
     using G = Geo<D, NT, MX>;
     CUtensorMap mk, mv;
-    // Short sequences are not shared between workers, which saves the join (2 us, and 3 us of the host's time for its
-    // launch).  Measured, shared and whole (us in a graph; calls from Python): 56 heads on 8 of 128, one sequence of 256
-    // tokens 8.0 and 6.2 (11.9 and 9.8), of 512 7.7 and 8.6 (12.5 and 9.9), of 1000 7.9 and 13.2 (12.3 and 13.6); 88 of 1
-    // to 256 20.5 and 19.0, of 1 to 500 26.0 and 24.9; 32 of 1 to 500 16.0 and 15.9, of 1 to 1000 19.8 and 20.5.
+    // Sequences are not shared between workers where the table holds at most 512 tokens (the lengths are known on the
+    // device only), which saves the join: 2 us, and 3 us of the host's time for its launch.  Measured, shared and whole (us
+    // in a graph; calls from Python): 56 heads on 8 of 128, one sequence of 256 tokens 8.0 and 6.2 (11.9 and 9.8), of 512
+    // 7.7 and 8.6 (12.5 and 9.9), of 1000 7.9 and 13.2 (12.3 and 13.6); 88 of 1 to 256 20.5 and 19.0, of 1 to 500 26.0 and
+    // 24.9; 32 of 1 to 500 16.0 and 15.9, of 1 to 1000 19.8 and 20.5.  One sequence of 512 so loses 0.9 us in a graph and
+    // gains 2.6 where it is called.
     a.whole = a.cap <= 512;
     auto kern = decode_kernel<D, NT, MX>;
     static std::atomic<int> attr_set[MAX_DEVICES];

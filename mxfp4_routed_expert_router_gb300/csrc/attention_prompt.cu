@@ -16,15 +16,15 @@
 // The maximum in use is kept until a row exceeds it by 2^8 (P is then up to 2^8, in BF16's and FP32's range alike):
 // rescaling O in tensor memory, which would be needed in every tile, becomes rare.
 //
-// Measured (device time): 8192 rows, 64 heads on 8 of 128, 670 to 706 us (1.1 TFLOP: 1,640 to 1,560 TFLOP/s, 0.87 to
-// 0.83 of a cuBLAS burst, by how far the card's power limit has brought the clock down; 4 key heads with pauses 1,700).
+// Measured (device time): 8192 rows, 64 heads on 8 of 128, 670 to 706 us (1.1 TFLOP: 1,640 to 1,560 TFLOP/s, 0.84 to
+// 0.80 of a cuBLAS burst, by how far the card's power limit has brought the clock down; 4 key heads with pauses 1,700).
 // A key tile takes 2,900 cycles for 2,048 of MMAs: a tile's softmax (load 150, maximum 400, exponentials 900, store
 // 110) and its own products (1,024 and 250 of latency) follow each other, and two tiles fill a third of each other's
 // gaps.  Tried without gain: P announced by halves; the exponentials with the old maximum while the new one is found;
 // two threads to a row (16 warps, a barrier of two per tile: 704 us for 673); rows that leave by TMA or, over shared
 // memory, by whole lines.  A new item costs 2 to 3 us beside its key tiles, so that short prompts get less (15 prompts
 // of 1 to 3001 rows, 56 heads on 8: 500 to 510 us for 650 GFLOP).  Heads of 64: 8192 rows, 32 heads on 4, 250 us, bound by
-// the softmax (exponentials: 49 % of their pipe).
+// the latency of the softmax (two warps a scheduler; issue slots 51 %, exponentials 49 % of their pipe, tensor 46 %).
 //
 // Masked values: P is 0 there, but 0 * inf is not.  Two warps clear the rows of V past the sequence's end, and values
 // that are not finite in tiles that some row must not see in full; rows that may see such a value get it added at the
@@ -838,8 +838,11 @@ __global__ void __launch_bounds__(THREADS, 1)
                                                       mul2, base2));
                         const float p0 = ex2(x.x), p1 = ex2(x.y);
                         sum[k & 3] = add2(sum[k & 3], pack2(p0, p1));
-                        // rounded to BF16 for the product (2^-9 of each, of random sign): v is BF16, and an MMA's
-                        // operands share a type
+                        // Rounded to BF16 for the product (2^-8 of each at most, of random sign: errors of 0.0020 of
+                        // the norm against 64 bits, 0.0016 without): v is BF16, and an MMA's operands share a type.
+                        // What the rounding leaves, in a product of its own, would take the tensor pipe from 2,048 to
+                        // 3,072 of a key tile's 2,900 cycles.  The sum is of the exact P: of the rounded ones it brought
+                        // 0.0019 and cost two instructions a pair (8192 rows 676 -> 716 us).
                         p[k] = bf16_pair(p0, p1);
                     }
                     tmem_st32(tp + c / 2, p);
