@@ -3,7 +3,7 @@ stream."""
 import pytest
 import torch
 
-from test_gpu_attention_layer import D, HEADS, KV, PAGE, ROW, _attention, _block, _i32
+from test_gpu_attention_layer import ROW, _attention, _block, _i32
 
 pytestmark = pytest.mark.gpu
 
